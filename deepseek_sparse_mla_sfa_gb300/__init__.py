@@ -7,10 +7,19 @@ library's CUDA kernels.  PyTorch provides device memory and streams.
     out, lse = decode(q, kv, block_table, seq_lens, topk_idx, scale)
     out_part, lse_part = decode(..., n_splits=8, merge=False)
     out, lse = lse_merge(out_part, lse_part)
+
+and, around it, one serving step over an 8-bit cache:
+
+    table, seq_lens, start, positions, slots, taken = step_plan(cached, new, table, free, taken, 64, T)
+    rope(q_pe, positions, inv_freq, out=q[..., 512:])
+    kv_write_q8(kv8, scales, slots, rows, workspace=ws)
+    out, lse = decode_q8(q, kv8, scales, table, seq_lens, topk_idx, scale)
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 from typing import Optional
 
 import torch
@@ -23,10 +32,13 @@ D_V = 512
 MAX_HEADS = 128
 MAX_SPLITS = 64
 BLOCK_TABLE_PER_TOKEN = 1   # sfa_decode_ex flag: one block-table row per query token
+OUT_BF16 = 2                # sfa_decode_q8 flag: out is bf16
 
 __all__ = ["decode", "lse_merge", "decode_host", "decode_host_staging_bytes",
            "workspace_bytes", "decode_noalloc", "decode_launches", "last_device_status", "set_kernel_path",
            "set_wait_limit", "set_stall_injection", "kv_write", "uv_proj", "topk", "HostPlan",
+           "decode_q8", "decode_q8_workspace_bytes", "kv_write_q8", "kv_write_q8_workspace_bytes", "step_plan",
+           "rope", "rope_inv_freq", "rope_mscale",
            "SfaError", "D_QK", "D_V", "BLOCK_TABLE_PER_TOKEN"]
 
 
@@ -38,6 +50,15 @@ def _stream_ptr(stream, device):
     if stream is None:
         stream = torch.cuda.current_stream(device)
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _on(dev, stream):
+    """Context of a call: `dev` current, and what the call allocates belongs to its stream."""
+    if stream is None:
+        return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream must be on {dev}, got {stream.device}")
+    return torch.cuda.stream(stream)
 
 
 def _need(t, name, dtype, device=None, ndim=None):
@@ -357,6 +378,247 @@ def topk(scores, k: int, seq_lens=None, Q: int = 1, S: Optional[int] = None, out
     code = lib.sfa_topk(_ptr(scores), stride, _ptr(seq_lens), B, int(Q), S, int(k), _ptr(out),
                         _stream_ptr(stream, dev))
     _lib.check("sfa_topk", code)
+    return out
+
+
+def decode_q8_workspace_bytes(B: int, Q: int, h: int, top_k: int, n_splits: int) -> int:
+    return int(_lib.load().sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits))
+
+
+def _need_cache_q8(kv8, scales):
+    """The checks of an 8-bit cache [num_blocks, block_size, 576] and its scales [num_blocks,
+    block_size / group]; returns the group."""
+    _need(kv8, "kv8", torch.float8_e4m3fn, None, 3)
+    _need(scales, "scales", torch.float32, None, 2)
+    nb, bs, d = kv8.shape
+    if d != D_QK:
+        raise ValueError("kv8 rows must have 576 columns")
+    groups = scales.shape[1]
+    if scales.shape[0] != nb or groups < 1 or bs % groups:
+        raise ValueError("scales must be [num_blocks, block_size / group] with group dividing block_size")
+    if kv8.device.type != "cuda":
+        raise ValueError("the 8-bit cache must be on a CUDA device")
+    if scales.device != kv8.device:
+        raise ValueError(f"scales must be on {kv8.device}, got {scales.device}")
+    return bs // groups
+
+
+def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_splits: int = 1, Q: int = 1,
+              merge: bool = True, out=None, lse=None, out_part=None, lse_part=None, workspace=None, stream=None,
+              interleave: int = 0, block_table_per_token: bool = False, out_dtype=torch.float32):
+    """Sparse MLA decode over an 8-bit latent cache (C ABI ``sfa_decode_q8``).
+
+    kv8 [num_blocks, block_size, 576] float8_e4m3fn and scales [num_blocks, block_size / group]
+    fp32: an element's value is kv8 * the scale of its group of slots (as kv_write_q8 writes
+    them).  out is [B*Q, h, 512] in `out_dtype` (torch.float32 or torch.bfloat16, or the dtype
+    of the `out` given).  Everything else as in ``decode``.
+    """
+    group = _need_cache_q8(kv8, scales)
+    for t, name, dt, nd in ((q, "q", torch.bfloat16, 3), (block_table, "block_table", torch.int32, 2),
+                            (seq_lens, "seq_lens", torch.int32, 1), (topk_idx, "topk_idx", torch.int32, 2)):
+        _need(t, name, dt, kv8.device, nd)
+    T, h, d = q.shape
+    if d != D_QK:
+        raise ValueError("q rows must have 576 columns")
+    if int(Q) != Q or Q < 1:
+        raise ValueError("Q must be an integer >= 1")
+    Q = int(Q)
+    B, top_k = seq_lens.shape[0], topk_idx.shape[1]
+    if T != B * Q or topk_idx.shape[0] != T or block_table.shape[0] != (T if block_table_per_token else B):
+        raise ValueError("inconsistent B / Q / T")
+    if interleave < 0:
+        raise ValueError("interleave must be >= 0")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+    lib, dev = _lib.load(), kv8.device
+    final = n_splits == 1 or merge
+    with _on(dev, stream):
+        if final:
+            if out is None:
+                out = torch.empty((T, h, D_V), dtype=out_dtype, device=dev)
+            if lse is None:
+                lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+            _need(out, "out", out_dtype, dev)
+            _need(lse, "lse", torch.float32, dev)
+            if tuple(out.shape) != (T, h, D_V) or tuple(lse.shape) != (T, h):
+                raise ValueError(f"out must be [{T}, {h}, {D_V}] and lse [{T}, {h}]")
+        if n_splits > 1:
+            if out_part is None:
+                out_part = torch.empty((n_splits, T, h, D_V), dtype=torch.float32, device=dev)
+            if lse_part is None:
+                lse_part = torch.empty((n_splits, T, h), dtype=torch.float32, device=dev)
+            _need(out_part, "out_part", torch.float32, dev)
+            _need(lse_part, "lse_part", torch.float32, dev)
+            if tuple(out_part.shape) != (n_splits, T, h, D_V) or tuple(lse_part.shape) != (n_splits, T, h):
+                raise ValueError(f"out_part must be [{n_splits}, {T}, {h}, {D_V}] and lse_part [{n_splits}, {T}, {h}]")
+        if workspace is None:
+            need = int(lib.sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits))
+            if need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        flags = (BLOCK_TABLE_PER_TOKEN if block_table_per_token else 0) | \
+                (OUT_BF16 if final and out_dtype == torch.bfloat16 else 0)
+        code = lib.sfa_decode_q8(_ptr(q), _ptr(kv8), _ptr(scales), group, _ptr(block_table), _ptr(seq_lens),
+                                 _ptr(topk_idx), B, Q, h, top_k, kv8.shape[0], kv8.shape[1], block_table.shape[1],
+                                 float(scale), n_splits, int(interleave), flags, _ptr(out if final else None),
+                                 _ptr(lse if final else None), _ptr(out_part if n_splits > 1 else None),
+                                 _ptr(lse_part if n_splits > 1 else None), _ptr(workspace), ws_bytes,
+                                 _stream_ptr(stream, dev))
+    _lib.check("sfa_decode_q8", code)
+    return (out, lse) if final else (out_part, lse_part)
+
+
+def kv_write_q8_workspace_bytes(num_slots: int, group: int) -> int:
+    return int(_lib.load().sfa_kv_write_q8_workspace_bytes(int(num_slots), int(group)))
+
+
+def kv_write_q8(kv8, scales, slot_mapping, rows, workspace=None, stream=None):
+    """Quantising write into the 8-bit latent cache (C ABI ``sfa_kv_write_q8``): row t of rows
+    [T, 576] bf16 goes to slot slot_mapping[t] (< 0 = padding) of kv8 [num_blocks, block_size,
+    576] float8_e4m3fn under the power-of-two scale of its group, scales [num_blocks,
+    block_size / group]; a group whose scale rises has its other rows stored again under it,
+    and one whose first slot is written starts anew.  In place; returns (kv8, scales).
+
+    workspace: kv_write_q8_workspace_bytes(num_blocks * block_size, group) bytes that belong to
+    this cache, zeroed once before the first write (not needed for groups of one slot).
+    """
+    group = _need_cache_q8(kv8, scales)
+    dev = kv8.device
+    _need(slot_mapping, "slot_mapping", torch.int32, dev, 1)
+    _need(rows, "rows", torch.bfloat16, dev, 2)
+    if rows.shape[1] != D_QK or rows.shape[0] != slot_mapping.shape[0]:
+        raise ValueError("rows must be [T, 576] with one slot per row")
+    ws_bytes = 0
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    with _on(dev, stream):
+        code = _lib.load().sfa_kv_write_q8(_ptr(kv8), _ptr(scales), kv8.shape[0] * kv8.shape[1], group,
+                                           _ptr(slot_mapping), _ptr(rows), rows.shape[0], _ptr(workspace), ws_bytes,
+                                           _stream_ptr(stream, dev))
+    _lib.check("sfa_kv_write_q8", code)
+    return kv8, scales
+
+
+def step_plan(cached_lens, new_lens, block_table, free_blocks, taken, block_size: int, num_tokens: int, stream=None):
+    """Block tables and slot maps of one step from request lengths (C ABI ``sfa_step_plan``).
+
+    cached_lens, new_lens [B] int32; block_table [B, max_blocks] int32 (in place: the blocks
+    that the new tokens need are taken from free_blocks [F] int32, from entry taken[0] on, in
+    request order); num_tokens is the step's room for new tokens.  Returns (block_table,
+    seq_lens [B], token_start [B + 1], positions [num_tokens], slot_mapping [num_tokens],
+    taken [1]), all int32; positions and slots behind the last token are -1, which rope and the
+    cache writes skip.
+    """
+    dev = block_table.device
+    if dev.type != "cuda":
+        raise ValueError("step_plan runs on a CUDA device only")
+    for t, name, nd in ((block_table, "block_table", 2), (cached_lens, "cached_lens", 1), (new_lens, "new_lens", 1),
+                        (free_blocks, "free_blocks", 1), (taken, "taken", 1)):
+        _need(t, name, torch.int32, dev, nd)
+    B = block_table.shape[0]
+    if cached_lens.shape[0] != B or new_lens.shape[0] != B or taken.shape[0] != 1:
+        raise ValueError("cached_lens and new_lens must be [B], block_table [B, max_blocks] and taken [1]")
+    N = int(num_tokens)
+    if N < 0:
+        raise ValueError("num_tokens must be >= 0")
+    with _on(dev, stream):
+        seq_lens, start, positions, slots, taken_out = torch.empty(
+            2 * B + 2 * N + 2, dtype=torch.int32, device=dev).split([B, B + 1, N, N, 1])
+        code = _lib.load().sfa_step_plan(_ptr(cached_lens), _ptr(new_lens), B, int(block_size), _ptr(block_table),
+                                         block_table.shape[1], _ptr(free_blocks), free_blocks.shape[0], _ptr(taken),
+                                         N, _ptr(seq_lens), _ptr(start), _ptr(positions), _ptr(slots),
+                                         _ptr(taken_out), _stream_ptr(stream, dev))
+    _lib.check("sfa_step_plan", code)
+    return block_table, seq_lens, start, positions, slots, taken_out
+
+
+def rope_inv_freq(rot_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                  original_len: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0, device="cuda"):
+    """The frequencies ``rope`` takes, [rot_dim / 2] float64: base ** (-2i / rot_dim), scaled
+    for contexts `factor` times `original_len`:
+
+    "linear"  all divided by factor (position interpolation);
+    "ntk"     the base grows by factor ** (rot_dim / (rot_dim - 2));
+    "yarn"    a frequency that turns more than beta_fast times in original_len positions stays,
+              one that turns less than beta_slow times is divided by factor, and those between
+              are mixed linearly in the number of turns (YaRN, arXiv:2309.00071, section 3.2;
+              its attention temperature is ``rope_mscale``).
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be even and >= 2")
+    if not (base > 0 and factor > 0):
+        raise ValueError("base and factor must be positive")
+    if scaling == "ntk":
+        if rot_dim < 4:
+            raise ValueError("ntk scaling needs rot_dim >= 4")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = torch.tensor([base ** (-2.0 * i / rot_dim) for i in range(rot_dim // 2)], dtype=torch.float64)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "yarn":
+        if not beta_fast > beta_slow:
+            raise ValueError("beta_fast must exceed beta_slow")
+        turns = original_len * f / (2.0 * math.pi)
+        keep = ((turns - beta_slow) / (beta_fast - beta_slow)).clamp(0.0, 1.0)
+        f = f / factor * (1.0 - keep) + f * keep
+    elif scaling not in (None, "ntk"):
+        raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+    return f.to(device)
+
+
+def rope_mscale(factor: float) -> float:
+    """The magnitude that YaRN gives rotated columns for a context `factor` times the trained."""
+    return 0.1 * math.log(factor) + 1.0 if factor > 1.0 else 1.0
+
+
+_ROPE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, inverse: bool = False, out=None,
+         stream=None):
+    """Rotary positions of the first 2 * len(inv_freq) columns of each head (C ABI ``sfa_rope``).
+
+    x [T, n, width] or [T, width] bf16, fp16 or fp32 with any row strides (a view of the rope
+    columns of wider heads); positions [T] int32 (< 0 = padding: those rows of out are left as
+    they were); inv_freq [rot_dim / 2] float64 (``rope_inv_freq``).  interleaved pairs columns
+    (2i, 2i + 1), else (i, i + rot_dim / 2).  inverse turns back by the same angles: the
+    transpose, so that rope(grad_out, ..., inverse=True) is the gradient of x.  out: x itself
+    (in place), another tensor of x's shape and dtype, or None for a new one.  Returns out.
+    """
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("rope runs on a CUDA device only")
+    if x.dtype not in _ROPE_DTYPES:
+        raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
+    if x.dim() not in (2, 3) or x.shape[-1] < 1 or x.stride(-1) != 1:
+        raise ValueError("x must be [T, n, width] or [T, width] with contiguous columns")
+    _need(positions, "positions", torch.int32, dev, 1)
+    _need(inv_freq, "inv_freq", torch.float64, dev, 1)
+    T, width, rot = x.shape[0], x.shape[-1], 2 * inv_freq.shape[0]
+    if positions.shape[0] != T:
+        raise ValueError("positions must be [T]")
+    if rot < 2 or rot > width:
+        raise ValueError("inv_freq must be [rot_dim / 2] with 2 <= rot_dim <= width")
+    with _on(dev, stream):
+        if out is None:
+            # a padding row has no result: a new tensor holds x's there
+            out = x.clone(memory_format=torch.contiguous_format)
+        elif out.dtype != x.dtype or out.device != dev or out.shape != x.shape or out.stride(-1) != 1:
+            raise ValueError("out must have x's shape, dtype and device, and contiguous columns")
+        n = x.shape[1] if x.dim() == 3 else 1
+        if n == 0:
+            return out
+        code = _lib.load().sfa_rope(_ptr(x), x.stride(0), x.stride(1) if x.dim() == 3 else 0, _ptr(out),
+                                    out.stride(0), out.stride(1) if out.dim() == 3 else 0, _ROPE_DTYPES[x.dtype], T,
+                                    n, width, rot, _ptr(positions), _ptr(inv_freq), float(mscale),
+                                    (1 if interleaved else 0) | (2 if inverse else 0), _stream_ptr(stream, dev))
+    _lib.check("sfa_rope", code)
     return out
 
 

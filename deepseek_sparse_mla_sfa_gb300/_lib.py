@@ -17,7 +17,7 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "sfa.h")
 
 STATUS = {0: "SFA_OK", -1: "SFA_ERR_INVALID_ARG", -2: "SFA_ERR_UNSUPPORTED",
           -3: "SFA_ERR_WORKSPACE", -4: "SFA_ERR_CUDA", -5: "SFA_ERR_DEVICE_TIMEOUT",
-          -6: "SFA_ERR_DEVICE_BAD_BLOCK"}
+          -6: "SFA_ERR_DEVICE_BAD_BLOCK", -7: "SFA_ERR_DEVICE_NO_BLOCKS"}
 
 _lock = threading.Lock()
 _lib = None
@@ -26,6 +26,7 @@ P = ctypes.c_void_p
 I = ctypes.c_int
 F = ctypes.c_float
 SZ = ctypes.c_size_t
+LL = ctypes.c_longlong
 
 SIGNATURES = {
     "sfa_decode": ([P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, P, P, P, P, SZ, P], I),
@@ -46,6 +47,12 @@ SIGNATURES = {
     "sfa_host_plan_create": ([P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, P, P, SZ, P], I),
     "sfa_host_plan_launch": ([P, P], I),
     "sfa_host_plan_destroy": ([P], None),
+    "sfa_decode_q8_workspace_bytes": ([I, I, I, I, I], SZ),
+    "sfa_decode_q8": ([P, P, P, I, P, P, P, I, I, I, I, I, I, I, F, I, I, I, P, P, P, P, P, SZ, P], I),
+    "sfa_kv_write_q8_workspace_bytes": ([LL, I], SZ),
+    "sfa_kv_write_q8": ([P, P, LL, I, P, P, I, P, SZ, P], I),
+    "sfa_step_plan": ([P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P], I),
+    "sfa_rope": ([P, LL, LL, P, LL, LL, I, I, I, I, I, P, P, F, I, P], I),
     "sfa_uv_proj": ([P, P, P, I, I, P], I),
 }
 
@@ -60,7 +67,7 @@ def header_functions(path: str = HEADER):
     """Names of the functions include/sfa.h declares."""
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(sfa_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(sfa_[a-z0-9_]+)\s*\(", text)))
 
 
 def load(path: str = LIB_PATH):

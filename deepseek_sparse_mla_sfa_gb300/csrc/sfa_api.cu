@@ -117,6 +117,7 @@ const char* sfa_status_string(sfa_status s) {
     case SFA_ERR_CUDA: return "SFA_ERR_CUDA";
     case SFA_ERR_DEVICE_TIMEOUT: return "SFA_ERR_DEVICE_TIMEOUT";
     case SFA_ERR_DEVICE_BAD_BLOCK: return "SFA_ERR_DEVICE_BAD_BLOCK";
+    case SFA_ERR_DEVICE_NO_BLOCKS: return "SFA_ERR_DEVICE_NO_BLOCKS";
   }
   return "SFA_UNKNOWN_STATUS";
 }
@@ -160,7 +161,7 @@ sfa_status sfa_lse_merge(const float* out_part, const float* lse_part, int n_spl
   if (!out_part || !lse_part || !out || !lse) return SFA_ERR_INVALID_ARG;
   if (!aligned(out_part, 16) || !aligned(out, 16) || !aligned(lse_part, 4) || !aligned(lse, 4))
     return SFA_ERR_INVALID_ARG;
-  cudaError_t e = sfa::launch_lse_merge(out_part, lse_part, n_splits, rows, dv, out, lse,
+  cudaError_t e = sfa::launch_lse_merge(out_part, lse_part, n_splits, rows, dv, out, 0, lse,
                                         static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA;
 }
@@ -241,7 +242,7 @@ sfa_status sfa_decode_ex(const void* q, const void* kv, const int32_t* block_tab
   cudaError_t e = tc ? sfa::launch_decode_tc(p, choice, s) : sfa::launch_decode_simt(p, s);
   if (e != cudaSuccess) return SFA_ERR_CUDA;
   if (merge_after) {
-    e = sfa::launch_lse_merge(out_part, lse_part, n_splits, T * h, SFA_D_V, out, lse, s);
+    e = sfa::launch_lse_merge(out_part, lse_part, n_splits, T * h, SFA_D_V, out, 0, lse, s);
     if (e != cudaSuccess) return SFA_ERR_CUDA;
   }
   return SFA_OK;
@@ -473,6 +474,161 @@ sfa_status sfa_topk(const float* scores, long long row_stride, const int32_t* se
     return SFA_ERR_INVALID_ARG;
   return sfa::launch_topk(scores, row_stride, seq_lens, B, Q, S, k, topk_idx, static_cast<cudaStream_t>(stream)) ==
                  cudaSuccess
+             ? SFA_OK
+             : SFA_ERR_CUDA;
+}
+
+size_t sfa_decode_q8_workspace_bytes(int B, int Q, int h, int top_k, int n_splits) {
+  (void)B; (void)Q; (void)h; (void)top_k; (void)n_splits;
+  return 0;
+}
+
+sfa_status sfa_decode_q8(const void* q, const void* kv8, const float* scales, int group, const int32_t* block_table,
+                         const int32_t* seq_lens, const int32_t* topk_idx, int B, int Q, int h, int top_k,
+                         int num_blocks, int block_size, int max_blocks_per_seq, float scale, int n_splits,
+                         int interleave_size, int flags, void* out, float* lse, float* out_part, float* lse_part,
+                         void* workspace, size_t workspace_bytes, sfa_stream stream) {
+  sfa_status st = check_decode_args(q, kv8, block_table, seq_lens, topk_idx, B, Q, h, top_k, num_blocks, block_size,
+                                    max_blocks_per_seq, scale, n_splits);
+  if (st != SFA_OK) return st;
+  if (interleave_size < 0 || (flags & ~(SFA_BLOCK_TABLE_PER_TOKEN | SFA_OUT_BF16)) != 0 || group < 1 ||
+      block_size % group != 0)
+    return SFA_ERR_INVALID_ARG;
+  if ((long long)num_blocks * block_size > INT_MAX) return SFA_ERR_UNSUPPORTED;
+  const int T = B * Q;
+  if (T == 0) return SFA_OK;
+  if (!scales || !aligned(scales, 4)) return SFA_ERR_INVALID_ARG;
+  const bool merge_after = n_splits > 1 && out && lse;
+  if (n_splits == 1) {
+    if (!out || !lse) return SFA_ERR_INVALID_ARG;
+  } else {
+    if (!out_part || !lse_part || !aligned(out_part, 16) || !aligned(lse_part, 4)) return SFA_ERR_INVALID_ARG;
+    if ((out && !lse) || (!out && lse)) return SFA_ERR_INVALID_ARG;
+  }
+  if (out && (!aligned(out, 16) || !aligned(lse, 4))) return SFA_ERR_INVALID_ARG;
+  const size_t need = sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits);
+  if (need == 0 || !workspace || workspace_bytes < need || !aligned(workspace, 256)) {
+    workspace = nullptr;
+    workspace_bytes = 0;
+  }
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SFA_ERR_CUDA;
+  int* status = status_word(dev);
+  if (!status) return SFA_ERR_CUDA;
+
+  sfa::DecodeQ8Params qp;
+  memset(&qp, 0, sizeof qp);
+  sfa::DecodeParams& p = qp.p;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv = static_cast<const __nv_bfloat16*>(kv8);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.topk_idx = topk_idx;
+  p.B = B;
+  p.Q = Q;
+  p.h = h;
+  p.top_k = top_k;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.scale = scale;
+  p.n_splits = n_splits;
+  p.out = n_splits == 1 ? static_cast<float*>(out) : out_part;
+  p.lse = n_splits == 1 ? lse : lse_part;
+  p.workspace = workspace;
+  p.workspace_bytes = workspace_bytes;
+  p.status = status;
+  const long long wl = g_wait_limit.load();
+  p.wait_limit = wl > 0 ? wl : kDefaultWaitLimit;
+  p.interleave = interleave_size;
+  p.bt_per_token = (flags & SFA_BLOCK_TABLE_PER_TOKEN) ? 1 : 0;
+  p.stall = g_stall.load();
+  qp.scales = scales;
+  qp.group = group;
+  const int bf16 = (flags & SFA_OUT_BF16) ? 1 : 0;
+  qp.out_bf16 = n_splits == 1 ? bf16 : 0;
+
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (sfa::launch_decode_q8_simt(qp, s) != cudaSuccess) return SFA_ERR_CUDA;
+  if (merge_after &&
+      sfa::launch_lse_merge(out_part, lse_part, n_splits, T * h, SFA_D_V, out, bf16, lse, s) != cudaSuccess)
+    return SFA_ERR_CUDA;
+  return SFA_OK;
+}
+
+size_t sfa_kv_write_q8_workspace_bytes(long long num_slots, int group) {
+  if (num_slots <= 0 || group <= 1) return 0;
+  return (size_t)((num_slots + group - 1) / group) * sfa::kQ8RecordBytes;
+}
+
+sfa_status sfa_kv_write_q8(void* kv8, float* scales, long long num_slots, int group, const int32_t* slot_mapping,
+                           const void* rows, int T, void* workspace, size_t workspace_bytes, sfa_stream stream) {
+  if (T < 0 || num_slots < 0 || group < 1 || num_slots % group != 0) return SFA_ERR_INVALID_ARG;
+  if (group > sfa::kQ8MaxWriteGroup) return SFA_ERR_UNSUPPORTED;
+  if (T == 0) return SFA_OK;
+  if (!kv8 || !scales || !slot_mapping || !rows || !aligned(kv8, 16) || !aligned(rows, 16) ||
+      !aligned(slot_mapping, 4) || !aligned(scales, 4))
+    return SFA_ERR_INVALID_ARG;
+  const size_t need = sfa_kv_write_q8_workspace_bytes(num_slots, group);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return SFA_ERR_WORKSPACE;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SFA_ERR_CUDA;
+  int* status = status_word(dev);
+  if (!status) return SFA_ERR_CUDA;
+  return sfa::launch_kv_write_q8(kv8, scales, num_slots, group, slot_mapping, rows, T, workspace, status,
+                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SFA_OK
+             : SFA_ERR_CUDA;
+}
+
+sfa_status sfa_step_plan(const int32_t* cached_lens, const int32_t* new_lens, int B, int block_size,
+                         int32_t* block_table, int max_blocks_per_seq, const int32_t* free_blocks, int num_free,
+                         const int32_t* taken, int num_tokens, int32_t* seq_lens, int32_t* token_start,
+                         int32_t* positions, int32_t* slot_mapping, int32_t* taken_out, sfa_stream stream) {
+  if (B < 0 || block_size < 1 || max_blocks_per_seq < 1 || num_free < 0 || num_tokens < 0) return SFA_ERR_INVALID_ARG;
+  if (B > sfa::kPlanMaxRequests) return SFA_ERR_UNSUPPORTED;
+  if (!taken || !taken_out || taken == taken_out || !token_start || (num_tokens > 0 && (!positions || !slot_mapping)) ||
+      (num_free > 0 && !free_blocks) || (B > 0 && (!cached_lens || !new_lens || !block_table || !seq_lens)))
+    return SFA_ERR_INVALID_ARG;
+  if (seq_lens && (seq_lens == cached_lens || seq_lens == new_lens)) return SFA_ERR_INVALID_ARG;
+  for (const void* ptr : {(const void*)cached_lens, (const void*)new_lens, (const void*)block_table,
+                          (const void*)free_blocks, (const void*)taken, (const void*)seq_lens,
+                          (const void*)token_start, (const void*)positions, (const void*)slot_mapping,
+                          (const void*)taken_out})
+    if (!aligned(ptr, 4)) return SFA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SFA_ERR_CUDA;
+  int* status = status_word(dev);
+  if (!status) return SFA_ERR_CUDA;
+  return sfa::launch_step_plan(cached_lens, new_lens, B, block_size, block_table, max_blocks_per_seq, free_blocks,
+                               num_free, taken, num_tokens, seq_lens, token_start, positions, slot_mapping,
+                               taken_out, status, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? SFA_OK
+             : SFA_ERR_CUDA;
+}
+
+static_assert(SFA_PLAN_MAX_REQUESTS == sfa::kPlanMaxRequests && SFA_Q8_MAX_WRITE_GROUP == sfa::kQ8MaxWriteGroup,
+              "limits of the header and the kernels");
+
+sfa_status sfa_rope(const void* x, long long x_token_stride, long long x_head_stride, void* out,
+                    long long out_token_stride, long long out_head_stride, int dtype, int T, int n, int width,
+                    int rot_dim, const int32_t* positions, const double* inv_freq, float mscale, int flags,
+                    sfa_stream stream) {
+  if (T < 0 || n < 1 || width < 1 || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > width || !isfinite(mscale) ||
+      dtype < 0 || dtype > 2 || (flags & ~(SFA_ROPE_INTERLEAVED | SFA_ROPE_INVERSE)) != 0)
+    return SFA_ERR_INVALID_ARG;
+  if (rot_dim > SFA_ROPE_MAX_DIM) return SFA_ERR_UNSUPPORTED;
+  if (T == 0) return SFA_OK;
+  const size_t size = dtype == SFA_DTYPE_FP32 ? 4 : 2;
+  if (!x || !out || !positions || !inv_freq || !aligned(x, size) || !aligned(out, size) || !aligned(positions, 4) ||
+      !aligned(inv_freq, 8))
+    return SFA_ERR_INVALID_ARG;
+  if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
+    return SFA_ERR_INVALID_ARG;
+  return sfa::launch_rope(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, dtype, T, n, width,
+                          rot_dim, positions, inv_freq, (flags & SFA_ROPE_INTERLEAVED) ? 1 : 0,
+                          (flags & SFA_ROPE_INVERSE) ? 1 : 0, mscale,
+                          static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SFA_OK
              : SFA_ERR_CUDA;
 }

@@ -19,6 +19,11 @@ constexpr int kTopkMaxS = 8 * kTopkChunkMax;          // a cluster of at most 8 
 // Device status codes (mirror sfa_status values).
 constexpr int kStatusTimeout = -5;
 constexpr int kStatusBadBlock = -6;
+constexpr int kStatusNoBlocks = -7;
+
+constexpr int kPlanMaxRequests = 8192;   // requests of one step plan (two prefix sums in shared memory)
+constexpr int kQ8MaxWriteGroup = 64;     // slots of a scale group that the 8-bit cache write handles
+constexpr int kQ8RecordBytes = 32;       // its workspace per group
 
 // One decode problem as the kernels see it.  Pointers are device pointers.
 struct DecodeParams {
@@ -39,6 +44,15 @@ struct DecodeParams {
   int interleave;         // > 0: shard r holds positions p with (p / interleave) % n_splits == r
   int bt_per_token;       // block_table has one row per query token (else one per sequence)
   int stall;              // test hook: first wait on a barrier that nothing completes
+};
+
+// The same problem over an 8-bit cache: p.kv is e4m3 [num_blocks, block_size, 576], and the
+// value of a row's element is e4m3 * scales[row / group].
+struct DecodeQ8Params {
+  DecodeParams p;
+  const float* scales;   // [num_blocks * block_size / group]
+  int group;
+  int out_bf16;          // p.out is bf16 (the final result; partials are fp32)
 };
 
 // Record the first device-side error in the status word (never traps).
@@ -107,8 +121,21 @@ cudaError_t launch_topk(const float* scores, long long row_stride, const int32_t
                         int k, int32_t* out, cudaStream_t stream);
 cudaError_t launch_kv_write(void* kv, long long num_slots, const int32_t* slot_mapping, const void* rows, int T,
                             int* status, cudaStream_t stream);
+// out_bf16: `out` holds bf16 (512-wide rows only)
 cudaError_t launch_lse_merge(const float* out_part, const float* lse_part, int n_splits, int rows,
-                             int dv, float* out, float* lse, cudaStream_t stream);
+                             int dv, void* out, int out_bf16, float* lse, cudaStream_t stream);
+cudaError_t launch_decode_q8_simt(const DecodeQ8Params& p, cudaStream_t stream);
+cudaError_t launch_kv_write_q8(void* kv8, float* scales, long long num_slots, int group, const int32_t* slots,
+                               const void* rows, int T, void* workspace, int* status, cudaStream_t stream);
+cudaError_t launch_step_plan(const int32_t* cached, const int32_t* fresh_tokens, int B, int block_size,
+                             int32_t* table, int max_blocks, const int32_t* free_blocks, int num_free,
+                             const int32_t* taken, int num_tokens, int32_t* seq_lens, int32_t* token_start,
+                             int32_t* positions, int32_t* slots, int32_t* taken_out, int* status,
+                             cudaStream_t stream);
+// dtype: 0 bf16, 1 fp16, 2 fp32; strides in elements
+cudaError_t launch_rope(const void* x, long long xt, long long xn, void* out, long long ot, long long on, int dtype,
+                        int T, int n, int width, int rot, const int32_t* pos, const double* inv_freq,
+                        int interleaved, int inverse, float mscale, cudaStream_t stream);
 
 // tcgen05 path: whether it handles this problem, its workspace, and its launch.  Three
 // kernels: the CTA-pair kernel (any h <= 128), the small-head kernel (h <= 32) and the

@@ -5,7 +5,8 @@
 // online-softmax merge; 2.1.4.3: the partials travel in fp32.  Here the shards
 // are all on one GPU and the merge is a streaming kernel: one warp per output
 // row, the n lse values spread over the lanes, 16-byte loads of the partial
-// rows, one pass over the data.
+// rows, one pass over the data.  The result is fp32, or bf16 for a caller that asks for it
+// (sums in fp32, one rounding at the end).
 #include "sfa_internal.h"
 
 namespace sfa {
@@ -22,11 +23,17 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+__device__ __forceinline__ void put4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, float4 v) {
+  __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
 // n <= 64: lane holds shards `lane` and `lane + 32`.
-template <bool kVec4>
+template <bool kVec4, typename Out>
 __global__ void __launch_bounds__(256) lse_merge_kernel(const float* __restrict__ out_part,
                                                         const float* __restrict__ lse_part, int n,
-                                                        int rows, int dv, float* __restrict__ out,
+                                                        int rows, int dv, Out* __restrict__ out,
                                                         float* __restrict__ lse) {
   const int lane = threadIdx.x & 31;
   const int warps_per_block = blockDim.x >> 5;
@@ -36,9 +43,9 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(const float* __restrict_
     const float l0 = lane < n ? lse_part[(size_t)lane * rows + row] : -INFINITY;
     const float l1 = lane + 32 < n ? lse_part[(size_t)(lane + 32) * rows + row] : -INFINITY;
     const float M = warp_max(fmaxf(l0, l1));
-    float* orow = out + (size_t)row * dv;
+    Out* orow = out + (size_t)row * dv;
     if (M == -INFINITY) {
-      for (int c = lane; c < dv; c += 32) orow[c] = 0.f;
+      for (int c = lane; c < dv; c += 32) orow[c] = Out(0.f);
       if (lane == 0) lse[row] = -INFINITY;
       continue;
     }
@@ -64,7 +71,7 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(const float* __restrict_
           acc.z += w * v.z;
           acc.w += w * v.w;
         }
-        if (c < dv4) reinterpret_cast<float4*>(orow)[c] = acc;
+        if (c < dv4) put4(orow + 4 * c, acc);
       }
     } else {
       for (int c0 = 0; c0 < dv; c0 += 32) {
@@ -75,7 +82,7 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(const float* __restrict_
           if (w == 0.f || c >= dv) continue;
           acc += w * out_part[((size_t)r * rows + row) * dv + c];
         }
-        if (c < dv) orow[c] = acc;
+        if (c < dv) orow[c] = Out(acc);
       }
     }
     if (lane == 0) lse[row] = L;
@@ -88,9 +95,10 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(const float* __restrict_
 constexpr int kFastShards = 8;
 constexpr int kFastCols4 = 512 / 4 / 32;   // float4 columns per lane
 
+template <typename Out>
 __global__ void __launch_bounds__(256) lse_merge_fast_kernel(const float* __restrict__ out_part,
                                                              const float* __restrict__ lse_part, int n,
-                                                             int rows, float* __restrict__ out,
+                                                             int rows, Out* __restrict__ out,
                                                              float* __restrict__ lse) {
   const int lane = threadIdx.x & 31;
   const int warps_per_block = blockDim.x >> 5;
@@ -136,40 +144,45 @@ __global__ void __launch_bounds__(256) lse_merge_fast_kernel(const float* __rest
         acc[j0 + jj] = a;
       }
     }
-    float4* orow = reinterpret_cast<float4*>(out + (size_t)row * 512) + lane;
+    Out* orow = out + (size_t)row * 512 + 4 * lane;
 #pragma unroll
-    for (int j = 0; j < kFastCols4; ++j) orow[32 * j] = empty ? make_float4(0.f, 0.f, 0.f, 0.f) : acc[j];
+    for (int j = 0; j < kFastCols4; ++j) put4(orow + 128 * j, empty ? make_float4(0.f, 0.f, 0.f, 0.f) : acc[j]);
     if (lane == 0) lse[row] = empty ? -INFINITY : L;
   }
 }
 
-}  // namespace
-
-cudaError_t launch_lse_merge(const float* out_part, const float* lse_part, int n_splits, int rows,
-                             int dv, float* out, float* lse, cudaStream_t stream) {
-  if (rows == 0) return cudaSuccess;
-  int dev = 0, sms = 148;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+template <typename Out>
+cudaError_t launch_merge_t(const float* out_part, const float* lse_part, int n_splits, int rows, int dv, Out* out,
+                           float* lse, cudaStream_t stream) {
   // small blocks (one warp a row, two rows a block) spread the rows evenly over the SMs:
   // with eight-warp blocks a short merge gave some SMs a third more rows than others
   const int warps_per_block = 2;
   long long blocks = ((long long)rows + warps_per_block - 1) / warps_per_block;
-  const long long cap = (long long)sms * 32;   // resident 64-thread blocks per SM
+  const long long cap = (long long)device_sm_count() * 32;   // resident 64-thread blocks per SM
   if (blocks > cap) blocks = cap;
   const bool vec4 = (dv % 4) == 0;
   const bool fast = dv == 512 && n_splits <= kFastShards && (reinterpret_cast<uintptr_t>(out_part) % 16) == 0 &&
                     (reinterpret_cast<uintptr_t>(out) % 16) == 0;
   if (fast)
-    lse_merge_fast_kernel<<<(int)blocks, warps_per_block * 32, 0, stream>>>(out_part, lse_part, n_splits, rows,
-                                                                            out, lse);
+    lse_merge_fast_kernel<Out><<<(int)blocks, warps_per_block * 32, 0, stream>>>(out_part, lse_part, n_splits, rows,
+                                                                                 out, lse);
   else if (vec4)
-    lse_merge_kernel<true><<<(int)blocks, warps_per_block * 32, 0, stream>>>(
-        out_part, lse_part, n_splits, rows, dv, out, lse);
+    lse_merge_kernel<true, Out><<<(int)blocks, warps_per_block * 32, 0, stream>>>(out_part, lse_part, n_splits,
+                                                                                  rows, dv, out, lse);
   else
-    lse_merge_kernel<false><<<(int)blocks, warps_per_block * 32, 0, stream>>>(
-        out_part, lse_part, n_splits, rows, dv, out, lse);
+    lse_merge_kernel<false, Out><<<(int)blocks, warps_per_block * 32, 0, stream>>>(out_part, lse_part, n_splits,
+                                                                                   rows, dv, out, lse);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_lse_merge(const float* out_part, const float* lse_part, int n_splits, int rows,
+                             int dv, void* out, int out_bf16, float* lse, cudaStream_t stream) {
+  if (rows == 0) return cudaSuccess;
+  return out_bf16 ? launch_merge_t(out_part, lse_part, n_splits, rows, dv, static_cast<__nv_bfloat16*>(out), lse,
+                                   stream)
+                  : launch_merge_t(out_part, lse_part, n_splits, rows, dv, static_cast<float*>(out), lse, stream);
 }
 
 }  // namespace sfa

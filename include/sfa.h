@@ -42,7 +42,8 @@ typedef enum {
   SFA_ERR_WORKSPACE = -3,      /* workspace / staging buffer missing or too small              */
   SFA_ERR_CUDA = -4,           /* a CUDA runtime call failed (launch error, copy error)        */
   SFA_ERR_DEVICE_TIMEOUT = -5, /* a bounded device-side wait gave up (device status only)      */
-  SFA_ERR_DEVICE_BAD_BLOCK = -6 /* a selected position mapped to an invalid block (device)     */
+  SFA_ERR_DEVICE_BAD_BLOCK = -6, /* a selected position mapped to an invalid block (device)    */
+  SFA_ERR_DEVICE_NO_BLOCKS = -7 /* a step plan ran out of blocks, table or token room (device) */
 } sfa_status;
 
 typedef void *sfa_stream; /* a cudaStream_t */
@@ -228,6 +229,127 @@ sfa_status sfa_kv_write(void *kv, long long num_slots, const int32_t *slot_mappi
 sfa_status sfa_uv_proj(const float *out, const void *w_uv, void *y, int T, int h, sfa_stream stream);
 
 /*
+ * sfa_decode_q8 -- sfa_decode over an 8-bit latent cache.  An MLA cache has one latent
+ * "head", so a scale belongs to a group of consecutive slots: the value of column c of slot
+ * s is e4m3(kv8[s, c]) * scales[s / group], and with it every formula is sfa_decode's.
+ *
+ *   kv8         device, e4m3 bytes [num_blocks, block_size, 576]; 16-byte aligned
+ *   scales      device, fp32 [num_blocks, block_size / group], finite, positive (sfa_kv_write_q8
+ *               writes powers of two; any others are taken as they are)
+ *   group       slots per scale: >= 1, divides block_size
+ *   interleave_size, flags  as in sfa_decode_ex; SFA_OUT_BF16: `out` is bf16 [B*Q, h, 512]
+ *               (16-byte aligned) instead of fp32.  lse and the shard partials are fp32.
+ *   workspace   optional, as in sfa_decode (sfa_decode_q8_workspace_bytes)
+ *   num_blocks * block_size <= INT_MAX (SFA_ERR_UNSUPPORTED above).
+ * Everything else, and the return codes, as in sfa_decode_ex.
+ *
+ * Accuracy: lse carries fp32 rounding only (q is exact to 2^-18 of its head's largest value);
+ * out, whatever its type, carries the rounding of the softmax weights to 8 significant bits,
+ * about 2^-9 of its norm (as sfa_decode's bf16 weights do), and then that of its own type.
+ */
+#define SFA_OUT_BF16 2
+size_t sfa_decode_q8_workspace_bytes(int B, int Q, int h, int top_k, int n_splits);
+sfa_status sfa_decode_q8(const void *q, const void *kv8, const float *scales, int group,
+                         const int32_t *block_table, const int32_t *seq_lens, const int32_t *topk_idx, int B, int Q,
+                         int h, int top_k, int num_blocks, int block_size, int max_blocks_per_seq, float scale,
+                         int n_splits, int interleave_size, int flags, void *out, float *lse, float *out_part,
+                         float *lse_part, void *workspace, size_t workspace_bytes, sfa_stream stream);
+
+/*
+ * sfa_kv_write_q8 -- sfa_kv_write into the 8-bit latent cache sfa_decode_q8 reads.
+ *
+ * For each group G of `group` slots that slot_mapping names:
+ *   before = 0 if the call writes G's first slot (the group starts anew), else scales[G]
+ *            (taken as 0 unless positive and finite)
+ *   after  = max(before, 2^k over the call's rows of G), 2^k the least power of two with
+ *            amax / 2^k <= 448, -100 <= k <= 120, amax the row's largest finite magnitude
+ *   the call's rows are stored as e4m3(x / after), rounded to nearest even; if 0 < before <
+ *   after, G's other rows are stored again as e4m3(value * before / after); scales[G] = after
+ * An infinity is stored as NaN (e4m3 has none); NaN stays NaN.
+ *
+ *   kv8           device, e4m3 bytes [num_slots, 576], in place; 16-byte aligned
+ *   scales        device, fp32 [num_slots / group], in place
+ *   num_slots     a multiple of group; 1 <= group <= SFA_Q8_MAX_WRITE_GROUP
+ *   slot_mapping  device int32 [T]; < 0 = padding; a slot >= num_slots writes nothing and sets
+ *                 SFA_ERR_DEVICE_BAD_BLOCK in the device status word
+ *   rows          device bf16 [T, 576]; 16-byte aligned
+ *   workspace     device, sfa_kv_write_q8_workspace_bytes(num_slots, group) bytes, 16-byte
+ *                 aligned (none for group 1; SFA_ERR_WORKSPACE when missing or too small).  It
+ *                 belongs to one cache, is zero before the first call and is left zero by every
+ *                 call; calls on the same cache must not overlap.
+ * A slot named twice ends up holding parts of its rows (as sfa_kv_write's); the rest of the
+ * group is unaffected.
+ */
+#define SFA_Q8_MAX_WRITE_GROUP 64
+size_t sfa_kv_write_q8_workspace_bytes(long long num_slots, int group);
+sfa_status sfa_kv_write_q8(void *kv8, float *scales, long long num_slots, int group, const int32_t *slot_mapping,
+                           const void *rows, int T, void *workspace, size_t workspace_bytes, sfa_stream stream);
+
+/*
+ * sfa_step_plan -- block tables and slot maps of one step from request lengths, on the GPU
+ * ("RFC: MsModeling 支持 Decode Context Parallel 仿真", 2.1.4.1: block_table and slot_mapping).
+ *
+ * Request b has c = cached_lens[b] positions in the cache and gets n = new_lens[b] more
+ * (negative lengths count as 0).  It holds ceil(c / block_size) blocks, its table's first
+ * entries, and needs ceil((c + n) / block_size) of them; what it lacks is taken from
+ * free_blocks, from entry *taken on, in request order.  With start_b the new tokens of the
+ * requests before b, the step's token i = start_b + j is position c + j of request b.
+ *
+ *   cached_lens, new_lens  device int32 [B]; 0 <= B <= SFA_PLAN_MAX_REQUESTS
+ *   block_table   device int32 [B, max_blocks_per_seq], in place: the entries of the blocks
+ *                 taken are written, no others
+ *   free_blocks   device int32 [num_free]: physical blocks no request holds
+ *   taken         device int32 [1]: entries of free_blocks taken by earlier steps
+ *   num_tokens    rows of positions and slot_mapping (the step's room for tokens)
+ *   seq_lens      device int32 [B]: c + n                    (what sfa_decode and sfa_topk take)
+ *   token_start   device int32 [B + 1]: start_b, and the number of new tokens last
+ *   positions     device int32 [num_tokens]: a token's position; -1 behind the last one
+ *   slot_mapping  device int32 [num_tokens]: its slot, block * block_size + position %
+ *                 block_size; -1 (which the cache writes skip) behind the last one
+ *   taken_out     device int32 [1]: *taken plus the blocks taken, at most num_free
+ * The outputs must not overlap the inputs (block_table apart), so that taken and taken_out
+ * change places from step to step.  A call repeated with the same inputs gives the same
+ * outputs.  A table whose width, a free list whose length or a room whose size does not
+ * suffice sets SFA_ERR_DEVICE_NO_BLOCKS in the device status word: table entries that find no
+ * block are -1, so are the slots of the tokens in them, and tokens without room are left out.
+ * A negative entry of a held or free block gives slot -1 and SFA_ERR_DEVICE_BAD_BLOCK.
+ */
+#define SFA_PLAN_MAX_REQUESTS 8192
+sfa_status sfa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, int B, int block_size,
+                         int32_t *block_table, int max_blocks_per_seq, const int32_t *free_blocks, int num_free,
+                         const int32_t *taken, int num_tokens, int32_t *seq_lens, int32_t *token_start,
+                         int32_t *positions, int32_t *slot_mapping, int32_t *taken_out, sfa_stream stream);
+
+/*
+ * sfa_rope -- rotary positions of part of each head: the rope columns of queries (before
+ * sfa_decode) and of new latent rows (before the cache write).
+ *
+ * For token t, head j and pair i < rot_dim / 2, with a = positions[t] * inv_freq[i]:
+ *   (u, v) = mscale * (x cos a - y sin a, x sin a + y cos a)
+ * where (x, y) and (u, v) are columns (2i, 2i + 1) with SFA_ROPE_INTERLEAVED, else
+ * (i, i + rot_dim / 2).  SFA_ROPE_INVERSE turns by -a: the transpose, which takes the gradient
+ * of (u, v) to that of (x, y).  Columns rot_dim .. width - 1 are copied.  The angle is reduced
+ * exactly for every position; arithmetic is fp32, rounded once to the type.
+ *
+ *   x, out      device, element (t, j, d) at t * token_stride + j * head_stride + d (strides in
+ *               elements): bf16, fp16 or fp32 (dtype), T tokens of n heads.  out may be x
+ *               itself (same strides); otherwise the two must not overlap.
+ *   positions   device int32 [T]; < 0 = padding: that token's rows of out are left as they were
+ *   inv_freq    device double [rot_dim / 2]: radians a position
+ *   2 <= rot_dim <= SFA_ROPE_MAX_DIM, even, <= width
+ */
+#define SFA_ROPE_INTERLEAVED 1
+#define SFA_ROPE_INVERSE 2
+#define SFA_ROPE_MAX_DIM 512
+#define SFA_DTYPE_BF16 0
+#define SFA_DTYPE_FP16 1
+#define SFA_DTYPE_FP32 2
+sfa_status sfa_rope(const void *x, long long x_token_stride, long long x_head_stride, void *out,
+                    long long out_token_stride, long long out_head_stride, int dtype, int T, int n, int width,
+                    int rot_dim, const int32_t *positions, const double *inv_freq, float mscale, int flags,
+                    sfa_stream stream);
+
+/*
  * sfa_decode_host -- one decode step whose per-step inputs and outputs live in
  * host memory, with the latent cache resident on the device (the form a serving
  * loop that keeps its cache in HBM uses).  Enqueues on `stream`: host->device
@@ -292,7 +414,8 @@ void sfa_host_plan_destroy(sfa_host_plan plan);
  * current device's status word: SFA_OK, SFA_ERR_DEVICE_TIMEOUT (a bounded wait
  * inside a kernel gave up; that kernel's outputs are undefined) or
  * SFA_ERR_DEVICE_BAD_BLOCK (a selected position's block-table entry was outside
- * [0, num_blocks); that row was skipped).  SFA_ERR_CUDA if the stream itself failed.
+ * [0, num_blocks); that row was skipped) or SFA_ERR_DEVICE_NO_BLOCKS (sfa_step_plan).
+ * The first error since the last read is kept.  SFA_ERR_CUDA if the stream itself failed.
  */
 sfa_status sfa_last_device_status(sfa_stream stream);
 
