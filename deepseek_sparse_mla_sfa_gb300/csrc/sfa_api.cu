@@ -549,7 +549,9 @@ sfa_status sfa_decode_q8(const void* q, const void* kv8, const float* scales, in
   qp.out_bf16 = n_splits == 1 ? bf16 : 0;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (sfa::launch_decode_q8_simt(qp, s) != cudaSuccess) return SFA_ERR_CUDA;
+  // kernel path 1: the CUDA-core kernel, to cross-check; else the tensor cores' (every shape)
+  const cudaError_t e = g_kernel_path.load() == 1 ? sfa::launch_decode_q8_simt(qp, s) : sfa::launch_decode_q8(qp, s);
+  if (e != cudaSuccess) return SFA_ERR_CUDA;
   if (merge_after &&
       sfa::launch_lse_merge(out_part, lse_part, n_splits, T * h, SFA_D_V, out, bf16, lse, s) != cudaSuccess)
     return SFA_ERR_CUDA;

@@ -125,6 +125,7 @@ cudaError_t launch_kv_write(void* kv, long long num_slots, const int32_t* slot_m
 cudaError_t launch_lse_merge(const float* out_part, const float* lse_part, int n_splits, int rows,
                              int dv, void* out, int out_bf16, float* lse, cudaStream_t stream);
 cudaError_t launch_decode_q8_simt(const DecodeQ8Params& p, cudaStream_t stream);
+cudaError_t launch_decode_q8(const DecodeQ8Params& p, cudaStream_t stream);   // the tcgen05 kernel
 cudaError_t launch_kv_write_q8(void* kv8, float* scales, long long num_slots, int group, const int32_t* slots,
                                const void* rows, int T, void* workspace, int* status, cudaStream_t stream);
 cudaError_t launch_step_plan(const int32_t* cached, const int32_t* fresh_tokens, int B, int block_size,

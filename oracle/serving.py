@@ -81,7 +81,8 @@ def kv_write_q8(codes, scales, slots, rows, group):
 def decode_q8(q, codes, scales, group, block_table, seq_lens, topk_idx, scale, Q=1, n_splits=1, interleave=0,
               bt_per_token=False):
     """Shard partials (out [n, T, h, 512], lse [n, T, h]) in fp64 and, for bounds, sum_j w_j |v_j|
-    [n, T, h, 512] and wmax * sum_j |v_j| [n, T, h, 512] (w the softmax weights).  q float64
+    and max_j(w_j c_j) * sum_j |e_j|, both [n, T, h, 512] (w the softmax weights, v = c e with c
+    a row's scale and e its e4m3 values).  q float64
     [T, h, 576], codes uint8 [num_blocks, block_size, 576], scales float64 [num_blocks, groups]."""
     T, h, _ = q.shape
     bs = codes.shape[1]
@@ -106,7 +107,8 @@ def decode_q8(q, codes, scales, group, block_table, seq_lens, topk_idx, scale, Q
                 sc.append(scales[blk, (p % bs) // group])
             if not rows:
                 continue
-            k = E4M3[np.array(rows)] * np.array(sc)[:, None]
+            e4, c4 = E4M3[np.array(rows)], np.array(sc)
+            k = e4 * c4[:, None]
             s = scale * (q[t] @ k.T)
             m = s.max(axis=1, keepdims=True)
             e = np.exp(s - m)
@@ -116,7 +118,7 @@ def decode_q8(q, codes, scales, group, block_table, seq_lens, topk_idx, scale, Q
             out[r, t] = w @ v
             lse[r, t] = (m + np.log(z))[:, 0]
             wabs[r, t] = w @ np.abs(v)
-            wmax[r, t] = w.max(axis=1)[:, None] * np.abs(v).sum(axis=0)[None, :]
+            wmax[r, t] = (w * c4).max(axis=1)[:, None] * np.abs(e4[:, :D_V]).sum(axis=0)[None, :]
     return out, lse, wabs, wmax
 
 
