@@ -18,11 +18,12 @@
 //
 // One CTA handles one unit (query token, shard, group of up to 64 heads), whole rows, no
 // exchange per tile:
-//   * tiles of 96 rows, 3 stages; each row's 576 bytes go to shared memory by 16-byte
-//     cp.async into the swizzled operand layout (4 column blocks of 128 bytes, SW128, and
-//     the 64 rope bytes, SW64).  An SM's TMA unit needs ~15 ns for a tile::gather4, five of
-//     which cover four rows: 1.8 us a tile, more than the matrix instructions take; the
-//     copies of four warps are not bound by that unit.
+//   * tiles of 96 rows, 3 stages, in the swizzled operand layout: 4 column blocks of 128
+//     latent bytes a row (SW128) by TMA tile::gather4, and the 64 rope bytes (SW64) by 16-byte
+//     cp.async.  An SM's TMA unit takes ~15 ns a gather4 whatever its size, so the half-width
+//     rope boxes would add a quarter to the 1.44 us of the latent ones; as cp.async they are 12
+//     instructions a tile.  (All 36 words of a row by cp.async: 5000 cycles a tile, and the
+//     softmax's shuffles wait behind them in the same unit.)
 //   * QK^T: S[heads hi|lo, rows] += q[128, 32] E^T, 18 steps, q in TMEM, N = 96;
 //   * P.V transposed, O^T[columns, heads] += E^T[128 columns, 32 rows] P^T: four blocks of
 //     128 columns, 3 K steps each for hi and lo, N = padded heads.  E^T is the same tile read
@@ -32,12 +33,14 @@
 // With few units a cluster of G CTAs shares one: CTA c takes tiles c, c + G, ...; they merge
 // (O, m, l) over distributed shared memory at the end.
 //
-// Warp roles (320 threads): warps 0-3 softmax, O rescale and output (warp w owns TMEM lanes
-// 32w..32w+31: 16 heads' hi rows and the same heads' lo rows); warps 4-7 gathers; warp 8
-// issues QK^T, warp 9 P.V.  Every wait is bounded; one that gives up records
-// SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
+// Warp roles (384 threads): warps 0-7 softmax, O rescale and output (warps w and w + 4 share
+// the TMEM lanes 32 (w % 4) ..: 16 heads' hi rows and the same heads' lo rows); warp 8 issues
+// QK^T, warp 9 P.V, warps 10 and 11 the gathers.  Every wait is bounded; one that gives up
+// records SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
 #include <atomic>
+#include <cuda.h>
 #include <cuda_fp16.h>
+#include <mutex>
 #include <string.h>
 
 #include "sfa_internal.h"
@@ -51,9 +54,10 @@ using namespace ptx;
 
 constexpr int kNt = 96;              // selected rows per tile: N of QK^T, K of P.V
 constexpr int kStages = 3;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kWarps = kThreads / 32;
-constexpr int kProducerWarp = 4, kProducerWarps = 4, kQkWarp = 8, kPvWarp = 9;
+constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
+constexpr int kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 2;
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPeak = 4.0f;        // log2 of P at the maximum a reference is taken from
@@ -68,10 +72,8 @@ constexpr int kOffList = kOffP + 4 * kPBytes;         // two buffers of hi and l
 constexpr int kListCap = 48 * kNt;                    // resolved rows kept at once (whole tiles)
 constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and row: (scale, ceil log2 scale)
 constexpr int kOffMisc = kOffScale + kStages * kNt * 8;
-// misc: (m, l) per head [64] float2; rescale factors [2][64]; partial maxima [2][4][32]; output
-// scales [64]; partial sums [4][32]; flags [16]; TMEM address; per-warp counts
-constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscMax = 1024, kMiscScale = 2048, kMiscSum = 2304,
-              kMiscFlags = 2816, kMiscTmem = 2880, kMiscCount = 2896, kMiscBytes = 2944;
+constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscMax = 1024, kMiscScale = 3072, kMiscSum = 3328,
+              kMiscC = 4352, kMiscFlags = 4608, kMiscTmem = 4624, kMiscCount = 4640, kMiscBytes = 4704;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
 constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarQReady = kBarKvEmpty + kStages,
               kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarPReady = kBarSFree + 2,
@@ -81,17 +83,22 @@ constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kBlk % 1024 == 0 && kStageBytes % 1024 == 0 && kOffP % 1024 == 0, "operands: 1024-byte alignment");
 static_assert(kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
-static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the cluster merge's buffer fits in the stages");
+static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the output and the cluster merge fit in the stages");
+static_assert(kMiscSum + 4 * 32 * kSoftWarps <= kMiscC && kMiscMax + 4 * 2 * 256 <= kMiscScale, "misc");
+// q's e4m3 rows on their way to TMEM, in stages 1 and 2: 128 rows (64 hi, 64 lo) of 576 bytes
+constexpr int kQPitch = 592;   // an odd number of 16-byte words: rows start in different banks
+static_assert(128 * kQPitch <= 2 * kStageBytes, "q fits in stages 1 and 2");
 static_assert(kMiscCount + 4 * kWarps <= kMiscBytes, "misc");
 
 constexpr long long kDrainLimit = 1LL << 40;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kColQ = 0, kColS = 160, kColO = 256, kColS1 = 400;
+constexpr uint32_t kColQ = 0, kColS = 160, kColO = 256, kColS1 = 400;   // S1 for up to 32 heads
 
 struct Q8Params {
   DecodeQ8Params qp;
   int groups;        // head groups of a token
   int group_heads;   // heads of a group (the last may have fewer)
+  int num_rows;      // rows of the cache: the index that the gathers read as zeros
 };
 
 // D[tmem] (+)= A * B, e4m3 operands, fp32 accumulation
@@ -147,37 +154,88 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
+// named barrier that also ORs a predicate over its threads
+__device__ __forceinline__ bool barrier_or(int id, int count, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %3, 0;\n\t"
+      "bar.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"((uint32_t)v)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void bulk_store_s2g(void* dst, uint32_t src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
+               : "memory");
+}
+
+// One lane's share of a warp's chunk [c_begin, c_end) of the selected list, E entries a round
+// with their loads in flight together: counts those that resolve to a row of this unit and
+// leaves the last round's rows in row (-1 for entries that do not).
+template <int E, bool kInterleaved>
+__device__ __forceinline__ int resolve_round(const DecodeParams& p, const int32_t* idx, int c_begin, int c_end,
+                                             int lane, const ShardSel& sel, int bt_row, bool report, int* row) {
+  const int32_t* table = p.block_table + (size_t)bt_row * p.max_blocks;
+  int cnt = 0;
+  for (int j0 = c_begin; j0 < c_end; j0 += 32 * E) {
+    int pos[E];
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const int j = j0 + 32 * k + lane;
+      pos[k] = j < c_end ? __ldg(idx + j) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const bool in = sel.has_fixed<kInterleaved>(pos[k]);
+      const int blk = in ? pos[k] / p.block_size : 0;
+      pos[k] = in ? pos[k] - blk * p.block_size : -1;      // the offset in its block
+      row[k] = in && blk < p.max_blocks ? __ldg(table + blk) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      const bool valid = row[k] >= 0 && row[k] < p.num_blocks;
+      if (pos[k] >= 0 && !valid && report) report_status(p.status, kStatusBadBlock);
+      cnt += valid;
+      row[k] = valid ? row[k] * p.block_size + pos[k] : -1;
+    }
+  }
+  return cnt;
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
   return v;
 }
 
-// NH: padded heads of a unit (16, 32 or 64), the N of P.V
+// NH: padded heads of a unit (32 or 64), the N of P.V
 template <int NH, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params kp) {
-  static_assert(NH == 16 || NH == 32 || NH == 64, "padded head count");
-  constexpr int HB = NH / 16;        // blocks of 16 heads; warp w holds block w % HB
-  constexpr int R = 4 / HB;          // warps that hold the same heads share a tile's rows
-  constexpr int kCols = kNt / R;     // rows of a tile per warp: the hi lanes take the first
-  constexpr int kHalf = kCols / 2;   // half of them, the lo lanes the second
+__global__ void __launch_bounds__(kThreads, 1)
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tmap_rows, const __grid_constant__ Q8Params kp) {
+  static_assert(NH == 32 || NH == 64, "padded head count");
+  constexpr int HB = NH / 16;             // blocks of 16 heads: TMEM lanes 32x.. hold block x % HB
+  constexpr int R = kSoftWarps / HB;      // warps that hold the same heads share a tile's rows
+  constexpr int kCols = kNt / R;          // rows of a tile per warp: the hi lanes take the first
+  constexpr int kHalf = kCols / 2;        // half of them, the lo lanes the second
   constexpr int kSBufs = NH == 64 ? 1 : 2;
   const DecodeParams& p = kp.qp.p;
   extern __shared__ char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   int* list_s = reinterpret_cast<int*>(smem + kOffList);
-  float2* rows_s = reinterpret_cast<float2*>(smem + kOffScale);                // [kStages][kNt]
+  float2* rows_s = reinterpret_cast<float2*>(smem + kOffScale);          // [kStages][kNt]
   char* misc = smem + kOffMisc;
-  float2* ml_s = reinterpret_cast<float2*>(misc + kMiscMl);
-  float* alpha_s = reinterpret_cast<float*>(misc + kMiscAlpha);
-  float* max_s = reinterpret_cast<float*>(misc + kMiscMax);
-  float* scale_s = reinterpret_cast<float*>(misc + kMiscScale);
-  float* lpart_s = reinterpret_cast<float*>(misc + kMiscSum);
-  volatile int* flags_s = reinterpret_cast<volatile int*>(misc + kMiscFlags);   // [0] abort, [1] stop, [4 + 4 b + w] rescale
+  float2* ml_s = reinterpret_cast<float2*>(misc + kMiscMl);              // [64] (m, l)
+  float* alpha_s = reinterpret_cast<float*>(misc + kMiscAlpha);          // [2][64] rescale factors
+  float* max_s = reinterpret_cast<float*>(misc + kMiscMax);              // [2][R][NH] partial maxima
+  float* scale_s = reinterpret_cast<float*>(misc + kMiscScale);          // [64] output scales
+  float* lpart_s = reinterpret_cast<float*>(misc + kMiscSum);            // [8][32] partial sums
+  float* qc_s = reinterpret_cast<float*>(misc + kMiscC);                 // [64] score scale, NaN for a bad head
+  volatile int* abort_s = reinterpret_cast<volatile int*>(misc + kMiscFlags);
+  volatile int* stop_s = abort_s + 1;                                    // [2]
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(misc + kMiscTmem);
-  int* wcount_s = reinterpret_cast<int*>(misc + kMiscCount);
-  volatile int* abort_s = flags_s;
+  int* wcount_s = reinterpret_cast<int*>(misc + kMiscCount);             // [kWarps]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
@@ -195,44 +253,48 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
   const ShardSel sel = shard_sel(seq_len, seq_len - (p.Q - 1 - qi), r, p.n_splits, p.interleave);
   const int bt_row = p.bt_per_token ? t : b;
   const int32_t* idx = p.topk_idx + (size_t)t * p.top_k;
+  const uint4* qsrc = reinterpret_cast<const uint4*>(p.q + ((size_t)t * p.h + h0) * kDQK);
   const long long wl = p.wait_limit;
 
   // ---- set-up ----------------------------------------------------------------------
+  for (int x = threadIdx.x; x < nh * (kDQK * 2 / 128); x += kThreads) prefetch_l2(qsrc + 8 * x);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars[kBarKvFull + s], kProducerWarps);
+      mbar_init(&bars[kBarKvFull + s], 2 * kProducerWarps);   // each: its gathers issued, its copies landed
       mbar_init(&bars[kBarKvEmpty + s], 1);
     }
-    mbar_init(&bars[kBarQReady], 4);
+    mbar_init(&bars[kBarQReady], kSoftWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarSFull + x], 1);
-      mbar_init(&bars[kBarSFree + x], 4);
-      mbar_init(&bars[kBarPReady + x], 4);
+      mbar_init(&bars[kBarSFree + x], kSoftWarps);
+      mbar_init(&bars[kBarPReady + x], kSoftWarps);
       mbar_init(&bars[kBarPFree + x], 1);
     }
     mbar_init(&bars[kBarPvFinal], 1);
     mbar_init(&bars[kBarMmaFin], 1);
     mbar_init(&bars[kBarMmaFin2], 1);
     mbar_init(&bars[kBarNever], 1);         // nothing arrives: the stall test hook waits on it
-    for (int x = 0; x < 16; ++x) flags_s[x] = 0;
+    *abort_s = stop_s[0] = stop_s[1] = 0;
     fence_barrier_init();
   }
   if (warp == 0) {
     tmem_alloc(tmem_base_s, kTmemCols);
     tmem_relinquish();
   }
+  if (warp == kProducerWarp && lane == 0) prefetch_tmap(&tmap_rows);
 
   // ---- index resolution: count per warp chunk, then ordered compaction into smem ----
+  // up to 8 entries a thread are resolved in one round, then up to 24, longer lists in rounds
+  // of 24 and once more for the compaction
   const int chunk = ((p.top_k + kWarps * 32 - 1) / (kWarps * 32)) * 32;
   const int c_begin = min(warp * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
-  const bool one_round = chunk <= 8 * 32;
-  int row_r[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) row_r[k] = -1;
+  int row_r[24];
+  const bool rep = crank == 0 && hg == 0;
   {
-    int cnt = resolve_chunk<kInterleaved>(p, idx, c_begin, c_end, lane, sel, bt_row, crank == 0 && hg == 0, row_r);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) cnt += __shfl_xor_sync(0xffffffffu, cnt, o);
+    int cnt = chunk <= 8 * 32
+                  ? resolve_round<8, kInterleaved>(p, idx, c_begin, c_end, lane, sel, bt_row, rep, row_r)
+                  : resolve_round<24, kInterleaved>(p, idx, c_begin, c_end, lane, sel, bt_row, rep, row_r);
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) wcount_s[warp] = cnt;
   }
   __syncthreads();
@@ -243,13 +305,16 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
     if (w < warp) off += c;
     total += c;
   }
-  if (one_round) {
+  if (chunk <= 24 * 32) {
+    if (c_begin < c_end) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
-      const int o = off + __popc(mask & lanemask_lt());
-      if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
-      off += __popc(mask);
+      for (int k = 0; k < 24; ++k) {
+        if (k >= 8 && chunk <= 8 * 32) break;
+        const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
+        const int o = off + __popc(mask & lanemask_lt());
+        if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
+        off += __popc(mask);
+      }
     }
   } else {
     for (int j0 = c_begin; j0 < c_end && off < kListCap; j0 += 32) {
@@ -276,112 +341,177 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
   };
 
-  // warps 0-3: this lane's head, its reference (log2 units, the same in every warp and lane
+  // warps 0-7: this lane's head, its reference (log2 units, the same in every warp and lane
   // that holds the head) and this lane's share of its sum
-  const int hh = 16 * (warp % HB) + (lane & 15);
+  const int quad = warp & 3, half = warp >> 2;
+  const int hh = 16 * (quad % HB) + (lane & 15);
   const bool lo_lane = lane >= 16;
+  const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
   float ref = -INFINITY, l_part = 0.f;
   bool bad_q = false;
-  if (warp < 4) {
-    // =================== q into TMEM, softmax, O rescale (warps 0-3) ================
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
-    float c_head;
-    {
-      const bool have = hh < nh;
-      const uint4* qsrc = reinterpret_cast<const uint4*>(p.q + ((size_t)t * p.h + h0 + (have ? hh : 0)) * kDQK);
-      uint32_t am = 0;
-#pragma unroll 6
-      for (int k = 0; k < 36; ++k) {
-        const uint4 x = __ldg(qsrc + (lo_lane ? 36 : 0) + k);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if (warp < kSoftWarps) {
+    // =================== q into TMEM, softmax, O rescale (warps 0-7) ================
+    if (n_local > 0) {
+      // q as hi and lo e4m3 rows: coalesced loads (a head a warp), 4 heads in flight; then
+      // through shared memory (stages 1 and 2, which the gathers leave alone until q is
+      // ready) to the TMEM lanes
+      char* qst = smem + kStageBytes;
+      for (int hb4 = warp; hb4 < NH; hb4 += 4 * kSoftWarps) {
+        uint4 x[4][3];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const int hd = hb4 + kSoftWarps * u, w = lane + 32 * k;
+            x[u][k] = hd < nh && w < 72 ? __ldg(qsrc + (size_t)hd * 72 + w) : make_uint4(0, 0, 0, 0);
+          }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int hd = hb4 + kSoftWarps * u;
+          if (hd >= NH) break;
+          uint32_t am = 0;
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t w[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+          }
+          am = __reduce_max_sync(0xffffffffu, am);
+          const bool bad = am >= 0x7f80u;     // an infinity or NaN: the head's result is NaN
+          // 2^ke: the least power of two with amax / 2^ke <= 448
+          int ke = (int)(am >> 7) - 135 + ((am & 0x7f) > 0x60 ? 1 : 0);
+          ke = am < 0x80u || bad ? 0 : max(ke, -100);
+          const float down = (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
+          if (lane == 0)
+            qc_s[hd] = bad ? __int_as_float(0x7fc00000)
+                           : fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t w[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = bad ? 0.f : __uint_as_float(w[i] << 16) * down;
+              const float c = bad ? 0.f : __uint_as_float(w[i] & 0xffff0000u) * down;
+              hi[i] = e4m3x2(a, c);
+              const float2 f = __half22float2(half2_of(hi[i]));
+              lo[i] = e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f);
+            }
+            if (lane + 32 * k < 72) {
+              char* at = qst + hd * kQPitch + 8 * (lane + 32 * k);
+              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+              *reinterpret_cast<uint2*>(at + 64 * kQPitch) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+            }
+          }
+        }
       }
-      am = max(am, __shfl_xor_sync(0xffffffffu, am, 16));
-      bad_q = have && am >= 0x7f80u;            // an infinity or NaN: the head's result is NaN
-      const bool zero = !have || bad_q;
-      // 2^ke: the least power of two with amax / 2^ke <= 448
-      int ke = (int)(am >> 7) - 135 + ((am & 0x7f) > 0x60 ? 1 : 0);
-      ke = am < 0x80u || zero ? 0 : max(ke, -100);
-      const float down = (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
-      c_head = fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
+      named_barrier(1, kSoftThreads);
+      const char* mine = qst + (hh + (lo_lane ? 64 : 0)) * kQPitch;
 #pragma unroll 1
-      for (int c = 0; c < 9; ++c) {             // 64 columns of q: 16 columns of TMEM
-        uint4 x[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = zero ? make_uint4(0, 0, 0, 0) : __ldg(qsrc + 8 * c + k);
+      for (int c = half; c < 9; c += 2) {     // 64 columns of q are 16 columns of TMEM
         uint32_t v[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          uint32_t pr[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = __uint_as_float(w[i] << 16) * down, bb = __uint_as_float(w[i] & 0xffff0000u) * down;
-            const uint32_t hi = e4m3x2(a, bb);
-            const float2 f = __half22float2(half2_of(hi));
-            pr[i] = lo_lane ? e4m3x2((a - f.x) * 16.f, (bb - f.y) * 16.f) : hi;
-          }
-          v[2 * k] = pr[0] | (pr[1] << 16);
-          v[2 * k + 1] = pr[2] | (pr[3] << 16);
+        for (int k = 0; k < 4; ++k) {
+          const uint4 x = *reinterpret_cast<const uint4*>(mine + 64 * c + 16 * k);
+          v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
         }
         tmem_st16(lane_base + kColQ + 16 * c, v);
       }
       tmem_st_wait();
       tc_fence_before();
+      fence_proxy_async_smem();               // the gathers write these stages next
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarQReady]);
     }
-    // S = hi + lo / 16, this lane's term times fa, its partner's times fb
+    float c_head = n_local > 0 ? qc_s[hh] : 0.f;
+    bad_q = c_head != c_head;
+    if (bad_q) c_head = 1e-30f;
+    // S = hi + lo / 16: this lane's term times fa, its partner's times fb
     const float fa = lo_lane ? 0.0625f : 1.f, fb = lo_lane ? 1.f : 0.0625f;
-    const int cb = (warp / HB) * kCols + (lo_lane ? kHalf : 0);   // this lane's first tile row
+    const int share = quad / HB + (4 / HB) * half;
+    const int cb = share * kCols + (lo_lane ? kHalf : 0);   // this lane's first tile row
+    // The warps leave the loop together: one that gives up a wait says so before barrier B of
+    // its tile (flags of even and odd tiles apart), and all look behind it.
     for (int i = 0; i < n_local; ++i) {
       const int bb = i & 1, sb = kSBufs == 2 ? bb : 0;
-      const uint32_t s_par = kSBufs == 2 ? (i >> 1) & 1 : i & 1;
-      if (warp == 0) {
-        bool go = !*abort_s;
-        if (go && !wait_warp(&bars[kBarSFull + sb], s_par)) { fail(); go = false; }
-        // P buffer bb is free once P.V of tile i-2 has read it
-        if (go && i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) { fail(); go = false; }
-        // (the rows' scales were published with the tile, which QK^T waited for)
-        if (go && !wait_warp(&bars[kBarKvFull + i % kStages], (i / kStages) & 1)) { fail(); go = false; }
-        if (lane == 0) flags_s[1] = go ? 0 : 1;
-      }
-      named_barrier(1, 128);   // A: the scores of tile i are in TMEM and P buffer bb is free
-      if (flags_s[1]) break;
+      if (*abort_s || !wait_warp(&bars[kBarSFull + sb], (kSBufs == 2 ? i >> 1 : i) & 1)) stop_s[bb] = 1;
+      // (complete: QK^T waited for it; this wait orders the reads of the rows' scales)
+      if (!wait_warp(&bars[kBarKvFull + i % kStages], (i / kStages) & 1)) stop_s[bb] = 1;
       tc_fence_after();
       uint32_t v[kCols];
-      const uint32_t sc_col = lane_base + (sb ? kColS1 : kColS) + (warp / HB) * kCols;
+      const uint32_t s_col = lane_base + (sb ? kColS1 : kColS) + share * kCols;
 #pragma unroll
-      for (int k = 0; k < kCols / 8; ++k) tmem_ld8(sc_col + 8 * k, v + 8 * k);
+      for (int k = 0; k < kCols / 8; ++k) tmem_ld8(s_col + 8 * k, v + 8 * k);
       tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarSFree + sb]);
-      const float2* rs = rows_s + (i % kStages) * kNt + cb;
+      const float4* rs = reinterpret_cast<const float4*>(rows_s + (i % kStages) * kNt + cb);
       const int nvalid = total - kNt * ((int)crank + (int)G * i) - cb;   // of this lane's rows
       float s[kHalf];
       float mx = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < kHalf; ++j) {
-        const float own = __uint_as_float(lo_lane ? v[kHalf + j] : v[j]);
-        const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(lo_lane ? v[j] : v[kHalf + j]), 16);
-        const float2 cr = rs[j];
-        const float x = fmaf(own, fa, got * fb) * cr.x;
-        s[j] = j < nvalid ? x : -INFINITY;
-        mx = fmaxf(mx, fmaf(s[j], c_head, cr.y));
+      for (int j = 0; j < kHalf; j += 2) {
+        const float4 cr = rs[j / 2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float own = __uint_as_float(lo_lane ? v[kHalf + j + u] : v[j + u]);
+          const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(lo_lane ? v[j + u] : v[kHalf + j + u]), 16);
+          const float x = fmaf(own, fa, got * fb) * (u ? cr.z : cr.x);
+          s[j + u] = j + u < nvalid ? x : -INFINITY;
+          mx = fmaxf(mx, fmaf(s[j + u], c_head, u ? cr.w : cr.y));
+        }
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      if (R > 1) {
-        float* m4 = max_s + 128 * bb;
-        m4[warp * 32 + lane] = mx;
-        named_barrier(2, 128);   // B: every warp's maximum of tile i is published
-#pragma unroll
-        for (int w = 0; w < R; ++w) mx = fmaxf(mx, m4[((warp % HB) + w * HB) * 32 + lane]);
+      float* mm = max_s + bb * (R * NH);
+      if (!lo_lane) mm[share * NH + hh] = mx;
+      // P buffer bb is free once P.V of tile i-2 has read it
+      if (i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) stop_s[bb] = 1;
+      // B: every warp's maxima of tile i are published; whether any head's reference moves
+      const bool move = barrier_or(2, kSoftThreads, i > 0 && mx > ref + kMostP);
+      if (stop_s[bb]) {
+        fail();
+        break;
       }
-      const float ref_new = (i == 0 || mx > ref + kMostP) ? mx - kPeak : ref;
-      const float alpha = i == 0 ? 1.f : ex2(ref - ref_new);
-      ref = ref_new;
+      if (i == 0 || move) {
+#pragma unroll
+        for (int w = 0; w < R; ++w) mx = fmaxf(mx, mm[w * NH + hh]);
+        const float ref_new = (i == 0 || mx > ref + kMostP) ? mx - kPeak : ref;
+        const float alpha = i == 0 ? 1.f : ex2(ref - ref_new);
+        ref = ref_new;
+        l_part *= alpha;
+        if (move) {
+          if (share == 0 && !lo_lane) alpha_s[64 * bb + hh] = alpha;
+          // O is rescaled once P.V of the previous tile has completed
+          bool okp = wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1);
+          if (!okp) fail();
+          tc_fence_after();
+          named_barrier(3, kSoftThreads);   // C: the factors are published
+          if (okp) {
+#pragma unroll 1
+            for (int c = half; c < 4 * HB; c += 2) {
+              // block c / HB of the columns, heads 16 (c % HB) ..: most heads stay
+              const float4* al4 = reinterpret_cast<const float4*>(alpha_s + 64 * bb + 16 * (c % HB));
+              float al[16];
+              bool any = false;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float4 a = al4[k];
+                al[4 * k] = a.x; al[4 * k + 1] = a.y; al[4 * k + 2] = a.z; al[4 * k + 3] = a.w;
+                any = any || a.x != 1.f || a.y != 1.f || a.z != 1.f || a.w != 1.f;
+              }
+              if (!any) continue;           // (the same for every lane)
+              uint32_t o[16];
+              tmem_ld16(lane_base + kColO + 16 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k]);
+              tmem_st16(lane_base + kColO + 16 * c, o);
+            }
+            tmem_st_wait();
+          }
+        }
+      }
       uint32_t hi[kHalf / 4], lo[kHalf / 4];
       float sum = 0.f;
 #pragma unroll
@@ -389,29 +519,27 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
         uint32_t h2[2], l2[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
+          const float4 cr = rs[j / 2 + u];
           const float e0 = ex2(fmaf(s[j + 2 * u], c_head, -ref)), e1 = ex2(fmaf(s[j + 2 * u + 1], c_head, -ref));
           sum += e0 + e1;
           // 11 bits are enough under the 8 that hi and lo keep
-          const __half2 w = __floats2half2_rn(e0 * rs[j + 2 * u].x, e1 * rs[j + 2 * u + 1].x);
+          const __half2 w = __floats2half2_rn(e0 * cr.x, e1 * cr.z);
           h2[u] = e4m3x2_h(w);
           l2[u] = e4m3x2_h(__hsub2(w, half2_of(h2[u])));
         }
         hi[j / 4] = h2[0] | (h2[1] << 16);
         lo[j / 4] = l2[0] | (l2[1] << 16);
       }
-      l_part = l_part * alpha + sum;
+      l_part += sum;
       {
         // this head's row of P^T, bytes cb .. cb + kHalf - 1 of the K-major SW128 row
         char* row = smem + kOffP + bb * 2 * kPBytes + hh * 128;
-        constexpr int kW = kHalf % 16 == 0 ? 4 : kHalf % 8 == 0 ? 2 : 1;   // words a store
+        constexpr int kW = kHalf % 8 == 0 ? 2 : 1;   // words a store
 #pragma unroll
         for (int u = 0; u < kHalf / 4; u += kW) {
           const int byte = cb + 4 * u;
           char* at = row + ((((byte >> 4) ^ (hh & 7)) << 4) | (byte & 15));
-          if constexpr (kW == 4) {
-            *reinterpret_cast<uint4*>(at) = make_uint4(hi[u], hi[u + 1], hi[u + 2], hi[u + 3]);
-            *reinterpret_cast<uint4*>(at + kPBytes) = make_uint4(lo[u], lo[u + 1], lo[u + 2], lo[u + 3]);
-          } else if constexpr (kW == 2) {
+          if constexpr (kW == 2) {
             *reinterpret_cast<uint2*>(at) = make_uint2(hi[u], hi[u + 1]);
             *reinterpret_cast<uint2*>(at + kPBytes) = make_uint2(lo[u], lo[u + 1]);
           } else {
@@ -421,114 +549,124 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
         }
         fence_proxy_async_smem();
       }
-      if (warp < HB && !lo_lane) alpha_s[64 * bb + hh] = alpha;
-      const bool resc = __any_sync(0xffffffffu, alpha != 1.f);
-      if (lane == 0) flags_s[4 + 4 * bb + warp] = resc ? 1 : 0;
-      named_barrier(3, 128);   // C: whether O is rescaled, and by what
-      if ((flags_s[4 + 4 * bb] | flags_s[5 + 4 * bb] | flags_s[6 + 4 * bb] | flags_s[7 + 4 * bb]) && !*abort_s) {
-        // once P.V of the previous tile has completed
-        if (!wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1)) fail();
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 0; c < 4 * HB; ++c) {
-          uint32_t o[16];
-          tmem_ld16(lane_base + kColO + 16 * c, o);
-          tmem_ld_wait();
-          const float* al = alpha_s + 64 * bb + 16 * (c % HB);
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k]);
-          tmem_st16(lane_base + kColO + 16 * c, o);
-        }
-        tmem_st_wait();
-      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
     }
-  } else if (warp < kProducerWarp + kProducerWarps) {
+  } else if (warp >= kProducerWarp) {
     // =================== gathers ===================================================
-    // Warp pw copies the tile's rows pw, pw + 4, ...: 24 rows of 36 16-byte words, 27 rounds
-    // of 32 lanes.  Up to three tiles are in flight; a tile is signalled when its copies have
-    // landed and are visible to the tensor cores' proxy.
+    // Warp pw takes the tile's row groups pw, pw + 2, ... (4 rows each): 48 gather4 for the
+    // latent columns, and the rope words of its 48 rows in 6 rounds of 32 lanes.  Up to three
+    // tiles are in flight; a tile's copies are signalled once they are visible to the tensor
+    // cores' proxy.
     const int pw = warp - kProducerWarp;
+    constexpr int kRowsOf = kNt / kProducerWarps;   // 48
     const char* kv = reinterpret_cast<const char*>(p.kv);
+    auto tile_row = [&](int q) { return 4 * (pw + kProducerWarps * (q >> 2)) + (q & 3); };
     int issued = 0, done = 0, seg = 0;
     bool ok = true;
-    float sc[kStages] = {0.f, 0.f, 0.f};
-    while (done < n_local && !*abort_s) {
-      bool can = issued < n_local && issued - done < kStages;
-      if (can && issued >= kStages) {
-        const uint32_t par = ((issued / kStages) - 1) & 1;
-        can = __all_sync(0xffffffffu, mbar_test(&bars[kBarKvEmpty + issued % kStages], par));
-        if (!can && issued == done) {
-          if (!(ok = wait_warp(&bars[kBarKvEmpty + issued % kStages], par))) break;
-          can = true;
-        }
-      }
-      if (can) {
-        const int first = kNt * ((int)crank + (int)G * issued);
-        if (first >= (seg + 1) * kListCap) {
-          // rare (more valid entries than the list holds): this warp re-resolves the
-          // entries of its own rows for the segment that holds this tile
-          seg = first / kListCap;
-          int ord = 0;
-          for (int j0 = 0; j0 < p.top_k; j0 += 32) {
-            const int j = j0 + lane;
-            const int row = j < p.top_k ? resolve_row<kInterleaved>(p, bt_row, __ldg(idx + j), sel, false) : -1;
-            const unsigned mask = __ballot_sync(0xffffffffu, row >= 0);
-            const int o = ord + __popc(mask & lanemask_lt()) - seg * kListCap;
-            if (row >= 0 && o >= 0 && o < kListCap && o % kProducerWarps == pw) list_s[o] = row;
-            ord += __popc(mask);
-          }
-          __syncwarp();
-        }
-        const int* rows = list_s + (first - seg * kListCap) + pw;
-        const int left = total - first - pw;                 // rows 4 i of this warp with 4 i < left exist
-        const uint32_t st = smem_u32(smem + (issued % kStages) * kStageBytes);
+    float sc[kStages][2];
 #pragma unroll
-        for (int i = 0; i < kNt / 4 * 36 / 32; ++i) {
-          const int c = 32 * i + lane, rr = c / 36, w = c - 36 * rr;   // word w of row 4 rr + pw
-          const bool in = 4 * rr < left;
-          const int row = in ? rows[4 * rr] : 0;
-          const int y = 4 * rr + pw;
-          const uint32_t dst = w < 32 ? st + (w >> 3) * kBlk + y * 128 + (((w & 7) ^ (y & 7)) << 4)
-                                      : st + 4 * kBlk + y * 64 + (((w & 3) ^ ((y >> 1) & 3)) << 4);
-          cp_async16(dst, kv + (size_t)row * kDQK + 16 * w, in ? 16 : 0);
-        }
-        cp_commit();
-        if (lane < kNt / 4) {
-          const float x = 4 * lane < left ? __ldg(kp.qp.scales + (unsigned)rows[4 * lane] / (unsigned)kp.qp.group) : 0.f;
-          const int at = issued % kStages;
-          if (at == 0) sc[0] = x; else if (at == 1) sc[1] = x; else sc[2] = x;
-        }
-        ++issued;
-        continue;
-      }
-      // the oldest tile in flight
+    for (int a = 0; a < kStages; ++a) sc[a][0] = sc[a][1] = 0.f;
+    auto finish = [&]() {                            // the oldest tile in flight
       switch (issued - done) {
         case 1: cp_wait<0>(); break;
         case 2: cp_wait<1>(); break;
         default: cp_wait<2>(); break;
       }
       const int at = done % kStages;
-      if (lane < kNt / 4) {
-        const float x = at == 0 ? sc[0] : at == 1 ? sc[1] : sc[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int q = lane + 32 * u;
+        const float x = at == 0 ? sc[0][u] : at == 1 ? sc[1][u] : sc[2][u];
         // ceil(log2 x): an upper bound of the weight's exponent, exact for powers of two
-        rows_s[at * kNt + 4 * lane + pw] =
-            make_float2(x, (float)(((int)__float_as_uint(x) + 0x7fffff) >> 23) - 127.f);
+        if (q < kRowsOf)
+          rows_s[at * kNt + tile_row(q)] = make_float2(x, (float)(((int)__float_as_uint(x) + 0x7fffff) >> 23) - 127.f);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarKvFull + at]);
       ++done;
+    };
+    while (done < n_local && !*abort_s) {
+      bool can = issued < n_local && issued - done < kStages;
+      if (can && issued > 0) {
+        // stages 1 and 2 hold q until it is in TMEM; later tiles wait for P.V of the stage's last
+        uint64_t* bar = issued >= kStages ? &bars[kBarKvEmpty + issued % kStages] : &bars[kBarQReady];
+        const uint32_t par = issued >= kStages ? ((issued / kStages) - 1) & 1 : 0;
+        can = __all_sync(0xffffffffu, mbar_test(bar, par));
+        if (!can && issued == done) {
+          if (!(ok = wait_warp(bar, par))) break;
+          can = true;
+        }
+      }
+      if (!can) {
+        finish();
+        continue;
+      }
+      const int first = kNt * ((int)crank + (int)G * issued);
+      if (first >= (seg + 1) * kListCap) {
+        // rare (more valid entries than the list holds): this warp re-resolves the
+        // entries of its own rows for the segment that holds this tile
+        seg = first / kListCap;
+        int ord = 0;
+        for (int j0 = 0; j0 < p.top_k; j0 += 32) {
+          const int j = j0 + lane;
+          const int row = j < p.top_k ? resolve_row<kInterleaved>(p, bt_row, __ldg(idx + j), sel, false) : -1;
+          const unsigned mask = __ballot_sync(0xffffffffu, row >= 0);
+          const int o = ord + __popc(mask & lanemask_lt()) - seg * kListCap;
+          if (row >= 0 && o >= 0 && o < kListCap && ((o % kNt) / 4) % kProducerWarps == pw) list_s[o] = row;
+          ord += __popc(mask);
+        }
+        __syncwarp();
+      }
+      const int* rows = list_s + (first - seg * kListCap);
+      const int left = total - first;
+      const int at = issued % kStages;
+      const uint32_t st = smem_u32(smem + at * kStageBytes);
+      if (lane == 0) mbar_arrive_expect_tx(&bars[kBarKvFull + at], kRowsOf * kDV);
+      __syncwarp();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int e = lane + 32 * u;                 // gather e: group e / 4 of this warp's, block e % 4
+        if (e < kRowsOf) {
+          const int y = 4 * (pw + kProducerWarps * (e >> 2));
+          int rr[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) rr[k] = y + k < left ? rows[y + k] : kp.num_rows;   // past the end: zeros
+          tma_gather4(st + (e & 3) * kBlk + y * 128, &tmap_rows, 128 * (e & 3), rr[0], rr[1], rr[2], rr[3],
+                      &bars[kBarKvFull + at]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRowsOf * 4 / 32; ++u) {
+        const int y = tile_row(8 * u + (lane >> 2)), w = lane & 3;
+        const bool in = y < left;
+        const int row = in ? rows[y] : 0;
+        cp_async16(st + 4 * kBlk + y * 64 + ((w ^ ((y >> 1) & 3)) << 4), kv + (size_t)row * kDQK + kDV + 16 * w,
+                   in ? 16 : 0);
+      }
+      cp_commit();
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int q = lane + 32 * u, y = tile_row(q);
+        const float x = q < kRowsOf && y < left ? __ldg(kp.qp.scales + (unsigned)rows[y] / (unsigned)kp.qp.group) : 0.f;
+        if (at == 0) sc[0][u] = x; else if (at == 1) sc[1][u] = x; else sc[2][u] = x;
+      }
+      ++issued;
     }
     if (!ok) fail();
-    cp_wait<0>();   // no copy of this CTA may still be landing in shared memory at exit
+    // no copy of this CTA may still be landing in shared memory at exit
+    while (done < issued) finish();
+    for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit)))
+        report_status(p.status, kStatusTimeout);
   } else if (warp == kQkWarp || warp == kPvWarp) {
     // =================== tcgen05 MMA issue: QK^T (warp 8) and P.V (warp 9) ========
     if (lane == 0 && n_local > 0) {
       bool ok = true;
       if (warp == kQkWarp) {
+        // test hook: a wait that cannot complete, so the wait limit runs out
         ok = !p.stall || mbar_wait(&bars[kBarNever], 0, wl);
         ok = ok && mbar_wait(&bars[kBarQReady], 0, wl);
         tc_fence_after();
@@ -588,14 +726,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
   // Every thread of every CTA of the cluster reaches both cluster barriers.
   __syncwarp();
   bool have_o = false;
-  if (warp < 4) {
+  if (warp < kSoftWarps) {
     if (n_local > 0 && !*abort_s) {
       have_o = wait_warp(&bars[kBarPvFinal], 0);
       if (!have_o) fail();
     }
     // the head's sum: its two lanes of each of its R warps, in a fixed order
     lpart_s[warp * 32 + lane] = l_part;
-    named_barrier(2, 128);
+    named_barrier(1, kSoftThreads);
     if (warp < HB && !lo_lane) {
       float l = 0.f;
 #pragma unroll
@@ -605,9 +743,9 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
     }
   }
   tc_fence_before();
-  cluster_sync();   // every CTA's (m, l) is published
+  cluster_sync();   // every CTA's (m, l) is published and its stages are idle
   tc_fence_after();
-  if (warp < 4 && warp < HB && !lo_lane) {
+  if (warp < HB && !lo_lane) {
     // this head's largest reference M, sum L and this CTA's weight 2^(m - M) / L
     float M = -INFINITY;
     for (uint32_t c = 0; c < G; ++c) M = fmaxf(M, ld_cluster_f32(mapa(&ml_s[hh], c)));
@@ -622,23 +760,14 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
     if (crank == 0 && hh < nh && !*abort_s)
       p.lse[((size_t)r * T + t) * p.h + h0 + hh] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
   }
-  // the merge buffer (in the idle stages): 32-column segment 4m + w, owned by CTA
-  // (4m + w) / (16 / G); slot of source CTA c: [lane][NH], 16-byte words swizzled by lane
-  float* recv = reinterpret_cast<float*>(smem);
+  const size_t out_at = (((size_t)r * T + t) * p.h + h0) * kDV;   // nh rows of 512, one after the other
   const int segs = 16 / (int)G;
-  const size_t out_at = (((size_t)r * T + t) * p.h + h0) * kDV;
-  auto put = [&](int head, int col, float val) {
-    if (kp.qp.out_bf16)
-      reinterpret_cast<__nv_bfloat16*>(p.out)[out_at + (size_t)head * kDV + col] = __float2bfloat16_rn(val);
-    else
-      p.out[out_at + (size_t)head * kDV + col] = val;
-  };
+  float* recv = reinterpret_cast<float*>(smem);
   __syncwarp();
-  if (warp < 4) {
-    named_barrier(2, 128);
-    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+  if (warp < kSoftWarps) {
+    named_barrier(1, kSoftThreads);
 #pragma unroll 1
-    for (int c = 0; c < 4 * HB; ++c) {
+    for (int c = half; c < 4 * HB; c += 2) {
       const int m = c / HB, hb = 16 * (c % HB);
       uint32_t o[16];
       if (have_o) {
@@ -648,38 +777,66 @@ __global__ void __launch_bounds__(kThreads, 1) decode_q8_kernel(const Q8Params k
       float f[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) f[k] = have_o ? __uint_as_float(o[k]) * scale_s[hb + k] : 0.f;
+      const int col = 128 * m + 32 * quad + lane;
       if (G == 1) {
+        // [head][512] in the idle stages, as it goes to global memory
+        if (kp.qp.out_bf16) {
+          __nv_bfloat16* o_s = reinterpret_cast<__nv_bfloat16*>(smem) + hb * kDV + col;
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (hb + k < nh && !*abort_s) put(hb + k, 128 * m + 32 * warp + lane, f[k]);
+          for (int k = 0; k < 16; ++k) o_s[k * kDV] = __float2bfloat16_rn(f[k]);
+        } else {
+          float* o_s = reinterpret_cast<float*>(smem) + hb * kDV + col;
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o_s[k * kDV] = f[k];
+        }
       } else {
-        const int seg = 4 * m + warp;
-        const uint32_t dst = mapa(recv + ((size_t)(crank * segs + seg % segs) * 32 + lane) * NH, seg / segs);
+        // 32-column segment 4m + quad to CTA (4m + quad) / segs, slot of this CTA:
+        // [lane][NH], 16-byte words swizzled by lane
+        const int sg = 4 * m + quad;
+        const uint32_t dst = mapa(recv + ((size_t)(crank * segs + sg % segs) * 32 + lane) * NH, sg / segs);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           st_cluster_v4(dst + 16u * ((hb / 4 + k) ^ (lane & (NH / 4 - 1))), __float_as_uint(f[4 * k]),
                         __float_as_uint(f[4 * k + 1]), __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3]));
       }
     }
+    if (G == 1) {
+      fence_proxy_async_smem();
+      named_barrier(1, kSoftThreads);
+      if (lane == 0 && !*abort_s) {
+        const uint32_t row = kDV * (kp.qp.out_bf16 ? 2 : 4);
+        char* dst = reinterpret_cast<char*>(p.out) + out_at * (row / kDV);
+        for (int hd = warp; hd < nh; hd += kSoftWarps)
+          bulk_store_s2g(dst + (size_t)hd * row, smem_u32(smem) + hd * row, row);
+        bulk_commit_group();
+        bulk_wait<0>();
+      }
+      __syncwarp();
+    }
   }
   tc_fence_before();
   cluster_sync();   // every CTA's scaled partial O has landed with its owner
   tc_fence_after();
-  if (G > 1 && warp < 4 && !*abort_s) {
-    for (int sg = warp; sg < segs; sg += 4) {
-      const int seg = (int)crank * segs + sg;
-#pragma unroll 1
-      for (int k4 = 0; k4 < NH / 4; ++k4) {
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (uint32_t c = 0; c < G; ++c) {
-          const float4 x = *reinterpret_cast<const float4*>(
-              recv + ((size_t)(c * segs + sg) * 32 + lane) * NH + 4 * (k4 ^ (lane & (NH / 4 - 1))));
-          a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-        }
-        const float f[4] = {a.x, a.y, a.z, a.w};
+  if (G > 1 && warp < kSoftWarps && !*abort_s) {
+    // this CTA's segments: the sum of the G scaled partials, in the order of the CTAs
+    for (int x = warp; x < segs * (NH / 4); x += kSoftWarps) {
+      const int sg = x % segs, k4 = x / segs;
+      if (4 * k4 >= nh) break;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (uint32_t c = 0; c < G; ++c) {
+        const float4 y = *reinterpret_cast<const float4*>(recv + ((size_t)(c * segs + sg) * 32 + lane) * NH +
+                                                          4 * (k4 ^ (lane & (NH / 4 - 1))));
+        a.x += y.x; a.y += y.y; a.z += y.z; a.w += y.w;
+      }
+      const float f[4] = {a.x, a.y, a.z, a.w};
+      const size_t at = out_at + 32 * ((int)crank * segs + sg) + lane;
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (4 * k4 + k < nh) put(4 * k4 + k, 32 * seg + lane, f[k]);
+      for (int k = 0; k < 4; ++k) {
+        if (4 * k4 + k >= nh) break;
+        if (kp.qp.out_bf16)
+          reinterpret_cast<__nv_bfloat16*>(p.out)[at + (size_t)(4 * k4 + k) * kDV] = __float2bfloat16_rn(f[k]);
+        else
+          p.out[at + (size_t)(4 * k4 + k) * kDV] = f[k];
       }
     }
   }
@@ -697,13 +854,36 @@ constexpr auto q8_kernel() {
   return decode_q8_kernel<NH, kIL>;
 }
 
+// the cache as [num_rows, 576] bytes; one box = 128 columns of one row (gathered four at a time)
+bool make_rows_map(CUtensorMap* m, const void* kv8, int num_rows) {
+  typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::once_flag once;
+  static EncodeFn fn = nullptr;
+  std::call_once(once, [] {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeFn>(ptr);
+  });
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)kDQK, (cuuint64_t)num_rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)kDQK};
+  const cuuint32_t box[2] = {128, 1}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(kv8), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 cudaError_t prepare_decode_q8() {
   static std::atomic<bool> attr_set[64];
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
-    for (auto kernel : {q8_kernel<16, false>(), q8_kernel<16, true>(), q8_kernel<32, false>(), q8_kernel<32, true>(),
-                        q8_kernel<64, false>(), q8_kernel<64, true>()}) {
+    for (auto kernel : {q8_kernel<32, false>(), q8_kernel<32, true>(), q8_kernel<64, false>(), q8_kernel<64, true>()}) {
       cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       if (e != cudaSuccess) return e;
     }
@@ -731,9 +911,11 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
   while (G < 8 && units * G * 2 <= device_sm_count() && G * kNt < p.top_k) G *= 2;
   if (units * G > 0x7fffffffLL) return cudaErrorInvalidValue;
   const bool il = p.interleave > 0 && p.n_splits > 1;
-  auto kernel = kp.group_heads <= 16   ? (il ? q8_kernel<16, true>() : q8_kernel<16, false>())
-                : kp.group_heads <= 32 ? (il ? q8_kernel<32, true>() : q8_kernel<32, false>())
-                                       : (il ? q8_kernel<64, true>() : q8_kernel<64, false>());
+  auto kernel = kp.group_heads <= 32 ? (il ? q8_kernel<32, true>() : q8_kernel<32, false>())
+                                     : (il ? q8_kernel<64, true>() : q8_kernel<64, false>());
+  CUtensorMap rows;
+  kp.num_rows = p.num_blocks * p.block_size;
+  if (!make_rows_map(&rows, p.kv, kp.num_rows)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3((unsigned)(units * G), 1, 1);
@@ -747,7 +929,7 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, kp);
+  e = cudaLaunchKernelEx(&cfg, kernel, rows, kp);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
