@@ -54,10 +54,13 @@ using namespace ptx;
 
 constexpr int kNt = 96;              // selected rows per tile: N of QK^T, K of P.V
 constexpr int kStages = 3;
-constexpr int kThreads = 384;
+#ifndef NPW
+#define NPW 6
+#endif
+constexpr int kThreads = 320 + 32 * NPW;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
-constexpr int kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 2;
+constexpr int kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = NPW;
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPeak = 4.0f;        // log2 of P at the maximum a reference is taken from
@@ -71,7 +74,8 @@ constexpr int kPBytes = kGroupHeads * 128;            // P^T [heads x 96 rows] e
 constexpr int kOffList = kOffP + 4 * kPBytes;         // two buffers of hi and lo
 constexpr int kListCap = 48 * kNt;                    // resolved rows kept at once (whole tiles)
 constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and row: (scale, ceil log2 scale)
-constexpr int kOffMisc = kOffScale + kStages * kNt * 8;
+constexpr int kOffRaw = kOffScale + kStages * kNt * 8;  // the scales as they land
+constexpr int kOffMisc = kOffRaw + kStages * kNt * 4;
 constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscMax = 1024, kMiscScale = 3072, kMiscSum = 3328,
               kMiscC = 4352, kMiscFlags = 4608, kMiscTmem = 4624, kMiscCount = 4640, kMiscBytes = 4704;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
@@ -101,20 +105,35 @@ struct Q8Params {
   int num_rows;      // rows of the cache: the index that the gathers read as zeros
 };
 
-// D[tmem] (+)= A * B, e4m3 operands, fp32 accumulation
-__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+// D[tmem] (+)= A * B, e4m3 operands, fp32 accumulation.  A shared-memory descriptor's high
+// word (strides, swizzle) is a constant of the operand; the low word is the address.
+template <uint32_t kHi>
+__device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHi)
       : "memory");
 }
-__device__ __forceinline__ void mma8_ss(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+template <uint32_t kHiA, uint32_t kHiB>
+__device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
       : "memory");
+}
+// the words of a shared-memory matrix descriptor (addresses and strides in 16-byte units)
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return (saddr >> 4) | ((lbo >> 4) << 16);
+}
+constexpr uint32_t desc_hi(uint32_t sbo, uint32_t swizzle) { return (sbo >> 4) | (1u << 14) | (swizzle << 29); }
+// one lane of the (converged) warp
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // instruction descriptor of kind::f8f6f4: e4m3 A and B (format 0), fp32 D
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_mn) {
@@ -126,6 +145,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 // two e4m3 codes of a (low byte) and b
@@ -147,6 +172,9 @@ __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int n>
@@ -170,35 +198,31 @@ __device__ __forceinline__ void bulk_store_s2g(void* dst, uint32_t src, uint32_t
                : "memory");
 }
 
-// One lane's share of a warp's chunk [c_begin, c_end) of the selected list, E entries a round
-// with their loads in flight together: counts those that resolve to a row of this unit and
-// leaves the last round's rows in row (-1 for entries that do not).
-template <int E, bool kInterleaved>
-__device__ __forceinline__ int resolve_round(const DecodeParams& p, const int32_t* idx, int c_begin, int c_end,
-                                             int lane, const ShardSel& sel, int bt_row, bool report, int* row) {
+// The rows of entries j0 + 32 k + lane < c_end (k < 8) of the selected list, -1 for those that
+// do not resolve to a row of this unit; returns how many do.
+template <bool kInterleaved>
+__device__ __forceinline__ int resolve8(const DecodeParams& p, const int32_t* idx, int j0, int c_end, int lane,
+                                        const ShardSel& sel, int bt_row, bool report, int (&row)[8]) {
   const int32_t* table = p.block_table + (size_t)bt_row * p.max_blocks;
-  int cnt = 0;
-  for (int j0 = c_begin; j0 < c_end; j0 += 32 * E) {
-    int pos[E];
+  int cnt = 0, pos[8];
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      const int j = j0 + 32 * k + lane;
-      pos[k] = j < c_end ? __ldg(idx + j) : -1;
-    }
+  for (int k = 0; k < 8; ++k) {
+    const int j = j0 + 32 * k + lane;
+    pos[k] = j < c_end ? __ldg(idx + j) : -1;
+  }
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      const bool in = sel.has_fixed<kInterleaved>(pos[k]);
-      const int blk = in ? pos[k] / p.block_size : 0;
-      pos[k] = in ? pos[k] - blk * p.block_size : -1;      // the offset in its block
-      row[k] = in && blk < p.max_blocks ? __ldg(table + blk) : -1;
-    }
+  for (int k = 0; k < 8; ++k) {
+    const bool in = sel.has_fixed<kInterleaved>(pos[k]);
+    const int blk = in ? (int)((unsigned)pos[k] / (unsigned)p.block_size) : 0;
+    pos[k] = in ? pos[k] - blk * p.block_size : -1;      // the offset in its block
+    row[k] = in && blk < p.max_blocks ? __ldg(table + blk) : -1;
+  }
 #pragma unroll
-    for (int k = 0; k < E; ++k) {
-      const bool valid = row[k] >= 0 && row[k] < p.num_blocks;
-      if (pos[k] >= 0 && !valid && report) report_status(p.status, kStatusBadBlock);
-      cnt += valid;
-      row[k] = valid ? row[k] * p.block_size + pos[k] : -1;
-    }
+  for (int k = 0; k < 8; ++k) {
+    const bool valid = row[k] >= 0 && row[k] < p.num_blocks;
+    if (pos[k] >= 0 && !valid && report) report_status(p.status, kStatusBadBlock);
+    cnt += valid;
+    row[k] = valid ? row[k] * p.block_size + pos[k] : -1;
   }
   return cnt;
 }
@@ -284,16 +308,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kProducerWarp && lane == 0) prefetch_tmap(&tmap_rows);
 
   // ---- index resolution: count per warp chunk, then ordered compaction into smem ----
-  // up to 8 entries a thread are resolved in one round, then up to 24, longer lists in rounds
-  // of 24 and once more for the compaction
+  // (rounds of 8 entries a lane; a list of one round stays in registers, a longer one is
+  // resolved again, from L1, for the compaction)
   const int chunk = ((p.top_k + kWarps * 32 - 1) / (kWarps * 32)) * 32;
   const int c_begin = min(warp * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
-  int row_r[24];
-  const bool rep = crank == 0 && hg == 0;
+  int row_r[8];
   {
-    int cnt = chunk <= 8 * 32
-                  ? resolve_round<8, kInterleaved>(p, idx, c_begin, c_end, lane, sel, bt_row, rep, row_r)
-                  : resolve_round<24, kInterleaved>(p, idx, c_begin, c_end, lane, sel, bt_row, rep, row_r);
+    int cnt = 0;
+#pragma unroll 1
+    for (int j0 = c_begin; j0 < c_end; j0 += 256)
+      cnt += resolve8<kInterleaved>(p, idx, j0, c_end, lane, sel, bt_row, crank == 0 && hg == 0, row_r);
     cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) wcount_s[warp] = cnt;
   }
@@ -305,27 +329,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (w < warp) off += c;
     total += c;
   }
-  if (chunk <= 24 * 32) {
-    if (c_begin < c_end) {
+#pragma unroll 1
+  for (int j0 = c_begin; j0 < c_end && off < kListCap; j0 += 256) {
+    if (chunk > 256) resolve8<kInterleaved>(p, idx, j0, c_end, lane, sel, bt_row, false, row_r);
 #pragma unroll
-      for (int k = 0; k < 24; ++k) {
-        if (k >= 8 && chunk <= 8 * 32) break;
-        const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
-        const int o = off + __popc(mask & lanemask_lt());
-        if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
-        off += __popc(mask);
-      }
-    }
-  } else {
-    for (int j0 = c_begin; j0 < c_end && off < kListCap; j0 += 32) {
-      const int j = j0 + lane;
-      const int row = j < c_end ? resolve_row<kInterleaved>(p, bt_row, __ldg(idx + j), sel, false) : -1;
-      const unsigned mask = __ballot_sync(0xffffffffu, row >= 0);
+    for (int k = 0; k < 8; ++k) {
+      const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
       const int o = off + __popc(mask & lanemask_lt());
-      if (row >= 0 && o < kListCap) list_s[o] = row;
+      if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
       off += __popc(mask);
     }
   }
+  // the last tile's missing rows: an index past the cache, which the gathers read as zeros
+  if (warp == 0)
+    for (int o = total + lane; o < min((total + kNt - 1) / kNt * kNt, kListCap); o += 32) list_s[o] = kp.num_rows;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -352,56 +369,53 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kSoftWarps) {
     // =================== q into TMEM, softmax, O rescale (warps 0-7) ================
     if (n_local > 0) {
-      // q as hi and lo e4m3 rows: coalesced loads (a head a warp), 4 heads in flight; then
+      // q as hi and lo e4m3 rows: coalesced loads (a head a warp), then
       // through shared memory (stages 1 and 2, which the gathers leave alone until q is
       // ready) to the TMEM lanes
       char* qst = smem + kStageBytes;
-      for (int hb4 = warp; hb4 < NH; hb4 += 4 * kSoftWarps) {
-        uint4 x[4][3];
+      uint4 nx[3];
+      auto load_head = [&](int hd) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int k = 0; k < 3; ++k)
+          nx[k] = hd < nh && lane + 32 * k < 72 ? __ldg(qsrc + (size_t)hd * 72 + lane + 32 * k) : make_uint4(0, 0, 0, 0);
+      };
+      load_head(warp);
+#pragma unroll 1
+      for (int hd = warp; hd < NH; hd += kSoftWarps) {
+        const uint4 x[3] = {nx[0], nx[1], nx[2]};
+        load_head(hd + kSoftWarps);
+        uint32_t am = 0;
 #pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const int hd = hb4 + kSoftWarps * u, w = lane + 32 * k;
-            x[u][k] = hd < nh && w < 72 ? __ldg(qsrc + (size_t)hd * 72 + w) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        }
+        am = __reduce_max_sync(0xffffffffu, am);
+        const bool bad = am >= 0x7f80u;     // an infinity or NaN: the head's result is NaN
+        // 2^ke: the least power of two with amax / 2^ke <= 448
+        int ke = (int)(am >> 7) - 135 + ((am & 0x7f) > 0x60 ? 1 : 0);
+        ke = am < 0x80u || bad ? 0 : max(ke, -100);
+        const float down = (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
+        if (lane == 0)
+          qc_s[hd] = bad ? __int_as_float(0x7fc00000)
+                         : fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float a = bad ? 0.f : __uint_as_float(w[i] << 16) * down;
+            const float c = bad ? 0.f : __uint_as_float(w[i] & 0xffff0000u) * down;
+            hi[i] = e4m3x2(a, c);
+            const float2 f = __half22float2(half2_of(hi[i]));
+            lo[i] = e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f);
           }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int hd = hb4 + kSoftWarps * u;
-          if (hd >= NH) break;
-          uint32_t am = 0;
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint32_t w[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-          }
-          am = __reduce_max_sync(0xffffffffu, am);
-          const bool bad = am >= 0x7f80u;     // an infinity or NaN: the head's result is NaN
-          // 2^ke: the least power of two with amax / 2^ke <= 448
-          int ke = (int)(am >> 7) - 135 + ((am & 0x7f) > 0x60 ? 1 : 0);
-          ke = am < 0x80u || bad ? 0 : max(ke, -100);
-          const float down = (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
-          if (lane == 0)
-            qc_s[hd] = bad ? __int_as_float(0x7fc00000)
-                           : fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
-#pragma unroll
-          for (int k = 0; k < 3; ++k) {
-            const uint32_t w[4] = {x[u][k].x, x[u][k].y, x[u][k].z, x[u][k].w};
-            uint32_t hi[4], lo[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float a = bad ? 0.f : __uint_as_float(w[i] << 16) * down;
-              const float c = bad ? 0.f : __uint_as_float(w[i] & 0xffff0000u) * down;
-              hi[i] = e4m3x2(a, c);
-              const float2 f = __half22float2(half2_of(hi[i]));
-              lo[i] = e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f);
-            }
-            if (lane + 32 * k < 72) {
-              char* at = qst + hd * kQPitch + 8 * (lane + 32 * k);
-              *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-              *reinterpret_cast<uint2*>(at + 64 * kQPitch) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-            }
+          if (lane + 32 * k < 72) {
+            char* at = qst + hd * kQPitch + 8 * (lane + 32 * k);
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+            *reinterpret_cast<uint2*>(at + 64 * kQPitch) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
           }
         }
       }
@@ -480,37 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = i == 0 ? 1.f : ex2(ref - ref_new);
         ref = ref_new;
         l_part *= alpha;
-        if (move) {
-          if (share == 0 && !lo_lane) alpha_s[64 * bb + hh] = alpha;
-          // O is rescaled once P.V of the previous tile has completed
-          bool okp = wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1);
-          if (!okp) fail();
-          tc_fence_after();
-          named_barrier(3, kSoftThreads);   // C: the factors are published
-          if (okp) {
-#pragma unroll 1
-            for (int c = half; c < 4 * HB; c += 2) {
-              // block c / HB of the columns, heads 16 (c % HB) ..: most heads stay
-              const float4* al4 = reinterpret_cast<const float4*>(alpha_s + 64 * bb + 16 * (c % HB));
-              float al[16];
-              bool any = false;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float4 a = al4[k];
-                al[4 * k] = a.x; al[4 * k + 1] = a.y; al[4 * k + 2] = a.z; al[4 * k + 3] = a.w;
-                any = any || a.x != 1.f || a.y != 1.f || a.z != 1.f || a.w != 1.f;
-              }
-              if (!any) continue;           // (the same for every lane)
-              uint32_t o[16];
-              tmem_ld16(lane_base + kColO + 16 * c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k]);
-              tmem_st16(lane_base + kColO + 16 * c, o);
-            }
-            tmem_st_wait();
-          }
-        }
+        if (move && share == 0 && !lo_lane) alpha_s[64 * bb + hh] = alpha;
       }
       uint32_t hi[kHalf / 4], lo[kHalf / 4];
       float sum = 0.f;
@@ -549,6 +533,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
       }
+      if (move) {
+        // O is rescaled once P.V of the previous tile has completed; only the heads (8 at a
+        // time) whose reference moved
+        const bool okp = wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1);
+        if (!okp) fail();
+        tc_fence_after();
+        named_barrier(3, kSoftThreads);   // C: the factors are published
+        const float2 a2 = *reinterpret_cast<const float2*>(alpha_s + 64 * bb + 2 * (lane % (NH / 2)));
+        unsigned moved = __ballot_sync(0xffffffffu, a2.x != 1.f || a2.y != 1.f) & (NH == 64 ? ~0u : 0xffffu);
+        while (moved && okp) {
+          const int oct = (__ffs(moved) - 1) >> 2;        // heads 8 oct ..: lanes 4 oct ..
+          moved &= ~(0xfu << (4 * oct));
+          const float4 a = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct);
+          const float4 c = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct + 4);
+          const float al[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+          uint32_t o[16];
+          const uint32_t at = lane_base + kColO + 2 * half * NH + 8 * oct;   // column blocks 2 half and 2 half + 1
+          tmem_ld8(at, o);
+          tmem_ld8(at + NH, o + 8);
+          tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k & 7]);
+          tmem_st8(at, o);
+          tmem_st8(at + NH, o + 8);
+        }
+        tmem_st_wait();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
@@ -565,9 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto tile_row = [&](int q) { return 4 * (pw + kProducerWarps * (q >> 2)) + (q & 3); };
     int issued = 0, done = 0, seg = 0;
     bool ok = true;
-    float sc[kStages][2];
-#pragma unroll
-    for (int a = 0; a < kStages; ++a) sc[a][0] = sc[a][1] = 0.f;
+    float* raw_s = reinterpret_cast<float*>(smem + kOffRaw);
     auto finish = [&]() {                            // the oldest tile in flight
       switch (issued - done) {
         case 1: cp_wait<0>(); break;
@@ -575,13 +584,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         default: cp_wait<2>(); break;
       }
       const int at = done % kStages;
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int q = lane + 32 * u;
-        const float x = at == 0 ? sc[0][u] : at == 1 ? sc[1][u] : sc[2][u];
+      for (int q = lane; q < kRowsOf; q += 32) {
         // ceil(log2 x): an upper bound of the weight's exponent, exact for powers of two
-        if (q < kRowsOf)
-          rows_s[at * kNt + tile_row(q)] = make_float2(x, (float)(((int)__float_as_uint(x) + 0x7fffff) >> 23) - 127.f);
+        const float x = raw_s[at * kNt + tile_row(q)];
+        rows_s[at * kNt + tile_row(q)] = make_float2(x, (float)(((int)__float_as_uint(x) + 0x7fffff) >> 23) - 127.f);
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -618,41 +624,40 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (row >= 0 && o >= 0 && o < kListCap && ((o % kNt) / 4) % kProducerWarps == pw) list_s[o] = row;
           ord += __popc(mask);
         }
+        for (int o = total - seg * kListCap + lane; o < min(n_tiles * kNt - seg * kListCap, kListCap); o += 32)
+          if (((o % kNt) / 4) % kProducerWarps == pw) list_s[o] = kp.num_rows;
         __syncwarp();
       }
       const int* rows = list_s + (first - seg * kListCap);
-      const int left = total - first;
       const int at = issued % kStages;
       const uint32_t st = smem_u32(smem + at * kStageBytes);
       if (lane == 0) mbar_arrive_expect_tx(&bars[kBarKvFull + at], kRowsOf * kDV);
       __syncwarp();
+      if (elect_one()) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int e = lane + 32 * u;                 // gather e: group e / 4 of this warp's, block e % 4
-        if (e < kRowsOf) {
-          const int y = 4 * (pw + kProducerWarps * (e >> 2));
-          int rr[4];
+        for (int g = 0; g < kRowsOf / 4; ++g) {
+          const int y = 4 * (pw + kProducerWarps * g);
+          const int4 rr = *reinterpret_cast<const int4*>(rows + y);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) rr[k] = y + k < left ? rows[y + k] : kp.num_rows;   // past the end: zeros
-          tma_gather4(st + (e & 3) * kBlk + y * 128, &tmap_rows, 128 * (e & 3), rr[0], rr[1], rr[2], rr[3],
-                      &bars[kBarKvFull + at]);
+          for (int m = 0; m < 4; ++m)
+            tma_gather4(st + m * kBlk + y * 128, &tmap_rows, 128 * m, rr.x, rr.y, rr.z, rr.w, &bars[kBarKvFull + at]);
         }
       }
+      __syncwarp();
 #pragma unroll
       for (int u = 0; u < kRowsOf * 4 / 32; ++u) {
-        const int y = tile_row(8 * u + (lane >> 2)), w = lane & 3;
-        const bool in = y < left;
-        const int row = in ? rows[y] : 0;
-        cp_async16(st + 4 * kBlk + y * 64 + ((w ^ ((y >> 1) & 3)) << 4), kv + (size_t)row * kDQK + kDV + 16 * w,
+        const int y = tile_row(8 * u + (lane >> 2)), w = lane & 3, row = rows[y];
+        const bool in = row < kp.num_rows;
+        cp_async16(st + 4 * kBlk + y * 64 + ((w ^ ((y >> 1) & 3)) << 4), kv + (size_t)(in ? row : 0) * kDQK + kDV + 16 * w,
                    in ? 16 : 0);
       }
-      cp_commit();
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int q = lane + 32 * u, y = tile_row(q);
-        const float x = q < kRowsOf && y < left ? __ldg(kp.qp.scales + (unsigned)rows[y] / (unsigned)kp.qp.group) : 0.f;
-        if (at == 0) sc[0][u] = x; else if (at == 1) sc[1][u] = x; else sc[2][u] = x;
+      for (int q = lane; q < kRowsOf; q += 32) {
+        const int y = tile_row(q), row = rows[y];
+        const bool in = row < kp.num_rows;
+        cp_async4(smem_u32(raw_s + at * kNt + y), kp.qp.scales + (in ? (unsigned)row / (unsigned)kp.qp.group : 0u),
+                  in ? 4 : 0);
       }
+      cp_commit();
       ++issued;
     }
     if (!ok) fail();
@@ -663,62 +668,76 @@ __global__ void __launch_bounds__(kThreads, 1)
         report_status(p.status, kStatusTimeout);
   } else if (warp == kQkWarp || warp == kPvWarp) {
     // =================== tcgen05 MMA issue: QK^T (warp 8) and P.V (warp 9) ========
-    if (lane == 0 && n_local > 0) {
+    // (the whole warp walks the tiles and waits; one lane issues)
+    if (n_local > 0) {
       bool ok = true;
+      const uint32_t st0 = smem_u32(smem);
       if (warp == kQkWarp) {
         // test hook: a wait that cannot complete, so the wait limit runs out
-        ok = !p.stall || mbar_wait(&bars[kBarNever], 0, wl);
-        ok = ok && mbar_wait(&bars[kBarQReady], 0, wl);
+        ok = !p.stall || wait_warp(&bars[kBarNever], 0);
+        ok = ok && wait_warp(&bars[kBarQReady], 0);
         tc_fence_after();
-        const uint32_t id = idesc_e4m3(128, kNt, 0, 0);
+        constexpr uint32_t id = idesc_e4m3(128, kNt, 0, 0);
+        int s = 0;
+        uint32_t full = 0;
         for (int n = 0; ok && n < n_local && !*abort_s; ++n) {
-          const int s = n % kStages, sb = kSBufs == 2 ? n & 1 : 0;
-          if (!(ok = mbar_wait(&bars[kBarKvFull + s], (n / kStages) & 1, wl))) break;
+          const int sb = kSBufs == 2 ? n & 1 : 0;
+          if (!(ok = wait_warp(&bars[kBarKvFull + s], full))) break;
           // the score buffer is free once the softmax has read the tile before from it
-          if (n >= kSBufs &&
-              !(ok = mbar_wait(&bars[kBarSFree + sb], (kSBufs == 2 ? (n >> 1) - 1 : n - 1) & 1, wl)))
-            break;
+          if (n >= kSBufs && !(ok = wait_warp(&bars[kBarSFree + sb], (kSBufs == 2 ? (n >> 1) - 1 : n - 1) & 1))) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * kStageBytes);
+          const uint32_t st = st0 + s * kStageBytes;
           const uint32_t d = tmem + (sb ? kColS1 : kColS);
+          if (elect_one()) {
+            const uint32_t b0 = desc_lo(st, 16);
 #pragma unroll
-          for (int k = 0; k < 16; ++k)
-            mma8_ts(d, tmem + kColQ + 8 * k, smem_desc(st + (k >> 2) * kBlk + (k & 3) * 32, 16, 1024, kSwizzle128),
-                    id, k > 0);
+            for (int k = 0; k < 16; ++k)
+              mma8_ts<desc_hi(1024, kSwizzle128)>(d, tmem + kColQ + 8 * k, b0 + (((k >> 2) * kBlk + (k & 3) * 32) >> 4),
+                                                  id, k > 0);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            mma8_ts(d, tmem + kColQ + 128 + 8 * k, smem_desc(st + 4 * kBlk + k * 32, 16, 512, kSwizzle64), id, 1);
-          mma_commit(&bars[kBarSFull + sb]);
+            for (int k = 0; k < 2; ++k)
+              mma8_ts<desc_hi(512, kSwizzle64)>(d, tmem + kColQ + 128 + 8 * k, b0 + ((4 * kBlk + k * 32) >> 4), id, 1);
+            mma_commit(&bars[kBarSFull + sb]);
+          }
+          __syncwarp();
+          if (++s == kStages) { s = 0; full ^= 1; }
         }
       } else {
         // A = E^T: columns 128m..128m+127 of 32 tile rows, MN-major (one SW128 atom wide);
         // B = P^T: NH heads x 32 rows, K-major.  The four blocks' accumulators alternate.
-        const uint32_t id = idesc_e4m3(128, NH, 1, 0);
-        const uint32_t pt = smem_u32(smem + kOffP);
+        constexpr uint32_t id = idesc_e4m3(128, NH, 1, 0);
+        int s = 0;
         for (int n = 0; ok && n < n_local && !*abort_s; ++n) {
-          const int s = n % kStages, bb = n & 1;
-          if (!(ok = mbar_wait(&bars[kBarPReady + bb], (n >> 1) & 1, wl))) break;
+          const int bb = n & 1;
+          if (!(ok = wait_warp(&bars[kBarPReady + bb], (n >> 1) & 1))) break;
           tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * kStageBytes);
+          if (elect_one()) {
+            const uint32_t a0 = desc_lo(st0 + s * kStageBytes, kBlk);
+            const uint32_t b0 = desc_lo(st0 + kOffP + 2 * bb * kPBytes, 16);
 #pragma unroll
-          for (int k = 0; k < kNt / 32; ++k)
+            for (int k = 0; k < kNt / 32; ++k)
 #pragma unroll
-            for (int part = 0; part < 2; ++part)
+              for (int part = 0; part < 2; ++part)
 #pragma unroll
-              for (int m = 0; m < 4; ++m)
-                mma8_ss(tmem + kColO + NH * m, smem_desc(st + m * kBlk + 4096 * k, kBlk, 1024, kSwizzle128),
-                        smem_desc(pt + (2 * bb + part) * kPBytes + 32 * k, 16, 1024, kSwizzle128), id,
-                        (n > 0 || k > 0 || part > 0) ? 1u : 0u);
-          mma_commit(&bars[kBarKvEmpty + s]);
-          mma_commit(&bars[kBarPFree + bb]);
-          if (n == n_local - 1) mma_commit(&bars[kBarPvFinal]);
+                for (int m = 0; m < 4; ++m)
+                  mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128)>(
+                      tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPBytes + 32 * k) >> 4), id,
+                      (k > 0 || part > 0) ? 1u : (n > 0 ? 1u : 0u));
+            mma_commit(&bars[kBarKvEmpty + s]);
+            mma_commit(&bars[kBarPFree + bb]);
+            if (n == n_local - 1) mma_commit(&bars[kBarPvFinal]);
+          }
+          __syncwarp();
+          if (++s == kStages) s = 0;
         }
       }
       if (!ok) fail();
-      // every MMA this thread issued has completed before TMEM is released
+      // every MMA this warp issued has completed before TMEM is released
+      // (the same lane is elected every time: a commit covers its thread's MMAs)
       uint64_t* fin_bar = &bars[warp == kQkWarp ? kBarMmaFin : kBarMmaFin2];
-      mma_commit(fin_bar);
-      if (!mbar_wait(fin_bar, 0, kDrainLimit)) report_status(p.status, kStatusTimeout);
+      if (elect_one()) mma_commit(fin_bar);
+      __syncwarp();
+      if (!__all_sync(0xffffffffu, mbar_wait(fin_bar, 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
     }
   }
 
