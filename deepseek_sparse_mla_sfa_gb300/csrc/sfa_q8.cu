@@ -54,13 +54,10 @@ using namespace ptx;
 
 constexpr int kNt = 96;              // selected rows per tile: N of QK^T, K of P.V
 constexpr int kStages = 3;
-#ifndef NPW
-#define NPW 6
-#endif
-constexpr int kThreads = 320 + 32 * NPW;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
-constexpr int kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = NPW;
+constexpr int kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 6;
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPeak = 4.0f;        // log2 of P at the maximum a reference is taken from
@@ -73,8 +70,9 @@ constexpr int kOffP = kStages * kStageBytes;
 constexpr int kPBytes = kGroupHeads * 128;            // P^T [heads x 96 rows] e4m3, K-major SW128 rows
 constexpr int kOffList = kOffP + 4 * kPBytes;         // two buffers of hi and lo
 constexpr int kListCap = 48 * kNt;                    // resolved rows kept at once (whole tiles)
-constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and row: (scale, ceil log2 scale)
-constexpr int kOffRaw = kOffScale + kStages * kNt * 8;  // the scales as they land
+constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and row: (scale, log2 scale)
+constexpr int kOffInv = kOffScale + kStages * kNt * 8;  // 1 / scale
+constexpr int kOffRaw = kOffInv + kStages * kNt * 4;    // the scales as they land
 constexpr int kOffMisc = kOffRaw + kStages * kNt * 4;
 constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscMax = 1024, kMiscScale = 3072, kMiscSum = 3328,
               kMiscC = 4352, kMiscFlags = 4608, kMiscTmem = 4624, kMiscCount = 4640, kMiscBytes = 4704;
@@ -146,7 +144,18 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-
+// 16 lanes x 8 columns (x2: 16 columns): thread i gets lane i / 4, columns 2 (i % 4) and + 1,
+// in r[0..1], lane i / 4 + 8, the same columns, in r[2..3]; the next 8 columns in r[4..7]
+__device__ __forceinline__ void tmem_ld_16x8(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t* r) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
@@ -240,8 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   static_assert(NH == 32 || NH == 64, "padded head count");
   constexpr int HB = NH / 16;             // blocks of 16 heads: TMEM lanes 32x.. hold block x % HB
   constexpr int R = kSoftWarps / HB;      // warps that hold the same heads share a tile's rows
-  constexpr int kCols = kNt / R;          // rows of a tile per warp: the hi lanes take the first
-  constexpr int kHalf = kCols / 2;        // half of them, the lo lanes the second
+  constexpr int kCols = kNt / R;          // rows of a tile per warp
   constexpr int kSBufs = NH == 64 ? 1 : 2;
   const DecodeParams& p = kp.qp.p;
   extern __shared__ char smem_raw[];
@@ -249,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   int* list_s = reinterpret_cast<int*>(smem + kOffList);
   float2* rows_s = reinterpret_cast<float2*>(smem + kOffScale);          // [kStages][kNt]
+  float* inv_s = reinterpret_cast<float*>(smem + kOffInv);               // [kStages][kNt]
   char* misc = smem + kOffMisc;
   float2* ml_s = reinterpret_cast<float2*>(misc + kMiscMl);              // [64] (m, l)
   float* alpha_s = reinterpret_cast<float*>(misc + kMiscAlpha);          // [2][64] rescale factors
@@ -358,14 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
   };
 
-  // warps 0-7: this lane's head, its reference (log2 units, the same in every warp and lane
-  // that holds the head) and this lane's share of its sum
+  // warps 0-7: a thread holds two heads of its warp's 16 (rows lane / 4 and + 8 of a 16-lane
+  // load), their references (log2 units, the same in every thread that holds the head) and
+  // its share of their sums
   const int quad = warp & 3, half = warp >> 2;
-  const int hh = 16 * (quad % HB) + (lane & 15);
-  const bool lo_lane = lane >= 16;
+  const int hA = 16 * (quad % HB) + (lane >> 2);
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-  float ref = -INFINITY, l_part = 0.f;
-  bool bad_q = false;
+  float ref[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
+  bool bad_q[2] = {false, false};
   if (warp < kSoftWarps) {
     // =================== q into TMEM, softmax, O rescale (warps 0-7) ================
     if (n_local > 0) {
@@ -420,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       named_barrier(1, kSoftThreads);
-      const char* mine = qst + (hh + (lo_lane ? 64 : 0)) * kQPitch;
+      const char* mine = qst + (16 * (quad % HB) + (lane & 15) + (lane >= 16 ? 64 : 0)) * kQPitch;
 #pragma unroll 1
       for (int c = half; c < 9; c += 2) {     // 64 columns of q are 16 columns of TMEM
         uint32_t v[16];
@@ -437,98 +446,103 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarQReady]);
     }
-    float c_head = n_local > 0 ? qc_s[hh] : 0.f;
-    bad_q = c_head != c_head;
-    if (bad_q) c_head = 1e-30f;
-    // S = hi + lo / 16: this lane's term times fa, its partner's times fb
-    const float fa = lo_lane ? 0.0625f : 1.f, fb = lo_lane ? 1.f : 0.0625f;
+    float c_head[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      c_head[u] = n_local > 0 ? qc_s[hA + 8 * u] : 0.f;
+      bad_q[u] = c_head[u] != c_head[u];
+      if (bad_q[u]) c_head[u] = 1e-30f;
+    }
     const int share = quad / HB + (4 / HB) * half;
-    const int cb = share * kCols + (lo_lane ? kHalf : 0);   // this lane's first tile row
+    const int col0 = share * kCols + 2 * (lane & 3);        // tile rows col0 + 8 j and + 1, j < kCols / 8
     // The warps leave the loop together: one that gives up a wait says so before barrier B of
     // its tile (flags of even and odd tiles apart), and all look behind it.
     for (int i = 0; i < n_local; ++i) {
-      const int bb = i & 1, sb = kSBufs == 2 ? bb : 0;
+      const int bb = i & 1, sb = kSBufs == 2 ? bb : 0, st = i % kStages;
       if (*abort_s || !wait_warp(&bars[kBarSFull + sb], (kSBufs == 2 ? i >> 1 : i) & 1)) stop_s[bb] = 1;
       // (complete: QK^T waited for it; this wait orders the reads of the rows' scales)
-      if (!wait_warp(&bars[kBarKvFull + i % kStages], (i / kStages) & 1)) stop_s[bb] = 1;
+      if (!wait_warp(&bars[kBarKvFull + st], (i / kStages) & 1)) stop_s[bb] = 1;
       tc_fence_after();
-      uint32_t v[kCols];
-      const uint32_t s_col = lane_base + (sb ? kColS1 : kColS) + share * kCols;
+      constexpr int kOct = kCols / 8;                       // 8-row groups of this warp
+      float x[4 * kOct];                                    // log2 of P: [j][head][row]
+      {
+        uint32_t vh[4 * kOct], vl[4 * kOct];
+        const uint32_t s_col = lane_base + (sb ? kColS1 : kColS) + share * kCols;
 #pragma unroll
-      for (int k = 0; k < kCols / 8; ++k) tmem_ld8(s_col + 8 * k, v + 8 * k);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarSFree + sb]);
-      const float4* rs = reinterpret_cast<const float4*>(rows_s + (i % kStages) * kNt + cb);
-      const int nvalid = total - kNt * ((int)crank + (int)G * i) - cb;   // of this lane's rows
-      float s[kHalf];
-      float mx = -INFINITY;
+        for (int k = 0; k < kOct / 2; ++k) {
+          tmem_ld_16x16(s_col + 16 * k, vh + 8 * k);
+          tmem_ld_16x16(s_col + (16u << 16) + 16 * k, vl + 8 * k);
+        }
+        if constexpr (kOct % 2 == 1) {
+          tmem_ld_16x8(s_col + 8 * (kOct - 1), vh + 4 * (kOct - 1));
+          tmem_ld_16x8(s_col + (16u << 16) + 8 * (kOct - 1), vl + 4 * (kOct - 1));
+        }
+        tmem_ld_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarSFree + sb]);
 #pragma unroll
-      for (int j = 0; j < kHalf; j += 2) {
-        const float4 cr = rs[j / 2];
+        for (int k = 0; k < 4 * kOct; ++k) x[k] = fmaf(__uint_as_float(vl[k]), 0.0625f, __uint_as_float(vh[k]));
+      }
+      const float2* rs = rows_s + st * kNt + col0;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int j = 0; j < kOct; ++j) {
+        const float4 cr = *reinterpret_cast<const float4*>(rs + 8 * j);   // two rows' (scale, log2 scale)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float own = __uint_as_float(lo_lane ? v[kHalf + j + u] : v[j + u]);
-          const float got = __shfl_xor_sync(0xffffffffu, __uint_as_float(lo_lane ? v[j + u] : v[kHalf + j + u]), 16);
-          const float x = fmaf(own, fa, got * fb) * (u ? cr.z : cr.x);
-          s[j + u] = j + u < nvalid ? x : -INFINITY;
-          mx = fmaxf(mx, fmaf(s[j + u], c_head, u ? cr.w : cr.y));
+          x[4 * j + 2 * u] = fmaf(x[4 * j + 2 * u], cr.x * c_head[u], cr.y);
+          x[4 * j + 2 * u + 1] = fmaf(x[4 * j + 2 * u + 1], cr.z * c_head[u], cr.w);
+          mx[u] = fmaxf(mx[u], fmaxf(x[4 * j + 2 * u], x[4 * j + 2 * u + 1]));
         }
       }
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
       float* mm = max_s + bb * (R * NH);
-      if (!lo_lane) mm[share * NH + hh] = mx;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
+        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
+        if ((lane & 3) == 0) mm[share * NH + hA + 8 * u] = mx[u];
+      }
       // P buffer bb is free once P.V of tile i-2 has read it
       if (i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) stop_s[bb] = 1;
       // B: every warp's maxima of tile i are published; whether any head's reference moves
-      const bool move = barrier_or(2, kSoftThreads, i > 0 && mx > ref + kMostP);
+      const bool move = barrier_or(2, kSoftThreads, i > 0 && (mx[0] > ref[0] + kMostP || mx[1] > ref[1] + kMostP));
       if (stop_s[bb]) {
         fail();
         break;
       }
       if (i == 0 || move) {
 #pragma unroll
-        for (int w = 0; w < R; ++w) mx = fmaxf(mx, mm[w * NH + hh]);
-        const float ref_new = (i == 0 || mx > ref + kMostP) ? mx - kPeak : ref;
-        const float alpha = i == 0 ? 1.f : ex2(ref - ref_new);
-        ref = ref_new;
-        l_part *= alpha;
-        if (move && share == 0 && !lo_lane) alpha_s[64 * bb + hh] = alpha;
-      }
-      uint32_t hi[kHalf / 4], lo[kHalf / 4];
-      float sum = 0.f;
-#pragma unroll
-      for (int j = 0; j < kHalf; j += 4) {
-        uint32_t h2[2], l2[2];
-#pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float4 cr = rs[j / 2 + u];
-          const float e0 = ex2(fmaf(s[j + 2 * u], c_head, -ref)), e1 = ex2(fmaf(s[j + 2 * u + 1], c_head, -ref));
-          sum += e0 + e1;
-          // 11 bits are enough under the 8 that hi and lo keep
-          const __half2 w = __floats2half2_rn(e0 * cr.x, e1 * cr.z);
-          h2[u] = e4m3x2_h(w);
-          l2[u] = e4m3x2_h(__hsub2(w, half2_of(h2[u])));
-        }
-        hi[j / 4] = h2[0] | (h2[1] << 16);
-        lo[j / 4] = l2[0] | (l2[1] << 16);
-      }
-      l_part += sum;
-      {
-        // this head's row of P^T, bytes cb .. cb + kHalf - 1 of the K-major SW128 row
-        char* row = smem + kOffP + bb * 2 * kPBytes + hh * 128;
-        constexpr int kW = kHalf % 8 == 0 ? 2 : 1;   // words a store
+          float m = mx[u];
 #pragma unroll
-        for (int u = 0; u < kHalf / 4; u += kW) {
-          const int byte = cb + 4 * u;
-          char* at = row + ((((byte >> 4) ^ (hh & 7)) << 4) | (byte & 15));
-          if constexpr (kW == 2) {
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[u], hi[u + 1]);
-            *reinterpret_cast<uint2*>(at + kPBytes) = make_uint2(lo[u], lo[u + 1]);
-          } else {
-            *reinterpret_cast<uint32_t*>(at) = hi[u];
-            *reinterpret_cast<uint32_t*>(at + kPBytes) = lo[u];
+          for (int w = 0; w < R; ++w) m = fmaxf(m, mm[w * NH + hA + 8 * u]);
+          const float ref_new = (i == 0 || m > ref[u] + kMostP) ? m - kPeak : ref[u];
+          const float alpha = i == 0 ? 1.f : ex2(ref[u] - ref_new);
+          ref[u] = ref_new;
+          l_part[u] *= alpha;
+          if (move && share == 0 && (lane & 3) == 0) alpha_s[64 * bb + hA + 8 * u] = alpha;
+        }
+      }
+      {
+        // P = 2^(x - ref) as hi + lo, two rows at a time, into bytes of the head's K-major
+        // SW128 row of P^T; p = P / scale into the sum
+        const float* iv = inv_s + st * kNt + col0;
+        char* row = smem + kOffP + bb * 2 * kPBytes + hA * 128;   // (hA + 8: the same swizzle)
+#pragma unroll
+        for (int j = 0; j < kOct; ++j) {
+          const float2 inv = *reinterpret_cast<const float2*>(iv + 8 * j);
+          const int byte = col0 + 8 * j;
+          char* at = row + ((((byte >> 4) ^ (hA & 7)) << 4) | (byte & 15));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const float p0 = ex2(x[4 * j + 2 * u] - ref[u]), p1 = ex2(x[4 * j + 2 * u + 1] - ref[u]);
+            l_part[u] = fmaf(p0, inv.x, fmaf(p1, inv.y, l_part[u]));
+            // 11 bits are enough under the 8 that hi and lo keep
+            const __half2 w = __floats2half2_rn(p0, p1);
+            const uint32_t hi = e4m3x2_h(w);
+            *reinterpret_cast<uint16_t*>(at + 1024 * u) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t*>(at + 1024 * u + kPBytes) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
           }
         }
         fence_proxy_async_smem();
@@ -585,9 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int at = done % kStages;
       for (int q = lane; q < kRowsOf; q += 32) {
-        // ceil(log2 x): an upper bound of the weight's exponent, exact for powers of two
-        const float x = raw_s[at * kNt + tile_row(q)];
-        rows_s[at * kNt + tile_row(q)] = make_float2(x, (float)(((int)__float_as_uint(x) + 0x7fffff) >> 23) - 127.f);
+        // a row that does not exist has weight 0 (the copies leave its scale 0)
+        const int y = at * kNt + tile_row(q);
+        const float x = raw_s[y];
+        rows_s[y] = make_float2(x, __log2f(x));
+        inv_s[y] = x > 0.f ? __frcp_rn(x) : 0.f;
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -750,21 +766,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       have_o = wait_warp(&bars[kBarPvFinal], 0);
       if (!have_o) fail();
     }
-    // the head's sum: its two lanes of each of its R warps, in a fixed order
-    lpart_s[warp * 32 + lane] = l_part;
+    // the head's sum: its four threads of each of its R warps, in a fixed order
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      float l = l_part[u];
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (bad_q[u]) l = __int_as_float(0x7fc00000);
+      if ((lane & 3) == 0) lpart_s[warp * 16 + (lane >> 2) + 8 * u] = l;
+      if (warp < HB && (lane & 3) == 0) ml_s[hA + 8 * u].x = ref[u];
+    }
     named_barrier(1, kSoftThreads);
-    if (warp < HB && !lo_lane) {
+    if (threadIdx.x < NH) {
+      const int hd = threadIdx.x;
       float l = 0.f;
 #pragma unroll
-      for (int w = 0; w < R; ++w) l += lpart_s[(warp + w * HB) * 32 + lane] + lpart_s[(warp + w * HB) * 32 + lane + 16];
-      if (bad_q && have_o) l = __int_as_float(0x7fc00000);
-      ml_s[hh] = have_o ? make_float2(ref, l) : make_float2(-INFINITY, 0.f);
+      for (int w = 0; w < R; ++w) l += lpart_s[(hd / 16 + w * HB) * 16 + hd % 16];
+      ml_s[hd] = have_o ? make_float2(ml_s[hd].x, l) : make_float2(-INFINITY, 0.f);
     }
   }
   tc_fence_before();
   cluster_sync();   // every CTA's (m, l) is published and its stages are idle
   tc_fence_after();
-  if (warp < HB && !lo_lane) {
+  if (threadIdx.x < NH) {
+    const int hh = threadIdx.x;
     // this head's largest reference M, sum L and this CTA's weight 2^(m - M) / L
     float M = -INFINITY;
     for (uint32_t c = 0; c < G; ++c) M = fmaxf(M, ld_cluster_f32(mapa(&ml_s[hh], c)));
