@@ -57,7 +57,7 @@ constexpr int kStages = 3;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
-constexpr int kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 6;
+constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 6;
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPeak = 4.0f;        // log2 of P at the maximum a reference is taken from
@@ -101,7 +101,19 @@ struct Q8Params {
   int groups;        // head groups of a token
   int group_heads;   // heads of a group (the last may have fewer)
   int num_rows;      // rows of the cache: the index that the gathers read as zeros
+  uint32_t bs_mul, bs_shift, gr_mul, gr_shift;   // division by block_size and by group
 };
+
+// n / d for 0 <= n < 2^31 as (n * mul) >> shift, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d)
+// (mul < 2^32, and the error n (mul d - 2^shift) / (d 2^shift) stays below 1 / d)
+__device__ __forceinline__ int div_by(int n, uint32_t mul, uint32_t shift) {
+  return (int)(((uint64_t)(uint32_t)n * mul) >> shift);
+}
+void divisor(int d, uint32_t& mul, uint32_t& shift) {
+  shift = 31;
+  while ((1ull << (shift - 31)) < (uint64_t)d) ++shift;
+  mul = (uint32_t)(((1ull << shift) + (uint64_t)d - 1) / (uint64_t)d);
+}
 
 // D[tmem] (+)= A * B, e4m3 operands, fp32 accumulation.  A shared-memory descriptor's high
 // word (strides, swizzle) is a constant of the operand; the low word is the address.
@@ -207,22 +219,25 @@ __device__ __forceinline__ void bulk_store_s2g(void* dst, uint32_t src, uint32_t
                : "memory");
 }
 
-// The rows of entries j0 + 32 k + lane < c_end (k < 8) of the selected list, -1 for those that
-// do not resolve to a row of this unit; returns how many do.
-template <bool kInterleaved>
-__device__ __forceinline__ int resolve8(const DecodeParams& p, const int32_t* idx, int j0, int c_end, int lane,
-                                        const ShardSel& sel, int bt_row, bool report, int (&row)[8]) {
-  const int32_t* table = p.block_table + (size_t)bt_row * p.max_blocks;
-  int cnt = 0, pos[8];
+// entries j0 + 32 k + lane < c_end (k < 8) of the selected list, -1 behind its end
+__device__ __forceinline__ void load8(const int32_t* idx, int j0, int c_end, int lane, int (&pos)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const int j = j0 + 32 * k + lane;
     pos[k] = j < c_end ? __ldg(idx + j) : -1;
   }
+}
+// their rows, -1 for those that do not resolve to a row of this unit; returns how many do
+template <bool kInterleaved>
+__device__ __forceinline__ int resolve8(const Q8Params& kp, int (&pos)[8], const ShardSel& sel, int bt_row, bool report,
+                                        int (&row)[8]) {
+  const DecodeParams& p = kp.qp.p;
+  const int32_t* table = p.block_table + (size_t)bt_row * p.max_blocks;
+  int cnt = 0;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
     const bool in = sel.has_fixed<kInterleaved>(pos[k]);
-    const int blk = in ? (int)((unsigned)pos[k] / (unsigned)p.block_size) : 0;
+    const int blk = in ? div_by(pos[k], kp.bs_mul, kp.bs_shift) : 0;
     pos[k] = in ? pos[k] - blk * p.block_size : -1;      // the offset in its block
     row[k] = in && blk < p.max_blocks ? __ldg(table + blk) : -1;
   }
@@ -282,15 +297,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int t = tr % T, r = p.n_splits - 1 - tr / T;
   const int h0 = hg * kp.group_heads, nh = min(kp.group_heads, p.h - h0);
   const int b = t / p.Q, qi = t % p.Q;
-  const int seq_len = p.seq_lens[b];
-  const ShardSel sel = shard_sel(seq_len, seq_len - (p.Q - 1 - qi), r, p.n_splits, p.interleave);
   const int bt_row = p.bt_per_token ? t : b;
   const int32_t* idx = p.topk_idx + (size_t)t * p.top_k;
   const uint4* qsrc = reinterpret_cast<const uint4*>(p.q + ((size_t)t * p.h + h0) * kDQK);
   const long long wl = p.wait_limit;
 
   // ---- set-up ----------------------------------------------------------------------
+  // Warps 0-7 bring q into TMEM; meanwhile warps 8-15 resolve the list and start the gathers.
   for (int x = threadIdx.x; x < nh * (kDQK * 2 / 128); x += kThreads) prefetch_l2(qsrc + 8 * x);
+  const int chunk = ((p.top_k + kListWarps * 32 - 1) / (kListWarps * 32)) * 32;
+  const int c_begin = min((warp - kSoftWarps) * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
+  int pos_r[8];
+  if (warp >= kSoftWarps) load8(idx, c_begin, c_end, lane, pos_r);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars[kBarKvFull + s], 2 * kProducerWarps);   // each: its gathers issued, its copies landed
@@ -310,54 +328,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_s = stop_s[0] = stop_s[1] = 0;
     fence_barrier_init();
   }
-  if (warp == 0) {
+  if (warp == 1) {
     tmem_alloc(tmem_base_s, kTmemCols);
     tmem_relinquish();
   }
   if (warp == kProducerWarp && lane == 0) prefetch_tmap(&tmap_rows);
-
-  // ---- index resolution: count per warp chunk, then ordered compaction into smem ----
-  // (rounds of 8 entries a lane; a list of one round stays in registers, a longer one is
-  // resolved again, from L1, for the compaction)
-  const int chunk = ((p.top_k + kWarps * 32 - 1) / (kWarps * 32)) * 32;
-  const int c_begin = min(warp * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
-  int row_r[8];
-  {
-    int cnt = 0;
-#pragma unroll 1
-    for (int j0 = c_begin; j0 < c_end; j0 += 256)
-      cnt += resolve8<kInterleaved>(p, idx, j0, c_end, lane, sel, bt_row, crank == 0 && hg == 0, row_r);
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
-    if (lane == 0) wcount_s[warp] = cnt;
-  }
-  __syncthreads();
-  int total = 0, off = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const int c = wcount_s[w];
-    if (w < warp) off += c;
-    total += c;
-  }
-#pragma unroll 1
-  for (int j0 = c_begin; j0 < c_end && off < kListCap; j0 += 256) {
-    if (chunk > 256) resolve8<kInterleaved>(p, idx, j0, c_end, lane, sel, bt_row, false, row_r);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
-      const int o = off + __popc(mask & lanemask_lt());
-      if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
-      off += __popc(mask);
-    }
-  }
-  // the last tile's missing rows: an index past the cache, which the gathers read as zeros
-  if (warp == 0)
-    for (int o = total + lane; o < min((total + kNt - 1) / kNt * kNt, kListCap); o += 32) list_s[o] = kp.num_rows;
+  const int seq_len = p.seq_lens[b];
+  const ShardSel sel = shard_sel(seq_len, seq_len - (p.Q - 1 - qi), r, p.n_splits, p.interleave);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_base_s;
-  const int n_tiles = (total + kNt - 1) / kNt;
-  const int n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) / (int)G : 0;
+
+  // ---- index resolution (warps 8-15): count per warp chunk, then ordered compaction ----
+  // (rounds of 8 entries a lane; a list of one round stays in registers, a longer one is
+  // resolved again, from L1, for the compaction)
+  int total = 0;
+  if (warp >= kSoftWarps) {
+    int row_r[8], cnt = 0;
+#pragma unroll 1
+    for (int j0 = c_begin; j0 < c_end; j0 += 256) {
+      if (j0 > c_begin) load8(idx, j0, c_end, lane, pos_r);
+      cnt += resolve8<kInterleaved>(kp, pos_r, sel, bt_row, crank == 0 && hg == 0, row_r);
+    }
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (lane == 0) wcount_s[warp - kSoftWarps] = cnt;
+    named_barrier(4, 32 * kListWarps);
+    int off = 0;
+#pragma unroll
+    for (int w = 0; w < kListWarps; ++w) {
+      const int c = wcount_s[w];
+      if (w < warp - kSoftWarps) off += c;
+      total += c;
+    }
+#pragma unroll 1
+    for (int j0 = c_begin; j0 < c_end && off < kListCap; j0 += 256) {
+      if (chunk > 256) {
+        load8(idx, j0, c_end, lane, pos_r);
+        resolve8<kInterleaved>(kp, pos_r, sel, bt_row, false, row_r);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
+        const int o = off + __popc(mask & lanemask_lt());
+        if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
+        off += __popc(mask);
+      }
+    }
+    // the last tile's missing rows: an index past the cache, which the gathers read as zeros
+    if (warp == kSoftWarps)
+      for (int o = total + lane; o < min((total + kNt - 1) / kNt * kNt, kListCap); o += 32) list_s[o] = kp.num_rows;
+    named_barrier(4, 32 * kListWarps);
+    if (lane == 0 && warp == kSoftWarps) wcount_s[kListWarps] = total;
+    __syncwarp();
+    asm volatile("bar.arrive %0, %1;" ::"r"(5), "r"(kThreads) : "memory");   // the softmax warps read `total`
+  }
+  int n_tiles = 0, n_local = 0;
+  auto count_tiles = [&]() {
+    n_tiles = (total + kNt - 1) / kNt;
+    n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) / (int)G : 0;
+  };
+  if (warp >= kSoftWarps) count_tiles();
 
   auto fail = [&](void) {
     report_status(p.status, kStatusTimeout);
@@ -377,22 +408,25 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool bad_q[2] = {false, false};
   if (warp < kSoftWarps) {
     // =================== q into TMEM, softmax, O rescale (warps 0-7) ================
-    if (n_local > 0) {
+    {
       // q as hi and lo e4m3 rows: coalesced loads (a head a warp), then
       // through shared memory (stages 1 and 2, which the gathers leave alone until q is
       // ready) to the TMEM lanes
       char* qst = smem + kStageBytes;
-      uint4 nx[3];
-      auto load_head = [&](int hd) {
+      uint4 n1[3], n2[3];
+      auto load_head = [&](int hd, uint4 (&x)[3]) {
 #pragma unroll
         for (int k = 0; k < 3; ++k)
-          nx[k] = hd < nh && lane + 32 * k < 72 ? __ldg(qsrc + (size_t)hd * 72 + lane + 32 * k) : make_uint4(0, 0, 0, 0);
+          x[k] = hd < nh && lane + 32 * k < 72 ? __ldg(qsrc + (size_t)hd * 72 + lane + 32 * k) : make_uint4(0, 0, 0, 0);
       };
-      load_head(warp);
+      load_head(warp, n1);
+      load_head(warp + kSoftWarps, n2);
 #pragma unroll 1
       for (int hd = warp; hd < NH; hd += kSoftWarps) {
-        const uint4 x[3] = {nx[0], nx[1], nx[2]};
-        load_head(hd + kSoftWarps);
+        const uint4 x[3] = {n1[0], n1[1], n1[2]};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) n1[k] = n2[k];
+        load_head(hd + 2 * kSoftWarps, n2);
         uint32_t am = 0;
 #pragma unroll
         for (int k = 0; k < 3; ++k) {
@@ -446,10 +480,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarQReady]);
     }
+    named_barrier(5, kThreads);
+    total = wcount_s[kListWarps];
+    count_tiles();
     float c_head[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-      c_head[u] = n_local > 0 ? qc_s[hA + 8 * u] : 0.f;
+      c_head[u] = qc_s[hA + 8 * u];
       bad_q[u] = c_head[u] != c_head[u];
       if (bad_q[u]) c_head[u] = 1e-30f;
     }
@@ -670,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int q = lane; q < kRowsOf; q += 32) {
         const int y = tile_row(q), row = rows[y];
         const bool in = row < kp.num_rows;
-        cp_async4(smem_u32(raw_s + at * kNt + y), kp.qp.scales + (in ? (unsigned)row / (unsigned)kp.qp.group : 0u),
+        cp_async4(smem_u32(raw_s + at * kNt + y), kp.qp.scales + (in ? div_by(row, kp.gr_mul, kp.gr_shift) : 0),
                   in ? 4 : 0);
       }
       cp_commit();
@@ -785,8 +822,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ml_s[hd] = have_o ? make_float2(ml_s[hd].x, l) : make_float2(-INFINITY, 0.f);
     }
   }
+  // (a CTA alone needs no cluster barrier, here and below)
   tc_fence_before();
-  cluster_sync();   // every CTA's (m, l) is published and its stages are idle
+  if (G > 1) cluster_sync(); else __syncthreads();   // every CTA's (m, l) is published and its stages are idle
   tc_fence_after();
   if (threadIdx.x < NH) {
     const int hh = threadIdx.x;
@@ -853,13 +891,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int hd = warp; hd < nh; hd += kSoftWarps)
           bulk_store_s2g(dst + (size_t)hd * row, smem_u32(smem) + hd * row, row);
         bulk_commit_group();
-        bulk_wait<0>();
+        bulk_wait_read<0>();
       }
       __syncwarp();
     }
   }
   tc_fence_before();
-  cluster_sync();   // every CTA's scaled partial O has landed with its owner
+  if (G > 1) cluster_sync();   // every CTA's scaled partial O has landed with its owner
   tc_fence_after();
   if (G > 1 && warp < kSoftWarps && !*abort_s) {
     // this CTA's segments: the sum of the G scaled partials, in the order of the CTAs
@@ -890,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 
 template <int NH, bool kIL>
@@ -959,6 +997,8 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
                                      : (il ? q8_kernel<64, true>() : q8_kernel<64, false>());
   CUtensorMap rows;
   kp.num_rows = p.num_blocks * p.block_size;
+  divisor(p.block_size, kp.bs_mul, kp.bs_shift);
+  divisor(qp.group, kp.gr_mul, kp.gr_shift);
   if (!make_rows_map(&rows, p.kv, kp.num_rows)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
