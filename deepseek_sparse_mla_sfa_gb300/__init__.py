@@ -52,13 +52,28 @@ def _stream_ptr(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on(dev, stream):
     """Context of a call: `dev` current, and what the call allocates belongs to its stream."""
     if stream is None:
-        return contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        return _HERE if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"stream must be on {dev}, got {stream.device}")
     return torch.cuda.stream(stream)
+
+
+def _raw_stream(dev):
+    """The stream of the call (inside `_on`)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
+def _check(t, name, dtype, dev, ndim):
+    """_need on a CUDA device, quick where nothing is wrong."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index and t.dim() == ndim
+            and t.is_contiguous()):
+        _need(t, name, dtype, dev, ndim)
 
 
 def _need(t, name, dtype, device=None, ndim=None):
@@ -387,20 +402,20 @@ def decode_q8_workspace_bytes(B: int, Q: int, h: int, top_k: int, n_splits: int)
 
 def _need_cache_q8(kv8, scales):
     """The checks of an 8-bit cache [num_blocks, block_size, 576] and its scales [num_blocks,
-    block_size / group]; returns the group."""
+    block_size / group]; returns (num_blocks, block_size, group)."""
     _need(kv8, "kv8", torch.float8_e4m3fn, None, 3)
     _need(scales, "scales", torch.float32, None, 2)
     nb, bs, d = kv8.shape
     if d != D_QK:
         raise ValueError("kv8 rows must have 576 columns")
-    groups = scales.shape[1]
-    if scales.shape[0] != nb or groups < 1 or bs % groups:
+    rows, groups = scales.shape
+    if rows != nb or groups < 1 or bs % groups:
         raise ValueError("scales must be [num_blocks, block_size / group] with group dividing block_size")
-    if kv8.device.type != "cuda":
+    if not kv8.is_cuda:
         raise ValueError("the 8-bit cache must be on a CUDA device")
-    if scales.device != kv8.device:
+    if scales.get_device() != kv8.get_device():
         raise ValueError(f"scales must be on {kv8.device}, got {scales.device}")
-    return bs // groups
+    return nb, bs, bs // groups
 
 
 def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_splits: int = 1, Q: int = 1,
@@ -413,62 +428,73 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
     them).  out is [B*Q, h, 512] in `out_dtype` (torch.float32 or torch.bfloat16, or the dtype
     of the `out` given).  Everything else as in ``decode``.
     """
-    group = _need_cache_q8(kv8, scales)
-    for t, name, dt, nd in ((q, "q", torch.bfloat16, 3), (block_table, "block_table", torch.int32, 2),
-                            (seq_lens, "seq_lens", torch.int32, 1), (topk_idx, "topk_idx", torch.int32, 2)):
-        _need(t, name, dt, kv8.device, nd)
+    num_blocks, block_size, group = _need_cache_q8(kv8, scales)
+    dev = kv8.device
+    _check(q, "q", torch.bfloat16, dev, 3)
+    _check(block_table, "block_table", torch.int32, dev, 2)
+    _check(seq_lens, "seq_lens", torch.int32, dev, 1)
+    _check(topk_idx, "topk_idx", torch.int32, dev, 2)
     T, h, d = q.shape
     if d != D_QK:
         raise ValueError("q rows must have 576 columns")
     if int(Q) != Q or Q < 1:
         raise ValueError("Q must be an integer >= 1")
     Q = int(Q)
-    B, top_k = seq_lens.shape[0], topk_idx.shape[1]
-    if T != B * Q or topk_idx.shape[0] != T or block_table.shape[0] != (T if block_table_per_token else B):
+    B = seq_lens.shape[0]
+    lists, top_k = topk_idx.shape
+    tables, max_blocks = block_table.shape
+    if T != B * Q or lists != T or tables != (T if block_table_per_token else B):
         raise ValueError("inconsistent B / Q / T")
     if interleave < 0:
         raise ValueError("interleave must be >= 0")
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype not in (torch.float32, torch.bfloat16):
+    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
-    lib, dev = _lib.load(), kv8.device
+    lib = _lib.load()
     final = n_splits == 1 or merge
+    out_p = lse_p = op_p = lp_p = ws_p = ws_bytes = 0
     with _on(dev, stream):
         if final:
             if out is None:
                 out = torch.empty((T, h, D_V), dtype=out_dtype, device=dev)
+            elif out.shape != (T, h, D_V):
+                raise ValueError(f"out must be [{T}, {h}, {D_V}] and lse [{T}, {h}]")
+            else:
+                _check(out, "out", out_dtype, dev, 3)
             if lse is None:
                 lse = torch.empty((T, h), dtype=torch.float32, device=dev)
-            _need(out, "out", out_dtype, dev)
-            _need(lse, "lse", torch.float32, dev)
-            if tuple(out.shape) != (T, h, D_V) or tuple(lse.shape) != (T, h):
+            elif lse.shape != (T, h):
                 raise ValueError(f"out must be [{T}, {h}, {D_V}] and lse [{T}, {h}]")
+            else:
+                _check(lse, "lse", torch.float32, dev, 2)
+            out_p, lse_p = out.data_ptr(), lse.data_ptr()
         if n_splits > 1:
             if out_part is None:
                 out_part = torch.empty((n_splits, T, h, D_V), dtype=torch.float32, device=dev)
             if lse_part is None:
                 lse_part = torch.empty((n_splits, T, h), dtype=torch.float32, device=dev)
-            _need(out_part, "out_part", torch.float32, dev)
-            _need(lse_part, "lse_part", torch.float32, dev)
-            if tuple(out_part.shape) != (n_splits, T, h, D_V) or tuple(lse_part.shape) != (n_splits, T, h):
+            if out_part.shape != (n_splits, T, h, D_V) or lse_part.shape != (n_splits, T, h):
                 raise ValueError(f"out_part must be [{n_splits}, {T}, {h}, {D_V}] and lse_part [{n_splits}, {T}, {h}]")
+            _check(out_part, "out_part", torch.float32, dev, 4)
+            _check(lse_part, "lse_part", torch.float32, dev, 3)
+            op_p, lp_p = out_part.data_ptr(), lse_part.data_ptr()
         if workspace is None:
-            need = int(lib.sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits))
+            need = lib.sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits)
             if need:
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         elif workspace.device != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {dev}")
-        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        if workspace is not None:
+            ws_p, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         flags = (BLOCK_TABLE_PER_TOKEN if block_table_per_token else 0) | \
-                (OUT_BF16 if final and out_dtype == torch.bfloat16 else 0)
-        code = lib.sfa_decode_q8(_ptr(q), _ptr(kv8), _ptr(scales), group, _ptr(block_table), _ptr(seq_lens),
-                                 _ptr(topk_idx), B, Q, h, top_k, kv8.shape[0], kv8.shape[1], block_table.shape[1],
-                                 float(scale), n_splits, int(interleave), flags, _ptr(out if final else None),
-                                 _ptr(lse if final else None), _ptr(out_part if n_splits > 1 else None),
-                                 _ptr(lse_part if n_splits > 1 else None), _ptr(workspace), ws_bytes,
-                                 _stream_ptr(stream, dev))
-    _lib.check("sfa_decode_q8", code)
+                (OUT_BF16 if final and out_dtype is torch.bfloat16 else 0)
+        code = lib.sfa_decode_q8(q.data_ptr(), kv8.data_ptr(), scales.data_ptr(), group, block_table.data_ptr(),
+                                 seq_lens.data_ptr(), topk_idx.data_ptr(), B, Q, h, top_k, num_blocks, block_size,
+                                 max_blocks, scale, n_splits, interleave, flags, out_p, lse_p, op_p, lp_p, ws_p,
+                                 ws_bytes, _raw_stream(dev))
+    if code:
+        _lib.check("sfa_decode_q8", code)
     return (out, lse) if final else (out_part, lse_part)
 
 
@@ -486,22 +512,24 @@ def kv_write_q8(kv8, scales, slot_mapping, rows, workspace=None, stream=None):
     workspace: kv_write_q8_workspace_bytes(num_blocks * block_size, group) bytes that belong to
     this cache, zeroed once before the first write (not needed for groups of one slot).
     """
-    group = _need_cache_q8(kv8, scales)
+    num_blocks, block_size, group = _need_cache_q8(kv8, scales)
     dev = kv8.device
-    _need(slot_mapping, "slot_mapping", torch.int32, dev, 1)
-    _need(rows, "rows", torch.bfloat16, dev, 2)
-    if rows.shape[1] != D_QK or rows.shape[0] != slot_mapping.shape[0]:
+    _check(slot_mapping, "slot_mapping", torch.int32, dev, 1)
+    _check(rows, "rows", torch.bfloat16, dev, 2)
+    T, d = rows.shape
+    if d != D_QK or T != slot_mapping.shape[0]:
         raise ValueError("rows must be [T, 576] with one slot per row")
-    ws_bytes = 0
+    ws_p = ws_bytes = 0
     if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
+        if workspace.get_device() != dev.index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be contiguous and on {dev}")
-        ws_bytes = workspace.numel() * workspace.element_size()
+        ws_p, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     with _on(dev, stream):
-        code = _lib.load().sfa_kv_write_q8(_ptr(kv8), _ptr(scales), kv8.shape[0] * kv8.shape[1], group,
-                                           _ptr(slot_mapping), _ptr(rows), rows.shape[0], _ptr(workspace), ws_bytes,
-                                           _stream_ptr(stream, dev))
-    _lib.check("sfa_kv_write_q8", code)
+        code = _lib.load().sfa_kv_write_q8(kv8.data_ptr(), scales.data_ptr(), num_blocks * block_size, group,
+                                           slot_mapping.data_ptr(), rows.data_ptr(), T, ws_p, ws_bytes,
+                                           _raw_stream(dev))
+    if code:
+        _lib.check("sfa_kv_write_q8", code)
     return kv8, scales
 
 
@@ -518,23 +546,31 @@ def step_plan(cached_lens, new_lens, block_table, free_blocks, taken, block_size
     dev = block_table.device
     if dev.type != "cuda":
         raise ValueError("step_plan runs on a CUDA device only")
-    for t, name, nd in ((block_table, "block_table", 2), (cached_lens, "cached_lens", 1), (new_lens, "new_lens", 1),
-                        (free_blocks, "free_blocks", 1), (taken, "taken", 1)):
-        _need(t, name, torch.int32, dev, nd)
-    B = block_table.shape[0]
+    _check(block_table, "block_table", torch.int32, dev, 2)
+    _check(cached_lens, "cached_lens", torch.int32, dev, 1)
+    _check(new_lens, "new_lens", torch.int32, dev, 1)
+    _check(free_blocks, "free_blocks", torch.int32, dev, 1)
+    _check(taken, "taken", torch.int32, dev, 1)
+    B, max_blocks = block_table.shape
     if cached_lens.shape[0] != B or new_lens.shape[0] != B or taken.shape[0] != 1:
         raise ValueError("cached_lens and new_lens must be [B], block_table [B, max_blocks] and taken [1]")
     N = int(num_tokens)
     if N < 0:
         raise ValueError("num_tokens must be >= 0")
     with _on(dev, stream):
-        seq_lens, start, positions, slots, taken_out = torch.empty(
-            2 * B + 2 * N + 2, dtype=torch.int32, device=dev).split([B, B + 1, N, N, 1])
-        code = _lib.load().sfa_step_plan(_ptr(cached_lens), _ptr(new_lens), B, int(block_size), _ptr(block_table),
-                                         block_table.shape[1], _ptr(free_blocks), free_blocks.shape[0], _ptr(taken),
-                                         N, _ptr(seq_lens), _ptr(start), _ptr(positions), _ptr(slots),
-                                         _ptr(taken_out), _stream_ptr(stream, dev))
-    _lib.check("sfa_step_plan", code)
+        # (five allocations take less of the host's time than five views of one)
+        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
+        start = torch.empty(B + 1, dtype=torch.int32, device=dev)
+        positions = torch.empty(N, dtype=torch.int32, device=dev)
+        slots = torch.empty(N, dtype=torch.int32, device=dev)
+        taken_out = torch.empty(1, dtype=torch.int32, device=dev)
+        code = _lib.load().sfa_step_plan(cached_lens.data_ptr(), new_lens.data_ptr(), B, block_size,
+                                         block_table.data_ptr(), max_blocks, free_blocks.data_ptr(),
+                                         free_blocks.shape[0], taken.data_ptr(), N, seq_lens.data_ptr(),
+                                         start.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                                         taken_out.data_ptr(), _raw_stream(dev))
+    if code:
+        _lib.check("sfa_step_plan", code)
     return block_table, seq_lens, start, positions, slots, taken_out
 
 
@@ -594,13 +630,21 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
     dev = x.device
     if dev.type != "cuda":
         raise ValueError("rope runs on a CUDA device only")
-    if x.dtype not in _ROPE_DTYPES:
+    dtype = _ROPE_DTYPES.get(x.dtype)
+    if dtype is None:
         raise TypeError(f"x must be bfloat16, float16 or float32, got {x.dtype}")
-    if x.dim() not in (2, 3) or x.shape[-1] < 1 or x.stride(-1) != 1:
+    shape, strides = x.shape, x.stride()
+    if len(shape) == 3:
+        (T, n, width), (xt, xn, xd) = shape, strides
+    elif len(shape) == 2:
+        (T, width), (xt, xd), n, xn = shape, strides, 1, 0
+    else:
+        xd = 0
+    if xd != 1 or width < 1:
         raise ValueError("x must be [T, n, width] or [T, width] with contiguous columns")
-    _need(positions, "positions", torch.int32, dev, 1)
-    _need(inv_freq, "inv_freq", torch.float64, dev, 1)
-    T, width, rot = x.shape[0], x.shape[-1], 2 * inv_freq.shape[0]
+    _check(positions, "positions", torch.int32, dev, 1)
+    _check(inv_freq, "inv_freq", torch.float64, dev, 1)
+    rot = 2 * inv_freq.shape[0]
     if positions.shape[0] != T:
         raise ValueError("positions must be [T]")
     if rot < 2 or rot > width:
@@ -609,16 +653,16 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
         if out is None:
             # a padding row has no result: a new tensor holds x's there
             out = x.clone(memory_format=torch.contiguous_format)
-        elif out.dtype != x.dtype or out.device != dev or out.shape != x.shape or out.stride(-1) != 1:
+        elif out.dtype is not x.dtype or out.get_device() != dev.index or out.shape != shape or out.stride(-1) != 1:
             raise ValueError("out must have x's shape, dtype and device, and contiguous columns")
-        n = x.shape[1] if x.dim() == 3 else 1
         if n == 0:
             return out
-        code = _lib.load().sfa_rope(_ptr(x), x.stride(0), x.stride(1) if x.dim() == 3 else 0, _ptr(out),
-                                    out.stride(0), out.stride(1) if out.dim() == 3 else 0, _ROPE_DTYPES[x.dtype], T,
-                                    n, width, rot, _ptr(positions), _ptr(inv_freq), float(mscale),
-                                    (1 if interleaved else 0) | (2 if inverse else 0), _stream_ptr(stream, dev))
-    _lib.check("sfa_rope", code)
+        os = out.stride()
+        code = _lib.load().sfa_rope(x.data_ptr(), xt, xn, out.data_ptr(), os[0], os[1] if len(shape) == 3 else 0,
+                                    dtype, T, n, width, rot, positions.data_ptr(), inv_freq.data_ptr(), mscale,
+                                    (1 if interleaved else 0) | (2 if inverse else 0), _raw_stream(dev))
+    if code:
+        _lib.check("sfa_rope", code)
     return out
 
 

@@ -73,6 +73,8 @@ def header_functions(path: str = HEADER):
 def load(path: str = LIB_PATH):
     """Load libsfa.so and declare its signatures (raises if it is missing)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

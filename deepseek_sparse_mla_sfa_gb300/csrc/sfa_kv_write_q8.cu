@@ -11,12 +11,15 @@
 //
 // Two launches: the first takes each row's amax and joins it to its group's record in the
 // workspace (atomic max / or / add: the result does not depend on their order); the second
-// quantises.  The first warp of a group to arrive there rewrites the group's other rows
-// when its scale rose; the last one stores the scale and clears the record, so the
+// quantises.  It is launched early (programmatic dependent launch) and loads its rows while
+// the first still runs.  The first row of a group to arrive there rewrites the group's other
+// rows when its scale rose; the last one stores the scale and clears the record, so the
 // workspace is zero between calls.  Groups of one slot need no record and take one launch.
 //
-// Bound: HBM, 1152 bytes read and 576 written a row; latency for a decode step's rows.
+// Bound: HBM, 1152 bytes read and 576 written a row; latency for a decode step's rows, where
+// four warps take a row (one load each, and a group is rewritten four times as fast).
 #include <cuda_fp8.h>
+#include <string.h>
 
 #include "sfa_internal.h"
 
@@ -25,7 +28,8 @@ namespace {
 
 constexpr int kRowWords = kDQK * 2 / 16;   // 72 x 16 bytes per bf16 row
 constexpr int kRow8Words = kDQK / 16;      // 36 x 16 bytes per e4m3 row
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;         // 8 rows a block, a warp each
+constexpr int kFewThreads = 128;      // or one row a block
 constexpr int kMinExp = -100, kMaxExp = 120;
 
 struct GroupRecord {
@@ -88,70 +92,106 @@ __device__ __forceinline__ unsigned requantise4(unsigned w, float ratio) {
   return out;
 }
 
-__device__ __forceinline__ unsigned warp_max(unsigned v) { return __reduce_max_sync(0xffffffffu, v); }
+// kRowThreads threads share a row: its words threadIdx.x % kRowThreads + kRowThreads i
+template <int kRowThreads>
+struct Row {
+  static constexpr int kWords = (kRowWords + kRowThreads - 1) / kRowThreads;
+  uint4 x[kWords];
+  long long slot;   // -1: padding, out of range or behind the last row
+  int lane;
 
-// this warp's row into registers; returns its slot, or -1 (padding, out of range)
-__device__ __forceinline__ long long load_row(const int32_t* slots, const uint4* rows, int T, long long num_slots,
-                                              int t, int lane, uint4 (&x)[3], int* status) {
-  if (t >= T) return -1;
-  const long long slot = slots[t];
-  if (slot < 0) return -1;
-  if (slot >= num_slots) {
-    if (status && lane == 0) report_status(status, kStatusBadBlock);
-    return -1;
+  __device__ __forceinline__ void load(const int32_t* slots, const uint4* rows, int T, long long num_slots,
+                                       int* status) {
+    const long long t = (blockIdx.x * (long long)blockDim.x + threadIdx.x) / kRowThreads;
+    lane = threadIdx.x % kRowThreads;
+    slot = -1;
+    if (t >= T) return;
+    slot = slots[t];
+    const uint4* src = rows + (size_t)t * kRowWords + lane;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      x[i] = lane + kRowThreads * i < kRowWords ? __ldg(src + kRowThreads * i) : make_uint4(0, 0, 0, 0);
+    if (slot >= num_slots) {
+      if (status && lane == 0) report_status(status, kStatusBadBlock);
+      slot = -1;
+    }
   }
-  const uint4* src = rows + (size_t)t * kRowWords;
+  // the row's largest finite magnitude, as bits (every thread of the row calls it; with more
+  // than a warp a row, every thread of the block)
+  __device__ __forceinline__ unsigned amax() const {
+    unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    x[i] = lane + 32 * i < kRowWords ? __ldg(src + lane + 32 * i) : make_uint4(0, 0, 0, 0);
-  return slot;
-}
-
-__device__ __forceinline__ void store_row(uint4* kv8, long long slot, int lane, const uint4 (&x)[3], float s) {
-  uint2* dst = reinterpret_cast<uint2*>(kv8 + (size_t)slot * kRow8Words);
+    for (int i = 0; i < kWords; ++i) m = max(m, amax_bits(x[i]));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if constexpr (kRowThreads > 32) {
+      __shared__ unsigned m_s[kRowThreads / 32];
+      if (lane % 32 == 0) m_s[lane / 32] = m;
+      __syncthreads();
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (lane + 32 * i < kRowWords) dst[lane + 32 * i] = quantise8(x[i], s);
-}
+      for (int w = 0; w < kRowThreads / 32; ++w) m = max(m, m_s[w]);
+    }
+    return m;
+  }
+  __device__ __forceinline__ void store(uint4* kv8, float s) const {
+    uint2* dst = reinterpret_cast<uint2*>(kv8 + (size_t)slot * kRow8Words) + lane;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+      if (lane + kRowThreads * i < kRowWords) dst[kRowThreads * i] = quantise8(x[i], s);
+  }
+  // a value of the row's thread 0 to all of them, and a barrier over the row
+  __device__ __forceinline__ int broadcast(int v) const {
+    if constexpr (kRowThreads > 32) {
+      __shared__ int v_s;
+      __syncthreads();
+      if (lane == 0) v_s = v;
+      __syncthreads();
+      return v_s;
+    } else {
+      return __shfl_sync(0xffffffffu, v, 0);
+    }
+  }
+};
 
+template <int kRowThreads>
 __global__ void __launch_bounds__(kThreads) q8_need_kernel(const float* __restrict__ scales, long long num_slots,
                                                            const int32_t* __restrict__ slots,
                                                            const uint4* __restrict__ rows, int T, int group,
                                                            GroupRecord* rec, int* status) {
-  const int t = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  uint4 x[3];
-  const long long slot = load_row(slots, rows, T, num_slots, t, lane, x, status);
-  if (slot < 0) return;
-  const unsigned m = warp_max(max(amax_bits(x[0]), max(amax_bits(x[1]), amax_bits(x[2]))));
-  if (lane == 0) {
-    const long long g = slot / group;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  Row<kRowThreads> row;
+  row.load(slots, rows, T, num_slots, status);
+  if (row.slot < 0) return;                      // (the same for all threads of a row)
+  const unsigned m = row.amax();
+  if (row.lane == 0) {
+    const long long g = row.slot / group;
     GroupRecord* r = rec + g;
     atomicMax(&r->need, scale_exp(m) - kMinExp + 1);
     r->old = scales[g];                          // the same value from every row of the group
     atomicAdd(&r->count, 1);
-    atomicOr(&r->mask, 1ull << (slot - g * group));
+    atomicOr(&r->mask, 1ull << (row.slot - g * group));
   }
 }
 
+template <int kRowThreads>
 __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* scales, long long num_slots,
                                                             const int32_t* __restrict__ slots,
                                                             const uint4* __restrict__ rows, int T, int group,
                                                             GroupRecord* rec) {
-  const int t = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  uint4 x[3];
-  const long long slot = load_row(slots, rows, T, num_slots, t, lane, x, nullptr);
-  if (slot < 0) return;
-  const long long g = slot / group;
+  Row<kRowThreads> row;
+  row.load(slots, rows, T, num_slots, nullptr);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the records are complete
+  if (row.slot < 0) return;
+  const long long g = row.slot / group;
   GroupRecord* r = rec + g;
-  const unsigned long long mask = r->mask;
-  const float was = r->old;
+  const unsigned long long mask = __ldcg(&r->mask);
+  const float was = __ldcg(&r->old);
   const float old = ((mask & 1) || !(was > 0.f) || was > 3e38f) ? 0.f : was;
-  const float s = fmaxf(old, exp2_int(r->need - 1 + kMinExp));
-  const int count = r->count;
-  store_row(kv8, slot, lane, x, s);
-  __syncwarp();                                  // every lane has its copy of the record
+  const float s = fmaxf(old, exp2_int(__ldcg(&r->need) - 1 + kMinExp));
+  const int count = __ldcg(&r->count);
+  row.store(kv8, s);
+  row.broadcast(0);                              // every thread has its copy of the record
   int ticket = 0;
-  if (lane == 0) {
+  if (row.lane == 0) {
     __threadfence();
     ticket = atomicAdd(&r->done, 1);
     if (ticket == count - 1) {                   // every row of the group has read the record
@@ -163,35 +203,69 @@ __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* s
       r->mask = 0;
     }
   }
-  ticket = __shfl_sync(0xffffffffu, ticket, 0);
+  ticket = row.broadcast(ticket);
   if (ticket == 0 && old > 0.f && s > old) {
     // the group's rows that this call does not write: from scale `old` to `s`
     const float ratio = old / s;
     uint4* base = kv8 + (size_t)g * group * kRow8Words;
-    for (int j = lane; j < group * kRow8Words; j += 32) {
-      if ((mask >> (j / kRow8Words)) & 1) continue;
-      uint4 w = base[j];
-      w.x = requantise4(w.x, ratio);
-      w.y = requantise4(w.y, ratio);
-      w.z = requantise4(w.z, ratio);
-      w.w = requantise4(w.w, ratio);
-      base[j] = w;
+    const int words = group * kRow8Words;
+    constexpr int kFly = 6;                      // words in flight a thread
+    for (int j0 = row.lane; j0 < words; j0 += kFly * kRowThreads) {
+      uint4 w[kFly];
+      bool in[kFly];
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        const int j = j0 + k * kRowThreads;
+        in[k] = j < words && !((mask >> (j / kRow8Words)) & 1);
+        if (in[k]) w[k] = base[j];
+      }
+#pragma unroll
+      for (int k = 0; k < kFly; ++k) {
+        if (!in[k]) continue;
+        base[j0 + k * kRowThreads] = make_uint4(requantise4(w[k].x, ratio), requantise4(w[k].y, ratio),
+                                                requantise4(w[k].z, ratio), requantise4(w[k].w, ratio));
+      }
     }
   }
 }
 
 // groups of one slot: a row's scale is its own
+template <int kRowThreads>
 __global__ void __launch_bounds__(kThreads) q8_row_kernel(uint4* kv8, float* scales, long long num_slots,
                                                           const int32_t* __restrict__ slots,
                                                           const uint4* __restrict__ rows, int T, int* status) {
-  const int t = (int)((blockIdx.x * (long long)kThreads + threadIdx.x) >> 5), lane = threadIdx.x & 31;
-  uint4 x[3];
-  const long long slot = load_row(slots, rows, T, num_slots, t, lane, x, status);
-  if (slot < 0) return;
-  const unsigned m = warp_max(max(amax_bits(x[0]), max(amax_bits(x[1]), amax_bits(x[2]))));
-  const float s = exp2_int(scale_exp(m));
-  if (lane == 0) scales[slot] = s;
-  store_row(kv8, slot, lane, x, s);
+  Row<kRowThreads> row;
+  row.load(slots, rows, T, num_slots, status);
+  if (row.slot < 0) return;
+  const float s = exp2_int(scale_exp(row.amax()));
+  if (row.lane == 0) scales[row.slot] = s;
+  row.store(kv8, s);
+}
+
+template <int kRowThreads>
+cudaError_t launch_rows(uint4* kv8, float* scales, long long num_slots, int group, const int32_t* slots,
+                        const uint4* rows, int T, GroupRecord* rec, int* status, cudaStream_t stream) {
+  const int threads = kRowThreads > 32 ? kRowThreads : kThreads;
+  const unsigned grid = (unsigned)(((long long)T * kRowThreads + threads - 1) / threads);
+  if (group == 1) {
+    q8_row_kernel<kRowThreads><<<grid, threads, 0, stream>>>(kv8, scales, num_slots, slots, rows, T, status);
+    return cudaGetLastError();
+  }
+  q8_need_kernel<kRowThreads><<<grid, threads, 0, stream>>>(scales, num_slots, slots, rows, T, group, rec, status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, q8_store_kernel<kRowThreads>, kv8, scales, num_slots, slots, rows, T, group, rec);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -199,19 +273,13 @@ __global__ void __launch_bounds__(kThreads) q8_row_kernel(uint4* kv8, float* sca
 cudaError_t launch_kv_write_q8(void* kv8, float* scales, long long num_slots, int group, const int32_t* slots,
                                const void* rows, int T, void* workspace, int* status, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  const unsigned grid = (unsigned)(((long long)T * 32 + kThreads - 1) / kThreads);
   uint4* kv = static_cast<uint4*>(kv8);
   const uint4* src = static_cast<const uint4*>(rows);
-  if (group == 1) {
-    q8_row_kernel<<<grid, kThreads, 0, stream>>>(kv, scales, num_slots, slots, src, T, status);
-    return cudaGetLastError();
-  }
   GroupRecord* rec = static_cast<GroupRecord*>(workspace);
-  q8_need_kernel<<<grid, kThreads, 0, stream>>>(scales, num_slots, slots, src, T, group, rec, status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  q8_store_kernel<<<grid, kThreads, 0, stream>>>(kv, scales, num_slots, slots, src, T, group, rec);
-  return cudaGetLastError();
+  // four warps a row while that leaves the GPU's blocks few
+  return T <= 4 * device_sm_count()
+             ? launch_rows<kFewThreads>(kv, scales, num_slots, group, slots, src, T, rec, status, stream)
+             : launch_rows<32>(kv, scales, num_slots, group, slots, src, T, rec, status, stream);
 }
 
 }  // namespace sfa

@@ -52,12 +52,16 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kNt = 96;              // selected rows per tile: N of QK^T, K of P.V
-constexpr int kStages = 3;
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+#ifndef CNT
+#define CNT 96
+#define CST 3
+#define CPW 6
+#endif
+constexpr int kNt = CNT;              // selected rows per tile: N of QK^T, K of P.V
+constexpr int kStages = CST;
+constexpr int kThreads = 640;
 constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
-constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 6;
+constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = CPW, kFixWarp = 16, kFixWarps = 4;
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPeak = 4.0f;        // log2 of P at the maximum a reference is taken from
@@ -68,29 +72,31 @@ constexpr int kBlk = kNt * 128;                       // 128 latent columns of a
 constexpr int kStageBytes = 4 * kBlk + kNt * 64;      // + 64 rope columns, SW64
 constexpr int kOffP = kStages * kStageBytes;
 constexpr int kPBytes = kGroupHeads * 128;            // P^T [heads x 96 rows] e4m3, K-major SW128 rows
-constexpr int kOffList = kOffP + 4 * kPBytes;         // two buffers of hi and lo
-constexpr int kListCap = 48 * kNt;                    // resolved rows kept at once (whole tiles)
-constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and row: (scale, log2 scale)
+constexpr int kPLo = kNt == 64 ? 64 : kPBytes;        // lo follows hi in the row where both fit, else in a tile of its own
+constexpr int kPBuf = kNt == 64 ? kPBytes : 2 * kPBytes;
+constexpr int kOffList = kOffP + 2 * kPBuf;           // two buffers
+constexpr int kListCap = 4608 / kNt * kNt;                    // resolved rows kept at once (whole tiles)
+constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and two rows: scales, then their log2
 constexpr int kOffInv = kOffScale + kStages * kNt * 8;  // 1 / scale
 constexpr int kOffRaw = kOffInv + kStages * kNt * 4;    // the scales as they land
 constexpr int kOffMisc = kOffRaw + kStages * kNt * 4;
-constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscMax = 1024, kMiscScale = 3072, kMiscSum = 3328,
-              kMiscC = 4352, kMiscFlags = 4608, kMiscTmem = 4624, kMiscCount = 4640, kMiscBytes = 4704;
+constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscScale = 1024, kMiscC = 1280, kMiscFlags = 1536, kMiscTmem = 1540,
+              kMiscMoved = 1544, kMiscCount = 1560, kMiscBytes = 1600;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
 constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarQReady = kBarKvEmpty + kStages,
-              kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarPReady = kBarSFree + 2,
+              kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarWReady = kBarSFree + 2, kBarPReady = kBarWReady + 2,
               kBarPFree = kBarPReady + 2, kBarPvFinal = kBarPFree + 2, kBarMmaFin = kBarPvFinal + 1,
               kBarMmaFin2 = kBarMmaFin + 1, kBarNever = kBarMmaFin2 + 1, kNumBars = kBarNever + 1;
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 1024;
+constexpr bool kRowsCheck = kNt % (4 * kProducerWarps) == 0 && (kNt / kProducerWarps) % 8 == 0;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kBlk % 1024 == 0 && kStageBytes % 1024 == 0 && kOffP % 1024 == 0, "operands: 1024-byte alignment");
 static_assert(kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
-static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the output and the cluster merge fit in the stages");
-static_assert(kMiscSum + 4 * 32 * kSoftWarps <= kMiscC && kMiscMax + 4 * 2 * 256 <= kMiscScale, "misc");
+static_assert(kRowsCheck && 2048 * kGroupHeads <= kStages * kStageBytes, "the output and the cluster merge fit in the stages");
 // q's e4m3 rows on their way to TMEM, in stages 1 and 2: 128 rows (64 hi, 64 lo) of 576 bytes
 constexpr int kQPitch = 592;   // an odd number of 16-byte words: rows start in different banks
-static_assert(128 * kQPitch <= 2 * kStageBytes, "q fits in stages 1 and 2");
-static_assert(kMiscCount + 4 * kWarps <= kMiscBytes, "misc");
+static_assert(128 * kQPitch <= (kStages - 1) * kStageBytes, "q fits in stages 1 and 2");
+static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscBytes, "misc");
 
 constexpr long long kDrainLimit = 1LL << 40;
 constexpr uint32_t kTmemCols = 512;
@@ -156,13 +162,8 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                : "r"(taddr));
 }
-// 16 lanes x 8 columns (x2: 16 columns): thread i gets lane i / 4, columns 2 (i % 4) and + 1,
-// in r[0..1], lane i / 4 + 8, the same columns, in r[2..3]; the next 8 columns in r[4..7]
-__device__ __forceinline__ void tmem_ld_16x8(uint32_t taddr, uint32_t* r) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(taddr));
-}
+// 16 lanes x 16 columns: thread i gets lane i / 4, columns 2 (i % 4) and + 1, in r[0..1], lane
+// i / 4 + 8, the same columns, in r[2..3]; columns 8 .. 15 in r[4..7]
 __device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
@@ -203,17 +204,6 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
-// named barrier that also ORs a predicate over its threads
-__device__ __forceinline__ bool barrier_or(int id, int count, bool v) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 q, %3, 0;\n\t"
-      "bar.red.or.pred p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"((uint32_t)v)
-      : "memory");
-  return r != 0;
-}
 __device__ __forceinline__ void bulk_store_s2g(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
                : "memory");
@@ -251,6 +241,34 @@ __device__ __forceinline__ int resolve8(const Q8Params& kp, int (&pos)[8], const
   return cnt;
 }
 
+// two fp32 in a register pair
+__device__ __forceinline__ uint64_t pack2u(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pack2(float a, float b) { return pack2u(__float_as_uint(a), __float_as_uint(b)); }
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  uint32_t a, b;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(a), "=r"(b) : "l"(v));
+  return make_float2(__uint_as_float(a), __uint_as_float(b));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
@@ -262,28 +280,24 @@ template <int NH, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 1)
     decode_q8_kernel(const __grid_constant__ CUtensorMap tmap_rows, const __grid_constant__ Q8Params kp) {
   static_assert(NH == 32 || NH == 64, "padded head count");
-  constexpr int HB = NH / 16;             // blocks of 16 heads: TMEM lanes 32x.. hold block x % HB
-  constexpr int R = kSoftWarps / HB;      // warps that hold the same heads share a tile's rows
-  constexpr int kCols = kNt / R;          // rows of a tile per warp
+  constexpr int HB = NH / 16;             // blocks of 16 heads: TMEM lanes 32x.. hold block x < HB
   constexpr int kSBufs = NH == 64 ? 1 : 2;
   const DecodeParams& p = kp.qp.p;
   extern __shared__ char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   int* list_s = reinterpret_cast<int*>(smem + kOffList);
-  float2* rows_s = reinterpret_cast<float2*>(smem + kOffScale);          // [kStages][kNt]
+  float4* rows_s = reinterpret_cast<float4*>(smem + kOffScale);          // [kStages][kNt / 2]
   float* inv_s = reinterpret_cast<float*>(smem + kOffInv);               // [kStages][kNt]
   char* misc = smem + kOffMisc;
   float2* ml_s = reinterpret_cast<float2*>(misc + kMiscMl);              // [64] (m, l)
   float* alpha_s = reinterpret_cast<float*>(misc + kMiscAlpha);          // [2][64] rescale factors
-  float* max_s = reinterpret_cast<float*>(misc + kMiscMax);              // [2][R][NH] partial maxima
+  uint8_t* moved_s = reinterpret_cast<uint8_t*>(misc + kMiscMoved);      // [2][8] whether 8 heads' references moved
   float* scale_s = reinterpret_cast<float*>(misc + kMiscScale);          // [64] output scales
-  float* lpart_s = reinterpret_cast<float*>(misc + kMiscSum);            // [8][32] partial sums
   float* qc_s = reinterpret_cast<float*>(misc + kMiscC);                 // [64] score scale, NaN for a bad head
   volatile int* abort_s = reinterpret_cast<volatile int*>(misc + kMiscFlags);
-  volatile int* stop_s = abort_s + 1;                                    // [2]
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(misc + kMiscTmem);
-  int* wcount_s = reinterpret_cast<int*>(misc + kMiscCount);             // [kWarps]
+  int* wcount_s = reinterpret_cast<int*>(misc + kMiscCount);             // [kListWarps + 1]: counts, total
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_ctarank();
@@ -308,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int chunk = ((p.top_k + kListWarps * 32 - 1) / (kListWarps * 32)) * 32;
   const int c_begin = min((warp - kSoftWarps) * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
   int pos_r[8];
-  if (warp >= kSoftWarps) load8(idx, c_begin, c_end, lane, pos_r);
+  if (warp >= kSoftWarps && warp < kFixWarp) load8(idx, c_begin, c_end, lane, pos_r);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars[kBarKvFull + s], 2 * kProducerWarps);   // each: its gathers issued, its copies landed
@@ -317,15 +331,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&bars[kBarQReady], kSoftWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarSFull + x], 1);
-      mbar_init(&bars[kBarSFree + x], kSoftWarps);
-      mbar_init(&bars[kBarPReady + x], kSoftWarps);
+      mbar_init(&bars[kBarSFree + x], 2 * HB);      // the softmax warps that hold heads
+      mbar_init(&bars[kBarWReady + x], 2 * HB);     // their weights are written
+      mbar_init(&bars[kBarPReady + x], kFixWarps);  // and O follows their references
       mbar_init(&bars[kBarPFree + x], 1);
     }
     mbar_init(&bars[kBarPvFinal], 1);
     mbar_init(&bars[kBarMmaFin], 1);
     mbar_init(&bars[kBarMmaFin2], 1);
     mbar_init(&bars[kBarNever], 1);         // nothing arrives: the stall test hook waits on it
-    *abort_s = stop_s[0] = stop_s[1] = 0;
+    *abort_s = 0;
+    for (int x = 0; x < 16; ++x) moved_s[x] = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (rounds of 8 entries a lane; a list of one round stays in registers, a longer one is
   // resolved again, from L1, for the compaction)
   int total = 0;
-  if (warp >= kSoftWarps) {
+  if (warp >= kSoftWarps && warp < kFixWarp) {
     int row_r[8], cnt = 0;
 #pragma unroll 1
     for (int j0 = c_begin; j0 < c_end; j0 += 256) {
@@ -381,13 +397,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_barrier(4, 32 * kListWarps);
     if (lane == 0 && warp == kSoftWarps) wcount_s[kListWarps] = total;
     __syncwarp();
-    asm volatile("bar.arrive %0, %1;" ::"r"(5), "r"(kThreads) : "memory");   // the softmax warps read `total`
+    asm volatile("bar.arrive %0, %1;" ::"r"(5), "r"(kThreads) : "memory");   // the other warps read `total`
   }
   int n_tiles = 0, n_local = 0;
   auto count_tiles = [&]() {
     n_tiles = (total + kNt - 1) / kNt;
     n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) / (int)G : 0;
   };
+  if (warp >= kFixWarp) {
+    named_barrier(5, kThreads);
+    total = wcount_s[kListWarps];
+  }
   if (warp >= kSoftWarps) count_tiles();
 
   auto fail = [&](void) {
@@ -398,14 +418,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
   };
 
-  // warps 0-7: a thread holds two heads of its warp's 16 (rows lane / 4 and + 8 of a 16-lane
-  // load), their references (log2 units, the same in every thread that holds the head) and
-  // its share of their sums
+  // warps 0-7: warp 4 half + quad holds heads 16 quad + 8 half .. + 7 whole, a thread one of
+  // them (row lane / 4 + 8 half of a 16-lane load), its reference (log2 units) and its share of
+  // its sum; with 32 heads or fewer the warps of two quadrants hold none
   const int quad = warp & 3, half = warp >> 2;
-  const int hA = 16 * (quad % HB) + (lane >> 2);
+  const int head = 16 * quad + 8 * half + (lane >> 2);
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-  float ref[2] = {-INFINITY, -INFINITY}, l_part[2] = {0.f, 0.f};
-  bool bad_q[2] = {false, false};
+  float ref = -INFINITY, l_sum = 0.f;
+  bool bad_q = false;
   if (warp < kSoftWarps) {
     // =================== q into TMEM, softmax, O rescale (warps 0-7) ================
     {
@@ -463,9 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       named_barrier(1, kSoftThreads);
-      const char* mine = qst + (16 * (quad % HB) + (lane & 15) + (lane >= 16 ? 64 : 0)) * kQPitch;
+      const char* mine = qst + (16 * quad + (lane & 15) + (lane >= 16 ? 64 : 0)) * kQPitch;
 #pragma unroll 1
-      for (int c = half; c < 9; c += 2) {     // 64 columns of q are 16 columns of TMEM
+      for (int c = half; c < 9 && quad < HB; c += 2) {     // 64 columns of q are 16 columns of TMEM
         uint32_t v[16];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -483,131 +503,135 @@ __global__ void __launch_bounds__(kThreads, 1)
     named_barrier(5, kThreads);
     total = wcount_s[kListWarps];
     count_tiles();
-    float c_head[2];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      c_head[u] = qc_s[hA + 8 * u];
-      bad_q[u] = c_head[u] != c_head[u];
-      if (bad_q[u]) c_head[u] = 1e-30f;
-    }
-    const int share = quad / HB + (4 / HB) * half;
-    const int col0 = share * kCols + 2 * (lane & 3);        // tile rows col0 + 8 j and + 1, j < kCols / 8
-    // The warps leave the loop together: one that gives up a wait says so before barrier B of
-    // its tile (flags of even and odd tiles apart), and all look behind it.
-    for (int i = 0; i < n_local; ++i) {
-      const int bb = i & 1, sb = kSBufs == 2 ? bb : 0, st = i % kStages;
-      if (*abort_s || !wait_warp(&bars[kBarSFull + sb], (kSBufs == 2 ? i >> 1 : i) & 1)) stop_s[bb] = 1;
-      // (complete: QK^T waited for it; this wait orders the reads of the rows' scales)
-      if (!wait_warp(&bars[kBarKvFull + st], (i / kStages) & 1)) stop_s[bb] = 1;
-      tc_fence_after();
-      constexpr int kOct = kCols / 8;                       // 8-row groups of this warp
-      float x[4 * kOct];                                    // log2 of P: [j][head][row]
-      {
-        uint32_t vh[4 * kOct], vl[4 * kOct];
-        const uint32_t s_col = lane_base + (sb ? kColS1 : kColS) + share * kCols;
-#pragma unroll
-        for (int k = 0; k < kOct / 2; ++k) {
-          tmem_ld_16x16(s_col + 16 * k, vh + 8 * k);
-          tmem_ld_16x16(s_col + (16u << 16) + 16 * k, vl + 8 * k);
+    if (quad < HB) {
+      float c_head = qc_s[head];
+      bad_q = c_head != c_head;
+      if (bad_q) c_head = 1e-30f;
+      const uint64_t c2 = pack2(c_head, c_head), sixteenth = pack2(0.0625f, 0.0625f);
+      uint64_t l2 = 0;                                        // two running sums
+      // this head's row of P^T (K-major SW128) and this thread's bytes 16 k + 8 u + 2 (lane % 4)
+      char* const p_row = smem + kOffP + head * 128 + 2 * (lane & 3);
+      for (int i = 0; i < n_local; ++i) {
+        const int bb = i & 1, sb = kSBufs == 2 ? bb : 0, st = i % kStages;
+        // (the tile is complete, QK^T waited for it: its wait orders the reads of the rows' scales)
+        if (*abort_s || !wait_warp(&bars[kBarSFull + sb], (kSBufs == 2 ? i >> 1 : i) & 1) ||
+            !wait_warp(&bars[kBarKvFull + st], (i / kStages) & 1)) {
+          fail();
+          break;
         }
-        if constexpr (kOct % 2 == 1) {
-          tmem_ld_16x8(s_col + 8 * (kOct - 1), vh + 4 * (kOct - 1));
-          tmem_ld_16x8(s_col + (16u << 16) + 8 * (kOct - 1), vl + 4 * (kOct - 1));
+        tc_fence_after();
+        // x = log2 of the weight: S = hi + lo / 16, then scale, head factor and log2 scale.
+        // Pairs of rows 8 j + 2 (lane % 4), j < 12
+        uint64_t x[kNt / 8];
+        constexpr int kBatch = kNt / 32;                    // 16-row loads in flight at a time
+        const uint32_t s_col = lane_base + (sb ? kColS1 : kColS);
+        const float4* rs = rows_s + st * (kNt / 2) + (lane & 3);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int k3 = 0; k3 < kNt / 16; k3 += kBatch) {
+          uint32_t vh[kBatch][8], vl[kBatch][8];
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k) {
+            tmem_ld_16x16(s_col + 16 * (k3 + k), vh[k]);
+            tmem_ld_16x16(s_col + (16u << 16) + 16 * (k3 + k), vl[k]);
+          }
+          tmem_ld_wait();
+          if (k3 + kBatch == kNt / 16) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[kBarSFree + sb]);
+          }
+#pragma unroll
+          for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const int j = 2 * (k3 + k) + u;
+              const uint64_t hi = half ? pack2u(vh[k][4 * u + 2], vh[k][4 * u + 3]) : pack2u(vh[k][4 * u], vh[k][4 * u + 1]);
+              const uint64_t lo = half ? pack2u(vl[k][4 * u + 2], vl[k][4 * u + 3]) : pack2u(vl[k][4 * u], vl[k][4 * u + 1]);
+              const float4 cr = rs[4 * j];
+              x[j] = fma2(fma2(lo, sixteenth, hi), mul2(pack2(cr.x, cr.y), c2), pack2(cr.z, cr.w));
+              const float2 f = unpack2(x[j]);
+              mx = fmaxf(mx, fmaxf(f.x, f.y));
+            }
         }
-        tmem_ld_wait();
-        tc_fence_before();
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // P buffer bb, and its flags and factors, are free once P.V of tile i-2 is done
+        if (i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) {
+          fail();
+          break;
+        }
+        const bool up = i == 0 || mx > ref + kMostP;
+        const float ref_new = up ? mx - kPeak : ref;
+        const bool moved = __any_sync(0xffffffffu, i > 0 && up);
+        if (moved) {
+          const float alpha = ex2(ref - ref_new);
+          l2 = mul2(l2, pack2(alpha, alpha));
+          if ((lane & 3) == 0) alpha_s[64 * bb + head] = alpha;
+        }
+        if (lane == 0) moved_s[8 * bb + 2 * quad + half] = moved;
+        ref = ref_new;
+        // P = 2^(x - ref) as hi + lo; p = P / scale into the sum
+        const uint64_t nref = pack2(-ref, -ref);
+        const float2* iv = reinterpret_cast<const float2*>(inv_s + st * kNt) + (lane & 3);
+        char* const row = p_row + bb * kPBuf;
+#pragma unroll
+        for (int j = 0; j < kNt / 8; ++j) {
+          const float2 f = unpack2(add2(x[j], nref));
+          const float p0 = ex2(f.x), p1 = ex2(f.y);
+          const float2 inv = iv[4 * j];
+          l2 = fma2(pack2(p0, p1), pack2(inv.x, inv.y), l2);
+          // 11 bits are enough under the 8 that hi and lo keep
+          const __half2 w = __floats2half2_rn(p0, p1);
+          const uint32_t hi = e4m3x2_h(w);
+          const int at = (((j >> 1) ^ (head & 7)) << 4) + 8 * (j & 1);
+          *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)hi;
+          *reinterpret_cast<uint16_t*>(row + (kNt == 64 ? at ^ kPLo : at + kPLo)) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
+        }
+        fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarSFree + sb]);
-#pragma unroll
-        for (int k = 0; k < 4 * kOct; ++k) x[k] = fmaf(__uint_as_float(vl[k]), 0.0625f, __uint_as_float(vh[k]));
+        if (lane == 0) mbar_arrive(&bars[kBarWReady + bb]);
       }
-      const float2* rs = rows_s + st * kNt + col0;
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int j = 0; j < kOct; ++j) {
-        const float4 cr = *reinterpret_cast<const float4*>(rs + 8 * j);   // two rows' (scale, log2 scale)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          x[4 * j + 2 * u] = fmaf(x[4 * j + 2 * u], cr.x * c_head[u], cr.y);
-          x[4 * j + 2 * u + 1] = fmaf(x[4 * j + 2 * u + 1], cr.z * c_head[u], cr.w);
-          mx[u] = fmaxf(mx[u], fmaxf(x[4 * j + 2 * u], x[4 * j + 2 * u + 1]));
-        }
-      }
-      float* mm = max_s + bb * (R * NH);
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 1));
-        mx[u] = fmaxf(mx[u], __shfl_xor_sync(0xffffffffu, mx[u], 2));
-        if ((lane & 3) == 0) mm[share * NH + hA + 8 * u] = mx[u];
-      }
-      // P buffer bb is free once P.V of tile i-2 has read it
-      if (i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) stop_s[bb] = 1;
-      // B: every warp's maxima of tile i are published; whether any head's reference moves
-      const bool move = barrier_or(2, kSoftThreads, i > 0 && (mx[0] > ref[0] + kMostP || mx[1] > ref[1] + kMostP));
-      if (stop_s[bb]) {
+      const float2 f = unpack2(l2);
+      l_sum = f.x + f.y;
+      l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 1);
+      l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
+      if (bad_q) l_sum = __int_as_float(0x7fc00000);
+    }
+  } else if (warp >= kFixWarp) {
+    // =================== O follows the references (warps 16-19) ====================
+    // Where a head's reference moved with tile i, its column of O^T is scaled between P.V of
+    // tiles i-1 and i; the softmax warps do not wait for that.
+    const uint32_t my_lanes = tmem + ((uint32_t)((warp - kFixWarp) * 32) << 16);
+    for (int i = 0; i < n_local && !*abort_s; ++i) {
+      const int bb = i & 1;
+      if (!wait_warp(&bars[kBarWReady + bb], (i >> 1) & 1)) {
         fail();
         break;
       }
-      if (i == 0 || move) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float m = mx[u];
-#pragma unroll
-          for (int w = 0; w < R; ++w) m = fmaxf(m, mm[w * NH + hA + 8 * u]);
-          const float ref_new = (i == 0 || m > ref[u] + kMostP) ? m - kPeak : ref[u];
-          const float alpha = i == 0 ? 1.f : ex2(ref[u] - ref_new);
-          ref[u] = ref_new;
-          l_part[u] *= alpha;
-          if (move && share == 0 && (lane & 3) == 0) alpha_s[64 * bb + hA + 8 * u] = alpha;
+      uint64_t m8 = *reinterpret_cast<const volatile uint64_t*>(moved_s + 8 * bb);
+      if (m8 != 0) {
+        if (!wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1)) {
+          fail();
+          break;
         }
-      }
-      {
-        // P = 2^(x - ref) as hi + lo, two rows at a time, into bytes of the head's K-major
-        // SW128 row of P^T; p = P / scale into the sum
-        const float* iv = inv_s + st * kNt + col0;
-        char* row = smem + kOffP + bb * 2 * kPBytes + hA * 128;   // (hA + 8: the same swizzle)
-#pragma unroll
-        for (int j = 0; j < kOct; ++j) {
-          const float2 inv = *reinterpret_cast<const float2*>(iv + 8 * j);
-          const int byte = col0 + 8 * j;
-          char* at = row + ((((byte >> 4) ^ (hA & 7)) << 4) | (byte & 15));
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const float p0 = ex2(x[4 * j + 2 * u] - ref[u]), p1 = ex2(x[4 * j + 2 * u + 1] - ref[u]);
-            l_part[u] = fmaf(p0, inv.x, fmaf(p1, inv.y, l_part[u]));
-            // 11 bits are enough under the 8 that hi and lo keep
-            const __half2 w = __floats2half2_rn(p0, p1);
-            const uint32_t hi = e4m3x2_h(w);
-            *reinterpret_cast<uint16_t*>(at + 1024 * u) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t*>(at + 1024 * u + kPBytes) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
-          }
-        }
-        fence_proxy_async_smem();
-      }
-      if (move) {
-        // O is rescaled once P.V of the previous tile has completed; only the heads (8 at a
-        // time) whose reference moved
-        const bool okp = wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1);
-        if (!okp) fail();
         tc_fence_after();
-        named_barrier(3, kSoftThreads);   // C: the factors are published
-        const float2 a2 = *reinterpret_cast<const float2*>(alpha_s + 64 * bb + 2 * (lane % (NH / 2)));
-        unsigned moved = __ballot_sync(0xffffffffu, a2.x != 1.f || a2.y != 1.f) & (NH == 64 ? ~0u : 0xffffu);
-        while (moved && okp) {
-          const int oct = (__ffs(moved) - 1) >> 2;        // heads 8 oct ..: lanes 4 oct ..
-          moved &= ~(0xfu << (4 * oct));
+#pragma unroll 1
+        while (m8 != 0) {
+          const int oct = (__ffsll((long long)m8) - 1) >> 3;
+          m8 &= m8 - 1;
           const float4 a = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct);
           const float4 c = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct + 4);
           const float al[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-          uint32_t o[16];
-          const uint32_t at = lane_base + kColO + 2 * half * NH + 8 * oct;   // column blocks 2 half and 2 half + 1
-          tmem_ld8(at, o);
-          tmem_ld8(at + NH, o + 8);
+          uint32_t o[32];
+          const uint32_t at = my_lanes + kColO + 8 * oct;
+#pragma unroll
+          for (int m = 0; m < 4; ++m) tmem_ld8(at + NH * m, o + 8 * m);
           tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k & 7]);
-          tmem_st8(at, o);
-          tmem_st8(at + NH, o + 8);
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k & 7]);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) tmem_st8(at + NH * m, o + 8 * m);
         }
         tmem_st_wait();
       }
@@ -615,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
     }
-  } else if (warp >= kProducerWarp) {
+  } else if (warp >= kProducerWarp && warp < kProducerWarp + kProducerWarps) {
     // =================== gathers ===================================================
     // Warp pw takes the tile's row groups pw, pw + 2, ... (4 rows each): 48 gather4 for the
     // latent columns, and the rope words of its 48 rows in 6 rounds of 32 lanes.  Up to three
@@ -632,14 +656,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       switch (issued - done) {
         case 1: cp_wait<0>(); break;
         case 2: cp_wait<1>(); break;
-        default: cp_wait<2>(); break;
+        case 3: cp_wait<2>(); break;
+        case 4: cp_wait<3>(); break;
+        default: cp_wait<4>(); break;
       }
       const int at = done % kStages;
       for (int q = lane; q < kRowsOf; q += 32) {
         // a row that does not exist has weight 0 (the copies leave its scale 0)
         const int y = at * kNt + tile_row(q);
         const float x = raw_s[y];
-        rows_s[y] = make_float2(x, __log2f(x));
+        float* rp = reinterpret_cast<float*>(rows_s) + 4 * (y >> 1) + (y & 1);
+        rp[0] = x;
+        rp[2] = __log2f(x);
         inv_s[y] = x > 0.f ? __frcp_rn(x) : 0.f;
       }
       fence_proxy_async_smem();
@@ -766,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (elect_one()) {
             const uint32_t a0 = desc_lo(st0 + s * kStageBytes, kBlk);
-            const uint32_t b0 = desc_lo(st0 + kOffP + 2 * bb * kPBytes, 16);
+            const uint32_t b0 = desc_lo(st0 + kOffP + bb * kPBuf, 16);
 #pragma unroll
             for (int k = 0; k < kNt / 32; ++k)
 #pragma unroll
@@ -774,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                   mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128)>(
-                      tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPBytes + 32 * k) >> 4), id,
+                      tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPLo + 32 * k) >> 4), id,
                       (k > 0 || part > 0) ? 1u : (n > 0 ? 1u : 0u));
             mma_commit(&bars[kBarKvEmpty + s]);
             mma_commit(&bars[kBarPFree + bb]);
@@ -803,24 +831,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       have_o = wait_warp(&bars[kBarPvFinal], 0);
       if (!have_o) fail();
     }
-    // the head's sum: its four threads of each of its R warps, in a fixed order
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      float l = l_part[u];
-      l += __shfl_xor_sync(0xffffffffu, l, 1);
-      l += __shfl_xor_sync(0xffffffffu, l, 2);
-      if (bad_q[u]) l = __int_as_float(0x7fc00000);
-      if ((lane & 3) == 0) lpart_s[warp * 16 + (lane >> 2) + 8 * u] = l;
-      if (warp < HB && (lane & 3) == 0) ml_s[hA + 8 * u].x = ref[u];
-    }
-    named_barrier(1, kSoftThreads);
-    if (threadIdx.x < NH) {
-      const int hd = threadIdx.x;
-      float l = 0.f;
-#pragma unroll
-      for (int w = 0; w < R; ++w) l += lpart_s[(hd / 16 + w * HB) * 16 + hd % 16];
-      ml_s[hd] = have_o ? make_float2(ml_s[hd].x, l) : make_float2(-INFINITY, 0.f);
-    }
+    if (quad < HB && (lane & 3) == 0)
+      ml_s[head] = have_o ? make_float2(ref, l_sum) : make_float2(-INFINITY, 0.f);
   }
   // (a CTA alone needs no cluster barrier, here and below)
   tc_fence_before();

@@ -13,9 +13,10 @@
 // would be off by 2^-8 rad at position 131072, a double one costs FP64 instructions, which
 // this part issues at 1/64 rate.)
 //
-// Bound: HBM, each element read and written once.  A thread keeps the phases of its 4 pairs
-// and walks rows of the same token, so sines are formed once a token and pair group, not
-// once a head.
+// Bound: HBM, each element read and written once.  A block takes some tokens (and, for few
+// tokens of many heads, a part of their heads): it forms the cosines and sines of its tokens
+// once, in shared memory, and its threads then walk the rows with 4 pairs each and several
+// rows' loads in flight.
 #include <cuda_fp16.h>
 
 #include "sfa_internal.h"
@@ -34,7 +35,8 @@ struct RopeParams {
   int T, n, width, rot;
   int interleaved, inverse, in_place;
   float mscale;
-  int rows_per_thread;
+  int tokens, heads, head_tiles;   // a block's share; blocks per token group
+  uint32_t heads_mul;              // row / heads as (row * heads_mul) >> 32, row < 2^16 (0: heads is 1)
 };
 
 template <typename E> __device__ __forceinline__ float to_f(E v);
@@ -88,83 +90,105 @@ __device__ __forceinline__ void store_elems(E* p, const E (&v)[N]) {
   }
 }
 
+constexpr int kRopeSmem = 32768;   // cosines and sines of a block's tokens
+constexpr int kRopeItems = 8;      // most pair groups a thread
+
 // VP pairs a thread: 4 where every access is aligned for it, else 1
 template <typename E, int VP, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
-  const int groups = p.rot / (2 * VP);                    // pair groups of a row
+  extern __shared__ float2 cs_s[];                        // [tokens][rot / 2], then the positions
+  const int pairs = p.rot / 2, groups = pairs / VP;
+  int* pos_s = reinterpret_cast<int*>(cs_s + p.tokens * pairs);
+  const int t0 = (blockIdx.x / p.head_tiles) * p.tokens, h0 = (blockIdx.x % p.head_tiles) * p.heads;
+  const int nt = min(p.tokens, p.T - t0), nh = min(p.heads, p.n - h0);
+  for (int x = threadIdx.x; x < nt * pairs; x += kRopeThreads) {
+    const int tl = x / pairs, i = x - tl * pairs;
+    const int pos = p.pos[t0 + tl];
+    const unsigned long long frac = turn_fraction(p.inv_freq[i]);
+    const long long ph = (long long)(frac * (unsigned long long)(long long)pos);
+    float sn, cs;
+    sincospif((float)(int)(ph >> 32) * 0x1p-31f, &sn, &cs);
+    cs_s[x] = make_float2(cs * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
+    if (i == 0) pos_s[tl] = pos;
+  }
+  __syncthreads();
   const int lanes = kRopeThreads / groups;                // rows side by side in a block
   const int v = threadIdx.x % groups, y = threadIdx.x / groups;
   if (y >= lanes) return;
-  const long long rows = (long long)p.T * p.n;
-  const long long r0 = (long long)blockIdx.x * lanes * p.rows_per_thread;
-  unsigned long long frac[VP];
+  const E* xb = static_cast<const E*>(p.x) + t0 * p.xt + h0 * p.xn;
+  E* ob = static_cast<E*>(p.out) + t0 * p.ot + h0 * p.on;
+  const int rows = nt * p.heads;                          // (heads past nh are skipped)
+  constexpr int kFly = 4;                                 // rows in flight
+  for (int r0 = y; r0 < rows; r0 += kFly * lanes) {
+    alignas(16) E a[kFly][2 * VP];
+    int tl[kFly], hd[kFly];
+    bool in[kFly];
 #pragma unroll
-  for (int i = 0; i < VP; ++i) frac[i] = turn_fraction(p.inv_freq[v * VP + i]);
-  int have = -1, pos = -1;
-  float c[VP], s[VP];
-  for (int j = 0; j < p.rows_per_thread; ++j) {
-    const long long row = r0 + (long long)j * lanes + y;
-    if (row >= rows) return;
-    const int t = (int)(row / p.n), hd = (int)(row - (long long)t * p.n);
-    if (t != have) {
-      have = t;
-      pos = p.pos[t];
-#pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        const long long ph = (long long)(frac[i] * (unsigned long long)(long long)pos);
-        float sn, cs;
-        sincospif((float)(int)(ph >> 32) * 0x1p-31f, &sn, &cs);
-        c[i] = cs * p.mscale;
-        s[i] = (p.inverse ? -sn : sn) * p.mscale;
+    for (int k = 0; k < kFly; ++k) {
+      const int row = r0 + k * lanes;
+      tl[k] = p.heads_mul ? (int)__umulhi((unsigned)row, p.heads_mul) : row;
+      hd[k] = row - tl[k] * p.heads;
+      in[k] = row < rows && hd[k] < nh && pos_s[min(tl[k], nt - 1)] >= 0;   // a padding row: out stays as it was
+      if (in[k]) {
+        const E* xr = xb + tl[k] * p.xt + hd[k] * p.xn;
+        if constexpr (kInterleaved) {
+          load_elems<(VP > 1), E, 2 * VP>(xr + 2 * VP * v, a[k]);
+        } else {
+          load_elems<(VP > 1), E, VP>(xr + VP * v, *reinterpret_cast<E(*)[VP]>(&a[k][0]));
+          load_elems<(VP > 1), E, VP>(xr + pairs + VP * v, *reinterpret_cast<E(*)[VP]>(&a[k][VP]));
+        }
       }
     }
-    if (pos < 0) continue;                                // a padding row: out stays as it was
-    const E* xr = static_cast<const E*>(p.x) + t * p.xt + hd * p.xn;
-    E* orow = static_cast<E*>(p.out) + t * p.ot + hd * p.on;
-    if constexpr (kInterleaved) {
-      alignas(16) E a[2 * VP];
-      load_elems<(VP > 1), E, 2 * VP>(xr + 2 * VP * v, a);
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      if (!in[k]) continue;
+      const float2* cs = cs_s + tl[k] * pairs + VP * v;
 #pragma unroll
       for (int i = 0; i < VP; ++i) {
-        const float x0 = to_f(a[2 * i]), x1 = to_f(a[2 * i + 1]);
-        a[2 * i] = from_f<E>(x0 * c[i] - x1 * s[i]);
-        a[2 * i + 1] = from_f<E>(x0 * s[i] + x1 * c[i]);
+        constexpr int dx = kInterleaved ? 2 : 1, dy = kInterleaved ? 1 : VP;
+        const float x0 = to_f(a[k][dx * i]), x1 = to_f(a[k][dx * i + dy]);
+        const float2 c = cs[i];
+        a[k][dx * i] = from_f<E>(x0 * c.x - x1 * c.y);
+        a[k][dx * i + dy] = from_f<E>(x0 * c.y + x1 * c.x);
       }
-      store_elems<(VP > 1), E, 2 * VP>(orow + 2 * VP * v, a);
-    } else {
-      alignas(16) E a[VP];
-      alignas(16) E b[VP];
-      load_elems<(VP > 1), E, VP>(xr + VP * v, a);
-      load_elems<(VP > 1), E, VP>(xr + p.rot / 2 + VP * v, b);
-#pragma unroll
-      for (int i = 0; i < VP; ++i) {
-        const float x0 = to_f(a[i]), x1 = to_f(b[i]);
-        a[i] = from_f<E>(x0 * c[i] - x1 * s[i]);
-        b[i] = from_f<E>(x0 * s[i] + x1 * c[i]);
+      E* orow = ob + tl[k] * p.ot + hd[k] * p.on;
+      if constexpr (kInterleaved) {
+        store_elems<(VP > 1), E, 2 * VP>(orow + 2 * VP * v, a[k]);
+      } else {
+        store_elems<(VP > 1), E, VP>(orow + VP * v, *reinterpret_cast<E(*)[VP]>(&a[k][0]));
+        store_elems<(VP > 1), E, VP>(orow + pairs + VP * v, *reinterpret_cast<E(*)[VP]>(&a[k][VP]));
       }
-      store_elems<(VP > 1), E, VP>(orow + VP * v, a);
-      store_elems<(VP > 1), E, VP>(orow + p.rot / 2 + VP * v, b);
+      if (!p.in_place)
+        for (int d = p.rot + v; d < p.width; d += groups) orow[d] = xb[tl[k] * p.xt + hd[k] * p.xn + d];
     }
-    if (!p.in_place)
-      for (int d = p.rot + v; d < p.width; d += groups) orow[d] = xr[d];
   }
 }
 
 template <typename E, int VP>
 cudaError_t launch_typed(RopeParams p, cudaStream_t stream) {
-  const int groups = p.rot / (2 * VP), lanes = kRopeThreads / groups;
-  const long long rows = (long long)p.T * p.n;
-  // rows a thread walks: enough blocks to fill the GPU first, then up to 8 rows of a token
-  // behind one set of sines
-  const long long fill = 8LL * device_sm_count() * lanes;
-  int per = (int)(rows / fill);
-  p.rows_per_thread = per < 1 ? 1 : per > 8 ? 8 : per;
-  const long long grid = (rows + (long long)lanes * p.rows_per_thread - 1) / ((long long)lanes * p.rows_per_thread);
+  const int pairs = p.rot / 2, groups = pairs / VP, lanes = kRopeThreads / groups;
+  // rows a block takes: enough blocks to fill the GPU 4 times over first, then up to
+  // kRopeItems rows a thread; whole tokens, as many as the cosines have room for, or a part
+  // of one token's heads
+  const long long want = (long long)p.T * p.n / (4LL * device_sm_count());
+  const long long most = (long long)lanes * kRopeItems;
+  const long long rows = want < lanes ? lanes : want > most ? most : want;
+  p.tokens = (int)(rows / p.n);
+  const int room = kRopeSmem / (pairs * 8 + 4);
+  p.tokens = p.tokens < 1 ? 1 : p.tokens > room ? room : p.tokens;
+  p.tokens = p.tokens < p.T ? p.tokens : p.T;
+  p.heads = (long long)p.n <= rows ? p.n : (int)rows;
+  p.head_tiles = (p.n + p.heads - 1) / p.heads;
+  p.heads = (p.n + p.head_tiles - 1) / p.head_tiles;
+  if ((long long)p.tokens * p.heads >= 65536) return cudaErrorInvalidValue;
+  p.heads_mul = p.heads == 1 ? 0 : 0xffffffffu / (unsigned)p.heads + 1;
+  const long long grid = (long long)((p.T + p.tokens - 1) / p.tokens) * p.head_tiles;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const size_t smem = (size_t)p.tokens * (pairs * 8 + 4);
   if (p.interleaved)
-    rope_kernel<E, VP, true><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
+    rope_kernel<E, VP, true><<<(unsigned)grid, kRopeThreads, smem, stream>>>(p);
   else
-    rope_kernel<E, VP, false><<<(unsigned)grid, kRopeThreads, 0, stream>>>(p);
+    rope_kernel<E, VP, false><<<(unsigned)grid, kRopeThreads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -187,7 +211,7 @@ cudaError_t launch_rope(const void* x, long long xt, long long xn, void* out, lo
                         int T, int n, int width, int rot, const int32_t* pos, const double* inv_freq,
                         int interleaved, int inverse, float mscale, cudaStream_t stream) {
   const RopeParams p{x,  out,   pos, inv_freq,    xt,      xn,        ot,     on, T,
-                     n,  width, rot, interleaved, inverse, x == out, mscale, 1};
+                     n,  width, rot, interleaved, inverse, x == out, mscale, 1, 1, 1, 0};
   switch (dtype) {
     case 0: return launch_rope_t<__nv_bfloat16>(p, stream);
     case 1: return launch_rope_t<__half>(p, stream);
