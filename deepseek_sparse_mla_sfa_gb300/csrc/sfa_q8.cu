@@ -52,16 +52,12 @@ namespace {
 
 using namespace ptx;
 
-#ifndef CNT
-#define CNT 96
-#define CST 3
-#define CPW 6
-#endif
-constexpr int kNt = CNT;              // selected rows per tile: N of QK^T, K of P.V
-constexpr int kStages = CST;
+constexpr int kNt = 96;              // selected rows per tile: N of QK^T, K of P.V
+constexpr int kStages = 3;
 constexpr int kThreads = 640;
 constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
-constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = CPW, kFixWarp = 16, kFixWarps = 4;
+constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 4, kRowWarp = 14,
+              kFixWarp = 16, kFixWarps = 4;
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPeak = 4.0f;        // log2 of P at the maximum a reference is taken from
@@ -72,27 +68,25 @@ constexpr int kBlk = kNt * 128;                       // 128 latent columns of a
 constexpr int kStageBytes = 4 * kBlk + kNt * 64;      // + 64 rope columns, SW64
 constexpr int kOffP = kStages * kStageBytes;
 constexpr int kPBytes = kGroupHeads * 128;            // P^T [heads x 96 rows] e4m3, K-major SW128 rows
-constexpr int kPLo = kNt == 64 ? 64 : kPBytes;        // lo follows hi in the row where both fit, else in a tile of its own
-constexpr int kPBuf = kNt == 64 ? kPBytes : 2 * kPBytes;
-constexpr int kOffList = kOffP + 2 * kPBuf;           // two buffers
-constexpr int kListCap = 4608 / kNt * kNt;                    // resolved rows kept at once (whole tiles)
+constexpr int kOffList = kOffP + 4 * kPBytes;         // two buffers of hi and lo
+constexpr int kListCap = 64 * kNt;                    // resolved rows kept at once (whole tiles)
 constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and two rows: scales, then their log2
 constexpr int kOffInv = kOffScale + kStages * kNt * 8;  // 1 / scale
-constexpr int kOffRaw = kOffInv + kStages * kNt * 4;    // the scales as they land
-constexpr int kOffMisc = kOffRaw + kStages * kNt * 4;
+constexpr int kOffMisc = kOffInv + kStages * kNt * 4;
 constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscScale = 1024, kMiscC = 1280, kMiscFlags = 1536, kMiscTmem = 1540,
-              kMiscMoved = 1544, kMiscCount = 1560, kMiscBytes = 1600;
+              kMiscMoved = 1544, kMiscCount = 1560, kMiscSeg = 1600, kMiscBytes = 1616;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
-constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarQReady = kBarKvEmpty + kStages,
+constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarRows = kBarKvEmpty + kStages,
+              kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQReady = kBarSegFull + 1,
               kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarWReady = kBarSFree + 2, kBarPReady = kBarWReady + 2,
               kBarPFree = kBarPReady + 2, kBarPvFinal = kBarPFree + 2, kBarMmaFin = kBarPvFinal + 1,
               kBarMmaFin2 = kBarMmaFin + 1, kBarNever = kBarMmaFin2 + 1, kNumBars = kBarNever + 1;
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 1024;
-constexpr bool kRowsCheck = kNt % (4 * kProducerWarps) == 0 && (kNt / kProducerWarps) % 8 == 0;
+static_assert(kNt % (4 * kProducerWarps) == 0, "whole row groups a producer");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kBlk % 1024 == 0 && kStageBytes % 1024 == 0 && kOffP % 1024 == 0, "operands: 1024-byte alignment");
 static_assert(kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
-static_assert(kRowsCheck && 2048 * kGroupHeads <= kStages * kStageBytes, "the output and the cluster merge fit in the stages");
+static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the output and the cluster merge fit in the stages");
 // q's e4m3 rows on their way to TMEM, in stages 1 and 2: 128 rows (64 hi, 64 lo) of 576 bytes
 constexpr int kQPitch = 592;   // an odd number of 16-byte words: rows start in different banks
 static_assert(128 * kQPitch <= (kStages - 1) * kStageBytes, "q fits in stages 1 and 2");
@@ -192,18 +186,6 @@ __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
   return *reinterpret_cast<__half2*>(&r);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int n>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
-}
-
 __device__ __forceinline__ void bulk_store_s2g(void* dst, uint32_t src, uint32_t bytes) {
   asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
                : "memory");
@@ -278,7 +260,8 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
 // NH: padded heads of a unit (32 or 64), the N of P.V
 template <int NH, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 1)
-    decode_q8_kernel(const __grid_constant__ CUtensorMap tmap_rows, const __grid_constant__ Q8Params kp) {
+    decode_q8_kernel(const __grid_constant__ CUtensorMap tmap_lat, const __grid_constant__ CUtensorMap tmap_rope,
+                     const __grid_constant__ Q8Params kp) {
   static_assert(NH == 32 || NH == 64, "padded head count");
   constexpr int HB = NH / 16;             // blocks of 16 heads: TMEM lanes 32x.. hold block x < HB
   constexpr int kSBufs = NH == 64 ? 1 : 2;
@@ -297,6 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* qc_s = reinterpret_cast<float*>(misc + kMiscC);                 // [64] score scale, NaN for a bad head
   volatile int* abort_s = reinterpret_cast<volatile int*>(misc + kMiscFlags);
   uint32_t* tmem_base_s = reinterpret_cast<uint32_t*>(misc + kMiscTmem);
+  int* seg_s = reinterpret_cast<int*>(misc + kMiscSeg);                  // where the next list segment starts: entry, ordinal
   int* wcount_s = reinterpret_cast<int*>(misc + kMiscCount);             // [kListWarps + 1]: counts, total
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -325,9 +309,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= kSoftWarps && warp < kFixWarp) load8(idx, c_begin, c_end, lane, pos_r);
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(&bars[kBarKvFull + s], 2 * kProducerWarps);   // each: its gathers issued, its copies landed
+      mbar_init(&bars[kBarKvFull + s], kProducerWarps);
+      mbar_init(&bars[kBarRows + s], 1);
       mbar_init(&bars[kBarKvEmpty + s], 1);
     }
+    mbar_init(&bars[kBarSegFree], kProducerWarps);
+    mbar_init(&bars[kBarSegFull], 1);
     mbar_init(&bars[kBarQReady], kSoftWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarSFull + x], 1);
@@ -348,7 +335,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(tmem_base_s, kTmemCols);
     tmem_relinquish();
   }
-  if (warp == kProducerWarp && lane == 0) prefetch_tmap(&tmap_rows);
+  if (warp == kProducerWarp && lane == 0) {
+    prefetch_tmap(&tmap_lat);
+    prefetch_tmap(&tmap_rope);
+  }
   const int seq_len = p.seq_lens[b];
   const ShardSel sel = shard_sel(seq_len, seq_len - (p.Q - 1 - qi), r, p.n_splits, p.interleave);
   tc_fence_before();
@@ -378,17 +368,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       total += c;
     }
 #pragma unroll 1
-    for (int j0 = c_begin; j0 < c_end && off < kListCap; j0 += 256) {
+    for (int j0 = c_begin; j0 < c_end && off <= kListCap; j0 += 256) {
       if (chunk > 256) {
         load8(idx, j0, c_end, lane, pos_r);
         resolve8<kInterleaved>(kp, pos_r, sel, bt_row, false, row_r);
       }
+      const int before = off;
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
         const int o = off + __popc(mask & lanemask_lt());
         if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
         off += __popc(mask);
+      }
+      if (lane == 0 && before <= kListCap && off > kListCap) {   // (one round at most)
+        seg_s[0] = j0;
+        seg_s[1] = before;
       }
     }
     // the last tile's missing rows: an index past the cache, which the gathers read as zeros
@@ -513,9 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       char* const p_row = smem + kOffP + head * 128 + 2 * (lane & 3);
       for (int i = 0; i < n_local; ++i) {
         const int bb = i & 1, sb = kSBufs == 2 ? bb : 0, st = i % kStages;
-        // (the tile is complete, QK^T waited for it: its wait orders the reads of the rows' scales)
         if (*abort_s || !wait_warp(&bars[kBarSFull + sb], (kSBufs == 2 ? i >> 1 : i) & 1) ||
-            !wait_warp(&bars[kBarKvFull + st], (i / kStages) & 1)) {
+            !wait_warp(&bars[kBarRows + st], (i / kStages) & 1)) {
           fail();
           break;
         }
@@ -574,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P = 2^(x - ref) as hi + lo; p = P / scale into the sum
         const uint64_t nref = pack2(-ref, -ref);
         const float2* iv = reinterpret_cast<const float2*>(inv_s + st * kNt) + (lane & 3);
-        char* const row = p_row + bb * kPBuf;
+        char* const row = p_row + 2 * bb * kPBytes;
 #pragma unroll
         for (int j = 0; j < kNt / 8; ++j) {
           const float2 f = unpack2(add2(x[j], nref));
@@ -586,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t hi = e4m3x2_h(w);
           const int at = (((j >> 1) ^ (head & 7)) << 4) + 8 * (j & 1);
           *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)hi;
-          *reinterpret_cast<uint16_t*>(row + (kNt == 64 ? at ^ kPLo : at + kPLo)) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
+          *reinterpret_cast<uint16_t*>(row + at + kPBytes) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -641,112 +635,124 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= kProducerWarp && warp < kProducerWarp + kProducerWarps) {
     // =================== gathers ===================================================
-    // Warp pw takes the tile's row groups pw, pw + 2, ... (4 rows each): 48 gather4 for the
-    // latent columns, and the rope words of its 48 rows in 6 rounds of 32 lanes.  Up to three
-    // tiles are in flight; a tile's copies are signalled once they are visible to the tensor
-    // cores' proxy.
+    // Warp pw takes the tile's row groups pw, pw + 4, ... (4 rows each), five gather4 a group,
+    // all from one lane: the lanes of a warp would issue theirs one after the other, each with
+    // its operands moved to uniform registers first.  The warp waits for nothing but stages.
     const int pw = warp - kProducerWarp;
-    constexpr int kRowsOf = kNt / kProducerWarps;   // 48
-    const char* kv = reinterpret_cast<const char*>(p.kv);
-    auto tile_row = [&](int q) { return 4 * (pw + kProducerWarps * (q >> 2)) + (q & 3); };
-    int issued = 0, done = 0, seg = 0;
+    constexpr int kGroupsOf = kNt / 4 / kProducerWarps;
+    int seg = 0, n = 0;
     bool ok = true;
-    float* raw_s = reinterpret_cast<float*>(smem + kOffRaw);
-    auto finish = [&]() {                            // the oldest tile in flight
-      switch (issued - done) {
-        case 1: cp_wait<0>(); break;
-        case 2: cp_wait<1>(); break;
-        case 3: cp_wait<2>(); break;
-        case 4: cp_wait<3>(); break;
-        default: cp_wait<4>(); break;
+    for (; n < n_local && !*abort_s; ++n) {
+      const int at = n % kStages;
+      // stages 1 and 2 hold q until it is in TMEM; later tiles wait for P.V of the stage's last
+      if (n > 0 && !(ok = n >= kStages ? wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1)
+                                       : wait_warp(&bars[kBarQReady], 0)))
+        break;
+      const int first = kNt * ((int)crank + (int)G * n);
+      if (first >= (seg + 1) * kListCap) {      // more valid entries than the list holds
+        if (lane == 0) mbar_arrive(&bars[kBarSegFree]);
+        if (!(ok = wait_warp(&bars[kBarSegFull], seg & 1))) break;
+        ++seg;
       }
-      const int at = done % kStages;
-      for (int q = lane; q < kRowsOf; q += 32) {
-        // a row that does not exist has weight 0 (the copies leave its scale 0)
-        const int y = at * kNt + tile_row(q);
-        const float x = raw_s[y];
-        float* rp = reinterpret_cast<float*>(rows_s) + 4 * (y >> 1) + (y & 1);
-        rp[0] = x;
-        rp[2] = __log2f(x);
-        inv_s[y] = x > 0.f ? __frcp_rn(x) : 0.f;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarKvFull + at]);
-      ++done;
-    };
-    while (done < n_local && !*abort_s) {
-      bool can = issued < n_local && issued - done < kStages;
-      if (can && issued > 0) {
-        // stages 1 and 2 hold q until it is in TMEM; later tiles wait for P.V of the stage's last
-        uint64_t* bar = issued >= kStages ? &bars[kBarKvEmpty + issued % kStages] : &bars[kBarQReady];
-        const uint32_t par = issued >= kStages ? ((issued / kStages) - 1) & 1 : 0;
-        can = __all_sync(0xffffffffu, mbar_test(bar, par));
-        if (!can && issued == done) {
-          if (!(ok = wait_warp(bar, par))) break;
-          can = true;
-        }
-      }
-      if (!can) {
-        finish();
-        continue;
-      }
-      const int first = kNt * ((int)crank + (int)G * issued);
-      if (first >= (seg + 1) * kListCap) {
-        // rare (more valid entries than the list holds): this warp re-resolves the
-        // entries of its own rows for the segment that holds this tile
-        seg = first / kListCap;
-        int ord = 0;
-        for (int j0 = 0; j0 < p.top_k; j0 += 32) {
-          const int j = j0 + lane;
-          const int row = j < p.top_k ? resolve_row<kInterleaved>(p, bt_row, __ldg(idx + j), sel, false) : -1;
-          const unsigned mask = __ballot_sync(0xffffffffu, row >= 0);
-          const int o = ord + __popc(mask & lanemask_lt()) - seg * kListCap;
-          if (row >= 0 && o >= 0 && o < kListCap && ((o % kNt) / 4) % kProducerWarps == pw) list_s[o] = row;
-          ord += __popc(mask);
-        }
-        for (int o = total - seg * kListCap + lane; o < min(n_tiles * kNt - seg * kListCap, kListCap); o += 32)
-          if (((o % kNt) / 4) % kProducerWarps == pw) list_s[o] = kp.num_rows;
-        __syncwarp();
-      }
-      const int* rows = list_s + (first - seg * kListCap);
-      const int at = issued % kStages;
+      const int* rows = list_s + (first - seg * kListCap) + 4 * pw;
       const uint32_t st = smem_u32(smem + at * kStageBytes);
-      if (lane == 0) mbar_arrive_expect_tx(&bars[kBarKvFull + at], kRowsOf * kDV);
-      __syncwarp();
+      uint64_t* full = &bars[kBarKvFull + at];
       if (elect_one()) {
+        mbar_arrive_expect_tx(full, kGroupsOf * 4 * kDQK);
 #pragma unroll
-        for (int g = 0; g < kRowsOf / 4; ++g) {
+        for (int g = 0; g < kGroupsOf; ++g) {
           const int y = 4 * (pw + kProducerWarps * g);
-          const int4 rr = *reinterpret_cast<const int4*>(rows + y);
+          const int4 rr = *reinterpret_cast<const int4*>(rows + 4 * kProducerWarps * g);
 #pragma unroll
           for (int m = 0; m < 4; ++m)
-            tma_gather4(st + m * kBlk + y * 128, &tmap_rows, 128 * m, rr.x, rr.y, rr.z, rr.w, &bars[kBarKvFull + at]);
+            tma_gather4(st + m * kBlk + y * 128, &tmap_lat, 128 * m, rr.x, rr.y, rr.z, rr.w, full);
+          tma_gather4(st + 4 * kBlk + y * 64, &tmap_rope, kDV, rr.x, rr.y, rr.z, rr.w, full);
         }
       }
       __syncwarp();
-#pragma unroll
-      for (int u = 0; u < kRowsOf * 4 / 32; ++u) {
-        const int y = tile_row(8 * u + (lane >> 2)), w = lane & 3, row = rows[y];
-        const bool in = row < kp.num_rows;
-        cp_async16(st + 4 * kBlk + y * 64 + ((w ^ ((y >> 1) & 3)) << 4), kv + (size_t)(in ? row : 0) * kDQK + kDV + 16 * w,
-                   in ? 16 : 0);
-      }
-      for (int q = lane; q < kRowsOf; q += 32) {
-        const int y = tile_row(q), row = rows[y];
-        const bool in = row < kp.num_rows;
-        cp_async4(smem_u32(raw_s + at * kNt + y), kp.qp.scales + (in ? div_by(row, kp.gr_mul, kp.gr_shift) : 0),
-                  in ? 4 : 0);
-      }
-      cp_commit();
-      ++issued;
     }
     if (!ok) fail();
-    // no copy of this CTA may still be landing in shared memory at exit
-    while (done < issued) finish();
-    for (int k = issued > kStages ? issued - kStages : 0; k < issued; ++k)
+    // no gather of this CTA may still be landing in shared memory at exit
+    for (int k = n > kStages ? n - kStages : 0; k < n; ++k)
       if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit)))
         report_status(p.status, kStatusTimeout);
+  } else if (warp == kRowWarp) {
+    // =================== the rows' scales, and the rest of a long list ==============
+    // Scales are single words anywhere in memory: those of the next four tiles are in flight
+    // while four are published.  A segment of the list begins with a group of four (64 tiles,
+    // dealt to at most 8 CTAs).
+    constexpr int kAhead = 4, kPer = kNt / 32;
+    static_assert(kListCap / kNt % (8 * kAhead) == 0, "segments begin with a group");
+    float cur[kAhead][kPer], nxt[kAhead][kPer];
+    int seg = 0, j = seg_s[0], ord = seg_s[1];   // the next segment's first round, entries before it
+    bool ok = true;
+    auto load4 = [&](int n0, float (&v)[kAhead][kPer]) {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        const int* rows = list_s + kNt * ((int)crank + (int)G * (n0 + d)) - seg * kListCap + lane;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          const int row = n0 + d < n_local ? rows[32 * u] : kp.num_rows;
+          v[d][u] = row < kp.num_rows ? __ldg(kp.qp.scales + div_by(row, kp.gr_mul, kp.gr_shift)) : 0.f;
+        }
+      }
+    };
+    load4(0, cur);
+#pragma unroll 1
+    for (int n0 = 0; n0 < n_local && ok && !*abort_s; n0 += kAhead) {
+      const int first = kNt * ((int)crank + (int)G * (n0 + kAhead));
+      const bool more = n0 + kAhead < n_local, turn = more && first >= (seg + 1) * kListCap;
+      if (more && !turn) load4(n0 + kAhead, nxt);
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        const int n = n0 + d, at = n % kStages;
+        if (n >= n_local || !ok) break;
+        if (n >= kStages && !(ok = wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1))) break;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          // (a row that does not exist has scale 0: weight 0)
+          const int y = at * kNt + lane + 32 * u;
+          float* rp = reinterpret_cast<float*>(rows_s) + 4 * (y >> 1) + (y & 1);
+          rp[0] = cur[d][u];
+          rp[2] = __log2f(cur[d][u]);
+          inv_s[y] = cur[d][u] > 0.f ? __frcp_rn(cur[d][u]) : 0.f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarRows + at]);
+      }
+      if (turn && ok) {
+        // once the producers have issued the segment's last tile, the next segment takes its
+        // place (they only wait for tiles that are published by now)
+        if (!(ok = wait_warp(&bars[kBarSegFree], seg & 1))) break;
+        ++seg;
+        const int base = seg * kListCap;
+#pragma unroll 1
+        while (j < p.top_k) {
+          int pos[8], row[8], to = ord;
+          load8(idx, j, p.top_k, lane, pos);
+          resolve8<kInterleaved>(kp, pos, sel, bt_row, false, row);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const unsigned mask = __ballot_sync(0xffffffffu, row[k] >= 0);
+            const int o = to + __popc(mask & lanemask_lt()) - base;
+            if (row[k] >= 0 && o >= 0 && o < kListCap) list_s[o] = row[k];
+            to += __popc(mask);
+          }
+          if (to > base + kListCap) break;       // the round goes on in the segment after
+          ord = to;
+          j += 256;
+        }
+        for (int o = total - base + lane; o < min(n_tiles * kNt - base, kListCap); o += 32) list_s[o] = kp.num_rows;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarSegFull]);
+        load4(n0 + kAhead, nxt);
+      }
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d)
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) cur[d][u] = nxt[d][u];
+    }
+    if (!ok) fail();
   } else if (warp == kQkWarp || warp == kPvWarp) {
     // =================== tcgen05 MMA issue: QK^T (warp 8) and P.V (warp 9) ========
     // (the whole warp walks the tiles and waits; one lane issues)
@@ -794,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc_fence_after();
           if (elect_one()) {
             const uint32_t a0 = desc_lo(st0 + s * kStageBytes, kBlk);
-            const uint32_t b0 = desc_lo(st0 + kOffP + bb * kPBuf, 16);
+            const uint32_t b0 = desc_lo(st0 + kOffP + 2 * bb * kPBytes, 16);
 #pragma unroll
             for (int k = 0; k < kNt / 32; ++k)
 #pragma unroll
@@ -802,7 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int m = 0; m < 4; ++m)
                   mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128)>(
-                      tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPLo + 32 * k) >> 4), id,
+                      tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPBytes + 32 * k) >> 4), id,
                       (k > 0 || part > 0) ? 1u : (n > 0 ? 1u : 0u));
             mma_commit(&bars[kBarKvEmpty + s]);
             mma_commit(&bars[kBarPFree + bb]);
@@ -948,8 +954,8 @@ constexpr auto q8_kernel() {
   return decode_q8_kernel<NH, kIL>;
 }
 
-// the cache as [num_rows, 576] bytes; one box = 128 columns of one row (gathered four at a time)
-bool make_rows_map(CUtensorMap* m, const void* kv8, int num_rows) {
+// the cache as [num_rows, 576] bytes; one box = `cols` columns of one row (gathered four at a time)
+bool make_rows_map(CUtensorMap* m, const void* kv8, int num_rows, int cols, CUtensorMapSwizzle swizzle) {
   typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -966,9 +972,9 @@ bool make_rows_map(CUtensorMap* m, const void* kv8, int num_rows) {
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)kDQK, (cuuint64_t)num_rows};
   const cuuint64_t strides[1] = {(cuuint64_t)kDQK};
-  const cuuint32_t box[2] = {128, 1}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)cols, 1}, es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(kv8), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1007,11 +1013,13 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
   const bool il = p.interleave > 0 && p.n_splits > 1;
   auto kernel = kp.group_heads <= 32 ? (il ? q8_kernel<32, true>() : q8_kernel<32, false>())
                                      : (il ? q8_kernel<64, true>() : q8_kernel<64, false>());
-  CUtensorMap rows;
+  CUtensorMap lat, rope;
   kp.num_rows = p.num_blocks * p.block_size;
   divisor(p.block_size, kp.bs_mul, kp.bs_shift);
   divisor(qp.group, kp.gr_mul, kp.gr_shift);
-  if (!make_rows_map(&rows, p.kv, kp.num_rows)) return cudaErrorInvalidValue;
+  if (!make_rows_map(&lat, p.kv, kp.num_rows, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_rows_map(&rope, p.kv, kp.num_rows, 64, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg;
   memset(&cfg, 0, sizeof cfg);
   cfg.gridDim = dim3((unsigned)(units * G), 1, 1);
@@ -1025,7 +1033,7 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kernel, rows, kp);
+  e = cudaLaunchKernelEx(&cfg, kernel, lat, rope, kp);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
