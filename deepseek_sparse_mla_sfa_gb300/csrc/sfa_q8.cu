@@ -78,7 +78,7 @@ constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscScale = 1024, kMiscC = 1280, k
 constexpr int kOffBar = kOffMisc + kMiscBytes;
 constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarRows = kBarKvEmpty + kStages,
               kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQReady = kBarSegFull + 1,
-              kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarWReady = kBarSFree + 2, kBarPReady = kBarWReady + 2,
+              kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarAReady = kBarSFree + 2, kBarPReady = kBarAReady + 2,
               kBarPFree = kBarPReady + 2, kBarPvFinal = kBarPFree + 2, kBarMmaFin = kBarPvFinal + 1,
               kBarMmaFin2 = kBarMmaFin + 1, kBarNever = kBarMmaFin2 + 1, kNumBars = kBarNever + 1;
 constexpr int kSmemBytes = kOffBar + kNumBars * 8 + 1024;
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarSFull + x], 1);
       mbar_init(&bars[kBarSFree + x], 2 * HB);      // the softmax warps that hold heads
-      mbar_init(&bars[kBarWReady + x], 2 * HB);     // their weights are written
-      mbar_init(&bars[kBarPReady + x], kFixWarps);  // and O follows their references
+      mbar_init(&bars[kBarAReady + x], 2 * HB);     // their references are known
+      mbar_init(&bars[kBarPReady + x], 2 * HB + kFixWarps);   // their weights are written, O follows the references
       mbar_init(&bars[kBarPFree + x], 1);
     }
     mbar_init(&bars[kBarPvFinal], 1);
@@ -564,6 +564,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if ((lane & 3) == 0) alpha_s[64 * bb + head] = alpha;
         }
         if (lane == 0) moved_s[8 * bb + 2 * quad + half] = moved;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars[kBarAReady + bb]);
         ref = ref_new;
         // P = 2^(x - ref) as hi + lo; p = P / scale into the sum
         const uint64_t nref = pack2(-ref, -ref);
@@ -584,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarWReady + bb]);
+        if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
       }
       const float2 f = unpack2(l2);
       l_sum = f.x + f.y;
@@ -595,11 +597,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kFixWarp) {
     // =================== O follows the references (warps 16-19) ====================
     // Where a head's reference moved with tile i, its column of O^T is scaled between P.V of
-    // tiles i-1 and i; the softmax warps do not wait for that.
+    // tiles i-1 and i, while the softmax warps write the weights.
     const uint32_t my_lanes = tmem + ((uint32_t)((warp - kFixWarp) * 32) << 16);
     for (int i = 0; i < n_local && !*abort_s; ++i) {
       const int bb = i & 1;
-      if (!wait_warp(&bars[kBarWReady + bb], (i >> 1) & 1)) {
+      if (!wait_warp(&bars[kBarAReady + bb], (i >> 1) & 1)) {
         fail();
         break;
       }
