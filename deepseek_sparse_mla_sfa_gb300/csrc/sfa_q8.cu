@@ -55,7 +55,7 @@ using namespace ptx;
 constexpr int kNt = 96;              // selected rows per tile: N of QK^T, K of P.V
 constexpr int kStages = 3;
 constexpr int kThreads = 640;
-constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
+constexpr int kSoftWarps = 8, kQWarps = 12;
 constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 4, kRowWarp = 14,
               kFixWarp = 16, kFixWarps = 4;
 constexpr int kGroupHeads = 64;      // heads of a unit
@@ -89,7 +89,9 @@ static_assert(kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
 static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the output and the cluster merge fit in the stages");
 // q's e4m3 rows on their way to TMEM, in stages 1 and 2: 128 rows (64 hi, 64 lo) of 576 bytes
 constexpr int kQPitch = 592;   // an odd number of 16-byte words: rows start in different banks
-static_assert(128 * kQPitch <= (kStages - 1) * kStageBytes, "q fits in stages 1 and 2");
+constexpr int kOffTmp = kStageBytes + 128 * kQPitch;   // behind it: the resolved list before its compaction
+constexpr int kTmpCap = (kStages * kStageBytes - kOffTmp) / 4;
+static_assert(kTmpCap >= 8192, "q and a list of 8192 entries fit in stages 1 and 2");
 static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscBytes, "misc");
 
 constexpr long long kDrainLimit = 1LL << 40;
@@ -102,6 +104,7 @@ struct Q8Params {
   int group_heads;   // heads of a group (the last may have fewer)
   int num_rows;      // rows of the cache: the index that the gathers read as zeros
   uint32_t bs_mul, bs_shift, gr_mul, gr_shift;   // division by block_size and by group
+  uint32_t T_mul, T_shift, Q_mul, Q_shift;       // by the tokens and by the tokens of a sequence
 };
 
 // n / d for 0 <= n < 2^31 as (n * mul) >> shift, mul = ceil(2^shift / d), shift = 31 + ceil(log2 d)
@@ -169,12 +172,7 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
                : "memory");
 }
 
-// two e4m3 codes of a (low byte) and b
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
-  return r;
-}
+// two e4m3 codes, v.x's in the low byte, and back
 __device__ __forceinline__ uint32_t e4m3x2_h(__half2 v) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<uint32_t*>(&v)));
@@ -287,26 +285,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t crank = cluster_ctarank();
   uint32_t G;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(G));
-  const int unit = blockIdx.x / G;
+  const int g_shift = 31 - __clz((int)G);
+  const int unit = (int)(blockIdx.x >> g_shift);
   const int T = p.B * p.Q;
-  // the head groups of a token go out next to each other (they read the same rows), the last
-  // shards first (the heaviest of a sparse selection)
-  const int hg = unit % kp.groups, tr = unit / kp.groups;
-  const int t = tr % T, r = p.n_splits - 1 - tr / T;
+  // the head groups (1 or 2) of a token go out next to each other (they read the same rows),
+  // the last shards first (the heaviest of a sparse selection)
+  const int hg = unit & (kp.groups - 1), tr = unit >> (kp.groups - 1);
+  const int ts = div_by(tr, kp.T_mul, kp.T_shift), t = tr - ts * T, r = p.n_splits - 1 - ts;
   const int h0 = hg * kp.group_heads, nh = min(kp.group_heads, p.h - h0);
-  const int b = t / p.Q, qi = t % p.Q;
+  const int b = div_by(t, kp.Q_mul, kp.Q_shift), qi = t - b * p.Q;
   const int bt_row = p.bt_per_token ? t : b;
   const int32_t* idx = p.topk_idx + (size_t)t * p.top_k;
   const uint4* qsrc = reinterpret_cast<const uint4*>(p.q + ((size_t)t * p.h + h0) * kDQK);
   const long long wl = p.wait_limit;
 
   // ---- set-up ----------------------------------------------------------------------
-  // Warps 0-7 bring q into TMEM; meanwhile warps 8-15 resolve the list and start the gathers.
-  for (int x = threadIdx.x; x < nh * (kDQK * 2 / 128); x += kThreads) prefetch_l2(qsrc + 8 * x);
+  // Warps 0-7 and 16-19 bring q into TMEM; meanwhile warps 8-15 resolve the list and start the
+  // gathers.  The first loads of both go out before anything waits.
+  const int wq = warp < kSoftWarps ? warp : warp - kListWarps;    // of the kQWarps that bring q
+  uint4 q1[3], q2[3];
+  auto load_head = [&](int hd, uint4 (&x)[3]) {
+#pragma unroll
+    for (int k = 0; k < 3; ++k)
+      x[k] = hd < nh && lane + 32 * k < 72 ? __ldg(qsrc + (size_t)hd * 72 + lane + 32 * k) : make_uint4(0, 0, 0, 0);
+  };
   const int chunk = ((p.top_k + kListWarps * 32 - 1) / (kListWarps * 32)) * 32;
   const int c_begin = min((warp - kSoftWarps) * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
   int pos_r[8];
-  if (warp >= kSoftWarps && warp < kFixWarp) load8(idx, c_begin, c_end, lane, pos_r);
+  if (warp >= kSoftWarps && warp < kFixWarp) {
+    load8(idx, c_begin, c_end, lane, pos_r);
+  } else {
+    load_head(wq, q1);
+    load_head(wq + kQWarps, q2);
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars[kBarKvFull + s], kProducerWarps);
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(&bars[kBarSegFree], kProducerWarps);
     mbar_init(&bars[kBarSegFull], 1);
-    mbar_init(&bars[kBarQReady], kSoftWarps);
+    mbar_init(&bars[kBarQReady], kQWarps);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&bars[kBarSFull + x], 1);
       mbar_init(&bars[kBarSFree + x], 2 * HB);      // the softmax warps that hold heads
@@ -347,17 +358,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_base_s;
 
   // ---- index resolution (warps 8-15): count per warp chunk, then ordered compaction ----
-  // (rounds of 8 entries a lane; a list of one round stays in registers, a longer one is
-  // resolved again, from L1, for the compaction)
+  // (rounds of 8 entries a lane; one round stays in registers, more go to a temporary list a
+  // warp, in the part of stage 2 that q leaves free)
   int total = 0;
   if (warp >= kSoftWarps && warp < kFixWarp) {
     int row_r[8], cnt = 0;
+    const bool keep = kListWarps * chunk <= kTmpCap;      // longer lists are resolved a second time
+    int* tmp = reinterpret_cast<int*>(smem + kOffTmp) + (warp - kSoftWarps) * chunk;
+    auto compact = [&](int* to, int at, int cap) {        // this round's rows from to[at] on; returns the next place
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
+        const int o = at + __popc(mask & lanemask_lt());
+        if (row_r[k] >= 0 && o < cap) to[o] = row_r[k];
+        at += __popc(mask);
+      }
+      return at;
+    };
 #pragma unroll 1
     for (int j0 = c_begin; j0 < c_end; j0 += 256) {
-      if (j0 > c_begin) load8(idx, j0, c_end, lane, pos_r);
-      cnt += resolve8<kInterleaved>(kp, pos_r, sel, bt_row, crank == 0 && hg == 0, row_r);
+      int pos[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) pos[k] = pos_r[k];
+      load8(idx, j0 + 256, c_end, lane, pos_r);           // the next round's entries are in flight
+      const int mine = resolve8<kInterleaved>(kp, pos, sel, bt_row, crank == 0 && hg == 0, row_r);
+      if (keep && chunk > 256) cnt = compact(tmp, cnt, kTmpCap); else cnt += __reduce_add_sync(0xffffffffu, mine);
     }
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
     if (lane == 0) wcount_s[warp - kSoftWarps] = cnt;
     named_barrier(4, 32 * kListWarps);
     int off = 0;
@@ -367,23 +393,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp - kSoftWarps) off += c;
       total += c;
     }
+    if (chunk <= 256) {
+      if (c_begin < c_end) compact(list_s, off, kListCap);
+    } else if (keep && total <= kListCap) {
+      for (int o = lane; o < cnt; o += 32) list_s[off + o] = tmp[o];
+    } else {
 #pragma unroll 1
-    for (int j0 = c_begin; j0 < c_end && off <= kListCap; j0 += 256) {
-      if (chunk > 256) {
-        load8(idx, j0, c_end, lane, pos_r);
-        resolve8<kInterleaved>(kp, pos_r, sel, bt_row, false, row_r);
-      }
-      const int before = off;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const unsigned mask = __ballot_sync(0xffffffffu, row_r[k] >= 0);
-        const int o = off + __popc(mask & lanemask_lt());
-        if (row_r[k] >= 0 && o < kListCap) list_s[o] = row_r[k];
-        off += __popc(mask);
-      }
-      if (lane == 0 && before <= kListCap && off > kListCap) {   // (one round at most)
-        seg_s[0] = j0;
-        seg_s[1] = before;
+      for (int j0 = c_begin; j0 < c_end && off <= kListCap; j0 += 256) {
+        int pos[8];
+        load8(idx, j0, c_end, lane, pos);
+        resolve8<kInterleaved>(kp, pos, sel, bt_row, false, row_r);
+        const int before = off;
+        off = compact(list_s, off, kListCap);
+        if (lane == 0 && before <= kListCap && off > kListCap) {   // (one round at most)
+          seg_s[0] = j0;
+          seg_s[1] = before;
+        }
       }
     }
     // the last tile's missing rows: an index past the cache, which the gathers read as zeros
@@ -397,13 +422,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   int n_tiles = 0, n_local = 0;
   auto count_tiles = [&]() {
     n_tiles = (total + kNt - 1) / kNt;
-    n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) / (int)G : 0;
+    n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) >> g_shift : 0;
   };
-  if (warp >= kFixWarp) {
+  if (warp < kSoftWarps || warp >= kFixWarp) {
+    // ---- q as hi and lo e4m3 rows: coalesced loads (a head a warp, two in flight), then
+    // through shared memory (stages 1 and 2, which the gathers leave alone until q is ready)
+    // to the TMEM lanes
+    char* qst = smem + kStageBytes;
+#pragma unroll 1
+    for (int hd = wq; hd < NH; hd += kQWarps) {
+      const uint4 x[3] = {q1[0], q1[1], q1[2]};
+#pragma unroll
+      for (int k = 0; k < 3; ++k) q1[k] = q2[k];
+      load_head(hd + 2 * kQWarps, q2);
+      uint32_t am = 0;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+      }
+      am = __reduce_max_sync(0xffffffffu, am);
+      const bool bad = am >= 0x7f80u;       // an infinity or NaN: the head's result is NaN
+      // 2^ke: the least power of two with amax / 2^ke <= 448
+      int ke = (int)(am >> 7) - 135 + ((am & 0x7f) > 0x60 ? 1 : 0);
+      ke = am < 0x80u || bad ? 0 : max(ke, -100);
+      const float down = bad ? 0.f : (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
+      if (lane == 0)
+        qc_s[hd] = bad ? __int_as_float(0x7fc00000)
+                       : fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
+      char* at = qst + hd * kQPitch + 8 * lane;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // a scaled value has 8 bits below 2^9: f16 holds it (to 2^-24, below lo's 2^-13)
+          const float a = __uint_as_float(w[i] << 16), c = __uint_as_float(w[i] & 0xffff0000u);
+          const __half2 v = __floats2half2_rn(bad ? 0.f : a * down, bad ? 0.f : c * down);
+          hi[i] = e4m3x2_h(v);
+          lo[i] = e4m3x2_h(__hmul2(__hsub2(v, half2_of(hi[i])), __floats2half2_rn(16.f, 16.f)));
+        }
+        if (lane + 32 * k < 72) {
+          *reinterpret_cast<uint2*>(at + 256 * k) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(at + 256 * k + 64 * kQPitch) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+        }
+      }
+    }
+    named_barrier(1, 32 * kQWarps);
+    const int quad = warp & 3;
+    const char* mine = qst + (16 * quad + (lane & 15) + (lane >= 16 ? 64 : 0)) * kQPitch;
+#pragma unroll 1
+    for (int c = wq >> 2; c < 9 && quad < HB; c += kQWarps / 4) {     // 64 columns of q are 16 columns of TMEM
+      uint32_t v[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + 64 * c + 16 * k);
+        v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
+      }
+      tmem_st16(tmem + ((uint32_t)(quad * 32) << 16) + kColQ + 16 * c, v);
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    fence_proxy_async_smem();               // the gathers write these stages next
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars[kBarQReady]);
     named_barrier(5, kThreads);
     total = wcount_s[kListWarps];
   }
-  if (warp >= kSoftWarps) count_tiles();
+  count_tiles();
 
   auto fail = [&](void) {
     report_status(p.status, kStatusTimeout);
@@ -420,87 +508,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int head = 16 * quad + 8 * half + (lane >> 2);
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
   float ref = -INFINITY, l_sum = 0.f;
-  bool bad_q = false;
   if (warp < kSoftWarps) {
     // =================== q into TMEM, softmax, O rescale (warps 0-7) ================
-    {
-      // q as hi and lo e4m3 rows: coalesced loads (a head a warp), then
-      // through shared memory (stages 1 and 2, which the gathers leave alone until q is
-      // ready) to the TMEM lanes
-      char* qst = smem + kStageBytes;
-      uint4 n1[3], n2[3];
-      auto load_head = [&](int hd, uint4 (&x)[3]) {
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-          x[k] = hd < nh && lane + 32 * k < 72 ? __ldg(qsrc + (size_t)hd * 72 + lane + 32 * k) : make_uint4(0, 0, 0, 0);
-      };
-      load_head(warp, n1);
-      load_head(warp + kSoftWarps, n2);
-#pragma unroll 1
-      for (int hd = warp; hd < NH; hd += kSoftWarps) {
-        const uint4 x[3] = {n1[0], n1[1], n1[2]};
-#pragma unroll
-        for (int k = 0; k < 3; ++k) n1[k] = n2[k];
-        load_head(hd + 2 * kSoftWarps, n2);
-        uint32_t am = 0;
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
-        }
-        am = __reduce_max_sync(0xffffffffu, am);
-        const bool bad = am >= 0x7f80u;     // an infinity or NaN: the head's result is NaN
-        // 2^ke: the least power of two with amax / 2^ke <= 448
-        int ke = (int)(am >> 7) - 135 + ((am & 0x7f) > 0x60 ? 1 : 0);
-        ke = am < 0x80u || bad ? 0 : max(ke, -100);
-        const float down = (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
-        if (lane == 0)
-          qc_s[hd] = bad ? __int_as_float(0x7fc00000)
-                         : fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-          uint32_t hi[4], lo[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float a = bad ? 0.f : __uint_as_float(w[i] << 16) * down;
-            const float c = bad ? 0.f : __uint_as_float(w[i] & 0xffff0000u) * down;
-            hi[i] = e4m3x2(a, c);
-            const float2 f = __half22float2(half2_of(hi[i]));
-            lo[i] = e4m3x2((a - f.x) * 16.f, (c - f.y) * 16.f);
-          }
-          if (lane + 32 * k < 72) {
-            char* at = qst + hd * kQPitch + 8 * (lane + 32 * k);
-            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-            *reinterpret_cast<uint2*>(at + 64 * kQPitch) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
-          }
-        }
-      }
-      named_barrier(1, kSoftThreads);
-      const char* mine = qst + (16 * quad + (lane & 15) + (lane >= 16 ? 64 : 0)) * kQPitch;
-#pragma unroll 1
-      for (int c = half; c < 9 && quad < HB; c += 2) {     // 64 columns of q are 16 columns of TMEM
-        uint32_t v[16];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint4 x = *reinterpret_cast<const uint4*>(mine + 64 * c + 16 * k);
-          v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
-        }
-        tmem_st16(lane_base + kColQ + 16 * c, v);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      fence_proxy_async_smem();               // the gathers write these stages next
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarQReady]);
-    }
-    named_barrier(5, kThreads);
-    total = wcount_s[kListWarps];
-    count_tiles();
     if (quad < HB) {
       float c_head = qc_s[head];
-      bad_q = c_head != c_head;
+      const bool bad_q = c_head != c_head;
       if (bad_q) c_head = 1e-30f;
       const uint64_t c2 = pack2(c_head, c_head), sixteenth = pack2(0.0625f, 0.0625f);
       uint64_t l2 = 0;                                        // two running sums
@@ -592,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       l_sum = f.x + f.y;
       l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 1);
       l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
-      if (bad_q) l_sum = __int_as_float(0x7fc00000);
+      if (bad_q && n_local > 0) l_sum = __int_as_float(0x7fc00000);
     }
   } else if (warp >= kFixWarp) {
     // =================== O follows the references (warps 16-19) ====================
@@ -831,124 +843,132 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---- merge of the cluster's partial results and the output ---------------------
-  // Every thread of every CTA of the cluster reaches both cluster barriers.
   __syncwarp();
-  bool have_o = false;
   if (warp < kSoftWarps) {
-    if (n_local > 0 && !*abort_s) {
-      have_o = wait_warp(&bars[kBarPvFinal], 0);
-      if (!have_o) fail();
+    if (n_local > 0 && !*abort_s && !wait_warp(&bars[kBarPvFinal], 0)) fail();
+    if (quad < HB && (lane & 3) == 0) {
+      ml_s[head] = make_float2(ref, l_sum);
+      if (G == 1) scale_s[head] = l_sum != 0.f ? 1.f / l_sum : 0.f;
     }
-    if (quad < HB && (lane & 3) == 0)
-      ml_s[head] = have_o ? make_float2(ref, l_sum) : make_float2(-INFINITY, 0.f);
   }
   // (a CTA alone needs no cluster barrier, here and below)
   tc_fence_before();
   if (G > 1) cluster_sync(); else __syncthreads();   // every CTA's (m, l) is published and its stages are idle
   tc_fence_after();
+  const bool good = !*abort_s, have_o = good && n_local > 0;
+  const size_t lse_at = ((size_t)r * T + t) * p.h + h0, out_at = lse_at * kDV;   // nh rows of 512, one after the other
+  const uint32_t my_lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+  if (G == 1) {
+    // O / l to [head][512] in the idle stages, as it goes to global memory; every warp takes
+    // (column block, 16 heads) pieces of its TMEM lanes
+    if (threadIdx.x < nh && good) {
+      const float2 ml = ml_s[threadIdx.x];
+      p.lse[lse_at + threadIdx.x] = ml.y != 0.f ? (ml.x + __log2f(ml.y)) * kLn2 : -INFINITY;
+    }
+#pragma unroll 1
+    for (int c = warp >> 2; c < 4 * HB; c += kThreads / 128) {
+      const int m = c / HB, hb = 16 * (c % HB);
+      uint32_t o[16];
+      if (have_o) tmem_ld16(my_lanes + kColO + 16 * c, o);
+      float f[16];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 sc = *reinterpret_cast<const float4*>(scale_s + hb + 4 * k);
+        f[4 * k] = sc.x; f[4 * k + 1] = sc.y; f[4 * k + 2] = sc.z; f[4 * k + 3] = sc.w;
+      }
+      if (have_o) tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) f[k] = have_o ? __uint_as_float(o[k]) * f[k] : 0.f;
+      const int col = hb * kDV + 128 * m + 32 * (warp & 3) + lane;
+      if (kp.qp.out_bf16) {
+        __nv_bfloat16* o_s = reinterpret_cast<__nv_bfloat16*>(smem) + col;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o_s[k * kDV] = __float2bfloat16_rn(f[k]);
+      } else {
+        float* o_s = reinterpret_cast<float*>(smem) + col;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o_s[k * kDV] = f[k];
+      }
+    }
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+    if (lane == 0 && good) {
+      const uint32_t row = kDV * (kp.qp.out_bf16 ? 2 : 4);
+      char* dst = reinterpret_cast<char*>(p.out) + out_at * (row / kDV);
+      for (int hd = warp; hd < nh; hd += kThreads / 32)
+        bulk_store_s2g(dst + (size_t)hd * row, smem_u32(smem) + hd * row, row);
+      bulk_commit_group();
+      bulk_wait_read<0>();
+    }
+    return;
+  }
+  // Every thread of every CTA of the cluster reaches both cluster barriers.
   if (threadIdx.x < NH) {
-    const int hh = threadIdx.x;
     // this head's largest reference M, sum L and this CTA's weight 2^(m - M) / L
-    float M = -INFINITY;
-    for (uint32_t c = 0; c < G; ++c) M = fmaxf(M, ld_cluster_f32(mapa(&ml_s[hh], c)));
-    float L = 0.f;
+    const int hd = threadIdx.x;
+    float M = -INFINITY, L = 0.f;
+    for (uint32_t c = 0; c < G; ++c) M = fmaxf(M, ld_cluster_f32(mapa(&ml_s[hd], c)));
     for (uint32_t c = 0; c < G; ++c) {
-      const uint32_t a = mapa(&ml_s[hh], c);
+      const uint32_t a = mapa(&ml_s[hd], c);
       const float lc = ld_cluster_f32(a + 4u);
       if (lc != 0.f) L += ex2(ld_cluster_f32(a) - M) * lc;
     }
-    const float2 mine = ml_s[hh];
-    scale_s[hh] = mine.y != 0.f ? ex2(mine.x - M) / L : 0.f;
-    if (crank == 0 && hh < nh && !*abort_s)
-      p.lse[((size_t)r * T + t) * p.h + h0 + hh] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
+    const float2 mine = ml_s[hd];
+    scale_s[hd] = mine.y != 0.f ? ex2(mine.x - M) / L : 0.f;
+    if (crank == 0 && hd < nh && good) p.lse[lse_at + hd] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
   }
-  const size_t out_at = (((size_t)r * T + t) * p.h + h0) * kDV;   // nh rows of 512, one after the other
-  const int segs = 16 / (int)G;
-  float* recv = reinterpret_cast<float*>(smem);
-  __syncwarp();
-  if (warp < kSoftWarps) {
-    named_barrier(1, kSoftThreads);
-#pragma unroll 1
-    for (int c = half; c < 4 * HB; c += 2) {
-      const int m = c / HB, hb = 16 * (c % HB);
-      uint32_t o[16];
-      if (have_o) {
-        tmem_ld16(lane_base + kColO + 16 * c, o);
-        tmem_ld_wait();
-      }
-      float f[16];
-#pragma unroll
-      for (int k = 0; k < 16; ++k) f[k] = have_o ? __uint_as_float(o[k]) * scale_s[hb + k] : 0.f;
-      const int col = 128 * m + 32 * quad + lane;
-      if (G == 1) {
-        // [head][512] in the idle stages, as it goes to global memory
-        if (kp.qp.out_bf16) {
-          __nv_bfloat16* o_s = reinterpret_cast<__nv_bfloat16*>(smem) + hb * kDV + col;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o_s[k * kDV] = __float2bfloat16_rn(f[k]);
-        } else {
-          float* o_s = reinterpret_cast<float*>(smem) + hb * kDV + col;
-#pragma unroll
-          for (int k = 0; k < 16; ++k) o_s[k * kDV] = f[k];
-        }
-      } else {
-        // 32-column segment 4m + quad to CTA (4m + quad) / segs, slot of this CTA:
-        // [lane][NH], 16-byte words swizzled by lane
-        const int sg = 4 * m + quad;
-        const uint32_t dst = mapa(recv + ((size_t)(crank * segs + sg % segs) * 32 + lane) * NH, sg / segs);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          st_cluster_v4(dst + 16u * ((hb / 4 + k) ^ (lane & (NH / 4 - 1))), __float_as_uint(f[4 * k]),
-                        __float_as_uint(f[4 * k + 1]), __float_as_uint(f[4 * k + 2]), __float_as_uint(f[4 * k + 3]));
-      }
-    }
-    if (G == 1) {
-      fence_proxy_async_smem();
-      named_barrier(1, kSoftThreads);
-      if (lane == 0 && !*abort_s) {
-        const uint32_t row = kDV * (kp.qp.out_bf16 ? 2 : 4);
-        char* dst = reinterpret_cast<char*>(p.out) + out_at * (row / kDV);
-        for (int hd = warp; hd < nh; hd += kSoftWarps)
-          bulk_store_s2g(dst + (size_t)hd * row, smem_u32(smem) + hd * row, row);
-        bulk_commit_group();
-        bulk_wait_read<0>();
-      }
-      __syncwarp();
-    }
-  }
-  tc_fence_before();
-  if (G > 1) cluster_sync();   // every CTA's scaled partial O has landed with its owner
-  tc_fence_after();
-  if (G > 1 && warp < kSoftWarps && !*abort_s) {
-    // this CTA's segments: the sum of the G scaled partials, in the order of the CTAs
-    for (int x = warp; x < segs * (NH / 4); x += kSoftWarps) {
-      const int sg = x % segs, k4 = x / segs;
-      if (4 * k4 >= nh) break;
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint32_t c = 0; c < G; ++c) {
-        const float4 y = *reinterpret_cast<const float4*>(recv + ((size_t)(c * segs + sg) * 32 + lane) * NH +
-                                                          4 * (k4 ^ (lane & (NH / 4 - 1))));
-        a.x += y.x; a.y += y.y; a.z += y.z; a.w += y.w;
-      }
-      const float f[4] = {a.x, a.y, a.z, a.w};
-      const size_t at = out_at + 32 * ((int)crank * segs + sg) + lane;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (4 * k4 + k >= nh) break;
-        if (kp.qp.out_bf16)
-          reinterpret_cast<__nv_bfloat16*>(p.out)[at + (size_t)(4 * k4 + k) * kDV] = __float2bfloat16_rn(f[k]);
-        else
-          p.out[at + (size_t)(4 * k4 + k) * kDV] = f[k];
-      }
-    }
-  }
-
-  // ---- teardown ------------------------------------------------------------------
-  __syncwarp();
-  tc_fence_before();
   __syncthreads();
+  // 32-column segment 4m + quad of O goes to CTA (4m + quad) / segs, into its idle stages, slot
+  // of this CTA: [lane][NH], 16-byte words swizzled by lane
+  const int segs = 16 >> g_shift;
+  float* recv = reinterpret_cast<float*>(smem);
+#pragma unroll 1
+  for (int c = warp >> 2; c < 4 * HB; c += kThreads / 128) {
+    const int m = c / HB, hb = 16 * (c % HB), sg = 4 * m + (warp & 3);
+    uint32_t o[16];
+    if (have_o) {
+      tmem_ld16(my_lanes + kColO + 16 * c, o);
+      tmem_ld_wait();
+    }
+    const uint32_t dst = mapa(recv + ((size_t)(crank * segs + (sg & (segs - 1))) * 32 + lane) * NH, sg / segs);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) f[u] = have_o ? __uint_as_float(o[4 * k + u]) * scale_s[hb + 4 * k + u] : 0.f;
+      st_cluster_v4(dst + 16u * ((hb / 4 + k) ^ (lane & (NH / 4 - 1))), __float_as_uint(f[0]), __float_as_uint(f[1]),
+                    __float_as_uint(f[2]), __float_as_uint(f[3]));
+    }
+  }
+  tc_fence_before();
+  cluster_sync();   // every CTA's scaled partial O has landed with its owner
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (!good) return;
+  // this CTA's segments: the sum of the G scaled partials, in the order of the CTAs
+  for (int x = warp; x < segs * (NH / 4); x += kThreads / 32) {
+    const int sg = x & (segs - 1), k4 = x / segs;
+    if (4 * k4 >= nh) break;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (uint32_t c = 0; c < G; ++c) {
+      const float4 y = *reinterpret_cast<const float4*>(recv + ((size_t)(c * segs + sg) * 32 + lane) * NH +
+                                                        4 * (k4 ^ (lane & (NH / 4 - 1))));
+      a.x += y.x; a.y += y.y; a.z += y.z; a.w += y.w;
+    }
+    const float f[4] = {a.x, a.y, a.z, a.w};
+    const size_t at = out_at + 32 * ((int)crank * segs + sg) + lane;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (4 * k4 + k >= nh) break;
+      if (kp.qp.out_bf16)
+        reinterpret_cast<__nv_bfloat16*>(p.out)[at + (size_t)(4 * k4 + k) * kDV] = __float2bfloat16_rn(f[k]);
+      else
+        p.out[at + (size_t)(4 * k4 + k) * kDV] = f[k];
+    }
+  }
 }
 
 template <int NH, bool kIL>
@@ -1019,6 +1039,8 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
   kp.num_rows = p.num_blocks * p.block_size;
   divisor(p.block_size, kp.bs_mul, kp.bs_shift);
   divisor(qp.group, kp.gr_mul, kp.gr_shift);
+  divisor((int)T, kp.T_mul, kp.T_shift);
+  divisor(p.Q, kp.Q_mul, kp.Q_shift);
   if (!make_rows_map(&lat, p.kv, kp.num_rows, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_rows_map(&rope, p.kv, kp.num_rows, 64, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
