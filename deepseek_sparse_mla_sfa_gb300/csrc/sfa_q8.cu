@@ -77,7 +77,7 @@ constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscScale = 1024, kMiscC = 1280, k
               kMiscMoved = 1544, kMiscCount = 1560, kMiscSeg = 1600, kMiscBytes = 1616;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
 constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarRows = kBarKvEmpty + kStages,
-              kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQReady = kBarSegFull + 1,
+              kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQLoad = kBarSegFull + 1, kBarQReady = kBarQLoad + 1,
               kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarAReady = kBarSFree + 2, kBarPReady = kBarAReady + 2,
               kBarPFree = kBarPReady + 2, kBarPvFinal = kBarPFree + 2, kBarMmaFin = kBarPvFinal + 1,
               kBarMmaFin2 = kBarMmaFin + 1, kBarNever = kBarMmaFin2 + 1, kNumBars = kBarNever + 1;
@@ -86,10 +86,10 @@ static_assert(kNt % (4 * kProducerWarps) == 0, "whole row groups a producer");
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kBlk % 1024 == 0 && kStageBytes % 1024 == 0 && kOffP % 1024 == 0, "operands: 1024-byte alignment");
 static_assert(kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
-static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the output and the cluster merge fit in the stages");
-// q's e4m3 rows on their way to TMEM, in stages 1 and 2: 128 rows (64 hi, 64 lo) of 576 bytes
-constexpr int kQPitch = 592;   // an odd number of 16-byte words: rows start in different banks
-constexpr int kOffTmp = kStageBytes + 128 * kQPitch;   // behind it: the resolved list before its compaction
+static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the cluster merge fits in the stages");
+// q on its way to TMEM, in stages 1 and 2: 64 rows of 576 bf16, then in place 576 hi and 576 lo bytes
+constexpr int kQPitch = 1168;  // an odd number of 16-byte words: rows start in different banks
+constexpr int kOffTmp = kStageBytes + kGroupHeads * kQPitch;   // behind it: the resolved list before its compaction
 constexpr int kTmpCap = (kStages * kStageBytes - kOffTmp) / 4;
 static_assert(kTmpCap >= 8192, "q and a list of 8192 entries fit in stages 1 and 2");
 static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscBytes, "misc");
@@ -182,11 +182,6 @@ __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
   return *reinterpret_cast<__half2*>(&r);
-}
-
-__device__ __forceinline__ void bulk_store_s2g(void* dst, uint32_t src, uint32_t bytes) {
-  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes)
-               : "memory");
 }
 
 // entries j0 + 32 k + lane < c_end (k < 8) of the selected list, -1 behind its end
@@ -303,22 +298,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Warps 0-7 and 16-19 bring q into TMEM; meanwhile warps 8-15 resolve the list and start the
   // gathers.  The first loads of both go out before anything waits.
   const int wq = warp < kSoftWarps ? warp : warp - kListWarps;    // of the kQWarps that bring q
-  uint4 q1[3], q2[3];
-  auto load_head = [&](int hd, uint4 (&x)[3]) {
-#pragma unroll
-    for (int k = 0; k < 3; ++k)
-      x[k] = hd < nh && lane + 32 * k < 72 ? __ldg(qsrc + (size_t)hd * 72 + lane + 32 * k) : make_uint4(0, 0, 0, 0);
-  };
   const int chunk = ((p.top_k + kListWarps * 32 - 1) / (kListWarps * 32)) * 32;
   const int c_begin = min((warp - kSoftWarps) * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
   int pos_r[8];
-  if (warp >= kSoftWarps && warp < kFixWarp) {
-    load8(idx, c_begin, c_end, lane, pos_r);
-  } else {
-    load_head(wq, q1);
-    load_head(wq + kQWarps, q2);
+  if (warp >= kSoftWarps && warp < kFixWarp) load8(idx, c_begin, c_end, lane, pos_r);
+  char* const qst = smem + kStageBytes;
+  if (warp == 0) {
+    if (lane == 0) {
+      mbar_init(&bars[kBarQLoad], 1);
+      fence_barrier_init();
+      mbar_arrive_expect_tx(&bars[kBarQLoad], (uint32_t)nh * kDQK * 2);
+    }
+    __syncwarp();
+    for (int hd = lane; hd < nh; hd += 32)
+      bulk_load_g2s(smem_u32(qst + hd * kQPitch), qsrc + (size_t)hd * 72, kDQK * 2, &bars[kBarQLoad]);
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 64) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars[kBarKvFull + s], kProducerWarps);
       mbar_init(&bars[kBarRows + s], 1);
@@ -425,16 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) >> g_shift : 0;
   };
   if (warp < kSoftWarps || warp >= kFixWarp) {
-    // ---- q as hi and lo e4m3 rows: coalesced loads (a head a warp, two in flight), then
-    // through shared memory (stages 1 and 2, which the gathers leave alone until q is ready)
-    // to the TMEM lanes
-    char* qst = smem + kStageBytes;
+    // ---- q as hi and lo e4m3 rows, a head a warp, in place in shared memory (stages 1 and 2,
+    // which the gathers leave alone until q is ready); then to the TMEM lanes
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarQLoad], 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
 #pragma unroll 1
     for (int hd = wq; hd < NH; hd += kQWarps) {
-      const uint4 x[3] = {q1[0], q1[1], q1[2]};
+      char* at = qst + hd * kQPitch;
+      uint4 x[3];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) q1[k] = q2[k];
-      load_head(hd + 2 * kQWarps, q2);
+      for (int k = 0; k < 3; ++k)
+        x[k] = hd < nh && lane + 32 * k < 72 ? *reinterpret_cast<const uint4*>(at + 16 * (lane + 32 * k))
+                                             : make_uint4(0, 0, 0, 0);
       uint32_t am = 0;
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
@@ -451,7 +447,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0)
         qc_s[hd] = bad ? __int_as_float(0x7fc00000)
                        : fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
-      char* at = qst + hd * kQPitch + 8 * lane;
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
@@ -465,14 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           lo[i] = e4m3x2_h(__hmul2(__hsub2(v, half2_of(hi[i])), __floats2half2_rn(16.f, 16.f)));
         }
         if (lane + 32 * k < 72) {
-          *reinterpret_cast<uint2*>(at + 256 * k) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
-          *reinterpret_cast<uint2*>(at + 256 * k + 64 * kQPitch) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+          char* to = at + 8 * (lane + 32 * k);
+          *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+          *reinterpret_cast<uint2*>(to + kDQK) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         }
       }
     }
     named_barrier(1, 32 * kQWarps);
     const int quad = warp & 3;
-    const char* mine = qst + (16 * quad + (lane & 15) + (lane >= 16 ? 64 : 0)) * kQPitch;
+    const char* mine = qst + (16 * quad + (lane & 15)) * kQPitch + (lane >= 16 ? kDQK : 0);
 #pragma unroll 1
     for (int c = wq >> 2; c < 9 && quad < HB; c += kQWarps / 4) {     // 64 columns of q are 16 columns of TMEM
       uint32_t v[16];
@@ -859,15 +855,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const size_t lse_at = ((size_t)r * T + t) * p.h + h0, out_at = lse_at * kDV;   // nh rows of 512, one after the other
   const uint32_t my_lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
   if (G == 1) {
-    // O / l to [head][512] in the idle stages, as it goes to global memory; every warp takes
-    // (column block, 16 heads) pieces of its TMEM lanes
+    // O / l straight to global memory: every warp takes (column block, 16 heads) pieces of its
+    // TMEM lanes, 32 columns of a head a store
     if (threadIdx.x < nh && good) {
       const float2 ml = ml_s[threadIdx.x];
       p.lse[lse_at + threadIdx.x] = ml.y != 0.f ? (ml.x + __log2f(ml.y)) * kLn2 : -INFINITY;
     }
 #pragma unroll 1
-    for (int c = warp >> 2; c < 4 * HB; c += kThreads / 128) {
+    for (int c = warp >> 2; c < 4 * HB && good; c += kThreads / 128) {
       const int m = c / HB, hb = 16 * (c % HB);
+      if (hb >= nh) continue;
       uint32_t o[16];
       if (have_o) tmem_ld16(my_lanes + kColO + 16 * c, o);
       float f[16];
@@ -879,30 +876,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have_o) tmem_ld_wait();
 #pragma unroll
       for (int k = 0; k < 16; ++k) f[k] = have_o ? __uint_as_float(o[k]) * f[k] : 0.f;
-      const int col = hb * kDV + 128 * m + 32 * (warp & 3) + lane;
+      const size_t at = out_at + (size_t)hb * kDV + 128 * m + 32 * (warp & 3) + lane;
       if (kp.qp.out_bf16) {
-        __nv_bfloat16* o_s = reinterpret_cast<__nv_bfloat16*>(smem) + col;
+        __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o_s[k * kDV] = __float2bfloat16_rn(f[k]);
+        for (int k = 0; k < 16; ++k)
+          if (hb + k < nh) to[k * kDV] = __float2bfloat16_rn(f[k]);
       } else {
-        float* o_s = reinterpret_cast<float*>(smem) + col;
+        float* to = p.out + at;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) o_s[k * kDV] = f[k];
+        for (int k = 0; k < 16; ++k)
+          if (hb + k < nh) to[k * kDV] = f[k];
       }
     }
-    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
-    if (lane == 0 && good) {
-      const uint32_t row = kDV * (kp.qp.out_bf16 ? 2 : 4);
-      char* dst = reinterpret_cast<char*>(p.out) + out_at * (row / kDV);
-      for (int hd = warp; hd < nh; hd += kThreads / 32)
-        bulk_store_s2g(dst + (size_t)hd * row, smem_u32(smem) + hd * row, row);
-      bulk_commit_group();
-      bulk_wait_read<0>();
-    }
     return;
   }
   // Every thread of every CTA of the cluster reaches both cluster barriers.
