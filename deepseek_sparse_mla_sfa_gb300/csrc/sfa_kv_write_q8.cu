@@ -67,17 +67,20 @@ __device__ __forceinline__ unsigned e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// x / s, infinities (which e4m3 does not have) to NaN
+// x / s (by its reciprocal where s is a power of two: exact), infinities, which e4m3 does not
+// have, to NaN
+template <bool kPow2>
 __device__ __forceinline__ float scaled(unsigned bf16_bits, float s) {
   const float x = __uint_as_float(bf16_bits << 16);
-  return (bf16_bits & 0x7fffu) == 0x7f80u ? __int_as_float(0x7fc00000) : x / s;
+  return (bf16_bits & 0x7fffu) == 0x7f80u ? __int_as_float(0x7fc00000) : kPow2 ? x * s : x / s;
 }
 
+template <bool kPow2>
 __device__ __forceinline__ uint2 quantise8(const uint4& x, float s) {
   const unsigned w[4] = {x.x, x.y, x.z, x.w};
   unsigned q[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = e4m3x2(scaled(w[i] & 0xffffu, s), scaled(w[i] >> 16, s));
+  for (int i = 0; i < 4; ++i) q[i] = e4m3x2(scaled<kPow2>(w[i] & 0xffffu, s), scaled<kPow2>(w[i] >> 16, s));
   return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
 }
 
@@ -134,9 +137,13 @@ struct Row {
   }
   __device__ __forceinline__ void store(uint4* kv8, float s) const {
     uint2* dst = reinterpret_cast<uint2*>(kv8 + (size_t)slot * kRow8Words) + lane;
+    // every scale that this file writes is a power of two within [2^-100, 2^120]
+    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-100f;
+    const float inv = 1.f / s;
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-      if (lane + kRowThreads * i < kRowWords) dst[kRowThreads * i] = quantise8(x[i], s);
+      if (lane + kRowThreads * i < kRowWords)
+        dst[kRowThreads * i] = pow2 ? quantise8<true>(x[i], inv) : quantise8<false>(x[i], s);
   }
   // a value of the row's thread 0 to all of them, and a barrier over the row
   __device__ __forceinline__ int broadcast(int v) const {

@@ -356,6 +356,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (rounds of 8 entries a lane; one round stays in registers, more go to a temporary list a
   // warp, in the part of stage 2 that q leaves free)
   int total = 0;
+  int n_tiles = 0, n_local = 0;
+  auto count_tiles = [&]() {
+    n_tiles = (total + kNt - 1) / kNt;
+    n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) >> g_shift : 0;
+  };
+  auto fail = [&](void) {
+    report_status(p.status, kStatusTimeout);
+    *abort_s = 1;
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
+  };
+
+  // warps 0-7: warp 4 half + quad holds heads 16 quad + 8 half .. + 7 whole, a thread one of
+  // them (row lane / 4 + 8 half of a 16-lane load), its reference (log2 units) and its share of
+  // its sum; with 32 heads or fewer the warps of two quadrants hold none
+  const int quad = warp & 3, half = warp >> 2;
+  const int head = 16 * quad + 8 * half + (lane >> 2);
+  const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+  float ref = -INFINITY, l_sum = 0.f;
+  // Roles follow in place, so that each warp runs through code that lies next to what it ran
+  // before (the instruction cache is cold at every launch).
   if (warp >= kSoftWarps && warp < kFixWarp) {
     int row_r[8], cnt = 0;
     const bool keep = kListWarps * chunk <= kTmpCap;      // longer lists are resolved a second time
@@ -413,13 +435,202 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && warp == kSoftWarps) wcount_s[kListWarps] = total;
     __syncwarp();
     asm volatile("bar.arrive %0, %1;" ::"r"(5), "r"(kThreads) : "memory");   // the other warps read `total`
-  }
-  int n_tiles = 0, n_local = 0;
-  auto count_tiles = [&]() {
-    n_tiles = (total + kNt - 1) / kNt;
-    n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) >> g_shift : 0;
-  };
-  if (warp < kSoftWarps || warp >= kFixWarp) {
+    count_tiles();
+    if (warp >= kProducerWarp && warp < kProducerWarp + kProducerWarps) {
+      // =================== gathers ===================================================
+      // Warp pw takes the tile's row groups pw, pw + 4, ... (4 rows each), five gather4 a group,
+      // all from one lane: the lanes of a warp would issue theirs one after the other, each with
+      // its operands moved to uniform registers first.  The warp waits for nothing but stages.
+      const int pw = warp - kProducerWarp;
+      constexpr int kGroupsOf = kNt / 4 / kProducerWarps;
+      int seg = 0, n = 0;
+      bool ok = true;
+      for (; n < n_local && !*abort_s; ++n) {
+        const int at = n % kStages;
+        // stages 1 and 2 hold q until it is in TMEM; later tiles wait for P.V of the stage's last
+        if (n > 0 && !(ok = n >= kStages ? wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1)
+                                         : wait_warp(&bars[kBarQReady], 0)))
+          break;
+        const int first = kNt * ((int)crank + (int)G * n);
+        if (first >= (seg + 1) * kListCap) {      // more valid entries than the list holds
+          if (lane == 0) mbar_arrive(&bars[kBarSegFree]);
+          if (!(ok = wait_warp(&bars[kBarSegFull], seg & 1))) break;
+          ++seg;
+        }
+        const int* rows = list_s + (first - seg * kListCap) + 4 * pw;
+        const uint32_t st = smem_u32(smem + at * kStageBytes);
+        uint64_t* full = &bars[kBarKvFull + at];
+        if (elect_one()) {
+          mbar_arrive_expect_tx(full, kGroupsOf * 4 * kDQK);
+  #pragma unroll
+          for (int g = 0; g < kGroupsOf; ++g) {
+            const int y = 4 * (pw + kProducerWarps * g);
+            const int4 rr = *reinterpret_cast<const int4*>(rows + 4 * kProducerWarps * g);
+  #pragma unroll
+            for (int m = 0; m < 4; ++m)
+              tma_gather4(st + m * kBlk + y * 128, &tmap_lat, 128 * m, rr.x, rr.y, rr.z, rr.w, full);
+            tma_gather4(st + 4 * kBlk + y * 64, &tmap_rope, kDV, rr.x, rr.y, rr.z, rr.w, full);
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) fail();
+      // no gather of this CTA may still be landing in shared memory at exit
+      for (int k = n > kStages ? n - kStages : 0; k < n; ++k)
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit)))
+          report_status(p.status, kStatusTimeout);
+    } else if (warp == kRowWarp) {
+      // =================== the rows' scales, and the rest of a long list ==============
+      // Scales are single words anywhere in memory: those of the next four tiles are in flight
+      // while four are published.  A segment of the list begins with a group of four (64 tiles,
+      // dealt to at most 8 CTAs).
+      constexpr int kAhead = 4, kPer = kNt / 32;
+      static_assert(kListCap / kNt % (8 * kAhead) == 0, "segments begin with a group");
+      float cur[kAhead][kPer], nxt[kAhead][kPer];
+      int seg = 0, j = seg_s[0], ord = seg_s[1];   // the next segment's first round, entries before it
+      bool ok = true;
+      auto load4 = [&](int n0, float (&v)[kAhead][kPer]) {
+  #pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const int* rows = list_s + kNt * ((int)crank + (int)G * (n0 + d)) - seg * kListCap + lane;
+  #pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            const int row = n0 + d < n_local ? rows[32 * u] : kp.num_rows;
+            v[d][u] = row < kp.num_rows ? __ldg(kp.qp.scales + div_by(row, kp.gr_mul, kp.gr_shift)) : 0.f;
+          }
+        }
+      };
+      load4(0, cur);
+  #pragma unroll 1
+      for (int n0 = 0; n0 < n_local && ok && !*abort_s; n0 += kAhead) {
+        const int first = kNt * ((int)crank + (int)G * (n0 + kAhead));
+        const bool more = n0 + kAhead < n_local, turn = more && first >= (seg + 1) * kListCap;
+        if (more && !turn) load4(n0 + kAhead, nxt);
+  #pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const int n = n0 + d, at = n % kStages;
+          if (n >= n_local || !ok) break;
+          if (n >= kStages && !(ok = wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1))) break;
+  #pragma unroll
+          for (int u = 0; u < kPer; ++u) {
+            // (a row that does not exist has scale 0: weight 0)
+            const int y = at * kNt + lane + 32 * u;
+            float* rp = reinterpret_cast<float*>(rows_s) + 4 * (y >> 1) + (y & 1);
+            rp[0] = cur[d][u];
+            rp[2] = __log2f(cur[d][u]);
+            inv_s[y] = cur[d][u] > 0.f ? __frcp_rn(cur[d][u]) : 0.f;
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarRows + at]);
+        }
+        if (turn && ok) {
+          // once the producers have issued the segment's last tile, the next segment takes its
+          // place (they only wait for tiles that are published by now)
+          if (!(ok = wait_warp(&bars[kBarSegFree], seg & 1))) break;
+          ++seg;
+          const int base = seg * kListCap;
+  #pragma unroll 1
+          while (j < p.top_k) {
+            int pos[8], row[8], to = ord;
+            load8(idx, j, p.top_k, lane, pos);
+            resolve8<kInterleaved>(kp, pos, sel, bt_row, false, row);
+  #pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const unsigned mask = __ballot_sync(0xffffffffu, row[k] >= 0);
+              const int o = to + __popc(mask & lanemask_lt()) - base;
+              if (row[k] >= 0 && o >= 0 && o < kListCap) list_s[o] = row[k];
+              to += __popc(mask);
+            }
+            if (to > base + kListCap) break;       // the round goes on in the segment after
+            ord = to;
+            j += 256;
+          }
+          for (int o = total - base + lane; o < min(n_tiles * kNt - base, kListCap); o += 32) list_s[o] = kp.num_rows;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarSegFull]);
+          load4(n0 + kAhead, nxt);
+        }
+  #pragma unroll
+        for (int d = 0; d < kAhead; ++d)
+  #pragma unroll
+          for (int u = 0; u < kPer; ++u) cur[d][u] = nxt[d][u];
+      }
+      if (!ok) fail();
+    } else if (warp == kQkWarp || warp == kPvWarp) {
+      // =================== tcgen05 MMA issue: QK^T (warp 8) and P.V (warp 9) ========
+      // (the whole warp walks the tiles and waits; one lane issues)
+      if (n_local > 0) {
+        bool ok = true;
+        const uint32_t st0 = smem_u32(smem);
+        if (warp == kQkWarp) {
+          // test hook: a wait that cannot complete, so the wait limit runs out
+          ok = !p.stall || wait_warp(&bars[kBarNever], 0);
+          ok = ok && wait_warp(&bars[kBarQReady], 0);
+          tc_fence_after();
+          constexpr uint32_t id = idesc_e4m3(128, kNt, 0, 0);
+          int s = 0;
+          uint32_t full = 0;
+          for (int n = 0; ok && n < n_local && !*abort_s; ++n) {
+            const int sb = kSBufs == 2 ? n & 1 : 0;
+            if (!(ok = wait_warp(&bars[kBarKvFull + s], full))) break;
+            // the score buffer is free once the softmax has read the tile before from it
+            if (n >= kSBufs && !(ok = wait_warp(&bars[kBarSFree + sb], (kSBufs == 2 ? (n >> 1) - 1 : n - 1) & 1))) break;
+            tc_fence_after();
+            const uint32_t st = st0 + s * kStageBytes;
+            const uint32_t d = tmem + (sb ? kColS1 : kColS);
+            if (elect_one()) {
+              const uint32_t b0 = desc_lo(st, 16);
+  #pragma unroll
+              for (int k = 0; k < 16; ++k)
+                mma8_ts<desc_hi(1024, kSwizzle128)>(d, tmem + kColQ + 8 * k, b0 + (((k >> 2) * kBlk + (k & 3) * 32) >> 4),
+                                                    id, k > 0);
+  #pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma8_ts<desc_hi(512, kSwizzle64)>(d, tmem + kColQ + 128 + 8 * k, b0 + ((4 * kBlk + k * 32) >> 4), id, 1);
+              mma_commit(&bars[kBarSFull + sb]);
+            }
+            __syncwarp();
+            if (++s == kStages) { s = 0; full ^= 1; }
+          }
+        } else {
+          // A = E^T: columns 128m..128m+127 of 32 tile rows, MN-major (one SW128 atom wide);
+          // B = P^T: NH heads x 32 rows, K-major.  The four blocks' accumulators alternate.
+          constexpr uint32_t id = idesc_e4m3(128, NH, 1, 0);
+          int s = 0;
+          for (int n = 0; ok && n < n_local && !*abort_s; ++n) {
+            const int bb = n & 1;
+            if (!(ok = wait_warp(&bars[kBarPReady + bb], (n >> 1) & 1))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t a0 = desc_lo(st0 + s * kStageBytes, kBlk);
+              const uint32_t b0 = desc_lo(st0 + kOffP + 2 * bb * kPBytes, 16);
+  #pragma unroll
+              for (int k = 0; k < kNt / 32; ++k)
+  #pragma unroll
+                for (int part = 0; part < 2; ++part)
+  #pragma unroll
+                  for (int m = 0; m < 4; ++m)
+                    mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128)>(
+                        tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPBytes + 32 * k) >> 4), id,
+                        (k > 0 || part > 0) ? 1u : (n > 0 ? 1u : 0u));
+              mma_commit(&bars[kBarKvEmpty + s]);
+              mma_commit(&bars[kBarPFree + bb]);
+              if (n == n_local - 1) mma_commit(&bars[kBarPvFinal]);
+            }
+            __syncwarp();
+            if (++s == kStages) s = 0;
+          }
+        }
+        if (!ok) fail();
+        // every MMA this warp issued has completed before TMEM is released
+        // (the same lane is elected every time: a commit covers its thread's MMAs)
+        uint64_t* fin_bar = &bars[warp == kQkWarp ? kBarMmaFin : kBarMmaFin2];
+        if (elect_one()) mma_commit(fin_bar);
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, mbar_wait(fin_bar, 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
+      }
+    }
+  } else {
     // ---- q as hi and lo e4m3 rows, a head a warp, in place in shared memory (stages 1 and 2,
     // which the gathers leave alone until q is ready); then to the TMEM lanes
     if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarQLoad], 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
@@ -486,355 +697,146 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) mbar_arrive(&bars[kBarQReady]);
     named_barrier(5, kThreads);
     total = wcount_s[kListWarps];
-  }
-  count_tiles();
-
-  auto fail = [&](void) {
-    report_status(p.status, kStatusTimeout);
-    *abort_s = 1;
-  };
-  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
-  };
-
-  // warps 0-7: warp 4 half + quad holds heads 16 quad + 8 half .. + 7 whole, a thread one of
-  // them (row lane / 4 + 8 half of a 16-lane load), its reference (log2 units) and its share of
-  // its sum; with 32 heads or fewer the warps of two quadrants hold none
-  const int quad = warp & 3, half = warp >> 2;
-  const int head = 16 * quad + 8 * half + (lane >> 2);
-  const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-  float ref = -INFINITY, l_sum = 0.f;
-  if (warp < kSoftWarps) {
-    // =================== q into TMEM, softmax, O rescale (warps 0-7) ================
-    if (quad < HB) {
-      float c_head = qc_s[head];
-      const bool bad_q = c_head != c_head;
-      if (bad_q) c_head = 1e-30f;
-      const uint64_t c2 = pack2(c_head, c_head), sixteenth = pack2(0.0625f, 0.0625f);
-      uint64_t l2 = 0;                                        // two running sums
-      // this head's row of P^T (K-major SW128) and this thread's bytes 16 k + 8 u + 2 (lane % 4)
-      char* const p_row = smem + kOffP + head * 128 + 2 * (lane & 3);
-      for (int i = 0; i < n_local; ++i) {
-        const int bb = i & 1, sb = kSBufs == 2 ? bb : 0, st = i % kStages;
-        if (*abort_s || !wait_warp(&bars[kBarSFull + sb], (kSBufs == 2 ? i >> 1 : i) & 1) ||
-            !wait_warp(&bars[kBarRows + st], (i / kStages) & 1)) {
-          fail();
-          break;
-        }
-        tc_fence_after();
-        // x = log2 of the weight: S = hi + lo / 16, then scale, head factor and log2 scale.
-        // Pairs of rows 8 j + 2 (lane % 4), j < 12
-        uint64_t x[kNt / 8];
-        constexpr int kBatch = kNt / 32;                    // 16-row loads in flight at a time
-        const uint32_t s_col = lane_base + (sb ? kColS1 : kColS);
-        const float4* rs = rows_s + st * (kNt / 2) + (lane & 3);
-        float mx = -INFINITY;
-#pragma unroll
-        for (int k3 = 0; k3 < kNt / 16; k3 += kBatch) {
-          uint32_t vh[kBatch][8], vl[kBatch][8];
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k) {
-            tmem_ld_16x16(s_col + 16 * (k3 + k), vh[k]);
-            tmem_ld_16x16(s_col + (16u << 16) + 16 * (k3 + k), vl[k]);
+    count_tiles();
+    if (warp < kSoftWarps) {
+      // =================== softmax (warps 0-7) ======================================
+      if (quad < HB) {
+        float c_head = qc_s[head];
+        const bool bad_q = c_head != c_head;
+        if (bad_q) c_head = 1e-30f;
+        const uint64_t c2 = pack2(c_head, c_head), sixteenth = pack2(0.0625f, 0.0625f);
+        uint64_t l2 = 0;                                        // two running sums
+        // this head's row of P^T (K-major SW128) and this thread's bytes 16 k + 8 u + 2 (lane % 4)
+        char* const p_row = smem + kOffP + head * 128 + 2 * (lane & 3);
+        for (int i = 0; i < n_local; ++i) {
+          const int bb = i & 1, sb = kSBufs == 2 ? bb : 0, st = i % kStages;
+          if (*abort_s || !wait_warp(&bars[kBarSFull + sb], (kSBufs == 2 ? i >> 1 : i) & 1) ||
+              !wait_warp(&bars[kBarRows + st], (i / kStages) & 1)) {
+            fail();
+            break;
           }
-          tmem_ld_wait();
-          if (k3 + kBatch == kNt / 16) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars[kBarSFree + sb]);
-          }
-#pragma unroll
-          for (int k = 0; k < kBatch; ++k)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int j = 2 * (k3 + k) + u;
-              const uint64_t hi = half ? pack2u(vh[k][4 * u + 2], vh[k][4 * u + 3]) : pack2u(vh[k][4 * u], vh[k][4 * u + 1]);
-              const uint64_t lo = half ? pack2u(vl[k][4 * u + 2], vl[k][4 * u + 3]) : pack2u(vl[k][4 * u], vl[k][4 * u + 1]);
-              const float4 cr = rs[4 * j];
-              x[j] = fma2(fma2(lo, sixteenth, hi), mul2(pack2(cr.x, cr.y), c2), pack2(cr.z, cr.w));
-              const float2 f = unpack2(x[j]);
-              mx = fmaxf(mx, fmaxf(f.x, f.y));
+          tc_fence_after();
+          // x = log2 of the weight: S = hi + lo / 16, then scale, head factor and log2 scale.
+          // Pairs of rows 8 j + 2 (lane % 4), j < 12
+          uint64_t x[kNt / 8];
+          constexpr int kBatch = kNt / 32;                    // 16-row loads in flight at a time
+          const uint32_t s_col = lane_base + (sb ? kColS1 : kColS);
+          const float4* rs = rows_s + st * (kNt / 2) + (lane & 3);
+          float mx = -INFINITY;
+  #pragma unroll
+          for (int k3 = 0; k3 < kNt / 16; k3 += kBatch) {
+            uint32_t vh[kBatch][8], vl[kBatch][8];
+  #pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+              tmem_ld_16x16(s_col + 16 * (k3 + k), vh[k]);
+              tmem_ld_16x16(s_col + (16u << 16) + 16 * (k3 + k), vl[k]);
             }
+            tmem_ld_wait();
+            if (k3 + kBatch == kNt / 16) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&bars[kBarSFree + sb]);
+            }
+  #pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+  #pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int j = 2 * (k3 + k) + u;
+                const uint64_t hi = half ? pack2u(vh[k][4 * u + 2], vh[k][4 * u + 3]) : pack2u(vh[k][4 * u], vh[k][4 * u + 1]);
+                const uint64_t lo = half ? pack2u(vl[k][4 * u + 2], vl[k][4 * u + 3]) : pack2u(vl[k][4 * u], vl[k][4 * u + 1]);
+                const float4 cr = rs[4 * j];
+                x[j] = fma2(fma2(lo, sixteenth, hi), mul2(pack2(cr.x, cr.y), c2), pack2(cr.z, cr.w));
+                const float2 f = unpack2(x[j]);
+                mx = fmaxf(mx, fmaxf(f.x, f.y));
+              }
+          }
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          // P buffer bb, and its flags and factors, are free once P.V of tile i-2 is done
+          if (i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) {
+            fail();
+            break;
+          }
+          const bool up = i == 0 || mx > ref + kMostP;
+          const float ref_new = up ? mx - kPeak : ref;
+          const bool moved = __any_sync(0xffffffffu, i > 0 && up);
+          if (moved) {
+            const float alpha = ex2(ref - ref_new);
+            l2 = mul2(l2, pack2(alpha, alpha));
+            if ((lane & 3) == 0) alpha_s[64 * bb + head] = alpha;
+          }
+          if (lane == 0) moved_s[8 * bb + 2 * quad + half] = moved;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarAReady + bb]);
+          ref = ref_new;
+          // P = 2^(x - ref) as hi + lo; p = P / scale into the sum
+          const uint64_t nref = pack2(-ref, -ref);
+          const float2* iv = reinterpret_cast<const float2*>(inv_s + st * kNt) + (lane & 3);
+          char* const row = p_row + 2 * bb * kPBytes;
+  #pragma unroll
+          for (int j = 0; j < kNt / 8; ++j) {
+            const float2 f = unpack2(add2(x[j], nref));
+            const float p0 = ex2(f.x), p1 = ex2(f.y);
+            const float2 inv = iv[4 * j];
+            l2 = fma2(pack2(p0, p1), pack2(inv.x, inv.y), l2);
+            // 11 bits are enough under the 8 that hi and lo keep
+            const __half2 w = __floats2half2_rn(p0, p1);
+            const uint32_t hi = e4m3x2_h(w);
+            const int at = (((j >> 1) ^ (head & 7)) << 4) + 8 * (j & 1);
+            *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)hi;
+            *reinterpret_cast<uint16_t*>(row + at + kPBytes) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // P buffer bb, and its flags and factors, are free once P.V of tile i-2 is done
-        if (i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) {
+        const float2 f = unpack2(l2);
+        l_sum = f.x + f.y;
+        l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 1);
+        l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
+        if (bad_q && n_local > 0) l_sum = __int_as_float(0x7fc00000);
+      }
+    } else if (warp >= kFixWarp) {
+      // =================== O follows the references (warps 16-19) ====================
+      // Where a head's reference moved with tile i, its column of O^T is scaled between P.V of
+      // tiles i-1 and i, while the softmax warps write the weights.
+      const uint32_t my_lanes = tmem + ((uint32_t)((warp - kFixWarp) * 32) << 16);
+      for (int i = 0; i < n_local && !*abort_s; ++i) {
+        const int bb = i & 1;
+        if (!wait_warp(&bars[kBarAReady + bb], (i >> 1) & 1)) {
           fail();
           break;
         }
-        const bool up = i == 0 || mx > ref + kMostP;
-        const float ref_new = up ? mx - kPeak : ref;
-        const bool moved = __any_sync(0xffffffffu, i > 0 && up);
-        if (moved) {
-          const float alpha = ex2(ref - ref_new);
-          l2 = mul2(l2, pack2(alpha, alpha));
-          if ((lane & 3) == 0) alpha_s[64 * bb + head] = alpha;
+        uint64_t m8 = *reinterpret_cast<const volatile uint64_t*>(moved_s + 8 * bb);
+        if (m8 != 0) {
+          if (!wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1)) {
+            fail();
+            break;
+          }
+          tc_fence_after();
+  #pragma unroll 1
+          while (m8 != 0) {
+            const int oct = (__ffsll((long long)m8) - 1) >> 3;
+            m8 &= m8 - 1;
+            const float4 a = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct);
+            const float4 c = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct + 4);
+            const float al[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+            uint32_t o[32];
+            const uint32_t at = my_lanes + kColO + 8 * oct;
+  #pragma unroll
+            for (int m = 0; m < 4; ++m) tmem_ld8(at + NH * m, o + 8 * m);
+            tmem_ld_wait();
+  #pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k & 7]);
+  #pragma unroll
+            for (int m = 0; m < 4; ++m) tmem_st8(at + NH * m, o + 8 * m);
+          }
+          tmem_st_wait();
         }
-        if (lane == 0) moved_s[8 * bb + 2 * quad + half] = moved;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarAReady + bb]);
-        ref = ref_new;
-        // P = 2^(x - ref) as hi + lo; p = P / scale into the sum
-        const uint64_t nref = pack2(-ref, -ref);
-        const float2* iv = reinterpret_cast<const float2*>(inv_s + st * kNt) + (lane & 3);
-        char* const row = p_row + 2 * bb * kPBytes;
-#pragma unroll
-        for (int j = 0; j < kNt / 8; ++j) {
-          const float2 f = unpack2(add2(x[j], nref));
-          const float p0 = ex2(f.x), p1 = ex2(f.y);
-          const float2 inv = iv[4 * j];
-          l2 = fma2(pack2(p0, p1), pack2(inv.x, inv.y), l2);
-          // 11 bits are enough under the 8 that hi and lo keep
-          const __half2 w = __floats2half2_rn(p0, p1);
-          const uint32_t hi = e4m3x2_h(w);
-          const int at = (((j >> 1) ^ (head & 7)) << 4) + 8 * (j & 1);
-          *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)hi;
-          *reinterpret_cast<uint16_t*>(row + at + kPBytes) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
-        }
-        fence_proxy_async_smem();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
       }
-      const float2 f = unpack2(l2);
-      l_sum = f.x + f.y;
-      l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 1);
-      l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
-      if (bad_q && n_local > 0) l_sum = __int_as_float(0x7fc00000);
-    }
-  } else if (warp >= kFixWarp) {
-    // =================== O follows the references (warps 16-19) ====================
-    // Where a head's reference moved with tile i, its column of O^T is scaled between P.V of
-    // tiles i-1 and i, while the softmax warps write the weights.
-    const uint32_t my_lanes = tmem + ((uint32_t)((warp - kFixWarp) * 32) << 16);
-    for (int i = 0; i < n_local && !*abort_s; ++i) {
-      const int bb = i & 1;
-      if (!wait_warp(&bars[kBarAReady + bb], (i >> 1) & 1)) {
-        fail();
-        break;
-      }
-      uint64_t m8 = *reinterpret_cast<const volatile uint64_t*>(moved_s + 8 * bb);
-      if (m8 != 0) {
-        if (!wait_warp(&bars[kBarPFree + (bb ^ 1)], ((i - 1) >> 1) & 1)) {
-          fail();
-          break;
-        }
-        tc_fence_after();
-#pragma unroll 1
-        while (m8 != 0) {
-          const int oct = (__ffsll((long long)m8) - 1) >> 3;
-          m8 &= m8 - 1;
-          const float4 a = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct);
-          const float4 c = *reinterpret_cast<const float4*>(alpha_s + 64 * bb + 8 * oct + 4);
-          const float al[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-          uint32_t o[32];
-          const uint32_t at = my_lanes + kColO + 8 * oct;
-#pragma unroll
-          for (int m = 0; m < 4; ++m) tmem_ld8(at + NH * m, o + 8 * m);
-          tmem_ld_wait();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * al[k & 7]);
-#pragma unroll
-          for (int m = 0; m < 4; ++m) tmem_st8(at + NH * m, o + 8 * m);
-        }
-        tmem_st_wait();
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
-    }
-  } else if (warp >= kProducerWarp && warp < kProducerWarp + kProducerWarps) {
-    // =================== gathers ===================================================
-    // Warp pw takes the tile's row groups pw, pw + 4, ... (4 rows each), five gather4 a group,
-    // all from one lane: the lanes of a warp would issue theirs one after the other, each with
-    // its operands moved to uniform registers first.  The warp waits for nothing but stages.
-    const int pw = warp - kProducerWarp;
-    constexpr int kGroupsOf = kNt / 4 / kProducerWarps;
-    int seg = 0, n = 0;
-    bool ok = true;
-    for (; n < n_local && !*abort_s; ++n) {
-      const int at = n % kStages;
-      // stages 1 and 2 hold q until it is in TMEM; later tiles wait for P.V of the stage's last
-      if (n > 0 && !(ok = n >= kStages ? wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1)
-                                       : wait_warp(&bars[kBarQReady], 0)))
-        break;
-      const int first = kNt * ((int)crank + (int)G * n);
-      if (first >= (seg + 1) * kListCap) {      // more valid entries than the list holds
-        if (lane == 0) mbar_arrive(&bars[kBarSegFree]);
-        if (!(ok = wait_warp(&bars[kBarSegFull], seg & 1))) break;
-        ++seg;
-      }
-      const int* rows = list_s + (first - seg * kListCap) + 4 * pw;
-      const uint32_t st = smem_u32(smem + at * kStageBytes);
-      uint64_t* full = &bars[kBarKvFull + at];
-      if (elect_one()) {
-        mbar_arrive_expect_tx(full, kGroupsOf * 4 * kDQK);
-#pragma unroll
-        for (int g = 0; g < kGroupsOf; ++g) {
-          const int y = 4 * (pw + kProducerWarps * g);
-          const int4 rr = *reinterpret_cast<const int4*>(rows + 4 * kProducerWarps * g);
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            tma_gather4(st + m * kBlk + y * 128, &tmap_lat, 128 * m, rr.x, rr.y, rr.z, rr.w, full);
-          tma_gather4(st + 4 * kBlk + y * 64, &tmap_rope, kDV, rr.x, rr.y, rr.z, rr.w, full);
-        }
-      }
-      __syncwarp();
-    }
-    if (!ok) fail();
-    // no gather of this CTA may still be landing in shared memory at exit
-    for (int k = n > kStages ? n - kStages : 0; k < n; ++k)
-      if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit)))
-        report_status(p.status, kStatusTimeout);
-  } else if (warp == kRowWarp) {
-    // =================== the rows' scales, and the rest of a long list ==============
-    // Scales are single words anywhere in memory: those of the next four tiles are in flight
-    // while four are published.  A segment of the list begins with a group of four (64 tiles,
-    // dealt to at most 8 CTAs).
-    constexpr int kAhead = 4, kPer = kNt / 32;
-    static_assert(kListCap / kNt % (8 * kAhead) == 0, "segments begin with a group");
-    float cur[kAhead][kPer], nxt[kAhead][kPer];
-    int seg = 0, j = seg_s[0], ord = seg_s[1];   // the next segment's first round, entries before it
-    bool ok = true;
-    auto load4 = [&](int n0, float (&v)[kAhead][kPer]) {
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        const int* rows = list_s + kNt * ((int)crank + (int)G * (n0 + d)) - seg * kListCap + lane;
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          const int row = n0 + d < n_local ? rows[32 * u] : kp.num_rows;
-          v[d][u] = row < kp.num_rows ? __ldg(kp.qp.scales + div_by(row, kp.gr_mul, kp.gr_shift)) : 0.f;
-        }
-      }
-    };
-    load4(0, cur);
-#pragma unroll 1
-    for (int n0 = 0; n0 < n_local && ok && !*abort_s; n0 += kAhead) {
-      const int first = kNt * ((int)crank + (int)G * (n0 + kAhead));
-      const bool more = n0 + kAhead < n_local, turn = more && first >= (seg + 1) * kListCap;
-      if (more && !turn) load4(n0 + kAhead, nxt);
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d) {
-        const int n = n0 + d, at = n % kStages;
-        if (n >= n_local || !ok) break;
-        if (n >= kStages && !(ok = wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1))) break;
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          // (a row that does not exist has scale 0: weight 0)
-          const int y = at * kNt + lane + 32 * u;
-          float* rp = reinterpret_cast<float*>(rows_s) + 4 * (y >> 1) + (y & 1);
-          rp[0] = cur[d][u];
-          rp[2] = __log2f(cur[d][u]);
-          inv_s[y] = cur[d][u] > 0.f ? __frcp_rn(cur[d][u]) : 0.f;
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarRows + at]);
-      }
-      if (turn && ok) {
-        // once the producers have issued the segment's last tile, the next segment takes its
-        // place (they only wait for tiles that are published by now)
-        if (!(ok = wait_warp(&bars[kBarSegFree], seg & 1))) break;
-        ++seg;
-        const int base = seg * kListCap;
-#pragma unroll 1
-        while (j < p.top_k) {
-          int pos[8], row[8], to = ord;
-          load8(idx, j, p.top_k, lane, pos);
-          resolve8<kInterleaved>(kp, pos, sel, bt_row, false, row);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const unsigned mask = __ballot_sync(0xffffffffu, row[k] >= 0);
-            const int o = to + __popc(mask & lanemask_lt()) - base;
-            if (row[k] >= 0 && o >= 0 && o < kListCap) list_s[o] = row[k];
-            to += __popc(mask);
-          }
-          if (to > base + kListCap) break;       // the round goes on in the segment after
-          ord = to;
-          j += 256;
-        }
-        for (int o = total - base + lane; o < min(n_tiles * kNt - base, kListCap); o += 32) list_s[o] = kp.num_rows;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars[kBarSegFull]);
-        load4(n0 + kAhead, nxt);
-      }
-#pragma unroll
-      for (int d = 0; d < kAhead; ++d)
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) cur[d][u] = nxt[d][u];
-    }
-    if (!ok) fail();
-  } else if (warp == kQkWarp || warp == kPvWarp) {
-    // =================== tcgen05 MMA issue: QK^T (warp 8) and P.V (warp 9) ========
-    // (the whole warp walks the tiles and waits; one lane issues)
-    if (n_local > 0) {
-      bool ok = true;
-      const uint32_t st0 = smem_u32(smem);
-      if (warp == kQkWarp) {
-        // test hook: a wait that cannot complete, so the wait limit runs out
-        ok = !p.stall || wait_warp(&bars[kBarNever], 0);
-        ok = ok && wait_warp(&bars[kBarQReady], 0);
-        tc_fence_after();
-        constexpr uint32_t id = idesc_e4m3(128, kNt, 0, 0);
-        int s = 0;
-        uint32_t full = 0;
-        for (int n = 0; ok && n < n_local && !*abort_s; ++n) {
-          const int sb = kSBufs == 2 ? n & 1 : 0;
-          if (!(ok = wait_warp(&bars[kBarKvFull + s], full))) break;
-          // the score buffer is free once the softmax has read the tile before from it
-          if (n >= kSBufs && !(ok = wait_warp(&bars[kBarSFree + sb], (kSBufs == 2 ? (n >> 1) - 1 : n - 1) & 1))) break;
-          tc_fence_after();
-          const uint32_t st = st0 + s * kStageBytes;
-          const uint32_t d = tmem + (sb ? kColS1 : kColS);
-          if (elect_one()) {
-            const uint32_t b0 = desc_lo(st, 16);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-              mma8_ts<desc_hi(1024, kSwizzle128)>(d, tmem + kColQ + 8 * k, b0 + (((k >> 2) * kBlk + (k & 3) * 32) >> 4),
-                                                  id, k > 0);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma8_ts<desc_hi(512, kSwizzle64)>(d, tmem + kColQ + 128 + 8 * k, b0 + ((4 * kBlk + k * 32) >> 4), id, 1);
-            mma_commit(&bars[kBarSFull + sb]);
-          }
-          __syncwarp();
-          if (++s == kStages) { s = 0; full ^= 1; }
-        }
-      } else {
-        // A = E^T: columns 128m..128m+127 of 32 tile rows, MN-major (one SW128 atom wide);
-        // B = P^T: NH heads x 32 rows, K-major.  The four blocks' accumulators alternate.
-        constexpr uint32_t id = idesc_e4m3(128, NH, 1, 0);
-        int s = 0;
-        for (int n = 0; ok && n < n_local && !*abort_s; ++n) {
-          const int bb = n & 1;
-          if (!(ok = wait_warp(&bars[kBarPReady + bb], (n >> 1) & 1))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t a0 = desc_lo(st0 + s * kStageBytes, kBlk);
-            const uint32_t b0 = desc_lo(st0 + kOffP + 2 * bb * kPBytes, 16);
-#pragma unroll
-            for (int k = 0; k < kNt / 32; ++k)
-#pragma unroll
-              for (int part = 0; part < 2; ++part)
-#pragma unroll
-                for (int m = 0; m < 4; ++m)
-                  mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128)>(
-                      tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPBytes + 32 * k) >> 4), id,
-                      (k > 0 || part > 0) ? 1u : (n > 0 ? 1u : 0u));
-            mma_commit(&bars[kBarKvEmpty + s]);
-            mma_commit(&bars[kBarPFree + bb]);
-            if (n == n_local - 1) mma_commit(&bars[kBarPvFinal]);
-          }
-          __syncwarp();
-          if (++s == kStages) s = 0;
-        }
-      }
-      if (!ok) fail();
-      // every MMA this warp issued has completed before TMEM is released
-      // (the same lane is elected every time: a commit covers its thread's MMAs)
-      uint64_t* fin_bar = &bars[warp == kQkWarp ? kBarMmaFin : kBarMmaFin2];
-      if (elect_one()) mma_commit(fin_bar);
-      __syncwarp();
-      if (!__all_sync(0xffffffffu, mbar_wait(fin_bar, 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
     }
   }
 
