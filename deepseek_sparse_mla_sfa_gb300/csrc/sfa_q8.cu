@@ -88,7 +88,7 @@ static_assert(kBlk % 1024 == 0 && kStageBytes % 1024 == 0 && kOffP % 1024 == 0, 
 static_assert(kOffBar % 8 == 0 && kOffScale % 16 == 0, "alignment");
 static_assert(2048 * kGroupHeads <= kStages * kStageBytes, "the cluster merge fits in the stages");
 // q on its way to TMEM, in stages 1 and 2: 64 rows of 576 bf16, then in place 576 hi and 576 lo bytes
-constexpr int kQPitch = 1168;  // an odd number of 16-byte words: rows start in different banks
+constexpr int kQPitch = 2 * kDQK;
 constexpr int kOffTmp = kStageBytes + kGroupHeads * kQPitch;   // behind it: the resolved list before its compaction
 constexpr int kTmpCap = (kStages * kStageBytes - kOffTmp) / 4;
 static_assert(kTmpCap >= 8192, "q and a list of 8192 entries fit in stages 1 and 2");
@@ -97,6 +97,9 @@ static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscBytes, "misc");
 constexpr long long kDrainLimit = 1LL << 40;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColQ = 0, kColS = 160, kColO = 256, kColS1 = 400;   // S1 for up to 32 heads
+
+// 16-byte word w of a converted row of q: moved so that eight rows' are in different banks
+__device__ __forceinline__ int q_word(int row, int w) { return w ^ (w < 32 ? row & 7 : row & 3); }
 
 struct Q8Params {
   DecodeQ8Params qp;
@@ -303,15 +306,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   int pos_r[8];
   if (warp >= kSoftWarps && warp < kFixWarp) load8(idx, c_begin, c_end, lane, pos_r);
   char* const qst = smem + kStageBytes;
-  if (warp == 0) {
-    if (lane == 0) {
-      mbar_init(&bars[kBarQLoad], 1);
-      fence_barrier_init();
-      mbar_arrive_expect_tx(&bars[kBarQLoad], (uint32_t)nh * kDQK * 2);
-    }
-    __syncwarp();
-    for (int hd = lane; hd < nh; hd += 32)
-      bulk_load_g2s(smem_u32(qst + hd * kQPitch), qsrc + (size_t)hd * 72, kDQK * 2, &bars[kBarQLoad]);
+  if (threadIdx.x == 0) {
+    mbar_init(&bars[kBarQLoad], 1);
+    fence_barrier_init();
+    mbar_arrive_expect_tx(&bars[kBarQLoad], (uint32_t)nh * kQPitch);
+    bulk_load_g2s(smem_u32(qst), qsrc, (uint32_t)nh * kQPitch, &bars[kBarQLoad]);
   }
   if (threadIdx.x == 64) {
     for (int s = 0; s < kStages; ++s) {
@@ -671,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           lo[i] = e4m3x2_h(__hmul2(__hsub2(v, half2_of(hi[i])), __floats2half2_rn(16.f, 16.f)));
         }
         if (lane + 32 * k < 72) {
-          char* to = at + 8 * (lane + 32 * k);
+          char* to = at + 16 * q_word(hd, (lane + 32 * k) >> 1) + 8 * (lane & 1);
           *reinterpret_cast<uint2*>(to) = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
           *reinterpret_cast<uint2*>(to + kDQK) = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
         }
@@ -679,13 +678,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     named_barrier(1, 32 * kQWarps);
     const int quad = warp & 3;
-    const char* mine = qst + (16 * quad + (lane & 15)) * kQPitch + (lane >= 16 ? kDQK : 0);
+    const int row = 16 * quad + (lane & 15);
+    const char* mine = qst + row * kQPitch + (lane >= 16 ? kDQK : 0);
 #pragma unroll 1
     for (int c = wq >> 2; c < 9 && quad < HB; c += kQWarps / 4) {     // 64 columns of q are 16 columns of TMEM
       uint32_t v[16];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const uint4 x = *reinterpret_cast<const uint4*>(mine + 64 * c + 16 * k);
+        const uint4 x = *reinterpret_cast<const uint4*>(mine + 16 * q_word(row, 4 * c + k));
         v[4 * k] = x.x; v[4 * k + 1] = x.y; v[4 * k + 2] = x.z; v[4 * k + 3] = x.w;
       }
       tmem_st16(tmem + ((uint32_t)(quad * 32) << 16) + kColQ + 16 * c, v);
@@ -878,17 +878,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (have_o) tmem_ld_wait();
 #pragma unroll
       for (int k = 0; k < 16; ++k) f[k] = have_o ? __uint_as_float(o[k]) * f[k] : 0.f;
-      const size_t at = out_at + (size_t)hb * kDV + 128 * m + 32 * (warp & 3) + lane;
-      if (kp.qp.out_bf16) {
-        __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+      // two columns of a head a store: even lanes take heads hb .. + 7, odd lanes the other 8
+      const int odd = lane & 1, hd = hb + 8 * odd;
+      const size_t at = out_at + (size_t)hd * kDV + 128 * m + 32 * (warp & 3) + (lane & 30);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (hb + k < nh) to[k * kDV] = __float2bfloat16_rn(f[k]);
-      } else {
-        float* to = p.out + at;
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-          if (hb + k < nh) to[k * kDV] = f[k];
+      for (int k = 0; k < 8; ++k) {
+        const float got = __shfl_xor_sync(0xffffffffu, odd ? f[k] : f[k + 8], 1);
+        const float2 v = odd ? make_float2(got, f[k + 8]) : make_float2(f[k], got);
+        if (hd + k >= nh) continue;
+        if (kp.qp.out_bf16)
+          *reinterpret_cast<__nv_bfloat162*>(reinterpret_cast<__nv_bfloat16*>(p.out) + at + k * kDV) =
+              __floats2bfloat162_rn(v.x, v.y);
+        else
+          *reinterpret_cast<float2*>(p.out + at + k * kDV) = v;
       }
     }
     tc_fence_before();
