@@ -641,19 +641,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 3; ++k)
         x[k] = hd < nh && lane + 32 * k < 72 ? *reinterpret_cast<const uint4*>(at + 16 * (lane + 32 * k))
                                              : make_uint4(0, 0, 0, 0);
-      uint32_t am = 0;
+      uint32_t am2 = 0;                       // magnitudes of both halves
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
-        const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) am = max(am, max(w[i] & 0x7fffu, (w[i] >> 16) & 0x7fffu));
+        am2 = __vimax3_u16x2(am2, x[k].x & 0x7fff7fffu, x[k].y & 0x7fff7fffu);
+        am2 = __vimax3_u16x2(am2, x[k].z & 0x7fff7fffu, x[k].w & 0x7fff7fffu);
       }
-      am = __reduce_max_sync(0xffffffffu, am);
+      const uint32_t am = __reduce_max_sync(0xffffffffu, max(am2 & 0xffffu, am2 >> 16));
       const bool bad = am >= 0x7f80u;       // an infinity or NaN: the head's result is NaN
       // 2^ke: the least power of two with amax / 2^ke <= 448
       int ke = (int)(am >> 7) - 135 + ((am & 0x7f) > 0x60 ? 1 : 0);
       ke = am < 0x80u || bad ? 0 : max(ke, -100);
-      const float down = bad ? 0.f : (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
+      const float down = (p.scale < 0.f ? -1.f : 1.f) * __int_as_float((127 - ke) << 23);
       if (lane == 0)
         qc_s[hd] = bad ? __int_as_float(0x7fc00000)
                        : fmaxf(fabsf(p.scale) * kLog2e * __int_as_float((127 + ke) << 23), 1e-30f);
@@ -665,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
           // a scaled value has 8 bits below 2^9: f16 holds it (to 2^-24, below lo's 2^-13)
           const float a = __uint_as_float(w[i] << 16), c = __uint_as_float(w[i] & 0xffff0000u);
-          const __half2 v = __floats2half2_rn(bad ? 0.f : a * down, bad ? 0.f : c * down);
+          const __half2 v = __floats2half2_rn(a * down, c * down);
           hi[i] = e4m3x2_h(v);
           lo[i] = e4m3x2_h(__hmul2(__hsub2(v, half2_of(hi[i])), __floats2half2_rn(16.f, 16.f)));
         }
