@@ -37,7 +37,7 @@ OUT_BF16 = 2                # sfa_decode_q8 flag: out is bf16
 __all__ = ["decode", "lse_merge", "decode_host", "decode_host_staging_bytes",
            "workspace_bytes", "decode_noalloc", "decode_launches", "last_device_status", "set_kernel_path",
            "set_wait_limit", "set_stall_injection", "kv_write", "uv_proj", "topk", "HostPlan",
-           "decode_q8", "decode_q8_workspace_bytes", "kv_write_q8", "kv_write_q8_workspace_bytes", "step_plan",
+           "decode_q8", "kv_write_q8", "kv_write_q8_workspace_bytes", "step_plan",
            "rope", "rope_inv_freq", "rope_mscale",
            "SfaError", "D_QK", "D_V", "BLOCK_TABLE_PER_TOKEN"]
 
@@ -396,10 +396,6 @@ def topk(scores, k: int, seq_lens=None, Q: int = 1, S: Optional[int] = None, out
     return out
 
 
-def decode_q8_workspace_bytes(B: int, Q: int, h: int, top_k: int, n_splits: int) -> int:
-    return int(_lib.load().sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits))
-
-
 def _need_cache_q8(kv8, scales):
     """The checks of an 8-bit cache [num_blocks, block_size, 576] and its scales [num_blocks,
     block_size / group]; returns (num_blocks, block_size, group)."""
@@ -419,7 +415,7 @@ def _need_cache_q8(kv8, scales):
 
 
 def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_splits: int = 1, Q: int = 1,
-              merge: bool = True, out=None, lse=None, out_part=None, lse_part=None, workspace=None, stream=None,
+              merge: bool = True, out=None, lse=None, out_part=None, lse_part=None, stream=None,
               interleave: int = 0, block_table_per_token: bool = False, out_dtype=torch.float32):
     """Sparse MLA decode over an 8-bit latent cache (C ABI ``sfa_decode_q8``).
 
@@ -453,7 +449,7 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
     lib = _lib.load()
     final = n_splits == 1 or merge
-    out_p = lse_p = op_p = lp_p = ws_p = ws_bytes = 0
+    out_p = lse_p = op_p = lp_p = 0
     with _on(dev, stream):
         if final:
             if out is None:
@@ -479,20 +475,12 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
             _check(out_part, "out_part", torch.float32, dev, 4)
             _check(lse_part, "lse_part", torch.float32, dev, 3)
             op_p, lp_p = out_part.data_ptr(), lse_part.data_ptr()
-        if workspace is None:
-            need = lib.sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits)
-            if need:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be contiguous and on {dev}")
-        if workspace is not None:
-            ws_p, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         flags = (BLOCK_TABLE_PER_TOKEN if block_table_per_token else 0) | \
                 (OUT_BF16 if final and out_dtype is torch.bfloat16 else 0)
         code = lib.sfa_decode_q8(q.data_ptr(), kv8.data_ptr(), scales.data_ptr(), group, block_table.data_ptr(),
                                  seq_lens.data_ptr(), topk_idx.data_ptr(), B, Q, h, top_k, num_blocks, block_size,
-                                 max_blocks, scale, n_splits, interleave, flags, out_p, lse_p, op_p, lp_p, ws_p,
-                                 ws_bytes, _raw_stream(dev))
+                                 max_blocks, scale, n_splits, interleave, flags, out_p, lse_p, op_p, lp_p,
+                                 _raw_stream(dev))
     if code:
         _lib.check("sfa_decode_q8", code)
     return (out, lse) if final else (out_part, lse_part)

@@ -47,8 +47,7 @@ SIGNATURES = {
     "sfa_host_plan_create": ([P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, P, P, SZ, P], I),
     "sfa_host_plan_launch": ([P, P], I),
     "sfa_host_plan_destroy": ([P], None),
-    "sfa_decode_q8_workspace_bytes": ([I, I, I, I, I], SZ),
-    "sfa_decode_q8": ([P, P, P, I, P, P, P, I, I, I, I, I, I, I, F, I, I, I, P, P, P, P, P, SZ, P], I),
+    "sfa_decode_q8": ([P, P, P, I, P, P, P, I, I, I, I, I, I, I, F, I, I, I, P, P, P, P, P], I),
     "sfa_kv_write_q8_workspace_bytes": ([LL, I], SZ),
     "sfa_kv_write_q8": ([P, P, LL, I, P, P, I, P, SZ, P], I),
     "sfa_step_plan": ([P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P], I),

@@ -478,16 +478,11 @@ sfa_status sfa_topk(const float* scores, long long row_stride, const int32_t* se
              : SFA_ERR_CUDA;
 }
 
-size_t sfa_decode_q8_workspace_bytes(int B, int Q, int h, int top_k, int n_splits) {
-  (void)B; (void)Q; (void)h; (void)top_k; (void)n_splits;
-  return 0;
-}
-
 sfa_status sfa_decode_q8(const void* q, const void* kv8, const float* scales, int group, const int32_t* block_table,
                          const int32_t* seq_lens, const int32_t* topk_idx, int B, int Q, int h, int top_k,
                          int num_blocks, int block_size, int max_blocks_per_seq, float scale, int n_splits,
                          int interleave_size, int flags, void* out, float* lse, float* out_part, float* lse_part,
-                         void* workspace, size_t workspace_bytes, sfa_stream stream) {
+                         sfa_stream stream) {
   sfa_status st = check_decode_args(q, kv8, block_table, seq_lens, topk_idx, B, Q, h, top_k, num_blocks, block_size,
                                     max_blocks_per_seq, scale, n_splits);
   if (st != SFA_OK) return st;
@@ -506,11 +501,6 @@ sfa_status sfa_decode_q8(const void* q, const void* kv8, const float* scales, in
     if ((out && !lse) || (!out && lse)) return SFA_ERR_INVALID_ARG;
   }
   if (out && (!aligned(out, 16) || !aligned(lse, 4))) return SFA_ERR_INVALID_ARG;
-  const size_t need = sfa_decode_q8_workspace_bytes(B, Q, h, top_k, n_splits);
-  if (need == 0 || !workspace || workspace_bytes < need || !aligned(workspace, 256)) {
-    workspace = nullptr;
-    workspace_bytes = 0;
-  }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SFA_ERR_CUDA;
   int* status = status_word(dev);
@@ -535,8 +525,6 @@ sfa_status sfa_decode_q8(const void* q, const void* kv8, const float* scales, in
   p.n_splits = n_splits;
   p.out = n_splits == 1 ? static_cast<float*>(out) : out_part;
   p.lse = n_splits == 1 ? lse : lse_part;
-  p.workspace = workspace;
-  p.workspace_bytes = workspace_bytes;
   p.status = status;
   const long long wl = g_wait_limit.load();
   p.wait_limit = wl > 0 ? wl : kDefaultWaitLimit;

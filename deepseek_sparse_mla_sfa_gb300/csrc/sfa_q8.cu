@@ -95,6 +95,8 @@ static_assert(kTmpCap >= 8192, "q and a list of 8192 entries fit in stages 1 and
 static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscBytes, "misc");
 
 constexpr long long kDrainLimit = 1LL << 40;
+constexpr uint64_t kLanded = 100000000ull;   // ns: copies in flight have landed long before (a tile that was given up
+                                             // half issued never completes its barrier)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColQ = 0, kColS = 160, kColO = 256, kColS1 = 400;   // S1 for up to 32 heads
 
@@ -186,6 +188,11 @@ __device__ __forceinline__ __half2 half2_of(uint32_t codes) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
   return *reinterpret_cast<__half2*>(&r);
 }
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // entries j0 + 32 k + lane < c_end (k < 8) of the selected list, -1 behind its end
 __device__ __forceinline__ void load8(const int32_t* idx, int j0, int c_end, int lane, int (&pos)[8]) {
@@ -304,7 +311,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int chunk = ((p.top_k + kListWarps * 32 - 1) / (kListWarps * 32)) * 32;
   const int c_begin = min((warp - kSoftWarps) * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
   int pos_r[8];
-  if (warp >= kSoftWarps && warp < kFixWarp) load8(idx, c_begin, c_end, lane, pos_r);
+  // (a list of one round, 8 entries a lane, is loaded to registers, a longer one to shared
+  // memory, where each warp then compacts its part in place; the longest come round by round)
+  const bool one_round = chunk <= 256, staged = !one_round && kListWarps * chunk <= kTmpCap;
+  int* const tmp = reinterpret_cast<int*>(smem + kOffTmp) + (warp - kSoftWarps) * chunk;
+  if (warp >= kSoftWarps && warp < kFixWarp) {
+    if (one_round) load8(idx, c_begin, c_end, lane, pos_r);
+    if (staged)
+      for (int j = c_begin + lane; j < c_end; j += 32) cp_async4(smem_u32(tmp + j - c_begin), idx + j);
+  }
   char* const qst = smem + kStageBytes;
   if (threadIdx.x == 0) {
     mbar_init(&bars[kBarQLoad], 1);
@@ -352,8 +367,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = *tmem_base_s;
 
   // ---- index resolution (warps 8-15): count per warp chunk, then ordered compaction ----
-  // (rounds of 8 entries a lane; one round stays in registers, more go to a temporary list a
-  // warp, in the part of stage 2 that q leaves free)
   int total = 0;
   int n_tiles = 0, n_local = 0;
   auto count_tiles = [&]() {
@@ -379,8 +392,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   // before (the instruction cache is cold at every launch).
   if (warp >= kSoftWarps && warp < kFixWarp) {
     int row_r[8], cnt = 0;
-    const bool keep = kListWarps * chunk <= kTmpCap;      // longer lists are resolved a second time
-    int* tmp = reinterpret_cast<int*>(smem + kOffTmp) + (warp - kSoftWarps) * chunk;
     auto compact = [&](int* to, int at, int cap) {        // this round's rows from to[at] on; returns the next place
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
@@ -391,14 +402,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return at;
     };
+    if (staged) cp_wait_all();
 #pragma unroll 1
     for (int j0 = c_begin; j0 < c_end; j0 += 256) {
-      int pos[8];
+      if (staged) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) pos[k] = pos_r[k];
-      load8(idx, j0 + 256, c_end, lane, pos_r);           // the next round's entries are in flight
-      const int mine = resolve8<kInterleaved>(kp, pos, sel, bt_row, crank == 0 && hg == 0, row_r);
-      if (keep && chunk > 256) cnt = compact(tmp, cnt, kTmpCap); else cnt += __reduce_add_sync(0xffffffffu, mine);
+        for (int k = 0; k < 8; ++k) {
+          const int j = j0 + 32 * k + lane;
+          pos_r[k] = j < c_end ? tmp[j - c_begin] : -1;       // what this lane copied
+        }
+      } else if (!one_round) {
+        load8(idx, j0, c_end, lane, pos_r);
+      }
+      const int mine = resolve8<kInterleaved>(kp, pos_r, sel, bt_row, crank == 0 && hg == 0, row_r);
+      if (staged) cnt = compact(tmp, cnt, chunk); else cnt += __reduce_add_sync(0xffffffffu, mine);
     }
     if (lane == 0) wcount_s[warp - kSoftWarps] = cnt;
     named_barrier(4, 32 * kListWarps);
@@ -409,9 +426,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (w < warp - kSoftWarps) off += c;
       total += c;
     }
-    if (chunk <= 256) {
+    if (one_round) {
       if (c_begin < c_end) compact(list_s, off, kListCap);
-    } else if (keep && total <= kListCap) {
+    } else if (staged && total <= kListCap) {
       for (int o = lane; o < cnt; o += 32) list_s[off + o] = tmp[o];
     } else {
 #pragma unroll 1
@@ -476,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail();
       // no gather of this CTA may still be landing in shared memory at exit
       for (int k = n > kStages ? n - kStages : 0; k < n; ++k)
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit)))
+        if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit, kLanded)))
           report_status(p.status, kStatusTimeout);
     } else if (warp == kRowWarp) {
       // =================== the rows' scales, and the rest of a long list ==============

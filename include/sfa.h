@@ -234,26 +234,26 @@ sfa_status sfa_uv_proj(const float *out, const void *w_uv, void *y, int T, int h
  * s is e4m3(kv8[s, c]) * scales[s / group], and with it every formula is sfa_decode's.
  *
  *   kv8         device, e4m3 bytes [num_blocks, block_size, 576]; 16-byte aligned
- *   scales      device, fp32 [num_blocks, block_size / group], finite, positive (sfa_kv_write_q8
- *               writes powers of two; any others are taken as they are)
+ *   scales      device, fp32 [num_blocks, block_size / group], in [2^-100, 2^120]
+ *               (sfa_kv_write_q8 writes powers of two; any others are taken as they are)
  *   group       slots per scale: >= 1, divides block_size
  *   interleave_size, flags  as in sfa_decode_ex; SFA_OUT_BF16: `out` is bf16 [B*Q, h, 512]
  *               (16-byte aligned) instead of fp32.  lse and the shard partials are fp32.
- *   workspace   optional, as in sfa_decode (sfa_decode_q8_workspace_bytes)
  *   num_blocks * block_size <= INT_MAX (SFA_ERR_UNSUPPORTED above).
  * Everything else, and the return codes, as in sfa_decode_ex.
  *
- * Accuracy: lse carries fp32 rounding only (q is exact to 2^-18 of its head's largest value);
+ * Accuracy: lse carries fp32 rounding only (q is exact to 2^-22 of its head's largest value);
  * out, whatever its type, carries the rounding of the softmax weights to 8 significant bits,
- * about 2^-9 of its norm (as sfa_decode's bf16 weights do), and then that of its own type.
+ * about 2^-10 of its norm (as sfa_decode's bf16 weights do), and then that of its own type.  A
+ * NaN or infinity in a head of q makes that head's out and lse NaN.
+ * sfa_set_kernel_path(1) selects a CUDA-core kernel here too, any other path the tensor cores'.
  */
 #define SFA_OUT_BF16 2
-size_t sfa_decode_q8_workspace_bytes(int B, int Q, int h, int top_k, int n_splits);
 sfa_status sfa_decode_q8(const void *q, const void *kv8, const float *scales, int group,
                          const int32_t *block_table, const int32_t *seq_lens, const int32_t *topk_idx, int B, int Q,
                          int h, int top_k, int num_blocks, int block_size, int max_blocks_per_seq, float scale,
                          int n_splits, int interleave_size, int flags, void *out, float *lse, float *out_part,
-                         float *lse_part, void *workspace, size_t workspace_bytes, sfa_stream stream);
+                         float *lse_part, sfa_stream stream);
 
 /*
  * sfa_kv_write_q8 -- sfa_kv_write into the 8-bit latent cache sfa_decode_q8 reads.

@@ -522,8 +522,7 @@ def test_decode_q8_given_buffers_and_refusals():
     assert o is out and l is lse
     _close(o, l, [x[0] for x in _oracle(pr)])
     for bad in (dict(out=out.half()), dict(out=out[:1]), dict(lse=lse[:1]), dict(out_dtype=torch.float16), dict(Q=3),
-                dict(interleave=-1), dict(n_splits=2, out_part=torch.empty((2, 2, 4, 511), device="cuda")),
-                dict(workspace=torch.empty(16, dtype=torch.uint8))):
+                dict(interleave=-1), dict(n_splits=2, out_part=torch.empty((2, 2, 4, 511), device="cuda"))):
         with pytest.raises((TypeError, ValueError)):
             sfa.decode_q8(*d, SCALE, **bad)
     with pytest.raises(sfa.SfaError):
@@ -610,3 +609,38 @@ def test_two_streams_and_a_graph():
         g.replay()
         _close(o, l, [x[0] for x in _oracle(pr)], f"replay {seed}")
     assert sfa.last_device_status() == 0
+
+
+# ------------------------------------------------------------------- bounded waits
+@pytest.mark.parametrize("h,n,B,k", [(4, 1, 2, 600), (64, 1, 3, 600), (128, 2, 2, 900), (64, 1, 160, 200), (30, 1, 1, 7000)])
+def test_decode_q8_reports_a_wait_that_runs_out_and_recovers(h, n, B, k):
+    # the score issuer first waits on a barrier that nothing completes: the call reports the
+    # timeout, every warp leaves, and the next call is right
+    pr = _problem(50 + h, B, 1, h, max(k, 300), k, bs=16, group=16)
+    d = _device(pr)
+    limit, stall = sfa.set_wait_limit(200), sfa.set_stall_injection(True)
+    try:
+        sfa.decode_q8(*d, SCALE, n_splits=n)
+        assert sfa.last_device_status() == TIMEOUT
+    finally:
+        sfa.set_wait_limit(limit)
+        sfa.set_stall_injection(stall)
+    _close(*sfa.decode_q8(*d, SCALE, n_splits=n), [x[0] for x in _oracle(pr)])
+    assert sfa.last_device_status() == 0
+
+
+def test_decode_q8_with_waits_of_a_few_polls():
+    # any wait may give up: a call reports a timeout or is right
+    pr = _problem(61, 4, 1, 64, 900, 700)
+    d, want = _device(pr), [x[0] for x in _oracle(pr)]
+    for polls in (1, 2, 5, 20, 100, 1000):
+        limit = sfa.set_wait_limit(polls)
+        try:
+            out, lse = sfa.decode_q8(*d, SCALE)
+            status = sfa.last_device_status()
+        finally:
+            sfa.set_wait_limit(limit)
+        assert status in (0, TIMEOUT)
+        if status == 0:
+            _close(out, lse, want, f"{polls} polls")
+    _close(*sfa.decode_q8(*d, SCALE), want)

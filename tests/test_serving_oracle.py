@@ -128,7 +128,7 @@ def _decode_q8(lib, **kw):
     a.update(kw)
     return lib.sfa_decode_q8(a["q"], a["kv"], a["sc"], a["g"], a["bt"], a["sl"], a["idx"], a["B"], a["Q"], a["h"],
                              a["k"], a["nb"], a["bs"], a["mb"], a["scale"], a["n"], a["il"], a["flags"], a["out"],
-                             a["lse"], a["op"], a["lp"], P0, 0, P0)
+                             a["lse"], a["op"], a["lp"], P0)
 
 
 @pytest.mark.parametrize("kw,code", [
