@@ -69,9 +69,12 @@ def _raw_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _check(t, name, dtype, dev, ndim):
+_BF16, _F32, _F64, _I32, _E4M3 = (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.float8_e4m3fn)
+
+
+def _check(t, name, dtype, dev, ndim, isinstance=isinstance, Tensor=torch.Tensor):
     """_need on a CUDA device, quick where nothing is wrong."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index and t.dim() == ndim
+    if not (isinstance(t, Tensor) and t.dtype is dtype and t.get_device() == dev.index and t.dim() == ndim
             and t.is_contiguous()):
         _need(t, name, dtype, dev, ndim)
 
@@ -399,8 +402,11 @@ def topk(scores, k: int, seq_lens=None, Q: int = 1, S: Optional[int] = None, out
 def _need_cache_q8(kv8, scales):
     """The checks of an 8-bit cache [num_blocks, block_size, 576] and its scales [num_blocks,
     block_size / group]; returns (num_blocks, block_size, group)."""
-    _need(kv8, "kv8", torch.float8_e4m3fn, None, 3)
-    _need(scales, "scales", torch.float32, None, 2)
+    if not (isinstance(kv8, torch.Tensor) and kv8.dtype is _E4M3 and kv8.dim() == 3 and kv8.is_contiguous()
+            and isinstance(scales, torch.Tensor) and scales.dtype is _F32 and scales.dim() == 2
+            and scales.is_contiguous()):
+        _need(kv8, "kv8", _E4M3, None, 3)
+        _need(scales, "scales", _F32, None, 2)
     nb, bs, d = kv8.shape
     if d != D_QK:
         raise ValueError("kv8 rows must have 576 columns")
@@ -426,10 +432,10 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
     """
     num_blocks, block_size, group = _need_cache_q8(kv8, scales)
     dev = kv8.device
-    _check(q, "q", torch.bfloat16, dev, 3)
-    _check(block_table, "block_table", torch.int32, dev, 2)
-    _check(seq_lens, "seq_lens", torch.int32, dev, 1)
-    _check(topk_idx, "topk_idx", torch.int32, dev, 2)
+    _check(q, "q", _BF16, dev, 3)
+    _check(block_table, "block_table", _I32, dev, 2)
+    _check(seq_lens, "seq_lens", _I32, dev, 1)
+    _check(topk_idx, "topk_idx", _I32, dev, 2)
     T, h, d = q.shape
     if d != D_QK:
         raise ValueError("q rows must have 576 columns")
@@ -445,7 +451,7 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
         raise ValueError("interleave must be >= 0")
     if out is not None:
         out_dtype = out.dtype
-    if out_dtype is not torch.float32 and out_dtype is not torch.bfloat16:
+    if out_dtype is not _F32 and out_dtype is not _BF16:
         raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
     lib = _lib.load()
     final = n_splits == 1 or merge
@@ -459,24 +465,24 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
             else:
                 _check(out, "out", out_dtype, dev, 3)
             if lse is None:
-                lse = torch.empty((T, h), dtype=torch.float32, device=dev)
+                lse = torch.empty((T, h), dtype=_F32, device=dev)
             elif lse.shape != (T, h):
                 raise ValueError(f"out must be [{T}, {h}, {D_V}] and lse [{T}, {h}]")
             else:
-                _check(lse, "lse", torch.float32, dev, 2)
+                _check(lse, "lse", _F32, dev, 2)
             out_p, lse_p = out.data_ptr(), lse.data_ptr()
         if n_splits > 1:
             if out_part is None:
-                out_part = torch.empty((n_splits, T, h, D_V), dtype=torch.float32, device=dev)
+                out_part = torch.empty((n_splits, T, h, D_V), dtype=_F32, device=dev)
             if lse_part is None:
-                lse_part = torch.empty((n_splits, T, h), dtype=torch.float32, device=dev)
+                lse_part = torch.empty((n_splits, T, h), dtype=_F32, device=dev)
             if out_part.shape != (n_splits, T, h, D_V) or lse_part.shape != (n_splits, T, h):
                 raise ValueError(f"out_part must be [{n_splits}, {T}, {h}, {D_V}] and lse_part [{n_splits}, {T}, {h}]")
-            _check(out_part, "out_part", torch.float32, dev, 4)
-            _check(lse_part, "lse_part", torch.float32, dev, 3)
+            _check(out_part, "out_part", _F32, dev, 4)
+            _check(lse_part, "lse_part", _F32, dev, 3)
             op_p, lp_p = out_part.data_ptr(), lse_part.data_ptr()
         flags = (BLOCK_TABLE_PER_TOKEN if block_table_per_token else 0) | \
-                (OUT_BF16 if final and out_dtype is torch.bfloat16 else 0)
+                (OUT_BF16 if final and out_dtype is _BF16 else 0)
         code = lib.sfa_decode_q8(q.data_ptr(), kv8.data_ptr(), scales.data_ptr(), group, block_table.data_ptr(),
                                  seq_lens.data_ptr(), topk_idx.data_ptr(), B, Q, h, top_k, num_blocks, block_size,
                                  max_blocks, scale, n_splits, interleave, flags, out_p, lse_p, op_p, lp_p,
@@ -502,8 +508,8 @@ def kv_write_q8(kv8, scales, slot_mapping, rows, workspace=None, stream=None):
     """
     num_blocks, block_size, group = _need_cache_q8(kv8, scales)
     dev = kv8.device
-    _check(slot_mapping, "slot_mapping", torch.int32, dev, 1)
-    _check(rows, "rows", torch.bfloat16, dev, 2)
+    _check(slot_mapping, "slot_mapping", _I32, dev, 1)
+    _check(rows, "rows", _BF16, dev, 2)
     T, d = rows.shape
     if d != D_QK or T != slot_mapping.shape[0]:
         raise ValueError("rows must be [T, 576] with one slot per row")
@@ -534,11 +540,11 @@ def step_plan(cached_lens, new_lens, block_table, free_blocks, taken, block_size
     dev = block_table.device
     if dev.type != "cuda":
         raise ValueError("step_plan runs on a CUDA device only")
-    _check(block_table, "block_table", torch.int32, dev, 2)
-    _check(cached_lens, "cached_lens", torch.int32, dev, 1)
-    _check(new_lens, "new_lens", torch.int32, dev, 1)
-    _check(free_blocks, "free_blocks", torch.int32, dev, 1)
-    _check(taken, "taken", torch.int32, dev, 1)
+    _check(block_table, "block_table", _I32, dev, 2)
+    _check(cached_lens, "cached_lens", _I32, dev, 1)
+    _check(new_lens, "new_lens", _I32, dev, 1)
+    _check(free_blocks, "free_blocks", _I32, dev, 1)
+    _check(taken, "taken", _I32, dev, 1)
     B, max_blocks = block_table.shape
     if cached_lens.shape[0] != B or new_lens.shape[0] != B or taken.shape[0] != 1:
         raise ValueError("cached_lens and new_lens must be [B], block_table [B, max_blocks] and taken [1]")
@@ -547,11 +553,11 @@ def step_plan(cached_lens, new_lens, block_table, free_blocks, taken, block_size
         raise ValueError("num_tokens must be >= 0")
     with _on(dev, stream):
         # (five allocations take less of the host's time than five views of one)
-        seq_lens = torch.empty(B, dtype=torch.int32, device=dev)
-        start = torch.empty(B + 1, dtype=torch.int32, device=dev)
-        positions = torch.empty(N, dtype=torch.int32, device=dev)
-        slots = torch.empty(N, dtype=torch.int32, device=dev)
-        taken_out = torch.empty(1, dtype=torch.int32, device=dev)
+        seq_lens = torch.empty(B, dtype=_I32, device=dev)
+        start = torch.empty(B + 1, dtype=_I32, device=dev)
+        positions = torch.empty(N, dtype=_I32, device=dev)
+        slots = torch.empty(N, dtype=_I32, device=dev)
+        taken_out = torch.empty(1, dtype=_I32, device=dev)
         code = _lib.load().sfa_step_plan(cached_lens.data_ptr(), new_lens.data_ptr(), B, block_size,
                                          block_table.data_ptr(), max_blocks, free_blocks.data_ptr(),
                                          free_blocks.shape[0], taken.data_ptr(), N, seq_lens.data_ptr(),
@@ -630,8 +636,8 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
         xd = 0
     if xd != 1 or width < 1:
         raise ValueError("x must be [T, n, width] or [T, width] with contiguous columns")
-    _check(positions, "positions", torch.int32, dev, 1)
-    _check(inv_freq, "inv_freq", torch.float64, dev, 1)
+    _check(positions, "positions", _I32, dev, 1)
+    _check(inv_freq, "inv_freq", _F64, dev, 1)
     rot = 2 * inv_freq.shape[0]
     if positions.shape[0] != T:
         raise ValueError("positions must be [T]")

@@ -615,6 +615,7 @@ sfa_status sfa_rope(const void* x, long long x_token_stride, long long x_head_st
     return SFA_ERR_INVALID_ARG;
   if (x == out && (x_token_stride != out_token_stride || x_head_stride != out_head_stride))
     return SFA_ERR_INVALID_ARG;
+  if ((T > 1 && out_token_stride == 0) || (n > 1 && out_head_stride == 0)) return SFA_ERR_INVALID_ARG;   // rows of out must differ
   return sfa::launch_rope(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, dtype, T, n, width,
                           rot_dim, positions, inv_freq, (flags & SFA_ROPE_INTERLEAVED) ? 1 : 0,
                           (flags & SFA_ROPE_INVERSE) ? 1 : 0, mscale,

@@ -333,7 +333,8 @@ sfa_status sfa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, in
  *
  *   x, out      device, element (t, j, d) at t * token_stride + j * head_stride + d (strides in
  *               elements): bf16, fp16 or fp32 (dtype), T tokens of n heads.  out may be x
- *               itself (same strides); otherwise the two must not overlap.
+ *               itself (same strides); otherwise the two must not overlap.  A stride of x may be 0
+ *               (a row shared by tokens or heads), of out only where it is not used.
  *   positions   device int32 [T]; < 0 = padding: that token's rows of out are left as they were
  *   inv_freq    device double [rot_dim / 2]: radians a position
  *   2 <= rot_dim <= SFA_ROPE_MAX_DIM, even, <= width

@@ -172,6 +172,19 @@ def test_rope_strides_offsets_and_padding_rows_of_out():
     assert y2.shape == (9, 64) and torch.equal(y2[1], src[1, 0, :64])
 
 
+def test_rope_of_a_row_shared_by_heads():
+    # x expanded over the heads: every head of out gets the rotated row
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn((7, 1, 32), generator=g).to(torch.float16).cuda()
+    pos, f = i32(range(7)), sfa.rope_inv_freq(32)
+    out = torch.empty((7, 5, 32), dtype=torch.float16, device="cuda")
+    sfa.rope(k.expand(7, 5, 32), pos, f, out=out)
+    one = sfa.rope(k, pos, f)
+    assert torch.equal(out, one.expand(7, 5, 32))
+    with pytest.raises(sfa.SfaError):
+        sfa.rope(out, pos, f, out=torch.empty((7, 1, 32), dtype=torch.float16, device="cuda").expand(7, 5, 32))
+
+
 def test_rope_inverse_is_the_gradient():
     # d/dx sum(g * rope(x)) = rope^T g, against the formula and against differences in fp32
     gen = torch.Generator().manual_seed(6)

@@ -178,13 +178,13 @@ def test_step_plan_argument_checks(lib, kw, code):
     (dict(T=0), 0), (dict(T=-1), -1), (dict(n=0), -1), (dict(rot=0), -1), (dict(rot=7), -1), (dict(rot=66), -1),
     (dict(width=1024, rot=514), -2), (dict(dtype=3), -1), (dict(flags=4), -1), (dict(m=float("inf")), -1),
     (dict(x=P0), -1), (dict(out=P0), -1), (dict(pos=P0), -1), (dict(f=P0), -1), (dict(f=ODD), -1),
-    (dict(x=ODD, dtype=2), -1), (dict(out=FAKE, os=65), -1),
+    (dict(x=ODD, dtype=2), -1), (dict(out=FAKE, os=65), -1), (dict(os=0), -1), (dict(n=2, oh=0), -1),
 ])
 def test_rope_argument_checks(lib, kw, code):
     a = dict(x=FAKE, xs=64, out=ctypes.c_void_p(2 << 20), os=64, dtype=0, T=3, n=1, width=64, rot=64, pos=FAKE, f=FAKE,
-             m=1.0, flags=0)
+             m=1.0, flags=0, oh=64)
     a.update(kw)
-    assert lib.sfa_rope(a["x"], a["xs"], 64, a["out"], a["os"], 64, a["dtype"], a["T"], a["n"], a["width"], a["rot"],
+    assert lib.sfa_rope(a["x"], a["xs"], 64, a["out"], a["os"], a["oh"], a["dtype"], a["T"], a["n"], a["width"], a["rot"],
                         a["pos"], a["f"], a["m"], a["flags"], P0) == code
 
 
