@@ -441,7 +441,7 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
         raise ValueError("q rows must have 576 columns")
     if int(Q) != Q or Q < 1:
         raise ValueError("Q must be an integer >= 1")
-    Q = int(Q)
+    Q, n_splits = int(Q), int(n_splits)
     B = seq_lens.shape[0]
     lists, top_k = topk_idx.shape
     tables, max_blocks = block_table.shape
@@ -471,7 +471,13 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
             else:
                 _check(lse, "lse", _F32, dev, 2)
             out_p, lse_p = out.data_ptr(), lse.data_ptr()
-        if n_splits > 1:
+        if n_splits > 1 and final and out_part is None and lse_part is None:
+            # partials that nobody sees: one buffer for both
+            n = n_splits * T * h
+            parts = torch.empty(n * (D_V + 1), dtype=_F32, device=dev)
+            op_p = parts.data_ptr()
+            lp_p = op_p + 4 * n * D_V
+        elif n_splits > 1:
             if out_part is None:
                 out_part = torch.empty((n_splits, T, h, D_V), dtype=_F32, device=dev)
             if lse_part is None:
@@ -485,7 +491,7 @@ def decode_q8(q, kv8, scales, block_table, seq_lens, topk_idx, scale: float, n_s
                 (OUT_BF16 if final and out_dtype is _BF16 else 0)
         code = lib.sfa_decode_q8(q.data_ptr(), kv8.data_ptr(), scales.data_ptr(), group, block_table.data_ptr(),
                                  seq_lens.data_ptr(), topk_idx.data_ptr(), B, Q, h, top_k, num_blocks, block_size,
-                                 max_blocks, scale, n_splits, interleave, flags, out_p, lse_p, op_p, lp_p,
+                                 max_blocks, float(scale), n_splits, int(interleave), flags, out_p, lse_p, op_p, lp_p,
                                  _raw_stream(dev))
     if code:
         _lib.check("sfa_decode_q8", code)
@@ -558,7 +564,7 @@ def step_plan(cached_lens, new_lens, block_table, free_blocks, taken, block_size
         positions = torch.empty(N, dtype=_I32, device=dev)
         slots = torch.empty(N, dtype=_I32, device=dev)
         taken_out = torch.empty(1, dtype=_I32, device=dev)
-        code = _lib.load().sfa_step_plan(cached_lens.data_ptr(), new_lens.data_ptr(), B, block_size,
+        code = _lib.load().sfa_step_plan(cached_lens.data_ptr(), new_lens.data_ptr(), B, int(block_size),
                                          block_table.data_ptr(), max_blocks, free_blocks.data_ptr(),
                                          free_blocks.shape[0], taken.data_ptr(), N, seq_lens.data_ptr(),
                                          start.data_ptr(), positions.data_ptr(), slots.data_ptr(),
@@ -653,7 +659,7 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
             return out
         os = out.stride()
         code = _lib.load().sfa_rope(x.data_ptr(), xt, xn, out.data_ptr(), os[0], os[1] if len(shape) == 3 else 0,
-                                    dtype, T, n, width, rot, positions.data_ptr(), inv_freq.data_ptr(), mscale,
+                                    dtype, T, n, width, rot, positions.data_ptr(), inv_freq.data_ptr(), float(mscale),
                                     (1 if interleaved else 0) | (2 if inverse else 0), _raw_stream(dev))
     if code:
         _lib.check("sfa_rope", code)
