@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   #pragma unroll
           for (int u = 0; u < kPer; ++u) {
             const int row = n0 + d < n_local ? rows[32 * u] : kp.num_rows;
-            v[d][u] = row < kp.num_rows ? __ldg(kp.qp.scales + div_by(row, kp.gr_mul, kp.gr_shift)) : 0.f;
+            v[d][u] = row < kp.num_rows ? __ldg(kp.qp.scales + div_by(row, kp.gr_mul, kp.gr_shift)) : -1.f;
           }
         }
       };
@@ -529,12 +529,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (n >= kStages && !(ok = wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1))) break;
   #pragma unroll
           for (int u = 0; u < kPer; ++u) {
-            // (a row that does not exist has scale 0: weight 0)
+            // a row that does not exist (-1) has scale 0: weight 0.  One whose group was never
+            // written (0) counts, with values of zero: its scale is the least one, and NaN stays
+            const float c = cur[d][u] < 0.f ? 0.f : cur[d][u] < 0x1p-100f ? 0x1p-100f : cur[d][u];
             const int y = at * kNt + lane + 32 * u;
             float* rp = reinterpret_cast<float*>(rows_s) + 4 * (y >> 1) + (y & 1);
-            rp[0] = cur[d][u];
-            rp[2] = __log2f(cur[d][u]);
-            inv_s[y] = cur[d][u] > 0.f ? __frcp_rn(cur[d][u]) : 0.f;
+            rp[0] = c;
+            rp[2] = __log2f(c);
+            inv_s[y] = c > 0.f ? __frcp_rn(c) : 0.f;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarRows + at]);

@@ -449,6 +449,21 @@ def test_decode_q8_reads_only_what_is_selected(path):
     _close(*_run(pr), [x[0] for x in _oracle(pr)])
 
 
+@pytest.mark.parametrize("written", ["none", "half"])
+@pytest.mark.parametrize("n", [1, 2])
+def test_decode_q8_groups_that_no_write_reached(path, written, n):
+    # a cache still zero where it was not written (the padding of a captured batch): such rows
+    # are rows of zeros, score 0 and count
+    pr = _problem(17, 2, 1, 64, 300, 220, bs=16, group=8)
+    blank = np.ones(pr["scales"].shape, bool) if written == "none" else np.arange(pr["scales"].size).reshape(-1, 2) % 3 == 0
+    pr["scales"][blank] = 0.0
+    pr["codes"].reshape(-1, 2, 8, 576)[blank] = 0
+    out, lse = _run(pr, n)
+    _close(out, lse, [x[0] for x in _oracle(pr)], f"n={n}")
+    if written == "none":
+        assert torch.all(out == 0)
+
+
 def test_decode_q8_per_token_tables_and_bad_blocks(path):
     pr = _problem(6, 2, 3, 16, 200, 64, bs=16, group=4)
     rng = np.random.default_rng(1)
