@@ -622,10 +622,11 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
 
     x [T, n, width] or [T, width] bf16, fp16 or fp32 with any row strides (a view of the rope
     columns of wider heads); positions [T] int32 (< 0 = padding: those rows of out are left as
-    they were); inv_freq [rot_dim / 2] float64 (``rope_inv_freq``).  interleaved pairs columns
-    (2i, 2i + 1), else (i, i + rot_dim / 2).  inverse turns back by the same angles: the
-    transpose, so that rope(grad_out, ..., inverse=True) is the gradient of x.  out: x itself
-    (in place), another tensor of x's shape and dtype, or None for a new one.  Returns out.
+    they were, and are x's in a new one); inv_freq [rot_dim / 2] float64 (``rope_inv_freq``).
+    interleaved pairs columns (2i, 2i + 1), else (i, i + rot_dim / 2).  inverse turns back by the
+    same angles: the transpose, so that rope(grad_out, ..., inverse=True) is the gradient of x.
+    out: x itself (in place), another tensor of x's shape and dtype, or None for a new one.
+    Returns out.
     """
     dev = x.device
     if dev.type != "cuda":
@@ -649,10 +650,12 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
         raise ValueError("positions must be [T]")
     if rot < 2 or rot > width:
         raise ValueError("inv_freq must be [rot_dim / 2] with 2 <= rot_dim <= width")
+    flags = (1 if interleaved else 0) | (2 if inverse else 0)
     with _on(dev, stream):
         if out is None:
             # a padding row has no result: a new tensor holds x's there
-            out = x.clone(memory_format=torch.contiguous_format)
+            out = torch.empty(shape, dtype=x.dtype, device=dev)
+            flags |= 4
         elif out.dtype is not x.dtype or out.get_device() != dev.index or out.shape != shape or out.stride(-1) != 1:
             raise ValueError("out must have x's shape, dtype and device, and contiguous columns")
         if n == 0:
@@ -660,7 +663,7 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
         os = out.stride()
         code = _lib.load().sfa_rope(x.data_ptr(), xt, xn, out.data_ptr(), os[0], os[1] if len(shape) == 3 else 0,
                                     dtype, T, n, width, rot, positions.data_ptr(), inv_freq.data_ptr(), float(mscale),
-                                    (1 if interleaved else 0) | (2 if inverse else 0), _raw_stream(dev))
+                                    flags, _raw_stream(dev))
     if code:
         _lib.check("sfa_rope", code)
     return out

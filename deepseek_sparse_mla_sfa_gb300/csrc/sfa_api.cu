@@ -605,7 +605,7 @@ sfa_status sfa_rope(const void* x, long long x_token_stride, long long x_head_st
                     int rot_dim, const int32_t* positions, const double* inv_freq, float mscale, int flags,
                     sfa_stream stream) {
   if (T < 0 || n < 1 || width < 1 || rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > width || !isfinite(mscale) ||
-      dtype < 0 || dtype > 2 || (flags & ~(SFA_ROPE_INTERLEAVED | SFA_ROPE_INVERSE)) != 0)
+      dtype < 0 || dtype > 2 || (flags & ~(SFA_ROPE_INTERLEAVED | SFA_ROPE_INVERSE | SFA_ROPE_COPY_PADDING)) != 0)
     return SFA_ERR_INVALID_ARG;
   if (rot_dim > SFA_ROPE_MAX_DIM) return SFA_ERR_UNSUPPORTED;
   if (T == 0) return SFA_OK;
@@ -618,7 +618,7 @@ sfa_status sfa_rope(const void* x, long long x_token_stride, long long x_head_st
   if ((T > 1 && out_token_stride == 0) || (n > 1 && out_head_stride == 0)) return SFA_ERR_INVALID_ARG;   // rows of out must differ
   return sfa::launch_rope(x, x_token_stride, x_head_stride, out, out_token_stride, out_head_stride, dtype, T, n, width,
                           rot_dim, positions, inv_freq, (flags & SFA_ROPE_INTERLEAVED) ? 1 : 0,
-                          (flags & SFA_ROPE_INVERSE) ? 1 : 0, mscale,
+                          (flags & SFA_ROPE_INVERSE) ? 1 : 0, (flags & SFA_ROPE_COPY_PADDING) ? 1 : 0, mscale,
                           static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SFA_OK
              : SFA_ERR_CUDA;

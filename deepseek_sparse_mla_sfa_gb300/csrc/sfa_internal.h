@@ -136,7 +136,7 @@ cudaError_t launch_step_plan(const int32_t* cached, const int32_t* fresh_tokens,
 // dtype: 0 bf16, 1 fp16, 2 fp32; strides in elements
 cudaError_t launch_rope(const void* x, long long xt, long long xn, void* out, long long ot, long long on, int dtype,
                         int T, int n, int width, int rot, const int32_t* pos, const double* inv_freq,
-                        int interleaved, int inverse, float mscale, cudaStream_t stream);
+                        int interleaved, int inverse, int copy_padding, float mscale, cudaStream_t stream);
 
 // tcgen05 path: whether it handles this problem, its workspace, and its launch.  Three
 // kernels: the CTA-pair kernel (any h <= 128), the small-head kernel (h <= 32) and the

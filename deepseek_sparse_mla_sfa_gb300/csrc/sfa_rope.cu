@@ -35,7 +35,7 @@ struct RopeParams {
   const double* inv_freq;
   long long xt, xn, ot, on;   // row strides in elements
   int T, n, width, rot;
-  int interleaved, inverse, in_place;
+  int interleaved, inverse, in_place, copy_padding;
   float mscale;
   int tokens, heads, head_tiles;   // a block's share; blocks per token group
   uint32_t heads_mul;              // row / heads as (row * heads_mul) >> 32, row < 2^16 (0: heads is 1)
@@ -150,6 +150,10 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams 
     if (!p.in_place)
       for (int d = p.rot + v; d < p.width; d += groups) orow[d] = xr[d];
   }
+  if (p.copy_padding && !p.in_place)                      // or is x's
+    for (int tl = 0; tl < nt; ++tl)
+      for (int hd = y; hd < nh && pos_s[tl] < 0; hd += lanes)
+        for (int d = v; d < p.width; d += groups) ob[tl * p.ot + hd * p.on + d] = xb[tl * p.xt + hd * p.xn + d];
 }
 
 template <typename E, int VP>
@@ -197,9 +201,9 @@ cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t stream) {
 
 cudaError_t launch_rope(const void* x, long long xt, long long xn, void* out, long long ot, long long on, int dtype,
                         int T, int n, int width, int rot, const int32_t* pos, const double* inv_freq,
-                        int interleaved, int inverse, float mscale, cudaStream_t stream) {
+                        int interleaved, int inverse, int copy_padding, float mscale, cudaStream_t stream) {
   const RopeParams p{x,  out,   pos, inv_freq,    xt,      xn,        ot,     on, T,
-                     n,  width, rot, interleaved, inverse, x == out, mscale, 1, 1, 1, 0};
+                     n,  width, rot, interleaved, inverse, x == out, copy_padding, mscale, 1, 1, 1, 0};
   switch (dtype) {
     case 0: return launch_rope_t<__nv_bfloat16>(p, stream);
     case 1: return launch_rope_t<__half>(p, stream);

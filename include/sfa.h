@@ -235,7 +235,8 @@ sfa_status sfa_uv_proj(const float *out, const void *w_uv, void *y, int T, int h
  *
  *   kv8         device, e4m3 bytes [num_blocks, block_size, 576]; 16-byte aligned
  *   scales      device, fp32 [num_blocks, block_size / group], in [2^-100, 2^120]
- *               (sfa_kv_write_q8 writes powers of two; any others are taken as they are)
+ *               (sfa_kv_write_q8 writes powers of two; any others are taken as they are), or 0
+ *               where nothing was written: such a group's rows are rows of zeros
  *   group       slots per scale: >= 1, divides block_size
  *   interleave_size, flags  as in sfa_decode_ex; SFA_OUT_BF16: `out` is bf16 [B*Q, h, 512]
  *               (16-byte aligned) instead of fp32.  lse and the shard partials are fp32.
@@ -335,12 +336,14 @@ sfa_status sfa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, in
  *               elements): bf16, fp16 or fp32 (dtype), T tokens of n heads.  out may be x
  *               itself (same strides); otherwise the two must not overlap.  A stride of x may be 0
  *               (a row shared by tokens or heads), of out only where it is not used.
- *   positions   device int32 [T]; < 0 = padding: that token's rows of out are left as they were
+ *   positions   device int32 [T]; < 0 = padding: that token's rows of out are left as they were,
+ *               or with SFA_ROPE_COPY_PADDING are x's
  *   inv_freq    device double [rot_dim / 2]: radians a position
  *   2 <= rot_dim <= SFA_ROPE_MAX_DIM, even, <= width
  */
 #define SFA_ROPE_INTERLEAVED 1
 #define SFA_ROPE_INVERSE 2
+#define SFA_ROPE_COPY_PADDING 4
 #define SFA_ROPE_MAX_DIM 512
 #define SFA_DTYPE_BF16 0
 #define SFA_DTYPE_FP16 1

@@ -172,6 +172,22 @@ def test_rope_strides_offsets_and_padding_rows_of_out():
     assert y2.shape == (9, 64) and torch.equal(y2[1], src[1, 0, :64])
 
 
+@pytest.mark.parametrize("dtype,width,rot", [(torch.bfloat16, 64, 64), (torch.float16, 72, 64), (torch.float32, 21, 14)])
+def test_rope_padding_rows_of_a_new_out_are_those_of_x(dtype, width, rot):
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn((5, 3, width), generator=g).to(dtype).cuda()
+    x[1, 0], x[3, 2] = float("nan"), float("inf")          # copied, not multiplied
+    pos, f = i32([4, -1, 9, -7, 0]), sfa.rope_inv_freq(rot)
+    old = torch.full_like(x, 3.0)
+    given = sfa.rope(x, pos, f, out=old.clone())
+    for src in (x, x.expand(5, 3, width), x.repeat_interleave(2, dim=1)[:, ::2]):
+        new = sfa.rope(src, pos, f)
+        bits = lambda t: t.contiguous().view(torch.uint8)
+        for t in range(5):
+            assert torch.equal(bits(new[t]), bits(x[t] if t in (1, 3) else given[t]))
+    assert torch.equal(given[1], old[1]) and torch.equal(given[3], old[3])
+
+
 def test_rope_of_a_row_shared_by_heads():
     # x expanded over the heads: every head of out gets the rotated row
     g = torch.Generator().manual_seed(5)
@@ -391,6 +407,20 @@ def test_decode_q8_head_counts(path, h, dtype):
 def test_decode_q8_list_lengths(path, k, S):
     pr = _problem(k, 2, 1, 20, S, k)
     _close(*_run(pr), [x[0] for x in _oracle(pr)])
+
+
+@pytest.mark.parametrize("h,B,k", [(4, 1, 20000), (4, 80, 13000), (64, 1, 12289)])
+def test_decode_q8_lists_of_several_segments(h, B, k):
+    # lists of more than two of the kernel's 6144-row segments, with every entry used: positions
+    # come back (each entry is a term of its own); by one CTA a token and by eight
+    pr = _problem(k, B, 1, h, 700, 700)
+    rng = np.random.default_rng(k)
+    pr["idx"] = np.stack([rng.integers(0, int(n), k) for n in pr["sl"]])
+    out, lse = _run(pr)
+    for t in (0, B - 1):
+        one = dict(pr, q=pr["q"][t:t + 1], bt=pr["bt"][t:t + 1], sl=pr["sl"][t:t + 1], idx=pr["idx"][t:t + 1])
+        _close(out[t:t + 1], lse[t:t + 1], [x[0] for x in _oracle(one)], f"token {t}")
+    assert sfa.last_device_status() == 0
 
 
 @pytest.mark.parametrize("bs,group", [(64, 1), (64, 16), (16, 16), (24, 8), (1, 1), (128, 128), (7, 7), (100, 50)])
