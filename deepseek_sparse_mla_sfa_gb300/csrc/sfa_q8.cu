@@ -13,30 +13,43 @@
 //     QK^T costs what one bf16 pass over half the bytes would.
 //   * weights: P_j = p_j c_j is stored as hi + lo, 8 significant bits as bf16 has, two K
 //     steps into the same accumulator.  The reference of the running softmax is the maximum
-//     of log2 P_j (so c_j is inside it): P stays in [0, 256], 16 at the maximum that the
-//     reference was taken from, where 2^-9 is the spacing of the smallest e4m3 values.
+//     of log2 P_j (so c_j is inside it): P is 8 at the maximum that the reference was taken
+//     from and may rise to 2^8.75 (e4m3 ends at 448) before the reference moves; 2^-9 is the
+//     spacing of the smallest e4m3 values, so a small weight is off by 2^-13 of the largest at
+//     most.  Where one of a warp's eight heads has to move, all that have risen move.
 //
 // One CTA handles one unit (query token, shard, group of up to 64 heads), whole rows, no
 // exchange per tile:
 //   * tiles of 96 rows, 3 stages, in the swizzled operand layout: 4 column blocks of 128
-//     latent bytes a row (SW128) by TMA tile::gather4, and the 64 rope bytes (SW64) by 16-byte
-//     cp.async.  An SM's TMA unit takes ~15 ns a gather4 whatever its size, so the half-width
-//     rope boxes would add a quarter to the 1.44 us of the latent ones; as cp.async they are 12
-//     instructions a tile.  (All 36 words of a row by cp.async: 5000 cycles a tile, and the
-//     softmax's shuffles wait behind them in the same unit.)
+//     latent bytes a row (SW128) and the 64 rope bytes (SW64), all by TMA tile::gather4 from the
+//     elected lanes of four warps;
 //   * QK^T: S[heads hi|lo, rows] += q[128, 32] E^T, 18 steps, q in TMEM, N = 96;
 //   * P.V transposed, O^T[columns, heads] += E^T[128 columns, 32 rows] P^T: four blocks of
-//     128 columns, 3 K steps each for hi and lo, N = padded heads.  E^T is the same tile read
-//     MN-major.  O takes 4 x 64 columns of TMEM.
+//     128 columns, 3 K steps, each hi and then lo with the same A, which the second takes from
+//     the collector buffer (at N = 64 the read of A from shared memory, 4 KB, takes longer than
+//     the products: 48.9 -> 47.4 us below).  E^T is the same tile read MN-major.
 // TMEM: q 144 columns, S 96 (two of them for 32 heads or fewer), O^T up to 256.
 //
 // With few units a cluster of G CTAs shares one: CTA c takes tiles c, c + G, ...; they merge
 // (O, m, l) over distributed shared memory at the end.
 //
-// Warp roles (384 threads): warps 0-7 softmax, O rescale and output (warps w and w + 4 share
-// the TMEM lanes 32 (w % 4) ..: 16 heads' hi rows and the same heads' lo rows); warp 8 issues
-// QK^T, warp 9 P.V, warps 10 and 11 the gathers.  Every wait is bounded; one that gives up
-// records SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
+// Warp roles (640 threads): warps 0-7 softmax (each 8 heads whole); 8 issues QK^T, 9 P.V; 10-13
+// the gathers; 14 the rows' scales and the later segments of a long list; 16-19 scale O where a
+// reference moved; all take a part in the output.  At the start warps 0-7 and 16-19 bring q to
+// TMEM while 8-15 resolve the list.  Every wait is bounded; one that gives up records
+// SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
+//
+// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.9 us, 256 tokens x 64
+// heads x 2048 rows 91.2 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
+// rows in four shards 48.8 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
+// ~2,700 cycles and the rest is the chain scores -> softmax -> P.V with one score buffer (TMEM
+// is full); the first scores come after 12,600-14,600 cycles (launch, list, table, q and the
+// first rows follow one another), the end takes 5,000, and a second round of units a whole
+// one's time.  The first step without the moves of references: 42.8 us, with half the P.V
+// 44.1, with a quarter of the gathers 45.7.
+// Taken back: 64-row tiles in 4 or 5 stages (63 vs 61 us at the time), part of the columns by
+// cp.async (64-94 vs 61), rows prefetched to L2 (67 vs 61, 72 vs 49), P.V handed over in
+// three parts (51.5 vs 49.0), references moved two groups of heads at a time (47.5 vs 45.9).
 #include <atomic>
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -60,8 +73,8 @@ constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kPro
               kFixWarp = 16, kFixWarps = 4;
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kPeak = 4.0f;        // log2 of P at the maximum a reference is taken from
-constexpr float kMostP = 8.0f;       // log2 of the largest P before the reference moves
+constexpr float kPeak = 3.0f;        // log2 of P at the maximum a reference is taken from
+constexpr float kMostP = 8.75f;      // log2 of the largest P before the reference moves
 
 // shared memory map (offsets from a 1024-byte aligned base)
 constexpr int kBlk = kNt * 128;                       // 128 latent columns of a tile, SW128
@@ -133,14 +146,24 @@ __device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint32_t b_
       "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHi)
       : "memory");
 }
-template <uint32_t kHiA, uint32_t kHiB>
+// (kFirst: A stays in the collector buffer, and the next MMA, with the same A, takes it from
+// there instead of from shared memory)
+template <uint32_t kHiA, uint32_t kHiB, bool kFirst>
 __device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}" ::"r"(d),
-      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
-      : "memory");
+  if constexpr (kFirst)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], da, db, %3, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
+        : "memory");
 }
 // the words of a shared-memory matrix descriptor (addresses and strides in 16-byte units)
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
@@ -625,12 +648,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   #pragma unroll
               for (int k = 0; k < kNt / 32; ++k)
   #pragma unroll
-                for (int part = 0; part < 2; ++part)
-  #pragma unroll
-                  for (int m = 0; m < 4; ++m)
-                    mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128)>(
-                        tmem + kColO + NH * m, a0 + ((m * kBlk + 4096 * k) >> 4), b0 + ((part * kPBytes + 32 * k) >> 4), id,
-                        (k > 0 || part > 0) ? 1u : (n > 0 ? 1u : 0u));
+                for (int m = 0; m < 4; ++m) {
+                  const uint32_t d = tmem + kColO + NH * m, a = a0 + ((m * kBlk + 4096 * k) >> 4), b = b0 + ((32 * k) >> 4);
+                  mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128), true>(d, a, b, id, k > 0 || n > 0);
+                  mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128), false>(d, a, b + (kPBytes >> 4), id, 1);
+                }
               mma_commit(&bars[kBarKvEmpty + s]);
               mma_commit(&bars[kBarPFree + bb]);
               if (n == n_local - 1) mma_commit(&bars[kBarPvFinal]);
@@ -775,9 +797,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             fail();
             break;
           }
-          const bool up = i == 0 || mx > ref + kMostP;
-          const float ref_new = up ? mx - kPeak : ref;
-          const bool moved = __any_sync(0xffffffffu, i > 0 && up);
+          // (where one of the warp's heads has to move, the others that have risen move with it)
+          const bool moved = __any_sync(0xffffffffu, i > 0 && mx > ref + kMostP);
+          const float ref_new = i == 0 || (moved && mx > ref + kPeak) ? mx - kPeak : ref;
           if (moved) {
             const float alpha = ex2(ref - ref_new);
             l2 = mul2(l2, pack2(alpha, alpha));
