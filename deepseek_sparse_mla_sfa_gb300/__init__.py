@@ -655,7 +655,7 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
         if out is None:
             # a padding row has no result: a new tensor holds x's there
             out = torch.empty(shape, dtype=x.dtype, device=dev)
-            flags |= 4
+            flags |= 8
         elif out.dtype is not x.dtype or out.get_device() != dev.index or out.shape != shape or out.stride(-1) != 1:
             raise ValueError("out must have x's shape, dtype and device, and contiguous columns")
         if n == 0:

@@ -343,7 +343,7 @@ sfa_status sfa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, in
  */
 #define SFA_ROPE_INTERLEAVED 1
 #define SFA_ROPE_INVERSE 2
-#define SFA_ROPE_COPY_PADDING 4
+#define SFA_ROPE_COPY_PADDING 8
 #define SFA_ROPE_MAX_DIM 512
 #define SFA_DTYPE_BF16 0
 #define SFA_DTYPE_FP16 1
