@@ -39,9 +39,9 @@
 // TMEM while 8-15 resolve the list.  Every wait is bounded; one that gives up records
 // SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
 //
-// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.9 us, 256 tokens x 64
-// heads x 2048 rows 91.2 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
-// rows in four shards 48.8 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
+// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.7 us, 256 tokens x 64
+// heads x 2048 rows 91.7 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
+// rows in four shards 47.3 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
 // ~2,700 cycles and the rest is the chain scores -> softmax -> P.V with one score buffer (TMEM
 // is full); the first scores come after 12,600-14,600 cycles (launch, list, table, q and the
 // first rows follow one another), the end takes 5,000, and a second round of units a whole
@@ -72,6 +72,7 @@ constexpr int kSoftWarps = 8, kQWarps = 12;
 constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kProducerWarps = 4, kRowWarp = 14,
               kFixWarp = 16, kFixWarps = 4;
 constexpr int kGroupHeads = 64;      // heads of a unit
+constexpr int kQParts = (kGroupHeads + kQWarps - 1) / kQWarps;   // copies of q, kQWarps heads each
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kPeak = 3.0f;        // log2 of P at the maximum a reference is taken from
 constexpr float kMostP = 8.75f;      // log2 of the largest P before the reference moves
@@ -90,7 +91,7 @@ constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscScale = 1024, kMiscC = 1280, k
               kMiscMoved = 1544, kMiscCount = 1560, kMiscSeg = 1600, kMiscBytes = 1616;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
 constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarRows = kBarKvEmpty + kStages,
-              kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQLoad = kBarSegFull + 1, kBarQReady = kBarQLoad + 1,
+              kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQLoad = kBarSegFull + 1, kBarQReady = kBarQLoad + kQParts,
               kBarSFull = kBarQReady + 1, kBarSFree = kBarSFull + 2, kBarAReady = kBarSFree + 2, kBarPReady = kBarAReady + 2,
               kBarPFree = kBarPReady + 2, kBarPvFinal = kBarPFree + 2, kBarMmaFin = kBarPvFinal + 1,
               kBarMmaFin2 = kBarMmaFin + 1, kBarNever = kBarMmaFin2 + 1, kNumBars = kBarNever + 1;
@@ -345,10 +346,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   char* const qst = smem + kStageBytes;
   if (threadIdx.x == 0) {
-    mbar_init(&bars[kBarQLoad], 1);
+    for (int x = 0; x < kQParts; ++x) mbar_init(&bars[kBarQLoad + x], 1);
     fence_barrier_init();
-    mbar_arrive_expect_tx(&bars[kBarQLoad], (uint32_t)nh * kQPitch);
-    bulk_load_g2s(smem_u32(qst), qsrc, (uint32_t)nh * kQPitch, &bars[kBarQLoad]);
+    for (int hd = 0, x = 0; hd < nh; hd += kQWarps, ++x) {
+      const uint32_t bytes = (uint32_t)min(kQWarps, nh - hd) * kQPitch;
+      mbar_arrive_expect_tx(&bars[kBarQLoad + x], bytes);
+      bulk_load_g2s(smem_u32(qst + hd * kQPitch), reinterpret_cast<const char*>(qsrc) + hd * kQPitch, bytes, &bars[kBarQLoad + x]);
+    }
   }
   if (threadIdx.x == 64) {
     for (int s = 0; s < kStages; ++s) {
@@ -671,11 +675,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else {
-    // ---- q as hi and lo e4m3 rows, a head a warp, in place in shared memory (stages 1 and 2,
-    // which the gathers leave alone until q is ready); then to the TMEM lanes
-    if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarQLoad], 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
-#pragma unroll 1
+    // ---- q as hi and lo e4m3 rows, a head a warp as it lands, in place in shared memory (stages
+    // 1 and 2, which the gathers leave alone until q is ready); then to the TMEM lanes
+#pragma unroll 2
     for (int hd = wq; hd < NH; hd += kQWarps) {
+      if (hd < nh && !__all_sync(0xffffffffu, mbar_wait(&bars[kBarQLoad + hd / kQWarps], 0, kDrainLimit)))
+        report_status(p.status, kStatusTimeout);
       char* at = qst + hd * kQPitch;
       uint4 x[3];
 #pragma unroll
