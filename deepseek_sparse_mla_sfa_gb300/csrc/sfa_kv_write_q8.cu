@@ -16,8 +16,10 @@
 // rows when its scale rose; the last one stores the scale and clears the record, so the
 // workspace is zero between calls.  Groups of one slot need no record and take one launch.
 //
-// Bound: HBM, 1152 bytes read and 576 written a row; latency for a decode step's rows, where
-// four warps take a row (one load each, and a group is rewritten four times as fast).
+// Bound: HBM, 1152 bytes read and 576 written a row, and the wait of the second launch for the
+// first's atomics: 8885 rows in groups of 16 take 9.5 us (2.3 us of bytes).  Latency for a decode
+// step's rows, where four warps take a row (one load each, and a group is rewritten four times as
+// fast): 64 rows that each join a filled group of 64 take 3.9 us.
 #include <cuda_fp8.h>
 #include <string.h>
 
@@ -283,7 +285,8 @@ cudaError_t launch_kv_write_q8(void* kv8, float* scales, long long num_slots, in
   uint4* kv = static_cast<uint4*>(kv8);
   const uint4* src = static_cast<const uint4*>(rows);
   GroupRecord* rec = static_cast<GroupRecord*>(workspace);
-  // four warps a row while that leaves the GPU's blocks few
+  // four warps a row while that leaves the GPU's blocks few: 64 rows that join filled groups 3.8 us
+  // (4.3 with a warp a row), 608 rows 4.2 (4.4), 1216 rows 4.8 (4.3), 2432 rows 8.0 (4.8)
   return T <= 4 * device_sm_count()
              ? launch_rows<kFewThreads>(kv, scales, num_slots, group, slots, src, T, rec, status, stream)
              : launch_rows<32>(kv, scales, num_slots, group, slots, src, T, rec, status, stream);

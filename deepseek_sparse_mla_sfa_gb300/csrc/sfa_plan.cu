@@ -12,8 +12,10 @@
 // share of the tokens, finding a token's request by binary search.  A fresh block's id is
 // read from the free list, never from the table entry that another CTA writes.
 //
-// Bound: latency (a launch, one dependent load of the lengths, one of the table); a step's
-// outputs are 8 bytes a token.
+// Bound: latency (a launch, one dependent load of the lengths, a scan, one load of the table or the
+// free list); a step's outputs are 8 bytes a token.  64 requests of one token take 4.4 us on the
+// device, 512 requests of up to 300 tokens 7.8 us.  A CTA takes 2048 tokens (four a thread): the
+// sums cost every CTA the same, so more CTAs than that only repeat them.
 #include <climits>
 
 #include "sfa_internal.h"

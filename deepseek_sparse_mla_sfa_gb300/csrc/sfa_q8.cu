@@ -1039,17 +1039,46 @@ bool make_rows_map(CUtensorMap* m, const void* kv8, int num_rows, int cols, CUte
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t prepare_decode_q8() {
-  static std::atomic<bool> attr_set[64];
+void launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, long long units, int G, cudaStream_t stream) {
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3((unsigned)(units * G), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  attr->id = cudaLaunchAttributeClusterDimension;
+  attr->val.clusterDim.x = (unsigned)G;
+  attr->val.clusterDim.y = 1;
+  attr->val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+}
+
+// once a device: the kernels' shared memory, and how many clusters of 2, 4 and 8 CTAs run at once
+// (fewer than the SMs would hold: a cluster stays within one group of SMs)
+cudaError_t prepare_decode_q8(int (&fit)[3]) {
+  static std::atomic<bool> ready[64];
+  static int fits[64][3];
   int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev >= 0 && dev < 64 && !attr_set[dev].load(std::memory_order_acquire)) {
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev].load(std::memory_order_acquire)) {
     for (auto kernel : {q8_kernel<32, false>(), q8_kernel<32, true>(), q8_kernel<64, false>(), q8_kernel<64, true>()}) {
-      cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       if (e != cudaSuccess) return e;
     }
-    attr_set[dev].store(true, std::memory_order_release);
+    static std::mutex once;
+    const std::lock_guard<std::mutex> hold(once);
+    for (int k = 0; k < 3; ++k) {
+      cudaLaunchConfig_t cfg;
+      cudaLaunchAttribute attr[1];
+      launch_config(cfg, attr, 1, 2 << k, 0);
+      e = cudaOccupancyMaxActiveClusters(&fits[dev][k], q8_kernel<64, false>(), &cfg);
+      if (e != cudaSuccess) return e;
+    }
+    ready[dev].store(true, std::memory_order_release);
   }
+  for (int k = 0; k < 3; ++k) fit[k] = fits[dev][k];
   return cudaSuccess;
 }
 
@@ -1059,19 +1088,24 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
   const DecodeParams& p = qp.p;
   const long long T = (long long)p.B * p.Q;
   if (T == 0) return cudaSuccess;
-  cudaError_t e = prepare_decode_q8();
+  int fit[3];
+  cudaError_t e = prepare_decode_q8(fit);
   if (e != cudaSuccess) return e;
   Q8Params kp;
   kp.qp = qp;
   kp.groups = (p.h + kGroupHeads - 1) / kGroupHeads;
   kp.group_heads = (p.h + kp.groups - 1) / kp.groups;
   const long long units = T * p.n_splits * kp.groups;
-  // a unit is shared by up to 8 CTAs while the units fill less than half the GPU and each
-  // CTA has a tile of the list
+  // A unit is shared by up to 8 CTAs while all its clusters run at once and a CTA keeps more than
+  // two tiles of the list (the merge costs 3-4 us for two CTAs and 1-2 more for each doubling; a
+  // tile 1.2).  9 tokens x 16 heads x 2048 rows, by 1, 2, 4, 8 CTAs: 33, 23, 18, 17 us; 64 heads 41,
+  // 30, 25, 25; 300 rows 16, 18, 18, 22.  (38 units by 4 CTAs, which do not run at once: 37 us, by 2:
+  // 25.)
   int G = 1;
-  while (G < 8 && units * G * 2 <= device_sm_count() && G * kNt < p.top_k) G *= 2;
+  for (int k = 0; k < 3 && units <= fit[k] && p.top_k > 4 * G * kNt; ++k) G *= 2;
   if (units * G > 0x7fffffffLL) return cudaErrorInvalidValue;
   const bool il = p.interleave > 0 && p.n_splits > 1;
+  // 32 padded heads or 64: 100 tokens x 32 heads x 2048 rows 39.8 us, as 64 heads 41.8; 4 tokens 15.7, 22.2
   auto kernel = kp.group_heads <= 32 ? (il ? q8_kernel<32, true>() : q8_kernel<32, false>())
                                      : (il ? q8_kernel<64, true>() : q8_kernel<64, false>());
   CUtensorMap lat, rope;
@@ -1084,18 +1118,8 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
       !make_rows_map(&rope, p.kv, kp.num_rows, 64, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3((unsigned)(units * G), 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)G;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  launch_config(cfg, attr, units, G, stream);
   e = cudaLaunchKernelEx(&cfg, kernel, lat, rope, kp);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

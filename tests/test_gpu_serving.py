@@ -409,6 +409,20 @@ def test_decode_q8_list_lengths(path, k, S):
     _close(*_run(pr), [x[0] for x in _oracle(pr)])
 
 
+@pytest.mark.parametrize("h", [1, 17, 32, 33, 64, 100, 128])
+@pytest.mark.parametrize("k", [384, 385, 700, 1000, 1537, 2048])
+def test_decode_q8_units_shared_by_several_ctas(h, k):
+    # by 1, 2, 4 and 8 CTAs a unit (more than four tiles of 96 rows for each CTA of half as many),
+    # in both output types and with an empty sequence, whose CTAs have no tile
+    pr = _problem(1000 + h + k, 3, 1, h, 2100, k)
+    pr["sl"][1] = 0
+    want = [x[0] for x in _oracle(pr)]
+    for dtype in (torch.float32, torch.bfloat16):
+        _close(*_run(pr, dtype=dtype), want, f"{dtype}")
+    _close(*_run(pr, 3), want, "three shards")
+    assert sfa.last_device_status() == 0
+
+
 @pytest.mark.parametrize("h,B,k", [(4, 1, 20000), (4, 80, 13000), (64, 1, 12289)])
 def test_decode_q8_lists_of_several_segments(h, B, k):
     # lists of more than two of the kernel's 6144-row segments, with every entry used: positions
