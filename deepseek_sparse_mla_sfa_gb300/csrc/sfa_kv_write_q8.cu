@@ -9,17 +9,18 @@
 // powers of two the change of scale moves exponents only, so a stored value is rounded
 // again only where it becomes subnormal, and a dequantised value is exact in bf16.
 //
-// Two launches: the first takes each row's amax and joins it to its group's record in the
-// workspace (atomic max / or / add: the result does not depend on their order); the second
-// quantises.  It is launched early (programmatic dependent launch) and loads its rows while
-// the first still runs.  The first row of a group to arrive there rewrites the group's other
-// rows when its scale rose; the last one stores the scale and clears the record, so the
-// workspace is zero between calls.  Groups of one slot need no record and take one launch.
+// Few rows (a decode step) take one launch and a block a group.  More take two: the first takes each
+// row's amax and joins it to its group's record in the workspace (atomic max / or / add: the result
+// does not depend on their order); the second quantises.  It is launched early (programmatic
+// dependent launch) and loads its rows while the first still runs.  The first row of a group to
+// arrive there rewrites the group's other rows when its scale rose; the last one stores the scale and
+// clears the record, so the workspace is zero between calls.  Groups of one slot need no record and
+// take one launch.
 //
 // Bound: HBM, 1152 bytes read and 576 written a row, and the wait of the second launch for the
 // first's atomics: 8885 rows in groups of 16 take 9.5 us (2.3 us of bytes).  Latency for a decode
-// step's rows, where four warps take a row (one load each, and a group is rewritten four times as
-// fast): 64 rows that each join a filled group of 64 take 3.9 us.
+// step's rows: 64 rows that each join a filled group of 64 take 2.9 us, a chain of slots, rows, the
+// group's largest value and, where its scale rose, its other rows.
 #include <cuda_fp8.h>
 #include <string.h>
 
@@ -31,7 +32,7 @@ namespace {
 constexpr int kRowWords = kDQK * 2 / 16;   // 72 x 16 bytes per bf16 row
 constexpr int kRow8Words = kDQK / 16;      // 36 x 16 bytes per e4m3 row
 constexpr int kThreads = 256;         // 8 rows a block, a warp each
-constexpr int kFewThreads = 128;      // or one row a block
+constexpr int kFewThreads = 512;      // of a block that takes a group, and as many slots a call at most
 constexpr int kMinExp = -100, kMaxExp = 120;
 
 struct GroupRecord {
@@ -97,77 +98,157 @@ __device__ __forceinline__ unsigned requantise4(unsigned w, float ratio) {
   return out;
 }
 
-// kRowThreads threads share a row: its words threadIdx.x % kRowThreads + kRowThreads i
-template <int kRowThreads>
+// every scale that this file writes is a power of two within [2^-100, 2^120]
+__device__ __forceinline__ bool is_pow2(float s) {
+  return (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-100f;
+}
+
+// a warp's row: its words threadIdx.x % 32 + 32 i
 struct Row {
-  static constexpr int kWords = (kRowWords + kRowThreads - 1) / kRowThreads;
+  static constexpr int kWords = (kRowWords + 31) / 32;
   uint4 x[kWords];
   long long slot;   // -1: padding, out of range or behind the last row
   int lane;
 
   __device__ __forceinline__ void load(const int32_t* slots, const uint4* rows, int T, long long num_slots,
                                        int* status) {
-    const long long t = (blockIdx.x * (long long)blockDim.x + threadIdx.x) / kRowThreads;
-    lane = threadIdx.x % kRowThreads;
+    const long long t = (blockIdx.x * (long long)blockDim.x + threadIdx.x) / 32;
+    lane = threadIdx.x % 32;
     slot = -1;
     if (t >= T) return;
     slot = slots[t];
     const uint4* src = rows + (size_t)t * kRowWords + lane;
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-      x[i] = lane + kRowThreads * i < kRowWords ? __ldg(src + kRowThreads * i) : make_uint4(0, 0, 0, 0);
+      x[i] = lane + 32 * i < kRowWords ? __ldg(src + 32 * i) : make_uint4(0, 0, 0, 0);
     if (slot >= num_slots) {
       if (status && lane == 0) report_status(status, kStatusBadBlock);
       slot = -1;
     }
   }
-  // the row's largest finite magnitude, as bits (every thread of the row calls it; with more
-  // than a warp a row, every thread of the block)
+  // the row's largest finite magnitude, as bits
   __device__ __forceinline__ unsigned amax() const {
     unsigned m = 0;
 #pragma unroll
     for (int i = 0; i < kWords; ++i) m = max(m, amax_bits(x[i]));
-    m = __reduce_max_sync(0xffffffffu, m);
-    if constexpr (kRowThreads > 32) {
-      __shared__ unsigned m_s[kRowThreads / 32];
-      if (lane % 32 == 0) m_s[lane / 32] = m;
-      __syncthreads();
-#pragma unroll
-      for (int w = 0; w < kRowThreads / 32; ++w) m = max(m, m_s[w]);
-    }
-    return m;
+    return __reduce_max_sync(0xffffffffu, m);
   }
   __device__ __forceinline__ void store(uint4* kv8, float s) const {
     uint2* dst = reinterpret_cast<uint2*>(kv8 + (size_t)slot * kRow8Words) + lane;
-    // every scale that this file writes is a power of two within [2^-100, 2^120]
-    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0 && s >= 0x1p-100f;
+    const bool pow2 = is_pow2(s);
     const float inv = 1.f / s;
 #pragma unroll
     for (int i = 0; i < kWords; ++i)
-      if (lane + kRowThreads * i < kRowWords)
-        dst[kRowThreads * i] = pow2 ? quantise8<true>(x[i], inv) : quantise8<false>(x[i], s);
-  }
-  // a value of the row's thread 0 to all of them, and a barrier over the row
-  __device__ __forceinline__ int broadcast(int v) const {
-    if constexpr (kRowThreads > 32) {
-      __shared__ int v_s;
-      __syncthreads();
-      if (lane == 0) v_s = v;
-      __syncthreads();
-      return v_s;
-    } else {
-      return __shfl_sync(0xffffffffu, v, 0);
-    }
+      if (lane + 32 * i < kRowWords) dst[32 * i] = pow2 ? quantise8<true>(x[i], inv) : quantise8<false>(x[i], s);
   }
 };
 
-template <int kRowThreads>
+// the rows of the group at `base` whose bit of `mask` is clear: from scale `old` to `s`, by the
+// threads `thread` of `threads`
+__device__ __forceinline__ void move_group(uint4* base, int group, unsigned long long mask, float old, float s,
+                                           int thread, int threads) {
+  const float ratio = old / s;
+  const int words = group * kRow8Words;
+  constexpr int kFly = 6;                      // words in flight a thread
+  for (int j0 = thread; j0 < words; j0 += kFly * threads) {
+    uint4 w[kFly];
+    bool in[kFly];
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      const int j = j0 + k * threads;
+      in[k] = j < words && !((mask >> (j / kRow8Words)) & 1);
+      if (in[k]) w[k] = base[j];
+    }
+#pragma unroll
+    for (int k = 0; k < kFly; ++k) {
+      if (!in[k]) continue;
+      base[j0 + k * threads] = make_uint4(requantise4(w[k].x, ratio), requantise4(w[k].y, ratio),
+                                          requantise4(w[k].z, ratio), requantise4(w[k].w, ratio));
+    }
+  }
+}
+
+// the scale that counts as a group's before a call
+__device__ __forceinline__ float scale_before(float was, unsigned long long mask) {
+  return ((mask & 1) || !(was > 0.f) || was > 3e38f) ? 0.f : was;
+}
+
+// Few rows, a block each: the block of a group's first row takes all the group's rows, which it
+// finds by reading every slot; the others have nothing to do.
+__global__ void __launch_bounds__(kFewThreads) q8_few_kernel(uint4* kv8, float* scales, long long num_slots,
+                                                          const int32_t* __restrict__ slots,
+                                                          const uint4* __restrict__ rows, int T, int group,
+                                                          int* status) {
+  constexpr int kKeep = (kQ8MaxWriteGroup * kRowWords + kFewThreads - 1) / kFewThreads;   // words a thread holds
+  __shared__ int member_s[kFewThreads], last_s[kQ8MaxWriteGroup], count_s;   // row | offset in the group << 16
+  __shared__ unsigned amax_s;
+  __shared__ unsigned long long mask_s;
+  const int t = blockIdx.x, tid = threadIdx.x;
+  uint4 x[kKeep];
+  if (tid < kRowWords) x[0] = __ldg(rows + (size_t)t * kRowWords + tid);
+  const int mine = __ldg(slots + t), other = tid < T ? __ldg(slots + tid) : -1;
+  if (mine < 0) return;
+  if (mine >= num_slots) {
+    if (tid == 0) report_status(status, kStatusBadBlock);
+    return;
+  }
+  const int g = mine / group, first = g * group, off = other - first;
+  const bool in = other >= first && off < group;
+  if (tid == 0) {
+    count_s = 1;
+    amax_s = 0;
+    mask_s = 0;
+  }
+  if (tid < kQ8MaxWriteGroup) last_s[tid] = -1;
+  if (__syncthreads_or(in && tid < t)) return;
+  const float was = scales[g];
+  if (in) {
+    member_s[tid == t ? 0 : atomicAdd(&count_s, 1)] = tid | off << 16;
+    atomicOr(&mask_s, 1ull << off);
+    atomicMax(&last_s[off], tid);              // of rows that name one slot the last is stored
+  }
+  __syncthreads();
+  const int words = count_s * kRowWords;
+  const unsigned long long mask = mask_s;
+  const auto word = [&](int i) { return rows + (size_t)(member_s[i / kRowWords] & 0xffff) * kRowWords + i % kRowWords; };
+  unsigned m = tid < kRowWords ? amax_bits(x[0]) : 0;
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int i = tid + kFewThreads * k;
+    if (i >= kRowWords && i < words) x[k] = __ldg(word(i));
+  }
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k) {
+    const int i = tid + kFewThreads * k;
+    if (i >= kRowWords && i < words) m = max(m, amax_bits(x[k]));
+  }
+  for (int i = tid + kFewThreads * kKeep; i < words; i += kFewThreads) m = max(m, amax_bits(__ldg(word(i))));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (tid % 32 == 0) atomicMax(&amax_s, m);
+  __syncthreads();
+  const float old = scale_before(was, mask), s = fmaxf(old, exp2_int(scale_exp(amax_s)));
+  const bool pow2 = is_pow2(s);
+  const float inv = 1.f / s;
+  uint2* dst = reinterpret_cast<uint2*>(kv8 + (size_t)first * kRow8Words);
+  const auto put = [&](int i, const uint4& v) {
+    const int member = member_s[i / kRowWords], at = member >> 16;
+    if (last_s[at] == (member & 0xffff))
+      dst[at * kRowWords + i % kRowWords] = pow2 ? quantise8<true>(v, inv) : quantise8<false>(v, s);
+  };
+#pragma unroll
+  for (int k = 0; k < kKeep; ++k)
+    if (tid + kFewThreads * k < words) put(tid + kFewThreads * k, x[k]);
+  for (int i = tid + kFewThreads * kKeep; i < words; i += kFewThreads) put(i, __ldg(word(i)));
+  if (tid == 0) scales[g] = s;
+  if (old > 0.f && s > old) move_group(kv8 + (size_t)first * kRow8Words, group, mask, old, s, tid, kFewThreads);
+}
+
 __global__ void __launch_bounds__(kThreads) q8_need_kernel(const float* __restrict__ scales, long long num_slots,
                                                            const int32_t* __restrict__ slots,
                                                            const uint4* __restrict__ rows, int T, int group,
                                                            GroupRecord* rec, int* status) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Row<kRowThreads> row;
+  Row row;
   row.load(slots, rows, T, num_slots, status);
   if (row.slot < 0) return;                      // (the same for all threads of a row)
   const unsigned m = row.amax();
@@ -181,12 +262,11 @@ __global__ void __launch_bounds__(kThreads) q8_need_kernel(const float* __restri
   }
 }
 
-template <int kRowThreads>
 __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* scales, long long num_slots,
                                                             const int32_t* __restrict__ slots,
                                                             const uint4* __restrict__ rows, int T, int group,
                                                             GroupRecord* rec) {
-  Row<kRowThreads> row;
+  Row row;
   row.load(slots, rows, T, num_slots, nullptr);
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the records are complete
   if (row.slot < 0) return;
@@ -194,11 +274,11 @@ __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* s
   GroupRecord* r = rec + g;
   const unsigned long long mask = __ldcg(&r->mask);
   const float was = __ldcg(&r->old);
-  const float old = ((mask & 1) || !(was > 0.f) || was > 3e38f) ? 0.f : was;
+  const float old = scale_before(was, mask);
   const float s = fmaxf(old, exp2_int(__ldcg(&r->need) - 1 + kMinExp));
   const int count = __ldcg(&r->count);
   row.store(kv8, s);
-  row.broadcast(0);                              // every thread has its copy of the record
+  __syncwarp();                                  // every thread has its copy of the record
   int ticket = 0;
   if (row.lane == 0) {
     __threadfence();
@@ -212,69 +292,21 @@ __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* s
       r->mask = 0;
     }
   }
-  ticket = row.broadcast(ticket);
-  if (ticket == 0 && old > 0.f && s > old) {
-    // the group's rows that this call does not write: from scale `old` to `s`
-    const float ratio = old / s;
-    uint4* base = kv8 + (size_t)g * group * kRow8Words;
-    const int words = group * kRow8Words;
-    constexpr int kFly = 6;                      // words in flight a thread
-    for (int j0 = row.lane; j0 < words; j0 += kFly * kRowThreads) {
-      uint4 w[kFly];
-      bool in[kFly];
-#pragma unroll
-      for (int k = 0; k < kFly; ++k) {
-        const int j = j0 + k * kRowThreads;
-        in[k] = j < words && !((mask >> (j / kRow8Words)) & 1);
-        if (in[k]) w[k] = base[j];
-      }
-#pragma unroll
-      for (int k = 0; k < kFly; ++k) {
-        if (!in[k]) continue;
-        base[j0 + k * kRowThreads] = make_uint4(requantise4(w[k].x, ratio), requantise4(w[k].y, ratio),
-                                                requantise4(w[k].z, ratio), requantise4(w[k].w, ratio));
-      }
-    }
-  }
+  ticket = __shfl_sync(0xffffffffu, ticket, 0);
+  if (ticket == 0 && old > 0.f && s > old)
+    move_group(kv8 + (size_t)g * group * kRow8Words, group, mask, old, s, row.lane, 32);
 }
 
 // groups of one slot: a row's scale is its own
-template <int kRowThreads>
 __global__ void __launch_bounds__(kThreads) q8_row_kernel(uint4* kv8, float* scales, long long num_slots,
                                                           const int32_t* __restrict__ slots,
                                                           const uint4* __restrict__ rows, int T, int* status) {
-  Row<kRowThreads> row;
+  Row row;
   row.load(slots, rows, T, num_slots, status);
   if (row.slot < 0) return;
   const float s = exp2_int(scale_exp(row.amax()));
   if (row.lane == 0) scales[row.slot] = s;
   row.store(kv8, s);
-}
-
-template <int kRowThreads>
-cudaError_t launch_rows(uint4* kv8, float* scales, long long num_slots, int group, const int32_t* slots,
-                        const uint4* rows, int T, GroupRecord* rec, int* status, cudaStream_t stream) {
-  const int threads = kRowThreads > 32 ? kRowThreads : kThreads;
-  const unsigned grid = (unsigned)(((long long)T * kRowThreads + threads - 1) / threads);
-  if (group == 1) {
-    q8_row_kernel<kRowThreads><<<grid, threads, 0, stream>>>(kv8, scales, num_slots, slots, rows, T, status);
-    return cudaGetLastError();
-  }
-  q8_need_kernel<kRowThreads><<<grid, threads, 0, stream>>>(scales, num_slots, slots, rows, T, group, rec, status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  memset(&cfg, 0, sizeof cfg);
-  cfg.gridDim = dim3(grid, 1, 1);
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, q8_store_kernel<kRowThreads>, kv8, scales, num_slots, slots, rows, T, group, rec);
-  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
@@ -285,11 +317,33 @@ cudaError_t launch_kv_write_q8(void* kv8, float* scales, long long num_slots, in
   uint4* kv = static_cast<uint4*>(kv8);
   const uint4* src = static_cast<const uint4*>(rows);
   GroupRecord* rec = static_cast<GroupRecord*>(workspace);
-  // four warps a row while that leaves the GPU's blocks few: 64 rows that join filled groups 3.8 us
-  // (4.3 with a warp a row), 608 rows 4.2 (4.4), 1216 rows 4.8 (4.3), 2432 rows 8.0 (4.8)
-  return T <= 4 * device_sm_count()
-             ? launch_rows<kFewThreads>(kv, scales, num_slots, group, slots, src, T, rec, status, stream)
-             : launch_rows<32>(kv, scales, num_slots, group, slots, src, T, rec, status, stream);
+  // One launch for the rows of a decode step: 64 rows that join as many groups 2.9 us (two launches
+  // 4.2), 304 rows 3.8 (4.4), 512 rows 6.4 (4.4).  Where groups get many rows each of these takes
+  // longer on the device: 304 rows in groups of 16 5.9 (4.5), of 64 8.6 (4.7).
+  if (group > 1 && T <= 2 * device_sm_count() && T <= kFewThreads) {
+    q8_few_kernel<<<T, kFewThreads, 0, stream>>>(kv, scales, num_slots, slots, src, T, group, status);
+    return cudaGetLastError();
+  }
+  const unsigned grid = (unsigned)(((long long)T * 32 + kThreads - 1) / kThreads);
+  if (group == 1) {
+    q8_row_kernel<<<grid, kThreads, 0, stream>>>(kv, scales, num_slots, slots, src, T, status);
+    return cudaGetLastError();
+  }
+  q8_need_kernel<<<grid, kThreads, 0, stream>>>(scales, num_slots, slots, src, T, group, rec, status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg;
+  memset(&cfg, 0, sizeof cfg);
+  cfg.gridDim = dim3(grid, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, q8_store_kernel, kv, scales, num_slots, slots, src, T, group, rec);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace sfa

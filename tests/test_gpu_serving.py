@@ -323,6 +323,76 @@ def test_kv_write_q8_bad_slots_repeats_and_nothing_to_do():
         sfa.kv_write_q8(kv8, sc, i32([1, 2]), rows[:1].cuda(), workspace=ws)
 
 
+@pytest.mark.parametrize("T", [14, 304, 305, 700])       # one launch, and two
+@pytest.mark.parametrize("bs,group", [(16, 8), (64, 64), (64, 1)])
+def test_kv_write_q8_few_rows_and_many_agree(T, bs, group):
+    # 14 rows among padding: infinities, NaN, zeros, the largest and smallest values, several rows
+    # a group, a bad slot, groups that start anew
+    rng = np.random.default_rng(T)
+    codes, scales, kv8, sc, ws = _cache(rng, 6, bs, group)
+    rows = torch.from_numpy(rng.standard_normal((T, 576))).to(torch.bfloat16)
+    slots, at = np.full(T, -1, np.int64), np.sort(rng.permutation(T)[:14])
+    slots[at] = [3, 4, 70, 5, 6 * bs, 64, 11, 9, 90, 91, 1, 2, 30, 32]
+    x = rows[torch.from_numpy(at)]
+    x[0, 3], x[0, 4], x[0, 5], x[1] = float("inf"), float("-inf"), float("nan"), 0
+    x[2], x[3], x[6], x[7] = 3e38, 1e-38, float("nan"), x[7] * 2.0 ** 40
+    rows[torch.from_numpy(at)] = x
+    codes, scales = _check_write(codes, scales, kv8, sc, ws, slots, rows, group, BAD_BLOCK)
+    # one slot named by three rows: the bytes of one of them in each place
+    before = codes_of(kv8).reshape(-1, 576)
+    slots[at] = -1
+    slots[at[:3]] = 20
+    rows[torch.from_numpy(at)] = torch.from_numpy(rng.standard_normal((14, 576))).to(torch.bfloat16)
+    sfa.kv_write_q8(kv8, sc, i32(slots), rows.cuda(), workspace=ws)
+    got, s20 = codes_of(kv8).reshape(-1, 576), float(sc.reshape(-1)[20 // group])
+    three = [serving.to_e4m3(rows[int(t)].double().numpy() / s20) for t in at[:3]]
+    assert np.all((got[20] == three[0]) | (got[20] == three[1]) | (got[20] == three[2]))
+    others = [s for s in range(6 * bs) if s // group != 20 // group]
+    assert np.array_equal(got[others], before[others]) and int(ws.sum()) == 0
+    assert sfa.last_device_status() == 0
+
+
+@pytest.mark.parametrize("T", [40, 400])
+def test_kv_write_q8_on_two_streams_and_in_a_graph(T):
+    # two caches written at the same time, then a captured write replayed over new rows and slots
+    rng = np.random.default_rng(T)
+    caches = [_cache(rng, 8, 64, 32) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    calls = [[(rng.permutation(512)[:T], torch.from_numpy(rng.standard_normal((T, 576)) * 2.0 ** k).to(torch.bfloat16))
+              for k in range(3)] for _ in range(2)]
+    dev = [[(i32(s), r.cuda()) for s, r in c] for c in calls]
+    torch.cuda.synchronize()
+    for k in range(3):
+        for j in range(2):
+            sfa.kv_write_q8(caches[j][2], caches[j][3], *dev[j][k], workspace=caches[j][4], stream=streams[j])
+    torch.cuda.synchronize()
+    state = []
+    for j in range(2):
+        c, s = caches[j][0].reshape(-1, 576), caches[j][1].reshape(-1)
+        for slots, rows in calls[j]:
+            c, s = serving.kv_write_q8(c, s, slots, rows.double().numpy(), 32)
+        got, nan = codes_of(caches[j][2]).reshape(-1, 576), (c & 127) == 127
+        assert np.array_equal((got & 127) == 127, nan) and np.array_equal(got[~nan], c[~nan])
+        assert np.array_equal(caches[j][3].double().cpu().numpy().reshape(-1), s)
+        state.append((c, s))
+    _, _, kv8, sc, ws = caches[0]
+    slots_d, rows_d = dev[0][0][0].clone(), dev[0][0][1].clone()
+    slots_d.fill_(-1)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sfa.kv_write_q8(kv8, sc, slots_d, rows_d, workspace=ws)
+    c, s = state[0]
+    for k in range(3):
+        slots, rows = rng.permutation(512)[:T], torch.from_numpy(rng.standard_normal((T, 576)) * 3.0 ** k).to(torch.bfloat16)
+        slots_d.copy_(i32(slots)), rows_d.copy_(rows)
+        g.replay()
+        c, s = serving.kv_write_q8(c, s, slots, rows.double().numpy(), 32)
+        got, nan = codes_of(kv8).reshape(-1, 576), (c & 127) == 127
+        assert np.array_equal((got & 127) == 127, nan) and np.array_equal(got[~nan], c[~nan])
+        assert np.array_equal(sc.double().cpu().numpy().reshape(-1), s) and int(ws.sum()) == 0
+    assert sfa.last_device_status() == 0
+
+
 # -------------------------------------------------------------------------- decode_q8
 def _problem(seed, B, Q, h, S, k, bs=64, group=64, spread=1, pow2=True, S_min=None, max_blocks_extra=0):
     rng = np.random.default_rng(seed)
