@@ -39,9 +39,9 @@
 // TMEM while 8-15 resolve the list.  Every wait is bounded; one that gives up records
 // SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
 //
-// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.7 us, 256 tokens x 64
-// heads x 2048 rows 91.7 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
-// rows in four shards 47.3 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
+// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.0 us, 256 tokens x 64
+// heads x 2048 rows 89.6 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
+// rows in four shards 46.2 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
 // ~2,700 cycles and the rest is the chain scores -> softmax -> P.V with one score buffer (TMEM
 // is full); the first scores come after 12,600-14,600 cycles (launch, list, table, q and the
 // first rows follow one another), the end takes 5,000, and a second round of units a whole
@@ -108,6 +108,15 @@ constexpr int kTmpCap = (kStages * kStageBytes - kOffTmp) / 4;
 static_assert(kTmpCap >= 8192, "q and a list of 8192 entries fit in stages 1 and 2");
 static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscBytes, "misc");
 
+
+// A wait that is not over at once goes on outside of the kernel's own code, which every launch
+// fetches anew: with the loops in line 64 tokens x 128 heads x 2048 rows take 45.7 us, without 45.0
+__device__ __noinline__ bool wait_slow(uint64_t* bar, uint32_t parity, long long limit, uint64_t cap_ns) {
+  return mbar_wait(bar, parity, limit, cap_ns);
+}
+__device__ __forceinline__ bool wait_bar(uint64_t* bar, uint32_t parity, long long limit, uint64_t cap_ns = 4000000000ull) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, limit, cap_ns);
+}
 constexpr long long kDrainLimit = 1LL << 40;
 constexpr uint64_t kLanded = 100000000ull;   // ns: copies in flight have landed long before (a tile that was given up
                                              // half issued never completes its barrier)
@@ -284,6 +293,10 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   return v;
 }
 
+__device__ __noinline__ void give_up(int* status, volatile int* abort_s) {
+  report_status(status, kStatusTimeout);
+  *abort_s = 1;
+}
 // NH: padded heads of a unit (32 or 64), the N of P.V
 template <int NH, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -401,11 +414,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) >> g_shift : 0;
   };
   auto fail = [&](void) {
-    report_status(p.status, kStatusTimeout);
-    *abort_s = 1;
+    give_up(p.status, abort_s);
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, wl));
   };
 
   // warps 0-7: warp 4 half + quad holds heads 16 quad + 8 half .. + 7 whole, a thread one of
@@ -520,15 +532,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) fail();
       // no gather of this CTA may still be landing in shared memory at exit
       for (int k = n > kStages ? n - kStages : 0; k < n; ++k)
-        if (!__all_sync(0xffffffffu, mbar_wait(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit, kLanded)))
+        if (!__all_sync(0xffffffffu, wait_bar(&bars[kBarKvFull + k % kStages], (k / kStages) & 1, kDrainLimit, kLanded)))
           report_status(p.status, kStatusTimeout);
     } else if (warp == kRowWarp) {
       // =================== the rows' scales, and the rest of a long list ==============
-      // Scales are single words anywhere in memory: those of the next four tiles are in flight
-      // while four are published.  A segment of the list begins with a group of four (64 tiles,
-      // dealt to at most 8 CTAs).
-      constexpr int kAhead = 4, kPer = kNt / 32;
-      static_assert(kListCap / kNt % (8 * kAhead) == 0, "segments begin with a group");
+      // Scales are single words anywhere in memory: those of the next two tiles are in flight
+      // while two are published.  A segment of the list begins with a pair (64 tiles, dealt to at
+      // most 8 CTAs).
+      constexpr int kAhead = 2, kPer = kNt / 32;
+      static_assert(kListCap / kNt % (8 * kAhead) == 0, "segments begin with a pair");
       float cur[kAhead][kPer], nxt[kAhead][kPer];
       int seg = 0, j = seg_s[0], ord = seg_s[1];   // the next segment's first round, entries before it
       bool ok = true;
@@ -671,15 +683,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* fin_bar = &bars[warp == kQkWarp ? kBarMmaFin : kBarMmaFin2];
         if (elect_one()) mma_commit(fin_bar);
         __syncwarp();
-        if (!__all_sync(0xffffffffu, mbar_wait(fin_bar, 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
+        if (!__all_sync(0xffffffffu, wait_bar(fin_bar, 0, kDrainLimit))) report_status(p.status, kStatusTimeout);
       }
     }
   } else {
     // ---- q as hi and lo e4m3 rows, a head a warp as it lands, in place in shared memory (stages
     // 1 and 2, which the gathers leave alone until q is ready); then to the TMEM lanes
-#pragma unroll 2
+#pragma unroll 1
     for (int hd = wq; hd < NH; hd += kQWarps) {
-      if (hd < nh && !__all_sync(0xffffffffu, mbar_wait(&bars[kBarQLoad + hd / kQWarps], 0, kDrainLimit)))
+      if (hd < nh && !__all_sync(0xffffffffu, wait_bar(&bars[kBarQLoad + hd / kQWarps], 0, kDrainLimit)))
         report_status(p.status, kStatusTimeout);
       char* at = qst + hd * kQPitch;
       uint4 x[3];
