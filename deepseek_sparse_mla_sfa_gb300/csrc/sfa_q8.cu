@@ -973,26 +973,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   // 32-column segment 4m + quad of O goes to CTA (4m + quad) / segs, into its idle stages, slot
-  // of this CTA: [lane][NH], 16-byte words swizzled by lane
+  // of this CTA: [head][32 columns], so that a store is 128 bytes in one place (as 16 bytes a lane,
+  // in 32 places, the exchange of 64 heads took several us)
   const int segs = 16 >> g_shift;
   float* recv = reinterpret_cast<float*>(smem);
 #pragma unroll 1
   for (int c = warp >> 2; c < 4 * HB; c += kThreads / 128) {
     const int m = c / HB, hb = 16 * (c % HB), sg = 4 * m + (warp & 3);
+    if (hb >= nh) continue;
     uint32_t o[16];
     if (have_o) {
       tmem_ld16(my_lanes + kColO + 16 * c, o);
       tmem_ld_wait();
     }
-    const uint32_t dst = mapa(recv + ((size_t)(crank * segs + (sg & (segs - 1))) * 32 + lane) * NH, sg / segs);
+    const uint32_t dst = mapa(recv + ((size_t)(crank * segs + (sg & (segs - 1))) * NH + hb) * 32 + lane, sg / segs);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      float f[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) f[u] = have_o ? __uint_as_float(o[4 * k + u]) * scale_s[hb + 4 * k + u] : 0.f;
-      st_cluster_v4(dst + 16u * ((hb / 4 + k) ^ (lane & (NH / 4 - 1))), __float_as_uint(f[0]), __float_as_uint(f[1]),
-                    __float_as_uint(f[2]), __float_as_uint(f[3]));
-    }
+    for (int k = 0; k < 16; ++k)
+      st_cluster_f32(dst + 128u * k, have_o ? __uint_as_float(o[k]) * scale_s[hb + k] : 0.f);
   }
   tc_fence_before();
   cluster_sync();   // every CTA's scaled partial O has landed with its owner
@@ -1003,13 +1000,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int x = warp; x < segs * (NH / 4); x += kThreads / 32) {
     const int sg = x & (segs - 1), k4 = x / segs;
     if (4 * k4 >= nh) break;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (uint32_t c = 0; c < G; ++c) {
-      const float4 y = *reinterpret_cast<const float4*>(recv + ((size_t)(c * segs + sg) * 32 + lane) * NH +
-                                                        4 * (k4 ^ (lane & (NH / 4 - 1))));
-      a.x += y.x; a.y += y.y; a.z += y.z; a.w += y.w;
-    }
-    const float f[4] = {a.x, a.y, a.z, a.w};
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+    const float* src = recv + ((size_t)sg * NH + 4 * k4) * 32 + lane;
+    for (uint32_t c = 0; c < G; ++c)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] += src[(size_t)c * segs * NH * 32 + 32 * k];
     const size_t at = out_at + 32 * ((int)crank * segs + sg) + lane;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -1108,13 +1103,13 @@ cudaError_t launch_decode_q8(const DecodeQ8Params& qp, cudaStream_t stream) {
   kp.groups = (p.h + kGroupHeads - 1) / kGroupHeads;
   kp.group_heads = (p.h + kp.groups - 1) / kp.groups;
   const long long units = T * p.n_splits * kp.groups;
-  // A unit is shared by up to 8 CTAs while all its clusters run at once and a CTA keeps more than
-  // two tiles of the list (the merge costs 3-4 us for two CTAs and 1-2 more for each doubling; a
-  // tile 1.2).  9 tokens x 16 heads x 2048 rows, by 1, 2, 4, 8 CTAs: 33, 23, 18, 17 us; 64 heads 41,
-  // 30, 25, 25; 300 rows 16, 18, 18, 22.  (38 units by 4 CTAs, which do not run at once: 37 us, by 2:
-  // 25.)
+  // A unit is shared by up to 8 CTAs while all clusters run at once and there is more than a tile of
+  // the list for each of half as many (three tiles for the first split).  9 tokens x 16 heads x 2048
+  // rows, by 1, 2, 4, 8 CTAs: 33, 22, 16, 13 us; 64 heads 41, 29, 22, 19; 300 rows 12, 11, 10, 11 and
+  // 15, 16, 15, 16; 180 rows 9.4, 10.1, 9.7, 10.2.  (38 units by 4 CTAs, which do not run at once: 32 us,
+  // by 2: 23.)
   int G = 1;
-  for (int k = 0; k < 3 && units <= fit[k] && p.top_k > 4 * G * kNt; ++k) G *= 2;
+  for (int k = 0; k < 3 && units <= fit[k] && p.top_k > (G > 2 ? G : 3) * kNt; ++k) G *= 2;
   if (units * G > 0x7fffffffLL) return cudaErrorInvalidValue;
   const bool il = p.interleave > 0 && p.n_splits > 1;
   // 32 padded heads or 64: 100 tokens x 32 heads x 2048 rows 39.8 us, as 64 heads 41.8; 4 tokens 15.7, 22.2

@@ -493,6 +493,15 @@ def test_decode_q8_units_shared_by_several_ctas(h, k):
     assert sfa.last_device_status() == 0
 
 
+@pytest.mark.parametrize("h,B", [(16, 50), (33, 60), (100, 25)])
+def test_decode_q8_units_shared_by_two_ctas(h, B):
+    # more units than clusters of four that run at once, fewer than of two
+    pr = _problem(2000 + h, B, 1, h, 900, 500, S_min=0)
+    for dtype in (torch.float32, torch.bfloat16):
+        _close(*_run(pr, dtype=dtype), [x[0] for x in _oracle(pr)], f"{dtype}")
+    assert sfa.last_device_status() == 0
+
+
 @pytest.mark.parametrize("h,B,k", [(4, 1, 20000), (4, 80, 13000), (64, 1, 12289)])
 def test_decode_q8_lists_of_several_segments(h, B, k):
     # lists of more than two of the kernel's 6144-row segments, with every entry used: positions
