@@ -30,7 +30,7 @@
 //     the products: 48.9 -> 47.4 us below).  E^T is the same tile read MN-major.
 // TMEM: q 144 columns, S 96 (two of them for 32 heads or fewer), O^T up to 256.
 //
-// With few units a cluster of G CTAs shares one: CTA c takes tiles c, c + G, ...; they merge
+// With few units a cluster of G CTAs shares one: CTA c takes every G-th 96 entries of the list; they merge
 // (O, m, l) over distributed shared memory at the end.
 //
 // Warp roles (640 threads): warps 0-7 softmax (each 8 heads whole); 8 issues QK^T, 9 P.V; 10-13
@@ -227,12 +227,30 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
 }
 __device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// entries j0 + 32 k + lane < c_end (k < 8) of the selected list, -1 behind its end
-__device__ __forceinline__ void load8(const int32_t* idx, int j0, int c_end, int lane, int (&pos)[8]) {
+// A CTA's part of the selected list: of the G CTAs that share a unit, CTA c takes the blocks of 96
+// entries c, c + G, ... (each resolves its own entries only: with every CTA resolving the whole list
+// one token x 16 heads x 16384 rows took 72 us, not 34)
+struct ListPart {
+  const int32_t* idx;
+  int top_k, g_shift, crank;
+  __device__ __forceinline__ int entries() const {
+    const int blocks = (top_k + kNt - 1) / kNt, g = 1 << g_shift;
+    if (blocks <= crank) return 0;
+    const int mine = ((blocks - crank + g - 1) >> g_shift) * kNt;
+    return ((blocks - 1) & (g - 1)) == crank ? mine - (blocks * kNt - top_k) : mine;
+  }
+  // where entry x of the part is in the list
+  __device__ __forceinline__ int at(int x) const {
+    return x + kNt * (x / kNt * ((1 << g_shift) - 1) + crank);
+  }
+};
+
+// entries j0 + 32 k + lane < end (k < 8) of the part, -1 behind its end
+__device__ __forceinline__ void load8(const ListPart& list, int j0, int end, int lane, int (&pos)[8]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const int j = j0 + 32 * k + lane;
-    pos[k] = j < c_end ? __ldg(idx + j) : -1;
+    const int x = j0 + 32 * k + lane;
+    pos[k] = x < end ? __ldg(list.idx + list.at(x)) : -1;
   }
 }
 // their rows, -1 for those that do not resolve to a row of this unit; returns how many do
@@ -337,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int h0 = hg * kp.group_heads, nh = min(kp.group_heads, p.h - h0);
   const int b = div_by(t, kp.Q_mul, kp.Q_shift), qi = t - b * p.Q;
   const int bt_row = p.bt_per_token ? t : b;
-  const int32_t* idx = p.topk_idx + (size_t)t * p.top_k;
+  const ListPart list{p.topk_idx + (size_t)t * p.top_k, p.top_k, g_shift, (int)crank};
+  const int entries = list.entries();
   const uint4* qsrc = reinterpret_cast<const uint4*>(p.q + ((size_t)t * p.h + h0) * kDQK);
   const long long wl = p.wait_limit;
 
@@ -345,17 +364,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Warps 0-7 and 16-19 bring q into TMEM; meanwhile warps 8-15 resolve the list and start the
   // gathers.  The first loads of both go out before anything waits.
   const int wq = warp < kSoftWarps ? warp : warp - kListWarps;    // of the kQWarps that bring q
-  const int chunk = ((p.top_k + kListWarps * 32 - 1) / (kListWarps * 32)) * 32;
-  const int c_begin = min((warp - kSoftWarps) * chunk, p.top_k), c_end = min(c_begin + chunk, p.top_k);
+  const int chunk = ((entries + kListWarps * 32 - 1) / (kListWarps * 32)) * 32;
+  const int c_begin = min((warp - kSoftWarps) * chunk, entries), c_end = min(c_begin + chunk, entries);
   int pos_r[8];
   // (a list of one round, 8 entries a lane, is loaded to registers, a longer one to shared
   // memory, where each warp then compacts its part in place; the longest come round by round)
   const bool one_round = chunk <= 256, staged = !one_round && kListWarps * chunk <= kTmpCap;
   int* const tmp = reinterpret_cast<int*>(smem + kOffTmp) + (warp - kSoftWarps) * chunk;
   if (warp >= kSoftWarps && warp < kFixWarp) {
-    if (one_round) load8(idx, c_begin, c_end, lane, pos_r);
+    if (one_round) load8(list, c_begin, c_end, lane, pos_r);
     if (staged)
-      for (int j = c_begin + lane; j < c_end; j += 32) cp_async4(smem_u32(tmp + j - c_begin), idx + j);
+      for (int x = c_begin + lane; x < c_end; x += 32) cp_async4(smem_u32(tmp + x - c_begin), list.idx + list.at(x));
   }
   char* const qst = smem + kStageBytes;
   if (threadIdx.x == 0) {
@@ -408,11 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ---- index resolution (warps 8-15): count per warp chunk, then ordered compaction ----
   int total = 0;
-  int n_tiles = 0, n_local = 0;
-  auto count_tiles = [&]() {
-    n_tiles = (total + kNt - 1) / kNt;
-    n_local = n_tiles > (int)crank ? (n_tiles - (int)crank + (int)G - 1) >> g_shift : 0;
-  };
+  int n_local = 0;                         // tiles
+  auto count_tiles = [&]() { n_local = (total + kNt - 1) / kNt; };
   auto fail = [&](void) {
     give_up(p.status, abort_s);
   };
@@ -451,9 +467,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           pos_r[k] = j < c_end ? tmp[j - c_begin] : -1;       // what this lane copied
         }
       } else if (!one_round) {
-        load8(idx, j0, c_end, lane, pos_r);
+        load8(list, j0, c_end, lane, pos_r);
       }
-      const int mine = resolve8<kInterleaved>(kp, pos_r, sel, bt_row, crank == 0 && hg == 0, row_r);
+      const int mine = resolve8<kInterleaved>(kp, pos_r, sel, bt_row, hg == 0, row_r);
       if (staged) cnt = compact(tmp, cnt, chunk); else cnt += __reduce_add_sync(0xffffffffu, mine);
     }
     if (lane == 0) wcount_s[warp - kSoftWarps] = cnt;
@@ -473,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int j0 = c_begin; j0 < c_end && off <= kListCap; j0 += 256) {
         int pos[8];
-        load8(idx, j0, c_end, lane, pos);
+        load8(list, j0, c_end, lane, pos);
         resolve8<kInterleaved>(kp, pos, sel, bt_row, false, row_r);
         const int before = off;
         off = compact(list_s, off, kListCap);
@@ -506,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0 && !(ok = n >= kStages ? wait_warp(&bars[kBarKvEmpty + at], ((n / kStages) - 1) & 1)
                                          : wait_warp(&bars[kBarQReady], 0)))
           break;
-        const int first = kNt * ((int)crank + (int)G * n);
+        const int first = kNt * n;
         if (first >= (seg + 1) * kListCap) {      // more valid entries than the list holds
           if (lane == 0) mbar_arrive(&bars[kBarSegFree]);
           if (!(ok = wait_warp(&bars[kBarSegFull], seg & 1))) break;
@@ -537,17 +553,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kRowWarp) {
       // =================== the rows' scales, and the rest of a long list ==============
       // Scales are single words anywhere in memory: those of the next two tiles are in flight
-      // while two are published.  A segment of the list begins with a pair (64 tiles, dealt to at
-      // most 8 CTAs).
+      // while two are published.  A segment of the list (64 tiles) begins with a
+      // pair.
       constexpr int kAhead = 2, kPer = kNt / 32;
-      static_assert(kListCap / kNt % (8 * kAhead) == 0, "segments begin with a pair");
+      static_assert(kListCap / kNt % kAhead == 0, "segments begin with a pair");
       float cur[kAhead][kPer], nxt[kAhead][kPer];
       int seg = 0, j = seg_s[0], ord = seg_s[1];   // the next segment's first round, entries before it
       bool ok = true;
       auto load4 = [&](int n0, float (&v)[kAhead][kPer]) {
   #pragma unroll
         for (int d = 0; d < kAhead; ++d) {
-          const int* rows = list_s + kNt * ((int)crank + (int)G * (n0 + d)) - seg * kListCap + lane;
+          const int* rows = list_s + kNt * (n0 + d) - seg * kListCap + lane;
   #pragma unroll
           for (int u = 0; u < kPer; ++u) {
             const int row = n0 + d < n_local ? rows[32 * u] : kp.num_rows;
@@ -558,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       load4(0, cur);
   #pragma unroll 1
       for (int n0 = 0; n0 < n_local && ok && !*abort_s; n0 += kAhead) {
-        const int first = kNt * ((int)crank + (int)G * (n0 + kAhead));
+        const int first = kNt * (n0 + kAhead);
         const bool more = n0 + kAhead < n_local, turn = more && first >= (seg + 1) * kListCap;
         if (more && !turn) load4(n0 + kAhead, nxt);
   #pragma unroll
@@ -587,9 +603,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++seg;
           const int base = seg * kListCap;
   #pragma unroll 1
-          while (j < p.top_k) {
+          while (j < entries) {
             int pos[8], row[8], to = ord;
-            load8(idx, j, p.top_k, lane, pos);
+            load8(list, j, entries, lane, pos);
             resolve8<kInterleaved>(kp, pos, sel, bt_row, false, row);
   #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -602,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ord = to;
             j += 256;
           }
-          for (int o = total - base + lane; o < min(n_tiles * kNt - base, kListCap); o += 32) list_s[o] = kp.num_rows;
+          for (int o = total - base + lane; o < min(n_local * kNt - base, kListCap); o += 32) list_s[o] = kp.num_rows;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarSegFull]);
           load4(n0 + kAhead, nxt);
