@@ -297,7 +297,8 @@ __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* s
     move_group(kv8 + (size_t)g * group * kRow8Words, group, mask, old, s, row.lane, 32);
 }
 
-// groups of one slot: a row's scale is its own
+// groups of one slot: a row's scale is its own (of a slot named twice parts of both rows are kept, and
+// one row's scale)
 __global__ void __launch_bounds__(kThreads) q8_row_kernel(uint4* kv8, float* scales, long long num_slots,
                                                           const int32_t* __restrict__ slots,
                                                           const uint4* __restrict__ rows, int T, int* status) {

@@ -1086,13 +1086,13 @@ cudaError_t prepare_decode_q8(int (&fit)[3]) {
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!ready[dev].load(std::memory_order_acquire)) {
+    static std::mutex once;
+    const std::lock_guard<std::mutex> hold(once);
     for (auto kernel : {q8_kernel<32, false>(), q8_kernel<32, true>(), q8_kernel<64, false>(), q8_kernel<64, true>()}) {
       e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
       if (e != cudaSuccess) return e;
     }
-    static std::mutex once;
-    const std::lock_guard<std::mutex> hold(once);
-    for (int k = 0; k < 3; ++k) {
+    for (int k = 0; k < 3 && !ready[dev].load(std::memory_order_relaxed); ++k) {
       cudaLaunchConfig_t cfg;
       cudaLaunchAttribute attr[1];
       launch_config(cfg, attr, 1, 2 << k, 0);
