@@ -15,10 +15,11 @@
 //
 // Bound: HBM, each element read and written once.  A block takes some tokens (and, for few
 // tokens of many heads, a part of their heads): it forms the cosines and sines of its tokens
-// once, in shared memory, and its threads then walk the rows with 4 pairs each.  Latency is
-// hidden by eight blocks an SM (32 registers a thread), not by rows in flight a thread: 4096
-// tokens x 64 heads x 64 columns, strided, take 16.4 us; 20.8 us with the registers free, 26 us
-// with four rows in flight, 33 us with eight.  (A dense copy of as many bytes takes 11.7 us.)
+// once, in shared memory, and its threads then walk the rows with 8 pairs each (4 of fp32).
+// Latency is hidden by eight blocks an SM (32 registers a thread), not by rows in flight a thread:
+// 4096 tokens x 64 heads x 64 columns, strided, take 14.9 us; 16.5 us with more registers.  With 4
+// pairs a thread and 8 rows each it was 16.4 us, then 20.8 with the registers free, 26 with four
+// rows in flight, 33 with eight.  (A dense copy of as many bytes takes 11.7 us.)
 #include <cuda_fp16.h>
 
 #include "sfa_internal.h"
@@ -93,9 +94,9 @@ __device__ __forceinline__ void store_elems(E* p, const E (&v)[N]) {
 }
 
 constexpr int kRopeSmem = 32768;   // cosines and sines of a block's tokens
-constexpr int kRopeItems = 8;      // most pair groups a thread
+constexpr int kRopeItems = 4;      // most pair groups a thread
 
-// VP pairs a thread: 4 where every access is aligned for it, else 1
+// VP pairs a thread: 8 (16-bit types) or 4 where every access is aligned for it, else 1
 template <typename E, int VP, bool kInterleaved>
 __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams p) {
   extern __shared__ float2 cs_s[];                        // [tokens][rot / 2], then the positions
@@ -186,15 +187,19 @@ cudaError_t launch_typed(RopeParams p, cudaStream_t stream) {
 
 template <typename E>
 cudaError_t launch_rope_t(const RopeParams& p, cudaStream_t stream) {
-  // 4 pairs a thread need 4 * 2 (interleaved) or 4 (halves) consecutive elements at an
-  // address that is a multiple of the access (at most 16 bytes)
-  const size_t run = (p.interleaved ? 8 : 4) * sizeof(E), acc = run < 16 ? run : 16;
-  const auto ok = [&](const void* q, long long a, long long b) {
-    return reinterpret_cast<uintptr_t>(q) % acc == 0 && (a * sizeof(E)) % acc == 0 && (b * sizeof(E)) % acc == 0;
+  // VP pairs a thread need 2 VP (interleaved) or VP (halves) consecutive elements at an address that
+  // is a multiple of the access (at most 16 bytes)
+  const auto fits = [&](int vp) {
+    const size_t run = (p.interleaved ? 2 : 1) * vp * sizeof(E), acc = run < 16 ? run : 16;
+    const auto ok = [&](const void* q, long long a, long long b) {
+      return reinterpret_cast<uintptr_t>(q) % acc == 0 && (a * sizeof(E)) % acc == 0 && (b * sizeof(E)) % acc == 0;
+    };
+    return p.rot % (2 * vp) == 0 && ok(p.x, p.xt, p.xn) && ok(p.out, p.ot, p.on) &&
+           (p.interleaved || (p.rot / 2 * sizeof(E)) % acc == 0);
   };
-  const bool vec = p.rot % 8 == 0 && ok(p.x, p.xt, p.xn) && ok(p.out, p.ot, p.on) &&
-                   (p.interleaved || (p.rot / 2 * sizeof(E)) % acc == 0);
-  return vec ? launch_typed<E, 4>(p, stream) : launch_typed<E, 1>(p, stream);
+  // 8 pairs of a 16-bit type are 16-byte accesses: 4096 x 64 x 64 columns 14.9 us, by 4 pairs 16.4
+  if (sizeof(E) == 2 && fits(8)) return launch_typed<E, sizeof(E) == 2 ? 8 : 4>(p, stream);
+  return fits(4) ? launch_typed<E, 4>(p, stream) : launch_typed<E, 1>(p, stream);
 }
 
 }  // namespace

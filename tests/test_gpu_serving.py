@@ -177,6 +177,21 @@ def test_rope_strides_offsets_and_padding_rows_of_out():
     assert y2.shape == (9, 64) and torch.equal(y2[1], src[1, 0, :64])
 
 
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("rot", [64, 48, 40, 24, 16])
+@pytest.mark.parametrize("off", [0, 1, 4, 8, 12])
+def test_rope_of_16_bit_types_at_every_alignment(interleaved, rot, off):
+    # 8 pairs a thread, 4 or one, by the alignment of rows and the number of pairs
+    g = torch.Generator().manual_seed(100 * rot + off)
+    src = torch.randn((11, 3, 96), generator=g).to(torch.bfloat16).cuda()
+    dst = torch.full((11, 3, 120), 7.0, dtype=torch.bfloat16, device="cuda")
+    x, out = src[..., off:off + rot + 8], dst[..., 2 * off:2 * off + rot + 8]
+    pos = torch.arange(11, dtype=torch.int32).mul_(977).cuda()
+    _check_rope(x, pos, sfa.rope_inv_freq(rot), out=out, interleaved=interleaved)
+    assert torch.equal(out[..., rot:], x[..., rot:])
+    assert torch.all(dst[..., :2 * off] == 7.0) and torch.all(dst[..., 2 * off + rot + 8:] == 7.0)
+
+
 @pytest.mark.parametrize("dtype,width,rot", [(torch.bfloat16, 64, 64), (torch.float16, 72, 64), (torch.float32, 21, 14)])
 def test_rope_padding_rows_of_a_new_out_are_those_of_x(dtype, width, rot):
     g = torch.Generator().manual_seed(8)
