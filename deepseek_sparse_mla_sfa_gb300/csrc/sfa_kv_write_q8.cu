@@ -18,7 +18,7 @@
 // take one launch.
 //
 // Bound: HBM, 1152 bytes read and 576 written a row, and the wait of the second launch for the
-// first's atomics: 8885 rows in groups of 16 take 9.5 us (2.3 us of bytes).  Latency for a decode
+// first's atomics: 8885 rows in groups of 16 take 8.9 us (2.3 us of bytes; the first launch 4.0).  Latency for a decode
 // step's rows: 64 rows that each join a filled group of 64 take 2.9 us, a chain of slots, rows, the
 // group's largest value and, where its scale rose, its other rows.
 #include <cuda_fp8.h>
@@ -31,7 +31,8 @@ namespace {
 
 constexpr int kRowWords = kDQK * 2 / 16;   // 72 x 16 bytes per bf16 row
 constexpr int kRow8Words = kDQK / 16;      // 36 x 16 bytes per e4m3 row
-constexpr int kThreads = 256;         // 8 rows a block, a warp each
+constexpr int kThreads = 128, kBlocks = 16;   // a warp a row; 64 warps an SM (32 registers a thread): 8.9 us
+                                              // for 8885 rows in groups of 16, 9.4 with the registers free
 constexpr int kFewThreads = 512;      // of a block that takes a group, and as many slots a call at most
 constexpr int kMinExp = -100, kMaxExp = 120;
 
@@ -144,8 +145,9 @@ struct Row {
 };
 
 // the rows of the group at `base` whose bit of `mask` is clear: from scale `old` to `s`, by the
-// threads `thread` of `threads`
-__device__ __forceinline__ void move_group(uint4* base, int group, unsigned long long mask, float old, float s,
+// threads `thread` of `threads` (out of line: rare, and its words in flight would take the kernels'
+// registers)
+__device__ __noinline__ void move_group(uint4* base, int group, unsigned long long mask, float old, float s,
                                            int thread, int threads) {
   const float ratio = old / s;
   const int words = group * kRow8Words;
@@ -262,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) q8_need_kernel(const float* __restri
   }
 }
 
-__global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* scales, long long num_slots,
+__global__ void __launch_bounds__(kThreads, kBlocks) q8_store_kernel(uint4* kv8, float* scales, long long num_slots,
                                                             const int32_t* __restrict__ slots,
                                                             const uint4* __restrict__ rows, int T, int group,
                                                             GroupRecord* rec) {
@@ -277,20 +279,20 @@ __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* s
   const float old = scale_before(was, mask);
   const float s = fmaxf(old, exp2_int(__ldcg(&r->need) - 1 + kMinExp));
   const int count = __ldcg(&r->count);
-  row.store(kv8, s);
   __syncwarp();                                  // every thread has its copy of the record
   int ticket = 0;
   if (row.lane == 0) {
-    __threadfence();
+    __threadfence();                             // (its reads come before the count; what is stored below need not)
     ticket = atomicAdd(&r->done, 1);
-    if (ticket == count - 1) {                   // every row of the group has read the record
-      scales[g] = s;
-      r->need = 0;
-      r->old = 0.f;
-      r->count = 0;
-      r->done = 0;
-      r->mask = 0;
-    }
+  }
+  row.store(kv8, s);
+  if (row.lane == 0 && ticket == count - 1) {    // every row of the group has read the record
+    scales[g] = s;
+    r->need = 0;
+    r->old = 0.f;
+    r->count = 0;
+    r->done = 0;
+    r->mask = 0;
   }
   ticket = __shfl_sync(0xffffffffu, ticket, 0);
   if (ticket == 0 && old > 0.f && s > old)
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kThreads) q8_store_kernel(uint4* kv8, float* s
 
 // groups of one slot: a row's scale is its own (of a slot named twice parts of both rows are kept, and
 // one row's scale)
-__global__ void __launch_bounds__(kThreads) q8_row_kernel(uint4* kv8, float* scales, long long num_slots,
+__global__ void __launch_bounds__(kThreads, kBlocks) q8_row_kernel(uint4* kv8, float* scales, long long num_slots,
                                                           const int32_t* __restrict__ slots,
                                                           const uint4* __restrict__ rows, int T, int* status) {
   Row row;
