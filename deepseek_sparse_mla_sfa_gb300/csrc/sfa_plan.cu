@@ -13,19 +13,14 @@
 // read from the free list, never from the table entry that another CTA writes.
 //
 // Bound: latency (a launch, one dependent load of the lengths, a scan, one load of the table or the
-// free list); a step's outputs are 8 bytes a token.  64 requests of one token take 4.4 us on the
-// device, 512 requests of up to 300 tokens 7.8 us.  A CTA takes 2048 tokens (four a thread): the
-// sums cost every CTA the same, so more CTAs than that only repeat them.
+// free list); a step's outputs are 8 bytes a token.  64 requests of one token take 3.9 us on the
+// device, 512 requests of up to 300 tokens 5.5 us.
 #include <climits>
 
 #include "sfa_internal.h"
 
 namespace sfa {
 namespace {
-
-constexpr int kPlanThreads = 512;
-constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kTokensPerCta = 4 * kPlanThreads;
 
 struct PlanParams {
   const int32_t* cached;
@@ -65,7 +60,9 @@ __device__ __forceinline__ int blocks_of(long long tokens, int bs, int most) {
   return n < most ? (int)n : most;
 }
 
+template <int kPlanThreads>
 __global__ void __launch_bounds__(kPlanThreads) step_plan_kernel(const PlanParams p) {
+  constexpr int kPlanWarps = kPlanThreads / 32;
   extern __shared__ int plan_smem[];
   int* tok_s = plan_smem;               // [B + 1] first token of each request
   int* blk_s = plan_smem + p.B + 1;     // [B + 1] fresh blocks of the requests before
@@ -171,16 +168,24 @@ cudaError_t launch_step_plan(const int32_t* cached, const int32_t* fresh_tokens,
                              cudaStream_t stream) {
   const PlanParams p{cached, fresh_tokens, B,        block_size,  table,     max_blocks, free_blocks, num_free,
                      taken,  num_tokens,   seq_lens, token_start, positions, slots,      taken_out,   status};
-  const int most = 4 * device_sm_count();
-  int grid = (num_tokens + kTokensPerCta - 1) / kTokensPerCta;
-  grid = grid < 1 ? 1 : grid > most ? most : grid;
+  // Few requests: small blocks and a token a thread (64 requests 3.9 us, by 512 threads 4.4; 512
+  // requests of up to 300 tokens 5.5, with four tokens a thread 7.5).  Many: more threads for the
+  // sums, and from some thousands on fewer blocks that form them (8192 requests of 20 tokens 24 us,
+  // with a token a thread 49; of 256 threads 128; 4096 requests 8.6 with one, 12.0 with four).
+  const bool wide = B > 1024;
+  const int threads = wide ? 512 : 256, per_block = (B > 4096 ? 4 : 1) * threads, most = 4 * device_sm_count();
+  long long blocks = ((long long)num_tokens + per_block - 1) / per_block;
+  const int grid = (int)(blocks < 1 ? 1 : blocks > most ? most : blocks);
   const size_t smem = (size_t)(2 * (B + 1)) * 4;
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(step_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(step_plan_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)(2 * (kPlanMaxRequests + 1) * 4));
     if (e != cudaSuccess) return e;
   }
-  step_plan_kernel<<<grid, kPlanThreads, smem, stream>>>(p);
+  if (wide)
+    step_plan_kernel<512><<<grid, threads, smem, stream>>>(p);
+  else
+    step_plan_kernel<256><<<grid, threads, smem, stream>>>(p);
   return cudaGetLastError();
 }
 

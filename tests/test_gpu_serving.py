@@ -62,6 +62,11 @@ def test_step_plan_matches_oracle(B, bs, max_cached, max_new):
     _check_plan(_plan_case(np.random.default_rng(B * 1000 + bs), B, bs, max_cached, max_new), bs)
 
 
+@pytest.mark.parametrize("B", [256, 257, 1024, 1025, 4096, 4097])
+def test_step_plan_block_sizes_of_the_kernel(B):
+    _check_plan(_plan_case(np.random.default_rng(B), B, 16, 40, 5), 16)
+
+
 def test_step_plan_empty_and_negative_lengths():
     got = sfa.step_plan(i32([]), i32([]), torch.empty((0, 4), dtype=torch.int32, device="cuda"), i32([1]), i32([1]), 16, 3)
     assert got[2].tolist() == [0] and got[3].tolist() == [-1] * 3 and got[5].tolist() == [1]
