@@ -41,7 +41,7 @@
 //
 // Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.0 us, 256 tokens x 64
 // heads x 2048 rows 89.6 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
-// rows in four shards 46.2 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
+// rows in four shards 46.8 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
 // ~2,700 cycles and the rest is the chain scores -> softmax -> P.V with one score buffer (TMEM
 // is full); the first scores come after 12,600-14,600 cycles (launch, list, table, q and the
 // first rows follow one another), the end takes 5,000, and a second round of units a whole
