@@ -502,6 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the last tile's missing rows: an index past the cache, which the gathers read as zeros
     if (warp == kSoftWarps)
       for (int o = total + lane; o < min((total + kNt - 1) / kNt * kNt, kListCap); o += 32) list_s[o] = kp.num_rows;
+    // the gathers of the producer warps (async proxy) write over the staged list: every list warp's
+    // accesses to it (generic proxy) come before them
+    if (staged) fence_proxy_async_smem();
     named_barrier(4, 32 * kListWarps);
     if (lane == 0 && warp == kSoftWarps) wcount_s[kListWarps] = total;
     __syncwarp();

@@ -544,6 +544,26 @@ def test_decode_q8_lists_of_several_segments(h, B, k):
     assert sfa.last_device_status() == 0
 
 
+@pytest.mark.parametrize("h,B,k,holes", [(16, 160, 2049, False), (64, 160, 3000, True), (8, 3, 17000, True), (4, 160, 8192, False)])
+def test_decode_q8_lists_staged_where_the_gathers_land(h, B, k, holes):
+    # lists of more than 2048 entries a CTA wait in the stages that the first gathers fill: by one CTA
+    # a token and by several, with and without entries that leave the list; the same bits every time
+    pr = _problem(3000 + k, B, 1, h, 500, 500)
+    rng = np.random.default_rng(k)
+    pr["idx"] = np.stack([rng.integers(0, int(n), k) for n in pr["sl"]])
+    if holes:
+        pr["idx"][rng.random(pr["idx"].shape) < 0.3] = -1
+    d = _device(pr)
+    out, lse = sfa.decode_q8(*d, SCALE)
+    for t in (0, B - 1):
+        one = dict(pr, q=pr["q"][t:t + 1], bt=pr["bt"][t:t + 1], sl=pr["sl"][t:t + 1], idx=pr["idx"][t:t + 1])
+        _close(out[t:t + 1], lse[t:t + 1], [x[0] for x in _oracle(one)], f"token {t}")
+    for _ in range(10):
+        o, l = sfa.decode_q8(*d, SCALE)
+        assert torch.equal(o, out) and torch.equal(l, lse)
+    assert sfa.last_device_status() == 0
+
+
 @pytest.mark.parametrize("bs,group", [(64, 1), (64, 16), (16, 16), (24, 8), (1, 1), (128, 128), (7, 7), (100, 50)])
 def test_decode_q8_block_sizes_and_scale_groups(path, bs, group):
     pr = _problem(bs + group, 2, 2, 40, 333, 200, bs=bs, group=group, S_min=50, max_blocks_extra=3)
