@@ -5,18 +5,21 @@
 // row's e4m3 values, c_j the scale of its group of slots): s_j = scale * c_j * (q . e_j),
 // out = sum_j p_j c_j e_j / sum_j p_j, p_j = exp(s_j).
 //
-// Both contractions run as kind::f8f6f4 on the cache's bytes, with no dequantised copy of
+// Both contractions run as 8-bit products (kind::f8f6f4, kind::mxf8f6f4) on the cache's bytes, with no dequantised copy of
 // them; the other operand is split into two e4m3 terms:
 //   * q: a bf16 value has 8 significant bits, e4m3 has 4, so q = hi + lo exactly (under a
 //     power-of-two scale per head; lo is stored times 16, and only values below 2^-22 of the
 //     head's largest are rounded).  hi and lo are two rows of M: 64 heads fill M = 128 and
 //     QK^T costs what one bf16 pass over half the bytes would.
-//   * weights: P_j = p_j c_j is stored as hi + lo, 8 significant bits as bf16 has, two K
-//     steps into the same accumulator.  The reference of the running softmax is the maximum
-//     of log2 P_j (so c_j is inside it): P is 8 at the maximum that the reference was taken
-//     from and may rise to 2^8.75 (e4m3 ends at 448) before the reference moves; 2^-9 is the
-//     spacing of the smallest e4m3 values, so a small weight is off by 2^-13 of the largest at
-//     most.  Where one of a warp's eight heads has to move, all that have risen move.
+//   * weights: P_j = p_j c_j is stored as hi + lo / 16, 8 significant bits as bf16 has, two K steps
+//     into the same accumulator, under a power-of-two scale for each head and 32 rows
+//     (kind::mxf8f6f4).  The largest of the 32 lies in (2^7, 2^8], so a weight is off by 2^-9 of itself,
+//     or by 2^-21 of that largest one where this is more (half of 2^-9, the spacing of e4m3's smallest
+//     values, by lo's 2^-4).  Under one scale for the whole list a row that takes most of a head's weight
+//     left those below 2^-13 of it no value at all: out was off by up to 0.9 of itself.
+//     The scales count from a reference that O of a head has; it is the first tile's largest, and
+//     moves only where a block is 2^24 above it.  The sum of the weights is fp32 and has a reference
+//     of its own, the largest so far.
 //
 // One CTA handles one unit (query token, shard, group of up to 64 heads), whole rows, no
 // exchange per tile:
@@ -28,25 +31,24 @@
 //     128 columns, 3 K steps, each hi and then lo with the same A, which the second takes from
 //     the collector buffer (at N = 64 the read of A from shared memory, 4 KB, takes longer than
 //     the products: 48.9 -> 47.4 us below).  E^T is the same tile read MN-major.
-// TMEM: q 144 columns, S 96 (two of them for 32 heads or fewer), O^T up to 256.
+// TMEM: q 144 columns, scales 12, S 96 (two of them for 32 heads or fewer), O^T up to 256.
 //
 // With few units a cluster of G CTAs shares one: CTA c takes every G-th 96 entries of the list; they merge
 // (O, m, l) over distributed shared memory at the end.
 //
 // Warp roles (640 threads): warps 0-7 softmax (each 8 heads whole); 8 issues QK^T, 9 P.V; 10-13
-// the gathers; 14 the rows' scales and the later segments of a long list; 16-19 scale O where a
-// reference moved; all take a part in the output.  At the start warps 0-7 and 16-19 bring q to
+// the gathers; 14 the rows' scales and the later segments of a long list; 16-19 bring the weights'
+// scales to TMEM and scale O where a reference moved; all take a part in the output.  At the start warps 0-7 and 16-19 bring q to
 // TMEM while 8-15 resolve the list.  Every wait is bounded; one that gives up records
 // SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
 //
-// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.0 us, 256 tokens x 64
-// heads x 2048 rows 89.6 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
-// rows in four shards 46.8 us (22.7).  Bound: at 64 heads a tile's MMAs take ~2,100 of its
-// ~2,700 cycles and the rest is the chain scores -> softmax -> P.V with one score buffer (TMEM
-// is full); the first scores come after 12,600-14,600 cycles (launch, list, table, q and the
-// first rows follow one another), the end takes 5,000, and a second round of units a whole
-// one's time.  The first step without the moves of references: 42.8 us, with half the P.V
-// 44.1, with a quarter of the gathers 45.7.
+// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 44.7 us, 256 tokens x 64
+// heads x 2048 rows 88.4 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
+// rows in four shards 47.8 us (22.7).  With one scale for the whole list, and O's reference moving with the
+// largest weight: 45.2, 89.8, 47.0.  Bound: at 64 heads a tile's MMAs take most of its time and the
+// rest is the chain scores -> softmax -> P.V with one score buffer (TMEM is full); the first
+// scores come after 12,600-14,600 cycles (launch, list, table, q and the first rows follow one
+// another), the end takes 5,000, and a second round of units a whole one's time.
 // Taken back: 64-row tiles in 4 or 5 stages (63 vs 61 us at the time), part of the columns by
 // cp.async (64-94 vs 61), rows prefetched to L2 (67 vs 61, 72 vs 49), P.V handed over in
 // three parts (51.5 vs 49.0), references moved two groups of heads at a time (47.5 vs 45.9).
@@ -74,8 +76,10 @@ constexpr int kListWarps = 8, kQkWarp = 8, kPvWarp = 9, kProducerWarp = 10, kPro
 constexpr int kGroupHeads = 64;      // heads of a unit
 constexpr int kQParts = (kGroupHeads + kQWarps - 1) / kQWarps;   // copies of q, kQWarps heads each
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kPeak = 3.0f;        // log2 of P at the maximum a reference is taken from
-constexpr float kMostP = 8.75f;      // log2 of the largest P before the reference moves
+constexpr int kWBlock = 32;          // weights under one scale: K of an MMA
+constexpr float kPeak = 8.0f;        // log2 of the most that a block's largest weight is stored as (e4m3 ends at 448)
+constexpr float kRise = 24.0f;       // log2 of what a block's scale may rise above its head's reference
+constexpr float kFall = 120.0f;      // and fall below it (a scale is 2^-127 at least)
 
 // shared memory map (offsets from a 1024-byte aligned base)
 constexpr int kBlk = kNt * 128;                       // 128 latent columns of a tile, SW128
@@ -88,7 +92,7 @@ constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and two rows:
 constexpr int kOffInv = kOffScale + kStages * kNt * 8;  // 1 / scale
 constexpr int kOffMisc = kOffInv + kStages * kNt * 4;
 constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscScale = 1024, kMiscC = 1280, kMiscFlags = 1536, kMiscTmem = 1540,
-              kMiscMoved = 1544, kMiscCount = 1560, kMiscSeg = 1600, kMiscBytes = 1616;
+              kMiscMoved = 1544, kMiscCount = 1560, kMiscSeg = 1600, kMiscSf = 1616, kMiscRef = 2128, kMiscBytes = 2384;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
 constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarRows = kBarKvEmpty + kStages,
               kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQLoad = kBarSegFull + 1, kBarQReady = kBarQLoad + kQParts,
@@ -106,7 +110,7 @@ constexpr int kQPitch = 2 * kDQK;
 constexpr int kOffTmp = kStageBytes + kGroupHeads * kQPitch;   // behind it: the resolved list before its compaction
 constexpr int kTmpCap = (kStages * kStageBytes - kOffTmp) / 4;
 static_assert(kTmpCap >= 8192, "q and a list of 8192 entries fit in stages 1 and 2");
-static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscBytes, "misc");
+static_assert(kMiscCount + 4 * (kListWarps + 1) <= kMiscSeg, "misc");
 
 
 // A wait that is not over at once goes on outside of the kernel's own code, which every launch
@@ -122,6 +126,8 @@ constexpr uint64_t kLanded = 100000000ull;   // ns: copies in flight have landed
                                              // half issued never completes its barrier)
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColQ = 0, kColS = 160, kColO = 256, kColS1 = 400;   // S1 for up to 32 heads
+// scales of P.V's operands: of E^T all 1; of two buffers of P^T, two words (64 heads) for hi and two for lo
+constexpr uint32_t kColSfE = 144, kColSfP = 148;
 
 // 16-byte word w of a converted row of q: moved so that eight rows' are in different banks
 __device__ __forceinline__ int q_word(int row, int w) { return w ^ (w < 32 ? row & 7 : row & 3); }
@@ -156,23 +162,28 @@ __device__ __forceinline__ void mma8_ts(uint32_t d, uint32_t a_tmem, uint32_t b_
       "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHi)
       : "memory");
 }
+// The same with a scale for each row of A and of B, 32 of K: ue8m0 bytes in TMEM, a row's at lane row %
+// 32 (of all four quadrants) of word row / 32, the byte that `idesc` names.
 // (kFirst: A stays in the collector buffer, and the next MMA, with the same A, takes it from
 // there instead of from shared memory)
 template <uint32_t kHiA, uint32_t kHiB, bool kFirst>
-__device__ __forceinline__ void mma8_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+__device__ __forceinline__ void mma8_scaled_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, uint32_t sf_a,
+                                               uint32_t sf_b, uint32_t acc) {
   if constexpr (kFirst)
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::fill [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
+        "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %8};\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X.collector::a::fill [%0], da, db, %3, [%5], "
+        "[%6], p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(sf_a), "r"(sf_b), "n"(kHiA), "n"(kHiB)
         : "memory");
   else
     asm volatile(
         "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %6};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4.collector::a::lastuse [%0], da, db, %3, p;\n\t}" ::"r"(d),
-        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "n"(kHiA), "n"(kHiB)
+        "mov.b64 da, {%1, %7};\n\tmov.b64 db, {%2, %8};\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X.collector::a::lastuse [%0], da, db, %3, "
+        "[%5], [%6], p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(acc), "r"(sf_a), "r"(sf_b), "n"(kHiA), "n"(kHiB)
         : "memory");
 }
 // the words of a shared-memory matrix descriptor (addresses and strides in 16-byte units)
@@ -191,6 +202,10 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, int a_mn, int b_
   return (1u << 4) | (static_cast<uint32_t>(a_mn) << 15) | (static_cast<uint32_t>(b_mn) << 16) |
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
+// of kind::mxf8f6f4 with block scales: the same, ue8m0 scales, A's byte 0 and B's byte `sf_b`
+__host__ __device__ constexpr uint32_t idesc_e4m3_scaled(int M, int N, int a_mn, int b_mn, int sf_b) {
+  return (idesc_e4m3(M, N, a_mn, b_mn) & ~(1u << 4)) | (static_cast<uint32_t>(sf_b) << 4) | (1u << 23);
+}
 
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t* r) {
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -207,6 +222,10 @@ __device__ __forceinline__ void tmem_ld_16x16(uint32_t taddr, uint32_t* r) {
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
 }
 
@@ -334,6 +353,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float2* ml_s = reinterpret_cast<float2*>(misc + kMiscMl);              // [64] (m, l)
   float* alpha_s = reinterpret_cast<float*>(misc + kMiscAlpha);          // [2][64] rescale factors
   uint8_t* moved_s = reinterpret_cast<uint8_t*>(misc + kMiscMoved);      // [2][8] whether 8 heads' references moved
+  uint32_t* sf_s = reinterpret_cast<uint32_t*>(misc + kMiscSf);          // [2][64] the scales of hi's three blocks, as ue8m0
+  float* below_s = reinterpret_cast<float*>(misc + kMiscRef);            // [64] O's reference, relative to that of (m, l)
   float* scale_s = reinterpret_cast<float*>(misc + kMiscScale);          // [64] output scales
   float* qc_s = reinterpret_cast<float*>(misc + kMiscC);                 // [64] score scale, NaN for a bad head
   volatile int* abort_s = reinterpret_cast<volatile int*>(misc + kMiscFlags);
@@ -442,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quad = warp & 3, half = warp >> 2;
   const int head = 16 * quad + 8 * half + (lane >> 2);
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-  float ref = -INFINITY, l_sum = 0.f;
+  float ref = -INFINITY, top = -INFINITY, l_sum = 0.f;   // reference of O; of l_sum (the largest so far)
   // Roles follow in place, so that each warp runs through code that lies next to what it ran
   // before (the instruction cache is cold at every launch).
   if (warp >= kSoftWarps && warp < kFixWarp) {
@@ -671,7 +692,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           // A = E^T: columns 128m..128m+127 of 32 tile rows, MN-major (one SW128 atom wide);
           // B = P^T: NH heads x 32 rows, K-major.  The four blocks' accumulators alternate.
-          constexpr uint32_t id = idesc_e4m3(128, NH, 1, 0);
           int s = 0;
           for (int n = 0; ok && n < n_local && !*abort_s; ++n) {
             const int bb = n & 1;
@@ -685,8 +705,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   #pragma unroll
                 for (int m = 0; m < 4; ++m) {
                   const uint32_t d = tmem + kColO + NH * m, a = a0 + ((m * kBlk + 4096 * k) >> 4), b = b0 + ((32 * k) >> 4);
-                  mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128), true>(d, a, b, id, k > 0 || n > 0);
-                  mma8_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128), false>(d, a, b + (kPBytes >> 4), id, 1);
+                  const uint32_t id = idesc_e4m3_scaled(128, NH, 1, 0, k);
+                  const uint32_t sf_e = tmem + kColSfE, sf_p = tmem + kColSfP + 4 * bb;
+                  mma8_scaled_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128), true>(d, a, b, id, sf_e, sf_p,
+                                                                                               k > 0 || n > 0);
+                  mma8_scaled_ss<desc_hi(1024, kSwizzle128), desc_hi(1024, kSwizzle128), false>(
+                      d, a, b + (kPBytes >> 4), id, sf_e, sf_p + 2, 1);
                 }
               mma_commit(&bars[kBarKvEmpty + s]);
               mma_commit(&bars[kBarPFree + bb]);
@@ -798,7 +822,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           constexpr int kBatch = kNt / 32;                    // 16-row loads in flight at a time
           const uint32_t s_col = lane_base + (sb ? kColS1 : kColS);
           const float4* rs = rows_s + st * (kNt / 2) + (lane & 3);
-          float mx = -INFINITY;
+          float mx[kNt / kWBlock] = {-INFINITY, -INFINITY, -INFINITY};   // of each 32 rows
   #pragma unroll
           for (int k3 = 0; k3 < kNt / 16; k3 += kBatch) {
             uint32_t vh[kBatch][8], vl[kBatch][8];
@@ -823,44 +847,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float4 cr = rs[4 * j];
                 x[j] = fma2(fma2(lo, sixteenth, hi), mul2(pack2(cr.x, cr.y), c2), pack2(cr.z, cr.w));
                 const float2 f = unpack2(x[j]);
-                mx = fmaxf(mx, fmaxf(f.x, f.y));
+                mx[j / 4] = fmaxf(mx[j / 4], fmaxf(f.x, f.y));
               }
           }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          // P buffer bb, and its flags and factors, are free once P.V of tile i-2 is done
+  #pragma unroll
+          for (int o = 1; o < 4; o <<= 1)
+  #pragma unroll
+            for (int k = 0; k < kNt / kWBlock; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], o));
+          // P buffer bb, and its flags, factors and scales, are free once P.V of tile i-2 is done
           if (i >= 2 && !wait_warp(&bars[kBarPFree + bb], ((i >> 1) - 1) & 1)) {
             fail();
             break;
           }
-          // (where one of the warp's heads has to move, the others that have risen move with it)
-          const bool moved = __any_sync(0xffffffffu, i > 0 && mx > ref + kMostP);
-          const float ref_new = i == 0 || (moved && mx > ref + kPeak) ? mx - kPeak : ref;
-          if (moved) {
-            const float alpha = ex2(ref - ref_new);
-            l2 = mul2(l2, pack2(alpha, alpha));
-            if ((lane & 3) == 0) alpha_s[64 * bb + head] = alpha;
+          // A block's weights are stored under 2^e, its largest in (2^7, 2^8].  O's reference moves only
+          // where a scale would be 2^kRise above it (and then those of the warp's heads that have risen)
+          float e[kNt / kWBlock];
+  #pragma unroll
+          for (int k = 0; k < kNt / kWBlock; ++k) e[k] = ceilf(mx[k]) - kPeak;
+          const float most = fmaxf(fmaxf(e[0], e[1]), e[2]);
+          const bool moved = __any_sync(0xffffffffu, i > 0 && most > ref + kRise);
+          const float ref_new = i == 0 || (moved && most > ref) ? most : ref;
+          if (moved && (lane & 3) == 0) alpha_s[64 * bb + head] = ex2(ref - ref_new);
+          ref = ref_new;
+          uint32_t sf = 0;
+  #pragma unroll
+          for (int k = 0; k < kNt / kWBlock; ++k) {
+            e[k] = fmaxf(e[k], ref - kFall);
+            sf |= (uint32_t)((int)(e[k] - ref) + 127) << (8 * k);     // (a NaN, of a spoilt head, becomes 0)
           }
+          if ((lane & 3) == 0) sf_s[64 * bb + head] = sf;
           if (lane == 0) moved_s[8 * bb + 2 * quad + half] = moved;
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars[kBarAReady + bb]);
-          ref = ref_new;
-          // P = 2^(x - ref) as hi + lo; p = P / scale into the sum
-          const uint64_t nref = pack2(-ref, -ref);
+          // the sum's reference is the largest e so far
+          const float top_new = fmaxf(top, most), fade = ex2(top - top_new);
+          l2 = mul2(l2, pack2(fade, fade));
+          top = top_new;
+          // P = 2^(x - e) as hi + lo / 16; p = P / scale into the sum
           const float2* iv = reinterpret_cast<const float2*>(inv_s + st * kNt) + (lane & 3);
           char* const row = p_row + 2 * bb * kPBytes;
   #pragma unroll
-          for (int j = 0; j < kNt / 8; ++j) {
-            const float2 f = unpack2(add2(x[j], nref));
-            const float p0 = ex2(f.x), p1 = ex2(f.y);
-            const float2 inv = iv[4 * j];
-            l2 = fma2(pack2(p0, p1), pack2(inv.x, inv.y), l2);
-            // 11 bits are enough under the 8 that hi and lo keep
-            const __half2 w = __floats2half2_rn(p0, p1);
-            const uint32_t hi = e4m3x2_h(w);
-            const int at = (((j >> 1) ^ (head & 7)) << 4) + 8 * (j & 1);
-            *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)hi;
-            *reinterpret_cast<uint16_t*>(row + at + kPBytes) = (uint16_t)e4m3x2_h(__hsub2(w, half2_of(hi)));
+          for (int k = 0; k < kNt / kWBlock; ++k) {
+            const uint64_t ne = pack2(-e[k], -e[k]);
+            uint64_t sum = 0;
+  #pragma unroll
+            for (int j = 4 * k; j < 4 * k + 4; ++j) {
+              const float2 f = unpack2(add2(x[j], ne));
+              const float p0 = ex2(f.x), p1 = ex2(f.y);
+              const float2 inv = iv[4 * j];
+              sum = fma2(pack2(p0, p1), pack2(inv.x, inv.y), sum);
+              // 11 bits are enough under the 8 that hi and lo keep
+              const __half2 w = __floats2half2_rn(p0, p1);
+              const uint32_t hi = e4m3x2_h(w);
+              const int at = (((j >> 1) ^ (head & 7)) << 4) + 8 * (j & 1);
+              *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)hi;
+              *reinterpret_cast<uint16_t*>(row + at + kPBytes) =
+                  (uint16_t)e4m3x2_h(__hmul2(__hsub2(w, half2_of(hi)), __floats2half2_rn(16.f, 16.f)));
+            }
+            const float part = ex2(e[k] - top);
+            l2 = fma2(sum, pack2(part, part), l2);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -874,14 +919,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else if (warp >= kFixWarp) {
       // =================== O follows the references (warps 16-19) ====================
+      // They put the scales of tile i's weights into TMEM while the softmax warps write the weights.
       // Where a head's reference moved with tile i, its column of O^T is scaled between P.V of
-      // tiles i-1 and i, while the softmax warps write the weights.
+      // tiles i-1 and i.
       const uint32_t my_lanes = tmem + ((uint32_t)((warp - kFixWarp) * 32) << 16);
+      tmem_st4(my_lanes + kColSfE, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
       for (int i = 0; i < n_local && !*abort_s; ++i) {
         const int bb = i & 1;
         if (!wait_warp(&bars[kBarAReady + bb], (i >> 1) & 1)) {
           fail();
           break;
+        }
+        {
+          // the scales of the tile's weights; lo's are 2^-4 of hi's
+          const volatile uint32_t* sp = sf_s + 64 * bb + lane;
+          const uint32_t s0 = sp[0], s1 = NH == 64 ? sp[32] : s0;
+          tmem_st4(my_lanes + kColSfP + 4 * bb, s0, s1, s0 - 0x040404u, s1 - 0x040404u);
         }
         uint64_t m8 = *reinterpret_cast<const volatile uint64_t*>(moved_s + 8 * bb);
         if (m8 != 0) {
@@ -907,8 +960,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   #pragma unroll
             for (int m = 0; m < 4; ++m) tmem_st8(at + NH * m, o + 8 * m);
           }
-          tmem_st_wait();
         }
+        tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars[kBarPReady + bb]);
@@ -921,8 +974,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kSoftWarps) {
     if (n_local > 0 && !*abort_s && !wait_warp(&bars[kBarPvFinal], 0)) fail();
     if (quad < HB && (lane & 3) == 0) {
-      ml_s[head] = make_float2(ref, l_sum);
-      if (G == 1) scale_s[head] = l_sum != 0.f ? 1.f / l_sum : 0.f;
+      ml_s[head] = make_float2(top, l_sum);
+      below_s[head] = ref - top;
+      if (G == 1) scale_s[head] = l_sum != 0.f ? ex2(ref - top) / l_sum : 0.f;
     }
   }
   // (a CTA alone needs no cluster barrier, here and below)
@@ -977,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // Every thread of every CTA of the cluster reaches both cluster barriers.
   if (threadIdx.x < NH) {
-    // this head's largest reference M, sum L and this CTA's weight 2^(m - M) / L
+    // this head's largest reference M, sum L and the weight of this CTA's O
     const int hd = threadIdx.x;
     float M = -INFINITY, L = 0.f;
     for (uint32_t c = 0; c < G; ++c) M = fmaxf(M, ld_cluster_f32(mapa(&ml_s[hd], c)));
@@ -987,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lc != 0.f) L += ex2(ld_cluster_f32(a) - M) * lc;
     }
     const float2 mine = ml_s[hd];
-    scale_s[hd] = mine.y != 0.f ? ex2(mine.x - M) / L : 0.f;
+    scale_s[hd] = mine.y != 0.f ? ex2(mine.x - M + below_s[hd]) / L : 0.f;
     if (crank == 0 && hd < nh && good) p.lse[lse_at + hd] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
   }
   __syncthreads();

@@ -1,6 +1,7 @@
 """GPU parity of the calls around decode over an 8-bit latent cache against the fp64 oracle:
 the step plan, rotary positions, the quantising cache write, decode_q8, and a run of them
 together as a serving step uses them."""
+import math
 import os
 import subprocess
 import sys
@@ -576,6 +577,105 @@ def test_decode_q8_scales_that_differ_between_groups(path, spread, pow2):
     if spread == 20:                      # scores of rows up to 2^20 large: keep their range
         pr["q"] = (pr["q"].float() * 2.0 ** -18).to(torch.bfloat16)
     _close(*_run(pr), [x[0] for x in _oracle(pr)])
+
+
+def _near(out, lse, want, what=""):
+    """Elementwise, relative to the output: a softmax weight keeps 8 significant bits (2^-8) at every
+    size, then fp32 arithmetic (1e-3) and the type's rounding.  That is what bf16 weights give."""
+    ro, rl, wabs, _ = want
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.all(np.isfinite(o)), what
+    eps = 2.0 ** -8 if out.dtype == torch.bfloat16 else 2.0 ** -24
+    bound = (2.0 ** -8 + 1e-3) * wabs + eps * np.abs(ro)
+    err = np.abs(o - ro)
+    assert np.all(err <= bound + 1e-30), f"{what}: {np.max(err / (bound + 1e-30))} of the bound"
+    assert np.all(np.abs(l - rl) <= 1e-3), what
+
+
+def _dominated(h, k, share, same=False, group=64, spread=0):
+    """k positions of one sequence, position 0's row drawing `share` of head 0's weight (the other heads
+    a little more or less) with small values; the rest share what is left nearly evenly (`same`: exactly)
+    and their values have a common part, so what is dropped of them does not cancel.  Scores come
+    from the 64 rope columns, where q is 1 +- 2 %.  spread: scales of groups apart by up to 2^spread."""
+    rng = np.random.default_rng(h + k)
+    nb = -(-k // 64)
+    scales = 2.0 ** (rng.integers(-spread, spread + 1, (nb, 64 // group)) - 6.0) if spread else np.full((nb, 64 // group), 2.0 ** -6)
+    rope = np.zeros((nb, 64, 64)) if same else rng.standard_normal((nb, 64, 64)) * 34.0
+    # scale * c * sum(e) = ln(share (k - 1) / (1 - share)) with all 64 columns alike
+    rope[0, 0] = math.log(share * (k - 1) / (1.0 - share)) / (64 * SCALE * 2.0 ** -6)
+    rel = np.repeat(scales * 2.0 ** 6, group, axis=1)[..., None]
+    lat = rng.standard_normal((nb, 64, 512)) * 24.0 + 32.0
+    lat[0, 0] = rng.standard_normal(512) * 0.5
+    codes = serving.to_e4m3(np.clip(np.concatenate([lat, rope / rel], 2), -448, 448))
+    q = np.zeros((1, h, 576))
+    q[0, :, 512:] = 1.0 + 0.02 * np.linspace(0.0, -1.0, h)[:, None]
+    return dict(q=torch.from_numpy(q).to(torch.bfloat16), codes=codes, scales=scales.astype(np.float32), group=group,
+                bt=rng.permutation(nb)[None], sl=np.array([k]), idx=None, Q=1)
+
+
+def _in_table_order(pr):
+    # position p of the sequence is row p of the arrays made above
+    for name in ("codes", "scales"):
+        a = np.empty_like(pr[name])
+        a[pr["bt"][0]] = pr[name]
+        pr[name] = a
+    return pr
+
+
+@pytest.mark.parametrize("k", [64, 300, 2048, 32768])
+@pytest.mark.parametrize("share", [0.5, 0.9, 0.99])
+@pytest.mark.parametrize("same", [False, True])
+def test_decode_q8_a_dominant_row_leaves_the_tail_its_weight(path, k, share, same):
+    # the row first, in the middle and last in the list; a token alone (its list goes to several CTAs)
+    # and more tokens than SMs (one CTA each)
+    pr = _in_table_order(_dominated(24, k, share, same))
+    want, rng = None, np.random.default_rng(k)
+    orders = []
+    for at in (0, k // 2, k - 1):
+        rest = 1 + rng.permutation(k - 1)
+        orders.append(np.concatenate([rest[:at], [0], rest[at:]]))
+    pr["idx"] = orders[0][None]
+    want = [x[0] for x in _oracle(pr)]                     # the order of the list does not matter
+    for j, order in enumerate(orders):
+        _near(*_run(dict(pr, idx=order[None])), want, f"alone, order {j}")
+    if path == 1 and k > 2048:
+        return                                             # (160 such tokens on CUDA cores take seconds)
+    many = dict(pr, q=pr["q"].expand(160, -1, -1).contiguous(), bt=np.repeat(pr["bt"], 160, 0), sl=np.repeat(pr["sl"], 160),
+                idx=np.stack([orders[t % 3] for t in range(160)]))
+    for dtype in (torch.float32, torch.bfloat16):
+        out, lse = _run(many, dtype=dtype)
+        for t in range(3):
+            _near(out[t:t + 1], lse[t:t + 1], want, f"many, order {t}, {dtype}")
+            assert torch.equal(out[t::3][:53], out[t:t + 1].expand(53, -1, -1))
+    assert sfa.last_device_status() == 0
+
+
+@pytest.mark.parametrize("h", [8, 33, 64, 128])
+@pytest.mark.parametrize("n,il", [(2, 0), (4, 16), (8, 0)])
+def test_decode_q8_a_dominant_row_in_one_of_several_shards(path, h, n, il):
+    pr = _in_table_order(_dominated(h, 5000, 0.95, group=16, spread=1))
+    pr["idx"] = np.random.default_rng(h).permutation(5000)[None]
+    _near(*_run(pr, n, il), [x[0] for x in _oracle(pr)], f"n={n}")
+
+
+@pytest.mark.parametrize("h", [16, 64])
+@pytest.mark.parametrize("step", [0.05, 0.7, 6.0, -0.05, -0.7, -6.0])
+def test_decode_q8_scores_that_climb_and_fall_through_the_list(path, h, step):
+    # a list whose weights change by a factor e^(96 step) from tile to tile, up or down: nearly all of
+    # the weight in the last (first) rows, where the first (last) ones are behind 2^-100 of it
+    pr = _in_table_order(_dominated(h, 1500, 0.5))
+    rope = np.arange(1500) * step / (64 * SCALE * 2.0 ** -6)
+    rope = np.clip(rope - rope.min() - 448.0, -448.0, 448.0)       # (e4m3's range; what is beyond is even)
+    codes = pr["codes"].copy()
+    pos = np.arange(1500)
+    codes[pr["bt"][0][pos // 64], pos % 64, 512:] = serving.to_e4m3(np.repeat(rope[:, None], 64, 1))
+    pr["codes"] = codes
+    q = pr["q"].float()
+    q[..., 512:] *= 4.0
+    pr["q"] = q.to(torch.bfloat16)
+    for order in (pos, pos[::-1], np.random.default_rng(1).permutation(1500)):
+        pr["idx"] = order[None].copy()
+        _near(*_run(pr), [x[0] for x in _oracle(pr)], f"{step}")
 
 
 @pytest.mark.parametrize("h,n,il", [(5, 2, 0), (16, 3, 16), (64, 8, 0), (128, 4, 1), (72, 64, 0), (30, 5, 7)])
