@@ -44,7 +44,8 @@ __global__ void __launch_bounds__(256) lse_merge_kernel(const float* __restrict_
     const float l1 = lane + 32 < n ? lse_part[(size_t)(lane + 32) * rows + row] : -INFINITY;
     const float M = warp_max(fmaxf(l0, l1));
     Out* orow = out + (size_t)row * dv;
-    if (M == -INFINITY) {
+    // (a maximum passes over NaN, which is no empty shard: it goes on to out and lse)
+    if (__all_sync(0xffffffffu, l0 == -INFINITY && l1 == -INFINITY)) {
       for (int c = lane; c < dv; c += 32) orow[c] = Out(0.f);
       if (lane == 0) lse[row] = -INFINITY;
       continue;
@@ -121,7 +122,7 @@ __global__ void __launch_bounds__(256) lse_merge_fast_kernel(const float* __rest
           v[jj][u] = u < n ? __ldg(base + (size_t)u * rstride4 + 32 * (j0 + jj)) : make_float4(0.f, 0.f, 0.f, 0.f);
       if (j0 == 0) {   // the weights, while the first round of rows is in flight
         const float M = warp_max(lv);
-        empty = M == -INFINITY;
+        empty = __all_sync(0xffffffffu, lv == -INFINITY);   // (a maximum passes over NaN, which is no empty shard)
         if (!empty) {
           const float Z = warp_sum(lane < n ? expf(lv - M) : 0.f);
           L = M + logf(Z);

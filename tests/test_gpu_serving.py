@@ -790,6 +790,41 @@ def test_decode_q8_infinite_and_nan_queries_spoil_only_their_head(path):
     _close(out, lse, want)
 
 
+@pytest.mark.parametrize("n", [1, 2, 8, 9, 33, 64])
+@pytest.mark.parametrize("dv", [512, 20, 7])
+def test_merge_of_partials_without_a_number_is_not_empty(n, dv):
+    # an lse that is NaN comes from a shard whose result is NaN: so are out and lse, whatever the
+    # other shards hold; only a row of -inf throughout is empty
+    rng = np.random.default_rng(n)
+    op = torch.from_numpy(rng.standard_normal((n, 5, dv))).float()
+    lp = torch.from_numpy(rng.standard_normal((n, 5))).float()
+    lp[:, 0] = float("nan")                                # every shard
+    lp[:, 1], lp[n - 1, 1] = -math.inf, float("nan")       # one, the others empty
+    lp[:, 2], lp[0, 2] = 1.0, float("nan")                 # one, beside numbers
+    lp[:, 3] = -math.inf                                   # empty
+    out, lse = sfa.lse_merge(op.cuda(), lp.cuda())
+    assert torch.all(torch.isnan(out[:3])) and torch.all(torch.isnan(lse[:3]))
+    assert torch.all(out[3] == 0) and torch.isneginf(lse[3])
+    w = torch.softmax(lp[:, 4].double(), 0)
+    want, lse4 = (w[:, None] * op[:, 4].double()).sum(0), torch.logsumexp(lp[:, 4].double(), 0)
+    # n terms with weights to 2^-20 (expf and the sum), fp32 accumulation
+    assert torch.all((out[4].cpu().double() - want).abs() <= 2.0 ** -18 * (w[:, None] * op[:, 4].double().abs()).sum(0) + 1e-30)
+    assert abs(float(lse[4]) - float(lse4)) <= 1e-5
+
+
+@pytest.mark.parametrize("n,il", [(2, 0), (5, 7), (33, 0), (64, 1)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_decode_q8_infinite_and_nan_queries_spoil_their_head_of_merged_shards(n, il, dtype):
+    pr = _problem(111, 2, 1, 18, 200, 100)
+    want = [x[0] for x in _oracle(pr)]
+    pr["q"][0, 3, 9], pr["q"][1, 17, 570] = float("nan"), float("inf")
+    out, lse = _run(pr, n, il, dtype=dtype)
+    for t, hh in ((0, 3), (1, 17)):
+        assert torch.all(torch.isnan(out[t, hh])) and torch.isnan(lse[t, hh])
+        out[t, hh], lse[t, hh] = torch.from_numpy(want[0][t, hh]).to(dtype), float(want[1][t, hh])
+    _close(out, lse, want)
+
+
 def test_decode_q8_cache_longer_than_32_bit_offsets(path):
     # 4.6 GB of cache: rows at both ends and in the middle
     nb, bs = 125000, 64
