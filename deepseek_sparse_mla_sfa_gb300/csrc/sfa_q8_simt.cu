@@ -25,6 +25,14 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
+// the largest of the warps' maxima; NaN, which fmaxf passes over, where one of them is NaN
+__device__ __forceinline__ float join_max(const float (&m)[kWarps][kHG], int hh) {
+  float M = m[0][hh];
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) M = m[w][hh] != m[w][hh] ? m[w][hh] : M != M ? M : fmaxf(M, m[w][hh]);
+  return M;
+}
+
 __global__ void __launch_bounds__(kWarps * 32) decode_q8_simt_kernel(const DecodeQ8Params qp) {
   const DecodeParams& p = qp.p;
   __shared__ float q_s[kHG * kDQK];
@@ -100,7 +108,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_q8_simt_kernel(const Decod
     if (warp == w) {
 #pragma unroll
       for (int hh = 0; hh < kHG; ++hh) {
-        const float M = fmaxf(fmaxf(m_s[0][hh], m_s[1][hh]), fmaxf(m_s[2][hh], m_s[3][hh]));
+        const float M = join_max(m_s, hh);
         const float f = m[hh] == -INFINITY ? 0.f : expf(m[hh] - M);
 #pragma unroll
         for (int c = 0; c < 2 * kVPairs; ++c) o_s[hh * kDV + 2 * lane + 64 * (c >> 1) + (c & 1)] += o[hh][c] * f;
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(kWarps * 32) decode_q8_simt_kernel(const Decod
   const size_t at = ((size_t)r * T + t) * p.h + h0;
   for (int x = threadIdx.x; x < nh * kDV; x += blockDim.x) {
     const int hh = x / kDV;
-    const float M = fmaxf(fmaxf(m_s[0][hh], m_s[1][hh]), fmaxf(m_s[2][hh], m_s[3][hh]));
+    const float M = join_max(m_s, hh);
     float lsum = 0.f;
     if (M != -INFINITY)
       for (int w = 0; w < kWarps; ++w) lsum += l_s[w][hh] * expf(m_s[w][hh] - M);

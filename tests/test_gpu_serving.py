@@ -825,6 +825,27 @@ def test_decode_q8_infinite_and_nan_queries_spoil_their_head_of_merged_shards(n,
     _close(out, lse, want)
 
 
+@pytest.mark.parametrize("k", [1, 2, 3, 5, 97])
+@pytest.mark.parametrize("n", [1, 3])
+def test_decode_q8_bad_queries_and_rows_over_lists_of_few_entries(path, k, n):
+    # fewer entries than warps (or shards) that share them: those without one have nothing to add
+    pr = _problem(112, 2, 1, 5, 300, k)
+    want = [x[0] for x in _oracle(pr)]
+    pr["q"][0, 2, 9], pr["q"][1, 4, 570] = float("nan"), float("-inf")
+    out, lse = _run(pr, n)
+    for t, hh in ((0, 2), (1, 4)):
+        assert torch.all(torch.isnan(out[t, hh])) and torch.isnan(lse[t, hh])
+        out[t, hh], lse[t, hh] = torch.from_numpy(want[0][t, hh]).float(), float(want[1][t, hh])
+    _close(out, lse, want)
+    # a NaN in the rope columns of a selected row: a score of NaN in every head of its token
+    p = int(pr["idx"][0, 0])
+    pr["q"] = torch.nan_to_num(pr["q"], 0.0, 0.0, 0.0)
+    pr["codes"][pr["bt"][0][p // 64], p % 64, 570] = 127
+    out, lse = _run(pr, n)
+    assert torch.all(torch.isnan(out[0])) and torch.all(torch.isnan(lse[0]))
+    assert torch.all(torch.isfinite(out[1])) and torch.all(torch.isfinite(lse[1]))
+
+
 def test_decode_q8_cache_longer_than_32_bit_offsets(path):
     # 4.6 GB of cache: rows at both ends and in the middle
     nb, bs = 125000, 64
