@@ -176,8 +176,8 @@ cudaError_t launch_step_plan(const int32_t* cached, const int32_t* fresh_tokens,
   const int threads = wide ? 512 : 256, per_block = (B > 4096 ? 4 : 1) * threads, most = 4 * device_sm_count();
   long long blocks = ((long long)num_tokens + per_block - 1) / per_block;
   const int grid = (int)(blocks < 1 ? 1 : blocks > most ? most : blocks);
-  const size_t smem = (size_t)(2 * (B + 1)) * 4;
-  if (smem > 48 * 1024) {
+  const size_t smem = (size_t)(2 * (B + 1)) * 4, fixed = 2 * (512 / 32) * sizeof(long long);   // (part_t, part_b)
+  if (smem + fixed > 48 * 1024) {              // what a launch has unasked holds both
     const cudaError_t e = cudaFuncSetAttribute(step_plan_kernel<512>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                (int)(2 * (kPlanMaxRequests + 1) * 4));
     if (e != cudaSuccess) return e;

@@ -118,6 +118,36 @@ def test_step_plan_steps_follow_each_other_in_a_graph():
     assert sfa.last_device_status() == 0
 
 
+FIRST_PLAN = """
+import sys, numpy as np, torch, deepseek_sparse_mla_sfa_gb300 as sfa
+from oracle import serving
+i32 = lambda x: torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+for B in map(int, sys.argv[1:]):
+    rng = np.random.default_rng(B)
+    cached, new = rng.integers(0, 40, B), rng.integers(0, 3, B)
+    held, need = -(-cached // 16), -(-(cached + new) // 16)
+    ids, at, table = rng.permutation(int(need.sum()) + 5), 0, np.full((B, 4), -1)
+    for b in range(B):
+        table[b, :held[b]] = ids[at:at + held[b]]
+        at += held[b]
+    N = int(new.sum()) + 3
+    got = sfa.step_plan(i32(cached), i32(new), i32(table), i32(ids[at:]), i32([0]), 16, N)
+    want = serving.step_plan(cached, new, table, ids[at:], 0, 16, N)
+    assert sfa.last_device_status() == 0
+    for g, w in zip(got, want):
+        assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), B
+"""
+
+
+@pytest.mark.parametrize("B", [["6111"], ["6112"], ["6143"], ["6144"], ["8192"], ["6128", "8192", "6128", "40"]])
+def test_step_plan_of_thousands_of_requests_as_the_first_of_a_process(B):
+    # the sums of more than 6112 requests take more shared memory than a launch has unasked: whether
+    # they get it does not depend on the calls before
+    r = subprocess.run([sys.executable, "-c", FIRST_PLAN, *B], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 # -------------------------------------------------------------------------------- rope
 ULP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
 
