@@ -9,7 +9,9 @@
 //
 // The angle is reduced exactly: inv_freq / 2 pi becomes a 64-bit fraction of a turn by
 // integer arithmetic on the double's mantissa, and position * fraction modulo 2^64 is the
-// phase, whatever the position; only its top 32 bits go to sincospif.  (A float angle
+// phase, whatever the position; only its top 32 bits go to sincospif.  (The fraction is off by
+// 2^-63 of a turn for frequencies below 4 rad a position, so the phase by 2^-32 at the last
+// position; by twice as much for each power of two above.)  (A float angle
 // would be off by 2^-8 rad at position 131072, a double one costs FP64 instructions, which
 // this part issues at 1/64 rate.)
 //
@@ -107,10 +109,12 @@ __global__ void __launch_bounds__(kRopeThreads, 8) rope_kernel(const RopeParams 
   for (int x = threadIdx.x; x < nt * pairs; x += kRopeThreads) {
     const int tl = x / pairs, i = x - tl * pairs;
     const int pos = p.pos[t0 + tl];
-    const unsigned long long frac = turn_fraction(p.inv_freq[i]);
+    const double freq = p.inv_freq[i];
+    const unsigned long long frac = turn_fraction(freq);
     const long long ph = (long long)(frac * (unsigned long long)(long long)pos);
     float sn, cs;
     sincospif((float)(int)(ph >> 32) * 0x1p-31f, &sn, &cs);
+    if ((__double2hiint(freq) & 0x7ff00000) == 0x7ff00000) sn = cs = __int_as_float(0x7fc00000);   // no angle
     cs_s[x] = make_float2(cs * p.mscale, (p.inverse ? -sn : sn) * p.mscale);
     if (i == 0) pos_s[tl] = pos;
   }

@@ -274,6 +274,40 @@ def test_rope_inverse_is_the_gradient():
             assert abs(float((gr.double() * d.double()).sum()) - float(grad[at])) <= 24 * 16 * 2.0 ** -22
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("interleaved", [True, False])
+def test_rope_of_a_frequency_that_is_no_number(dtype, interleaved):
+    # its pair has no angle, at any position that is not padding; the others are as ever
+    rng = np.random.default_rng(31)
+    x = torch.from_numpy(rng.standard_normal((6, 3, 40))).to(dtype).cuda()
+    f = sfa.rope_inv_freq(32)
+    pos = i32([0, 1, -1, 77, 2 ** 31 - 1, 5])
+    good = sfa.rope(x, pos, f, interleaved=interleaved)
+    f[3], f[9], f[10] = float("inf"), float("nan"), float("-inf")
+    got = sfa.rope(x, pos, f, interleaved=interleaved)
+    spoilt = torch.zeros(40, dtype=torch.bool, device="cuda")
+    for i in (3, 9, 10):
+        spoilt[[2 * i, 2 * i + 1] if interleaved else [i, i + 16]] = True
+    real = pos >= 0
+    assert torch.all(torch.isnan(got[real][..., spoilt]))
+    assert torch.equal(got[real][..., ~spoilt], good[real][..., ~spoilt]) and torch.equal(got[~real], x[~real])
+
+
+@pytest.mark.parametrize("f", [3.9, 700.0, 1023.9])
+def test_rope_of_fast_frequencies_at_far_positions(f):
+    # the angle is known to 2^-32 turns times 2^8 below 1024 rad a position; the oracle's, by 80 digits
+    from decimal import Decimal, getcontext
+    getcontext().prec = 80
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+    pos = [1, 12345, 2 ** 20 + 1, 2 ** 31 - 1]
+    x = torch.tensor([1.0, 0.0], device="cuda").expand(4, 2).contiguous()
+    got = sfa.rope(x, i32(pos), torch.tensor([f], dtype=torch.float64, device="cuda")).double().cpu().numpy()
+    turns = [(Decimal(p) * Decimal(f) / (2 * pi)) % 1 for p in pos]
+    want = np.array([[math.cos(2 * math.pi * float(t)), math.sin(2 * math.pi * float(t))] for t in turns])
+    # 2^-24 turns, 2^-25 turns of the 24 bits that go to the sine, and its rounding
+    assert np.all(np.abs(got - want) <= 2 * math.pi * (2.0 ** -24 + 2.0 ** -25) + 2.0 ** -22)
+
+
 def test_rope_refusals_on_the_gpu():
     x, pos, f = torch.zeros((3, 2, 8), device="cuda"), i32([0, 1, 2]), sfa.rope_inv_freq(8)
     for bad, err in ((lambda: sfa.rope(x.double(), pos, f), TypeError), (lambda: sfa.rope(x, pos[:2], f), ValueError),
