@@ -5,8 +5,8 @@
 // row's e4m3 values, c_j the scale of its group of slots): s_j = scale * c_j * (q . e_j),
 // out = sum_j p_j c_j e_j / sum_j p_j, p_j = exp(s_j).
 //
-// Both contractions run as 8-bit products (kind::f8f6f4, kind::mxf8f6f4) on the cache's bytes, with no dequantised copy of
-// them; the other operand is split into two e4m3 terms:
+// Both contractions run as 8-bit products (kind::f8f6f4, kind::mxf8f6f4) on the cache's bytes, with
+// no dequantised copy of them; the other operand is split into two e4m3 terms:
 //   * q: a bf16 value has 8 significant bits, e4m3 has 4, so q = hi + lo exactly (under a
 //     power-of-two scale per head; lo is stored times 16, and only values below 2^-22 of the
 //     head's largest are rounded).  hi and lo are two rows of M: 64 heads fill M = 128 and
@@ -19,7 +19,9 @@
 //     left those below 2^-13 of it no value at all: out was off by up to 0.9 of itself.
 //     The scales count from a reference that O of a head has; it is the first tile's largest, and
 //     moves only where a block is 2^24 above it.  The sum of the weights is fp32 and has a reference
-//     of its own, the largest so far.
+//     of its own, the largest so far.  out is divided by the sum of the weights as they are stored (large
+//     ones rounded, small ones not), so that a row with most of the weight is not off by the rounding
+//     of its own: error of the shapes below 2.3e-4 to 2.9e-4 of out, divided by lse's sum 6.6e-4 to 7.2e-4.
 //
 // One CTA handles one unit (query token, shard, group of up to 64 heads), whole rows, no
 // exchange per tile:
@@ -38,17 +40,18 @@
 //
 // Warp roles (640 threads): warps 0-7 softmax (each 8 heads whole); 8 issues QK^T, 9 P.V; 10-13
 // the gathers; 14 the rows' scales and the later segments of a long list; 16-19 bring the weights'
-// scales to TMEM and scale O where a reference moved; all take a part in the output.  At the start warps 0-7 and 16-19 bring q to
-// TMEM while 8-15 resolve the list.  Every wait is bounded; one that gives up records
+// scales to TMEM and scale O where a reference moved; all take a part in the output.  At the start
+// warps 0-7 and 16-19 bring q to TMEM while 8-15 resolve the list.  Every wait is bounded; one that gives up records
 // SFA_ERR_DEVICE_TIMEOUT and the kernel unwinds without trapping.
 //
-// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 44.7 us, 256 tokens x 64
-// heads x 2048 rows 88.4 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
-// rows in four shards 47.8 us (22.7).  With one scale for the whole list, and O's reference moving with the
-// largest weight: 45.2, 89.8, 47.0.  Bound: at 64 heads a tile's MMAs take most of its time and the
-// rest is the chain scores -> softmax -> P.V with one score buffer (TMEM is full); the first
-// scores come after 12,600-14,600 cycles (launch, list, table, q and the first rows follow one
-// another), the end takes 5,000, and a second round of units a whole one's time.
+// Measured (device time in a graph): 64 tokens x 128 heads x 2048 rows 45.4 us, 256 tokens x 64
+// heads x 2048 rows 89.9 us (their bytes alone: 13.9 and 50.4 us), 32 tokens x 16 heads x 8192
+// rows in four shards 47.4 us (22.7).  Without the second sum 44.6, 88.5, 46.7; with one scale for
+// the whole list, and O's reference moving with the largest weight, 45.2, 89.8, 47.0.  Bound: at 64
+// heads a tile's MMAs take most of its time and the rest is the chain scores -> softmax -> P.V with
+// one score buffer (TMEM is full); the first scores come after 12,600-14,600 cycles (launch, list,
+// table, q and the first rows follow one another), the end takes 5,000, and a second round of
+// units a whole one's time.
 // Taken back: 64-row tiles in 4 or 5 stages (63 vs 61 us at the time), part of the columns by
 // cp.async (64-94 vs 61), rows prefetched to L2 (67 vs 61, 72 vs 49), P.V handed over in
 // three parts (51.5 vs 49.0), references moved two groups of heads at a time (47.5 vs 45.9).
@@ -78,6 +81,7 @@ constexpr int kQParts = (kGroupHeads + kQWarps - 1) / kQWarps;   // copies of q,
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kWBlock = 32;          // weights under one scale: K of an MMA
 constexpr float kPeak = 8.0f;        // log2 of the most that a block's largest weight is stored as (e4m3 ends at 448)
+constexpr float kFine = 0x1p-6f;     // weights from here on are stored to 2^-9 of themselves
 constexpr float kRise = 24.0f;       // log2 of what a block's scale may rise above its head's reference
 constexpr float kFall = 120.0f;      // and fall below it (a scale is 2^-127 at least)
 
@@ -92,7 +96,7 @@ constexpr int kOffScale = kOffList + kListCap * 4;    // per stage and two rows:
 constexpr int kOffInv = kOffScale + kStages * kNt * 8;  // 1 / scale
 constexpr int kOffMisc = kOffInv + kStages * kNt * 4;
 constexpr int kMiscMl = 0, kMiscAlpha = 512, kMiscScale = 1024, kMiscC = 1280, kMiscFlags = 1536, kMiscTmem = 1540,
-              kMiscMoved = 1544, kMiscCount = 1560, kMiscSeg = 1600, kMiscSf = 1616, kMiscRef = 2128, kMiscBytes = 2384;
+              kMiscMoved = 1544, kMiscCount = 1560, kMiscSeg = 1600, kMiscSf = 1616, kMiscRef = 2128, kMiscKept = 2384, kMiscBytes = 2640;
 constexpr int kOffBar = kOffMisc + kMiscBytes;
 constexpr int kBarKvFull = 0, kBarKvEmpty = kBarKvFull + kStages, kBarRows = kBarKvEmpty + kStages,
               kBarSegFree = kBarRows + kStages, kBarSegFull = kBarSegFree + 1, kBarQLoad = kBarSegFull + 1, kBarQReady = kBarQLoad + kQParts,
@@ -355,6 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* moved_s = reinterpret_cast<uint8_t*>(misc + kMiscMoved);      // [2][8] whether 8 heads' references moved
   uint32_t* sf_s = reinterpret_cast<uint32_t*>(misc + kMiscSf);          // [2][64] the scales of hi's three blocks, as ue8m0
   float* below_s = reinterpret_cast<float*>(misc + kMiscRef);            // [64] O's reference, relative to that of (m, l)
+  float* kept_s = reinterpret_cast<float*>(misc + kMiscKept);            // [64] l of the weights as they are stored
   float* scale_s = reinterpret_cast<float*>(misc + kMiscScale);          // [64] output scales
   float* qc_s = reinterpret_cast<float*>(misc + kMiscC);                 // [64] score scale, NaN for a bad head
   volatile int* abort_s = reinterpret_cast<volatile int*>(misc + kMiscFlags);
@@ -463,7 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quad = warp & 3, half = warp >> 2;
   const int head = 16 * quad + 8 * half + (lane >> 2);
   const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
-  float ref = -INFINITY, top = -INFINITY, l_sum = 0.f;   // reference of O; of l_sum (the largest so far)
+  float ref = -INFINITY, top = -INFINITY;   // reference of O; of the sums (the largest so far)
+  float l_sum = 0.f, l_kept = 0.f;          // of the weights, and of the weights as they are stored
   // Roles follow in place, so that each warp runs through code that lies next to what it ran
   // before (the instruction cache is cold at every launch).
   if (warp >= kSoftWarps && warp < kFixWarp) {
@@ -790,6 +796,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tmem_st16(tmem + ((uint32_t)(quad * 32) << 16) + kColQ + 16 * c, v);
     }
+    if (warp >= kFixWarp)                   // (warps 16-19 reach the lanes of all quadrants)
+      tmem_st4(tmem + ((uint32_t)(quad * 32) << 16) + kColSfE, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
     tmem_st_wait();
     tc_fence_before();
     fence_proxy_async_smem();               // the gathers write these stages next
@@ -805,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool bad_q = c_head != c_head;
         if (bad_q) c_head = 1e-30f;
         const uint64_t c2 = pack2(c_head, c_head), sixteenth = pack2(0.0625f, 0.0625f);
-        uint64_t l2 = 0;                                        // two running sums
+        uint64_t l2 = 0, k2 = 0;                                // two running sums each
         // this head's row of P^T (K-major SW128) and this thread's bytes 16 k + 8 u + 2 (lane % 4)
         char* const p_row = smem + kOffP + head * 128 + 2 * (lane & 3);
         for (int i = 0; i < n_local; ++i) {
@@ -882,14 +890,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the sum's reference is the largest e so far
           const float top_new = fmaxf(top, most), fade = ex2(top - top_new);
           l2 = mul2(l2, pack2(fade, fade));
+          k2 = mul2(k2, pack2(fade, fade));
           top = top_new;
-          // P = 2^(x - e) as hi + lo / 16; p = P / scale into the sum
+          // P = 2^(x - e) as hi + lo / 16.  Into one sum goes p = P / scale; into another 16 times what the
+          // rounding of a large weight added to its p (a small one may be off by more than itself, and
+          // one of a small scale then by more than all others)
           const float2* iv = reinterpret_cast<const float2*>(inv_s + st * kNt) + (lane & 3);
           char* const row = p_row + 2 * bb * kPBytes;
   #pragma unroll
           for (int k = 0; k < kNt / kWBlock; ++k) {
             const uint64_t ne = pack2(-e[k], -e[k]);
-            uint64_t sum = 0;
+            uint64_t sum = 0, more = 0;
   #pragma unroll
             for (int j = 4 * k; j < 4 * k + 4; ++j) {
               const float2 f = unpack2(add2(x[j], ne));
@@ -901,11 +912,15 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint32_t hi = e4m3x2_h(w);
               const int at = (((j >> 1) ^ (head & 7)) << 4) + 8 * (j & 1);
               *reinterpret_cast<uint16_t*>(row + at) = (uint16_t)hi;
-              *reinterpret_cast<uint16_t*>(row + at + kPBytes) =
-                  (uint16_t)e4m3x2_h(__hmul2(__hsub2(w, half2_of(hi)), __floats2half2_rn(16.f, 16.f)));
+              const __half2 left = __hmul2(__hsub2(w, half2_of(hi)), __floats2half2_rn(16.f, 16.f));
+              const uint32_t lo = e4m3x2_h(left);
+              *reinterpret_cast<uint16_t*>(row + at + kPBytes) = (uint16_t)lo;
+              const float2 d = __half22float2(__hmul2(__hsub2(half2_of(lo), left), __hge2(w, __floats2half2_rn(kFine, kFine))));
+              more = fma2(pack2(d.x, d.y), pack2(inv.x, inv.y), more);
             }
             const float part = ex2(e[k] - top);
             l2 = fma2(sum, pack2(part, part), l2);
+            k2 = fma2(more, pack2(part, part), k2);
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -915,7 +930,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         l_sum = f.x + f.y;
         l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 1);
         l_sum += __shfl_xor_sync(0xffffffffu, l_sum, 2);
-        if (bad_q && n_local > 0) l_sum = __int_as_float(0x7fc00000);
+        const float2 g = unpack2(k2);
+        l_kept = g.x + g.y;
+        l_kept += __shfl_xor_sync(0xffffffffu, l_kept, 1);
+        l_kept += __shfl_xor_sync(0xffffffffu, l_kept, 2);
+        l_kept = l_sum + l_kept * 0.0625f;
+        if (bad_q && n_local > 0) l_sum = l_kept = __int_as_float(0x7fc00000);
       }
     } else if (warp >= kFixWarp) {
       // =================== O follows the references (warps 16-19) ====================
@@ -923,7 +943,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Where a head's reference moved with tile i, its column of O^T is scaled between P.V of
       // tiles i-1 and i.
       const uint32_t my_lanes = tmem + ((uint32_t)((warp - kFixWarp) * 32) << 16);
-      tmem_st4(my_lanes + kColSfE, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu, 0x7f7f7f7fu);
       for (int i = 0; i < n_local && !*abort_s; ++i) {
         const int bb = i & 1;
         if (!wait_warp(&bars[kBarAReady + bb], (i >> 1) & 1)) {
@@ -976,7 +995,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (quad < HB && (lane & 3) == 0) {
       ml_s[head] = make_float2(top, l_sum);
       below_s[head] = ref - top;
-      if (G == 1) scale_s[head] = l_sum != 0.f ? ex2(ref - top) / l_sum : 0.f;
+      kept_s[head] = l_kept;
+      if (G == 1) scale_s[head] = l_kept != 0.f ? ex2(ref - top) / l_kept : 0.f;
     }
   }
   // (a CTA alone needs no cluster barrier, here and below)
@@ -1033,15 +1053,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x < NH) {
     // this head's largest reference M, sum L and the weight of this CTA's O
     const int hd = threadIdx.x;
-    float M = -INFINITY, L = 0.f;
+    float M = -INFINITY, L = 0.f, K = 0.f;
     for (uint32_t c = 0; c < G; ++c) M = fmaxf(M, ld_cluster_f32(mapa(&ml_s[hd], c)));
     for (uint32_t c = 0; c < G; ++c) {
       const uint32_t a = mapa(&ml_s[hd], c);
       const float lc = ld_cluster_f32(a + 4u);
-      if (lc != 0.f) L += ex2(ld_cluster_f32(a) - M) * lc;
+      if (lc == 0.f) continue;
+      const float f = ex2(ld_cluster_f32(a) - M);
+      L += f * lc;
+      K += f * ld_cluster_f32(mapa(&kept_s[hd], c));
     }
     const float2 mine = ml_s[hd];
-    scale_s[hd] = mine.y != 0.f ? ex2(mine.x - M + below_s[hd]) / L : 0.f;
+    scale_s[hd] = mine.y != 0.f ? ex2(mine.x - M + below_s[hd]) / K : 0.f;
     if (crank == 0 && hd < nh && good) p.lse[lse_at + hd] = L != 0.f ? (M + __log2f(L)) * kLn2 : -INFINITY;
   }
   __syncthreads();

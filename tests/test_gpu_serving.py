@@ -722,6 +722,30 @@ def test_decode_q8_a_dominant_row_in_one_of_several_shards(path, h, n, il):
     _near(*_run(pr, n, il), [x[0] for x in _oracle(pr)], f"n={n}")
 
 
+@pytest.mark.parametrize("h", [3, 64, 128])
+@pytest.mark.parametrize("others", [0, 5, 700])
+def test_decode_q8_a_row_with_all_the_weight_comes_back(path, h, others):
+    # one used row, or one 60 nats above the others: out is its values, whatever its weight's rounding.
+    # 2^-11 for the half-precision step of the weight, 2^-16 for fp32 arithmetic
+    pr = _problem(140 + h, 3, 1, h, 800, others + 1, group=16)
+    q = pr["q"].float()
+    q[..., 512:] = 1.0
+    pr["q"] = q.to(torch.bfloat16)
+    want = np.zeros((3, h, 512))
+    for t in range(3):
+        for j, p in enumerate(pr["idx"][t]):
+            b, r = pr["bt"][t][p // 64], p % 64
+            c = pr["scales"][b, r // 16]
+            pr["codes"][b, r, 512:] = serving.to_e4m3(np.clip((5.0 if j == others // 2 else -8.0) / c, -448, 448))
+            pr["codes"][b, r, :512] &= 0x7f if j == others // 2 else 0xff
+            if j == others // 2:
+                want[t] = serving.E4M3[pr["codes"][b, r, :512]] * float(c)
+    pr["q"][..., :512] = 0
+    out, lse = _run(pr, scale=0.08)
+    assert np.all(np.abs(out.double().cpu().numpy() - want) <= (2.0 ** -11 + 2.0 ** -16) * np.abs(want) + 1e-20)
+    assert torch.all(torch.isfinite(lse))
+
+
 @pytest.mark.parametrize("h", [16, 64])
 @pytest.mark.parametrize("step", [0.05, 0.7, 6.0, -0.05, -0.7, -6.0])
 def test_decode_q8_scores_that_climb_and_fall_through_the_list(path, h, step):
