@@ -320,9 +320,13 @@ cudaError_t launch_kv_write_q8(void* kv8, float* scales, long long num_slots, in
   uint4* kv = static_cast<uint4*>(kv8);
   const uint4* src = static_cast<const uint4*>(rows);
   GroupRecord* rec = static_cast<GroupRecord*>(workspace);
-  // One launch for the rows of a decode step: 64 rows that join as many groups 2.9 us (two launches
-  // 4.2), 304 rows 3.8 (4.4), 512 rows 6.4 (4.4).  Where groups get many rows each of these takes
-  // longer on the device: 304 rows in groups of 16 5.9 (4.5), of 64 8.6 (4.7).
+  // One launch for few rows.  A block a group moves the group's other rows when their scale rises, the
+  // two launches do it by one warp: rows of as many groups whose scales all rise take 4.2 us at 64 rows
+  // and 5.8 at 304 in groups of 64 (two launches 22 and 23), 3.7 and 4.9 in groups of 16 (8.6 and 9.1); a
+  // chunk that begins inside a group 6.8 and 8.4 in groups of 64 (13).  Where nothing has to move, as
+  // for a prompt from a block's start, the block of a group with many rows is the longer way: 64 to 304
+  // rows 8.3-8.4 us in groups of 64 (3.5), 4.3-5.8 in groups of 16 (3.4-3.8); at one row a group 64 rows
+  // take 2.9 (4.2), 304 rows 3.8 (4.4), 512 rows 6.4 (4.4).
   if (group > 1 && T <= 2 * device_sm_count() && T <= kFewThreads) {
     q8_few_kernel<<<T, kFewThreads, 0, stream>>>(kv, scales, num_slots, slots, src, T, group, status);
     return cudaGetLastError();
