@@ -7,7 +7,7 @@
 // fp32) and their states are joined at the end.  A row is dequantised to fp32 in registers
 // (e4m3 * scale of its group is exact there for power-of-two scales).  Bound by the
 // arithmetic: rows are read again for every 8 heads (64 tokens x 128 heads x 2048 rows: 4957 us,
-// the tensor-core kernel 46).
+// the tensor-core kernel 45).
 #include <cuda_fp8.h>
 
 #include "sfa_internal.h"

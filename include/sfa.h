@@ -129,6 +129,7 @@ size_t sfa_decode_workspace_bytes(int B, int Q, int h, int top_k, int n_splits);
  *   M = max_r lse_part[r, x];  lse[x] = M + ln sum_r exp(lse_part[r, x] - M)
  *   out[x, :] = sum_r exp(lse_part[r, x] - lse[x]) * out_part[r, x, :]
  *   every lse_part[r, x] = -inf  ->  out[x, :] = 0, lse[x] = -inf
+ *   an lse_part[r, x] that is NaN ->  out[x, :] and lse[x] are NaN
  *
  *   out_part device fp32 [n_splits, rows, dv], lse_part device fp32 [n_splits, rows]
  *   out      device fp32 [rows, dv],           lse      device fp32 [rows]
@@ -244,9 +245,13 @@ sfa_status sfa_uv_proj(const float *out, const void *w_uv, void *y, int T, int h
  * Everything else, and the return codes, as in sfa_decode_ex.
  *
  * Accuracy: lse carries fp32 rounding only (q is exact to 2^-22 of its head's largest value);
- * out, whatever its type, carries the rounding of the softmax weights to 8 significant bits,
- * about 2^-10 of its norm (as sfa_decode's bf16 weights do), and then that of its own type.  A
- * NaN or infinity in a head of q makes that head's out and lse NaN.
+ * out, whatever its type, carries the rounding of the softmax weights, and then that of its own
+ * type.  With w_j the weight of row j times its scale, w_j is off by at most 2^-8 w_j, or by 2^-21
+ * of the largest w of the 32 used rows that it is taken with, where this is more; so out differs by
+ * at most 2^-8 sum_j w_j |kv8_j|, and by about 2^-10 of its norm (as by sfa_decode's bf16 weights),
+ * also where one row has most of the weight.  Rows whose w is below 2^-110 of the largest may count
+ * as none, in lse too.  A NaN or infinity in a head of q makes that head's out and lse NaN, merged
+ * or not; so does a score that is none.
  * sfa_set_kernel_path(1) selects a CUDA-core kernel here too, any other path the tensor cores'.
  */
 #define SFA_OUT_BF16 2
@@ -307,7 +312,7 @@ sfa_status sfa_kv_write_q8(void *kv8, float *scales, long long num_slots, int gr
  *   positions     device int32 [num_tokens]: a token's position; -1 behind the last one
  *   slot_mapping  device int32 [num_tokens]: its slot, block * block_size + position %
  *                 block_size; -1 (which the cache writes skip) behind the last one
- *   taken_out     device int32 [1]: *taken plus the blocks taken, at most num_free
+ *   taken_out     device int32 [1]: *taken plus the blocks taken, at most num_free (or *taken)
  * The outputs must not overlap the inputs (block_table apart), so that taken and taken_out
  * change places from step to step.  A call repeated with the same inputs gives the same
  * outputs.  A table whose width, a free list whose length or a room whose size does not
@@ -330,7 +335,8 @@ sfa_status sfa_step_plan(const int32_t *cached_lens, const int32_t *new_lens, in
  * where (x, y) and (u, v) are columns (2i, 2i + 1) with SFA_ROPE_INTERLEAVED, else
  * (i, i + rot_dim / 2).  SFA_ROPE_INVERSE turns by -a: the transpose, which takes the gradient
  * of (u, v) to that of (x, y).  Columns rot_dim .. width - 1 are copied.  The angle is reduced
- * exactly for every position; arithmetic is fp32, rounded once to the type.
+ * to 2^-22 rad for every position and |inv_freq| < 1024; arithmetic is fp32, rounded once to the
+ * type.  A frequency that is not finite gives NaN in its pair.
  *
  *   x, out      device, element (t, j, d) at t * token_stride + j * head_stride + d (strides in
  *               elements): bf16, fp16 or fp32 (dtype), T tokens of n heads.  out may be x
