@@ -14,6 +14,18 @@ and, around it, one serving step over an 8-bit cache:
     rope(q_pe, positions, inv_freq, out=q[..., 512:])
     kv_write_q8(kv8, scales, slots, rows, workspace=ws)
     out, lse = decode_q8(q, kv8, scales, table, seq_lens, topk_idx, scale)
+
+a step that verifies a tree of drafted tokens, and the blocks that requests hold:
+
+    table, _, start, _, slots, taken = step_plan(cached, nodes, table, free, taken, 64, T)
+    mask, positions = tree_plan(parents, start, cached, max_nodes)
+    kv_write(kv, slots, rows)
+    out, lse = decode_tree(q, kv, table, cached, start, mask, scale)
+    path, accepted, next_tokens, lens = tree_accept(tokens, targets, parents, start, cached, max_nodes)
+    kv_commit(kv, table, cached, path, accepted)
+    taken = blocks_free(table, cached + nodes, lens, shares, free, taken, 64)
+    copies, taken = blocks_fork(table, lens, src, dst, shares, free, taken, 64)
+    kv_copy_blocks(kv, copies)
 """
 from __future__ import annotations
 
@@ -39,6 +51,8 @@ __all__ = ["decode", "lse_merge", "decode_host", "decode_host_staging_bytes",
            "set_wait_limit", "set_stall_injection", "kv_write", "uv_proj", "topk", "HostPlan",
            "decode_q8", "kv_write_q8", "kv_write_q8_workspace_bytes", "step_plan",
            "rope", "rope_inv_freq", "rope_mscale",
+           "tree_plan", "decode_tree", "decode_tree_workspace_bytes", "tree_accept", "kv_commit",
+           "blocks_fork", "blocks_free", "blocks_compact", "kv_copy_blocks", "kv_copy_blocks_q8",
            "SfaError", "D_QK", "D_V", "BLOCK_TABLE_PER_TOKEN"]
 
 
@@ -70,6 +84,7 @@ def _raw_stream(dev):
 
 
 _BF16, _F32, _F64, _I32, _E4M3 = (torch.bfloat16, torch.float32, torch.float64, torch.int32, torch.float8_e4m3fn)
+_I64 = torch.int64
 
 
 def _check(t, name, dtype, dev, ndim, isinstance=isinstance, Tensor=torch.Tensor):
@@ -670,6 +685,318 @@ def rope(x, positions, inv_freq, interleaved: bool = True, mscale: float = 1.0, 
     if code:
         _lib.check("sfa_rope", code)
     return out
+
+
+def _need_tree(token_start, cached_lens, max_nodes, dev):
+    """The checks of what every call of a drafted tree takes; returns (B, max_nodes)."""
+    if dev.type != "cuda":
+        raise ValueError("the calls of drafted trees run on a CUDA device only")
+    _check(token_start, "token_start", _I32, dev, 1)
+    _check(cached_lens, "cached_lens", _I32, dev, 1)
+    B = cached_lens.shape[0]
+    if token_start.shape[0] != B + 1:
+        raise ValueError("token_start must be [B + 1] and cached_lens [B]")
+    max_nodes = int(max_nodes)
+    if max_nodes < 1:
+        raise ValueError("max_nodes must be >= 1")
+    return B, max_nodes
+
+
+def tree_plan(parents, token_start, cached_lens, max_nodes: int, stream=None):
+    """Masks and positions of drafted trees (C ABI ``sfa_tree_plan``).
+
+    parents [T] int32: a node's parent by its number within the request (smaller than its own), -1
+    for a child of the last cached token; token_start [B + 1], cached_lens [B] int32 (request b's
+    nodes are the tokens token_start[b] .. token_start[b + 1] - 1, at most max_nodes).  Returns
+    (mask [T, ceil(max_nodes / 64)] int64, with the bits of each node and its ancestors; positions
+    [T] int32 = cached_lens + depth, -1 for padding tokens).
+    """
+    dev = parents.device
+    B, max_nodes = _need_tree(token_start, cached_lens, max_nodes, dev)
+    _check(parents, "parents", _I32, dev, 1)
+    T = parents.shape[0]
+    with _on(dev, stream):
+        mask = torch.empty((T, (max_nodes + 63) // 64), dtype=_I64, device=dev)
+        positions = torch.empty(T, dtype=_I32, device=dev)
+        code = _lib.load().sfa_tree_plan(parents.data_ptr(), token_start.data_ptr(), cached_lens.data_ptr(), B, T,
+                                         max_nodes, mask.data_ptr(), positions.data_ptr(), _raw_stream(dev))
+    if code:
+        _lib.check("sfa_tree_plan", code)
+    return mask, positions
+
+
+def decode_tree_workspace_bytes(B: int, num_tokens: int, h: int) -> int:
+    return int(_lib.load().sfa_decode_tree_workspace_bytes(int(B), int(num_tokens), int(h)))
+
+
+def decode_tree(q, kv, block_table, cached_lens, token_start, mask, scale: float, out=None, lse=None, workspace=None,
+                stream=None, out_dtype=torch.float32):
+    """Attention of drafted nodes over every cached position of their sequence and the nodes that
+    their mask names (C ABI ``sfa_decode_tree``).
+
+    q [T, h, 576] bf16, kv [num_blocks, block_size, 576] bf16, block_table [B, max_blocks],
+    cached_lens [B], token_start [B + 1] int32, mask [T, words] int64 (``tree_plan``); node j of
+    request b is the token token_start[b] + j and its row lies at position cached_lens[b] + j.
+    Returns (out [T, h, 512] in out_dtype, torch.float32 or torch.bfloat16, or the dtype of the `out`
+    given; lse [T, h] fp32); the rows of padding tokens are left as they were.
+    workspace: decode_tree_workspace_bytes(B, T, h) bytes (allocated when None).
+    """
+    dev = q.device
+    if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+        raise ValueError("mask must be a [T, words] tensor")
+    B, max_nodes = _need_tree(token_start, cached_lens, 64 * mask.shape[1], dev)
+    _check(q, "q", _BF16, dev, 3)
+    _check(kv, "kv", _BF16, dev, 3)
+    _check(block_table, "block_table", _I32, dev, 2)
+    _check(mask, "mask", _I64, dev, 2)
+    T, h, d = q.shape
+    if d != D_QK or kv.shape[2] != D_QK:
+        raise ValueError("q and kv rows must have 576 columns")
+    if mask.shape[0] != T or block_table.shape[0] != B:
+        raise ValueError("mask must be [T, words] and block_table [B, max_blocks]")
+    if out is not None:
+        out_dtype = out.dtype
+    if out_dtype is not _F32 and out_dtype is not _BF16:
+        raise TypeError("out_dtype must be torch.float32 or torch.bfloat16")
+    lib = _lib.load()
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty((T, h, D_V), dtype=out_dtype, device=dev)
+        elif out.shape != (T, h, D_V):
+            raise ValueError(f"out must be [{T}, {h}, {D_V}] and lse [{T}, {h}]")
+        else:
+            _check(out, "out", out_dtype, dev, 3)
+        if lse is None:
+            lse = torch.empty((T, h), dtype=_F32, device=dev)
+        elif lse.shape != (T, h):
+            raise ValueError(f"out must be [{T}, {h}, {D_V}] and lse [{T}, {h}]")
+        else:
+            _check(lse, "lse", _F32, dev, 2)
+        need = lib.sfa_decode_tree_workspace_bytes(B, T, h)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace is not None and (workspace.get_device() != dev.index or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        code = lib.sfa_decode_tree(q.data_ptr(), kv.data_ptr(), block_table.data_ptr(), cached_lens.data_ptr(),
+                                   token_start.data_ptr(), mask.data_ptr(), B, T, h, max_nodes, kv.shape[0],
+                                   kv.shape[1], block_table.shape[1], float(scale),
+                                   OUT_BF16 if out_dtype is _BF16 else 0, out.data_ptr(), lse.data_ptr(),
+                                   workspace.data_ptr() if ws_bytes else 0, ws_bytes, _raw_stream(dev))
+    if code:
+        _lib.check("sfa_decode_tree", code)
+    return out, lse
+
+
+def tree_accept(tokens, targets, parents, token_start, cached_lens, max_nodes: int, stream=None):
+    """The accepted path of each drafted tree (C ABI ``sfa_tree_accept``): from node 0 on, the child
+    with the lowest number whose token is its parent's target.
+
+    tokens, targets, parents [T] int32 (targets: the model's token behind each node).  Returns (path
+    [B, max_nodes]: the accepted nodes' numbers, then -1; accepted [B]; next_tokens [B]: the target
+    behind the last accepted node; seq_lens [B] = cached_lens + accepted), all int32.
+    """
+    dev = tokens.device
+    B, max_nodes = _need_tree(token_start, cached_lens, max_nodes, dev)
+    _check(tokens, "tokens", _I32, dev, 1)
+    _check(targets, "targets", _I32, dev, 1)
+    _check(parents, "parents", _I32, dev, 1)
+    T = tokens.shape[0]
+    if targets.shape[0] != T or parents.shape[0] != T:
+        raise ValueError("tokens, targets and parents must be [T]")
+    with _on(dev, stream):
+        path = torch.empty((B, max_nodes), dtype=_I32, device=dev)
+        accepted = torch.empty(B, dtype=_I32, device=dev)
+        next_tokens = torch.empty(B, dtype=_I32, device=dev)
+        seq_lens = torch.empty(B, dtype=_I32, device=dev)
+        code = _lib.load().sfa_tree_accept(tokens.data_ptr(), targets.data_ptr(), parents.data_ptr(),
+                                           token_start.data_ptr(), cached_lens.data_ptr(), B, T, max_nodes,
+                                           path.data_ptr(), accepted.data_ptr(), next_tokens.data_ptr(),
+                                           seq_lens.data_ptr(), _raw_stream(dev))
+    if code:
+        _lib.check("sfa_tree_accept", code)
+    return path, accepted, next_tokens, seq_lens
+
+
+def _need_layers(kv, name, dtype):
+    """A cache [num_blocks, block_size, 576] or the caches of layers, [layers, ...]; returns (layers,
+    num_blocks, block_size)."""
+    if not isinstance(kv, torch.Tensor) or kv.dim() not in (3, 4):
+        raise ValueError(f"{name} must be a [num_blocks, block_size, 576] or [layers, num_blocks, block_size, 576] tensor")
+    _need(kv, name, dtype)
+    if not kv.is_cuda:
+        raise ValueError(f"{name} must be on a CUDA device")
+    if kv.shape[-1] != D_QK:
+        raise ValueError(f"{name} rows must have 576 columns")
+    return (kv.shape[0] if kv.dim() == 4 else 1), kv.shape[-3], kv.shape[-2]
+
+
+def kv_commit(kv, block_table, cached_lens, path, accepted, stream=None):
+    """The accepted nodes' rows move to consecutive positions (C ABI ``sfa_kv_commit``): the row at
+    position cached_lens[b] + path[b, k] goes to cached_lens[b] + k, for k < accepted[b].
+
+    kv [num_blocks, block_size, 576] bf16, or the caches of several layers with one block table,
+    [layers, num_blocks, block_size, 576]; path [B, max_nodes], accepted [B] as ``tree_accept`` gives
+    them, cached_lens [B] the lengths before the step.  In place; returns kv.
+    """
+    layers, num_blocks, block_size = _need_layers(kv, "kv", _BF16)
+    dev = kv.device
+    _check(block_table, "block_table", _I32, dev, 2)
+    _check(cached_lens, "cached_lens", _I32, dev, 1)
+    _check(path, "path", _I32, dev, 2)
+    _check(accepted, "accepted", _I32, dev, 1)
+    B, max_nodes = path.shape
+    if block_table.shape[0] != B or cached_lens.shape[0] != B or accepted.shape[0] != B:
+        raise ValueError("block_table must be [B, max_blocks], cached_lens and accepted [B] and path [B, max_nodes]")
+    with _on(dev, stream):
+        code = _lib.load().sfa_kv_commit(kv.data_ptr(), layers, num_blocks, block_size, block_table.data_ptr(),
+                                         block_table.shape[1], cached_lens.data_ptr(), path.data_ptr(),
+                                         accepted.data_ptr(), B, max_nodes, _raw_stream(dev))
+    if code:
+        _lib.check("sfa_kv_commit", code)
+    return kv
+
+
+def _need_pool(block_table, shares, free_blocks, taken):
+    """The checks of a block table and its pool; returns (device, rows, max_blocks)."""
+    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda:
+        raise ValueError("block_table must be on a CUDA device")
+    dev = block_table.device
+    _check(block_table, "block_table", _I32, dev, 2)
+    _check(shares, "shares", _I32, dev, 1)
+    _check(free_blocks, "free_blocks", _I32, dev, 1)
+    _check(taken, "taken", _I32, dev, 1)
+    if taken.shape[0] != 1:
+        raise ValueError("taken must be [1]")
+    return dev, block_table.shape[0], block_table.shape[1]
+
+
+def blocks_fork(block_table, lens, src, dst, shares, free_blocks, taken, block_size: int, stream=None):
+    """Rows dst become copies of rows src (C ABI ``sfa_blocks_fork``): whole blocks are shared, the
+    last, partial one gets a block of its own from the free list.
+
+    block_table [rows, max_blocks], lens [rows], shares [num_blocks] int32, in place (shares: the
+    requests that hold a block beyond the first); src, dst [n] int32 rows (< 0 = padding), no row
+    twice in dst and none of dst in src; free_blocks [F], taken [1] as in ``step_plan``.  Returns
+    (copies [n, 3] int32 for ``kv_copy_blocks``: block, its copy, rows, or -1; taken [1]).
+    """
+    dev, rows, max_blocks = _need_pool(block_table, shares, free_blocks, taken)
+    _check(lens, "lens", _I32, dev, 1)
+    _check(src, "src", _I32, dev, 1)
+    _check(dst, "dst", _I32, dev, 1)
+    n = src.shape[0]
+    if lens.shape[0] != rows or dst.shape[0] != n:
+        raise ValueError("lens must be [rows], src and dst [n]")
+    with _on(dev, stream):
+        copies = torch.empty((n, 3), dtype=_I32, device=dev)
+        taken_out = torch.empty(1, dtype=_I32, device=dev)
+        code = _lib.load().sfa_blocks_fork(block_table.data_ptr(), rows, max_blocks, lens.data_ptr(), src.data_ptr(),
+                                           dst.data_ptr(), n, shares.data_ptr(), shares.shape[0],
+                                           free_blocks.data_ptr(), free_blocks.shape[0], taken.data_ptr(),
+                                           int(block_size), copies.data_ptr(), taken_out.data_ptr(), _raw_stream(dev))
+    if code:
+        _lib.check("sfa_blocks_fork", code)
+    return copies, taken_out
+
+
+def blocks_free(block_table, held_lens, keep_lens, shares, free_blocks, taken, block_size: int, stream=None):
+    """Rows give back the blocks between keep_lens and held_lens positions (C ABI
+    ``sfa_blocks_free``): keep 0 ends a request, a little less than held drops rejected drafts.
+
+    held_lens, keep_lens [rows] int32; shares [num_blocks] and free_blocks [F] int32 in place: a
+    shared block loses a share, another goes before entry taken[0] of the free list, in the order of
+    the table.  Returns taken [1].  The table is left as it is.
+    """
+    dev, rows, max_blocks = _need_pool(block_table, shares, free_blocks, taken)
+    _check(held_lens, "held_lens", _I32, dev, 1)
+    _check(keep_lens, "keep_lens", _I32, dev, 1)
+    if held_lens.shape[0] != rows or keep_lens.shape[0] != rows:
+        raise ValueError("held_lens and keep_lens must be [rows]")
+    with _on(dev, stream):
+        taken_out = torch.empty(1, dtype=_I32, device=dev)
+        code = _lib.load().sfa_blocks_free(block_table.data_ptr(), held_lens.data_ptr(), keep_lens.data_ptr(), rows,
+                                           max_blocks, shares.data_ptr(), shares.shape[0], free_blocks.data_ptr(),
+                                           free_blocks.shape[0], taken.data_ptr(), int(block_size),
+                                           taken_out.data_ptr(), _raw_stream(dev))
+    if code:
+        _lib.check("sfa_blocks_free", code)
+    return taken_out
+
+
+def blocks_compact(block_table, lens, shares, free_blocks, taken, block_size: int, max_moves: int, stream=None):
+    """Held blocks move to the front of the pool (C ABI ``sfa_blocks_compact``): the k-th lowest free
+    block takes the place of the k-th highest held one while it lies below it, at most max_moves.
+
+    lens [rows] int32: the positions that each row holds.  Returns new (block_table, shares,
+    free_blocks, copies [max_moves, 3]); ``kv_copy_blocks`` of copies moves a cache's rows, -1 behind
+    the last.  taken stays.
+    """
+    dev, rows, max_blocks = _need_pool(block_table, shares, free_blocks, taken)
+    _check(lens, "lens", _I32, dev, 1)
+    if lens.shape[0] != rows:
+        raise ValueError("lens must be [rows]")
+    max_moves = int(max_moves)
+    if max_moves < 0:
+        raise ValueError("max_moves must be >= 0")
+    with _on(dev, stream):
+        table = torch.empty_like(block_table)
+        shares_out = torch.empty_like(shares)
+        free_out = torch.empty_like(free_blocks)
+        copies = torch.empty((max_moves, 3), dtype=_I32, device=dev)
+        code = _lib.load().sfa_blocks_compact(block_table.data_ptr(), lens.data_ptr(), rows, max_blocks,
+                                              shares.data_ptr(), shares.shape[0], free_blocks.data_ptr(),
+                                              free_blocks.shape[0], taken.data_ptr(), int(block_size), max_moves,
+                                              table.data_ptr(), shares_out.data_ptr(), free_out.data_ptr(),
+                                              copies.data_ptr(), _raw_stream(dev))
+    if code:
+        _lib.check("sfa_blocks_compact", code)
+    return table, shares_out, free_out, copies
+
+
+def _need_copies(copies, dev):
+    _check(copies, "copies", _I32, dev, 2)
+    if copies.shape[1] != 3:
+        raise ValueError("copies must be [n, 3]")
+    return copies.shape[0]
+
+
+def kv_copy_blocks(kv, copies, stream=None):
+    """Copies rows between blocks of a cache (C ABI ``sfa_kv_copy_blocks``): the first copies[i, 2]
+    rows of block copies[i, 0] (< 0 = padding) go to block copies[i, 1].
+
+    kv [num_blocks, block_size, 576] bf16, or the caches of several layers, [layers, num_blocks,
+    block_size, 576]; copies [n, 3] int32, no block twice as a destination and none both source and
+    destination.  In place; returns kv.
+    """
+    layers, num_blocks, block_size = _need_layers(kv, "kv", _BF16)
+    dev = kv.device
+    n = _need_copies(copies, dev)
+    with _on(dev, stream):
+        code = _lib.load().sfa_kv_copy_blocks(kv.data_ptr(), layers, num_blocks, block_size, copies.data_ptr(), n,
+                                              _raw_stream(dev))
+    if code:
+        _lib.check("sfa_kv_copy_blocks", code)
+    return kv
+
+
+def kv_copy_blocks_q8(kv8, scales, copies, stream=None):
+    """``kv_copy_blocks`` of an 8-bit cache (C ABI ``sfa_kv_copy_blocks_q8``): kv8 [(layers,)
+    num_blocks, block_size, 576] float8_e4m3fn with scales [(layers,) num_blocks, block_size / group]
+    fp32, of which the groups that the rows touch are copied too.  In place; returns (kv8, scales).
+    """
+    layers, num_blocks, block_size = _need_layers(kv8, "kv8", _E4M3)
+    dev = kv8.device
+    _need(scales, "scales", _F32, dev, kv8.dim() - 1)
+    groups = scales.shape[-1]
+    if scales.shape[:-1] != kv8.shape[:-2] or groups < 1 or block_size % groups:
+        raise ValueError("scales must be [(layers,) num_blocks, block_size / group] with group dividing block_size")
+    n = _need_copies(copies, dev)
+    with _on(dev, stream):
+        code = _lib.load().sfa_kv_copy_blocks_q8(kv8.data_ptr(), scales.data_ptr(), block_size // groups, layers,
+                                                 num_blocks, block_size, copies.data_ptr(), n, _raw_stream(dev))
+    if code:
+        _lib.check("sfa_kv_copy_blocks_q8", code)
+    return kv8, scales
 
 
 def decode_launches(B, Q, h, top_k, block_size, n_splits, merge=True):

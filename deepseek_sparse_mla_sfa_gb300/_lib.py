@@ -17,7 +17,8 @@ HEADER = os.path.join(os.path.dirname(_HERE), "include", "sfa.h")
 
 STATUS = {0: "SFA_OK", -1: "SFA_ERR_INVALID_ARG", -2: "SFA_ERR_UNSUPPORTED",
           -3: "SFA_ERR_WORKSPACE", -4: "SFA_ERR_CUDA", -5: "SFA_ERR_DEVICE_TIMEOUT",
-          -6: "SFA_ERR_DEVICE_BAD_BLOCK", -7: "SFA_ERR_DEVICE_NO_BLOCKS"}
+          -6: "SFA_ERR_DEVICE_BAD_BLOCK", -7: "SFA_ERR_DEVICE_NO_BLOCKS",
+          -8: "SFA_ERR_DEVICE_BAD_TREE"}
 
 _lock = threading.Lock()
 _lib = None
@@ -53,6 +54,16 @@ SIGNATURES = {
     "sfa_step_plan": ([P, P, I, I, P, I, P, I, P, I, P, P, P, P, P, P], I),
     "sfa_rope": ([P, LL, LL, P, LL, LL, I, I, I, I, I, P, P, F, I, P], I),
     "sfa_uv_proj": ([P, P, P, I, I, P], I),
+    "sfa_tree_plan": ([P, P, P, I, I, I, P, P, P], I),
+    "sfa_tree_accept": ([P, P, P, P, P, I, I, I, P, P, P, P, P], I),
+    "sfa_kv_commit": ([P, I, I, I, P, I, P, P, P, I, I, P], I),
+    "sfa_decode_tree_workspace_bytes": ([I, I, I], SZ),
+    "sfa_decode_tree": ([P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, P, P, SZ, P], I),
+    "sfa_blocks_fork": ([P, I, I, P, P, P, I, P, I, P, I, P, I, P, P, P], I),
+    "sfa_blocks_free": ([P, P, P, I, I, P, I, P, I, P, I, P, P], I),
+    "sfa_blocks_compact": ([P, P, I, I, P, I, P, I, P, I, I, P, P, P, P, P], I),
+    "sfa_kv_copy_blocks": ([P, I, I, I, P, I, P], I),
+    "sfa_kv_copy_blocks_q8": ([P, P, I, I, I, I, P, I, P], I),
 }
 
 

@@ -77,6 +77,14 @@ int* status_word(int dev) {
   return g_status_ptr[dev];
 }
 
+// the status word of the current device (null: none)
+int* current_status() {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess ? status_word(dev) : nullptr;
+}
+
+sfa_status done(cudaError_t e) { return e == cudaSuccess ? SFA_OK : SFA_ERR_CUDA; }
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -118,6 +126,7 @@ const char* sfa_status_string(sfa_status s) {
     case SFA_ERR_DEVICE_TIMEOUT: return "SFA_ERR_DEVICE_TIMEOUT";
     case SFA_ERR_DEVICE_BAD_BLOCK: return "SFA_ERR_DEVICE_BAD_BLOCK";
     case SFA_ERR_DEVICE_NO_BLOCKS: return "SFA_ERR_DEVICE_NO_BLOCKS";
+    case SFA_ERR_DEVICE_BAD_TREE: return "SFA_ERR_DEVICE_BAD_TREE";
   }
   return "SFA_UNKNOWN_STATUS";
 }
@@ -622,6 +631,201 @@ sfa_status sfa_rope(const void* x, long long x_token_stride, long long x_head_st
                           static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? SFA_OK
              : SFA_ERR_CUDA;
+}
+
+static_assert(SFA_TREE_MAX_NODES == sfa::kTreeMaxNodes && SFA_COMPACT_MAX_BLOCKS == sfa::kMaxPoolBlocks,
+              "limits of the header and the kernels");
+
+sfa_status sfa_tree_plan(const int32_t* parents, const int32_t* token_start, const int32_t* cached_lens, int B,
+                         int num_tokens, int max_nodes, int64_t* mask, int32_t* positions, sfa_stream stream) {
+  if (B < 0 || num_tokens < 0 || max_nodes < 1) return SFA_ERR_INVALID_ARG;
+  if (max_nodes > SFA_TREE_MAX_NODES) return SFA_ERR_UNSUPPORTED;
+  if (!token_start || !aligned(token_start, 4) || (B > 0 && (!cached_lens || !aligned(cached_lens, 4))))
+    return SFA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return SFA_OK;
+  if (!parents || !mask || !positions || !aligned(parents, 4) || !aligned(mask, 8) || !aligned(positions, 4))
+    return SFA_ERR_INVALID_ARG;
+  int* status = current_status();
+  if (!status) return SFA_ERR_CUDA;
+  return done(sfa::launch_tree_plan(parents, token_start, cached_lens, B, num_tokens, max_nodes,
+                                    reinterpret_cast<long long*>(mask), positions, status,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+sfa_status sfa_tree_accept(const int32_t* tokens, const int32_t* targets, const int32_t* parents,
+                           const int32_t* token_start, const int32_t* cached_lens, int B, int num_tokens,
+                           int max_nodes, int32_t* path, int32_t* accepted, int32_t* next_tokens, int32_t* seq_lens,
+                           sfa_stream stream) {
+  if (B < 0 || num_tokens < 0 || max_nodes < 1) return SFA_ERR_INVALID_ARG;
+  if (max_nodes > SFA_TREE_MAX_NODES) return SFA_ERR_UNSUPPORTED;
+  if (B == 0) return SFA_OK;
+  if (!token_start || !cached_lens || !path || !accepted || !next_tokens || !seq_lens ||
+      (num_tokens > 0 && (!tokens || !targets || !parents)))
+    return SFA_ERR_INVALID_ARG;
+  for (const int32_t* ptr : {tokens, targets, parents, token_start, cached_lens, (const int32_t*)path,
+                             (const int32_t*)accepted, (const int32_t*)next_tokens, (const int32_t*)seq_lens})
+    if (!aligned(ptr, 4)) return SFA_ERR_INVALID_ARG;
+  int* status = current_status();
+  if (!status) return SFA_ERR_CUDA;
+  return done(sfa::launch_tree_accept(tokens, targets, parents, token_start, cached_lens, B, num_tokens, max_nodes,
+                                      path, accepted, next_tokens, seq_lens, status,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+sfa_status sfa_kv_commit(void* kv, int layers, int num_blocks, int block_size, const int32_t* block_table,
+                         int max_blocks_per_seq, const int32_t* cached_lens, const int32_t* path,
+                         const int32_t* accepted, int B, int max_nodes, sfa_stream stream) {
+  if (layers < 0 || num_blocks < 1 || block_size < 1 || max_blocks_per_seq < 1 || B < 0 || max_nodes < 1)
+    return SFA_ERR_INVALID_ARG;
+  if (max_nodes > SFA_TREE_MAX_NODES) return SFA_ERR_UNSUPPORTED;
+  if (B == 0 || layers == 0) return SFA_OK;
+  if (!kv || !block_table || !cached_lens || !path || !accepted || !aligned(kv, 16) || !aligned(block_table, 4) ||
+      !aligned(cached_lens, 4) || !aligned(path, 4) || !aligned(accepted, 4))
+    return SFA_ERR_INVALID_ARG;
+  int* status = current_status();
+  if (!status) return SFA_ERR_CUDA;
+  return done(sfa::launch_kv_commit(kv, layers, num_blocks, block_size, block_table, max_blocks_per_seq, cached_lens,
+                                    path, accepted, B, max_nodes, status, static_cast<cudaStream_t>(stream)));
+}
+
+sfa_status sfa_decode_tree(const void* q, const void* kv, const int32_t* block_table, const int32_t* cached_lens,
+                           const int32_t* token_start, const int64_t* mask, int B, int num_tokens, int h,
+                           int max_nodes, int num_blocks, int block_size, int max_blocks_per_seq, float scale,
+                           int flags, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                           sfa_stream stream) {
+  if (B < 0 || num_tokens < 0 || h < 1 || max_nodes < 1 || num_blocks < 1 || block_size < 1 ||
+      max_blocks_per_seq < 1 || !isfinite(scale) || (flags & ~SFA_OUT_BF16) != 0)
+    return SFA_ERR_INVALID_ARG;
+  if (h > SFA_MAX_HEADS || max_nodes > SFA_TREE_MAX_NODES || B > SFA_PLAN_MAX_REQUESTS ||
+      (long long)num_blocks * block_size >= INT_MAX || (long long)num_tokens * h >= INT_MAX)
+    return SFA_ERR_UNSUPPORTED;
+  if (B == 0 || num_tokens == 0) return SFA_OK;
+  if (!q || !kv || !block_table || !cached_lens || !token_start || !mask || !out || !lse || !aligned(q, 16) ||
+      !aligned(kv, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(block_table, 4) ||
+      !aligned(cached_lens, 4) || !aligned(token_start, 4) || !aligned(mask, 8))
+    return SFA_ERR_INVALID_ARG;
+  if (workspace_bytes < sfa_decode_tree_workspace_bytes(B, num_tokens, h) ||
+      (workspace_bytes > 0 && (!workspace || !aligned(workspace, 256))))
+    return SFA_ERR_WORKSPACE;
+  sfa::TreeParams p;
+  memset(&p, 0, sizeof p);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.kv = static_cast<const __nv_bfloat16*>(kv);
+  p.block_table = block_table;
+  p.cached = cached_lens;
+  p.token_start = token_start;
+  p.mask = reinterpret_cast<const long long*>(mask);
+  p.B = B;
+  p.T = num_tokens;
+  p.h = h;
+  p.max_nodes = max_nodes;
+  p.words = (max_nodes + 63) / 64;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks_per_seq;
+  p.scale = scale;
+  p.out_bf16 = (flags & SFA_OUT_BF16) ? 1 : 0;
+  p.out = out;
+  p.lse = lse;
+  p.workspace = workspace;
+  p.status = current_status();
+  if (!p.status) return SFA_ERR_CUDA;
+  const long long wl = g_wait_limit.load();
+  p.wait_limit = wl > 0 ? wl : kDefaultWaitLimit;
+  p.stall = g_stall.load();
+  return done(sfa::launch_decode_tree_simt(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t sfa_decode_tree_workspace_bytes(int B, int num_tokens, int h) {
+  (void)B; (void)num_tokens; (void)h;
+  return 0;
+}
+
+sfa_status sfa_blocks_fork(int32_t* block_table, int rows, int max_blocks_per_seq, int32_t* lens, const int32_t* src,
+                           const int32_t* dst, int n, int32_t* shares, int num_blocks, const int32_t* free_blocks,
+                           int num_free, const int32_t* taken, int block_size, int32_t* copies, int32_t* taken_out,
+                           sfa_stream stream) {
+  if (rows < 0 || max_blocks_per_seq < 1 || n < 0 || num_blocks < 1 || num_free < 0 || block_size < 1)
+    return SFA_ERR_INVALID_ARG;
+  if (!taken || !taken_out || taken == taken_out || !shares || (num_free > 0 && !free_blocks) ||
+      (rows > 0 && (!block_table || !lens)) || (n > 0 && (!src || !dst || !copies)))
+    return SFA_ERR_INVALID_ARG;
+  for (const void* ptr : {(const void*)block_table, (const void*)lens, (const void*)src, (const void*)dst,
+                          (const void*)shares, (const void*)free_blocks, (const void*)taken, (const void*)copies,
+                          (const void*)taken_out})
+    if (!aligned(ptr, 4)) return SFA_ERR_INVALID_ARG;
+  int* status = current_status();
+  if (!status) return SFA_ERR_CUDA;
+  return done(sfa::launch_blocks_fork(block_table, rows, max_blocks_per_seq, lens, src, dst, n, shares, num_blocks,
+                                      free_blocks, num_free, taken, block_size, copies, taken_out, status,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+sfa_status sfa_blocks_free(const int32_t* block_table, const int32_t* held_lens, const int32_t* keep_lens, int rows,
+                           int max_blocks_per_seq, int32_t* shares, int num_blocks, int32_t* free_blocks,
+                           int num_free, const int32_t* taken, int block_size, int32_t* taken_out,
+                           sfa_stream stream) {
+  if (rows < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || num_free < 0 || block_size < 1)
+    return SFA_ERR_INVALID_ARG;
+  if (rows > SFA_PLAN_MAX_REQUESTS || (long long)rows * max_blocks_per_seq >= (1 << 30)) return SFA_ERR_UNSUPPORTED;
+  if (!taken || !taken_out || taken == taken_out || !shares || (num_free > 0 && !free_blocks) ||
+      (rows > 0 && (!block_table || !held_lens || !keep_lens)))
+    return SFA_ERR_INVALID_ARG;
+  for (const void* ptr : {(const void*)block_table, (const void*)held_lens, (const void*)keep_lens,
+                          (const void*)shares, (const void*)free_blocks, (const void*)taken, (const void*)taken_out})
+    if (!aligned(ptr, 4)) return SFA_ERR_INVALID_ARG;
+  int* status = current_status();
+  if (!status) return SFA_ERR_CUDA;
+  return done(sfa::launch_blocks_free(block_table, held_lens, keep_lens, rows, max_blocks_per_seq, shares, num_blocks,
+                                      free_blocks, num_free, taken, block_size, taken_out, status,
+                                      static_cast<cudaStream_t>(stream)));
+}
+
+sfa_status sfa_blocks_compact(const int32_t* block_table, const int32_t* lens, int rows, int max_blocks_per_seq,
+                              const int32_t* shares, int num_blocks, const int32_t* free_blocks, int num_free,
+                              const int32_t* taken, int block_size, int max_moves, int32_t* table_out,
+                              int32_t* shares_out, int32_t* free_out, int32_t* copies, sfa_stream stream) {
+  if (rows < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || num_free < 0 || block_size < 1 || max_moves < 0)
+    return SFA_ERR_INVALID_ARG;
+  if (rows > SFA_PLAN_MAX_REQUESTS || (long long)rows * max_blocks_per_seq >= (1 << 30) ||
+      num_blocks > SFA_COMPACT_MAX_BLOCKS)
+    return SFA_ERR_UNSUPPORTED;
+  if (!taken || !shares || !shares_out || (num_free > 0 && (!free_blocks || !free_out)) ||
+      (rows > 0 && (!block_table || !lens || !table_out)) || (max_moves > 0 && !copies) || shares == shares_out ||
+      (num_free > 0 && free_blocks == free_out) || (rows > 0 && block_table == table_out))
+    return SFA_ERR_INVALID_ARG;
+  for (const void* ptr : {(const void*)block_table, (const void*)lens, (const void*)shares, (const void*)free_blocks,
+                          (const void*)taken, (const void*)table_out, (const void*)shares_out, (const void*)free_out,
+                          (const void*)copies})
+    if (!aligned(ptr, 4)) return SFA_ERR_INVALID_ARG;
+  int* status = current_status();
+  if (!status) return SFA_ERR_CUDA;
+  return done(sfa::launch_blocks_compact(block_table, lens, rows, max_blocks_per_seq, shares, num_blocks, free_blocks,
+                                         num_free, taken, block_size, max_moves, table_out, shares_out, free_out,
+                                         copies, status, static_cast<cudaStream_t>(stream)));
+}
+
+static sfa_status copy_blocks(void* kv, float* scales, int group, int row_bytes, int layers, int num_blocks,
+                              int block_size, const int32_t* copies, int n, sfa_stream stream) {
+  if (layers < 0 || num_blocks < 1 || block_size < 1 || n < 0) return SFA_ERR_INVALID_ARG;
+  if (layers == 0 || n == 0) return SFA_OK;
+  if (!kv || !copies || !aligned(kv, 16) || !aligned(copies, 4)) return SFA_ERR_INVALID_ARG;
+  int* status = current_status();
+  if (!status) return SFA_ERR_CUDA;
+  return done(sfa::launch_kv_copy_blocks(kv, scales, group, row_bytes, layers, num_blocks, block_size, copies, n,
+                                         status, static_cast<cudaStream_t>(stream)));
+}
+
+sfa_status sfa_kv_copy_blocks(void* kv, int layers, int num_blocks, int block_size, const int32_t* copies, int n,
+                              sfa_stream stream) {
+  return copy_blocks(kv, nullptr, 1, SFA_D_QK * 2, layers, num_blocks, block_size, copies, n, stream);
+}
+
+sfa_status sfa_kv_copy_blocks_q8(void* kv8, float* scales, int group, int layers, int num_blocks, int block_size,
+                                 const int32_t* copies, int n, sfa_stream stream) {
+  if (group < 1 || block_size < 1 || block_size % group != 0) return SFA_ERR_INVALID_ARG;
+  if (layers > 0 && n > 0 && (!scales || !aligned(scales, 4))) return SFA_ERR_INVALID_ARG;
+  return copy_blocks(kv8, scales, group, SFA_D_QK, layers, num_blocks, block_size, copies, n, stream);
 }
 
 sfa_status sfa_last_device_status(sfa_stream stream) {

@@ -1,0 +1,588 @@
+// sfa_blocks.cu -- the blocks that requests hold: forking a request's blocks, giving blocks back,
+// moving held blocks to the front of the pool, and the copies of cache rows that go with them.
+//
+// The pool is the one the step plan hands out from: free_blocks[taken ..] are free.  shares[x]
+// counts the requests that hold block x beyond the first, so a block fresh from the free list has 0
+// and the plan need not know of it.
+//   fork      a request's whole blocks are shared (shares + 1), its last, partial one is copied
+//   free      a block named m times with s shares is free when m > s, else it has s - m
+//   compact   the k-th lowest free block takes the place of the k-th highest held one, while lower
+// Every output is a function of the inputs alone: counts come from commutative atomics, the order of
+// freed blocks from the first place that names them, ranks from prefix sums.
+//
+// free and compact run as one cluster whose CTAs split the table's entries (and, for compact, the
+// pool's bitmaps) and meet at cluster barriers: no workspace, one launch.
+// Bound: latency (a chain of launch, lengths, table, block counters and the barriers between them)
+// up to some 10^5 table entries; kv_copy_blocks: HBM.
+#include <climits>
+
+#include <cooperative_groups.h>
+
+#include "sfa_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace sfa {
+namespace {
+
+__device__ __forceinline__ int warp_inclusive_sum(int v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// exclusive sum of v over the block's threads, the total in `total`; part: blockDim / 32 words
+__device__ __forceinline__ int block_exclusive_sum(int v, int* part, int& total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, warps = blockDim.x / 32;
+  const int in = warp_inclusive_sum(v, lane);
+  __syncthreads();   // part may still be read
+  if (lane == 31) part[warp] = in;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += part[w];
+    total += part[w];
+  }
+  return before + in - v;
+}
+
+// blocks that `tokens` positions take, at most `most`
+__device__ __forceinline__ int blocks_for(int tokens, int block_size, int most) {
+  const long long n = ((long long)max(tokens, 0) + block_size - 1) / block_size;
+  return n < most ? (int)n : most;
+}
+
+// the last entry e of the non-decreasing a[0..n) with a[e] <= x (a[0] <= x)
+__device__ __forceinline__ int last_at_most(const int* a, int n, int x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// ---------------------------------------------------------------------------- fork
+struct ForkParams {
+  int32_t* table;
+  int rows, max_blocks;
+  int32_t* lens;
+  const int32_t *src, *dst;
+  int n;
+  int32_t* shares;
+  int num_blocks;
+  const int32_t* free_blocks;
+  int num_free;
+  const int32_t* taken;
+  int block_size;
+  int32_t *copies, *taken_out;
+  int* status;
+};
+
+constexpr int kForkThreads = 256, kForkItems = kForkThreads / 32;
+
+// the positions that item i's source holds; -1 where the item is padding or names no row
+__device__ __forceinline__ int fork_len(const ForkParams& p, int i, bool& bad) {
+  const int s = p.src[i], d = p.dst[i];
+  if (s < 0 || d < 0) return -1;
+  if (s >= p.rows || d >= p.rows || s == d) {
+    bad = true;
+    return -1;
+  }
+  return (int)min((long long)max(p.lens[s], 0), min((long long)p.max_blocks * p.block_size, (long long)INT_MAX));
+}
+
+// a warp an item; how many items before it take a block, every CTA counts for itself
+__global__ void __launch_bounds__(kForkThreads) blocks_fork_kernel(const ForkParams p) {
+  __shared__ int part[kForkThreads / 32];
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int i0 = blockIdx.x * kForkItems, i = i0 + warp;
+  bool ignored = false, bad = false, bad_block = false, none = false;
+  int before = 0;
+  for (int j = threadIdx.x; j < min(i0 + kForkItems, p.n); j += kForkThreads) {
+    const int len = fork_len(p, j, ignored);
+    if (j < i0 && len > 0 && len % p.block_size != 0) ++before;
+  }
+  int total;
+  (void)block_exclusive_sum(before, part, total);
+  const long long head = max(*p.taken, 0);
+  long long at = head + total;   // the free entry of this item, if it takes one
+  for (int j = i0; j < i0 + kForkItems && j < p.n; ++j) {
+    const int len = fork_len(p, j, ignored);
+    if (j == i) break;
+    if (len > 0 && len % p.block_size != 0) ++at;
+  }
+  if (i < p.n) {
+    const int len = fork_len(p, i, bad);
+    int c[3] = {-1, -1, -1};
+    if (len >= 0) {
+      const int s = p.src[i], d = p.dst[i];
+      const int full = len / p.block_size, rows = len % p.block_size;
+      const int32_t* from = p.table + (size_t)s * p.max_blocks;
+      int32_t* to = p.table + (size_t)d * p.max_blocks;
+      for (int j = lane; j < full; j += 32) {
+        const int x = from[j];
+        to[j] = x;
+        if (x >= 0 && x < p.num_blocks) atomicAdd(p.shares + x, 1); else bad_block = true;
+      }
+      if (rows > 0) {
+        const int x = from[full];
+        const int fresh = at < p.num_free ? p.free_blocks[at] : -1;
+        if (at >= p.num_free) none = true;
+        const bool ok = x >= 0 && x < p.num_blocks && (fresh >= 0 && fresh < p.num_blocks);
+        if (!ok && at < p.num_free) bad_block = true;
+        if (lane == 0) to[full] = fresh;
+        if (ok) {
+          c[0] = x;
+          c[1] = fresh;
+          c[2] = rows;
+        }
+        ++at;
+      }
+      if (lane == 0) p.lens[d] = len;
+    }
+    if (lane < 3) p.copies[3 * (size_t)i + lane] = lane == 0 ? c[0] : lane == 1 ? c[1] : c[2];
+    if (i == p.n - 1 && lane == 0) *p.taken_out = (int)min(at, max((long long)p.num_free, head));
+  }
+  if (bad || bad_block) report_status(p.status, kStatusBadBlock);
+  if (none) report_status(p.status, kStatusNoBlocks);
+}
+
+// ---------------------------------------------------------------------------- free
+struct FreeParams {
+  const int32_t* table;
+  const int32_t *held, *keep;
+  int rows, max_blocks;
+  int32_t* shares;
+  int num_blocks;
+  int32_t* free_blocks;
+  int num_free;
+  const int32_t* taken;
+  int block_size;
+  int32_t* taken_out;
+  int* status;
+};
+
+constexpr int kClusterThreads = 1024;
+constexpr int kClusterCtas = 8;            // of the forms for large tables
+constexpr int kMarked = INT_MIN;           // shares of a freed block while the call runs: kMarked + e
+
+// sums [rows + 1] of the entries per row, counted by `count(row)`; returns the total
+template <class Count>
+__device__ __forceinline__ int row_sums(int rows, int* sums, int* part, Count count) {
+  const int per = (rows + blockDim.x - 1) / blockDim.x;
+  const int r0 = min((int)threadIdx.x * per, rows), r1 = min(r0 + per, rows);
+  long long mine = 0;
+  for (int r = r0; r < r1; ++r) mine += count(r);
+  int total;
+  int at = block_exclusive_sum((int)mine, part, total);
+  for (int r = r0; r < r1; ++r) {
+    sums[r] = at;
+    at += count(r);
+  }
+  if (threadIdx.x == 0) sums[rows] = total;
+  __syncthreads();
+  return total;
+}
+
+template <int kCtas>
+__global__ void __launch_bounds__(kClusterThreads) blocks_free_kernel(const FreeParams p) {
+  extern __shared__ int sums[];            // [rows + 1]
+  __shared__ int part[kClusterThreads / 32];
+  __shared__ int pushed;                   // blocks that this CTA's entries free
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = kCtas > 1 ? (int)cluster.block_rank() : 0;
+  auto meet = [&] {
+    if (kCtas > 1) {
+      __threadfence();
+      cluster.sync();
+    } else {
+      __syncthreads();
+    }
+  };
+  auto kept = [&](int r) { return blocks_for(p.keep[r], p.block_size, p.max_blocks); };
+  const int total = row_sums(p.rows, sums, part, [&](int r) {
+    return max(0, blocks_for(p.held[r], p.block_size, p.max_blocks) - kept(r));
+  });
+  const int each = (total + kCtas - 1) / kCtas;
+  const int e0 = min(rank * each, total), e1 = min(e0 + each, total);
+  auto entry = [&](int e) -> int {         // the block that entry e names, -1 if none
+    const int r = last_at_most(sums, p.rows, e);
+    const int x = p.table[(size_t)r * p.max_blocks + kept(r) + (e - sums[r])];
+    return x >= 0 && x < p.num_blocks ? x : -1;
+  };
+  bool bad = false;
+  for (int e = e0 + threadIdx.x; e < e1; e += kClusterThreads) {
+    const int x = entry(e);
+    if (x >= 0) atomicSub(p.shares + x, 1); else bad = true;
+  }
+  meet();
+  // below zero: free, and the first entry that names it puts it back
+  for (int e = e0 + threadIdx.x; e < e1; e += kClusterThreads) {
+    const int x = entry(e);
+    if (x < 0) continue;
+    const int v = __ldcg(p.shares + x);
+    if (v >= 0) continue;
+    if (v < -1 && v > INT_MIN / 2) bad = true;   // given back more often than held
+    atomicMin(p.shares + x, kMarked + e);
+  }
+  meet();
+  int mine = 0;
+  for (int e = e0 + threadIdx.x; e < e1; e += kClusterThreads) {
+    const int x = entry(e);
+    mine += x >= 0 && __ldcg(p.shares + x) == kMarked + e;
+  }
+  int sum;
+  (void)block_exclusive_sum(mine, part, sum);
+  if (threadIdx.x == 0) pushed = sum;
+  meet();
+  int before = 0, all = 0;
+  if (kCtas > 1) {
+    for (int c = 0; c < kCtas; ++c) {
+      const int v = *cluster.map_shared_rank(&pushed, c);
+      if (c < rank) before += v;
+      all += v;
+    }
+  } else {
+    all = pushed;
+  }
+  const int head = min(max(*p.taken, 0), p.num_free);
+  long long at = (long long)head - all + before;
+  for (int s0 = e0; s0 < e1; s0 += kClusterThreads) {
+    const int e = s0 + threadIdx.x;
+    const int x = e < e1 ? entry(e) : -1;
+    const bool push = x >= 0 && __ldcg(p.shares + x) == kMarked + e;
+    int n;
+    const int k = block_exclusive_sum(push ? 1 : 0, part, n);
+    if (push) {
+      if (at + k >= 0) p.free_blocks[at + k] = x;
+      p.shares[x] = 0;
+    }
+    at += n;
+  }
+  if (bad) report_status(p.status, kStatusBadBlock);
+  if (rank == 0 && threadIdx.x == 0) {
+    if (all > head) report_status(p.status, kStatusNoBlocks);
+    *p.taken_out = max(head - all, 0);
+  }
+  if (kCtas > 1) cluster.sync();           // `pushed` is read by the others
+}
+
+// ------------------------------------------------------------------------- compact
+struct CompactParams {
+  const int32_t* table;
+  const int32_t* lens;
+  int rows, max_blocks;
+  const int32_t* shares;
+  int num_blocks;
+  const int32_t* free_blocks;
+  int num_free;
+  const int32_t* taken;
+  int block_size, max_moves, words;        // words: bitmap words of a CTA
+  int32_t *table_out, *shares_out, *free_out, *copies;
+  int* status;
+};
+
+// shared memory of a CTA: words of held, free and filled (free blocks that take a held one's
+// place), the held and free blocks of the CTA before each word, then the sums over the rows
+template <int kCtas>
+__global__ void __launch_bounds__(kClusterThreads) blocks_compact_kernel(const CompactParams p) {
+  extern __shared__ unsigned smem_u[];
+  unsigned *held = smem_u, *open = held + p.words, *filled = open + p.words;
+  int *held_before = reinterpret_cast<int*>(filled + p.words), *open_before = held_before + p.words;
+  int* sums = open_before + p.words;
+  __shared__ int part[kClusterThreads / 32];
+  __shared__ int n_held, n_open, n_now, n_moved;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = kCtas > 1 ? (int)cluster.block_rank() : 0;
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int gid = rank * kClusterThreads + tid;
+  constexpr int kAll = kCtas * kClusterThreads;
+  auto meet = [&] {
+    if (kCtas > 1) {
+      __threadfence();
+      cluster.sync();
+    } else {
+      __syncthreads();
+    }
+  };
+  auto remote = [&](auto* at, int c) { return kCtas > 1 ? cluster.map_shared_rank(at, c) : at; };
+  const int head = min(max(*p.taken, 0), p.num_free);
+  bool bad = false;
+
+  for (int w = tid; w < p.words; w += kClusterThreads) held[w] = open[w] = 0;
+  const int total = row_sums(p.rows, sums, part, [&](int r) { return blocks_for(p.lens[r], p.block_size, p.max_blocks); });
+  meet();
+  // what requests hold and what the list has
+  for (int e = gid; e < total; e += kAll) {
+    const int r = last_at_most(sums, p.rows, e);
+    const int x = p.table[(size_t)r * p.max_blocks + (e - sums[r])];
+    if (x < 0 || x >= p.num_blocks) {
+      bad = true;
+      continue;
+    }
+    const int w = x / 32;
+    atomicOr(remote(held, w / p.words) + w % p.words, 1u << (x % 32));
+  }
+  for (int i = head + gid; i < p.num_free; i += kAll) {
+    const int x = p.free_blocks[i];
+    if (x < 0 || x >= p.num_blocks) {
+      bad = true;
+      continue;
+    }
+    const int w = x / 32;
+    const unsigned was = atomicOr(remote(open, w / p.words) + w % p.words, 1u << (x % 32));
+    if (was >> (x % 32) & 1) bad = true;   // listed twice
+  }
+  meet();
+  // blocks before each word: a thread sums a run of words
+  const int per = (p.words + kClusterThreads - 1) / kClusterThreads;
+  const int w0 = min(tid * per, p.words), w1 = min(w0 + per, p.words);
+  int nh = 0, no = 0;
+  for (int w = w0; w < w1; ++w) {
+    if (held[w] & open[w]) {               // held and listed as free: held
+      bad = true;
+      open[w] &= ~held[w];
+    }
+    nh += __popc(held[w]);
+    no += __popc(open[w]);
+  }
+  int sum_h, sum_o;
+  int ah = block_exclusive_sum(nh, part, sum_h);
+  int ao = block_exclusive_sum(no, part, sum_o);
+  for (int w = w0; w < w1; ++w) {
+    held_before[w] = ah;
+    open_before[w] = ao;
+    ah += __popc(held[w]);
+    ao += __popc(open[w]);
+  }
+  if (tid == 0) {
+    n_held = sum_h;
+    n_open = sum_o;
+  }
+  meet();
+  int all_held = 0, base_open = 0;
+  for (int c = 0; c < kCtas; ++c) {
+    const int h = *remote(&n_held, c), o = *remote(&n_open, c);
+    if (c < rank) base_open += o;
+    all_held += h;
+  }
+  // held blocks before the words of CTA c
+  auto base_held = [&](int c) {
+    int n = 0;
+    for (int d = 0; d < c; ++d) n += *remote(&n_held, d);
+    return n;
+  };
+  const int my_base_held = base_held(rank);
+  // pair up: a word a warp, a block a lane
+  int moved = 0;
+  for (int w = warp; w < p.words; w += kClusterThreads / 32) {
+    const unsigned hw = held[w], ow = open[w], below = (1u << lane) - 1;
+    const int x = (rank * p.words + w) * 32 + lane;
+    const int hb = my_base_held + held_before[w] + __popc(hw & below);
+    const int ob = base_open + open_before[w] + __popc(ow & below);
+    bool fill = false, leave = false;
+    if (ow >> lane & 1) {
+      fill = ob < p.max_moves && ob < all_held - hb;
+      if (fill) p.copies[3 * (size_t)ob + 1] = x;
+    } else if (hw >> lane & 1) {
+      const int k = all_held - hb - 1;     // held blocks above it
+      leave = k < p.max_moves && k < ob;
+      if (leave) {
+        p.copies[3 * (size_t)k] = x;
+        p.copies[3 * (size_t)k + 2] = p.block_size;
+      }
+    }
+    const unsigned f = __ballot_sync(0xffffffffu, fill), l = __ballot_sync(0xffffffffu, leave);
+    moved += __popc(l);
+    if (lane == 0) {
+      filled[w] = f;
+      open[w] = (ow & ~f) | l;
+    }
+  }
+  int sum_m;
+  (void)block_exclusive_sum(lane == 0 ? moved : 0, part, sum_m);
+  int nn = 0;
+  for (int w = w0; w < w1; ++w) nn += __popc(open[w]);
+  int sum_n;
+  int an = block_exclusive_sum(nn, part, sum_n);
+  for (int w = w0; w < w1; ++w) {
+    open_before[w] = an;                   // from here on: of the new free blocks
+    an += __popc(open[w]);
+  }
+  if (tid == 0) {
+    n_now = sum_n;
+    n_moved = sum_m;
+  }
+  meet();
+  int base_now = 0, all_now = 0, moves = 0;
+  for (int c = 0; c < kCtas; ++c) {
+    const int n = *remote(&n_now, c);
+    if (c < rank) base_now += n;
+    all_now += n;
+    moves += *remote(&n_moved, c);
+  }
+  // the pool
+  for (int w = warp; w < p.words; w += kClusterThreads / 32) {
+    const int x = (rank * p.words + w) * 32 + lane;
+    const unsigned hw = held[w], ow = open[w];
+    if (x >= p.num_blocks) continue;
+    const bool leave = (hw & ow) >> lane & 1;
+    if (ow >> lane & 1) {
+      const long long at = (long long)head + base_now + open_before[w] + __popc(ow & ((1u << lane) - 1));
+      if (at < p.num_free) p.free_out[at] = x;
+    }
+    if (leave) {
+      const int k = all_held - (my_base_held + held_before[w] + __popc(hw & ((1u << lane) - 1))) - 1;
+      p.shares_out[__ldcg(p.copies + 3 * (size_t)k + 1)] = p.shares[x];
+      p.shares_out[x] = 0;
+    } else if (!(filled[w] >> lane & 1)) {
+      p.shares_out[x] = p.shares[x];
+    }
+  }
+  for (int i = gid; i < p.num_free; i += kAll) {
+    if (i < head) p.free_out[i] = p.free_blocks[i];
+    else if (i >= head + all_now) p.free_out[i] = -1;
+  }
+  for (long long k = 3ll * moves + gid; k < 3ll * p.max_moves; k += kAll) p.copies[k] = -1;
+  // the tables
+  const long long entries = (long long)p.rows * p.max_blocks;
+  for (long long e = gid; e < entries; e += kAll) {
+    const int r = (int)(e / p.max_blocks), j = (int)(e % p.max_blocks);
+    int x = p.table[e];
+    if (j < sums[r + 1] - sums[r] && x >= 0 && x < p.num_blocks) {
+      const int w = x / 32, c = w / p.words, i = w % p.words;
+      const unsigned hw = remote(held, c)[i];
+      if ((hw & remote(open, c)[i]) >> (x % 32) & 1) {
+        const int k = all_held - (base_held(c) + remote(held_before, c)[i] + __popc(hw & ((1u << (x % 32)) - 1))) - 1;
+        x = __ldcg(p.copies + 3 * (size_t)k + 1);
+      }
+    }
+    p.table_out[e] = x;
+  }
+  if (bad) report_status(p.status, kStatusBadBlock);
+  if (kCtas > 1) cluster.sync();           // bitmaps and counts are read by the others
+}
+
+// ---------------------------------------------------------------------------- copy
+struct CopyParams {
+  uint4* kv;
+  float* scales;
+  int layers, num_blocks, block_size, row_words, group;
+  const int32_t* copies;
+  long long n;
+  int chunks;                              // of kCopyWords words a block
+  int* status;
+};
+
+constexpr int kCopyThreads = 256, kCopyPer = 4, kCopyWords = kCopyThreads * kCopyPer;
+
+// a CTA a chunk of 16 KB of one copy in one layer
+__global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const CopyParams p) {
+  const long long id = blockIdx.x;
+  const int chunk = (int)(id % p.chunks);
+  const long long item = id / p.chunks % p.n;
+  const int layer = (int)(id / p.chunks / p.n);
+  const int src = p.copies[3 * item], dst = p.copies[3 * item + 1];
+  const int rows = min(max(p.copies[3 * item + 2], 0), p.block_size);
+  if (src < 0) return;
+  if (src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
+    if (threadIdx.x == 0) report_status(p.status, kStatusBadBlock);
+    return;
+  }
+  const size_t block_words = (size_t)p.block_size * p.row_words;
+  const uint4* from = p.kv + ((size_t)layer * p.num_blocks + src) * block_words;
+  uint4* to = p.kv + ((size_t)layer * p.num_blocks + dst) * block_words;
+  const long long end = (long long)rows * p.row_words, at = (long long)chunk * kCopyWords + threadIdx.x;
+  uint4 x[kCopyPer];
+#pragma unroll
+  for (int u = 0; u < kCopyPer; ++u)
+    if (at + u * kCopyThreads < end) x[u] = from[at + u * kCopyThreads];
+#pragma unroll
+  for (int u = 0; u < kCopyPer; ++u)
+    if (at + u * kCopyThreads < end) to[at + u * kCopyThreads] = x[u];
+  if (p.scales && chunk == 0) {
+    const int per = p.block_size / p.group, n = (rows + p.group - 1) / p.group;
+    for (int g = threadIdx.x; g < n; g += kCopyThreads)
+      p.scales[((size_t)layer * p.num_blocks + dst) * per + g] = p.scales[((size_t)layer * p.num_blocks + src) * per + g];
+  }
+}
+
+template <class Kernel, class Params>
+cudaError_t launch_cluster(Kernel kernel, int ctas, size_t smem, const Params& p, cudaStream_t stream) {
+  if (smem > 40 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kClusterThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = ctas;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t* lens, const int32_t* src,
+                               const int32_t* dst, int n, int32_t* shares, int num_blocks, const int32_t* free_blocks,
+                               int num_free, const int32_t* taken, int block_size, int32_t* copies, int32_t* taken_out,
+                               int* status, cudaStream_t stream) {
+  if (n == 0) return cudaMemcpyAsync(taken_out, taken, 4, cudaMemcpyDeviceToDevice, stream);
+  const ForkParams p{table, rows, max_blocks, lens, src, dst, n, shares, num_blocks, free_blocks,
+                     num_free, taken, block_size, copies, taken_out, status};
+  blocks_fork_kernel<<<(n + kForkItems - 1) / kForkItems, kForkThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_blocks_free(const int32_t* table, const int32_t* held, const int32_t* keep, int rows,
+                               int max_blocks, int32_t* shares, int num_blocks, int32_t* free_blocks, int num_free,
+                               const int32_t* taken, int block_size, int32_t* taken_out, int* status,
+                               cudaStream_t stream) {
+  const FreeParams p{table, held, keep, rows, max_blocks, shares, num_blocks, free_blocks, num_free, taken,
+                     block_size, taken_out, status};
+  const size_t smem = (size_t)(rows + 1) * 4;
+  if ((long long)rows * max_blocks <= 4 * kClusterThreads)
+    return launch_cluster(blocks_free_kernel<1>, 1, smem, p, stream);
+  return launch_cluster(blocks_free_kernel<kClusterCtas>, kClusterCtas, smem, p, stream);
+}
+
+cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int rows, int max_blocks,
+                                  const int32_t* shares, int num_blocks, const int32_t* free_blocks, int num_free,
+                                  const int32_t* taken, int block_size, int max_moves, int32_t* table_out,
+                                  int32_t* shares_out, int32_t* free_out, int32_t* copies, int* status,
+                                  cudaStream_t stream) {
+  const bool small = (long long)rows * max_blocks <= 4 * kClusterThreads && num_blocks <= 8 * kClusterThreads;
+  const int ctas = small ? 1 : kClusterCtas;
+  const int all = (num_blocks + 31) / 32, words = (all + ctas - 1) / ctas;
+  const CompactParams p{table, lens, rows, max_blocks, shares, num_blocks, free_blocks, num_free, taken, block_size,
+                        max_moves, words, table_out, shares_out, free_out, copies, status};
+  const size_t smem = (size_t)words * 20 + (size_t)(rows + 1) * 4;
+  if (small) return launch_cluster(blocks_compact_kernel<1>, 1, smem, p, stream);
+  return launch_cluster(blocks_compact_kernel<kClusterCtas>, kClusterCtas, smem, p, stream);
+}
+
+cudaError_t launch_kv_copy_blocks(void* kv, float* scales, int group, int row_bytes, int layers, int num_blocks,
+                                  int block_size, const int32_t* copies, int n, int* status, cudaStream_t stream) {
+  const int row_words = row_bytes / 16;
+  const long long chunks = ((long long)block_size * row_words + kCopyWords - 1) / kCopyWords;
+  const long long grid = chunks * n * layers;
+  if (grid == 0) return cudaSuccess;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
+  const CopyParams p{static_cast<uint4*>(kv), scales, layers, num_blocks, block_size, row_words, group, copies, n,
+                     (int)chunks, status};
+  kv_copy_blocks_kernel<<<(unsigned)grid, kCopyThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace sfa

@@ -20,10 +20,13 @@ constexpr int kTopkMaxS = 8 * kTopkChunkMax;          // a cluster of at most 8 
 constexpr int kStatusTimeout = -5;
 constexpr int kStatusBadBlock = -6;
 constexpr int kStatusNoBlocks = -7;
+constexpr int kStatusBadTree = -8;
 
 constexpr int kPlanMaxRequests = 8192;   // requests of one step plan (two prefix sums in shared memory)
 constexpr int kQ8MaxWriteGroup = 64;     // slots of a scale group that the 8-bit cache write handles
 constexpr int kQ8RecordBytes = 32;       // its workspace per group
+constexpr int kTreeMaxNodes = 256;       // drafted tokens of a request
+constexpr int kMaxPoolBlocks = 1 << 20;  // blocks of a pool that can be compacted
 
 // One decode problem as the kernels see it.  Pointers are device pointers.
 struct DecodeParams {
@@ -53,6 +56,26 @@ struct DecodeQ8Params {
   const float* scales;   // [num_blocks * block_size / group]
   int group;
   int out_bf16;          // p.out is bf16 (the final result; partials are fp32)
+};
+
+// The attention of drafted trees: request b's nodes are the tokens [token_start[b], token_start[b +
+// 1]), and node j's row is position cached[b] + j of the sequence.
+struct TreeParams {
+  const __nv_bfloat16* q;       // [T, h, 576]
+  const __nv_bfloat16* kv;      // [num_blocks, block_size, 576]
+  const int32_t* block_table;   // [B, max_blocks]
+  const int32_t* cached;        // [B]
+  const int32_t* token_start;   // [B + 1]
+  const long long* mask;        // [T, words]: bit j of a token's words: it attends to node j
+  int B, T, h, max_nodes, words, num_blocks, block_size, max_blocks;
+  float scale;
+  int out_bf16;
+  void* out;                    // [T, h, 512]
+  float* lse;                   // [T, h]
+  void* workspace;
+  int* status;
+  long long wait_limit;
+  int stall;
 };
 
 // Record the first device-side error in the status word (never traps).
@@ -137,6 +160,33 @@ cudaError_t launch_step_plan(const int32_t* cached, const int32_t* fresh_tokens,
 cudaError_t launch_rope(const void* x, long long xt, long long xn, void* out, long long ot, long long on, int dtype,
                         int T, int n, int width, int rot, const int32_t* pos, const double* inv_freq,
                         int interleaved, int inverse, int copy_padding, float mscale, cudaStream_t stream);
+
+cudaError_t launch_tree_plan(const int32_t* parents, const int32_t* token_start, const int32_t* cached, int B, int T,
+                             int max_nodes, long long* mask, int32_t* positions, int* status, cudaStream_t stream);
+cudaError_t launch_tree_accept(const int32_t* tokens, const int32_t* targets, const int32_t* parents,
+                               const int32_t* token_start, const int32_t* cached, int B, int T, int max_nodes,
+                               int32_t* path, int32_t* accepted, int32_t* next_tokens, int32_t* seq_lens, int* status,
+                               cudaStream_t stream);
+cudaError_t launch_kv_commit(void* kv, int layers, int num_blocks, int block_size, const int32_t* table,
+                             int max_blocks, const int32_t* cached, const int32_t* path, const int32_t* accepted,
+                             int B, int max_nodes, int* status, cudaStream_t stream);
+cudaError_t launch_decode_tree_simt(const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t* lens, const int32_t* src,
+                               const int32_t* dst, int n, int32_t* shares, int num_blocks, const int32_t* free_blocks,
+                               int num_free, const int32_t* taken, int block_size, int32_t* copies, int32_t* taken_out,
+                               int* status, cudaStream_t stream);
+cudaError_t launch_blocks_free(const int32_t* table, const int32_t* held, const int32_t* keep, int rows,
+                               int max_blocks, int32_t* shares, int num_blocks, int32_t* free_blocks, int num_free,
+                               const int32_t* taken, int block_size, int32_t* taken_out, int* status,
+                               cudaStream_t stream);
+cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int rows, int max_blocks,
+                                  const int32_t* shares, int num_blocks, const int32_t* free_blocks, int num_free,
+                                  const int32_t* taken, int block_size, int max_moves, int32_t* table_out,
+                                  int32_t* shares_out, int32_t* free_out, int32_t* copies, int* status,
+                                  cudaStream_t stream);
+// scales (one for `group` slots) may be null; row_bytes a multiple of 16
+cudaError_t launch_kv_copy_blocks(void* kv, float* scales, int group, int row_bytes, int layers, int num_blocks,
+                                  int block_size, const int32_t* copies, int n, int* status, cudaStream_t stream);
 
 // tcgen05 path: whether it handles this problem, its workspace, and its launch.  Three
 // kernels: the CTA-pair kernel (any h <= 128), the small-head kernel (h <= 32) and the

@@ -1,0 +1,34 @@
+// sfa_tree_simt.cu -- the attention of a tree of drafted tokens on CUDA cores, every shape: one CTA
+// per (token, group of 8 heads).  The plain form of the definition, to cross-check the tensor cores'
+// kernel.  Bound: fp32 arithmetic and shared-memory reads of q.
+#include <atomic>
+
+#include "sfa_tree.cuh"
+
+namespace sfa {
+namespace {
+
+__global__ void __launch_bounds__(kTreeSimtWarps * 32) decode_tree_simt_kernel(const TreeParams p) {
+  extern __shared__ float smem[];
+  tree_simt(p, blockIdx.x, blockIdx.y * kTreeSimtHeads, smem);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_tree_simt(const TreeParams& p, cudaStream_t stream) {
+  if (p.T == 0 || p.B == 0) return cudaSuccess;
+  static std::atomic<bool> attr_set[64];   // per device: set once (a repeat is harmless)
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(decode_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSimtSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
+  }
+  const dim3 grid(p.T, (p.h + kTreeSimtHeads - 1) / kTreeSimtHeads);
+  decode_tree_simt_kernel<<<grid, kTreeSimtWarps * 32, kTreeSimtSmem, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace sfa

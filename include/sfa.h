@@ -43,7 +43,8 @@ typedef enum {
   SFA_ERR_CUDA = -4,           /* a CUDA runtime call failed (launch error, copy error)        */
   SFA_ERR_DEVICE_TIMEOUT = -5, /* a bounded device-side wait gave up (device status only)      */
   SFA_ERR_DEVICE_BAD_BLOCK = -6, /* a selected position mapped to an invalid block (device)    */
-  SFA_ERR_DEVICE_NO_BLOCKS = -7 /* a step plan ran out of blocks, table or token room (device) */
+  SFA_ERR_DEVICE_NO_BLOCKS = -7, /* a step plan ran out of blocks, table or token room (device) */
+  SFA_ERR_DEVICE_BAD_TREE = -8 /* parents or a path that are no tree's, or too many nodes (device) */
 } sfa_status;
 
 typedef void *sfa_stream; /* a cudaStream_t */
@@ -360,6 +361,192 @@ sfa_status sfa_rope(const void *x, long long x_token_stride, long long x_head_st
                     sfa_stream stream);
 
 /*
+ * A step that verifies drafted trees.  Request b drafts n_b = token_start[b + 1] - token_start[b]
+ * nodes, 0 <= n_b <= max_nodes: the step's tokens token_start[b] .. (sfa_step_plan's token_start,
+ * with new_lens the numbers of nodes).  Node j of request b is the token token_start[b] + j, and its
+ * latent row lies at position cached_lens[b] + j of the sequence (sfa_step_plan's slots), whatever
+ * its depth.  Tokens before token_start[0] and from token_start[B] on are padding.
+ *
+ *   sfa_tree_plan, rope at its positions, the cache write, sfa_decode_tree, ..., sfa_tree_accept,
+ *   sfa_kv_commit in every layer's cache, sfa_blocks_free of what the rejected nodes held
+ *
+ * For all of them: token_start device int32 [B + 1], ascending; cached_lens device int32 [B] (below
+ * 0 counts as 0); num_tokens = rows of the step's token arrays; 1 <= max_nodes <=
+ * SFA_TREE_MAX_NODES; words = ceil(max_nodes / 64).  A request of more than max_nodes nodes sets
+ * SFA_ERR_DEVICE_BAD_TREE, and its nodes from max_nodes on are left out as padding is.
+ */
+#define SFA_TREE_MAX_NODES 256
+
+/*
+ * sfa_tree_plan -- masks and positions of drafted trees from their parents.
+ *
+ *   parents    device int32 [num_tokens]: the number, within its request, of a node's parent
+ *              (smaller than its own), -1 for a child of the last cached token
+ *   mask       device int64 [num_tokens, words], written: bit j % 64 of word j / 64 is set where node
+ *              j is the token itself or one of its ancestors
+ *   positions  device int32 [num_tokens], written: cached_lens[b] + the token's depth (0 without a
+ *              parent), which sfa_rope takes
+ * Padding tokens get no bits and position -1.  A parent that is not smaller than its child, or below
+ * -1, sets SFA_ERR_DEVICE_BAD_TREE and counts as -1.
+ */
+sfa_status sfa_tree_plan(const int32_t *parents, const int32_t *token_start, const int32_t *cached_lens, int B,
+                         int num_tokens, int max_nodes, int64_t *mask, int32_t *positions, sfa_stream stream);
+
+/*
+ * sfa_decode_tree -- attention of each drafted node over all cached positions of its sequence and the
+ * nodes of its own tree that its mask names (dense: every position; for lists of positions, give
+ * sfa_decode a list that holds the node's ancestors).
+ *
+ * For node i of request b (token t) and head hh, over the positions p < cached_lens[b] and
+ * cached_lens[b] + j for every j < n_b with bit j of mask[t]:
+ *   s_p = scale * dot(q[t, hh], kv[row of p]),  out = softmax(s) . kv[rows, 0:512],  lse = ln sum exp(s)
+ *   no position: out = 0, lse = -inf
+ *
+ *   q            device bf16 [num_tokens, h, 576]
+ *   kv, block_table, num_blocks, block_size, max_blocks_per_seq, scale, 1 <= h <= 128  as in sfa_decode;
+ *                num_blocks * block_size < INT_MAX
+ *   mask         device int64 [num_tokens, words]; bits from n_b on are ignored; any mask will do, a
+ *                tree's (sfa_tree_plan) or another
+ *   flags        SFA_OUT_BF16: out is bf16
+ *   out, lse     device fp32 (or bf16) [num_tokens, h, 512] and fp32 [num_tokens, h]; the rows of padding
+ *                tokens are left as they were
+ *   workspace    device, sfa_decode_tree_workspace_bytes(B, num_tokens, h) bytes, 256-byte aligned;
+ *                contents need no initialisation; calls that overlap on the GPU must not share it
+ *   B <= SFA_PLAN_MAX_REQUESTS.
+ * A position whose block-table entry is outside [0, num_blocks) is skipped and sets
+ * SFA_ERR_DEVICE_BAD_BLOCK.  What rows hold that a node does not attend to (other branches, rows
+ * behind the last node) does not reach its result, NaN and infinities included; a NaN or infinity in
+ * a row that it attends to, or in its q, makes its out and lse NaN or infinite.
+ * Accuracy: the softmax weights are rounded to bf16 for the second product, out by at most 2^-8 sum_p
+ * w_p |kv_p| and its own type's rounding, lse by fp32 rounding.
+ * sfa_set_kernel_path(1) selects a CUDA-core kernel.
+ */
+size_t sfa_decode_tree_workspace_bytes(int B, int num_tokens, int h);
+sfa_status sfa_decode_tree(const void *q, const void *kv, const int32_t *block_table, const int32_t *cached_lens,
+                           const int32_t *token_start, const int64_t *mask, int B, int num_tokens, int h,
+                           int max_nodes, int num_blocks, int block_size, int max_blocks_per_seq, float scale,
+                           int flags, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                           sfa_stream stream);
+
+/*
+ * sfa_tree_accept -- the accepted path of each drafted tree: from node 0 (the token that the step
+ * before chose, always accepted) on, the child with the lowest number whose token is its parent's
+ * target, as long as there is one.
+ *
+ *   tokens      device int32 [num_tokens]: the drafted tokens
+ *   targets     device int32 [num_tokens]: the model's token behind each node (its most likely one, or
+ *               one drawn from its distribution)
+ *   parents     device int32 [num_tokens], as in sfa_tree_plan
+ *   path        device int32 [B, max_nodes], written: the accepted nodes' numbers, then -1
+ *   accepted    device int32 [B], written: how many (0 for a request without nodes)
+ *   next_tokens device int32 [B], written: the target of the last accepted node, -1 without one
+ *   seq_lens    device int32 [B], written: cached_lens + accepted (may be cached_lens itself)
+ */
+sfa_status sfa_tree_accept(const int32_t *tokens, const int32_t *targets, const int32_t *parents,
+                           const int32_t *token_start, const int32_t *cached_lens, int B, int num_tokens,
+                           int max_nodes, int32_t *path, int32_t *accepted, int32_t *next_tokens, int32_t *seq_lens,
+                           sfa_stream stream);
+
+/*
+ * sfa_kv_commit -- the accepted nodes' rows move to consecutive positions: row of position
+ * cached_lens[b] + path[b, k] -> position cached_lens[b] + k, for k < accepted[b], in every layer.
+ *
+ *   kv           device bf16 [layers, num_blocks, block_size, 576], in place; 16-byte aligned
+ *   block_table  device int32 [B, max_blocks_per_seq]
+ *   path         device int32 [B, max_nodes], ascending, below SFA_TREE_MAX_NODES; accepted device int32
+ *                [B] (clipped to [0, max_nodes]); cached_lens: the lengths before the step
+ * A path that is not so sets SFA_ERR_DEVICE_BAD_TREE, and the rows from there on stay; a
+ * position whose block-table entry is outside [0, num_blocks) sets SFA_ERR_DEVICE_BAD_BLOCK, and that
+ * row is not moved.  Positions of different requests must lie in different rows.
+ */
+sfa_status sfa_kv_commit(void *kv, int layers, int num_blocks, int block_size, const int32_t *block_table,
+                         int max_blocks_per_seq, const int32_t *cached_lens, const int32_t *path,
+                         const int32_t *accepted, int B, int max_nodes, sfa_stream stream);
+
+/*
+ * Blocks that requests hold.  free_blocks[taken ..] are free, as sfa_step_plan takes them; shares
+ * (device int32 [num_blocks]) counts the requests that hold a block beyond the first.  A block fresh
+ * from the free list has 0, so the step plan need not know of it, and a pool begins with zeros.
+ * Writes go to a block that no other request holds: a fork copies the last, partial block, and a
+ * request that is cut inside a shared block is forked to another row (and the old row freed) first.
+ *
+ *   block_table  device int32 [rows, max_blocks_per_seq]; a row's first ceil(length / block_size)
+ *                entries are the blocks it holds, the others have any value
+ *   taken, taken_out  device int32 [1], two places, as in sfa_step_plan
+ * An entry outside [0, num_blocks) that a call meets is left out and sets SFA_ERR_DEVICE_BAD_BLOCK.
+ */
+
+/*
+ * sfa_blocks_fork -- row dst[i] becomes a copy of row src[i], for every i < n: it shares the whole
+ * blocks (shares + 1) and takes a block of its own for the last, partial one.
+ *
+ *   block_table, lens (device int32 [rows], the positions that each row holds), shares  in place
+ *   src, dst   device int32 [n]: rows; < 0 = padding.  A row is named once as dst, and no dst is a
+ *              src (else the contents of these rows are not defined); src == dst and rows >= `rows` set
+ *              SFA_ERR_DEVICE_BAD_BLOCK and count as padding.  What dst held before is not given back.
+ *   copies     device int32 [n, 3], written: the partial block, the block taken for it and the rows
+ *              to copy, which sfa_kv_copy_blocks takes for each layer; -1 where there is none
+ *   taken_out  *taken plus the blocks taken, at most num_free (or *taken)
+ * Blocks are taken in the order of i.  Where the list ends, the entry is -1, nothing is copied and
+ * SFA_ERR_DEVICE_NO_BLOCKS is set.
+ */
+sfa_status sfa_blocks_fork(int32_t *block_table, int rows, int max_blocks_per_seq, int32_t *lens, const int32_t *src,
+                           const int32_t *dst, int n, int32_t *shares, int num_blocks, const int32_t *free_blocks,
+                           int num_free, const int32_t *taken, int block_size, int32_t *copies, int32_t *taken_out,
+                           sfa_stream stream);
+
+/*
+ * sfa_blocks_free -- every row gives back the blocks that held_lens[r] positions take and
+ * keep_lens[r] positions do not (0: the request is over; less than held: rejected drafts).
+ *
+ *   shares       in place: a block named m times with s shares has s - m after it, or, where m > s, 0
+ *                and is free (m > s + 1 sets SFA_ERR_DEVICE_BAD_BLOCK)
+ *   free_blocks  device int32 [num_free], in place: the freed blocks go before entry *taken, in the
+ *                order in which rows and entries name them first
+ *   taken_out    *taken less the blocks freed; where that is below 0 the first ones are lost and
+ *                SFA_ERR_DEVICE_NO_BLOCKS is set
+ *   rows <= SFA_PLAN_MAX_REQUESTS, rows * max_blocks_per_seq < 2^30.  The table is left as it is.
+ */
+sfa_status sfa_blocks_free(const int32_t *block_table, const int32_t *held_lens, const int32_t *keep_lens, int rows,
+                           int max_blocks_per_seq, int32_t *shares, int num_blocks, int32_t *free_blocks,
+                           int num_free, const int32_t *taken, int block_size, int32_t *taken_out,
+                           sfa_stream stream);
+
+/*
+ * sfa_blocks_compact -- held blocks move to the front of the pool: the k-th lowest free block takes
+ * the place of the k-th highest held one, for k < max_moves and as long as it lies below it.  With
+ * every move made, the held blocks lie below the free ones.  Blocks neither held nor free stay.
+ *
+ *   lens        device int32 [rows]: the positions that each row holds
+ *   table_out   device int32 [rows, max_blocks_per_seq]: the table with the moved blocks' places
+ *   shares_out  device int32 [num_blocks]: shares, moved with their blocks
+ *   free_out    device int32 [num_free]: entries before *taken as they were, then the free blocks after
+ *               the moves in ascending order, then -1
+ *   copies      device int32 [max_moves, 3]: block, its place, block_size, which sfa_kv_copy_blocks
+ *               takes for each layer; -1 behind the last
+ * The outputs overlap no input.  num_blocks <= SFA_COMPACT_MAX_BLOCKS, rows as in sfa_blocks_free.
+ */
+#define SFA_COMPACT_MAX_BLOCKS (1 << 20)
+sfa_status sfa_blocks_compact(const int32_t *block_table, const int32_t *lens, int rows, int max_blocks_per_seq,
+                              const int32_t *shares, int num_blocks, const int32_t *free_blocks, int num_free,
+                              const int32_t *taken, int block_size, int max_moves, int32_t *table_out,
+                              int32_t *shares_out, int32_t *free_out, int32_t *copies, sfa_stream stream);
+
+/*
+ * sfa_kv_copy_blocks -- in every layer, the first copies[i, 2] rows (clipped to [0, block_size]) of
+ * block copies[i, 0] go to block copies[i, 1]; a first block < 0 is padding.  No block is named twice as
+ * a destination, and no destination is a source.
+ *   kv      device bf16 [layers, num_blocks, block_size, 576], in place; 16-byte aligned
+ *   copies  device int32 [n, 3]
+ * sfa_kv_copy_blocks_q8: the same in an 8-bit cache, with the scales (device fp32 [layers, num_blocks,
+ * block_size / group]) of the groups that the rows touch.
+ */
+sfa_status sfa_kv_copy_blocks(void *kv, int layers, int num_blocks, int block_size, const int32_t *copies, int n,
+                              sfa_stream stream);
+sfa_status sfa_kv_copy_blocks_q8(void *kv8, float *scales, int group, int layers, int num_blocks, int block_size,
+                                 const int32_t *copies, int n, sfa_stream stream);
+
+/*
  * sfa_decode_host -- one decode step whose per-step inputs and outputs live in
  * host memory, with the latent cache resident on the device (the form a serving
  * loop that keeps its cache in HBM uses).  Enqueues on `stream`: host->device
@@ -424,7 +611,8 @@ void sfa_host_plan_destroy(sfa_host_plan plan);
  * current device's status word: SFA_OK, SFA_ERR_DEVICE_TIMEOUT (a bounded wait
  * inside a kernel gave up; that kernel's outputs are undefined) or
  * SFA_ERR_DEVICE_BAD_BLOCK (a selected position's block-table entry was outside
- * [0, num_blocks); that row was skipped) or SFA_ERR_DEVICE_NO_BLOCKS (sfa_step_plan).
+ * [0, num_blocks); that row was skipped) or SFA_ERR_DEVICE_NO_BLOCKS (sfa_step_plan,
+ * sfa_blocks_fork, sfa_blocks_free) or SFA_ERR_DEVICE_BAD_TREE (the calls of drafted trees).
  * The first error since the last read is kept.  SFA_ERR_CUDA if the stream itself failed.
  */
 sfa_status sfa_last_device_status(sfa_stream stream);

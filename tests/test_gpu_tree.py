@@ -1,0 +1,415 @@
+"""GPU parity of a step that verifies drafted trees against the fp64 oracle: plan, attention,
+accepted path, commit, and a run of them together over several steps."""
+import numpy as np
+import pytest
+import torch
+
+import deepseek_sparse_mla_sfa_gb300 as sfa
+from oracle import tree
+
+pytestmark = pytest.mark.gpu
+
+BAD_BLOCK, TIMEOUT, BAD_TREE = -6, -5, -8
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def trees(rng, nodes, chain=0.3):
+    """Parents of trees with these numbers of nodes; node 0 is the root."""
+    out = []
+    for n in nodes:
+        for i in range(n):
+            out.append(-1 if i == 0 else i - 1 if rng.random() < chain else int(rng.integers(0, i)))
+    return out
+
+
+# -------------------------------------------------------------------------------- plan
+@pytest.mark.parametrize("nodes,most", [
+    ([1], 1), ([0, 3, 0], 4), ([64, 1, 63], 64), ([65, 0, 64], 65), ([256, 1, 200], 256), ([5] * 300, 8), ([], 3),
+    ([33, 32, 31], 40)])
+@pytest.mark.parametrize("before,behind", [(0, 0), (3, 1500)])
+def test_plan_matches_oracle(nodes, most, before, behind):
+    rng = np.random.default_rng(len(nodes) + most)
+    parents = [7] * before + trees(rng, nodes) + [99] * behind
+    start = before + np.concatenate([[0], np.cumsum(nodes)]).astype(int)
+    cached = rng.integers(0, 1000, len(nodes))
+    mask, pos = sfa.tree_plan(i32(parents), i32(start), i32(cached), most)
+    assert sfa.last_device_status() == 0
+    want, wpos = tree.tree_plan(parents, start, cached, most)
+    assert np.array_equal(mask.cpu().numpy(), tree.mask_words(want, -(-most // 64)))
+    assert pos.tolist() == wpos
+
+
+def test_plan_reports_what_is_no_tree():
+    for parents in ([-1, 1, 0], [-1, 0, 5], [-1, -2, 1]):
+        mask, pos = sfa.tree_plan(i32(parents), i32([0, 3]), i32([4]), 8)
+        assert sfa.last_device_status() == BAD_TREE
+        want, wpos = tree.tree_plan(parents, [0, 3], [4], 8)
+        assert mask.flatten().tolist() == want and pos.tolist() == wpos
+    mask, pos = sfa.tree_plan(i32([-1, 0, 1, 2]), i32([0, 4]), i32([4]), 2)       # more nodes than max_nodes
+    assert sfa.last_device_status() == BAD_TREE
+    assert mask.flatten().tolist() == [1, 3, 0, 0] and pos.tolist() == [4, 5, -1, -1]
+    mask, pos = sfa.tree_plan(i32([-1, 0, 1, 2]), i32([0, 9]), i32([-3]), 16)     # beyond the step's tokens
+    assert sfa.last_device_status() == 0 and pos.tolist() == [0, 1, 2, 3]
+
+
+# ------------------------------------------------------------------------------ accept
+@pytest.mark.parametrize("nodes,most", [([1], 1), ([0, 3, 0, 9], 9), ([256, 100, 33, 2], 256), ([8] * 301, 8)])
+@pytest.mark.parametrize("hit", [0.0, 0.5, 1.0])
+def test_accept_matches_oracle(nodes, most, hit):
+    rng = np.random.default_rng(most + int(10 * hit))
+    parents = trees(rng, nodes, chain=0.7) + [0, 0]
+    start = np.concatenate([[0], np.cumsum(nodes)]).astype(int)
+    T = len(parents)
+    tokens, targets = rng.integers(0, 5, T), rng.integers(0, 5, T)
+    for b, n in enumerate(nodes):
+        for i in range(1, n):
+            if rng.random() < hit:
+                targets[start[b] + parents[start[b] + i]] = tokens[start[b] + i]
+    cached = rng.integers(0, 100, len(nodes))
+    got = sfa.tree_accept(i32(tokens), i32(targets), i32(parents), i32(start), i32(cached), most)
+    assert sfa.last_device_status() == 0
+    for g, w in zip(got, tree.tree_accept(tokens, targets, parents, start, cached, most)):
+        assert np.array_equal(g.cpu().numpy(), w)
+
+
+def test_accept_of_too_many_nodes_and_bad_parents():
+    # parents that point ahead or at themselves never match, so the walk ends
+    got = sfa.tree_accept(i32([1, 1, 1, 1]), i32([1] * 4), i32([0, 1, 3, 0]), i32([0, 4]), i32([5]), 4)
+    assert sfa.last_device_status() == 0 and got[0].tolist() == [[0, 3, -1, -1]] and got[3].tolist() == [7]
+    got = sfa.tree_accept(i32([1] * 4), i32([1] * 4), i32([-1, 0, 1, 2]), i32([0, 4]), i32([5]), 2)
+    assert sfa.last_device_status() == BAD_TREE and got[0].tolist() == [[0, 1]] and got[1].tolist() == [2]
+
+
+# ------------------------------------------------------------------------------ commit
+def paged(rng, lens, bs, spare=3):
+    n = [-(-int(x) // bs) for x in lens]
+    ids, at, table = rng.permutation(sum(n) + spare), 0, np.full((len(lens), max(n, default=0) + 2), -1)
+    for b, k in enumerate(n):
+        table[b, :k] = ids[at:at + k]
+        at += k
+    return table, sum(n) + spare
+
+
+@pytest.mark.parametrize("layers", [None, 1, 3])
+@pytest.mark.parametrize("bs", [1, 7, 64])
+@pytest.mark.parametrize("B,most", [(1, 1), (5, 8), (70, 33), (2, 256)])
+def test_commit_matches_oracle(layers, bs, B, most):
+    rng = np.random.default_rng(B + bs)
+    cached = rng.integers(0, 90, B)
+    path, acc = np.full((B, most), -1), np.zeros(B, int)
+    for b in range(B):
+        acc[b] = rng.integers(0, most + 1)
+        path[b, :acc[b]] = np.sort(rng.permutation(most)[:acc[b]])
+    table, nb = paged(rng, cached + most, bs)
+    kv = torch.randn((layers or 1, nb, bs, 576)).to(torch.bfloat16)
+    want = np.stack([tree.kv_commit(x.float().numpy(), table, cached, path, acc) for x in kv])
+    dev = kv.cuda() if layers else kv[0].cuda()
+    assert sfa.kv_commit(dev, i32(table), i32(cached), i32(path), i32(acc)) is dev
+    assert sfa.last_device_status() == 0
+    assert np.array_equal(dev.float().cpu().numpy().reshape(want.shape), want)
+
+
+def test_commit_of_bad_paths_and_blocks():
+    kv = torch.arange(6 * 4, dtype=torch.float32).reshape(6, 4, 1).expand(6, 4, 576).to(torch.bfloat16).cuda()
+    rows = lambda x: x[..., 0].flatten().tolist()  # noqa: E731
+    base = rows(kv)
+    for path, status, moved in (([0, 2, 2], BAD_TREE, {1: 2}), ([2, 1, 3], BAD_TREE, {0: 2}), ([0, 256, 257], BAD_TREE, {}),
+                                ([-1, 1, 2], BAD_TREE, {}), ([1, 3, -1], 0, {0: 1, 1: 3})):
+        x = kv.clone()
+        sfa.kv_commit(x, i32([[0, 1]]), i32([0]), i32([path + [-1] * 5]), i32([3 if path[-1] >= 0 else 2]))
+        assert sfa.last_device_status() == status
+        want = list(base)
+        for a, b in moved.items():
+            want[a] = base[b]
+        assert rows(x) == want, path
+    for table in ([[0, -1]], [[0, 6]]):
+        x = kv.clone()
+        sfa.kv_commit(x, i32(table), i32([2]), i32([[1, 2, 3]]), i32([3]))        # positions 4 and 5 have no block
+        assert sfa.last_device_status() == BAD_BLOCK
+        assert rows(x) == [0, 1, 3] + base[3:]
+    x = kv.clone()
+    sfa.kv_commit(x, i32([[0]]), i32([2 ** 31 - 2]), i32([[1, 2, 3]]), i32([7]))  # behind every table
+    assert sfa.last_device_status() == BAD_BLOCK and rows(x) == base
+
+
+# -------------------------------------------------------------------------------- decode
+def problem(seed, cached, nodes, h, bs, most=None, before=0, behind=2, std=1.0):
+    rng = np.random.default_rng(seed)
+    cached, nodes = np.asarray(cached), np.asarray(nodes)
+    most = most or max(int(nodes.max(initial=1)), 1)
+    table, nb = paged(rng, cached + nodes, bs)
+    g = torch.Generator().manual_seed(seed)
+    T = before + int(nodes.sum()) + behind
+    start = before + np.concatenate([[0], np.cumsum(nodes)]).astype(int)
+    mask, _ = tree.tree_plan([-1] * before + trees(rng, nodes) + [-1] * behind, start, cached, most)
+    return dict(q=(torch.randn((T, h, 576), generator=g) * std).to(torch.bfloat16),
+                kv=torch.randn((nb, bs, 576), generator=g).to(torch.bfloat16), table=table, cached=cached, start=start,
+                mask=mask, most=most, scale=192 ** -0.5)
+
+
+def device(p):
+    return dict(q=p["q"].cuda(), kv=p["kv"].cuda(), block_table=i32(p["table"]), cached_lens=i32(p["cached"]),
+                token_start=i32(p["start"]), mask=torch.from_numpy(tree.mask_words(p["mask"], -(-p["most"] // 64))).cuda(),
+                scale=p["scale"])
+
+
+def check(p, got, what=""):
+    """Element by element.  Bounds: the weights' rounding to bf16 (half a step, 2^-8 of each), the
+    scores' fp32 sums of 576 products (at most 2^-18 of sum |q k|, which moves a weight by as much
+    relatively; the same twice for numerator and sum), fp32 sums over the positions and exponentials
+    (2^-20), and the rounding of a bf16 result (2^-8)."""
+    out, lse = (x.double().cpu().numpy() for x in got)
+    w_out, w_lse, wabs, smax = tree.decode_tree(p["q"].double().numpy(), p["kv"].double().numpy(), p["table"], p["cached"],
+                                                p["start"], p["mask"], p["scale"], p["most"])
+    real = ~np.isnan(w_lse)
+    d = 2.0 ** -18 * smax + 2.0 ** -20
+    empty = np.isneginf(w_lse)
+    assert np.array_equal(np.isneginf(lse) & real, empty), what
+    assert np.all(out[empty] == 0), what
+    some = real & ~empty
+    assert np.all(np.abs(lse - w_lse)[some] <= (d + 2.0 ** -22 * np.abs(w_lse))[some]), what
+    tol = (2.0 ** -8 + 2 * d[..., None]) * wabs + (2.0 ** -8 if got[0].dtype == torch.bfloat16 else 2.0 ** -22) * np.abs(w_out)
+    assert np.all(np.abs(out - w_out)[some] <= (tol + 1e-30)[some]), (what, np.nanmax((np.abs(out - w_out) / (tol + 1e-30))[some]))
+    return real
+
+
+def run(p, **kw):
+    """The call with outputs of its own; what belongs to padding tokens has to stay."""
+    d = device(p)
+    T, h, _ = p["q"].shape
+    out = torch.full((T, h, 512), 7.0, device="cuda", dtype=kw.pop("out_dtype", torch.float32))
+    lse = torch.full((T, h), 7.0, device="cuda")
+    got = sfa.decode_tree(**d, out=out, lse=lse, **kw)
+    assert got[0] is out and got[1] is lse
+    assert sfa.last_device_status() == 0
+    real = check(p, got)
+    none = torch.from_numpy(~real[:, 0]).cuda()
+    assert bool((out[none] == 7).all()) and bool((lse[none] == 7).all())
+    return got
+
+
+@pytest.fixture(params=[0, 1], ids=["auto", "cuda_cores"])
+def path(request):
+    old = sfa.set_kernel_path(request.param)
+    yield request.param
+    sfa.set_kernel_path(old)
+
+
+@pytest.mark.parametrize("cached,nodes,h,bs", [
+    ([0], [1], 1, 16), ([1], [1], 3, 16), ([0, 5, 0], [4, 0, 1], 16, 7), ([200], [6], 4, 64),
+    ([127, 128, 129], [1, 2, 3], 16, 64), ([63, 64, 65, 120], [9, 8, 1, 60], 8, 16),
+    ([300, 10, 77], [16, 3, 8], 128, 64), ([256], [64], 27, 128), ([130], [65], 5, 24), ([5, 400], [130, 7], 2, 16),
+    ([900], [256], 1, 64), ([33] * 40, [3] * 40, 16, 16), ([1000, 0, 513], [7, 5, 0], 64, 1), ([640], [5], 72, 4),
+    ([700], [3], 100, 40), ([1500], [2], 32, 8)])
+def test_decode_matches_oracle(path, cached, nodes, h, bs):
+    p = problem(len(cached) + h, cached, nodes, h, bs)
+    run(p)
+    run(p, out_dtype=torch.bfloat16)
+
+
+def test_decode_of_long_sequences(path):
+    run(problem(3, [9000, 4321], [5, 12], 16, 64))
+    run(problem(4, [20011], [2], 3, 16))
+
+
+def test_decode_with_padding_before_and_behind(path):
+    run(problem(5, [40, 9], [6, 2], 16, 16, before=5, behind=9))
+
+
+def test_decode_with_any_mask_and_rows_that_see_nothing(path):
+    rng = np.random.default_rng(6)
+    for c, n, h in ((0, 20, 16), (0, 70, 4), (130, 33, 8), (0, 130, 2), (126, 5, 128)):
+        p = problem(n, [c, 3], [n, 2], h, 16)
+        for t in range(n):
+            p["mask"][t] = sum(1 << j for j in range(n) if rng.random() < 0.5) if t % 3 else 0
+        p["mask"][n - 1] |= 1 << (n + 2)              # a bit behind the last node counts for nothing
+        p["most"] = max(p["most"], n + 3)
+        run(p)
+
+
+def test_decode_of_large_scores_and_other_scales(path):
+    for scale in (4.0, -0.5, 0.0, 1e-3):
+        p = problem(7, [300, 61], [9, 4], 16, 64)
+        p["scale"] = scale
+        run(p)
+
+
+def test_decode_rows_that_a_node_does_not_see_do_not_reach_it(path):
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for c, n, h in ((5, 9, 16), (120, 17, 128), (256, 70, 3)):
+            p = problem(8, [c, 40], [n, 5], h, 16)
+            kv = p["kv"].float()
+            row = lambda pos: (int(p["table"][0, pos // 16]), pos % 16)  # noqa: E731
+            victim = n // 2
+            seen = [t for t in range(n) if p["mask"][t] >> victim & 1]
+            kv[row(c + victim)] = bad
+            for pos in range(c + n, -(-(c + n) // 16) * 16):       # behind the last node
+                kv[row(pos)] = bad
+            p["kv"] = kv.to(torch.bfloat16)
+            d = device(p)
+            out, lse = sfa.decode_tree(**d)
+            assert sfa.last_device_status() == 0
+            o, l = out.cpu(), lse.cpu()
+            assert bool((~torch.isfinite(o[seen])).any(-1).all()), "a node that sees the row has no finite result"
+            clean = dict(p, kv=torch.where(torch.isfinite(kv), kv, torch.zeros(())).to(torch.bfloat16))
+            rest = [t for t in range(n + 5) if t not in seen]
+            ref = sfa.decode_tree(**device(clean))
+            w = tree.decode_tree(clean["q"].double().numpy(), clean["kv"].double().numpy(), p["table"], p["cached"], p["start"],
+                                 p["mask"], p["scale"], p["most"])
+            tol = (2.0 ** -8 + 2.0 ** -16 * (1 + w[3][..., None])) * w[2] + 1e-6
+            assert np.all(np.abs(o.double().numpy() - w[0])[rest] <= tol[rest])
+            assert np.all(np.abs(l.double().numpy() - w[1])[rest] <= 1e-3)
+            assert bool(torch.isfinite(ref[0][:n + 5]).all())
+
+
+def test_decode_of_a_query_that_is_no_number(path):
+    p = problem(9, [100, 20], [5, 3], 16, 16)
+    p["q"][2, 3, 100] = float("nan")
+    p["q"][4, 0, 7] = float("inf")
+    out, lse = sfa.decode_tree(**device(p))
+    assert sfa.last_device_status() == 0
+    bad = torch.zeros((10, 16), dtype=torch.bool)
+    bad[2, 3] = bad[4, 0] = True
+    assert bool(torch.isnan(out[:8].cpu())[bad[:8]].all()) and not bool(torch.isfinite(lse[:8].cpu()[bad[:8]]).any())
+    assert bool(torch.isfinite(out[:8].cpu()[~bad[:8]]).all()) and bool(torch.isfinite(lse[:8].cpu()[~bad[:8]]).all())
+
+
+@pytest.mark.parametrize("bs", [7, 16, 64])
+def test_decode_skips_bad_blocks(path, bs):
+    p = problem(10, [200, 30], [6, 4], 8, bs)
+    p["table"][0, 1], p["table"][1, 0] = -1, p["kv"].shape[0]
+    d = device(p)
+    got = sfa.decode_tree(**d)
+    assert sfa.last_device_status() == BAD_BLOCK
+    check(p, [x.clone() for x in got])
+
+
+def test_decode_gives_the_same_bits_on_every_call(path):
+    p = problem(11, [5000, 700, 3], [16, 1, 30], 32, 64)
+    d = device(p)
+    first = [x[:47].clone() for x in sfa.decode_tree(**d)]
+    for _ in range(5):
+        again = sfa.decode_tree(**d)
+        assert all(torch.equal(x, y[:47]) for x, y in zip(first, again))
+
+
+def test_decode_captured_and_replayed_with_other_lengths(path):
+    sizes = [([300, 20], [8, 3]), ([10, 2000], [1, 7]), ([0, 0], [4, 8])]
+    probs = [problem(20 + i, c, n, 16, 16, most=8, behind=16 - sum(n)) for i, (c, n) in enumerate(sizes)]
+    nb, mb = max(p["kv"].shape[0] for p in probs), max(p["table"].shape[1] for p in probs)
+    buf = dict(q=torch.zeros((16, 16, 576), dtype=torch.bfloat16, device="cuda"),
+               kv=torch.zeros((nb, 16, 576), dtype=torch.bfloat16, device="cuda"), block_table=i32(np.full((2, mb), -1)),
+               cached_lens=i32([0, 0]), token_start=i32([0, 0, 0]), mask=torch.zeros((16, 1), dtype=torch.int64, device="cuda"))
+    ws = torch.full((max(sfa.decode_tree_workspace_bytes(2, 16, 16), 1),), 255, dtype=torch.uint8, device="cuda")
+
+    def fill(p):
+        d = device(p)
+        buf["q"].copy_(d["q"])
+        buf["kv"][:d["kv"].shape[0]].copy_(d["kv"])
+        buf["block_table"][:, :d["block_table"].shape[1]].copy_(d["block_table"])
+        for k in ("cached_lens", "token_start", "mask"):
+            buf[k].copy_(d[k])
+
+    fill(probs[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        sfa.decode_tree(**buf, scale=192 ** -0.5, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = sfa.decode_tree(**buf, scale=192 ** -0.5, workspace=ws)
+    for p in probs + probs[:1]:
+        fill(p)
+        g.replay()
+        torch.cuda.synchronize()
+        check(p, got)
+    assert sfa.last_device_status() == 0
+
+
+def test_decode_on_a_stream_of_its_own(path):
+    p = problem(12, [600], [9], 16, 64)
+    s = torch.cuda.Stream()
+    d = device(p)
+    torch.cuda.synchronize()
+    got = sfa.decode_tree(**d, stream=s)
+    s.synchronize()
+    check(p, got)
+
+
+def test_decode_of_nothing(path):
+    p = problem(13, [5], [2], 4, 16)
+    d = device(p)
+    out = torch.full((4, 4, 512), 3.0, device="cuda")
+    for kw in (dict(token_start=i32([0, 0])), dict(token_start=i32([4, 4])), dict(token_start=i32([3, 1]))):
+        sfa.decode_tree(**dict(d, **kw), out=out)
+        assert sfa.last_device_status() == 0 and bool((out == 3).all())
+    d = dict(d, block_table=i32(np.zeros((0, 3))), cached_lens=i32([]), token_start=i32([0]))
+    sfa.decode_tree(**d, out=out)
+    assert sfa.last_device_status() == 0 and bool((out == 3).all())
+
+
+def test_decode_of_more_nodes_than_the_mask_has_bits(path):
+    p = problem(14, [50], [70], 4, 16)                    # two words a node
+    d = device(p)
+    out = torch.full((72, 4, 512), 3.0, device="cuda")
+    sfa.decode_tree(**dict(d, mask=d["mask"][:, :1].contiguous()), out=out)
+    assert sfa.last_device_status() == BAD_TREE and bool((out[64:] == 3).all())
+    p["most"] = 64
+    w = tree.decode_tree(p["q"].double().numpy(), p["kv"].double().numpy(), p["table"], p["cached"], p["start"], p["mask"],
+                         p["scale"], 64)
+    assert np.nanmax(np.abs(out.double().cpu().numpy() - w[0])[:64]) < 2e-2
+
+
+# ------------------------------------------------------------------------------ together
+def test_steps_of_drafted_trees():
+    """Three steps over one pool: blocks from the step plan, rows by the cache write, attention, path,
+    commit, the rejected nodes' blocks back; against the oracle's state throughout."""
+    rng = np.random.default_rng(30)
+    B, bs, most, h, T, width = 5, 4, 12, 8, 64, 24
+    table, free = np.full((B, width), -1), rng.permutation(120)
+    kv = torch.zeros((120, bs, 576), dtype=torch.bfloat16)
+    cached, taken, shares = np.zeros(B, int), 0, np.zeros(120, int)
+    d = dict(kv=kv.cuda(), table=i32(table), free=i32(free), taken=i32([0]), cached=i32(cached), shares=i32(shares))
+    for step in range(4):
+        nodes = rng.integers(0, most + 1, B)
+        parents = trees(rng, nodes, 0.8)
+        T0 = len(parents)
+        parents += [-1] * (T - T0)
+        tokens, targets = rng.integers(0, 3, T), rng.integers(0, 3, T)
+        rows = torch.randn((T, 576)).to(torch.bfloat16)
+        q = torch.randn((T, h, 576)).to(torch.bfloat16)
+        # the framework
+        table_d, seq, start, _, slots, taken_d = sfa.step_plan(d["cached"], i32(nodes), d["table"], d["free"], d["taken"], bs, T)
+        mask, pos = sfa.tree_plan(i32(parents), start, d["cached"], most)
+        sfa.kv_write(d["kv"], slots, rows.cuda())
+        out, lse = sfa.decode_tree(q.cuda(), d["kv"], table_d, d["cached"], start, mask, 0.07)
+        path, acc, nxt, lens = sfa.tree_accept(i32(tokens), i32(targets), i32(parents), start, d["cached"], most)
+        before = d["kv"].clone()
+        sfa.kv_commit(d["kv"], table_d, d["cached"], path, acc)
+        back = sfa.blocks_free(table_d, seq, lens, d["shares"], d["free"], taken_d, bs)
+        assert sfa.last_device_status() == 0
+        # the oracle
+        from oracle import serving
+        table, seq_o, start_o, _, slots_o, taken_o = serving.step_plan(cached, nodes, table, free, taken, bs, T)
+        assert np.array_equal(table_d.cpu(), table) and int(taken_d) == taken_o
+        m_o, pos_o = tree.tree_plan(parents, start_o, cached, most)
+        assert pos.tolist() == pos_o
+        flat = kv.view(-1, 576)
+        for t, s in enumerate(slots_o):
+            if s >= 0:
+                flat[s] = rows[t]
+        assert torch.equal(before.cpu(), kv)
+        p = dict(q=q, kv=kv, table=table, cached=cached, start=start_o, mask=m_o, scale=0.07, most=most)
+        check(p, (out, lse))
+        p_o, a_o, n_o, l_o = tree.tree_accept(tokens, targets, parents, start_o, cached, most)
+        assert np.array_equal(path.cpu(), p_o) and acc.tolist() == a_o.tolist() and nxt.tolist() == n_o.tolist()
+        kv = torch.from_numpy(tree.kv_commit(kv.float().numpy(), table, cached, p_o, a_o)).to(torch.bfloat16)
+        assert torch.equal(d["kv"].cpu(), kv)
+        shares, free, taken = tree.blocks_free(table, seq_o, l_o, shares, free, taken_o, bs)
+        assert int(back) == taken and np.array_equal(d["free"].cpu(), free) and lens.tolist() == l_o.tolist()
+        cached = l_o
+        d["cached"], d["taken"], d["table"] = lens, back, table_d
