@@ -733,12 +733,14 @@ sfa_status sfa_decode_tree(const void* q, const void* kv, const int32_t* block_t
   const long long wl = g_wait_limit.load();
   p.wait_limit = wl > 0 ? wl : kDefaultWaitLimit;
   p.stall = g_stall.load();
-  return done(sfa::launch_decode_tree_simt(p, static_cast<cudaStream_t>(stream)));
+  // kernel path 1: the CUDA-core kernel, to cross-check; else the tensor cores'
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return done(g_kernel_path.load() == 1 ? sfa::launch_decode_tree_simt(p, s) : sfa::launch_decode_tree(p, s));
 }
 
 size_t sfa_decode_tree_workspace_bytes(int B, int num_tokens, int h) {
-  (void)B; (void)num_tokens; (void)h;
-  return 0;
+  if (B <= 0 || num_tokens <= 0 || h <= 0 || h > SFA_MAX_HEADS) return 0;
+  return sfa::tree_workspace_bytes(num_tokens, h);
 }
 
 sfa_status sfa_blocks_fork(int32_t* block_table, int rows, int max_blocks_per_seq, int32_t* lens, const int32_t* src,

@@ -171,6 +171,11 @@ cudaError_t launch_kv_commit(void* kv, int layers, int num_blocks, int block_siz
                              int max_blocks, const int32_t* cached, const int32_t* path, const int32_t* accepted,
                              int B, int max_nodes, int* status, cudaStream_t stream);
 cudaError_t launch_decode_tree_simt(const TreeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream);   // the tcgen05 kernel
+size_t tree_workspace_bytes(int T, int h);                                  // of the current device
+// rows of 576 bf16 (q's or the cache's), boxes of 64 columns x box_rows rows, 128-byte swizzle;
+// remembered per host thread
+bool make_rows_map(CUtensorMap* m, const void* base, long long num_rows, int box_rows);
 cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t* lens, const int32_t* src,
                                const int32_t* dst, int n, int32_t* shares, int num_blocks, const int32_t* free_blocks,
                                int num_free, const int32_t* taken, int block_size, int32_t* copies, int32_t* taken_out,

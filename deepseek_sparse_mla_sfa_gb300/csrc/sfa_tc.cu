@@ -731,6 +731,14 @@ bool make_row_map(CUtensorMap* m, const void* kv, int num_rows, int box_cols, CU
 
 }  // namespace
 
+bool make_rows_map(CUtensorMap* m, const void* base, long long num_rows, int box_rows) {
+  cuuint64_t dims[2] = {(cuuint64_t)kDQK, (cuuint64_t)num_rows};
+  cuuint64_t strides[1] = {(cuuint64_t)kDQK * 2};
+  cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 bool tc_supports(int h, int block_size) {
   (void)block_size;
   return h >= 1 && h <= kHeads;

@@ -18,9 +18,10 @@ __device__ __forceinline__ int tree_request(const int32_t* token_start, int B, i
   return lo;
 }
 
-constexpr int kTreeSimtHeads = 8, kTreeSimtWarps = 4;
-constexpr int kTreeSimtSmem = 4 * (kTreeSimtHeads * kDQK + kTreeSimtWarps * kTreeSimtHeads * kDV +
-                                   2 * kTreeSimtWarps * kTreeSimtHeads);
+constexpr int kTreeSimtWarps = 4;
+constexpr int tree_simt_smem(int heads) {
+  return 4 * (heads * kDQK + kTreeSimtWarps * heads * kDV + 2 * kTreeSimtWarps * heads);
+}
 
 __device__ __forceinline__ void tree_store(const TreeParams& p, size_t at, float v) {
   if (p.out_bf16)
@@ -29,11 +30,12 @@ __device__ __forceinline__ void tree_store(const TreeParams& p, size_t at, float
     static_cast<float*>(p.out)[at] = v;
 }
 
-// Heads [h0, h0 + 8) of token t, the first 128 threads of the CTA: its warps take the positions by
+// Heads [h0, h0 + kHG) of token t, the first 128 threads of the CTA: its warps take the positions by
 // turns, each with an online softmax (maximum, sum, output) a head, and join at the end.  A position
 // that the token does not attend to is never read.
+template <int kHG>
 __device__ __forceinline__ void tree_simt(const TreeParams& p, int t, int h0, float* smem) {
-  constexpr int kHG = kTreeSimtHeads, kWarps = kTreeSimtWarps, kQK = kDQK / 64, kV = kDV / 64;
+  constexpr int kWarps = kTreeSimtWarps, kQK = kDQK / 64, kV = kDV / 64;
   float* q_s = smem;                                  // [kHG][576]
   float* o_s = q_s + kHG * kDQK;                      // [kWarps][kHG][512]
   float* m_s = o_s + kWarps * kHG * kDV;              // [kWarps][kHG]

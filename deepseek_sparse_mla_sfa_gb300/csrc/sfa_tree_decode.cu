@@ -1,0 +1,879 @@
+// sfa_tree_decode.cu -- tcgen05 / TMA path of the attention of drafted trees on sm_103a.
+//
+// All nodes of a request attend to the same cached rows, so a request's n_b nodes x h heads are the
+// n_b * h rows of one dense attention whose keys and values are the request's c_b + n_b cache rows;
+// only the columns of the nodes themselves carry a mask (a node's ancestors).
+//
+// Work.  A unit is 128 of those query rows (consecutive rows of q) of one request; its keys go by in
+// tiles of 256 positions.  A pair of CTAs takes a tile with two-CTA MMAs (cta_group::2, M = 128): each
+// CTA owns 64 query rows.  Per tile and CTA
+//   S[64 x 256]  = q[64 x 576] K^T: the A operand is the CTA's q in shared memory, the B operand's 256
+//                  keys lie half in either CTA, brought 64 columns at a time;
+//   P = exp2(S - m), bf16, the CTA's own 64 rows, in shared memory;
+//   O[64 x 512] += P V: either CTA holds the 256 value columns that its half of each N = 256 takes, of
+//                  all 256 keys, brought 64 keys x 128 columns at a time.
+// TMEM lanes 0-63 hold the CTA's 64 rows with the first half of an MMA's N, lanes 64-127 the same rows
+// with the second half: O fills 256 columns, two score buffers the other 256.  One CTA's TMEM could not
+// hold 128 rows of O and any scores; with 64 rows a CTA both fit, the softmax of a row stays in its CTA
+// (two threads a row), and the pair reads each key once for 128 rows.  N = 256 in both products since
+// an MMA of M = 128 takes 64 cycles for N = 256 and 66 for N = 128 (measured): tiles of 128 keys take
+// 1.5 times as long a key.
+//
+// Order of the chunks (16 KB a CTA, a ring of 7): K(0), then K(i+1), V(i) by turns (V's first 128
+// columns of each half, then the others), so QK^T of the
+// next tile covers the softmax of this one.  The value columns of the CTA's own keys come twice (as
+// keys and as values); the second time is from L2, which gives 180 GB/s an SM where the ring takes 130.
+//
+// Split.  Units in order of requests, each as long as its tiles (and kUnitCost for its start), are cut
+// into equal ranges, one for each pair; a unit that a cut goes through leaves partial results in the
+// workspace, which the second kernel joins.  A cut never goes through the tiles that hold nodes.
+//
+// Rows that nobody may see.  Positions behind the last node are brought as rows of zeros.  A cached row
+// of NaN or infinities that only some nodes see would reach the others as 0 x NaN in P V: such a row
+// shows as a score that is not finite in a masked place, and so does a block-table entry that names no
+// block to the loading warps.  Both mark the request, and the second kernel computes its nodes on CUDA
+// cores, which reads only what a node attends to.
+//
+// Warps (320 threads): 0-3 softmax, rescaling, output; 4 issues the MMAs (in the pair's first CTA);
+// 5-8 bring keys and values; 9 brings q.  Every wait is bounded; one that gives up records
+// SFA_ERR_DEVICE_TIMEOUT and both CTAs unwind.
+#include <atomic>
+#include <cuda.h>
+#include <string.h>
+
+#include "sfa_ptx.cuh"
+#include "sfa_tree.cuh"
+
+namespace sfa {
+namespace {
+
+using namespace ptx;
+
+constexpr int kThreads = 320, kMmaWarp = 4, kLoadWarp = 5, kLoadWarps = 4;
+constexpr int kRows = 128, kHalf = 64;         // query rows of a unit, of a CTA
+constexpr int kTile = 256;                     // positions of a tile
+constexpr int kKChunks = 9, kVChunks = 8;      // of a tile
+constexpr int kChunk = 16384;
+constexpr int kSlots = 7;
+constexpr int kUnitCost = 1;                   // of starting a unit, in tiles
+constexpr int kMinSpan = 3;                    // tiles a pair gets at least
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kRescaleThreshold = 8.0f;      // log2 units: weights stay below 2^8
+
+// shared memory (offsets from a 1024-byte aligned base)
+constexpr int kQBlk = kHalf * 128;             // 64 rows x 64 columns
+constexpr int kQBytes = 9 * kQBlk;
+constexpr int kOffP = kQBytes;                 // P: four blocks of 64 rows x 64 keys
+constexpr int kPBytes = 4 * kQBlk;
+constexpr int kOffRing = kOffP + kPBytes;
+constexpr int kOffMx = kOffRing + kSlots * kChunk;       // float [2][128]: row maxima, then sums
+constexpr int kOffScan = kOffMx + 1024;                  // long long [kThreads / 32], then int [8]
+constexpr int kOffBar = kOffScan + 8 * 16 + 32;
+constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 1,
+              kBarS = kBarQEmpty + 1, kBarP = kBarS + 2, kBarPv = kBarP + 1, kBarO = kBarPv + 1,
+              kBarMx = kBarO + 1, kBarFin = kBarMx + 2, kBarNever = kBarFin + 1, kNumBars = kBarNever + 1;
+constexpr int kOffMisc = kOffBar + 8 * kNumBars;         // TMEM address, abort, bad range
+constexpr int kSmem = kOffMisc + 64 + 1024;
+static_assert(kSmem <= 232448, "shared memory budget");
+static_assert(kOffRing % 1024 == 0 && kOffBar % 8 == 0, "alignment");
+
+constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;
+constexpr long long kDrainLimit = 1LL << 40;
+
+// what the second kernel needs to know of a pair's partial results
+struct Record {
+  int head_row, head_rows, head_request;   // a unit that begins here and goes on in the next pair: slot 2k + 1
+  int tail_row, tail_ends;                 // a unit that began before: slot 2k; whether it ends here
+  int pad[3];
+};
+
+struct Workspace {
+  float* part;       // [2 * pairs][cap][512]
+  float* lse;        // [2 * pairs][cap]
+  Record* rec;       // [pairs]
+  int2* bad;         // [2 * pairs]: requests to compute again, first and last
+  int cap;           // rows of a slot
+};
+
+struct TreeTcParams {
+  TreeParams p;
+  Workspace ws;
+  int pairs, num_rows, box;   // box: rows of a tiled load (0: rows one by one)
+};
+
+// ---------------------------------------------------------------- cta_group::2 forms
+__device__ __forceinline__ void tmem_alloc2(uint32_t* dst, uint32_t n) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish2() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t a, uint32_t n) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(a), "r"(n) : "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// arrive on this barrier of both CTAs when every MMA issued so far has completed
+__device__ __forceinline__ void commit2(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// loads into this CTA that complete on a barrier of the pair's first CTA
+__device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_rows4(uint32_t dst, const void* map, int x, int r0, int r1, int r2, int r3,
+                                           uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// two floats as bf16, rounded to nearest: a in the low half
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// ---------------------------------------------------------------- the schedule
+struct Request {
+  int first, n, cached, tiles, cuts;   // cuts: tiles without nodes, behind each of which a cut may go
+  long long cost;                      // of all its units
+};
+__device__ __forceinline__ Request request_of(const TreeParams& p, int b) {
+  Request r;
+  r.first = min(max(p.token_start[b], 0), p.T);
+  r.n = min(min(max(p.token_start[b + 1], r.first), p.T) - r.first, p.max_nodes);
+  r.cached = max(p.cached[b], 0);
+  r.tiles = (int)(((long long)r.cached + r.n + kTile - 1) / kTile);
+  r.cuts = r.cached / kTile;
+  r.cost = r.n > 0 ? (long long)((r.n * p.h + kRows - 1) / kRows) * (r.tiles + kUnitCost) : 0;
+  return r;
+}
+
+struct Piece {
+  int row0, rows, k0, k1, tiles;       // query rows; the tiles [k0, k1) of `tiles`
+  int request, cached, n, first, node_row;   // node_row: row0 within the request
+};
+
+// the pieces of one pair's range, in order
+struct Walk {
+  int b;
+  long long off, left;
+  Request r;
+  __device__ __forceinline__ void start(const TreeParams& p, int b0, long long off0, long long n) {
+    b = b0;
+    off = off0;
+    left = n;
+    if (left > 0) r = request_of(p, b);
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p, Piece& x) {
+    while (left > 0) {
+      if (off >= r.cost) {
+        if (++b >= p.B) return false;
+        r = request_of(p, b);
+        off = 0;
+        continue;
+      }
+      const int unit = r.tiles + kUnitCost;
+      const int m = (int)(off / unit), u = (int)(off % unit);
+      const int take = (int)min(left, (long long)(unit - u));
+      off += take;
+      left -= take;
+      auto cut = [&](int v) { return v <= 0 ? 0 : v > r.cuts ? r.tiles : v; };
+      x.k0 = cut(u - kUnitCost);
+      x.k1 = cut(u + take - kUnitCost);
+      if (x.k1 <= x.k0) continue;
+      x.tiles = r.tiles;
+      x.node_row = m * kRows;
+      x.row0 = r.first * p.h + x.node_row;
+      x.rows = min(kRows, r.n * p.h - x.node_row);
+      x.request = b;
+      x.cached = r.cached;
+      x.n = r.n;
+      x.first = r.first;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Shared by the CTA: where its pair's range starts.  Every CTA sums the requests' costs itself.
+__device__ __forceinline__ void find_range(const TreeParams& p, int pair, int pairs, char* smem, int& b0,
+                                           long long& off0, long long& len) {
+  long long* part = reinterpret_cast<long long*>(smem + kOffScan);
+  int* found = reinterpret_cast<int*>(smem + kOffScan + 8 * 16);
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
+  long long mine = 0;
+  for (int b = r0; b < r1; ++b) {
+    mine += request_of(p, b).cost;
+    if (pair == 0 && min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
+      report_status(p.status, kStatusBadTree);
+  }
+  long long in = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, in, o);
+    if (lane >= o) in += u;
+  }
+  if (lane == 31) part[warp] = in;
+  if (tid == 0) found[0] = -1;
+  __syncthreads();
+  long long at = in - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) at += part[w];
+    total += part[w];
+  }
+  const long long span = max((total + pairs - 1) / pairs, (long long)kMinSpan);
+  const long long lo = min(pair * span, total), hi = min(lo + span, total);
+  if (lo < hi && lo >= at && lo < at + mine) {
+    long long a = at;
+    for (int b = r0; b < r1; ++b) {
+      const long long c = request_of(p, b).cost;
+      if (lo < a + c) {
+        found[0] = b;
+        *reinterpret_cast<long long*>(found + 2) = lo - a;
+        break;
+      }
+      a += c;
+    }
+  }
+  __syncthreads();
+  b0 = found[0];
+  off0 = *reinterpret_cast<long long*>(found + 2);
+  len = b0 < 0 ? 0 : hi - lo;
+}
+
+// bits [d, d + 64) of the positions that a node attends to, counted from the first node's: all
+// before it, its mask among the n nodes, none behind
+__device__ __forceinline__ unsigned long long mask_bits(const long long* words, int n_words, int n, int d) {
+  auto word = [&](int i) -> unsigned long long {
+    if (i < 0) return ~0ull;
+    if (i >= n_words || 64 * i >= n) return 0;
+    const unsigned long long w = (unsigned long long)words[i];
+    return n - 64 * i >= 64 ? w : w & ((1ull << (n - 64 * i)) - 1);
+  };
+  const int q = d >> 6, r = d & 63;
+  const unsigned long long lo = word(q);
+  return r == 0 ? lo : lo >> r | word(q + 1) << (64 - r);
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    decode_tree_kernel(const __grid_constant__ CUtensorMap map_box, const __grid_constant__ CUtensorMap map_row,
+                       const __grid_constant__ CUtensorMap map_q, const TreeTcParams tp) {
+  const TreeParams& p = tp.p;
+  extern __shared__ char smem_raw[];
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint32_t* tmem_s = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int* abort_s = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
+  int* bad_s = reinterpret_cast<int*>(smem + kOffMisc + 8);   // first and last request to compute again
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1;
+  const long long wl = p.wait_limit;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(&bars[kBarFull + s], 1);      // (first CTA) armed for both CTAs' bytes
+      mbar_init(&bars[kBarEmpty + s], 1);     // the MMAs that read the slot have completed
+    }
+    mbar_init(&bars[kBarQFull], 1);           // (first CTA) q of both CTAs
+    mbar_init(&bars[kBarQEmpty], 1);          // the piece's last QK^T has completed
+    mbar_init(&bars[kBarS], 1);               // scores of this buffer complete
+    mbar_init(&bars[kBarS + 1], 1);
+    mbar_init(&bars[kBarP], 8);               // (first CTA) both CTAs' softmax warps: P written, O rescaled
+    mbar_init(&bars[kBarPv], 1);              // P V of a tile has completed
+    mbar_init(&bars[kBarO], 8);               // (first CTA) the softmax warps have read O
+    mbar_init(&bars[kBarMx], 2);              // the two warps of a row have left their values
+    mbar_init(&bars[kBarMx + 1], 2);
+    mbar_init(&bars[kBarFin], 1);
+    mbar_init(&bars[kBarNever], 1);           // nothing arrives: the stall test hook waits on it
+    *abort_s = 0;
+    bad_s[0] = 0x7fffffff;
+    bad_s[1] = -1;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc2(tmem_s, kTmemCols);
+    tmem_relinquish2();
+  }
+  if (warp == kLoadWarp && lane == 0) {
+    prefetch_tmap(&map_box);
+    prefetch_tmap(&map_row);
+    prefetch_tmap(&map_q);
+  }
+  int b0;
+  long long off0, len;
+  find_range(p, pair, tp.pairs, smem, b0, off0, len);
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_s;
+  Walk walk;
+  walk.start(p, b0, off0, len);
+  Piece x;
+
+  auto fail = [&] {
+    report_status(p.status, kStatusTimeout);
+    *abort_s = 1;
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa((const void*)abort_s, rank ^ 1u)), "r"(1) : "memory");
+  };
+  auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, wl));
+  };
+  auto aborted = [&] { return __any_sync(0xffffffffu, *abort_s) != 0; };
+  auto mark_bad = [&](int request) {
+    atomicMin(&bad_s[0], request);
+    atomicMax(&bad_s[1], request);
+  };
+
+  if (warp < 4) {
+    // =================== softmax, rescaling, output =================================
+    const int tid = threadIdx.x, r = tid & 63, half = tid >> 6;   // row of the CTA, half of the tile's keys
+    const int row = kHalf * (int)rank + r;                        // of the unit
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t p_ready = mapa(&bars[kBarP], 0), o_read = mapa(&bars[kBarO], 0);
+    float* mx = reinterpret_cast<float*>(smem + kOffMx);
+    const float c_scale = p.scale * kLog2e;
+    // masked scores are -inf, and -inf times a zero scale would be NaN: any valid score times 1e-30
+    // still has weight 1
+    const float c_abs = fmaxf(fabsf(c_scale), 1e-30f);
+    Record* rec = tp.ws.rec + pair;
+    if (tid == 0 && rank == 0) rec->head_row = rec->tail_row = -1;
+    int g = 0, swaps = 0;
+    bool ok = true;
+    // the value of the thread with the row's other half
+    auto other = [&](float v) {
+      float* at = mx + 128 * (swaps & 1);
+      at[tid] = v;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars[kBarMx + (warp & 1)]);
+      ok = ok && wait_warp(&bars[kBarMx + (warp & 1)], swaps & 1);
+      ++swaps;
+      return at[tid ^ 64];
+    };
+    while (ok && walk.next(p, x)) {
+      float m_ref = -INFINITY, l_sum = 0.f;
+      const bool live = row < x.rows;
+      const int node = live ? (x.node_row + row) / p.h : 0;
+      const long long* words = p.mask + (size_t)(x.first + node) * p.words;
+      for (int k = x.k0; k < x.k1; ++k, ++g) {
+        const int bb = g & 1;
+        if (!(ok = !aborted() && wait_warp(&bars[kBarS + bb], (g >> 1) & 1))) break;
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(lanes + kColS + 128 * bb + 32 * i, v[i]);
+        tmem_ld_wait();
+        float s[128];
+#pragma unroll
+        for (int j = 0; j < 128; ++j) s[j] = __uint_as_float(v[j >> 5][j & 31]);
+        if (c_scale < 0.f) {
+#pragma unroll
+          for (int j = 0; j < 128; ++j) s[j] = -s[j];
+        }
+        if (k >= x.cached / kTile) {           // a tile with nodes, or with the end
+          const int d = (int)((long long)k * kTile + 128 * half - x.cached);
+          unsigned long long see[2] = {~0ull, ~0ull};
+          if (live) {
+            see[0] = mask_bits(words, p.words, x.n, d);
+            see[1] = mask_bits(words, p.words, x.n, d + 64);
+          }
+          bool bad = false;
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (!(see[j >> 6] >> (j & 63) & 1)) {
+              bad |= !(fabsf(s[j]) <= 3.0e38f);   // (rows behind the end are zeros)
+              s[j] = -INFINITY;
+            }
+          if (bad) mark_bad(x.request);
+        }
+        float t[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) t[j] = s[j];
+#pragma unroll
+        for (int j = 16; j < 128; ++j) t[j & 15] = fmaxf(t[j & 15], s[j]);
+#pragma unroll
+        for (int w = 8; w > 0; w >>= 1)
+#pragma unroll
+          for (int j = 0; j < w; ++j) t[j] = fmaxf(t[j], t[j + w]);
+        const float mt = fmaxf(t[0], other(t[0])) * c_abs;
+        if (!ok) break;
+        float m_new = m_ref;
+        if (mt > m_ref + kRescaleThreshold || m_ref == -INFINITY) m_new = fmaxf(mt, m_ref);
+        const float base = m_new == -INFINITY ? 0.f : m_new;
+        const float alpha = m_ref == m_new ? 1.f : ex2(m_ref - base);
+        const bool first = k == x.k0;
+        m_ref = m_new;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[64];
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          const float e0 = ex2(fmaf(s[2 * j], c_abs, -base)), e1 = ex2(fmaf(s[2 * j + 1], c_abs, -base));
+          sum[j & 3] += e0 + e1;
+          pk[j] = pack_bf16(e0, e1);
+        }
+        l_sum = l_sum * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        // P's place and O are free once P V of the tile before has completed
+        if (g > 0) {
+          if (!(ok = wait_warp(&bars[kBarPv], (g - 1) & 1))) break;
+          tc_fence_after();
+        }
+        char* pb = smem + kOffP + 2 * half * kQBlk + r * 128;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          *reinterpret_cast<uint4*>(pb + (j >> 3) * kQBlk + (((j & 7) ^ (r & 7)) * 16)) =
+              make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        fence_proxy_async_smem();
+        if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < 256; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(lanes + kColO + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tmem_st16(lanes + kColO + c, *reinterpret_cast<const uint32_t(*)[16]>(&o[0]));
+            tmem_st16(lanes + kColO + c + 16, *reinterpret_cast<const uint32_t(*)[16]>(&o[16]));
+          }
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(p_ready);
+      }
+      if (!ok) break;
+      // ---- the piece's result
+      const float l = l_sum + other(l_sum);
+      if (!ok || !(ok = wait_warp(&bars[kBarPv], (g - 1) & 1))) break;
+      tc_fence_after();
+      const bool none = l == 0.f;
+      const float inv = none ? 0.f : 1.f / l;
+      const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
+      const bool whole = x.k0 == 0 && x.k1 == x.tiles, head = x.k0 == 0;
+      const int slot = 2 * pair + (head ? 1 : 0);
+      float* part = whole ? static_cast<float*>(p.out) + (size_t)(x.row0 + row) * kDV
+                          : tp.ws.part + ((size_t)slot * tp.ws.cap + row) * kDV;
+      __nv_bfloat16* out16 = static_cast<__nv_bfloat16*>(p.out) + (size_t)(x.row0 + row) * kDV;
+      const bool as16 = whole && p.out_bf16;
+#pragma unroll 1
+      for (int c = 0; c < 256; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(lanes + kColO + c, o);
+        tmem_ld_wait();
+        const int at = 256 * half + c;
+        if (live && as16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = pack_bf16(__uint_as_float(o[8 * j + 2 * u]) * inv, __uint_as_float(o[8 * j + 2 * u + 1]) * inv);
+            *reinterpret_cast<uint4*>(out16 + at + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        } else if (live) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4*>(part + at + 4 * j) =
+                make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
+                            __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
+        }
+        __syncwarp();
+      }
+      if (live && half == 0) {
+        if (whole) p.lse[x.row0 + row] = lse;
+        else tp.ws.lse[(size_t)slot * tp.ws.cap + row] = lse;
+      }
+      if (tid == 0 && rank == 0 && !whole) {
+        if (head) {
+          rec->head_rows = x.rows;
+          rec->head_request = x.request;
+          rec->head_row = x.row0;
+        } else {
+          rec->tail_ends = x.k1 == x.tiles;
+          rec->tail_row = x.row0;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_remote(o_read);
+    }
+    if (!ok) fail();
+  } else if (warp == kMmaWarp) {
+    // =================== MMAs =========================================================
+    if (rank == 0 && lane == 0 && len > 0) {
+      const uint32_t id_qk = idesc_bf16(128, 256, 0, 0), id_pv = idesc_bf16(128, 256, 0, 1);
+      const uint64_t dq = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128);
+      const uint64_t dp = smem_desc(smem_u32(smem + kOffP), 16, 1024, kSwizzle128);
+      const uint64_t dk = smem_desc(smem_u32(smem + kOffRing), 16, 1024, kSwizzle128);
+      const uint64_t dv = smem_desc(smem_u32(smem + kOffRing), 8192, 1024, kSwizzle128);
+      int slot = 0, round = 0, g = 0, pieces = 0;
+      // test hook: a wait that cannot complete, so the wait limit runs out
+      bool ok = !p.stall || mbar_wait(&bars[kBarNever], 0, wl);
+      auto full = [&]() -> bool {
+        ok = ok && !*abort_s && mbar_wait<true>(&bars[kBarFull + slot], round & 1, wl);
+        tc_fence_after();
+        return ok;
+      };
+      auto release = [&] {
+        commit2(&bars[kBarEmpty + slot]);
+        if (++slot == kSlots) {
+          slot = 0;
+          ++round;
+        }
+      };
+      auto qk = [&](int tile, bool last) {     // scores of the tile-th tile of all
+        const uint32_t d = tmem + kColS + 128 * (tile & 1);
+        uint64_t a = dq;
+#pragma unroll 1
+        for (int j = 0; j < kKChunks; ++j, a += kQBlk >> 4) {
+          if (!full()) return;
+          const uint64_t b = dk + (uint64_t)(slot * (kChunk >> 4));
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mma2(d, a + 2 * u, b + 2 * u, id_qk, j > 0 || u > 0);
+          release();
+        }
+        commit2(&bars[kBarS + (tile & 1)]);
+        if (last) commit2(&bars[kBarQEmpty]);
+      };
+      while (ok && walk.next(p, x)) {
+        if (!(ok = mbar_wait<true>(&bars[kBarQFull], pieces & 1, wl))) break;
+        tc_fence_after();
+        qk(g, x.k0 + 1 == x.k1);
+        for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
+          if (k + 1 < x.k1) qk(g + 1, k + 2 == x.k1);
+          if (!ok || !(ok = mbar_wait<true>(&bars[kBarP], g & 1, wl))) break;
+          if (k == x.k0 && pieces > 0 && !(ok = mbar_wait<true>(&bars[kBarO], (pieces - 1) & 1, wl))) break;
+          tc_fence_after();
+          uint64_t a = dp;
+#pragma unroll 1
+          for (int j = 0; j < kVChunks; ++j) {
+            if (!full()) break;
+            const uint64_t b = dv + (uint64_t)(slot * (kChunk >> 4));
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              mma2(tmem + kColO + 128 * (j >> 2), a + 2 * u, b + 128 * u, id_pv, k > x.k0 || (j & 3) > 0 || u > 0);
+            release();
+            a = (j & 3) == 3 ? dp : a + (kQBlk >> 4);
+          }
+          commit2(&bars[kBarPv]);
+        }
+        ++pieces;
+      }
+      // the second CTA's last arrivals here: no one else waits for them
+      if (ok && pieces > 0) ok = mbar_wait<true>(&bars[kBarO], (pieces - 1) & 1, wl);
+      if (!ok) fail();
+      commit2(&bars[kBarFin]);
+    }
+    // Every MMA has completed, and every arrival that commits send to either CTA has landed, before
+    // TMEM and shared memory go away: an arrival at a CTA that has ended is a fault.
+    if (lane == 0 && len > 0 && !mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit))
+      report_status(p.status, kStatusTimeout);
+  } else if (warp < kLoadWarp + kLoadWarps) {
+    // =================== keys and values ============================================
+    // Warp w brings the key chunks j with j % 4 == w (64 columns of the CTA's 128 keys) and the value
+    // chunks w and 4 + w (128 columns of the tile's w-th 64 keys); a lane brings a box of `box` rows,
+    // whose places it looks up a tile ahead.
+    // A wait for a slot's round r is by parity, so it takes round r - 2 for done where that is all that is:
+    // a warp's chunks lie at most 5 places apart, and the wait for one of them says that every chunk up to
+    // kSlots places before it has been read, so the next one's slot is at most one round behind.
+    static_assert(kSlots >= 5, "the distance of a warp's chunks");
+    const int w = warp - kLoadWarp;
+    const int box = tp.box ? tp.box : 4;
+    const int boxes = 128 / box, per_v = 64 / box;
+    const bool mine = lane < boxes;
+    const int v_cb = lane / per_v, v_at = (lane % per_v) * box;
+    const uint32_t full0 = mapa(&bars[kBarFull], 0);
+    bool ok = true, bad = false;
+    int slot_at = 0, round = 0;                // of the next chunk in order
+    struct Place { int r[4]; int n; };         // rows of a box, and how many of them exist
+    const int32_t* table = nullptr;
+    long long end = 0;
+    auto look = [&](long long pos) {
+      Place q;
+      q.n = mine ? (int)min(max(end - pos, 0ll), (long long)box) : 0;
+      q.r[0] = q.r[1] = q.r[2] = q.r[3] = tp.num_rows;
+      if (tp.box) {
+        if (q.n > 0) {
+          const int blk = (int)((uint32_t)pos / (uint32_t)p.block_size);   // (below 2^31 + 256)
+          const int phys = blk < p.max_blocks ? table[blk] : -1;
+          if (phys < 0 || phys >= p.num_blocks) {
+            bad = true;
+            q.n = 0;
+          } else {
+            q.r[0] = phys * p.block_size + (int)((uint32_t)pos - (uint32_t)blk * (uint32_t)p.block_size);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (u < q.n) {
+            const int blk = (int)((uint32_t)(pos + u) / (uint32_t)p.block_size);
+            const int phys = blk < p.max_blocks ? table[blk] : -1;
+            if (phys < 0 || phys >= p.num_blocks) bad = true;
+            else q.r[u] = phys * p.block_size + (int)((uint32_t)(pos + u) - (uint32_t)blk * (uint32_t)p.block_size);
+          }
+      }
+      return q;
+    };
+    auto bring = [&](uint32_t dst, int col, const Place& q, uint32_t bar) {
+      if (!tp.box) {
+        if (mine) load_rows4(dst, &map_row, col, q.r[0], q.r[1], q.r[2], q.r[3], bar);
+        return;
+      }
+      const bool cut = q.n != box && q.n != 0;   // the sequence ends in it: rows behind the end are zeros
+      if (mine && !cut) load_box(dst, &map_box, col, q.n ? q.r[0] : tp.num_rows, bar);
+      if (__any_sync(0xffffffffu, cut)) {
+        for (int i = 0; i < box; i += 4) {
+          auto at = [&](int u) { return i + u < q.n ? q.r[0] + i + u : tp.num_rows; };
+          if (cut) load_rows4(dst + i * 128, &map_row, col, at(0), at(1), at(2), at(3), bar);
+          __syncwarp();
+        }
+      }
+    };
+    // the chunk `ahead` places on in the order: its slot, once that is free; false: gave up
+    auto take = [&](int ahead, int& slot) -> bool {
+      int rd = round;
+      slot = slot_at + ahead;
+      while (slot >= kSlots) {
+        slot -= kSlots;
+        ++rd;
+      }
+      if (aborted()) return false;
+      if (rd > 0 && !wait_warp(&bars[kBarEmpty + slot], (rd - 1) & 1)) return false;
+      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bars[kBarFull + slot], 2 * kChunk);
+      __syncwarp();
+      return true;
+    };
+    auto pass = [&](int chunks) {
+      slot_at += chunks;
+      while (slot_at >= kSlots) {
+        slot_at -= kSlots;
+        ++round;
+      }
+    };
+    auto keys = [&](const Place& q) {
+      for (int j = w; ok && j < kKChunks; j += kLoadWarps) {
+        int slot;
+        if (!(ok = take(j, slot))) break;
+        bring(smem_u32(smem + kOffRing + slot * kChunk + lane * box * 128), 64 * j, q, full0 + 8 * slot);
+      }
+      pass(kKChunks);
+    };
+    auto values = [&](const Place& q) {
+      for (int h = 0; ok && h < 2; ++h) {
+        int slot;
+        if (!(ok = take(4 * h + w, slot))) break;
+        bring(smem_u32(smem + kOffRing + slot * kChunk + v_cb * 8192 + v_at * 128),
+              256 * (int)rank + 128 * h + 64 * v_cb, q, full0 + 8 * slot);
+      }
+      pass(kVChunks);
+    };
+    while (ok && walk.next(p, x)) {
+      table = p.block_table + (size_t)x.request * p.max_blocks;
+      end = (long long)x.cached + x.n;
+      const long long k_off = 128 * (int)rank + lane * box, v_off = 64 * w + v_at;
+      Place kq = look((long long)x.k0 * kTile + k_off), vq = look((long long)x.k0 * kTile + v_off);
+      keys(kq);
+      kq = look((long long)(x.k0 + 1) * kTile + k_off);
+      for (int k = x.k0; ok && k < x.k1; ++k) {
+        if (k + 1 < x.k1) {
+          keys(kq);
+          kq = look((long long)(k + 2) * kTile + k_off);
+        }
+        const Place vn = look((long long)(k + 1) * kTile + v_off);
+        values(vq);
+        vq = vn;
+      }
+      if (bad) {                               // (also from a look past the piece: the request's all the same)
+        mark_bad(x.request);
+        report_status(p.status, kStatusBadBlock);
+        bad = false;
+      }
+    }
+    if (!ok) fail();
+  } else {
+    // =================== q ==============================================================
+    if (lane == 0) {
+      bool ok = true;
+      const uint32_t qfull = mapa(&bars[kBarQFull], 0);
+      for (int i = 0; ok && walk.next(p, x); ++i) {
+        if (*abort_s) break;
+        if (i > 0 && !(ok = mbar_wait<true>(&bars[kBarQEmpty], (i - 1) & 1, wl))) break;
+        if (rank == 0) mbar_arrive_expect_tx(&bars[kBarQFull], 2 * kQBytes);
+        for (int j = 0; j < 9; ++j)
+          load_box(smem_u32(smem + j * kQBlk), &map_q, 64 * j, x.row0 + kHalf * (int)rank, qfull);
+      }
+      if (!ok) fail();
+    }
+  }
+
+  // ---- teardown
+  __syncwarp();
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    tp.ws.bad[blockIdx.x] = make_int2(bad_s[0], bad_s[1]);
+    if (*abort_s) {
+      // loads of either CTA may be in flight: they land within microseconds
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = 0; i < (1 << 20) && globaltimer_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
+    }
+  }
+  __syncthreads();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc2(tmem, kTmemCols);
+}
+
+// ---------------------------------------------------------------- joining, and the marked requests
+constexpr int kJoinThreads = 128, kJoinRows = 64;   // row chunks of a unit: blocks in y
+constexpr int kFixHeads = 2;
+
+__global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcParams tp) {
+  extern __shared__ float smem_f[];
+  const TreeParams& p = tp.p;
+  const int k = blockIdx.x, y = blockIdx.y, tid = threadIdx.x;
+  int any = 0, skip = 0;
+  const Record rec = tp.ws.rec[k];
+  for (int i = tid; i < 2 * tp.pairs; i += kJoinThreads) {
+    const int2 b = tp.ws.bad[i];
+    if (b.x <= b.y) {
+      any = 1;
+      if (rec.head_row >= 0 && b.x <= rec.head_request && rec.head_request <= b.y) skip = 1;
+    }
+  }
+  any = __syncthreads_or(any);
+  if (any) skip = __syncthreads_or(skip);
+  if (rec.head_row >= 0 && !skip && rec.head_rows <= tp.ws.cap) {
+    int last = k;                              // the unit's pieces: slot 2k + 1, then 2j for k < j <= last
+    while (last + 1 < tp.pairs && tp.ws.rec[last + 1].tail_row == rec.head_row) {
+      ++last;
+      if (tp.ws.rec[last].tail_ends) break;
+    }
+    const size_t cap = tp.ws.cap;
+    for (int r = y; r < rec.head_rows; r += gridDim.y) {
+      const float* lse = tp.ws.lse + r;
+      auto slot = [&](int j) { return (size_t)(j == k ? 2 * k + 1 : 2 * j); };
+      float m = -INFINITY;
+      for (int j = k; j <= last; ++j) m = fmaxf(m, lse[slot(j) * cap]);
+      float sum = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int j = k; j <= last; ++j) {
+        const float l = lse[slot(j) * cap];
+        const float e = l == -INFINITY ? 0.f : __expf(l - m);   // NaN goes on
+        const float4 v = *reinterpret_cast<const float4*>(tp.ws.part + (slot(j) * cap + r) * kDV + 4 * tid);
+        sum += e;
+        o.x += e * v.x; o.y += e * v.y; o.z += e * v.z; o.w += e * v.w;
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t row = (size_t)rec.head_row + r;
+      if (p.out_bf16) {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kDV + 4 * tid) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+      } else {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kDV + 4 * tid) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      }
+      if (tid == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
+    }
+  }
+  if (!any) return;
+  // rare: the nodes of every marked request, a node and two heads at a time
+  const int groups = (p.h + kFixHeads - 1) / kFixHeads;
+  const int me = blockIdx.y * gridDim.x + blockIdx.x, all = gridDim.x * gridDim.y;
+  for (int i = 0; i < 2 * tp.pairs; ++i) {
+    const int2 range = tp.ws.bad[i];
+    for (int b = max(range.x, 0); b <= min(range.y, p.B - 1); ++b) {
+      const Request r = request_of(p, b);
+      for (int it = me; it < r.n * groups; it += all)
+        tree_simt<kFixHeads>(p, r.first + it / groups, it % groups * kFixHeads, smem_f);
+    }
+  }
+}
+
+size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+
+int pairs_of_device() { return device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1; }
+
+// places of the workspace's parts; returns its size
+size_t lay_out(char* base, int pairs, int cap, Workspace& ws) {
+  size_t at = 0;
+  auto part = [&](size_t bytes) {
+    char* q = base + at;
+    at += round256(bytes);
+    return q;
+  };
+  ws.cap = cap;
+  ws.part = reinterpret_cast<float*>(part((size_t)2 * pairs * cap * kDV * 4));
+  ws.lse = reinterpret_cast<float*>(part((size_t)2 * pairs * cap * 4));
+  ws.rec = reinterpret_cast<Record*>(part((size_t)pairs * sizeof(Record)));
+  ws.bad = reinterpret_cast<int2*>(part((size_t)2 * pairs * sizeof(int2)));
+  return at;
+}
+
+int rows_of_slot(long long rows) { return rows < kRows ? (int)rows : kRows; }
+
+}  // namespace
+
+size_t tree_workspace_bytes(int T, int h) {
+  Workspace ws;
+  return lay_out(nullptr, pairs_of_device(), rows_of_slot((long long)T * h), ws);
+}
+
+cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
+  if (p.T == 0 || p.B == 0) return cudaSuccess;
+  static std::atomic<bool> attr_set[64];   // per device: set once (a repeat is harmless)
+  constexpr int kFixSmem = tree_simt_smem(kFixHeads);
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+    cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
+  }
+  TreeTcParams tp;
+  tp.p = p;
+  tp.pairs = pairs_of_device();
+  tp.num_rows = p.num_blocks * p.block_size;
+  // rows of a box: the largest power of two up to 64 that divides the block size, from 8 on
+  tp.box = 64;
+  while (p.block_size % tp.box != 0) tp.box /= 2;
+  if (tp.box < 8) tp.box = 0;
+  lay_out(static_cast<char*>(p.workspace), tp.pairs, rows_of_slot((long long)p.T * p.h), tp.ws);
+  CUtensorMap box, row, q;
+  if (!make_rows_map(&box, p.kv, tp.num_rows, tp.box ? tp.box : 8) || !make_rows_map(&row, p.kv, tp.num_rows, 1) ||
+      !make_rows_map(&q, p.q, (long long)p.T * p.h, kHalf))
+    return cudaErrorInvalidValue;
+  decode_tree_kernel<<<2 * tp.pairs, kThreads, kSmem, stream>>>(box, row, q, tp);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  join_tree_kernel<<<dim3(tp.pairs, kJoinRows), kJoinThreads, kFixSmem, stream>>>(tp);
+  return cudaGetLastError();
+}
+
+}  // namespace sfa

@@ -8,9 +8,11 @@
 namespace sfa {
 namespace {
 
+constexpr int kHeads = 8;   // of a CTA
+
 __global__ void __launch_bounds__(kTreeSimtWarps * 32) decode_tree_simt_kernel(const TreeParams p) {
   extern __shared__ float smem[];
-  tree_simt(p, blockIdx.x, blockIdx.y * kTreeSimtHeads, smem);
+  tree_simt<kHeads>(p, blockIdx.x, blockIdx.y * kHeads, smem);
 }
 
 }  // namespace
@@ -22,12 +24,12 @@ cudaError_t launch_decode_tree_simt(const TreeParams& p, cudaStream_t stream) {
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(decode_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTreeSimtSmem);
+        cudaFuncSetAttribute(decode_tree_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tree_simt_smem(kHeads));
     if (e != cudaSuccess) return e;
     if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
   }
-  const dim3 grid(p.T, (p.h + kTreeSimtHeads - 1) / kTreeSimtHeads);
-  decode_tree_simt_kernel<<<grid, kTreeSimtWarps * 32, kTreeSimtSmem, stream>>>(p);
+  const dim3 grid(p.T, (p.h + kHeads - 1) / kHeads);
+  decode_tree_simt_kernel<<<grid, kTreeSimtWarps * 32, tree_simt_smem(kHeads), stream>>>(p);
   return cudaGetLastError();
 }
 
