@@ -30,8 +30,8 @@
 //
 // Rows that nobody may see.  Positions behind the last node are brought as rows of zeros.  A cached row
 // of NaN or infinities that only some nodes see would reach the others as 0 x NaN in P V: such a row
-// shows as a score that is not finite in a masked place, and so does a block-table entry that names no
-// block to the loading warps.  Both mark the request, and the second kernel computes its nodes on CUDA
+// shows as a score that is not finite in a masked place; the loading warps see a position that a node
+// attends to and that has no block.  Both mark the request, and the second kernel computes its nodes on CUDA
 // cores, which reads only what a node attends to.
 //
 // Warps (320 threads): 0-3 softmax, rescaling, output; 4 issues the MMAs (in the pair's first CTA);
@@ -613,6 +613,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     struct Place { int r[4]; int n; };         // rows of a box, and how many of them exist
     const int32_t* table = nullptr;
     long long end = 0;
+    // no block for the positions [pos, pos + n): that matters where a node attends to one of them
+    auto missed = [&](long long pos, int n) {
+      for (int u = 0; u < n && !bad; ++u) {
+        const long long j = pos + u - x.cached;
+        if (j < 0) bad = true;
+        for (int i = 0; i < x.n && j >= 0 && !bad; ++i)
+          bad = p.mask[(size_t)(x.first + i) * p.words + j / 64] >> (j % 64) & 1;
+      }
+    };
     auto look = [&](long long pos) {
       Place q;
       q.n = mine ? (int)min(max(end - pos, 0ll), (long long)box) : 0;
@@ -622,7 +631,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int blk = (int)((uint32_t)pos / (uint32_t)p.block_size);   // (below 2^31 + 256)
           const int phys = blk < p.max_blocks ? table[blk] : -1;
           if (phys < 0 || phys >= p.num_blocks) {
-            bad = true;
+            missed(pos, q.n);
             q.n = 0;
           } else {
             q.r[0] = phys * p.block_size + (int)((uint32_t)pos - (uint32_t)blk * (uint32_t)p.block_size);
@@ -634,7 +643,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (u < q.n) {
             const int blk = (int)((uint32_t)(pos + u) / (uint32_t)p.block_size);
             const int phys = blk < p.max_blocks ? table[blk] : -1;
-            if (phys < 0 || phys >= p.num_blocks) bad = true;
+            if (phys < 0 || phys >= p.num_blocks) missed(pos + u, 1);
             else q.r[u] = phys * p.block_size + (int)((uint32_t)(pos + u) - (uint32_t)blk * (uint32_t)p.block_size);
           }
       }
@@ -711,7 +720,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (bad) {                               // (also from a look past the piece: the request's all the same)
         mark_bad(x.request);
-        report_status(p.status, kStatusBadBlock);
         bad = false;
       }
     }
