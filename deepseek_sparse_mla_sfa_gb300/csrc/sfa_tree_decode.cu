@@ -9,17 +9,18 @@
 // CTA owns 64 query rows.  Per tile and CTA
 //   S[64 x 256]  = q[64 x 576] K^T: the A operand is the CTA's q in shared memory, the B operand's 256
 //                  keys lie half in either CTA, brought 64 columns at a time;
-//   P = exp2(S - m), bf16, the CTA's own 64 rows, in shared memory;
+//   P = exp2(S - m), the CTA's own 64 rows, in shared memory, in one bf16 term, or in two (the value and
+//                  what its rounding left) where the result is fp32;
 //   O[64 x 512] += P V: either CTA holds the 256 value columns that its half of each N = 256 takes, of
 //                  all 256 keys, brought 64 keys x 128 columns at a time.
 // TMEM lanes 0-63 hold the CTA's 64 rows with the first half of an MMA's N, lanes 64-127 the same rows
 // with the second half: O fills 256 columns, two score buffers the other 256.  One CTA's TMEM could not
 // hold 128 rows of O and any scores; with 64 rows a CTA both fit, the softmax of a row stays in its CTA
-// (two threads a row), and the pair reads each key once for 128 rows.  N = 256 in both products since
+// (four threads a row), and the pair reads each key once for 128 rows.  N = 256 in both products since
 // an MMA of M = 128 takes 64 cycles for N = 256 and 66 for N = 128 (measured): tiles of 128 keys take
 // 1.5 times as long a key.
 //
-// Order of the chunks (16 KB a CTA, a ring of 7): K(0), then K(i+1), V(i) by turns (V's first 128
+// Order of the chunks (16 KB a CTA, a ring of 7, or of 5 beside two terms): K(0), then K(i+1), V(i) by turns (V's first 128
 // columns of each half, then the others), so QK^T of the
 // next tile covers the softmax of this one.  The value columns of the CTA's own keys come twice (as
 // keys and as values); the second time is from L2, which gives 180 GB/s an SM where the ring takes 130.
@@ -34,8 +35,8 @@
 // attends to and that has no block.  Both mark the request, and the second kernel computes its nodes on CUDA
 // cores, which reads only what a node attends to.
 //
-// Warps (320 threads): 0-3 softmax, rescaling, output; 4 issues the MMAs (in the pair's first CTA);
-// 5-8 bring keys and values; 9 brings q.  Every wait is bounded; one that gives up records
+// Warps (448 threads): 0-7 softmax, rescaling, output; 8 issues the MMAs (in the pair's first CTA);
+// 9-12 bring keys and values; 13 brings q.  Every wait is bounded; one that gives up records
 // SFA_ERR_DEVICE_TIMEOUT and both CTAs unwind.
 #include <atomic>
 #include <cuda.h>
@@ -49,34 +50,38 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kThreads = 320, kMmaWarp = 4, kLoadWarp = 5, kLoadWarps = 4;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 4, kThreads = 14 * 32;
 constexpr int kRows = 128, kHalf = 64;         // query rows of a unit, of a CTA
 constexpr int kTile = 256;                     // positions of a tile
 constexpr int kKChunks = 9, kVChunks = 8;      // of a tile
 constexpr int kChunk = 16384;
-constexpr int kSlots = 7;
 constexpr int kUnitCost = 1;                   // of starting a unit, in tiles
 constexpr int kMinSpan = 3;                    // tiles a pair gets at least
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;      // log2 units: weights stay below 2^8
 
-// shared memory (offsets from a 1024-byte aligned base)
+// shared memory (offsets from a 1024-byte aligned base): q, P (one bf16 term of the weights or two), the ring
 constexpr int kQBlk = kHalf * 128;             // 64 rows x 64 columns
 constexpr int kQBytes = 9 * kQBlk;
-constexpr int kOffP = kQBytes;                 // P: four blocks of 64 rows x 64 keys
+constexpr int kOffP = kQBytes;                 // P: four blocks of 64 rows x 64 keys a term
 constexpr int kPBytes = 4 * kQBlk;
-constexpr int kOffRing = kOffP + kPBytes;
-constexpr int kOffMx = kOffRing + kSlots * kChunk;       // float [2][128]: row maxima, then sums
-constexpr int kOffScan = kOffMx + 1024;                  // long long [kThreads / 32], then int [8]
+template <bool kTwo>
+struct Ring {
+  static constexpr int kSlots = kTwo ? 5 : 7;
+  static constexpr int kOff = kOffP + (kTwo ? 2 : 1) * kPBytes;
+  static_assert(kOff % 1024 == 0 && kOff + kSlots * kChunk == kOffP + kPBytes + 7 * kChunk, "the ring fills the rest");
+};
+constexpr int kOffMx = kOffP + kPBytes + 7 * kChunk;     // float [2][256]: row maxima, then sums
+constexpr int kOffScan = kOffMx + 2048;                  // long long [kThreads / 32], then int [8]
 constexpr int kOffBar = kOffScan + 8 * 16 + 32;
-constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 1,
+constexpr int kBarFull = 0, kBarEmpty = 7, kBarQFull = 14, kBarQEmpty = kBarQFull + 1,
               kBarS = kBarQEmpty + 1, kBarP = kBarS + 2, kBarPv = kBarP + 1, kBarO = kBarPv + 1,
               kBarMx = kBarO + 1, kBarFin = kBarMx + 2, kBarNever = kBarFin + 1, kNumBars = kBarNever + 1;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;         // TMEM address, abort, bad range
 constexpr int kSmem = kOffMisc + 64 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
-static_assert(kOffRing % 1024 == 0 && kOffBar % 8 == 0, "alignment");
+static_assert(kOffBar % 8 == 0 && kThreads / 32 <= 16, "alignment, room for the sums");
 
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;
 constexpr long long kDrainLimit = 1LL << 40;
@@ -113,12 +118,25 @@ __device__ __forceinline__ void tmem_relinquish2() {
 __device__ __forceinline__ void tmem_dealloc2(uint32_t a, uint32_t n) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(a), "r"(n) : "memory");
 }
-__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Operand descriptors by their low words (address and leading offset); the high words (stride 1024,
+// version 1, 128-byte swizzle) are the same for all.  From an elected lane of a converged warp, with
+// uniform operands: 64-bit descriptors put together by one lane take it 80 to 140 cycles an MMA, more
+// than the MMA.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (kSwizzle128 << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | (lbo >> 4) << 16; }
+__device__ __forceinline__ void mma2(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
+}
+// one lane of the (converged) warp, the same every time
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 // arrive on this barrier of both CTAs when every MMA issued so far has completed
 __device__ __forceinline__ void commit2(uint64_t* bar) {
@@ -143,6 +161,12 @@ __device__ __forceinline__ void load_rows4(uint32_t dst, const void* map, int x,
       "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
       "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
       : "memory");
+}
+// arrive on a barrier of the pair's first CTA.  What it announces lies in this SM (shared memory behind a
+// proxy fence, TMEM behind a tcgen05 fence) and is read by the tensor core here, so release at the CTA's
+// scope is enough; at the cluster's scope it waits some 2000 cycles for every store of the thread.
+__device__ __forceinline__ void arrive_first(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -281,9 +305,12 @@ __device__ __forceinline__ unsigned long long mask_bits(const long long* words, 
   return r == 0 ? lo : lo >> r | word(q + 1) << (64 - r);
 }
 
+// kTwo: the weights in two bf16 terms (their rounding, 2^-17, is below fp32 results' needs), else one
+template <bool kTwo>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_tree_kernel(const __grid_constant__ CUtensorMap map_box, const __grid_constant__ CUtensorMap map_row,
                        const __grid_constant__ CUtensorMap map_q, const TreeTcParams tp) {
+  constexpr int kSlots = Ring<kTwo>::kSlots, kOffRing = Ring<kTwo>::kOff;
   const TreeParams& p = tp.p;
   extern __shared__ char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -305,11 +332,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bars[kBarQEmpty], 1);          // the piece's last QK^T has completed
     mbar_init(&bars[kBarS], 1);               // scores of this buffer complete
     mbar_init(&bars[kBarS + 1], 1);
-    mbar_init(&bars[kBarP], 8);               // (first CTA) both CTAs' softmax warps: P written, O rescaled
+    mbar_init(&bars[kBarP], 2 * kSoftWarps);  // (first CTA) both CTAs' softmax warps: P written, O rescaled
     mbar_init(&bars[kBarPv], 1);              // P V of a tile has completed
-    mbar_init(&bars[kBarO], 8);               // (first CTA) the softmax warps have read O
-    mbar_init(&bars[kBarMx], 2);              // the two warps of a row have left their values
-    mbar_init(&bars[kBarMx + 1], 2);
+    mbar_init(&bars[kBarO], 2 * kSoftWarps);  // (first CTA) the softmax warps have read O
+    mbar_init(&bars[kBarMx], 4);              // the four warps of a row have left their values
+    mbar_init(&bars[kBarMx + 1], 4);
     mbar_init(&bars[kBarFin], 1);
     mbar_init(&bars[kBarNever], 1);           // nothing arrives: the stall test hook waits on it
     *abort_s = 0;
@@ -343,7 +370,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa((const void*)abort_s, rank ^ 1u)), "r"(1) : "memory");
   };
   auto wait_warp = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, mbar_wait<true>(bar, parity, wl));
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, wl));
   };
   auto aborted = [&] { return __any_sync(0xffffffffu, *abort_s) != 0; };
   auto mark_bad = [&](int request) {
@@ -351,11 +378,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     atomicMax(&bad_s[1], request);
   };
 
-  if (warp < 4) {
+  if (warp < kSoftWarps) {
     // =================== softmax, rescaling, output =================================
-    const int tid = threadIdx.x, r = tid & 63, half = tid >> 6;   // row of the CTA, half of the tile's keys
+    // Four threads a row: TMEM lane r + 64 half holds the row's scores of keys [128 half, +128), of which
+    // warps 0-3 take the first 64 and warps 4-7 the others; they rescale and write the first or the
+    // second 128 of the lane's 256 columns of O.
+    const int tid = threadIdx.x, lane4 = tid & 127, r = lane4 & 63, half = lane4 >> 6, part = warp >> 2;
     const int row = kHalf * (int)rank + r;                        // of the unit
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t p_ready = mapa(&bars[kBarP], 0), o_read = mapa(&bars[kBarO], 0);
     float* mx = reinterpret_cast<float*>(smem + kOffMx);
     const float c_scale = p.scale * kLog2e;
@@ -366,18 +396,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (tid == 0 && rank == 0) rec->head_row = rec->tail_row = -1;
     int g = 0, swaps = 0;
     bool ok = true;
-    // the value of the thread with the row's other half
-    auto other = [&](float v) {
-      float* at = mx + 128 * (swaps & 1);
+    // the values of the three threads with the rest of the row
+    auto others = [&](float v, float (&u)[3]) {
+      float* at = mx + 256 * (swaps & 1);
       at[tid] = v;
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars[kBarMx + (warp & 1)]);
       ok = ok && wait_warp(&bars[kBarMx + (warp & 1)], swaps & 1);
       ++swaps;
-      return at[tid ^ 64];
+      u[0] = at[tid ^ 64];
+      u[1] = at[tid ^ 128];
+      u[2] = at[tid ^ 192];
     };
     while (ok && walk.next(p, x)) {
-      float m_ref = -INFINITY, l_sum = 0.f;
+      float m_ref = -INFINITY, l_sum = 0.f, u[3];
       const bool live = row < x.rows;
       const int node = live ? (x.node_row + row) / p.h : 0;
       const long long* words = p.mask + (size_t)(x.first + node) * p.words;
@@ -385,28 +417,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int bb = g & 1;
         if (!(ok = !aborted() && wait_warp(&bars[kBarS + bb], (g >> 1) & 1))) break;
         tc_fence_after();
-        uint32_t v[4][32];
+        float s[64];
+        {
+          uint32_t v[2][32];
+          tmem_ld32(lanes + kColS + 128 * bb + 64 * part, v[0]);
+          tmem_ld32(lanes + kColS + 128 * bb + 64 * part + 32, v[1]);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_ld32(lanes + kColS + 128 * bb + 32 * i, v[i]);
-        tmem_ld_wait();
-        float s[128];
-#pragma unroll
-        for (int j = 0; j < 128; ++j) s[j] = __uint_as_float(v[j >> 5][j & 31]);
+          for (int j = 0; j < 64; ++j) s[j] = __uint_as_float(v[j >> 5][j & 31]);
+        }
         if (c_scale < 0.f) {
 #pragma unroll
-          for (int j = 0; j < 128; ++j) s[j] = -s[j];
+          for (int j = 0; j < 64; ++j) s[j] = -s[j];
         }
         if (k >= x.cached / kTile) {           // a tile with nodes, or with the end
-          const int d = (int)((long long)k * kTile + 128 * half - x.cached);
-          unsigned long long see[2] = {~0ull, ~0ull};
-          if (live) {
-            see[0] = mask_bits(words, p.words, x.n, d);
-            see[1] = mask_bits(words, p.words, x.n, d + 64);
-          }
+          const int d = (int)((long long)k * kTile + 128 * half + 64 * part - x.cached);
+          unsigned long long see = ~0ull;
+          if (live) see = mask_bits(words, p.words, x.n, d);
           bool bad = false;
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (!(see[j >> 6] >> (j & 63) & 1)) {
+          for (int j = 0; j < 64; ++j)
+            if (!(see >> j & 1)) {
               bad |= !(fabsf(s[j]) <= 3.0e38f);   // (rows behind the end are zeros)
               s[j] = -INFINITY;
             }
@@ -414,15 +445,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         float t[16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) t[j] = s[j];
-#pragma unroll
-        for (int j = 16; j < 128; ++j) t[j & 15] = fmaxf(t[j & 15], s[j]);
+        for (int j = 0; j < 16; ++j) t[j] = fmaxf(fmaxf(s[j], s[j + 16]), fmaxf(s[j + 32], s[j + 48]));
 #pragma unroll
         for (int w = 8; w > 0; w >>= 1)
 #pragma unroll
           for (int j = 0; j < w; ++j) t[j] = fmaxf(t[j], t[j + w]);
-        const float mt = fmaxf(t[0], other(t[0])) * c_abs;
+        others(t[0], u);
         if (!ok) break;
+        const float mt = fmaxf(fmaxf(t[0], u[0]), fmaxf(u[1], u[2])) * c_abs;
         float m_new = m_ref;
         if (mt > m_ref + kRescaleThreshold || m_ref == -INFINITY) m_new = fmaxf(mt, m_ref);
         const float base = m_new == -INFINITY ? 0.f : m_new;
@@ -430,12 +460,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const bool first = k == x.k0;
         m_ref = m_new;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        uint32_t pk[64];
+        uint32_t pk[32], pl[kTwo ? 32 : 1];
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
+        for (int j = 0; j < 32; ++j) {
           const float e0 = ex2(fmaf(s[2 * j], c_abs, -base)), e1 = ex2(fmaf(s[2 * j + 1], c_abs, -base));
           sum[j & 3] += e0 + e1;
           pk[j] = pack_bf16(e0, e1);
+          if (kTwo) pl[j] = pack_bf16(e0 - __uint_as_float(pk[j] << 16), e1 - __uint_as_float(pk[j] & 0xffff0000u));
         }
         l_sum = l_sum * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
         // P's place and O are free once P V of the tile before has completed
@@ -443,15 +474,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (!(ok = wait_warp(&bars[kBarPv], (g - 1) & 1))) break;
           tc_fence_after();
         }
-        char* pb = smem + kOffP + 2 * half * kQBlk + r * 128;
+        char* pb = smem + kOffP + (2 * half + part) * kQBlk + r * 128;
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          *reinterpret_cast<uint4*>(pb + (j >> 3) * kQBlk + (((j & 7) ^ (r & 7)) * 16)) =
+        for (int j = 0; j < 8; ++j) {
+          *reinterpret_cast<uint4*>(pb + ((j ^ (r & 7)) * 16)) =
               make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+          if (kTwo)
+            *reinterpret_cast<uint4*>(pb + kPBytes + ((j ^ (r & 7)) * 16)) =
+                make_uint4(pl[4 * j], pl[4 * j + 1], pl[4 * j + 2], pl[4 * j + 3]);
+        }
         fence_proxy_async_smem();
         if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll 1
-          for (int c = 0; c < 256; c += 32) {
+          for (int c = 128 * part; c < 128 * part + 128; c += 32) {
             uint32_t o[32];
             tmem_ld32(lanes + kColO + c, o);
             tmem_ld_wait();
@@ -464,11 +499,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(p_ready);
+        if (lane == 0) arrive_first(p_ready);
       }
       if (!ok) break;
       // ---- the piece's result
-      const float l = l_sum + other(l_sum);
+      others(l_sum, u);
+      const float l = (l_sum + u[0]) + (u[1] + u[2]);
       if (!ok || !(ok = wait_warp(&bars[kBarPv], (g - 1) & 1))) break;
       tc_fence_after();
       const bool none = l == 0.f;
@@ -476,35 +512,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
       const bool whole = x.k0 == 0 && x.k1 == x.tiles, head = x.k0 == 0;
       const int slot = 2 * pair + (head ? 1 : 0);
-      float* part = whole ? static_cast<float*>(p.out) + (size_t)(x.row0 + row) * kDV
-                          : tp.ws.part + ((size_t)slot * tp.ws.cap + row) * kDV;
-      __nv_bfloat16* out16 = static_cast<__nv_bfloat16*>(p.out) + (size_t)(x.row0 + row) * kDV;
+      // A warp's 32 rows go through its own 4 KB of P, 128 bytes a row at a time, so that eight lanes write
+      // a row's 128 bytes (a row a lane, 16 bytes a store, took 17000 cycles a piece)
       const bool as16 = whole && p.out_bf16;
+      char* stage = smem + kOffP + (2 * half + part) * kQBlk + (warp & 1) * 32 * 128;
+      const int row0 = kHalf * (int)rank + (warp & 1) * 32;         // the warp's first row
+      char* to = whole ? static_cast<char*>(p.out) + (size_t)(x.row0 + row0) * kDV * (as16 ? 2 : 4)
+                       : reinterpret_cast<char*>(tp.ws.part + ((size_t)slot * tp.ws.cap + row0) * kDV);
+      const int pitch = kDV * (as16 ? 2 : 4), left = x.rows - row0;
+      to += (256 * half + 128 * part) * (as16 ? 2 : 4);
+      const int wide = as16 ? 64 : 32;                              // columns of 128 bytes
 #pragma unroll 1
-      for (int c = 0; c < 256; c += 32) {
+      for (int c = 0; c < 128; c += wide) {
         uint32_t o[32];
-        tmem_ld32(lanes + kColO + c, o);
+        tmem_ld32(lanes + kColO + 128 * part + c, o);
         tmem_ld_wait();
-        const int at = 256 * half + c;
-        if (live && as16) {
+        if (as16) {
+          uint32_t o2[32];
+          tmem_ld32(lanes + kColO + 128 * part + c + 32, o2);
+          tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
+          for (int j = 0; j < 16; ++j)
+            o[j] = pack_bf16(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              w[u] = pack_bf16(__uint_as_float(o[8 * j + 2 * u]) * inv, __uint_as_float(o[8 * j + 2 * u + 1]) * inv);
-            *reinterpret_cast<uint4*>(out16 + at + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (live) {
+          for (int j = 0; j < 16; ++j)
+            o[16 + j] = pack_bf16(__uint_as_float(o2[2 * j]) * inv, __uint_as_float(o2[2 * j + 1]) * inv);
+        } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4*>(part + at + 4 * j) =
-                make_float4(__uint_as_float(o[4 * j]) * inv, __uint_as_float(o[4 * j + 1]) * inv,
-                            __uint_as_float(o[4 * j + 2]) * inv, __uint_as_float(o[4 * j + 3]) * inv);
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * inv);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+              make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = 4 * i + (lane >> 3);
+          const uint4 y = *reinterpret_cast<const uint4*>(stage + rr * 128 + (((lane & 7) ^ (rr & 7)) * 16));
+          if (rr < left) *reinterpret_cast<uint4*>(to + (size_t)rr * pitch + c * (as16 ? 2 : 4) + (lane & 7) * 16) = y;
         }
         __syncwarp();
       }
-      if (live && half == 0) {
+      if (live && half == 0 && part == 0) {
         if (whole) p.lse[x.row0 + row] = lse;
         else tp.ws.lse[(size_t)slot * tp.ws.cap + row] = lse;
       }
@@ -520,99 +570,126 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_remote(o_read);
+      if (lane == 0) arrive_first(o_read);
     }
     if (!ok) fail();
   } else if (warp == kMmaWarp) {
     // =================== MMAs =========================================================
-    if (rank == 0 && lane == 0 && len > 0) {
+    // The whole warp walks, one elected lane issues.
+    if (rank == 0 && len > 0) {
       const uint32_t id_qk = idesc_bf16(128, 256, 0, 0), id_pv = idesc_bf16(128, 256, 0, 1);
-      const uint64_t dq = smem_desc(smem_u32(smem), 16, 1024, kSwizzle128);
-      const uint64_t dp = smem_desc(smem_u32(smem + kOffP), 16, 1024, kSwizzle128);
-      const uint64_t dk = smem_desc(smem_u32(smem + kOffRing), 16, 1024, kSwizzle128);
-      const uint64_t dv = smem_desc(smem_u32(smem + kOffRing), 8192, 1024, kSwizzle128);
-      int slot = 0, round = 0, g = 0, pieces = 0;
+      const uint32_t sm0 = smem_u32(smem);
+      const uint32_t dq = desc_lo(sm0, 16), dp = desc_lo(sm0 + kOffP, 16);
+      const uint32_t dk = desc_lo(sm0 + kOffRing, 16), dv = desc_lo(sm0 + kOffRing, 8192);
+      int slot = 0, g = 0, pieces = 0;
+      uint32_t round = 0;
       // test hook: a wait that cannot complete, so the wait limit runs out
-      bool ok = !p.stall || mbar_wait(&bars[kBarNever], 0, wl);
+      bool ok = !p.stall || wait_warp(&bars[kBarNever], 0);
       auto full = [&]() -> bool {
-        ok = ok && !*abort_s && mbar_wait<true>(&bars[kBarFull + slot], round & 1, wl);
+        ok = ok && wait_warp(&bars[kBarFull + slot], round);
         tc_fence_after();
         return ok;
       };
-      auto release = [&] {
-        commit2(&bars[kBarEmpty + slot]);
+      auto pass = [&] {
         if (++slot == kSlots) {
           slot = 0;
-          ++round;
+          round ^= 1;
         }
       };
       auto qk = [&](int tile, bool last) {     // scores of the tile-th tile of all
         const uint32_t d = tmem + kColS + 128 * (tile & 1);
-        uint64_t a = dq;
 #pragma unroll 1
-        for (int j = 0; j < kKChunks; ++j, a += kQBlk >> 4) {
+        for (int j = 0; j < kKChunks; ++j) {
           if (!full()) return;
-          const uint64_t b = dk + (uint64_t)(slot * (kChunk >> 4));
+          if (elect_one()) {
+            const uint32_t a = dq + j * (kQBlk >> 4), b = dk + slot * (kChunk >> 4);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) mma2(d, a + 2 * u, b + 2 * u, id_qk, j > 0 || u > 0);
-          release();
+            for (int u = 0; u < 4; ++u) mma2(d, a + 2 * u, b + 2 * u, id_qk, j > 0 || u > 0);
+            commit2(&bars[kBarEmpty + slot]);
+          }
+          __syncwarp();
+          pass();
         }
-        commit2(&bars[kBarS + (tile & 1)]);
-        if (last) commit2(&bars[kBarQEmpty]);
+        if (elect_one()) {
+          commit2(&bars[kBarS + (tile & 1)]);
+          if (last) commit2(&bars[kBarQEmpty]);
+        }
+        __syncwarp();
       };
       while (ok && walk.next(p, x)) {
-        if (!(ok = mbar_wait<true>(&bars[kBarQFull], pieces & 1, wl))) break;
+        if (!(ok = wait_warp(&bars[kBarQFull], pieces & 1))) break;
         tc_fence_after();
         qk(g, x.k0 + 1 == x.k1);
         for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
           if (k + 1 < x.k1) qk(g + 1, k + 2 == x.k1);
-          if (!ok || !(ok = mbar_wait<true>(&bars[kBarP], g & 1, wl))) break;
-          if (k == x.k0 && pieces > 0 && !(ok = mbar_wait<true>(&bars[kBarO], (pieces - 1) & 1, wl))) break;
+          if (!ok || aborted() || !(ok = wait_warp(&bars[kBarP], g & 1))) break;
+          if (k == x.k0 && pieces > 0 && !(ok = wait_warp(&bars[kBarO], (pieces - 1) & 1))) break;
           tc_fence_after();
-          uint64_t a = dp;
 #pragma unroll 1
           for (int j = 0; j < kVChunks; ++j) {
             if (!full()) break;
-            const uint64_t b = dv + (uint64_t)(slot * (kChunk >> 4));
+            if (elect_one()) {
+              const uint32_t a = dp + (j & 3) * (kQBlk >> 4), b = dv + slot * (kChunk >> 4);
+              const uint32_t d = tmem + kColO + 128 * (j >> 2);
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              mma2(tmem + kColO + 128 * (j >> 2), a + 2 * u, b + 128 * u, id_pv, k > x.k0 || (j & 3) > 0 || u > 0);
-            release();
-            a = (j & 3) == 3 ? dp : a + (kQBlk >> 4);
+              for (int u = 0; u < 4; ++u) mma2(d, a + 2 * u, b + 128 * u, id_pv, k > x.k0 || (j & 3) > 0 || u > 0);
+              if (kTwo) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) mma2(d, a + (kPBytes >> 4) + 2 * u, b + 128 * u, id_pv, 1);
+              }
+              commit2(&bars[kBarEmpty + slot]);
+            }
+            __syncwarp();
+            pass();
           }
-          commit2(&bars[kBarPv]);
+          if (elect_one()) commit2(&bars[kBarPv]);
+          __syncwarp();
         }
+        if (aborted()) ok = false;
         ++pieces;
       }
       // the second CTA's last arrivals here: no one else waits for them
-      if (ok && pieces > 0) ok = mbar_wait<true>(&bars[kBarO], (pieces - 1) & 1, wl);
+      if (ok && pieces > 0) ok = wait_warp(&bars[kBarO], (pieces - 1) & 1);
       if (!ok) fail();
-      commit2(&bars[kBarFin]);
+      if (elect_one()) commit2(&bars[kBarFin]);
+      __syncwarp();
     }
     // Every MMA has completed, and every arrival that commits send to either CTA has landed, before
     // TMEM and shared memory go away: an arrival at a CTA that has ended is a fault.
-    if (lane == 0 && len > 0 && !mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit))
+    if (len > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit)))
       report_status(p.status, kStatusTimeout);
   } else if (warp < kLoadWarp + kLoadWarps) {
     // =================== keys and values ============================================
     // Warp w brings the key chunks j with j % 4 == w (64 columns of the CTA's 128 keys) and the value
-    // chunks w and 4 + w (128 columns of the tile's w-th 64 keys); a lane brings a box of `box` rows,
-    // whose places it looks up a tile ahead.
+    // chunks w and 4 + w (128 columns of the tile's w-th 64 keys), in boxes of `box` rows, or row by row
+    // where the block size has no such power of two.  A lane looks up the place of a box (of four rows), a
+    // tile ahead; an elected lane issues the loads.
     // A wait for a slot's round r is by parity, so it takes round r - 2 for done where that is all that is:
     // a warp's chunks lie at most 5 places apart, and the wait for one of them says that every chunk up to
     // kSlots places before it has been read, so the next one's slot is at most one round behind.
     static_assert(kSlots >= 5, "the distance of a warp's chunks");
     const int w = warp - kLoadWarp;
-    const int box = tp.box ? tp.box : 4;
-    const int boxes = 128 / box, per_v = 64 / box;
-    const bool mine = lane < boxes;
-    const int v_cb = lane / per_v, v_at = (lane % per_v) * box;
-    const uint32_t full0 = mapa(&bars[kBarFull], 0);
+    const int step = tp.box ? tp.box : 4, k_boxes = 128 / step, v_boxes = 64 / step;
+    const uint32_t full0 = mapa(&bars[kBarFull], 0), ring = smem_u32(smem + kOffRing);
     bool ok = true, bad = false;
-    int slot_at = 0, round = 0;                // of the next chunk in order
-    struct Place { int r[4]; int n; };         // rows of a box, and how many of them exist
     const int32_t* table = nullptr;
     long long end = 0;
+    // a lane's step rows from `pos` on: the table's entries (as they are), and how many rows exist
+    struct Place { long long pos; int e[4], n; };
+    auto look = [&](long long pos, bool mine) {
+      Place q;
+      q.pos = pos;
+      q.n = mine ? (int)min(max(end - pos, 0ll), (long long)step) : 0;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        q.e[u] = -1;
+        if (u == 0 ? q.n > 0 : !tp.box && u < q.n) {
+          const int blk = (int)((uint32_t)(pos + u) / (uint32_t)p.block_size);   // (below 2^31 + 256)
+          if (blk < p.max_blocks) q.e[u] = table[blk];
+        }
+      }
+      return q;
+    };
     // no block for the positions [pos, pos + n): that matters where a node attends to one of them
     auto missed = [&](long long pos, int n) {
       for (int u = 0; u < n && !bad; ++u) {
@@ -622,106 +699,104 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bad = p.mask[(size_t)(x.first + i) * p.words + j / 64] >> (j % 64) & 1;
       }
     };
-    auto look = [&](long long pos) {
-      Place q;
-      q.n = mine ? (int)min(max(end - pos, 0ll), (long long)box) : 0;
-      q.r[0] = q.r[1] = q.r[2] = q.r[3] = tp.num_rows;
-      if (tp.box) {
-        if (q.n > 0) {
-          const int blk = (int)((uint32_t)pos / (uint32_t)p.block_size);   // (below 2^31 + 256)
-          const int phys = blk < p.max_blocks ? table[blk] : -1;
-          if (phys < 0 || phys >= p.num_blocks) {
-            missed(pos, q.n);
-            q.n = 0;
+    // cache rows of a place; rows that do not exist are the row behind the last, which loads as zeros
+    struct Rows { int r[4], n; };
+    auto rows_of = [&](const Place& q) {
+      Rows x4;
+      x4.n = q.n;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        x4.r[u] = tp.num_rows;
+        if (u == 0 ? q.n > 0 : !tp.box && u < q.n) {
+          if (q.e[u] < 0 || q.e[u] >= p.num_blocks) {
+            missed(q.pos + u, tp.box ? q.n : 1);
+            if (tp.box) x4.n = 0;
           } else {
-            q.r[0] = phys * p.block_size + (int)((uint32_t)pos - (uint32_t)blk * (uint32_t)p.block_size);
+            x4.r[u] = q.e[u] * p.block_size + (int)((uint32_t)(q.pos + u) % (uint32_t)p.block_size);
           }
         }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          if (u < q.n) {
-            const int blk = (int)((uint32_t)(pos + u) / (uint32_t)p.block_size);
-            const int phys = blk < p.max_blocks ? table[blk] : -1;
-            if (phys < 0 || phys >= p.num_blocks) missed(pos + u, 1);
-            else q.r[u] = phys * p.block_size + (int)((uint32_t)(pos + u) - (uint32_t)blk * (uint32_t)p.block_size);
-          }
       }
-      return q;
+      return x4;
     };
-    auto bring = [&](uint32_t dst, int col, const Place& q, uint32_t bar) {
+    // Every lane with a place brings it, in one instruction (a loop over an elected lane's loads took half as
+    // long again); where the sequence ends in a box, its rows four at a time, with zeros behind the end.
+    auto bring = [&](uint32_t dst, int col, const Rows& q, bool mine, bool cut, uint32_t bar) {
       if (!tp.box) {
         if (mine) load_rows4(dst, &map_row, col, q.r[0], q.r[1], q.r[2], q.r[3], bar);
         return;
       }
-      const bool cut = q.n != box && q.n != 0;   // the sequence ends in it: rows behind the end are zeros
-      if (mine && !cut) load_box(dst, &map_box, col, q.n ? q.r[0] : tp.num_rows, bar);
-      if (__any_sync(0xffffffffu, cut)) {
-        for (int i = 0; i < box; i += 4) {
-          auto at = [&](int u) { return i + u < q.n ? q.r[0] + i + u : tp.num_rows; };
-          if (cut) load_rows4(dst + i * 128, &map_row, col, at(0), at(1), at(2), at(3), bar);
+      const bool whole = !cut || q.n == step || q.n == 0;
+      if (mine && whole) load_box(dst, &map_box, col, q.r[0], bar);
+      if (cut) {
+        __syncwarp();
+        for (int a = 0; a < step; a += 4) {
+          auto at = [&](int u) { return a + u < q.n ? q.r[0] + a + u : tp.num_rows; };
+          if (mine && !whole) load_rows4(dst + a * 128, &map_row, col, at(0), at(1), at(2), at(3), bar);
           __syncwarp();
         }
       }
     };
-    // the chunk `ahead` places on in the order: its slot, once that is free; false: gave up
-    auto take = [&](int ahead, int& slot) -> bool {
-      int rd = round;
-      slot = slot_at + ahead;
-      while (slot >= kSlots) {
+    // the warp's next chunk, `ahead` places behind its last one: its slot, once that is free
+    int slot = -1;
+    uint32_t round = 0;
+    auto take = [&](int ahead) -> bool {
+      slot += ahead;
+      if (slot >= kSlots) {
         slot -= kSlots;
-        ++rd;
-      }
-      if (aborted()) return false;
-      if (rd > 0 && !wait_warp(&bars[kBarEmpty + slot], (rd - 1) & 1)) return false;
-      if (rank == 0 && lane == 0) mbar_arrive_expect_tx(&bars[kBarFull + slot], 2 * kChunk);
-      __syncwarp();
-      return true;
-    };
-    auto pass = [&](int chunks) {
-      slot_at += chunks;
-      while (slot_at >= kSlots) {
-        slot_at -= kSlots;
         ++round;
       }
+      if (round > 0 && !wait_warp(&bars[kBarEmpty + slot], (round - 1) & 1)) return false;
+      if (rank == 0) {
+        if (lane == 0) mbar_arrive_expect_tx(&bars[kBarFull + slot], 2 * kChunk);
+        __syncwarp();
+      }
+      return true;
     };
-    auto keys = [&](const Place& q) {
+    const bool mine = lane < k_boxes;
+    const uint32_t k_dst = ring + lane * step * 128;
+    const uint32_t v_dst = ring + lane / v_boxes * 8192 + lane % v_boxes * step * 128;
+    const int v_col = 256 * (int)rank + 64 * (lane / v_boxes);
+    int ahead = w + 1;                         // from the warp's last chunk to its next
+    auto keys = [&](const Rows& q) {
+      const bool cut = __any_sync(0xffffffffu, q.n != 0 && q.n != step);
       for (int j = w; ok && j < kKChunks; j += kLoadWarps) {
-        int slot;
-        if (!(ok = take(j, slot))) break;
-        bring(smem_u32(smem + kOffRing + slot * kChunk + lane * box * 128), 64 * j, q, full0 + 8 * slot);
+        if (!(ok = take(ahead))) break;
+        bring(k_dst + slot * kChunk, 64 * j, q, mine, cut, full0 + 8 * slot);
+        ahead = kLoadWarps;
       }
-      pass(kKChunks);
+      ahead = w == 0 ? 1 : kKChunks - kLoadWarps;   // keys w, w + 4 (, 8), then whatever begins behind them
     };
-    auto values = [&](const Place& q) {
+    auto values = [&](const Rows& q) {
+      const bool cut = __any_sync(0xffffffffu, q.n != 0 && q.n != step);
       for (int h = 0; ok && h < 2; ++h) {
-        int slot;
-        if (!(ok = take(4 * h + w, slot))) break;
-        bring(smem_u32(smem + kOffRing + slot * kChunk + v_cb * 8192 + v_at * 128),
-              256 * (int)rank + 128 * h + 64 * v_cb, q, full0 + 8 * slot);
+        if (!(ok = take(ahead))) break;
+        bring(v_dst + slot * kChunk, v_col + 128 * h, q, mine, cut, full0 + 8 * slot);
+        ahead = kLoadWarps;
       }
-      pass(kVChunks);
     };
     while (ok && walk.next(p, x)) {
       table = p.block_table + (size_t)x.request * p.max_blocks;
       end = (long long)x.cached + x.n;
-      const long long k_off = 128 * (int)rank + lane * box, v_off = 64 * w + v_at;
-      Place kq = look((long long)x.k0 * kTile + k_off), vq = look((long long)x.k0 * kTile + v_off);
-      keys(kq);
-      kq = look((long long)(x.k0 + 1) * kTile + k_off);
+      const long long k_off = 128 * (int)rank + lane * step, v_off = 64 * w + lane % v_boxes * step;
+      Place kq = look((long long)x.k0 * kTile + k_off, mine), vq = look((long long)x.k0 * kTile + v_off, mine);
+      keys(rows_of(kq));
+      kq = look((long long)(x.k0 + 1) * kTile + k_off, mine);
       for (int k = x.k0; ok && k < x.k1; ++k) {
+        if (aborted()) ok = false;
         if (k + 1 < x.k1) {
-          keys(kq);
-          kq = look((long long)(k + 2) * kTile + k_off);
+          const Place kn = look((long long)(k + 2) * kTile + k_off, mine);
+          keys(rows_of(kq));
+          kq = kn;
         }
-        const Place vn = look((long long)(k + 1) * kTile + v_off);
-        values(vq);
+        const Place vn = look((long long)(k + 1) * kTile + v_off, mine);
+        values(rows_of(vq));
         vq = vn;
       }
-      if (bad) {                               // (also from a look past the piece: the request's all the same)
+      if (bad) {
         mark_bad(x.request);
         bad = false;
       }
+      __syncwarp();
     }
     if (!ok) fail();
   } else {
@@ -731,7 +806,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t qfull = mapa(&bars[kBarQFull], 0);
       for (int i = 0; ok && walk.next(p, x); ++i) {
         if (*abort_s) break;
-        if (i > 0 && !(ok = mbar_wait<true>(&bars[kBarQEmpty], (i - 1) & 1, wl))) break;
+        if (i > 0 && !(ok = mbar_wait(&bars[kBarQEmpty], (i - 1) & 1, wl))) break;
         if (rank == 0) mbar_arrive_expect_tx(&bars[kBarQFull], 2 * kQBytes);
         for (int j = 0; j < 9; ++j)
           load_box(smem_u32(smem + j * kQBlk), &map_q, 64 * j, x.row0 + kHalf * (int)rank, qfull);
@@ -860,8 +935,10 @@ cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-    cudaError_t e = cudaFuncSetAttribute(decode_tree_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
+    for (auto kernel : {decode_tree_kernel<false>, decode_tree_kernel<true>}) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+      if (e != cudaSuccess) return e;
+    }
     if (dev >= 0 && dev < 64) attr_set[dev].store(true, std::memory_order_release);
   }
   TreeTcParams tp;
@@ -877,7 +954,8 @@ cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
   if (!make_rows_map(&box, p.kv, tp.num_rows, tp.box ? tp.box : 8) || !make_rows_map(&row, p.kv, tp.num_rows, 1) ||
       !make_rows_map(&q, p.q, (long long)p.T * p.h, kHalf))
     return cudaErrorInvalidValue;
-  decode_tree_kernel<<<2 * tp.pairs, kThreads, kSmem, stream>>>(box, row, q, tp);
+  const auto kernel = p.out_bf16 ? decode_tree_kernel<false> : decode_tree_kernel<true>;
+  kernel<<<2 * tp.pairs, kThreads, kSmem, stream>>>(box, row, q, tp);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   join_tree_kernel<<<dim3(tp.pairs, kJoinRows), kJoinThreads, kFixSmem, stream>>>(tp);
