@@ -673,27 +673,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t full0 = mapa(&bars[kBarFull], 0), ring = smem_u32(smem + kOffRing);
     bool ok = true, bad = false;
     const int32_t* table = nullptr;
-    long long end = 0;
-    // a lane's step rows from `pos` on: the table's entries (as they are), and how many rows exist
-    struct Place { long long pos; int e[4], n; };
-    auto look = [&](long long pos, bool mine) {
-      Place q;
-      q.pos = pos;
-      q.n = mine ? (int)min(max(end - pos, 0ll), (long long)step) : 0;
+    int end = 0;
+    // Where a lane's next box (of `step` rows; without boxes, of four rows found one by one) lies: moved on by
+    // a tile at a time, without divisions, and its table entries loaded a tile ahead.
+    struct Place { int blk, off, left, e[4]; };
+    const int tile_blk = kTile / p.block_size, tile_off = kTile % p.block_size;
+    const bool mine = lane < k_boxes;
+    auto load_entries = [&](Place& q) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        q.e[u] = -1;
-        if (u == 0 ? q.n > 0 : !tp.box && u < q.n) {
-          const int blk = (int)((uint32_t)(pos + u) / (uint32_t)p.block_size);   // (below 2^31 + 256)
-          if (blk < p.max_blocks) q.e[u] = table[blk];
+      for (int u = 0; u < 4; ++u) q.e[u] = -1;
+      if (!mine || q.left <= 0) return;
+      if (q.blk < p.max_blocks) q.e[0] = table[q.blk];
+      if (tp.box) return;
+      int blk = q.blk, off = q.off;
+#pragma unroll
+      for (int u = 1; u < 4; ++u) {
+        if (++off == p.block_size) {
+          off = 0;
+          ++blk;
         }
+        if (u < q.left && blk < p.max_blocks) q.e[u] = table[blk];
       }
+    };
+    auto place_at = [&](long long pos) {
+      Place q;
+      q.blk = (int)(pos / p.block_size);
+      q.off = (int)(pos % p.block_size);
+      q.left = (int)max((long long)end - pos, -1ll);
+      load_entries(q);
       return q;
     };
+    auto next_tile = [&](Place& q) {
+      q.blk += tile_blk;
+      q.off += tile_off;
+      if (q.off >= p.block_size) {
+        q.off -= p.block_size;
+        ++q.blk;
+      }
+      q.left = max(q.left, 0) - kTile;
+      load_entries(q);
+    };
     // no block for the positions [pos, pos + n): that matters where a node attends to one of them
-    auto missed = [&](long long pos, int n) {
+    auto missed = [&](int pos, int n) {
       for (int u = 0; u < n && !bad; ++u) {
-        const long long j = pos + u - x.cached;
+        const int j = pos + u - x.cached;
         if (j < 0) bad = true;
         for (int i = 0; i < x.n && j >= 0 && !bad; ++i)
           bad = p.mask[(size_t)(x.first + i) * p.words + j / 64] >> (j % 64) & 1;
@@ -702,25 +725,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // cache rows of a place; rows that do not exist are the row behind the last, which loads as zeros
     struct Rows { int r[4], n; };
     auto rows_of = [&](const Place& q) {
-      Rows x4;
-      x4.n = q.n;
+      Rows y;
+      y.n = mine ? min(max(q.left, 0), step) : 0;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        x4.r[u] = tp.num_rows;
-        if (u == 0 ? q.n > 0 : !tp.box && u < q.n) {
-          if (q.e[u] < 0 || q.e[u] >= p.num_blocks) {
-            missed(q.pos + u, tp.box ? q.n : 1);
-            if (tp.box) x4.n = 0;
-          } else {
-            x4.r[u] = q.e[u] * p.block_size + (int)((uint32_t)(q.pos + u) % (uint32_t)p.block_size);
-          }
+      for (int u = 0; u < 4; ++u) y.r[u] = tp.num_rows;
+      if (tp.box) {
+        if ((uint32_t)q.e[0] < (uint32_t)p.num_blocks) {
+          y.r[0] = q.e[0] * p.block_size + q.off;
+        } else if (y.n > 0) {
+          missed(end - q.left, y.n);
+          y.n = 0;
+        }
+      } else {
+        int off = q.off;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if ((uint32_t)q.e[u] < (uint32_t)p.num_blocks) y.r[u] = q.e[u] * p.block_size + off;
+          else if (u < y.n) missed(end - q.left + u, 1);
+          if (++off == p.block_size) off = 0;
         }
       }
-      return x4;
+      return y;
     };
     // Every lane with a place brings it, in one instruction (a loop over an elected lane's loads took half as
     // long again); where the sequence ends in a box, its rows four at a time, with zeros behind the end.
-    auto bring = [&](uint32_t dst, int col, const Rows& q, bool mine, bool cut, uint32_t bar) {
+    auto bring = [&](uint32_t dst, int col, const Rows& q, bool cut, uint32_t bar) {
       if (!tp.box) {
         if (mine) load_rows4(dst, &map_row, col, q.r[0], q.r[1], q.r[2], q.r[3], bar);
         return;
@@ -752,7 +781,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    const bool mine = lane < k_boxes;
     const uint32_t k_dst = ring + lane * step * 128;
     const uint32_t v_dst = ring + lane / v_boxes * 8192 + lane % v_boxes * step * 128;
     const int v_col = 256 * (int)rank + 64 * (lane / v_boxes);
@@ -761,7 +789,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool cut = __any_sync(0xffffffffu, q.n != 0 && q.n != step);
       for (int j = w; ok && j < kKChunks; j += kLoadWarps) {
         if (!(ok = take(ahead))) break;
-        bring(k_dst + slot * kChunk, 64 * j, q, mine, cut, full0 + 8 * slot);
+        bring(k_dst + slot * kChunk, 64 * j, q, cut, full0 + 8 * slot);
         ahead = kLoadWarps;
       }
       ahead = w == 0 ? 1 : kKChunks - kLoadWarps;   // keys w, w + 4 (, 8), then whatever begins behind them
@@ -770,27 +798,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool cut = __any_sync(0xffffffffu, q.n != 0 && q.n != step);
       for (int h = 0; ok && h < 2; ++h) {
         if (!(ok = take(ahead))) break;
-        bring(v_dst + slot * kChunk, v_col + 128 * h, q, mine, cut, full0 + 8 * slot);
+        bring(v_dst + slot * kChunk, v_col + 128 * h, q, cut, full0 + 8 * slot);
         ahead = kLoadWarps;
       }
     };
     while (ok && walk.next(p, x)) {
       table = p.block_table + (size_t)x.request * p.max_blocks;
-      end = (long long)x.cached + x.n;
-      const long long k_off = 128 * (int)rank + lane * step, v_off = 64 * w + lane % v_boxes * step;
-      Place kq = look((long long)x.k0 * kTile + k_off, mine), vq = look((long long)x.k0 * kTile + v_off, mine);
-      keys(rows_of(kq));
-      kq = look((long long)(x.k0 + 1) * kTile + k_off, mine);
+      end = (int)min((long long)x.cached + x.n, 0x7fffffffll);
+      // ahead of the loop: the first tile's keys; in it, the next tile's keys, then the values.  A kind's rows
+      // are worked out, and the entries behind them asked for, before its first wait for a slot.
+      const long long p0 = (long long)x.k0 * kTile;
+      Place kp = place_at(p0 + 128 * (int)rank + lane * step), vp = place_at(p0 + 64 * w + lane % v_boxes * step);
+      Rows kr = rows_of(kp);
+      next_tile(kp);
+      keys(kr);
       for (int k = x.k0; ok && k < x.k1; ++k) {
         if (aborted()) ok = false;
         if (k + 1 < x.k1) {
-          const Place kn = look((long long)(k + 2) * kTile + k_off, mine);
-          keys(rows_of(kq));
-          kq = kn;
+          kr = rows_of(kp);
+          next_tile(kp);
+          keys(kr);
         }
-        const Place vn = look((long long)(k + 1) * kTile + v_off, mine);
-        values(rows_of(vq));
-        vq = vn;
+        const Rows vr = rows_of(vp);
+        next_tile(vp);
+        values(vr);
       }
       if (bad) {
         mark_bad(x.request);
