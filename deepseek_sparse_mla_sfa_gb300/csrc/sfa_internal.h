@@ -176,6 +176,8 @@ size_t tree_workspace_bytes(int T, int h);                                  // o
 // rows of 576 bf16 (q's or the cache's), boxes of 64 columns x box_rows rows, 128-byte swizzle;
 // remembered per host thread
 bool make_rows_map(CUtensorMap* m, const void* base, long long num_rows, int box_rows);
+// the same rows as (64 columns, rows, 9 blocks of columns); boxes of box_blocks blocks one behind the other
+bool make_blocks_map(CUtensorMap* m, const void* base, long long num_rows, int box_rows, int box_blocks);
 cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t* lens, const int32_t* src,
                                const int32_t* dst, int n, int32_t* shares, int num_blocks, const int32_t* free_blocks,
                                int num_free, const int32_t* taken, int block_size, int32_t* copies, int32_t* taken_out,

@@ -739,6 +739,14 @@ bool make_rows_map(CUtensorMap* m, const void* base, long long num_rows, int box
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
 }
 
+bool make_blocks_map(CUtensorMap* m, const void* base, long long num_rows, int box_rows, int box_blocks) {
+  cuuint64_t dims[3] = {64, (cuuint64_t)num_rows, (cuuint64_t)(kDQK / 64)};
+  cuuint64_t strides[2] = {(cuuint64_t)kDQK * 2, 128};
+  cuuint32_t box[3] = {64, (cuuint32_t)box_rows, (cuuint32_t)box_blocks};
+  return encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, base, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+}
+
 bool tc_supports(int h, int block_size) {
   (void)block_size;
   return h >= 1 && h <= kHeads;

@@ -35,8 +35,8 @@
 // attends to and that has no block.  Both mark the request, and the second kernel computes its nodes on CUDA
 // cores, which reads only what a node attends to.
 //
-// Warps (448 threads): 0-7 softmax, rescaling, output; 8 issues the MMAs (in the pair's first CTA);
-// 9-12 bring keys and values; 13 brings q.  Every wait is bounded; one that gives up records
+// Warps (512 threads): 0-7 softmax, rescaling, output (the first thread brings q); 8 issues the MMAs (in
+// the pair's first CTA); 9-15 bring keys and values, one a slot of the ring.  Every wait is bounded; one that gives up records
 // SFA_ERR_DEVICE_TIMEOUT and both CTAs unwind.
 #include <atomic>
 #include <cuda.h>
@@ -50,7 +50,7 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kLoadWarps = 4, kThreads = 14 * 32;
+constexpr int kSoftWarps = 8, kMmaWarp = 8, kLoadWarp = 9, kThreads = 16 * 32;
 constexpr int kRows = 128, kHalf = 64;         // query rows of a unit, of a CTA
 constexpr int kTile = 256;                     // positions of a tile
 constexpr int kKChunks = 9, kVChunks = 8;      // of a tile
@@ -75,8 +75,7 @@ struct Ring {
 constexpr int kOffMx = kOffP + kPBytes + 7 * kChunk;     // float [2][256]: row maxima, then sums
 constexpr int kOffScan = kOffMx + 2048;                  // long long [kThreads / 32], then int [8]
 constexpr int kOffBar = kOffScan + 8 * 16 + 32;
-constexpr int kBarFull = 0, kBarEmpty = 7, kBarQFull = 14, kBarQEmpty = kBarQFull + 1,
-              kBarS = kBarQEmpty + 1, kBarP = kBarS + 2, kBarPv = kBarP + 1, kBarO = kBarPv + 1,
+constexpr int kBarFull = 0, kBarEmpty = 7, kBarQFull = 14, kBarS = kBarQFull + 1, kBarP = kBarS + 2, kBarPv = kBarP + 1, kBarO = kBarPv + 1,
               kBarMx = kBarO + 1, kBarFin = kBarMx + 2, kBarNever = kBarFin + 1, kNumBars = kBarNever + 1;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;         // TMEM address, abort, bad range
 constexpr int kSmem = kOffMisc + 64 + 1024;
@@ -152,6 +151,14 @@ __device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, i
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
       "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
       "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+// two blocks of 64 columns (from the block-th on) of the rows from y on
+__device__ __forceinline__ void load_box2(uint32_t dst, const void* map, int y, int block, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
+      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(y), "r"(block), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void load_rows4(uint32_t dst, const void* map, int x, int r0, int r1, int r2, int r3,
@@ -308,8 +315,9 @@ __device__ __forceinline__ unsigned long long mask_bits(const long long* words, 
 // kTwo: the weights in two bf16 terms (their rounding, 2^-17, is below fp32 results' needs), else one
 template <bool kTwo>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    decode_tree_kernel(const __grid_constant__ CUtensorMap map_box, const __grid_constant__ CUtensorMap map_row,
-                       const __grid_constant__ CUtensorMap map_q, const TreeTcParams tp) {
+    decode_tree_kernel(const __grid_constant__ CUtensorMap map_box, const __grid_constant__ CUtensorMap map_two,
+                       const __grid_constant__ CUtensorMap map_row, const __grid_constant__ CUtensorMap map_q,
+                       const TreeTcParams tp) {
   constexpr int kSlots = Ring<kTwo>::kSlots, kOffRing = Ring<kTwo>::kOff;
   const TreeParams& p = tp.p;
   extern __shared__ char smem_raw[];
@@ -329,7 +337,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       mbar_init(&bars[kBarEmpty + s], 1);     // the MMAs that read the slot have completed
     }
     mbar_init(&bars[kBarQFull], 1);           // (first CTA) q of both CTAs
-    mbar_init(&bars[kBarQEmpty], 1);          // the piece's last QK^T has completed
     mbar_init(&bars[kBarS], 1);               // scores of this buffer complete
     mbar_init(&bars[kBarS + 1], 1);
     mbar_init(&bars[kBarP], 2 * kSoftWarps);  // (first CTA) both CTAs' softmax warps: P written, O rescaled
@@ -350,7 +357,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (warp == kLoadWarp && lane == 0) {
     prefetch_tmap(&map_box);
-    prefetch_tmap(&map_row);
+    prefetch_tmap(&map_two);
     prefetch_tmap(&map_q);
   }
   int b0;
@@ -408,7 +415,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       u[1] = at[tid ^ 128];
       u[2] = at[tid ^ 192];
     };
-    while (ok && walk.next(p, x)) {
+    // q of a piece: once the piece before has its last scores (the first thread has seen them)
+    const uint32_t q_full = mapa(&bars[kBarQFull], 0);
+    auto bring_q = [&](const Piece& y) {
+      if (tid != 0) return;
+      if (rank == 0) mbar_arrive_expect_tx(&bars[kBarQFull], 2 * kQBytes);
+      for (int j = 0; j < 9; ++j)
+        load_box(smem_u32(smem + j * kQBlk), &map_q, 64 * j, y.row0 + kHalf * (int)rank, q_full);
+    };
+    Piece y;
+    bool more = walk.next(p, y);
+    if (more) bring_q(y);
+    while (ok && more) {
+      x = y;
       float m_ref = -INFINITY, l_sum = 0.f, u[3];
       const bool live = row < x.rows;
       const int node = live ? (x.node_row + row) / p.h : 0;
@@ -502,6 +521,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive_first(p_ready);
       }
       if (!ok) break;
+      more = walk.next(p, y);
+      if (more) bring_q(y);
       // ---- the piece's result
       others(l_sum, u);
       const float l = (l_sum + u[0]) + (u[1] + u[2]);
@@ -596,7 +617,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           round ^= 1;
         }
       };
-      auto qk = [&](int tile, bool last) {     // scores of the tile-th tile of all
+      auto qk = [&](int tile) {     // scores of the tile-th tile of all
         const uint32_t d = tmem + kColS + 128 * (tile & 1);
 #pragma unroll 1
         for (int j = 0; j < kKChunks; ++j) {
@@ -612,16 +633,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         if (elect_one()) {
           commit2(&bars[kBarS + (tile & 1)]);
-          if (last) commit2(&bars[kBarQEmpty]);
         }
         __syncwarp();
       };
       while (ok && walk.next(p, x)) {
         if (!(ok = wait_warp(&bars[kBarQFull], pieces & 1))) break;
         tc_fence_after();
-        qk(g, x.k0 + 1 == x.k1);
+        qk(g);
         for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
-          if (k + 1 < x.k1) qk(g + 1, k + 2 == x.k1);
+          if (k + 1 < x.k1) qk(g + 1);
           if (!ok || aborted() || !(ok = wait_warp(&bars[kBarP], g & 1))) break;
           if (k == x.k0 && pieces > 0 && !(ok = wait_warp(&bars[kBarO], (pieces - 1) & 1))) break;
           tc_fence_after();
@@ -658,61 +678,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // TMEM and shared memory go away: an arrival at a CTA that has ended is a fault.
     if (len > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit)))
       report_status(p.status, kStatusTimeout);
-  } else if (warp < kLoadWarp + kLoadWarps) {
+  } else if (warp < kLoadWarp + kSlots) {
     // =================== keys and values ============================================
-    // Warp w brings the key chunks j with j % 4 == w (64 columns of the CTA's 128 keys) and the value
-    // chunks w and 4 + w (128 columns of the tile's w-th 64 keys), in boxes of `box` rows, or row by row
-    // where the block size has no such power of two.  A lane looks up the place of a box (of four rows), a
-    // tile ahead; an elected lane issues the loads.
-    // A wait for a slot's round r is by parity, so it takes round r - 2 for done where that is all that is:
-    // a warp's chunks lie at most 5 places apart, and the wait for one of them says that every chunk up to
-    // kSlots places before it has been read, so the next one's slot is at most one round behind.
-    static_assert(kSlots >= 5, "the distance of a warp's chunks");
-    const int w = warp - kLoadWarp;
+    // Warp s fills slot s of the ring, every kSlots-th chunk of the order: it works out where its next chunk
+    // lies while it waits for the slot, so a slot is asked for again ~200 cycles after it was read (four
+    // warps that took chunks by turns: 400 to 1000).  Each waits for every round of its slot, so that a wait
+    // by parity cannot take an older round for its own.
+    const int slot = warp - kLoadWarp;
     const int step = tp.box ? tp.box : 4, k_boxes = 128 / step, v_boxes = 64 / step;
-    const uint32_t full0 = mapa(&bars[kBarFull], 0), ring = smem_u32(smem + kOffRing);
+    const uint32_t full = mapa(&bars[kBarFull + slot], 0), dst = smem_u32(smem + kOffRing + slot * kChunk);
     bool ok = true, bad = false;
-    const int32_t* table = nullptr;
-    int end = 0;
-    // Where a lane's next box (of `step` rows; without boxes, of four rows found one by one) lies: moved on by
-    // a tile at a time, without divisions, and its table entries loaded a tile ahead.
-    struct Place { int blk, off, left, e[4]; };
-    const int tile_blk = kTile / p.block_size, tile_off = kTile % p.block_size;
-    const bool mine = lane < k_boxes;
-    auto load_entries = [&](Place& q) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) q.e[u] = -1;
-      if (!mine || q.left <= 0) return;
-      if (q.blk < p.max_blocks) q.e[0] = table[q.blk];
-      if (tp.box) return;
-      int blk = q.blk, off = q.off;
-#pragma unroll
-      for (int u = 1; u < 4; ++u) {
-        if (++off == p.block_size) {
-          off = 0;
-          ++blk;
-        }
-        if (u < q.left && blk < p.max_blocks) q.e[u] = table[blk];
-      }
-    };
-    auto place_at = [&](long long pos) {
-      Place q;
-      q.blk = (int)(pos / p.block_size);
-      q.off = (int)(pos % p.block_size);
-      q.left = (int)max((long long)end - pos, -1ll);
-      load_entries(q);
-      return q;
-    };
-    auto next_tile = [&](Place& q) {
-      q.blk += tile_blk;
-      q.off += tile_off;
-      if (q.off >= p.block_size) {
-        q.off -= p.block_size;
-        ++q.blk;
-      }
-      q.left = max(q.left, 0) - kTile;
-      load_entries(q);
-    };
+    int round = 0, group = 0, r = slot;        // r-th chunk of the piece's group (K or V of a tile)
     // no block for the positions [pos, pos + n): that matters where a node attends to one of them
     auto missed = [&](int pos, int n) {
       for (int u = 0; u < n && !bad; ++u) {
@@ -722,128 +698,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bad = p.mask[(size_t)(x.first + i) * p.words + j / 64] >> (j % 64) & 1;
       }
     };
-    // cache rows of a place; rows that do not exist are the row behind the last, which loads as zeros
-    struct Rows { int r[4], n; };
-    auto rows_of = [&](const Place& q) {
-      Rows y;
-      y.n = mine ? min(max(q.left, 0), step) : 0;
+    bool more = walk.next(p, x);
+    while (more) {
+      // groups of a piece of t tiles: K(0), K(1), V(0), ..., K(t - 1), V(t - 2), V(t - 1)
+      const int t = x.k1 - x.k0;
+      const bool is_k = group == 0 || ((group & 1) && group < 2 * t - 1);
+      const int count = is_k ? kKChunks : kVChunks;
+      if (r >= count) {
+        r -= count;
+        if (++group == 2 * t) {
+          if (bad) mark_bad(x.request);
+          bad = false;
+          group = 0;
+          more = walk.next(p, x);
+        }
+        continue;
+      }
+      const int tile = x.k0 + (is_k ? (group + 1) / 2 : group == 2 * t - 1 ? t - 1 : group / 2 - 1);
+      // the lane's box: `step` rows from `pos` on; of V with boxes of 64 rows, one lane brings 128 columns
+      const int boxes = is_k ? k_boxes : v_boxes == 1 ? 1 : 2 * v_boxes;
+      const int at = (is_k ? lane : lane % v_boxes) * step;
+      const long long pos = (long long)tile * kTile + (is_k ? 128 * (int)rank : 64 * (r & 3)) + at;
+      const int col = is_k ? 64 * r : 256 * (int)rank + 128 * (r >> 2) + 64 * (lane / v_boxes);
+      const uint32_t to = dst + (is_k ? 0 : lane / v_boxes * 8192) + at * 128;
+      const int n = lane < boxes ? (int)min(max((long long)x.cached + x.n - pos, 0ll), (long long)step) : 0;
+      const int32_t* table = p.block_table + (size_t)x.request * p.max_blocks;
+      // its cache rows; those that do not exist are the row behind the last, which loads as zeros
+      int row[4], have = n;
 #pragma unroll
-      for (int u = 0; u < 4; ++u) y.r[u] = tp.num_rows;
-      if (tp.box) {
-        if ((uint32_t)q.e[0] < (uint32_t)p.num_blocks) {
-          y.r[0] = q.e[0] * p.block_size + q.off;
-        } else if (y.n > 0) {
-          missed(end - q.left, y.n);
-          y.n = 0;
-        }
-      } else {
-        int off = q.off;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if ((uint32_t)q.e[u] < (uint32_t)p.num_blocks) y.r[u] = q.e[u] * p.block_size + off;
-          else if (u < y.n) missed(end - q.left + u, 1);
-          if (++off == p.block_size) off = 0;
+      for (int u = 0; u < 4; ++u) {
+        row[u] = tp.num_rows;
+        if (u == 0 ? n > 0 : !tp.box && u < n) {
+          const uint32_t q = (uint32_t)(pos + u), blk = q / (uint32_t)p.block_size;   // (below 2^31 + 256)
+          const int phys = blk < (uint32_t)p.max_blocks ? table[blk] : -1;
+          if ((uint32_t)phys < (uint32_t)p.num_blocks) {
+            row[u] = phys * p.block_size + (int)(q - blk * (uint32_t)p.block_size);
+          } else {
+            missed((int)(pos + u), tp.box ? n : 1);
+            if (tp.box) have = 0;
+          }
         }
       }
-      return y;
-    };
-    // Every lane with a place brings it, in one instruction (a loop over an elected lane's loads took half as
-    // long again); where the sequence ends in a box, its rows four at a time, with zeros behind the end.
-    auto bring = [&](uint32_t dst, int col, const Rows& q, bool cut, uint32_t bar) {
-      if (!tp.box) {
-        if (mine) load_rows4(dst, &map_row, col, q.r[0], q.r[1], q.r[2], q.r[3], bar);
-        return;
+      const bool cut = __any_sync(0xffffffffu, tp.box && have != 0 && have != step);
+      if (round > 0 && (aborted() || !wait_warp(&bars[kBarEmpty + slot], (round - 1) & 1))) {
+        ok = false;
+        break;
       }
-      const bool whole = !cut || q.n == step || q.n == 0;
-      if (mine && whole) load_box(dst, &map_box, col, q.r[0], bar);
-      if (cut) {
-        __syncwarp();
-        for (int a = 0; a < step; a += 4) {
-          auto at = [&](int u) { return a + u < q.n ? q.r[0] + a + u : tp.num_rows; };
-          if (mine && !whole) load_rows4(dst + a * 128, &map_row, col, at(0), at(1), at(2), at(3), bar);
-          __syncwarp();
-        }
-      }
-    };
-    // the warp's next chunk, `ahead` places behind its last one: its slot, once that is free
-    int slot = -1;
-    uint32_t round = 0;
-    auto take = [&](int ahead) -> bool {
-      slot += ahead;
-      if (slot >= kSlots) {
-        slot -= kSlots;
-        ++round;
-      }
-      if (round > 0 && !wait_warp(&bars[kBarEmpty + slot], (round - 1) & 1)) return false;
       if (rank == 0) {
         if (lane == 0) mbar_arrive_expect_tx(&bars[kBarFull + slot], 2 * kChunk);
         __syncwarp();
       }
-      return true;
-    };
-    const uint32_t k_dst = ring + lane * step * 128;
-    const uint32_t v_dst = ring + lane / v_boxes * 8192 + lane % v_boxes * step * 128;
-    const int v_col = 256 * (int)rank + 64 * (lane / v_boxes);
-    int ahead = w + 1;                         // from the warp's last chunk to its next
-    auto keys = [&](const Rows& q) {
-      const bool cut = __any_sync(0xffffffffu, q.n != 0 && q.n != step);
-      for (int j = w; ok && j < kKChunks; j += kLoadWarps) {
-        if (!(ok = take(ahead))) break;
-        bring(k_dst + slot * kChunk, 64 * j, q, cut, full0 + 8 * slot);
-        ahead = kLoadWarps;
-      }
-      ahead = w == 0 ? 1 : kKChunks - kLoadWarps;   // keys w, w + 4 (, 8), then whatever begins behind them
-    };
-    auto values = [&](const Rows& q) {
-      const bool cut = __any_sync(0xffffffffu, q.n != 0 && q.n != step);
-      for (int h = 0; ok && h < 2; ++h) {
-        if (!(ok = take(ahead))) break;
-        bring(v_dst + slot * kChunk, v_col + 128 * h, q, cut, full0 + 8 * slot);
-        ahead = kLoadWarps;
-      }
-    };
-    while (ok && walk.next(p, x)) {
-      table = p.block_table + (size_t)x.request * p.max_blocks;
-      end = (int)min((long long)x.cached + x.n, 0x7fffffffll);
-      // ahead of the loop: the first tile's keys; in it, the next tile's keys, then the values.  A kind's rows
-      // are worked out, and the entries behind them asked for, before its first wait for a slot.
-      const long long p0 = (long long)x.k0 * kTile;
-      Place kp = place_at(p0 + 128 * (int)rank + lane * step), vp = place_at(p0 + 64 * w + lane % v_boxes * step);
-      Rows kr = rows_of(kp);
-      next_tile(kp);
-      keys(kr);
-      for (int k = x.k0; ok && k < x.k1; ++k) {
-        if (aborted()) ok = false;
-        if (k + 1 < x.k1) {
-          kr = rows_of(kp);
-          next_tile(kp);
-          keys(kr);
+      // every lane with a box in one instruction (a loop over an elected lane's took half as long again);
+      // where the sequence ends in a box, its rows four at a time, with zeros behind the end
+      const bool two = !is_k && v_boxes == 1;
+      if (!tp.box) {
+        if (lane < boxes) load_rows4(to, &map_row, col, row[0], row[1], row[2], row[3], full);
+      } else if (!cut) {
+        if (two) {
+          if (lane == 0) load_box2(to, &map_two, row[0], col / 64, full);
+        } else if (lane < boxes) {
+          load_box(to, &map_box, col, row[0], full);
         }
-        const Rows vr = rows_of(vp);
-        next_tile(vp);
-        values(vr);
-      }
-      if (bad) {
-        mark_bad(x.request);
-        bad = false;
+      } else {
+        const bool whole = have == 0 || have == step;
+        for (int c = 0; c < (two ? 2 : 1); ++c) {
+          if (lane < boxes && whole) load_box(to + c * 8192, &map_box, col + 64 * c, row[0], full);
+          __syncwarp();
+          for (int a = 0; a < step; a += 4) {
+            auto row_at = [&](int u) { return a + u < have ? row[0] + a + u : tp.num_rows; };
+            if (lane < boxes && !whole)
+              load_rows4(to + c * 8192 + a * 128, &map_row, col + 64 * c, row_at(0), row_at(1), row_at(2), row_at(3), full);
+            __syncwarp();
+          }
+        }
       }
       __syncwarp();
+      ++round;
+      r += kSlots;
     }
     if (!ok) fail();
-  } else {
-    // =================== q ==============================================================
-    if (lane == 0) {
-      bool ok = true;
-      const uint32_t qfull = mapa(&bars[kBarQFull], 0);
-      for (int i = 0; ok && walk.next(p, x); ++i) {
-        if (*abort_s) break;
-        if (i > 0 && !(ok = mbar_wait(&bars[kBarQEmpty], (i - 1) & 1, wl))) break;
-        if (rank == 0) mbar_arrive_expect_tx(&bars[kBarQFull], 2 * kQBytes);
-        for (int j = 0; j < 9; ++j)
-          load_box(smem_u32(smem + j * kQBlk), &map_q, 64 * j, x.row0 + kHalf * (int)rank, qfull);
-      }
-      if (!ok) fail();
-    }
   }
 
   // ---- teardown
@@ -981,12 +914,13 @@ cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
   while (p.block_size % tp.box != 0) tp.box /= 2;
   if (tp.box < 8) tp.box = 0;
   lay_out(static_cast<char*>(p.workspace), tp.pairs, rows_of_slot((long long)p.T * p.h), tp.ws);
-  CUtensorMap box, row, q;
+  CUtensorMap box, two, row, q;
   if (!make_rows_map(&box, p.kv, tp.num_rows, tp.box ? tp.box : 8) || !make_rows_map(&row, p.kv, tp.num_rows, 1) ||
+      !make_blocks_map(&two, p.kv, tp.num_rows, 64, 2) ||
       !make_rows_map(&q, p.q, (long long)p.T * p.h, kHalf))
     return cudaErrorInvalidValue;
   const auto kernel = p.out_bf16 ? decode_tree_kernel<false> : decode_tree_kernel<true>;
-  kernel<<<2 * tp.pairs, kThreads, kSmem, stream>>>(box, row, q, tp);
+  kernel<<<2 * tp.pairs, kThreads, kSmem, stream>>>(box, two, row, q, tp);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   join_tree_kernel<<<dim3(tp.pairs, kJoinRows), kJoinThreads, kFixSmem, stream>>>(tp);
