@@ -740,7 +740,7 @@ sfa_status sfa_decode_tree(const void* q, const void* kv, const int32_t* block_t
 
 size_t sfa_decode_tree_workspace_bytes(int B, int num_tokens, int h) {
   if (B <= 0 || num_tokens <= 0 || h <= 0 || h > SFA_MAX_HEADS) return 0;
-  return sfa::tree_workspace_bytes(num_tokens, h);
+  return sfa::tree_workspace_bytes(B, num_tokens, h);
 }
 
 sfa_status sfa_blocks_fork(int32_t* block_table, int rows, int max_blocks_per_seq, int32_t* lens, const int32_t* src,

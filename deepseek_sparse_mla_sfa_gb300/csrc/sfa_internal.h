@@ -172,7 +172,7 @@ cudaError_t launch_kv_commit(void* kv, int layers, int num_blocks, int block_siz
                              int B, int max_nodes, int* status, cudaStream_t stream);
 cudaError_t launch_decode_tree_simt(const TreeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream);   // the tcgen05 kernel
-size_t tree_workspace_bytes(int T, int h);                                  // of the current device
+size_t tree_workspace_bytes(int B, int T, int h);                                  // of the current device
 // rows of 576 bf16 (q's or the cache's), boxes of 64 columns x box_rows rows, 128-byte swizzle;
 // remembered per host thread
 bool make_rows_map(CUtensorMap* m, const void* base, long long num_rows, int box_rows);

@@ -25,14 +25,13 @@
 // next tile covers the softmax of this one.  The value columns of the CTA's own keys come twice (as
 // keys and as values); the second time is from L2, which gives 180 GB/s an SM where the ring takes 130.
 //
-// Split.  Units in order of requests, each as long as its tiles (and kUnitCost for its start), are cut
-// into equal ranges, one for each pair; a unit that a cut goes through leaves partial results in the
-// workspace, which the second kernel joins.  A cut never goes through the tiles that hold nodes.
-//
+// Three launches: a block that lays out who works on what (the schedule, below), the pairs, and the joining
+// of units that several pairs had parts of.
+
 // Rows that nobody may see.  Positions behind the last node are brought as rows of zeros.  A cached row
 // of NaN or infinities that only some nodes see would reach the others as 0 x NaN in P V: such a row
 // shows as a score that is not finite in a masked place; the loading warps see a position that a node
-// attends to and that has no block.  Both mark the request, and the second kernel computes its nodes on CUDA
+// attends to and that has no block.  Both mark the request, and the last kernel computes its nodes on CUDA
 // cores, which reads only what a node attends to.
 //
 // Warps (512 threads): 0-7 softmax, rescaling, output (the first thread brings q); 8 issues the MMAs (in
@@ -57,6 +56,7 @@ constexpr int kKChunks = 9, kVChunks = 8;      // of a tile
 constexpr int kChunk = 16384;
 constexpr int kUnitCost = 1;                   // of starting a unit, in tiles
 constexpr int kMinSpan = 3;                    // tiles a pair gets at least
+constexpr int kMaxPairs = 128, kMaxSlots = 4 * kMaxPairs;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleThreshold = 8.0f;      // log2 units: weights stay below 2^8
@@ -73,31 +73,37 @@ struct Ring {
   static_assert(kOff % 1024 == 0 && kOff + kSlots * kChunk == kOffP + kPBytes + 7 * kChunk, "the ring fills the rest");
 };
 constexpr int kOffMx = kOffP + kPBytes + 7 * kChunk;     // float [2][256]: row maxima, then sums
-constexpr int kOffScan = kOffMx + 2048;                  // long long [kThreads / 32], then int [8]
-constexpr int kOffBar = kOffScan + 8 * 16 + 32;
+constexpr int kOffBar = kOffMx + 2048;
 constexpr int kBarFull = 0, kBarEmpty = 7, kBarQFull = 14, kBarS = kBarQFull + 1, kBarP = kBarS + 2, kBarPv = kBarP + 1, kBarO = kBarPv + 1,
               kBarMx = kBarO + 1, kBarFin = kBarMx + 2, kBarNever = kBarFin + 1, kNumBars = kBarNever + 1;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;         // TMEM address, abort, bad range
 constexpr int kSmem = kOffMisc + 64 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
-static_assert(kOffBar % 8 == 0 && kThreads / 32 <= 16, "alignment, room for the sums");
+static_assert(kOffBar % 8 == 0, "alignment");
 
 constexpr uint32_t kTmemCols = 512, kColO = 0, kColS = 256;
 constexpr long long kDrainLimit = 1LL << 40;
 
-// what the second kernel needs to know of a pair's partial results
-struct Record {
-  int head_row, head_rows, head_request;   // a unit that begins here and goes on in the next pair: slot 2k + 1
-  int tail_row, tail_ends;                 // a unit that began before: slot 2k; whether it ends here
-  int pad[3];
+// A part of a unit that one pair works through: its query rows and its tiles [k0, k1).
+struct alignas(16) Piece {
+  int row0, rows, k0, k1;
+  int request, cached, n, first;       // the request, its cached positions, nodes and first token
+  int slot, pad[3];                    // of its partial result; -1: the piece is the whole unit
+};
+// a partial result: a unit's rows, and whether it has the unit's first tile
+struct alignas(16) Partial {
+  int row0, rows, request, begins;
 };
 
 struct Workspace {
-  float* part;       // [2 * pairs][cap][512]
-  float* lse;        // [2 * pairs][cap]
-  Record* rec;       // [pairs]
+  Piece* pieces;     // of pair k: [start[k], start[k + 1])
+  int* start;        // [pairs + 1]
+  int* partials;     // [1]: slots in use
+  Partial* list;     // [slots]
+  float* part;       // [slots][cap][512]
+  float* lse;        // [slots][cap]
   int2* bad;         // [2 * pairs]: requests to compute again, first and last
-  int cap;           // rows of a slot
+  int cap, slots;    // rows of a slot, slots
 };
 
 struct TreeTcParams {
@@ -188,115 +194,305 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 }
 
 // ---------------------------------------------------------------- the schedule
+// One block lays out the pieces of every pair.  Units in order of requests make an axis, each as long as
+// its tiles and kUnitCost for its start; pair k gets the range [k span, (k + 1) span).  A cut never goes
+// through the tiles that hold nodes, so that one piece sees all masks.
+//
+// Where requests have several units and their rows together do not stay in L2, ranges alone would have each
+// unit of a request read the rows at another time (16 requests x 16 units x 8192 positions read 2.4 GB
+// from memory, not 0.15).  There the units of a request first come as chunks of about `limit` tiles, in
+// the order (request, chunk, unit), and are dealt to the pairs one by one, so that neighbouring pairs read
+// the same rows at the same time; what is left of the last, unfilled round goes to ranges that even out
+// what the dealt chunks left uneven.
+constexpr int kPlanThreads = 512;
+constexpr int kDealRequests = 256;             // requests that chunks are dealt of
+constexpr int kFarTiles = 240;                 // tiles (256 rows of 1152 bytes) that stay in L2: 70 MB
+constexpr int kWhole = 0x7fffffff;             // `limit` that cuts nothing
+
 struct Request {
   int first, n, cached, tiles, cuts;   // cuts: tiles without nodes, behind each of which a cut may go
-  long long cost;                      // of all its units
+  int units, chunks, len;              // chunks of a unit, their tiles (the last one's may differ)
+  __device__ __forceinline__ int tasks() const { return units * chunks; }
+  __device__ __forceinline__ int cost() const { return len + kUnitCost; }   // of a task
+  // where the axis' place v of a unit's tiles may be cut
+  __device__ __forceinline__ int cut(int v) const { return v > cuts ? tiles : max(v, 0); }
 };
-__device__ __forceinline__ Request request_of(const TreeParams& p, int b) {
+__device__ __forceinline__ Request request_of(const TreeParams& p, int b, int limit = kWhole) {
   Request r;
   r.first = min(max(p.token_start[b], 0), p.T);
   r.n = min(min(max(p.token_start[b + 1], r.first), p.T) - r.first, p.max_nodes);
   r.cached = max(p.cached[b], 0);
   r.tiles = (int)(((long long)r.cached + r.n + kTile - 1) / kTile);
   r.cuts = r.cached / kTile;
-  r.cost = r.n > 0 ? (long long)((r.n * p.h + kRows - 1) / kRows) * (r.tiles + kUnitCost) : 0;
+  r.units = r.n > 0 ? (r.n * p.h + kRows - 1) / kRows : 0;
+  r.chunks = 1;
+  r.len = r.tiles;
+  if (r.tiles > limit) {
+    r.len = (r.tiles + (r.tiles + limit - 1) / limit - 1) / ((r.tiles + limit - 1) / limit);
+    r.chunks = min(r.cuts / r.len + 1, (r.tiles + r.len - 1) / r.len);   // none begins behind the last cut
+  }
   return r;
 }
 
-struct Piece {
-  int row0, rows, k0, k1, tiles;       // query rows; the tiles [k0, k1) of `tiles`
-  int request, cached, n, first, node_row;   // node_row: row0 within the request
+struct Plan {
+  int limit, rounds;                   // chunks dealt: `rounds` to every pair
+  int dealt;                           // rounds * pairs
 };
 
-// the pieces of one pair's range, in order
-struct Walk {
-  int b;
-  long long off, left;
-  Request r;
-  __device__ __forceinline__ void start(const TreeParams& p, int b0, long long off0, long long n) {
-    b = b0;
-    off = off0;
-    left = n;
-    if (left > 0) r = request_of(p, b);
-  }
-  __device__ __forceinline__ bool next(const TreeParams& p, Piece& x) {
-    while (left > 0) {
-      if (off >= r.cost) {
-        if (++b >= p.B) return false;
-        r = request_of(p, b);
-        off = 0;
-        continue;
-      }
-      const int unit = r.tiles + kUnitCost;
-      const int m = (int)(off / unit), u = (int)(off % unit);
-      const int take = (int)min(left, (long long)(unit - u));
-      off += take;
-      left -= take;
-      auto cut = [&](int v) { return v <= 0 ? 0 : v > r.cuts ? r.tiles : v; };
-      x.k0 = cut(u - kUnitCost);
-      x.k1 = cut(u + take - kUnitCost);
-      if (x.k1 <= x.k0) continue;
-      x.tiles = r.tiles;
-      x.node_row = m * kRows;
-      x.row0 = r.first * p.h + x.node_row;
-      x.rows = min(kRows, r.n * p.h - x.node_row);
-      x.request = b;
-      x.cached = r.cached;
-      x.n = r.n;
-      x.first = r.first;
-      return true;
+// the pieces of one pair, in order: f(request number, request, unit, k0, k1)
+template <class F>
+__device__ __forceinline__ void walk_pair(const TreeParams& p, const Plan& plan, const int* tasks_before, int pair,
+                                          int pairs, int b, long long off, long long left, F f) {
+  auto piece = [&](int bb, const Request& r, int task, int from, int to) {   // places [from, to) of a task
+    const int begin = task / r.units * r.len;
+    const bool last = task / r.units == r.chunks - 1;
+    const int end = last ? r.tiles : r.cut(begin + r.len);
+    const int k0 = max(r.cut(begin + from - kUnitCost), begin);
+    const int k1 = to >= r.cost() ? end : min(max(r.cut(begin + to - kUnitCost), begin), end);
+    if (k1 > k0) f(bb, r, task % r.units, k0, k1);
+  };
+  for (int i = 0; i < plan.rounds; ++i) {
+    const int t = pair + i * pairs;
+    int lo = 0, hi = p.B;                      // the last request with tasks_before <= t
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tasks_before[mid] <= t) lo = mid; else hi = mid;
     }
-    return false;
+    const Request r = request_of(p, lo, plan.limit);
+    piece(lo, r, t - tasks_before[lo], 0, r.cost());
   }
-};
+  if (left <= 0) return;
+  Request r = request_of(p, b, plan.limit);
+  auto skipped = [&] { return plan.dealt ? min(max(plan.dealt - tasks_before[b], 0), r.tasks()) : 0; };
+  int skip = skipped();
+  while (left > 0) {
+    if (off >= (long long)(r.tasks() - skip) * r.cost()) {
+      if (++b >= p.B) return;
+      r = request_of(p, b, plan.limit);
+      skip = skipped();
+      off = 0;
+      continue;
+    }
+    const int c = r.cost(), task = (int)(off / c), u = (int)(off % c);
+    const int take = (int)min(left, (long long)(c - u));
+    off += take;
+    left -= take;
+    piece(b, r, skip + task, u, u + take);
+  }
+}
 
-// Shared by the CTA: where its pair's range starts.  Every CTA sums the requests' costs itself.
-__device__ __forceinline__ void find_range(const TreeParams& p, int pair, int pairs, char* smem, int& b0,
-                                           long long& off0, long long& len) {
-  long long* part = reinterpret_cast<long long*>(smem + kOffScan);
-  int* found = reinterpret_cast<int*>(smem + kOffScan + 8 * 16);
-  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
-  long long mine = 0;
-  for (int b = r0; b < r1; ++b) {
-    mine += request_of(p, b).cost;
-    if (pair == 0 && min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
-      report_status(p.status, kStatusBadTree);
-  }
-  long long in = mine;
+__device__ __forceinline__ long long block_sum(long long v, long long* part) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  long long t = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) t += part[w];
+  return t;
+}
+// the sum over the threads before
+__device__ __forceinline__ long long block_before(long long v, long long* part, long long& total) {
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  long long in = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long u = __shfl_up_sync(0xffffffffu, in, o);
     if (lane >= o) in += u;
   }
-  if (lane == 31) part[warp] = in;
-  if (tid == 0) found[0] = -1;
   __syncthreads();
-  long long at = in - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) at += part[w];
+  if (lane == 31) part[warp] = in;
+  __syncthreads();
+  long long before = in - v;
+  total = 0;
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += part[w];
     total += part[w];
   }
-  const long long span = max((total + pairs - 1) / pairs, (long long)kMinSpan);
-  const long long lo = min(pair * span, total), hi = min(lo + span, total);
-  if (lo < hi && lo >= at && lo < at + mine) {
-    long long a = at;
-    for (int b = r0; b < r1; ++b) {
-      const long long c = request_of(p, b).cost;
-      if (lo < a + c) {
-        found[0] = b;
-        *reinterpret_cast<long long*>(found + 2) = lo - a;
-        break;
+  return before;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeTcParams tp) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ long long part[kPlanThreads / 32];
+  __shared__ int tasks_before[kDealRequests + 1];
+  __shared__ int load[kMaxPairs], begin_b[kMaxPairs];
+  __shared__ long long cost_before[kPlanThreads];
+  __shared__ long long share_at[kMaxPairs + 1], begin_off[kMaxPairs];   // where the pairs' ranges lie
+  const TreeParams& p = tp.p;
+  const int tid = threadIdx.x, pairs = tp.pairs;
+  const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
+  const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
+  Plan plan{kWhole, 0, 0};
+  long long cost = 0, tiles = 0, far = 0;      // of the units; their tiles; tiles of different rows
+  for (int b = r0; b < r1; ++b) {
+    const Request r = request_of(p, b);
+    cost += (long long)r.units * r.cost();
+    tiles += (long long)r.units * r.tiles;
+    far += r.units > 0 ? r.tiles : 0;
+    if (min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
+      report_status(p.status, kStatusBadTree);
+  }
+  if (p.B <= kDealRequests) {
+    tiles = block_sum(tiles, part);
+    far = block_sum(far, part);
+    if (far > kFarTiles && 2 * tiles >= 3 * far) {
+      // whole units, or chunks that make a round or two; what is not dealt counts a third more
+      float best = 1e30f;
+      for (int c = 0; c < 3; ++c) {
+        const int limit = c == 0 ? kWhole : (int)min((tiles + c * pairs - 1) / (c * pairs), (long long)kWhole);
+        long long n = 0, all = 0, split = 0;
+        for (int b = r0; b < r1; ++b) {
+          const Request r = request_of(p, b, limit);
+          n += r.tasks();
+          all += (long long)r.tasks() * r.cost();
+          split += r.chunks > 1 ? r.tasks() : 0;
+        }
+        n = block_sum(n, part);
+        all = block_sum(all, part);
+        split = block_sum(split, part);
+        if (n < pairs || n > (1 << 24) || split + 2 * pairs > tp.ws.slots) continue;
+        const float done = (float)(n / pairs * pairs) / (float)n, t = (float)all * (done + 1.3f * (1.f - done));
+        if (t < best) {
+          best = t;
+          plan.limit = limit;
+          plan.rounds = (int)(n / pairs);
+          plan.dealt = plan.rounds * pairs;
+        }
       }
-      a += c;
     }
   }
+  if (plan.rounds > 0) {
+    // tasks before each request (one request a thread at most), what the dealt ones load each pair with
+    const Request r = tid < p.B ? request_of(p, tid, plan.limit) : Request{};
+    const int mine = tid < p.B ? r.tasks() : 0;
+    long long n;
+    const int before = (int)block_before(mine, part, n);
+    if (tid < p.B) tasks_before[tid] = before;
+    if (tid == 0) tasks_before[p.B] = (int)n;
+    if (tid < pairs) load[tid] = 0;
+    __syncthreads();
+    for (int i = tid; i < pairs * p.B; i += kPlanThreads) {
+      const int k = i % pairs, b = i / pairs;
+      const int lo = min(tasks_before[b], plan.dealt), hi = min(tasks_before[b + 1], plan.dealt);
+      const int count = (hi - 1 - k + pairs) / pairs - (lo - 1 - k + pairs) / pairs;   // tasks t = k mod pairs in [lo, hi)
+      if (count > 0) atomicAdd(&load[k], count * request_of(p, b, plan.limit).cost());
+    }
+    // the rest of the tasks, in cost: level the pairs
+    const int skip = min(max(plan.dealt - before, 0), mine);
+    cost = tid < p.B ? (long long)(mine - skip) * r.cost() : 0;
+    const long long rest = block_sum(cost, part);
+    __syncthreads();
+    if (tid < 32) {
+      long long lo = 0, hi = rest;             // the least level whose room is `rest`
+      for (int k = tid; k < pairs; k += 32) hi = max(hi, rest + load[k]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+      while (lo < hi) {
+        const long long mid = (lo + hi) >> 1;
+        long long room = 0;
+        for (int k = tid; k < pairs; k += 32) room += max(mid - load[k], 0ll);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) room += __shfl_xor_sync(0xffffffffu, room, o);
+        if (room >= rest) hi = mid; else lo = mid + 1;
+      }
+      if (tid == 0) {
+        long long at = 0;
+        for (int k = 0; k < pairs; ++k) {
+          share_at[k] = min(at, rest);
+          at += max(lo - load[k], 0ll);
+        }
+        share_at[pairs] = rest;
+      }
+    }
+    __syncthreads();
+  } else {
+    const long long total = block_sum(cost, part);
+    const long long span = max((total + pairs - 1) / pairs, (long long)kMinSpan);
+    if (tid <= pairs) share_at[tid] = min(tid * span, total);
+    __syncthreads();
+  }
+  // where the pairs' ranges begin
+  long long total;
+  cost_before[tid] = block_before(cost, part, total);
   __syncthreads();
-  b0 = found[0];
-  off0 = *reinterpret_cast<long long*>(found + 2);
-  len = b0 < 0 ? 0 : hi - lo;
+  if (tid < pairs) {
+    const long long from = share_at[tid];
+    begin_b[tid] = -1;
+    if (share_at[tid + 1] > from) {
+      int lo = 0, hi = kPlanThreads;           // the last thread with requests that begin at `from` or before
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (cost_before[mid] <= from) lo = mid; else hi = mid;
+      }
+      long long a = cost_before[lo];
+      for (int b = lo * per; b < min(lo * per + per, p.B); ++b) {
+        const Request r = request_of(p, b, plan.limit);
+        const int skip = plan.dealt ? min(max(plan.dealt - tasks_before[b], 0), r.tasks()) : 0;
+        const long long c = (long long)(r.tasks() - skip) * r.cost();
+        if (from < a + c) {
+          begin_b[tid] = b;
+          begin_off[tid] = from - a;
+          break;
+        }
+        a += c;
+      }
+    }
+  }
+  // count, then write
+  int pieces = 0, partials = 0;
+  const bool have = tid < pairs;
+  auto pair_walk = [&](auto f) {
+    if (have)
+      walk_pair(p, plan, tasks_before, tid, pairs, begin_b[tid], begin_off[tid],
+                begin_b[tid] < 0 ? 0 : share_at[tid + 1] - share_at[tid], f);
+  };
+  pair_walk([&](int, const Request& r, int, int k0, int k1) {
+    ++pieces;
+    partials += !(k0 == 0 && k1 == r.tiles);
+  });
+  long long all_pieces, all_partials;
+  int at_piece = (int)block_before(pieces, part, all_pieces), at_partial = (int)block_before(partials, part, all_partials);
+  if (have) tp.ws.start[tid] = at_piece;
+  if (tid == 0) {
+    tp.ws.start[pairs] = (int)all_pieces;
+    *tp.ws.partials = (int)all_partials;
+  }
+  pair_walk([&](int b, const Request& r, int unit, int k0, int k1) {
+    Piece x;
+    x.row0 = r.first * p.h + unit * kRows;
+    x.rows = min(kRows, r.n * p.h - unit * kRows);
+    x.k0 = k0;
+    x.k1 = k1;
+    x.request = b;
+    x.cached = r.cached;
+    x.n = r.n;
+    x.first = r.first;
+    x.slot = -1;
+    x.pad[0] = x.pad[1] = x.pad[2] = 0;
+    if (!(k0 == 0 && k1 == r.tiles)) {
+      x.slot = at_partial;
+      tp.ws.list[at_partial++] = Partial{x.row0, x.rows, b, k0 == 0};
+    }
+    tp.ws.pieces[at_piece++] = x;
+  });
 }
+
+// a pair's pieces, one after the other
+struct Walk {
+  const Piece* at;
+  const Piece* end;
+  __device__ __forceinline__ bool next(Piece& x) {
+    if (at >= end) return false;
+    int4* to = reinterpret_cast<int4*>(&x);
+    const int4* from = reinterpret_cast<const int4*>(at++);
+    to[0] = __ldcg(from);
+    to[1] = __ldcg(from + 1);
+    to[2] = __ldcg(from + 2);
+    return true;
+  }
+};
 
 // bits [d, d + 64) of the positions that a node attends to, counted from the first node's: all
 // before it, its mask among the n nodes, none behind
@@ -360,15 +556,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tmap(&map_two);
     prefetch_tmap(&map_q);
   }
-  int b0;
-  long long off0, len;
-  find_range(p, pair, tp.pairs, smem, b0, off0, len);
+  asm volatile("griddepcontrol.launch_dependents;");
+  __syncwarp();
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = *tmem_s;
-  Walk walk;
-  walk.start(p, b0, off0, len);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the schedule is there
+  const int begin = __ldcg(tp.ws.start + pair), len = __ldcg(tp.ws.start + pair + 1) - begin;
+  Walk walk{tp.ws.pieces + begin, tp.ws.pieces + begin + len};
   Piece x;
 
   auto fail = [&] {
@@ -410,8 +606,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // masked scores are -inf, and -inf times a zero scale would be NaN: any valid score times 1e-30
     // still has weight 1
     const float c_abs = fmaxf(fabsf(c_scale), 1e-30f);
-    Record* rec = tp.ws.rec + pair;
-    if (tid == 0 && rank == 0) rec->head_row = rec->tail_row = -1;
     int g = 0, swaps = 0;
     bool ok = true;
     // the values of the three threads with the rest of the row
@@ -435,13 +629,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         load_box(smem_u32(smem + j * kQBlk), &map_q, 64 * j, y.row0 + kHalf * (int)rank, q_full);
     };
     Piece y;
-    bool more = walk.next(p, y);
+    bool more = walk.next(y);
     if (more) bring_q(y);
     while (ok && more) {
       x = y;
       float m_ref = -INFINITY, l_sum = 0.f, u[3];
       const bool live = row < x.rows;
-      const int node = live ? (x.node_row + row) / p.h : 0;
+      const int node = live ? (x.row0 + row) / p.h - x.first : 0;
       const long long* words = p.mask + (size_t)(x.first + node) * p.words;
       for (int k = x.k0; k < x.k1; ++k, ++g) {
         const int bb = g & 1;
@@ -532,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (lane == 0) arrive_first(p_ready);
       }
       if (!ok) break;
-      more = walk.next(p, y);
+      more = walk.next(y);
       if (more) bring_q(y);
       // ---- the piece's result
       others(l_sum, u);
@@ -542,15 +736,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool none = l == 0.f;
       const float inv = none ? 0.f : 1.f / l;
       const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
-      const bool whole = x.k0 == 0 && x.k1 == x.tiles, head = x.k0 == 0;
-      const int slot = 2 * pair + (head ? 1 : 0);
+      const bool whole = x.slot < 0;
       // A warp's 32 rows go through its own 4 KB of P, 128 bytes a row at a time, so that eight lanes write
       // a row's 128 bytes (a row a lane, 16 bytes a store, took 17000 cycles a piece)
       const bool as16 = whole && p.out_bf16;
       char* stage = smem + kOffP + (2 * half + part) * kQBlk + (warp & 1) * 32 * 128;
       const int row0 = kHalf * (int)rank + (warp & 1) * 32;         // the warp's first row
       char* to = whole ? static_cast<char*>(p.out) + (size_t)(x.row0 + row0) * kDV * (as16 ? 2 : 4)
-                       : reinterpret_cast<char*>(tp.ws.part + ((size_t)slot * tp.ws.cap + row0) * kDV);
+                       : reinterpret_cast<char*>(tp.ws.part + ((size_t)x.slot * tp.ws.cap + row0) * kDV);
       const int pitch = kDV * (as16 ? 2 : 4), left = x.rows - row0;
       to += (256 * half + 128 * part) * (as16 ? 2 : 4);
       const int wide = as16 ? 64 : 32;                              // columns of 128 bytes
@@ -588,17 +781,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (live && half == 0 && part == 0) {
         if (whole) p.lse[x.row0 + row] = lse;
-        else tp.ws.lse[(size_t)slot * tp.ws.cap + row] = lse;
-      }
-      if (tid == 0 && rank == 0 && !whole) {
-        if (head) {
-          rec->head_rows = x.rows;
-          rec->head_request = x.request;
-          rec->head_row = x.row0;
-        } else {
-          rec->tail_ends = x.k1 == x.tiles;
-          rec->tail_row = x.row0;
-        }
+        else tp.ws.lse[(size_t)x.slot * tp.ws.cap + row] = lse;
       }
       tc_fence_before();
       __syncwarp();
@@ -647,7 +830,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       };
-      while (ok && all(walk.next(p, x))) {
+      while (ok && all(walk.next(x))) {
         if (!(ok = wait_warp(&bars[kBarQFull], pieces & 1))) break;
         tc_fence_after();
         qk(g);
@@ -710,7 +893,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           bad = p.mask[(size_t)(x.first + i) * p.words + j / 64] >> (j % 64) & 1;
       }
     };
-    bool more = walk.next(p, x);
+    bool more = walk.next(x);
     while (more) {
       // groups of a piece of t tiles: K(0), K(1), V(0), ..., K(t - 1), V(t - 2), V(t - 1)
       const int t = x.k1 - x.k0;
@@ -722,7 +905,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (bad) mark_bad(x.request);
           bad = false;
           group = 0;
-          more = walk.next(p, x);
+          more = walk.next(x);
         }
         continue;
       }
@@ -810,66 +993,112 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- joining, and the marked requests
-constexpr int kJoinThreads = 128, kJoinRows = 64;   // row chunks of a unit: blocks in y
+constexpr int kJoinThreads = 128;
 constexpr int kFixHeads = 2;
 
+// Blocks take the rows of the cut units by turns, a row four columns a thread.
 __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcParams tp) {
   extern __shared__ float smem_f[];
+  __shared__ int slots[kMaxSlots];             // a unit's parts
+  __shared__ int begins[kMaxSlots], rows_before[kMaxSlots + 1];   // partial results that begin a unit
+  __shared__ int sums[kJoinThreads / 32], n_parts;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const TreeParams& p = tp.p;
-  const int k = blockIdx.x, y = blockIdx.y, tid = threadIdx.x;
-  int any = 0, skip = 0;
-  const Record rec = tp.ws.rec[k];
-  for (int i = tid; i < 2 * tp.pairs; i += kJoinThreads) {
-    const int2 b = tp.ws.bad[i];
-    if (b.x <= b.y) {
-      any = 1;
-      if (rec.head_row >= 0 && b.x <= rec.head_request && rec.head_request <= b.y) skip = 1;
-    }
-  }
+  const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+  const int partials = min(*tp.ws.partials, tp.ws.slots);
+  int any = 0;
+  for (int j = tid; j < 2 * tp.pairs; j += kJoinThreads) any |= tp.ws.bad[j].x <= tp.ws.bad[j].y;
   any = __syncthreads_or(any);
-  if (any) skip = __syncthreads_or(skip);
-  if (rec.head_row >= 0 && !skip && rec.head_rows <= tp.ws.cap) {
-    int last = k;                              // the unit's pieces: slot 2k + 1, then 2j for k < j <= last
-    while (last + 1 < tp.pairs && tp.ws.rec[last + 1].tail_row == rec.head_row) {
-      ++last;
-      if (tp.ws.rec[last].tail_ends) break;
+  int n_begins = 0, n_rows = 0;
+  for (int j0 = 0; j0 < partials; j0 += kJoinThreads) {
+    const int j = j0 + tid;
+    const Partial x = j < partials ? tp.ws.list[j] : Partial{0, 0, 0, 0};
+    const int v = x.begins ? x.rows | 1 << 16 : 0;   // rows (at most 128 x 128 of a round) and a count
+    int in = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, in, o);
+      if (lane >= o) in += u;
     }
+    if (lane == 31) sums[warp] = in;
+    __syncthreads();
+    int before = in - v, all = 0;
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
+      if (w < warp) before += sums[w];
+      all += sums[w];
+    }
+    if (x.begins) {
+      begins[n_begins + (before >> 16)] = j;
+      rows_before[n_begins + (before >> 16)] = n_rows + (before & 0xffff);
+    }
+    n_begins += all >> 16;
+    n_rows += all & 0xffff;
+    __syncthreads();
+  }
+  int unit = -1, n = 0;
+  for (int it = blockIdx.x; it < n_rows; it += gridDim.x) {
+    int lo = 0, hi = n_begins;                 // the last unit that begins with this row or before
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (rows_before[mid] <= it) lo = mid; else hi = mid;
+    }
+    const Partial me = tp.ws.list[begins[lo]];
+    if (lo != unit) {                          // its parts, in the order of the slots: the same sums every time
+      unit = lo;
+      __syncthreads();
+      if (tid < 32) {
+        int k = 0;
+        for (int j0 = 0; j0 < partials; j0 += 32) {
+          const bool one = j0 + tid < partials && tp.ws.list[j0 + tid].row0 == me.row0;
+          const unsigned m = __ballot_sync(0xffffffffu, one);
+          if (one) slots[k + __popc(m & ((1u << tid) - 1))] = j0 + tid;
+          k += __popc(m);
+        }
+        if (tid == 0) n_parts = k;
+      }
+      __syncthreads();
+      n = n_parts;
+    }
+    bool skip = false;                         // all of the request is computed again below
+    if (any)
+      for (int j = 0; j < 2 * tp.pairs; ++j) skip |= tp.ws.bad[j].x <= me.request && me.request <= tp.ws.bad[j].y;
+    const int r = it - rows_before[lo], col = 4 * tid;
+    if (skip || r >= tp.ws.cap) continue;
     const size_t cap = tp.ws.cap;
-    for (int r = y; r < rec.head_rows; r += gridDim.y) {
-      const float* lse = tp.ws.lse + r;
-      auto slot = [&](int j) { return (size_t)(j == k ? 2 * k + 1 : 2 * j); };
-      float m = -INFINITY;
-      for (int j = k; j <= last; ++j) m = fmaxf(m, lse[slot(j) * cap]);
-      float sum = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int j = k; j <= last; ++j) {
-        const float l = lse[slot(j) * cap];
-        const float e = l == -INFINITY ? 0.f : __expf(l - m);   // NaN goes on
-        const float4 v = *reinterpret_cast<const float4*>(tp.ws.part + (slot(j) * cap + r) * kDV + 4 * tid);
-        sum += e;
-        o.x += e * v.x; o.y += e * v.y; o.z += e * v.z; o.w += e * v.w;
-      }
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      const size_t row = (size_t)rec.head_row + r;
-      if (p.out_bf16) {
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kDV + 4 * tid) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-      } else {
-        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kDV + 4 * tid) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      }
-      if (tid == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
+    const float* lse = tp.ws.lse + r;
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) m = fmaxf(m, lse[slots[j] * cap]);
+    float sum = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) {
+      const float l = lse[slots[j] * cap];
+      const float e = l == -INFINITY ? 0.f : __expf(l - m);   // NaN goes on
+      const float4 v = *reinterpret_cast<const float4*>(tp.ws.part + (slots[j] * cap + r) * kDV + col);
+      sum += e;
+      o.x += e * v.x; o.y += e * v.y; o.z += e * v.z; o.w += e * v.w;
     }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const size_t row = (size_t)me.row0 + r;
+    if (p.out_bf16) {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kDV + col) =
+          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kDV + col) =
+          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
+    if (tid == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
   }
   if (!any) return;
   // rare: the nodes of every marked request, a node and two heads at a time
   const int groups = (p.h + kFixHeads - 1) / kFixHeads;
-  const int me = blockIdx.y * gridDim.x + blockIdx.x, all = gridDim.x * gridDim.y;
-  for (int i = 0; i < 2 * tp.pairs; ++i) {
-    const int2 range = tp.ws.bad[i];
+  const int first = blockIdx.x, all = gridDim.x;
+  for (int j = 0; j < 2 * tp.pairs; ++j) {
+    const int2 range = tp.ws.bad[j];
     for (int b = max(range.x, 0); b <= min(range.y, p.B - 1); ++b) {
       const Request r = request_of(p, b);
-      for (int it = me; it < r.n * groups; it += all)
+      for (int it = first; it < r.n * groups; it += all)
         tree_simt<kFixHeads>(p, r.first + it / groups, it % groups * kFixHeads, smem_f);
     }
   }
@@ -877,31 +1106,56 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-int pairs_of_device() { return device_sm_count() / 2 > 0 ? device_sm_count() / 2 : 1; }
+int pairs_of_device() {
+  const int n = device_sm_count() / 2;
+  return n < 1 ? 1 : n > kMaxPairs ? kMaxPairs : n;
+}
+
+long long units_at_most(int B, int T, int h) { return (long long)T * h / kRows + B; }
 
 // places of the workspace's parts; returns its size
-size_t lay_out(char* base, int pairs, int cap, Workspace& ws) {
+size_t lay_out(char* base, int pairs, int B, int T, int h, Workspace& ws) {
   size_t at = 0;
   auto part = [&](size_t bytes) {
     char* q = base + at;
     at += round256(bytes);
     return q;
   };
-  ws.cap = cap;
-  ws.part = reinterpret_cast<float*>(part((size_t)2 * pairs * cap * kDV * 4));
-  ws.lse = reinterpret_cast<float*>(part((size_t)2 * pairs * cap * 4));
-  ws.rec = reinterpret_cast<Record*>(part((size_t)pairs * sizeof(Record)));
+  const long long rows = (long long)T * h;
+  ws.cap = rows < kRows ? (int)rows : kRows;
+  // ranges: two cut units a pair; dealt chunks as many again, where there can be several units of a request
+  ws.slots = (rows > kRows ? 4 : 2) * pairs;
+  ws.pieces = reinterpret_cast<Piece*>(part((size_t)(units_at_most(B, T, h) + 2 * ws.slots) * sizeof(Piece)));
+  ws.start = reinterpret_cast<int*>(part((size_t)(pairs + 1) * 4));
+  ws.partials = reinterpret_cast<int*>(part(4));
+  ws.list = reinterpret_cast<Partial*>(part((size_t)ws.slots * sizeof(Partial)));
+  ws.part = reinterpret_cast<float*>(part((size_t)ws.slots * ws.cap * kDV * 4));
+  ws.lse = reinterpret_cast<float*>(part((size_t)ws.slots * ws.cap * 4));
   ws.bad = reinterpret_cast<int2*>(part((size_t)2 * pairs * sizeof(int2)));
   return at;
 }
 
-int rows_of_slot(long long rows) { return rows < kRows ? (int)rows : kRows; }
+// launched early: what it does before griddepcontrol.wait runs beside the end of the kernel before
+template <class Kernel, class... Args>
+cudaError_t launch_after(Kernel kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr = {};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 
 }  // namespace
 
-size_t tree_workspace_bytes(int T, int h) {
+size_t tree_workspace_bytes(int B, int T, int h) {
   Workspace ws;
-  return lay_out(nullptr, pairs_of_device(), rows_of_slot((long long)T * h), ws);
+  return lay_out(nullptr, pairs_of_device(), B, T, h, ws);
 }
 
 cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
@@ -925,18 +1179,19 @@ cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
   tp.box = 64;
   while (p.block_size % tp.box != 0) tp.box /= 2;
   if (tp.box < 8) tp.box = 0;
-  lay_out(static_cast<char*>(p.workspace), tp.pairs, rows_of_slot((long long)p.T * p.h), tp.ws);
+  lay_out(static_cast<char*>(p.workspace), tp.pairs, p.B, p.T, p.h, tp.ws);
   CUtensorMap box, two, row, q;
   if (!make_rows_map(&box, p.kv, tp.num_rows, tp.box ? tp.box : 8) || !make_rows_map(&row, p.kv, tp.num_rows, 1) ||
       !make_blocks_map(&two, p.kv, tp.num_rows, 64, 2) ||
       !make_rows_map(&q, p.q, (long long)p.T * p.h, kHalf))
     return cudaErrorInvalidValue;
-  const auto kernel = p.out_bf16 ? decode_tree_kernel<false> : decode_tree_kernel<true>;
-  kernel<<<2 * tp.pairs, kThreads, kSmem, stream>>>(box, two, row, q, tp);
+  tree_schedule_kernel<<<1, kPlanThreads, 0, stream>>>(tp);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  join_tree_kernel<<<dim3(tp.pairs, kJoinRows), kJoinThreads, kFixSmem, stream>>>(tp);
-  return cudaGetLastError();
+  e = launch_after(p.out_bf16 ? decode_tree_kernel<false> : decode_tree_kernel<true>, dim3(2 * tp.pairs), kThreads, kSmem,
+                   stream, box, two, row, q, tp);
+  if (e != cudaSuccess) return e;
+  return launch_after(join_tree_kernel, dim3(8 * device_sm_count()), kJoinThreads, kFixSmem, stream, tp);
 }
 
 }  // namespace sfa

@@ -215,6 +215,18 @@ def test_decode_of_long_sequences(path):
     run(problem(4, [20011], [2], 3, 16))
 
 
+@pytest.mark.parametrize("cached,nodes,h", [([70000], [5], 64), ([40000, 300, 33000], [4, 9, 3], 128), ([66000], [33], 4)])
+def test_decode_of_units_dealt_in_chunks(cached, nodes, h):
+    # several units over more rows than stay in L2: whole units or chunks of them by turns, the rest in ranges
+    run(problem(h, cached, nodes, h, 64))
+
+
+def test_decode_of_many_short_requests(path):
+    rng = np.random.default_rng(40)
+    for B, h, most in ((300, 4, 3), (1500, 16, 2)):
+        run(problem(B, rng.integers(0, 40, B), rng.integers(0, most + 1, B), h, 16))
+
+
 def test_decode_with_padding_before_and_behind(path):
     run(problem(5, [40, 9], [6, 2], 16, 16, before=5, behind=9))
 
