@@ -240,9 +240,9 @@ struct Plan {
 };
 
 // the pieces of one pair, in order: f(request number, request, unit, k0, k1)
-template <class F>
-__device__ __forceinline__ void walk_pair(const TreeParams& p, const Plan& plan, const int* tasks_before, int pair,
-                                          int pairs, int b, long long off, long long left, F f) {
+template <class Get, class F>
+__device__ __forceinline__ void walk_pair(const TreeParams& p, const Plan& plan, const int* tasks_before, Get request,
+                                          int pair, int pairs, int b, long long off, long long left, F f) {
   auto piece = [&](int bb, const Request& r, int task, int from, int to) {   // places [from, to) of a task
     const int begin = task / r.units * r.len;
     const bool last = task / r.units == r.chunks - 1;
@@ -258,22 +258,24 @@ __device__ __forceinline__ void walk_pair(const TreeParams& p, const Plan& plan,
       const int mid = (lo + hi) >> 1;
       if (tasks_before[mid] <= t) lo = mid; else hi = mid;
     }
-    const Request r = request_of(p, lo, plan.limit);
+    const Request r = request(lo);
     piece(lo, r, t - tasks_before[lo], 0, r.cost());
   }
   if (left <= 0) return;
-  Request r = request_of(p, b, plan.limit);
+  Request r = request(b);
   auto skipped = [&] { return plan.dealt ? min(max(plan.dealt - tasks_before[b], 0), r.tasks()) : 0; };
   int skip = skipped();
   while (left > 0) {
     if (off >= (long long)(r.tasks() - skip) * r.cost()) {
       if (++b >= p.B) return;
-      r = request_of(p, b, plan.limit);
+      r = request(b);
       skip = skipped();
       off = 0;
       continue;
     }
-    const int c = r.cost(), task = (int)(off / c), u = (int)(off % c);
+    const int c = r.cost();
+    const int task = off >> 32 ? (int)(off / c) : (int)((uint32_t)off / (uint32_t)c);   // (64 bits are slow)
+    const int u = (int)(off - (long long)task * c);
     const int take = (int)min(left, (long long)(c - u));
     off += take;
     left -= take;
@@ -324,13 +326,16 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   const int tid = threadIdx.x, pairs = tp.pairs;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
+  __shared__ Request requests[kPlanThreads];   // where there is one a thread
   Plan plan{kWhole, 0, 0};
+  auto request = [&](int b) { return p.B <= kPlanThreads ? requests[b] : request_of(p, b, plan.limit); };
   long long cost = 0, tiles = 0, far = 0;      // of the units; their tiles; tiles of different rows
   for (int b = r0; b < r1; ++b) {
     const Request r = request_of(p, b);
     cost += (long long)r.units * r.cost();
     tiles += (long long)r.units * r.tiles;
     far += r.units > 0 ? r.tiles : 0;
+    if (p.B <= kPlanThreads) requests[b] = r;
     if (min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
       report_status(p.status, kStatusBadTree);
   }
@@ -367,6 +372,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     // tasks before each request (one request a thread at most), what the dealt ones load each pair with
     const Request r = tid < p.B ? request_of(p, tid, plan.limit) : Request{};
     const int mine = tid < p.B ? r.tasks() : 0;
+    if (tid < p.B) requests[tid] = r;
     long long n;
     const int before = (int)block_before(mine, part, n);
     if (tid < p.B) tasks_before[tid] = before;
@@ -377,7 +383,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
       const int k = i % pairs, b = i / pairs;
       const int lo = min(tasks_before[b], plan.dealt), hi = min(tasks_before[b + 1], plan.dealt);
       const int count = (hi - 1 - k + pairs) / pairs - (lo - 1 - k + pairs) / pairs;   // tasks t = k mod pairs in [lo, hi)
-      if (count > 0) atomicAdd(&load[k], count * request_of(p, b, plan.limit).cost());
+      if (count > 0) atomicAdd(&load[k], count * requests[b].cost());
     }
     // the rest of the tasks, in cost: level the pairs
     const int skip = min(max(plan.dealt - before, 0), mine);
@@ -409,7 +415,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     __syncthreads();
   } else {
     const long long total = block_sum(cost, part);
-    const long long span = max((total + pairs - 1) / pairs, (long long)kMinSpan);
+    const long long span = max(total >> 31 ? (total + pairs - 1) / pairs : (long long)(((uint32_t)total + pairs - 1) / pairs),
+                               (long long)kMinSpan);
     if (tid <= pairs) share_at[tid] = min(tid * span, total);
     __syncthreads();
   }
@@ -428,7 +435,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
       }
       long long a = cost_before[lo];
       for (int b = lo * per; b < min(lo * per + per, p.B); ++b) {
-        const Request r = request_of(p, b, plan.limit);
+        const Request r = request(b);
         const int skip = plan.dealt ? min(max(plan.dealt - tasks_before[b], 0), r.tasks()) : 0;
         const long long c = (long long)(r.tasks() - skip) * r.cost();
         if (from < a + c) {
@@ -445,7 +452,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   const bool have = tid < pairs;
   auto pair_walk = [&](auto f) {
     if (have)
-      walk_pair(p, plan, tasks_before, tid, pairs, begin_b[tid], begin_off[tid],
+      walk_pair(p, plan, tasks_before, request, tid, pairs, begin_b[tid], begin_off[tid],
                 begin_b[tid] < 0 ? 0 : share_at[tid + 1] - share_at[tid], f);
   };
   pair_walk([&](int, const Request& r, int, int k0, int k1) {
@@ -996,7 +1003,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 constexpr int kJoinThreads = 128;
 constexpr int kFixHeads = 2;
 
-// Blocks take the rows of the cut units by turns, a row four columns a thread.
+// Every block takes a run of the cut units' rows.
 __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcParams tp) {
   extern __shared__ float smem_f[];
   __shared__ int slots[kMaxSlots];             // a unit's parts
@@ -1035,26 +1042,30 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
     n_rows += all & 0xffff;
     __syncthreads();
   }
+  // a row a warp; a block's rows lie next to each other, so that they mostly are of one unit
+  constexpr int kWarps = kJoinThreads / 32;
   int unit = -1, n = 0;
-  for (int it = blockIdx.x; it < n_rows; it += gridDim.x) {
+  const int run = (n_rows + gridDim.x - 1) / gridDim.x, to = min((int)(blockIdx.x + 1) * run, n_rows);
+  for (int it0 = blockIdx.x * run; it0 < to;) {
     int lo = 0, hi = n_begins;                 // the last unit that begins with this row or before
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (rows_before[mid] <= it) lo = mid; else hi = mid;
+      if (rows_before[mid] <= it0) lo = mid; else hi = mid;
     }
     const Partial me = tp.ws.list[begins[lo]];
+    const int end = min(to, rows_before[lo] + me.rows);
     if (lo != unit) {                          // its parts, in the order of the slots: the same sums every time
       unit = lo;
       __syncthreads();
-      if (tid < 32) {
+      if (warp == 0) {
         int k = 0;
         for (int j0 = 0; j0 < partials; j0 += 32) {
-          const bool one = j0 + tid < partials && tp.ws.list[j0 + tid].row0 == me.row0;
+          const bool one = j0 + lane < partials && tp.ws.list[j0 + lane].row0 == me.row0;
           const unsigned m = __ballot_sync(0xffffffffu, one);
-          if (one) slots[k + __popc(m & ((1u << tid) - 1))] = j0 + tid;
+          if (one) slots[k + __popc(m & ((1u << lane) - 1))] = j0 + lane;
           k += __popc(m);
         }
-        if (tid == 0) n_parts = k;
+        if (lane == 0) n_parts = k;
       }
       __syncthreads();
       n = n_parts;
@@ -1062,33 +1073,44 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
     bool skip = false;                         // all of the request is computed again below
     if (any)
       for (int j = 0; j < 2 * tp.pairs; ++j) skip |= tp.ws.bad[j].x <= me.request && me.request <= tp.ws.bad[j].y;
-    const int r = it - rows_before[lo], col = 4 * tid;
-    if (skip || r >= tp.ws.cap) continue;
-    const size_t cap = tp.ws.cap;
-    const float* lse = tp.ws.lse + r;
-    float m = -INFINITY;
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) m = fmaxf(m, lse[slots[j] * cap]);
-    float sum = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int j = 0; j < n; ++j) {
-      const float l = lse[slots[j] * cap];
-      const float e = l == -INFINITY ? 0.f : __expf(l - m);   // NaN goes on
-      const float4 v = *reinterpret_cast<const float4*>(tp.ws.part + (slots[j] * cap + r) * kDV + col);
-      sum += e;
-      o.x += e * v.x; o.y += e * v.y; o.z += e * v.z; o.w += e * v.w;
+    for (int it = it0 + warp; it < end && !skip; it += kWarps) {
+      const int r = it - rows_before[lo];
+      if (r >= tp.ws.cap) break;
+      const size_t cap = tp.ws.cap;
+      const float* lse = tp.ws.lse + r;
+      float m = -INFINITY;
+      for (int j = lane; j < n; j += 32) m = fmaxf(m, lse[slots[j] * cap]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float sum = 0.f;
+      float4 o[4] = {};
+#pragma unroll 2
+      for (int j = 0; j < n; ++j) {
+        const float l = lse[slots[j] * cap];
+        const float e = l == -INFINITY ? 0.f : __expf(l - m);   // NaN goes on
+        const float4* v = reinterpret_cast<const float4*>(tp.ws.part + (slots[j] * cap + r) * kDV) + lane;
+        sum += e;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float4 y = v[32 * c];
+          o[c].x += e * y.x; o[c].y += e * y.y; o[c].z += e * y.z; o[c].w += e * y.w;
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t row = (size_t)me.row0 + r;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const size_t at = row * kDV + 4 * (lane + 32 * c);
+        if (p.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+              make_uint2(pack_bf16(o[c].x * inv, o[c].y * inv), pack_bf16(o[c].z * inv, o[c].w * inv));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) =
+              make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
+      }
+      if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
     }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const size_t row = (size_t)me.row0 + r;
-    if (p.out_bf16) {
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kDV + col) =
-          make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * kDV + col) =
-          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    }
-    if (tid == 0) p.lse[row] = sum == 0.f ? -INFINITY : m + logf(sum);
+    it0 = end;
   }
   if (!any) return;
   // rare: the nodes of every marked request, a node and two heads at a time
@@ -1191,7 +1213,7 @@ cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
   e = launch_after(p.out_bf16 ? decode_tree_kernel<false> : decode_tree_kernel<true>, dim3(2 * tp.pairs), kThreads, kSmem,
                    stream, box, two, row, q, tp);
   if (e != cudaSuccess) return e;
-  return launch_after(join_tree_kernel, dim3(8 * device_sm_count()), kJoinThreads, kFixSmem, stream, tp);
+  return launch_after(join_tree_kernel, dim3(12 * device_sm_count()), kJoinThreads, kFixSmem, stream, tp);
 }
 
 }  // namespace sfa
