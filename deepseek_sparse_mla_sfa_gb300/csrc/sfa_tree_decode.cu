@@ -204,7 +204,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 // the order (request, chunk, unit), and are dealt to the pairs one by one, so that neighbouring pairs read
 // the same rows at the same time; what is left of the last, unfilled round goes to ranges that even out
 // what the dealt chunks left uneven.
-constexpr int kPlanThreads = 512;
+constexpr int kPlanThreads = 256;
 constexpr int kDealRequests = 256;             // requests that chunks are dealt of
 constexpr int kFarTiles = 240;                 // tiles (256 rows of 1152 bytes) that stay in L2: 70 MB
 constexpr int kWhole = 0x7fffffff;             // `limit` that cuts nothing
@@ -283,18 +283,7 @@ __device__ __forceinline__ void walk_pair(const TreeParams& p, const Plan& plan,
   }
 }
 
-__device__ __forceinline__ long long block_sum(long long v, long long* part) {
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if (lane == 0) part[warp] = v;
-  __syncthreads();
-  long long t = 0;
-  for (int w = 0; w < kPlanThreads / 32; ++w) t += part[w];
-  return t;
-}
-// the sum over the threads before
+// the sum over the threads before, the sum of all in `total`
 __device__ __forceinline__ long long block_before(long long v, long long* part, long long& total) {
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   long long in = v;
@@ -306,63 +295,91 @@ __device__ __forceinline__ long long block_before(long long v, long long* part, 
   __syncthreads();
   if (lane == 31) part[warp] = in;
   __syncthreads();
-  long long before = in - v;
-  total = 0;
+  long long before = in - v, sum = 0;
+#pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before += part[w];
-    total += part[w];
+    const long long x = part[w];
+    before += w < warp ? x : 0;
+    sum += x;
   }
+  total = sum;
   return before;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeTcParams tp) {
   asm volatile("griddepcontrol.launch_dependents;");
-  __shared__ long long part[kPlanThreads / 32];
-  __shared__ int tasks_before[kDealRequests + 1];
-  __shared__ int load[kMaxPairs], begin_b[kMaxPairs];
-  __shared__ long long cost_before[kPlanThreads];
-  __shared__ long long share_at[kMaxPairs + 1], begin_off[kMaxPairs];   // where the pairs' ranges lie
+  constexpr int kKept = 4;                     // pieces of a pair that its first walk keeps for the second
+  __shared__ long long part[kPlanThreads / 32], cost_before[kPlanThreads];
+  __shared__ int tasks_before[kDealRequests + 1], load[kMaxPairs];
+  __shared__ long long share_at[kMaxPairs + 1];             // where the pairs' ranges lie
+  __shared__ Request requests[kPlanThreads];                // where there is one a thread
+  __shared__ Piece kept[kMaxPairs][kKept];
+  __shared__ int n_of[3], split_of[3];
+  __shared__ float cost_of[3], tiles_of, far_of;
   const TreeParams& p = tp.p;
-  const int tid = threadIdx.x, pairs = tp.pairs;
+  const int tid = threadIdx.x, lane = tid % 32, pairs = tp.pairs;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
   const int r0 = min(tid * per, p.B), r1 = min(r0 + per, p.B);
-  __shared__ Request requests[kPlanThreads];   // where there is one a thread
   Plan plan{kWhole, 0, 0};
   auto request = [&](int b) { return p.B <= kPlanThreads ? requests[b] : request_of(p, b, plan.limit); };
-  long long cost = 0, tiles = 0, far = 0;      // of the units; their tiles; tiles of different rows
+  if (tid < 3) {
+    n_of[tid] = split_of[tid] = 0;
+    cost_of[tid] = 0.f;
+  }
+  if (tid == 0) tiles_of = far_of = 0.f;
+  long long cost = 0;                          // of the units
+  float tiles = 0.f, far = 0.f;                // their tiles; tiles of different rows
   for (int b = r0; b < r1; ++b) {
     const Request r = request_of(p, b);
     cost += (long long)r.units * r.cost();
-    tiles += (long long)r.units * r.tiles;
+    tiles += (float)r.units * r.tiles;
     far += r.units > 0 ? r.tiles : 0;
     if (p.B <= kPlanThreads) requests[b] = r;
     if (min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
       report_status(p.status, kStatusBadTree);
   }
-  if (p.B <= kDealRequests) {
-    tiles = block_sum(tiles, part);
-    far = block_sum(far, part);
-    if (far > kFarTiles && 2 * tiles >= 3 * far) {
+  long long total;
+  long long at = block_before(cost, part, total);
+  if (p.B <= kDealRequests && total > 2 * kFarTiles) {
+    auto add = [&](float v, float* to) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) atomicAdd(to, v);
+    };
+    add(tiles, &tiles_of);
+    add(far, &far_of);
+    __syncthreads();
+    if (far_of > kFarTiles && tiles_of >= 1.5f * far_of) {
       // whole units, or chunks that make a round or two; what is not dealt counts a third more
+      int limits[3] = {kWhole, 0, 0};
+      for (int c = 0; c < 3; ++c) {
+        if (c > 0) limits[c] = (int)fminf(ceilf(tiles_of / (c * pairs)), 1e9f);
+        int n = 0, split = 0;
+        float all = 0.f;
+        if (tid < p.B) {
+          const Request r = request_of(p, tid, limits[c]);
+          n = r.tasks();
+          all = (float)n * r.cost();
+          split = r.chunks > 1 ? n : 0;
+        }
+        add(all, &cost_of[c]);
+        n = __reduce_add_sync(0xffffffffu, n);
+        split = __reduce_add_sync(0xffffffffu, split);
+        if (lane == 0) {
+          atomicAdd(&n_of[c], n);
+          atomicAdd(&split_of[c], split);
+        }
+      }
+      __syncthreads();
       float best = 1e30f;
       for (int c = 0; c < 3; ++c) {
-        const int limit = c == 0 ? kWhole : (int)min((tiles + c * pairs - 1) / (c * pairs), (long long)kWhole);
-        long long n = 0, all = 0, split = 0;
-        for (int b = r0; b < r1; ++b) {
-          const Request r = request_of(p, b, limit);
-          n += r.tasks();
-          all += (long long)r.tasks() * r.cost();
-          split += r.chunks > 1 ? r.tasks() : 0;
-        }
-        n = block_sum(n, part);
-        all = block_sum(all, part);
-        split = block_sum(split, part);
-        if (n < pairs || n > (1 << 24) || split + 2 * pairs > tp.ws.slots) continue;
-        const float done = (float)(n / pairs * pairs) / (float)n, t = (float)all * (done + 1.3f * (1.f - done));
+        const int n = n_of[c];
+        if (n < pairs || n > (1 << 24) || split_of[c] + 2 * pairs > tp.ws.slots) continue;
+        const float done = (float)(n / pairs * pairs) / (float)n, t = cost_of[c] * (done + 1.3f * (1.f - done));
         if (t < best) {
           best = t;
-          plan.limit = limit;
-          plan.rounds = (int)(n / pairs);
+          plan.limit = limits[c];
+          plan.rounds = n / pairs;
           plan.dealt = plan.rounds * pairs;
         }
       }
@@ -370,103 +387,115 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   }
   if (plan.rounds > 0) {
     // tasks before each request (one request a thread at most), what the dealt ones load each pair with
-    const Request r = tid < p.B ? request_of(p, tid, plan.limit) : Request{};
+    Request r{};
+    if (tid < p.B) requests[tid] = r = request_of(p, tid, plan.limit);
     const int mine = tid < p.B ? r.tasks() : 0;
-    if (tid < p.B) requests[tid] = r;
     long long n;
     const int before = (int)block_before(mine, part, n);
     if (tid < p.B) tasks_before[tid] = before;
     if (tid == 0) tasks_before[p.B] = (int)n;
     if (tid < pairs) load[tid] = 0;
-    __syncthreads();
-    for (int i = tid; i < pairs * p.B; i += kPlanThreads) {
-      const int k = i % pairs, b = i / pairs;
-      const int lo = min(tasks_before[b], plan.dealt), hi = min(tasks_before[b + 1], plan.dealt);
-      const int count = (hi - 1 - k + pairs) / pairs - (lo - 1 - k + pairs) / pairs;   // tasks t = k mod pairs in [lo, hi)
-      if (count > 0) atomicAdd(&load[k], count * requests[b].cost());
-    }
-    // the rest of the tasks, in cost: level the pairs
+    // the rest of the tasks, in cost
     const int skip = min(max(plan.dealt - before, 0), mine);
     cost = tid < p.B ? (long long)(mine - skip) * r.cost() : 0;
-    const long long rest = block_sum(cost, part);
-    __syncthreads();
-    if (tid < 32) {
-      long long lo = 0, hi = rest;             // the least level whose room is `rest`
-      for (int k = tid; k < pairs; k += 32) hi = max(hi, rest + load[k]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) hi = max(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-      while (lo < hi) {
-        const long long mid = (lo + hi) >> 1;
-        long long room = 0;
-        for (int k = tid; k < pairs; k += 32) room += max(mid - load[k], 0ll);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) room += __shfl_xor_sync(0xffffffffu, room, o);
-        if (room >= rest) hi = mid; else lo = mid + 1;
-      }
-      if (tid == 0) {
-        long long at = 0;
-        for (int k = 0; k < pairs; ++k) {
-          share_at[k] = min(at, rest);
-          at += max(lo - load[k], 0ll);
+    at = block_before(cost, part, total);
+    if (tid < p.B) {
+      // tasks lo .. hi - 1 go to the pairs lo, lo + 1, ... (mod pairs), so many times each
+      const int lo = min(before, plan.dealt), hi = min(before + mine, plan.dealt), c = r.cost();
+      const int times = (hi - lo) / pairs, more = (hi - lo) % pairs, k0 = lo % pairs;
+      if (hi > lo)
+        for (int i = 0, k = k0; i < (times > 0 ? pairs : more); ++i) {
+          atomicAdd(&load[k], (times + (i < more)) * c);
+          if (++k == pairs) k = 0;
         }
-        share_at[pairs] = rest;
-      }
     }
     __syncthreads();
+    if (tid < 32) {
+      // Level the pairs: the least level that gives the rest room, among the pairs below it.
+      constexpr int kEach = kMaxPairs / 32;
+      long long sum = total;
+      int count = pairs, v[kEach];
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int k = kEach * lane + i;
+        v[i] = k < pairs ? load[k] : 0;
+        long long x = v[i];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        sum += x;
+      }
+      long long level;
+      for (;;) {                               // (each turn leaves out a pair, or ends)
+        level = (sum + count - 1) / count;
+        long long s2 = total;
+        int c2 = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          const bool in = kEach * lane + i < pairs && v[i] < level;
+          c2 += in;
+          long long x = in ? v[i] : 0;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+          s2 += x;
+        }
+        c2 = __reduce_add_sync(0xffffffffu, c2);
+        if (c2 == count || c2 == 0) break;
+        sum = s2;
+        count = c2;
+      }
+      long long mine_sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) mine_sum += kEach * lane + i < pairs ? max(level - v[i], 0ll) : 0;
+      long long in = mine_sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, in, o);
+        if (lane >= o) in += u;
+      }
+      long long from = in - mine_sum;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int k = kEach * lane + i;
+        if (k < pairs) {
+          share_at[k] = min(from, total);
+          from += max(level - v[i], 0ll);
+        }
+      }
+      if (lane == 0) share_at[pairs] = total;
+    }
   } else {
-    const long long total = block_sum(cost, part);
     const long long span = max(total >> 31 ? (total + pairs - 1) / pairs : (long long)(((uint32_t)total + pairs - 1) / pairs),
                                (long long)kMinSpan);
     if (tid <= pairs) share_at[tid] = min(tid * span, total);
-    __syncthreads();
   }
-  // where the pairs' ranges begin
-  long long total;
-  cost_before[tid] = block_before(cost, part, total);
+  cost_before[tid] = at;
   __syncthreads();
-  if (tid < pairs) {
+  // the pairs' pieces: counted, then written
+  const bool have = tid < pairs;
+  int first = 0;
+  long long off = 0, left = 0;
+  if (have) {
     const long long from = share_at[tid];
-    begin_b[tid] = -1;
-    if (share_at[tid + 1] > from) {
-      int lo = 0, hi = kPlanThreads;           // the last thread with requests that begin at `from` or before
+    left = share_at[tid + 1] - from;
+    if (left > 0) {                            // its range begins in this request, this far in
+      int lo = 0, hi = kPlanThreads;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cost_before[mid] <= from) lo = mid; else hi = mid;
       }
       long long a = cost_before[lo];
-      for (int b = lo * per; b < min(lo * per + per, p.B); ++b) {
+      for (int b = lo * per; b < p.B; ++b) {
         const Request r = request(b);
         const int skip = plan.dealt ? min(max(plan.dealt - tasks_before[b], 0), r.tasks()) : 0;
         const long long c = (long long)(r.tasks() - skip) * r.cost();
-        if (from < a + c) {
-          begin_b[tid] = b;
-          begin_off[tid] = from - a;
-          break;
-        }
+        first = b;
+        off = from - a;
+        if (from < a + c) break;
         a += c;
       }
     }
   }
-  // count, then write
-  int pieces = 0, partials = 0;
-  const bool have = tid < pairs;
-  auto pair_walk = [&](auto f) {
-    if (have)
-      walk_pair(p, plan, tasks_before, request, tid, pairs, begin_b[tid], begin_off[tid],
-                begin_b[tid] < 0 ? 0 : share_at[tid + 1] - share_at[tid], f);
-  };
-  pair_walk([&](int, const Request& r, int, int k0, int k1) {
-    ++pieces;
-    partials += !(k0 == 0 && k1 == r.tiles);
-  });
-  long long all_pieces, all_partials;
-  int at_piece = (int)block_before(pieces, part, all_pieces), at_partial = (int)block_before(partials, part, all_partials);
-  if (have) tp.ws.start[tid] = at_piece;
-  if (tid == 0) {
-    tp.ws.start[pairs] = (int)all_pieces;
-    *tp.ws.partials = (int)all_partials;
-  }
-  pair_walk([&](int b, const Request& r, int unit, int k0, int k1) {
+  auto describe = [&](int b, const Request& r, int unit, int k0, int k1) {
     Piece x;
     x.row0 = r.first * p.h + unit * kRows;
     x.rows = min(kRows, r.n * p.h - unit * kRows);
@@ -476,14 +505,40 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     x.cached = r.cached;
     x.n = r.n;
     x.first = r.first;
-    x.slot = -1;
+    x.slot = k0 == 0 && k1 == r.tiles ? -1 : 0;
     x.pad[0] = x.pad[1] = x.pad[2] = 0;
-    if (!(k0 == 0 && k1 == r.tiles)) {
+    return x;
+  };
+  int pieces = 0, partials = 0;
+  if (have)
+    walk_pair(p, plan, tasks_before, request, tid, pairs, first, off, left,
+              [&](int b, const Request& r, int unit, int k0, int k1) {
+                if (pieces < kKept) kept[tid][pieces] = describe(b, r, unit, k0, k1);
+                ++pieces;
+                partials += !(k0 == 0 && k1 == r.tiles);
+              });
+  long long all;                               // (both counts in one sum)
+  const long long before = block_before((long long)pieces << 32 | partials, part, all);
+  int at_piece = (int)(before >> 32), at_partial = (int)(before & 0xffffffff);
+  if (have) tp.ws.start[tid] = at_piece;
+  if (tid == 0) {
+    tp.ws.start[pairs] = (int)(all >> 32);
+    *tp.ws.partials = (int)(all & 0xffffffff);
+  }
+  auto write = [&](Piece x) {
+    if (x.slot == 0) {
       x.slot = at_partial;
-      tp.ws.list[at_partial++] = Partial{x.row0, x.rows, b, k0 == 0};
+      tp.ws.list[at_partial++] = Partial{x.row0, x.rows, x.request, x.k0 == 0};
     }
     tp.ws.pieces[at_piece++] = x;
-  });
+  };
+  if (have) {
+    if (pieces <= kKept)
+      for (int i = 0; i < pieces; ++i) write(kept[tid][i]);
+    else
+      walk_pair(p, plan, tasks_before, request, tid, pairs, first, off, left,
+                [&](int b, const Request& r, int unit, int k0, int k1) { write(describe(b, r, unit, k0, k1)); });
+  }
 }
 
 // a pair's pieces, one after the other
@@ -807,22 +862,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t round = 0;
       // test hook: a wait that cannot complete, so the wait limit runs out
       bool ok = !p.stall || wait_warp(&bars[kBarNever], 0);
+      bool ready = false;                      // the next chunk is there
       auto full = [&]() -> bool {
-        ok = ok && wait_warp(&bars[kBarFull + slot], round);
+        if (!ready) ok = ok && wait_warp(&bars[kBarFull + slot], round);
         tc_fence_after();
         return ok;
+      };
+      // on to the next chunk; whether it is there was asked before this one's MMAs, so that the answer does
+      // not stand between the two
+      bool answer = false;
+      auto ask = [&] {
+        const int s = slot + 1 == kSlots ? 0 : slot + 1;
+        answer = mbar_test(&bars[kBarFull + s], s == 0 ? round ^ 1 : round);
       };
       auto pass = [&] {
         if (++slot == kSlots) {
           slot = 0;
           round ^= 1;
         }
+        ready = all(answer);
       };
       auto qk = [&](int tile) {     // scores of the tile-th tile of all
         const uint32_t d = tmem + kColS + 128 * (tile & 1);
 #pragma unroll 1
         for (int j = 0; j < kKChunks; ++j) {
           if (!full()) return;
+          ask();
           if (elect_one()) {
             const uint32_t a = dq + j * (kQBlk >> 4), b = dk + slot * (kChunk >> 4);
 #pragma unroll
@@ -850,6 +915,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int j = 0; j < kVChunks; ++j) {
             if (!full()) break;
+            ask();
             if (elect_one()) {
               const uint32_t a = dp + (j & 3) * (kQBlk >> 4), b = dv + slot * (kChunk >> 4);
               const uint32_t d = tmem + kColO + 128 * (j >> 2);
