@@ -12,7 +12,7 @@
 //   P = exp2(S - m), the CTA's own 64 rows, in shared memory, in one bf16 term, or in two (the value and
 //                  what its rounding left) where the result is fp32;
 //   O[64 x 512] += P V: either CTA holds the 256 value columns that its half of each N = 256 takes, of
-//                  all 256 keys, brought 64 keys x 128 columns at a time.
+//                  all 256 keys, brought 32 keys at a time; both halves of O take P from the collector.
 // TMEM lanes 0-63 hold the CTA's 64 rows with the first half of an MMA's N, lanes 64-127 the same rows
 // with the second half: O fills 256 columns, two score buffers the other 256.  One CTA's TMEM could not
 // hold 128 rows of O and any scores; with 64 rows a CTA both fit, the softmax of a row stays in its CTA
@@ -20,8 +20,7 @@
 // an MMA of M = 128 takes 64 cycles for N = 256 and 66 for N = 128 (measured): tiles of 128 keys take
 // 1.5 times as long a key.
 //
-// Order of the chunks (16 KB a CTA, a ring of 7, or of 5 beside two terms): K(0), then K(i+1), V(i) by turns (V's first 128
-// columns of each half, then the others), so QK^T of the
+// Order of the chunks (16 KB a CTA, a ring of 7, or of 5 beside two terms): K(0), then K(i+1), V(i) by turns, so QK^T of the
 // next tile covers the softmax of this one.  The value columns of the CTA's own keys come twice (as
 // keys and as values); the second time is from L2, which gives 180 GB/s an SM where the ring takes 130.
 //
@@ -137,6 +136,17 @@ __device__ __forceinline__ void mma2(uint32_t d, uint32_t a, uint32_t b, uint32_
       "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(kDescHi)
       : "memory");
 }
+// two MMAs with one A, which the second takes from the collector
+__device__ __forceinline__ void mma2_pair(uint32_t d0, uint32_t d1, uint32_t a, uint32_t b0, uint32_t b1, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db, dc;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%2, %7};\n\tmov.b64 db, {%3, %7};\n\tmov.b64 dc, {%4, %7};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], da, db, %5, p;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [%1], da, dc, %5, p;\n\t}" ::"r"(d0),
+      "r"(d1), "r"(a), "r"(b0), "r"(b1), "r"(idesc), "r"(accumulate), "n"(kDescHi)
+      : "memory");
+}
 // one lane of the (converged) warp, the same every time
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -159,8 +169,8 @@ __device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, i
       "l"(map), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-// two blocks of 64 columns (from the block-th on) of the rows from y on
-__device__ __forceinline__ void load_box2(uint32_t dst, const void* map, int y, int block, uint32_t bar) {
+// four blocks of 64 columns (from the block-th on) of the rows from y on
+__device__ __forceinline__ void load_blocks(uint32_t dst, const void* map, int y, int block, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
       "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
@@ -573,7 +583,7 @@ __device__ __forceinline__ unsigned long long mask_bits(const long long* words, 
 // kTwo: the weights in two bf16 terms (their rounding, 2^-17, is below fp32 results' needs), else one
 template <bool kTwo>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-    decode_tree_kernel(const __grid_constant__ CUtensorMap map_box, const __grid_constant__ CUtensorMap map_two,
+    decode_tree_kernel(const __grid_constant__ CUtensorMap map_box, const __grid_constant__ CUtensorMap map_v,
                        const __grid_constant__ CUtensorMap map_row, const __grid_constant__ CUtensorMap map_q,
                        const TreeTcParams tp) {
   constexpr int kSlots = Ring<kTwo>::kSlots, kOffRing = Ring<kTwo>::kOff;
@@ -615,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   if (warp == kLoadWarp && lane == 0) {
     prefetch_tmap(&map_box);
-    prefetch_tmap(&map_two);
+    prefetch_tmap(&map_v);
     prefetch_tmap(&map_q);
   }
   asm volatile("griddepcontrol.launch_dependents;");
@@ -857,7 +867,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint32_t id_qk = idesc_bf16(128, 256, 0, 0), id_pv = idesc_bf16(128, 256, 0, 1);
       const uint32_t sm0 = smem_u32(smem);
       const uint32_t dq = desc_lo(sm0, 16), dp = desc_lo(sm0 + kOffP, 16);
-      const uint32_t dk = desc_lo(sm0 + kOffRing, 16), dv = desc_lo(sm0 + kOffRing, 8192);
+      const uint32_t dk = desc_lo(sm0 + kOffRing, 16), dv = desc_lo(sm0 + kOffRing, 4096);
       int slot = 0, g = 0, pieces = 0;
       uint32_t round = 0;
       // test hook: a wait that cannot complete, so the wait limit runs out
@@ -917,13 +927,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (!full()) break;
             ask();
             if (elect_one()) {
-              const uint32_t a = dp + (j & 3) * (kQBlk >> 4), b = dv + slot * (kChunk >> 4);
-              const uint32_t d = tmem + kColO + 128 * (j >> 2);
+              // 32 keys, all of the CTA's columns: two steps of 16 keys, both halves of O with one P
+              const uint32_t a = dp + (j >> 1) * (kQBlk >> 4) + (j & 1) * 4, b = dv + slot * (kChunk >> 4);
+              const uint32_t d = tmem + kColO;
 #pragma unroll
-              for (int u = 0; u < 4; ++u) mma2(d, a + 2 * u, b + 128 * u, id_pv, !begin || (j & 3) > 0 || u > 0);
-              if (kTwo) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) mma2(d, a + (kPBytes >> 4) + 2 * u, b + 128 * u, id_pv, 1);
+              for (int u = 0; u < 2; ++u) {
+                mma2_pair(d, d + 128, a + 2 * u, b + 128 * u, b + 512 + 128 * u, id_pv, !begin || j > 0 || u > 0);
+                if (kTwo) mma2_pair(d, d + 128, a + (kPBytes >> 4) + 2 * u, b + 128 * u, b + 512 + 128 * u, id_pv, 1);
               }
               commit2(&bars[kBarEmpty + slot]);
             }
@@ -953,7 +963,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // warps that took chunks by turns: 400 to 1000).  Each waits for every round of its slot, so that a wait
     // by parity cannot take an older round for its own.
     const int slot = warp - kLoadWarp;
-    const int step = tp.box ? tp.box : 4, k_boxes = 128 / step, v_boxes = 64 / step;
+    const int k_step = tp.box ? tp.box : 4, v_step = min(k_step, 32), v_boxes = 32 / v_step;
     const uint32_t full = mapa(&bars[kBarFull + slot], 0), dst = smem_u32(smem + kOffRing + slot * kChunk);
     bool ok = true, bad = false;
     int round = 0, group = 0, r = slot;        // r-th chunk of the piece's group (K or V of a tile)
@@ -983,12 +993,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         continue;
       }
       const int tile = x.k0 + (is_k ? (group + 1) / 2 : group == 2 * t - 1 ? t - 1 : group / 2 - 1);
-      // the lane's box: `step` rows from `pos` on; of V with boxes of 64 rows, one lane brings 128 columns
-      const int boxes = is_k ? k_boxes : v_boxes == 1 ? 1 : 2 * v_boxes;
+      // the lane's box: `step` rows from `pos` on, 64 columns; of V, with boxes of 32 rows, one lane brings
+      // the four blocks of columns
+      const int step = is_k ? k_step : v_step;
+      const int boxes = is_k ? 128 / k_step : v_boxes == 1 ? 1 : 4 * v_boxes;
       const int at = (is_k ? lane : lane % v_boxes) * step;
-      const long long pos = (long long)tile * kTile + (is_k ? 128 * (int)rank : 64 * (r & 3)) + at;
-      const int col = is_k ? 64 * r : 256 * (int)rank + 128 * (r >> 2) + 64 * (lane / v_boxes);
-      const uint32_t to = dst + (is_k ? 0 : lane / v_boxes * 8192) + at * 128;
+      const long long pos = (long long)tile * kTile + (is_k ? 128 * (int)rank : 32 * r) + at;
+      const int col = is_k ? 64 * r : 256 * (int)rank + 64 * (lane / v_boxes);
+      const uint32_t to = dst + (is_k ? 0 : lane / v_boxes * 4096) + at * 128;
       const int n = lane < boxes ? (int)min(max((long long)x.cached + x.n - pos, 0ll), (long long)step) : 0;
       const int32_t* table = p.block_table + (size_t)x.request * p.max_blocks;
       // its cache rows; those that do not exist are the row behind the last, which loads as zeros
@@ -1018,27 +1030,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // every lane with a box in one instruction (a loop over an elected lane's took half as long again);
       // where the sequence ends in a box, its rows four at a time, with zeros behind the end
-      const bool two = !is_k && v_boxes == 1;
+      const bool four = !is_k && v_boxes == 1;
       if (!tp.box) {
         if (lane < boxes) load_rows4(to, &map_row, col, row[0], row[1], row[2], row[3], full);
       } else if (!cut) {
-        if (two) {
-          if (lane == 0) load_box2(to, &map_two, row[0], col / 64, full);
+        if (four) {
+          if (lane == 0) load_blocks(to, &map_v, row[0], col / 64, full);
         } else if (lane < boxes) {
           load_box(to, &map_box, col, row[0], full);
         }
       } else {
         const bool whole = have == 0 || have == step;
-        for (int c = 0; c < (two ? 2 : 1); ++c) {
-          if (lane < boxes && whole) load_box(to + c * 8192, &map_box, col + 64 * c, row[0], full);
-          __syncwarp();
+        if (lane < boxes && whole) {
+          if (four) load_blocks(to, &map_v, row[0], col / 64, full); else load_box(to, &map_box, col, row[0], full);
+        }
+        __syncwarp();
+        for (int c = 0; c < (four ? 4 : 1); ++c)
           for (int a = 0; a < step; a += 4) {
             auto row_at = [&](int u) { return a + u < have ? row[0] + a + u : tp.num_rows; };
             if (lane < boxes && !whole)
-              load_rows4(to + c * 8192 + a * 128, &map_row, col + 64 * c, row_at(0), row_at(1), row_at(2), row_at(3), full);
+              load_rows4(to + c * 4096 + a * 128, &map_row, col + 64 * c, row_at(0), row_at(1), row_at(2), row_at(3), full);
             __syncwarp();
           }
-        }
       }
       __syncwarp();
       ++round;
@@ -1268,16 +1281,16 @@ cudaError_t launch_decode_tree(const TreeParams& p, cudaStream_t stream) {
   while (p.block_size % tp.box != 0) tp.box /= 2;
   if (tp.box < 8) tp.box = 0;
   lay_out(static_cast<char*>(p.workspace), tp.pairs, p.B, p.T, p.h, tp.ws);
-  CUtensorMap box, two, row, q;
+  CUtensorMap box, v, row, q;
   if (!make_rows_map(&box, p.kv, tp.num_rows, tp.box ? tp.box : 8) || !make_rows_map(&row, p.kv, tp.num_rows, 1) ||
-      !make_blocks_map(&two, p.kv, tp.num_rows, 64, 2) ||
+      !make_blocks_map(&v, p.kv, tp.num_rows, 32, 4) ||
       !make_rows_map(&q, p.q, (long long)p.T * p.h, kHalf))
     return cudaErrorInvalidValue;
   tree_schedule_kernel<<<1, kPlanThreads, 0, stream>>>(tp);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   e = launch_after(p.out_bf16 ? decode_tree_kernel<false> : decode_tree_kernel<true>, dim3(2 * tp.pairs), kThreads, kSmem,
-                   stream, box, two, row, q, tp);
+                   stream, box, v, row, q, tp);
   if (e != cudaSuccess) return e;
   return launch_after(join_tree_kernel, dim3(12 * device_sm_count()), kJoinThreads, kFixSmem, stream, tp);
 }
