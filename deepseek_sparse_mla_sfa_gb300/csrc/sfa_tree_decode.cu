@@ -862,8 +862,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (!ok) fail();
   } else if (warp == kMmaWarp) {
     // =================== MMAs =========================================================
-    // The whole warp walks, one elected lane issues.
-    if (rank == 0 && len > 0) {
+    // One elected lane, the waits included: in a region of one lane the operands stay in uniform registers
+    // and four MMAs take it 267 cycles, their own time being 256 (a lane chosen by its number 375; a warp
+    // whose lanes all wait, with the MMAs elected, 480).
+    if (rank == 0 && len > 0 && elect_one()) {
       const uint32_t id_qk = idesc_bf16(128, 256, 0, 0), id_pv = idesc_bf16(128, 256, 0, 1);
       const uint32_t sm0 = smem_u32(smem);
       const uint32_t dq = desc_lo(sm0, 16), dp = desc_lo(sm0 + kOffP, 16);
@@ -871,87 +873,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int slot = 0, g = 0, pieces = 0;
       uint32_t round = 0;
       // test hook: a wait that cannot complete, so the wait limit runs out
-      bool ok = !p.stall || wait_warp(&bars[kBarNever], 0);
-      bool ready = false;                      // the next chunk is there
-      auto full = [&]() -> bool {
-        if (!ready) ok = ok && wait_warp(&bars[kBarFull + slot], round);
-        tc_fence_after();
-        return ok;
-      };
-      // on to the next chunk; whether it is there was asked before this one's MMAs, so that the answer does
-      // not stand between the two
-      bool answer = false;
-      auto ask = [&] {
-        const int s = slot + 1 == kSlots ? 0 : slot + 1;
-        answer = mbar_test(&bars[kBarFull + s], s == 0 ? round ^ 1 : round);
-      };
-      auto pass = [&] {
-        if (++slot == kSlots) {
-          slot = 0;
-          round ^= 1;
-        }
-        ready = all(answer);
-      };
-      auto qk = [&](int tile) {     // scores of the tile-th tile of all
+      bool ok = !p.stall || mbar_wait(&bars[kBarNever], 0, wl);
+      auto qk = [&](int tile) {                // scores of the tile-th tile of all
         const uint32_t d = tmem + kColS + 128 * (tile & 1);
 #pragma unroll 1
         for (int j = 0; j < kKChunks; ++j) {
-          if (!full()) return;
-          ask();
-          if (elect_one()) {
-            const uint32_t a = dq + j * (kQBlk >> 4), b = dk + slot * (kChunk >> 4);
+          ok = ok && mbar_wait(&bars[kBarFull + slot], round, wl);
+          if (!ok) return;
+          tc_fence_after();
+          const uint32_t a = dq + j * (kQBlk >> 4), b = dk + slot * (kChunk >> 4);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) mma2(d, a + 2 * u, b + 2 * u, id_qk, j > 0 || u > 0);
-            commit2(&bars[kBarEmpty + slot]);
+          for (int u = 0; u < 4; ++u) mma2(d, a + 2 * u, b + 2 * u, id_qk, j > 0 || u > 0);
+          commit2(&bars[kBarEmpty + slot]);
+          if (++slot == kSlots) {
+            slot = 0;
+            round ^= 1;
           }
-          __syncwarp();
-          pass();
         }
-        if (elect_one()) {
-          commit2(&bars[kBarS + (tile & 1)]);
-        }
-        __syncwarp();
+        commit2(&bars[kBarS + (tile & 1)]);
       };
-      while (ok && all(walk.next(x))) {
-        if (!(ok = wait_warp(&bars[kBarQFull], pieces & 1))) break;
+      while (ok && walk.next(x)) {
+        if (!(ok = mbar_wait(&bars[kBarQFull], pieces & 1, wl))) break;
         tc_fence_after();
         qk(g);
-        for (int k = x.k0; ok && all(k < x.k1); ++k, ++g) {
-          if (all(k + 1 < x.k1)) qk(g + 1);
-          if (!ok || aborted() || !(ok = wait_warp(&bars[kBarP], g & 1))) break;
-          const bool begin = all(k == x.k0);
-          if (begin && pieces > 0 && !(ok = wait_warp(&bars[kBarO], (pieces - 1) & 1))) break;
+        for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
+          if (k + 1 < x.k1) qk(g + 1);
+          if (*abort_s) ok = false;
+          ok = ok && mbar_wait<true>(&bars[kBarP], g & 1, wl);
+          const bool begin = k == x.k0;
+          if (begin && pieces > 0) ok = ok && mbar_wait<true>(&bars[kBarO], (pieces - 1) & 1, wl);
+          if (!ok) break;
           tc_fence_after();
 #pragma unroll 1
           for (int j = 0; j < kVChunks; ++j) {
-            if (!full()) break;
-            ask();
-            if (elect_one()) {
-              // 32 keys, all of the CTA's columns: two steps of 16 keys, both halves of O with one P
-              const uint32_t a = dp + (j >> 1) * (kQBlk >> 4) + (j & 1) * 4, b = dv + slot * (kChunk >> 4);
-              const uint32_t d = tmem + kColO;
+            ok = ok && mbar_wait(&bars[kBarFull + slot], round, wl);
+            if (!ok) break;
+            tc_fence_after();
+            // 32 keys, all of the CTA's columns: two steps of 16 keys, both halves of O with one P
+            const uint32_t a = dp + (j >> 1) * (kQBlk >> 4) + (j & 1) * 4, b = dv + slot * (kChunk >> 4);
+            const uint32_t d = tmem + kColO;
 #pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                mma2_pair(d, d + 128, a + 2 * u, b + 128 * u, b + 512 + 128 * u, id_pv, !begin || j > 0 || u > 0);
-                if (kTwo) mma2_pair(d, d + 128, a + (kPBytes >> 4) + 2 * u, b + 128 * u, b + 512 + 128 * u, id_pv, 1);
-              }
-              commit2(&bars[kBarEmpty + slot]);
+            for (int u = 0; u < 2; ++u) {
+              mma2_pair(d, d + 128, a + 2 * u, b + 128 * u, b + 512 + 128 * u, id_pv, !begin || j > 0 || u > 0);
+              if (kTwo) mma2_pair(d, d + 128, a + (kPBytes >> 4) + 2 * u, b + 128 * u, b + 512 + 128 * u, id_pv, 1);
             }
-            __syncwarp();
-            pass();
+            commit2(&bars[kBarEmpty + slot]);
+            if (++slot == kSlots) {
+              slot = 0;
+              round ^= 1;
+            }
           }
-          if (elect_one()) commit2(&bars[kBarPv]);
-          __syncwarp();
+          commit2(&bars[kBarPv]);
         }
-        if (aborted()) ok = false;
         ++pieces;
       }
       // the second CTA's last arrivals here: no one else waits for them
-      if (ok && pieces > 0) ok = wait_warp(&bars[kBarO], (pieces - 1) & 1);
+      if (ok && pieces > 0) ok = mbar_wait<true>(&bars[kBarO], (pieces - 1) & 1, wl);
       if (!ok) fail();
-      if (elect_one()) commit2(&bars[kBarFin]);
-      __syncwarp();
+      commit2(&bars[kBarFin]);
     }
+    __syncwarp();
     // Every MMA has completed, and every arrival that commits send to either CTA has landed, before
     // TMEM and shared memory go away: an arrival at a CTA that has ended is a fault.
     if (len > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit)))
