@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   asm volatile("griddepcontrol.launch_dependents;");
   constexpr int kKept = 4;                     // pieces of a pair that its first walk keeps for the second
   __shared__ long long part[kPlanThreads / 32], cost_before[kPlanThreads];
-  __shared__ int tasks_before[kDealRequests + 1], load[kMaxPairs];
+  __shared__ int tasks_before[kDealRequests + 1], load[kMaxPairs + 1], load_all;
   __shared__ long long share_at[kMaxPairs + 1];             // where the pairs' ranges lie
   __shared__ Request requests[kPlanThreads];                // where there is one a thread
   __shared__ Piece kept[kMaxPairs][kKept];
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   }
   long long total;
   long long at = block_before(cost, part, total);
-  if (p.B <= kDealRequests && total > 2 * kFarTiles) {
+  if (p.B <= kDealRequests && total > 2 * kFarTiles && total < (1 << 28)) {   // (32 bits from here on)
     auto add = [&](float v, float* to) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -404,71 +404,78 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     const int before = (int)block_before(mine, part, n);
     if (tid < p.B) tasks_before[tid] = before;
     if (tid == 0) tasks_before[p.B] = (int)n;
-    if (tid < pairs) load[tid] = 0;
+    if (tid <= pairs) load[tid] = 0;
+    if (tid == 0) load_all = 0;
     // the rest of the tasks, in cost
     const int skip = min(max(plan.dealt - before, 0), mine);
     cost = tid < p.B ? (long long)(mine - skip) * r.cost() : 0;
     at = block_before(cost, part, total);
     if (tid < p.B) {
-      // tasks lo .. hi - 1 go to the pairs lo, lo + 1, ... (mod pairs), so many times each
+      // tasks lo .. hi - 1 go to the pairs lo, lo + 1, ... (mod pairs): so many times to each, and once more
+      // to `more` of them; `load` gets the steps at both ends
       const int lo = min(before, plan.dealt), hi = min(before + mine, plan.dealt), c = r.cost();
-      const int times = (hi - lo) / pairs, more = (hi - lo) % pairs, k0 = lo % pairs;
-      if (hi > lo)
-        for (int i = 0, k = k0; i < (times > 0 ? pairs : more); ++i) {
-          atomicAdd(&load[k], (times + (i < more)) * c);
-          if (++k == pairs) k = 0;
-        }
+      const int times = (hi - lo) / pairs, more = (hi - lo) - times * pairs, k0 = lo % pairs, k1 = k0 + more;
+      if (times > 0) atomicAdd(&load_all, times * c);
+      if (more > 0) {
+        atomicAdd(&load[k0], c);
+        atomicAdd(&load[k1 <= pairs ? k1 : k1 - pairs], -c);
+        if (k1 > pairs) atomicAdd(&load[0], c);
+      }
     }
     __syncthreads();
     if (tid < 32) {
-      // Level the pairs: the least level that gives the rest room, among the pairs below it.
       constexpr int kEach = kMaxPairs / 32;
-      long long sum = total;
-      int count = pairs, v[kEach];
+      int v[kEach], run = 0;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int k = kEach * lane + i;
-        v[i] = k < pairs ? load[k] : 0;
-        long long x = v[i];
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        sum += x;
+        run += k < pairs ? load[k] : 0;
+        v[i] = run;
       }
-      long long level;
+      int up = run;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, up, o);
+        if (lane >= o) up += u;
+      }
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) v[i] += up - run + load_all;
+      // Level the pairs: the least level that gives the rest room, among the pairs below it.
+      int level, count = pairs, sum = 0;
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) sum += kEach * lane + i < pairs ? v[i] : 0;
+      sum = __reduce_add_sync(0xffffffffu, sum) + (int)total;
       for (;;) {                               // (each turn leaves out a pair, or ends)
         level = (sum + count - 1) / count;
-        long long s2 = total;
-        int c2 = 0;
+        int s2 = 0, c2 = 0;
 #pragma unroll
-        for (int i = 0; i < kEach; ++i) {
-          const bool in = kEach * lane + i < pairs && v[i] < level;
-          c2 += in;
-          long long x = in ? v[i] : 0;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-          s2 += x;
-        }
+        for (int i = 0; i < kEach; ++i)
+          if (kEach * lane + i < pairs && v[i] < level) {
+            ++c2;
+            s2 += v[i];
+          }
         c2 = __reduce_add_sync(0xffffffffu, c2);
+        s2 = __reduce_add_sync(0xffffffffu, s2) + (int)total;
         if (c2 == count || c2 == 0) break;
         sum = s2;
         count = c2;
       }
-      long long mine_sum = 0;
+      int room = 0;
 #pragma unroll
-      for (int i = 0; i < kEach; ++i) mine_sum += kEach * lane + i < pairs ? max(level - v[i], 0ll) : 0;
-      long long in = mine_sum;
+      for (int i = 0; i < kEach; ++i) room += kEach * lane + i < pairs ? max(level - v[i], 0) : 0;
+      int in = room;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, in, o);
+        const int u = __shfl_up_sync(0xffffffffu, in, o);
         if (lane >= o) in += u;
       }
-      long long from = in - mine_sum;
+      int from = in - room;
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
         const int k = kEach * lane + i;
         if (k < pairs) {
-          share_at[k] = min(from, total);
-          from += max(level - v[i], 0ll);
+          share_at[k] = min(from, (int)total);
+          from += max(level - v[i], 0);
         }
       }
       if (lane == 0) share_at[pairs] = total;
