@@ -52,7 +52,8 @@ __all__ = ["decode", "lse_merge", "decode_host", "decode_host_staging_bytes",
            "decode_q8", "kv_write_q8", "kv_write_q8_workspace_bytes", "step_plan",
            "rope", "rope_inv_freq", "rope_mscale",
            "tree_plan", "decode_tree", "decode_tree_workspace_bytes", "tree_accept", "kv_commit",
-           "blocks_fork", "blocks_free", "blocks_compact", "kv_copy_blocks", "kv_copy_blocks_q8",
+           "blocks_fork", "blocks_free", "blocks_free_workspace_bytes", "blocks_compact",
+           "kv_copy_blocks", "kv_copy_blocks_q8",
            "SfaError", "D_QK", "D_V", "BLOCK_TABLE_PER_TOKEN"]
 
 
@@ -899,25 +900,38 @@ def blocks_fork(block_table, lens, src, dst, shares, free_blocks, taken, block_s
     return copies, taken_out
 
 
-def blocks_free(block_table, held_lens, keep_lens, shares, free_blocks, taken, block_size: int, stream=None):
+def blocks_free_workspace_bytes(rows: int, max_blocks: int) -> int:
+    return int(_lib.load().sfa_blocks_free_workspace_bytes(int(rows), int(max_blocks)))
+
+
+def blocks_free(block_table, held_lens, keep_lens, shares, free_blocks, taken, block_size: int, workspace=None,
+                stream=None):
     """Rows give back the blocks between keep_lens and held_lens positions (C ABI
     ``sfa_blocks_free``): keep 0 ends a request, a little less than held drops rejected drafts.
 
     held_lens, keep_lens [rows] int32; shares [num_blocks] and free_blocks [F] int32 in place: a
     shared block loses a share, another goes before entry taken[0] of the free list, in the order of
-    the table.  Returns taken [1].  The table is left as it is.
+    the table.  Returns taken [1].  The table is left as it is.  workspace:
+    blocks_free_workspace_bytes(rows, max_blocks) bytes (allocated when None).
     """
     dev, rows, max_blocks = _need_pool(block_table, shares, free_blocks, taken)
     _check(held_lens, "held_lens", _I32, dev, 1)
     _check(keep_lens, "keep_lens", _I32, dev, 1)
     if held_lens.shape[0] != rows or keep_lens.shape[0] != rows:
         raise ValueError("held_lens and keep_lens must be [rows]")
+    lib = _lib.load()
     with _on(dev, stream):
         taken_out = torch.empty(1, dtype=_I32, device=dev)
-        code = _lib.load().sfa_blocks_free(block_table.data_ptr(), held_lens.data_ptr(), keep_lens.data_ptr(), rows,
-                                           max_blocks, shares.data_ptr(), shares.shape[0], free_blocks.data_ptr(),
-                                           free_blocks.shape[0], taken.data_ptr(), int(block_size),
-                                           taken_out.data_ptr(), _raw_stream(dev))
+        need = lib.sfa_blocks_free_workspace_bytes(rows, max_blocks)
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace is not None and (workspace.get_device() != dev.index or not workspace.is_contiguous()):
+            raise ValueError(f"workspace must be contiguous and on {dev}")
+        ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+        code = lib.sfa_blocks_free(block_table.data_ptr(), held_lens.data_ptr(), keep_lens.data_ptr(), rows,
+                                   max_blocks, shares.data_ptr(), shares.shape[0], free_blocks.data_ptr(),
+                                   free_blocks.shape[0], taken.data_ptr(), int(block_size), taken_out.data_ptr(),
+                                   workspace.data_ptr() if ws_bytes else 0, ws_bytes, _raw_stream(dev))
     if code:
         _lib.check("sfa_blocks_free", code)
     return taken_out

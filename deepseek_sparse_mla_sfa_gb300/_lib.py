@@ -60,7 +60,8 @@ SIGNATURES = {
     "sfa_decode_tree_workspace_bytes": ([I, I, I], SZ),
     "sfa_decode_tree": ([P, P, P, P, P, P, I, I, I, I, I, I, I, F, I, P, P, P, SZ, P], I),
     "sfa_blocks_fork": ([P, I, I, P, P, P, I, P, I, P, I, P, I, P, P, P], I),
-    "sfa_blocks_free": ([P, P, P, I, I, P, I, P, I, P, I, P, P], I),
+    "sfa_blocks_free_workspace_bytes": ([I, I], SZ),
+    "sfa_blocks_free": ([P, P, P, I, I, P, I, P, I, P, I, P, P, SZ, P], I),
     "sfa_blocks_compact": ([P, P, I, I, P, I, P, I, P, I, I, P, P, P, P, P], I),
     "sfa_kv_copy_blocks": ([P, I, I, I, P, I, P], I),
     "sfa_kv_copy_blocks_q8": ([P, P, I, I, I, I, P, I, P], I),

@@ -763,10 +763,17 @@ sfa_status sfa_blocks_fork(int32_t* block_table, int rows, int max_blocks_per_se
                                       static_cast<cudaStream_t>(stream)));
 }
 
+size_t sfa_blocks_free_workspace_bytes(int rows, int max_blocks_per_seq) {
+  if (rows < 1 || max_blocks_per_seq < 1 || rows > SFA_PLAN_MAX_REQUESTS ||
+      (long long)rows * max_blocks_per_seq >= (1 << 30))
+    return 0;
+  return sfa::blocks_free_workspace_bytes(rows, max_blocks_per_seq);
+}
+
 sfa_status sfa_blocks_free(const int32_t* block_table, const int32_t* held_lens, const int32_t* keep_lens, int rows,
                            int max_blocks_per_seq, int32_t* shares, int num_blocks, int32_t* free_blocks,
-                           int num_free, const int32_t* taken, int block_size, int32_t* taken_out,
-                           sfa_stream stream) {
+                           int num_free, const int32_t* taken, int block_size, int32_t* taken_out, void* workspace,
+                           size_t workspace_bytes, sfa_stream stream) {
   if (rows < 0 || max_blocks_per_seq < 1 || num_blocks < 1 || num_free < 0 || block_size < 1)
     return SFA_ERR_INVALID_ARG;
   if (rows > SFA_PLAN_MAX_REQUESTS || (long long)rows * max_blocks_per_seq >= (1 << 30)) return SFA_ERR_UNSUPPORTED;
@@ -774,12 +781,15 @@ sfa_status sfa_blocks_free(const int32_t* block_table, const int32_t* held_lens,
       (rows > 0 && (!block_table || !held_lens || !keep_lens)))
     return SFA_ERR_INVALID_ARG;
   for (const void* ptr : {(const void*)block_table, (const void*)held_lens, (const void*)keep_lens,
-                          (const void*)shares, (const void*)free_blocks, (const void*)taken, (const void*)taken_out})
+                          (const void*)shares, (const void*)free_blocks, (const void*)taken, (const void*)taken_out,
+                          (const void*)workspace})
     if (!aligned(ptr, 4)) return SFA_ERR_INVALID_ARG;
+  const size_t need = sfa::blocks_free_workspace_bytes(rows, max_blocks_per_seq);
+  if (need && (!workspace || workspace_bytes < need)) return SFA_ERR_WORKSPACE;
   int* status = current_status();
   if (!status) return SFA_ERR_CUDA;
   return done(sfa::launch_blocks_free(block_table, held_lens, keep_lens, rows, max_blocks_per_seq, shares, num_blocks,
-                                      free_blocks, num_free, taken, block_size, taken_out, status,
+                                      free_blocks, num_free, taken, block_size, taken_out, workspace, status,
                                       static_cast<cudaStream_t>(stream)));
 }
 

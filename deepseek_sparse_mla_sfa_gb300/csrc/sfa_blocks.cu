@@ -10,10 +10,11 @@
 // Every output is a function of the inputs alone: counts come from commutative atomics, the order of
 // freed blocks from the first place that names them, ranks from prefix sums.
 //
-// free and compact run as one cluster whose CTAs split the table's entries (and, for compact, the
-// pool's bitmaps) and meet at cluster barriers: no workspace, one launch.
+// compact runs as one cluster whose CTAs split the table's entries and the pool's bitmaps and meet
+// at cluster barriers: no workspace, one launch.
 // Bound: latency (a chain of launch, lengths, table, block counters and the barriers between them)
 // up to some 10^5 table entries; kv_copy_blocks: HBM.
+#include <algorithm>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -41,19 +42,16 @@ __device__ __forceinline__ int block_exclusive_sum(int v, int* part, int& total)
   __syncthreads();   // part may still be read
   if (lane == 31) part[warp] = in;
   __syncthreads();
-  int before = 0;
-  total = 0;
-  for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += part[w];
-    total += part[w];
-  }
+  const int w = lane < warps ? part[lane] : 0;   // (at most 32 warps)
+  const int before = __reduce_add_sync(0xffffffffu, lane < warp ? w : 0);
+  total = __reduce_add_sync(0xffffffffu, w);
   return before + in - v;
 }
 
 // blocks that `tokens` positions take, at most `most`
 __device__ __forceinline__ int blocks_for(int tokens, int block_size, int most) {
-  const long long n = ((long long)max(tokens, 0) + block_size - 1) / block_size;
-  return n < most ? (int)n : most;
+  const unsigned n = ((unsigned)max(tokens, 0) + (unsigned)(block_size - 1)) / (unsigned)block_size;   // (below 2^32)
+  return (int)min(n, (unsigned)most);
 }
 
 // the last entry e of the non-decreasing a[0..n) with a[e] <= x (a[0] <= x)
@@ -164,6 +162,7 @@ struct FreeParams {
   const int32_t* taken;
   int block_size;
   int32_t* taken_out;
+  int* counts;                             // workspace [grid]: blocks that a CTA's entries put back
   int* status;
 };
 
@@ -176,100 +175,158 @@ template <class Count>
 __device__ __forceinline__ int row_sums(int rows, int* sums, int* part, Count count) {
   const int per = (rows + blockDim.x - 1) / blockDim.x;
   const int r0 = min((int)threadIdx.x * per, rows), r1 = min(r0 + per, rows);
-  long long mine = 0;
-  for (int r = r0; r < r1; ++r) mine += count(r);
+  int mine = 0;
+  for (int r = r0; r < r1; ++r) mine += sums[r] = count(r);
   int total;
-  int at = block_exclusive_sum((int)mine, part, total);
+  int at = block_exclusive_sum(mine, part, total);
   for (int r = r0; r < r1; ++r) {
+    const int n = sums[r];
     sums[r] = at;
-    at += count(r);
+    at += n;
   }
   if (threadIdx.x == 0) sums[rows] = total;
   __syncthreads();
   return total;
 }
 
-template <int kCtas>
+// The entries between the kept and the held positions, counted through the rows, are dealt to the
+// CTAs in ranges, and four steps follow one another: every entry takes a share of its block; entries of
+// blocks below zero leave the lowest entry's number there; a CTA counts the blocks that its
+// entries put back; they go to their places.  kStep 0: one cluster does the four, barriers between
+// them.  1 to 4: a launch each, since the next step needs all of the one before; a launch fetches
+// the lengths and its first entries while the one before it ends.
+// Bound: latency, three to four dependent accesses a step.  No warp meets more than kFreeHeld * 32
+// entries at a time, which stay in registers from the table to the last step.
+constexpr int kFreeCtas = 152, kFreeHeld = 4, kFreeWarps = kClusterThreads / 32, kFreeRound = kFreeHeld * kClusterThreads;
+
+template <int kStep>
 __global__ void __launch_bounds__(kClusterThreads) blocks_free_kernel(const FreeParams p) {
-  extern __shared__ int sums[];            // [rows + 1]
-  __shared__ int part[kClusterThreads / 32];
-  __shared__ int pushed;                   // blocks that this CTA's entries free
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = kCtas > 1 ? (int)cluster.block_rank() : 0;
-  auto meet = [&] {
-    if (kCtas > 1) {
+  extern __shared__ int sums[];            // [rows + 1], then [rows]: where in the table a row's entries begin
+  int* firsts = sums + p.rows + 1;
+  __shared__ int part[kFreeWarps];
+  __shared__ int puts_here;
+  constexpr bool kAll = kStep == 0;
+  auto meet = [] {
+    if (gridDim.x > 1) {
       __threadfence();
-      cluster.sync();
+      cg::this_cluster().sync();
     } else {
       __syncthreads();
     }
   };
-  auto kept = [&](int r) { return blocks_for(p.keep[r], p.block_size, p.max_blocks); };
+  const int rank = blockIdx.x, ctas = gridDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  if (!kAll) asm volatile("griddepcontrol.launch_dependents;");
   const int total = row_sums(p.rows, sums, part, [&](int r) {
-    return max(0, blocks_for(p.held[r], p.block_size, p.max_blocks) - kept(r));
+    const int kept = blocks_for(p.keep[r], p.block_size, p.max_blocks);
+    firsts[r] = r * p.max_blocks + kept;
+    return max(0, blocks_for(p.held[r], p.block_size, p.max_blocks) - kept);
   });
-  const int each = (total + kCtas - 1) / kCtas;
-  const int e0 = min(rank * each, total), e1 = min(e0 + each, total);
-  auto entry = [&](int e) -> int {         // the block that entry e names, -1 if none
-    const int r = last_at_most(sums, p.rows, e);
-    const int x = p.table[(size_t)r * p.max_blocks + kept(r) + (e - sums[r])];
-    return x >= 0 && x < p.num_blocks ? x : -1;
+  const int each = (total + ctas - 1) / ctas;
+  const int e0 = (int)min((long long)rank * each, (long long)total), e1 = min(e0 + each, total);
+  int x[kFreeHeld];                        // the blocks that the lane's entries name, -1 if none
+  auto first = [&](int round) { return e0 + round * kFreeRound + warp * kFreeHeld * 32 + lane; };
+  auto fetch = [&](int round) {
+    const int e = first(round);
+    int row[kFreeHeld] = {};
+    for (int n = p.rows; n > 1;) {         // each row[u] begins the n rows in which entry u's is
+      const int half = n >> 1;
+#pragma unroll
+      for (int u = 0; u < kFreeHeld; ++u)
+        if (sums[row[u] + half] <= e + 32 * u) row[u] += half;
+      n -= half;
+    }
+#pragma unroll
+    for (int u = 0; u < kFreeHeld; ++u)
+      x[u] = e + 32 * u < e1 ? p.table[firsts[row[u]] - sums[row[u]] + e + 32 * u] : -1;
+#pragma unroll
+    for (int u = 0; u < kFreeHeld; ++u)
+      if (x[u] < 0 || x[u] >= p.num_blocks) x[u] = -1;
   };
+  const int rounds = (e1 - e0 + kFreeRound - 1) / kFreeRound;
+  fetch(0);
+  if (!kAll) asm volatile("griddepcontrol.wait;" ::: "memory");
   bool bad = false;
-  for (int e = e0 + threadIdx.x; e < e1; e += kClusterThreads) {
-    const int x = entry(e);
-    if (x >= 0) atomicSub(p.shares + x, 1); else bad = true;
-  }
-  meet();
+  if (kAll || kStep == 1)
+    for (int i = 0; i < rounds; ++i) {
+      if (i > 0) fetch(i);
+#pragma unroll
+      for (int u = 0; u < kFreeHeld; ++u) {
+        if (x[u] >= 0) atomicSub(p.shares + x[u], 1);
+        else if (first(i) + 32 * u < e1) bad = true;
+      }
+    }
+  if (kAll) meet();
   // below zero: free, and the first entry that names it puts it back
-  for (int e = e0 + threadIdx.x; e < e1; e += kClusterThreads) {
-    const int x = entry(e);
-    if (x < 0) continue;
-    const int v = __ldcg(p.shares + x);
-    if (v >= 0) continue;
-    if (v < -1 && v > INT_MIN / 2) bad = true;   // given back more often than held
-    atomicMin(p.shares + x, kMarked + e);
-  }
-  meet();
-  int mine = 0;
-  for (int e = e0 + threadIdx.x; e < e1; e += kClusterThreads) {
-    const int x = entry(e);
-    mine += x >= 0 && __ldcg(p.shares + x) == kMarked + e;
-  }
-  int sum;
-  (void)block_exclusive_sum(mine, part, sum);
-  if (threadIdx.x == 0) pushed = sum;
-  meet();
-  int before = 0, all = 0;
-  if (kCtas > 1) {
-    for (int c = 0; c < kCtas; ++c) {
-      const int v = *cluster.map_shared_rank(&pushed, c);
-      if (c < rank) before += v;
-      all += v;
+  if (kAll || kStep == 2)
+    for (int i = 0; i < rounds; ++i) {
+      if (i > 0) fetch(i);
+      int v[kFreeHeld];
+#pragma unroll
+      for (int u = 0; u < kFreeHeld; ++u) v[u] = x[u] >= 0 ? __ldcg(p.shares + x[u]) : 0;
+#pragma unroll
+      for (int u = 0; u < kFreeHeld; ++u)
+        if (v[u] < 0) {
+          if (v[u] < -1 && v[u] > INT_MIN / 2) bad = true;   // given back more often than held
+          atomicMin(p.shares + x[u], kMarked + first(i) + 32 * u);
+        }
     }
-  } else {
-    all = pushed;
-  }
-  const int head = min(max(*p.taken, 0), p.num_free);
-  long long at = (long long)head - all + before;
-  for (int s0 = e0; s0 < e1; s0 += kClusterThreads) {
-    const int e = s0 + threadIdx.x;
-    const int x = e < e1 ? entry(e) : -1;
-    const bool push = x >= 0 && __ldcg(p.shares + x) == kMarked + e;
-    int n;
-    const int k = block_exclusive_sum(push ? 1 : 0, part, n);
-    if (push) {
-      if (at + k >= 0) p.free_blocks[at + k] = x;
-      p.shares[x] = 0;
+  if (kAll) meet();
+  auto puts = [&](int i, bool (&put)[kFreeHeld]) {           // how many of the lane's entries put a block back
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < kFreeHeld; ++u) put[u] = x[u] >= 0 && __ldcg(p.shares + x[u]) == kMarked + first(i) + 32 * u;
+#pragma unroll
+    for (int u = 0; u < kFreeHeld; ++u) n += put[u];
+    return n;
+  };
+  bool put[kFreeHeld];
+  int all = 0, before = 0;
+  if (kAll || kStep == 3) {
+    int mine = 0;
+    for (int i = 0; i < rounds; ++i) {
+      if (i > 0) fetch(i);
+      mine += puts(i, put);
     }
-    at += n;
+    (void)block_exclusive_sum(mine, part, all);
+    if (threadIdx.x == 0) (kAll ? puts_here : p.counts[rank]) = all;
+  }
+  if (kAll) meet();
+  if (kAll || kStep == 4) {
+    int n = 0;
+    if (threadIdx.x < ctas) n = kAll ? *cg::this_cluster().map_shared_rank(&puts_here, threadIdx.x) : __ldcg(p.counts + threadIdx.x);
+    (void)block_exclusive_sum(threadIdx.x < rank ? n : 0, part, before);
+    (void)block_exclusive_sum(n, part, all);
+  }
+  if (kAll || kStep == 4) {
+    const int head = min(max(*p.taken, 0), p.num_free);
+    int at = head - all + before;          // (-all may be below the list's begin)
+    for (int i = 0; i < rounds; ++i) {
+      if (i > 0) fetch(i);
+      if (!kAll) (void)puts(i, put);
+      unsigned votes[kFreeHeld];
+      int mine = 0, n;
+#pragma unroll
+      for (int u = 0; u < kFreeHeld; ++u) mine += __popc(votes[u] = __ballot_sync(0xffffffffu, put[u]));
+      int k = block_exclusive_sum(lane == 0 ? mine : 0, part, n);
+      k = at + __shfl_sync(0xffffffffu, k, 0);
+#pragma unroll
+      for (int u = 0; u < kFreeHeld; ++u) {
+        const int to = k + __popc(votes[u] & ((1u << lane) - 1));
+        if (put[u]) {
+          if (to >= 0) p.free_blocks[to] = x[u];
+          p.shares[x[u]] = 0;
+        }
+        k += __popc(votes[u]);
+      }
+      at += n;
+    }
+    if (rank == 0 && threadIdx.x == 0) {
+      if (all > head) report_status(p.status, kStatusNoBlocks);
+      *p.taken_out = max(head - all, 0);
+    }
   }
   if (bad) report_status(p.status, kStatusBadBlock);
-  if (rank == 0 && threadIdx.x == 0) {
-    if (all > head) report_status(p.status, kStatusNoBlocks);
-    *p.taken_out = max(head - all, 0);
-  }
-  if (kCtas > 1) cluster.sync();           // `pushed` is read by the others
+  if (kAll) meet();                        // the others read puts_here
 }
 
 // ------------------------------------------------------------------------- compact
@@ -512,8 +569,10 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const Copy
   }
 }
 
+// after: begins while the launch before it on the stream ends (and waits for it itself)
 template <class Kernel, class Params>
-cudaError_t launch_cluster(Kernel kernel, int ctas, size_t smem, const Params& p, cudaStream_t stream) {
+cudaError_t launch_ctas(Kernel kernel, int ctas, int cluster, size_t smem, const Params& p, cudaStream_t stream,
+                        bool after = false) {
   if (smem > 40 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -523,12 +582,14 @@ cudaError_t launch_cluster(Kernel kernel, int ctas, size_t smem, const Params& p
   cfg.blockDim = dim3(kClusterThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = cluster;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = after ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
@@ -545,16 +606,33 @@ cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t
   return cudaGetLastError();
 }
 
+// CTAs: one for each round of the table's entries, up to a cluster (one launch); else one for each
+// kClusterThreads entries, at most one for each SM
+static int free_ctas(int rows, int max_blocks) {
+  const long long entries = (long long)rows * max_blocks;
+  if (entries <= kClusterCtas * kFreeRound) return std::max(1, (int)((entries + kFreeRound - 1) / kFreeRound));
+  return (int)std::min<long long>((entries + kClusterThreads - 1) / kClusterThreads, kFreeCtas);
+}
+
+size_t blocks_free_workspace_bytes(int rows, int max_blocks) {
+  const int ctas = free_ctas(rows, max_blocks);
+  return ctas > kClusterCtas ? (size_t)ctas * 4 : 0;
+}
+
 cudaError_t launch_blocks_free(const int32_t* table, const int32_t* held, const int32_t* keep, int rows,
                                int max_blocks, int32_t* shares, int num_blocks, int32_t* free_blocks, int num_free,
-                               const int32_t* taken, int block_size, int32_t* taken_out, int* status,
+                               const int32_t* taken, int block_size, int32_t* taken_out, void* workspace, int* status,
                                cudaStream_t stream) {
   const FreeParams p{table, held, keep, rows, max_blocks, shares, num_blocks, free_blocks, num_free, taken,
-                     block_size, taken_out, status};
-  const size_t smem = (size_t)(rows + 1) * 4;
-  if ((long long)rows * max_blocks <= 4 * kClusterThreads)
-    return launch_cluster(blocks_free_kernel<1>, 1, smem, p, stream);
-  return launch_cluster(blocks_free_kernel<kClusterCtas>, kClusterCtas, smem, p, stream);
+                     block_size, taken_out, static_cast<int*>(workspace), status};
+  const size_t smem = (size_t)(2 * rows + 1) * 4;
+  const int ctas = free_ctas(rows, max_blocks);
+  if (ctas <= kClusterCtas) return launch_ctas(blocks_free_kernel<0>, ctas, ctas, smem, p, stream);
+  cudaError_t e = launch_ctas(blocks_free_kernel<1>, ctas, 1, smem, p, stream);
+  if (e == cudaSuccess) e = launch_ctas(blocks_free_kernel<2>, ctas, 1, smem, p, stream, true);
+  if (e == cudaSuccess) e = launch_ctas(blocks_free_kernel<3>, ctas, 1, smem, p, stream, true);
+  if (e == cudaSuccess) e = launch_ctas(blocks_free_kernel<4>, ctas, 1, smem, p, stream, true);
+  return e;
 }
 
 cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int rows, int max_blocks,
@@ -568,8 +646,8 @@ cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int
   const CompactParams p{table, lens, rows, max_blocks, shares, num_blocks, free_blocks, num_free, taken, block_size,
                         max_moves, words, table_out, shares_out, free_out, copies, status};
   const size_t smem = (size_t)words * 20 + (size_t)(rows + 1) * 4;
-  if (small) return launch_cluster(blocks_compact_kernel<1>, 1, smem, p, stream);
-  return launch_cluster(blocks_compact_kernel<kClusterCtas>, kClusterCtas, smem, p, stream);
+  if (small) return launch_ctas(blocks_compact_kernel<1>, 1, 1, smem, p, stream);
+  return launch_ctas(blocks_compact_kernel<kClusterCtas>, kClusterCtas, kClusterCtas, smem, p, stream);
 }
 
 cudaError_t launch_kv_copy_blocks(void* kv, float* scales, int group, int row_bytes, int layers, int num_blocks,

@@ -184,8 +184,9 @@ cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t
                                int* status, cudaStream_t stream);
 cudaError_t launch_blocks_free(const int32_t* table, const int32_t* held, const int32_t* keep, int rows,
                                int max_blocks, int32_t* shares, int num_blocks, int32_t* free_blocks, int num_free,
-                               const int32_t* taken, int block_size, int32_t* taken_out, int* status,
+                               const int32_t* taken, int block_size, int32_t* taken_out, void* workspace, int* status,
                                cudaStream_t stream);
+size_t blocks_free_workspace_bytes(int rows, int max_blocks);
 cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int rows, int max_blocks,
                                   const int32_t* shares, int num_blocks, const int32_t* free_blocks, int num_free,
                                   const int32_t* taken, int block_size, int max_moves, int32_t* table_out,

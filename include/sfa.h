@@ -505,12 +505,16 @@ sfa_status sfa_blocks_fork(int32_t *block_table, int rows, int max_blocks_per_se
  *                order in which rows and entries name them first
  *   taken_out    *taken less the blocks freed; where that is below 0 the first ones are lost and
  *                SFA_ERR_DEVICE_NO_BLOCKS is set
+ *   workspace    device, sfa_blocks_free_workspace_bytes(rows, max_blocks_per_seq) bytes (0 for small
+ *                tables), 4-byte aligned; SFA_ERR_WORKSPACE when missing or too small.  Calls that may run
+ *                at once need one each
  *   rows <= SFA_PLAN_MAX_REQUESTS, rows * max_blocks_per_seq < 2^30.  The table is left as it is.
  */
+size_t sfa_blocks_free_workspace_bytes(int rows, int max_blocks_per_seq);
 sfa_status sfa_blocks_free(const int32_t *block_table, const int32_t *held_lens, const int32_t *keep_lens, int rows,
                            int max_blocks_per_seq, int32_t *shares, int num_blocks, int32_t *free_blocks,
                            int num_free, const int32_t *taken, int block_size, int32_t *taken_out,
-                           sfa_stream stream);
+                           void *workspace, size_t workspace_bytes, sfa_stream stream);
 
 /*
  * sfa_blocks_compact -- held blocks move to the front of the pool: the k-th lowest free block takes

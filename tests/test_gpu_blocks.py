@@ -80,7 +80,8 @@ def test_fork_reports_what_does_not_fit():
 
 
 # -------------------------------------------------------------------------------- free
-@pytest.mark.parametrize("R,bs,most", [(1, 16, 40), (64, 64, 8192), (700, 16, 3000), (8192, 64, 130), (3, 1, 2000), (0, 4, 1)])
+@pytest.mark.parametrize("R,bs,most", [(1, 16, 40), (64, 64, 8192), (700, 16, 3000), (8192, 64, 130), (400, 1, 5000), (3, 1, 2000),
+                                       (0, 4, 1)])
 @pytest.mark.parametrize("shared", [False, True])
 def test_free_matches_oracle(R, bs, most, shared):
     rng = np.random.default_rng(R + bs)

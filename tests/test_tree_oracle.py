@@ -90,7 +90,7 @@ DECODE = dict(q=FAKE, kv=FAKE, table=FAKE, cached=FAKE, start=FAKE, mask=FAKE, B
 FORK = dict(table=FAKE, rows=3, mb=2, lens=FAKE, src=FAKE, dst=FAKE, n=1, shares=FAKE, nb=4, free=FAKE, F=4,
             taken=FAKE, bs=16, copies=FAKE, out=ctypes.c_void_p(1 << 21), stream=P0)
 FREE = dict(table=FAKE, held=FAKE, keep=FAKE, rows=3, mb=2, shares=FAKE, nb=4, free=FAKE, F=4, taken=FAKE, bs=16,
-            out=ctypes.c_void_p(1 << 21), stream=P0)
+            out=ctypes.c_void_p(1 << 21), ws=FAKE, wsb=1 << 20, stream=P0)
 COMPACT = dict(table=FAKE, lens=FAKE, rows=3, mb=2, shares=FAKE, nb=4, free=FAKE, F=4, taken=FAKE, bs=16, moves=2,
                t2=ctypes.c_void_p(1 << 21), s2=ctypes.c_void_p(1 << 22), f2=ctypes.c_void_p(1 << 23), copies=FAKE, stream=P0)
 COPY = dict(kv=FAKE, layers=1, nb=4, bs=16, copies=FAKE, n=1, stream=P0)
@@ -139,6 +139,18 @@ def test_decode_tree_wants_its_workspace(lib):
         assert _call(lib, "sfa_decode_tree", DECODE, wsb=need - 1) == -3
         assert _call(lib, "sfa_decode_tree", DECODE, ws=P0, wsb=need) == -3
         assert _call(lib, "sfa_decode_tree", DECODE, ws=ctypes.c_void_p((1 << 20) + 16), wsb=need) == -3
+
+
+def test_blocks_free_wants_its_workspace(lib):
+    assert lib.sfa_blocks_free_workspace_bytes(512, 64) == 0     # a cluster's registers hold the entries
+    assert lib.sfa_blocks_free_workspace_bytes(513, 64) > 0
+    assert lib.sfa_blocks_free_workspace_bytes(8193, 64) == 0 and lib.sfa_blocks_free_workspace_bytes(-1, 64) == 0
+    need = lib.sfa_blocks_free_workspace_bytes(700, 1026)
+    assert need == 152 * 4
+    kw = dict(rows=700, mb=1026)
+    assert _call(lib, "sfa_blocks_free", FREE, wsb=need - 1, **kw) == -3
+    assert _call(lib, "sfa_blocks_free", FREE, ws=P0, wsb=need, **kw) == -3
+    assert _call(lib, "sfa_blocks_free", FREE, ws=ODD, wsb=need, **kw) == -1
 
 
 def test_binding_refuses_what_does_not_fit():
