@@ -376,6 +376,91 @@ def test_decode_of_more_nodes_than_the_mask_has_bits(path):
     assert np.nanmax(np.abs(out.double().cpu().numpy() - w[0])[:64]) < 2e-2
 
 
+@pytest.mark.parametrize("cached,nodes,h,bs", [([3], [4], 16, 16), ([60, 250], [4, 9], 128, 64), ([300], [16], 5, 7)])
+def test_decode_in_fp32_is_closer_than_bf16_weights(path, cached, nodes, h, bs):
+    # fp32 results take the weights in two bf16 terms: what the second leaves is half a step of half a step, 2^-16 of
+    # a weight.  Besides it the scores' 2^-18 sum |q k| (twice, numerator and sum), exponentials (2^-20, twice), and
+    # sums of P positions in fp32, each step at most 2^-23 of sum w |v| (by rounding or by cutting off).
+    p = problem(50 + h, cached, nodes, h, bs, std=0.1)
+    out, lse = sfa.decode_tree(**device(p))
+    assert sfa.last_device_status() == 0
+    w_out, w_lse, wabs, smax = tree.decode_tree(p["q"].double().numpy(), p["kv"].double().numpy(), p["table"], p["cached"],
+                                                p["start"], p["mask"], p["scale"], p["most"])
+    real = ~np.isnan(w_lse)
+    tol = (2.0 ** -16 + 2 * (2.0 ** -18 * smax + 2.0 ** -20) + 2.0 ** -23 * max(np.add(cached, nodes)))[..., None] * wabs
+    assert np.all(np.abs(out.double().cpu().numpy() - w_out)[real] <= (tol + 2.0 ** -22 * np.abs(w_out))[real])
+
+
+def test_decode_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    p = problem(60, [700, 30], [9, 4], 128, 64)
+    d = device(p)
+    prev, stall = sfa.set_wait_limit(1000), sfa.set_stall_injection(True)
+    try:
+        sfa.decode_tree(**d)
+        status = sfa.last_device_status()
+    finally:
+        sfa.set_stall_injection(stall)
+        sfa.set_wait_limit(prev)
+    assert status == TIMEOUT
+    run(p)
+
+
+def test_decode_on_two_streams_at_once(path):
+    probs = [problem(70 + i, c, n, 32, 64) for i, (c, n) in enumerate((([5000, 40], [12, 3]), ([300] * 9, [5] * 9)))]
+    ds = [device(p) for p in probs]
+    streams = [torch.cuda.Stream() for _ in probs]
+    ws = [torch.full((max(sfa.decode_tree_workspace_bytes(len(p["cached"]), p["q"].shape[0], 32), 1),), 255, dtype=torch.uint8,
+                     device="cuda") for p in probs]
+    torch.cuda.synchronize()
+    got = [None, None]
+    for _ in range(10):
+        for i in (0, 1):
+            got[i] = sfa.decode_tree(**ds[i], workspace=ws[i], stream=streams[i])
+    torch.cuda.synchronize()
+    assert sfa.last_device_status() == 0
+    for p, x in zip(probs, got):
+        check(p, x)
+
+
+@pytest.mark.parametrize("bs", [64, 24, 7])
+def test_decode_of_blocks_past_four_gigabytes(path, bs):
+    p = problem(80, [333, 100], [5, 9], 8, bs)
+    d = device(p)
+    nb = (1 << 22) // bs                                   # 4.8 GB of rows; the sequences' blocks lie at the end
+    small, kv = d["kv"], torch.empty((nb, bs, 576), dtype=torch.bfloat16, device="cuda")
+    kv[nb - small.shape[0]:] = small
+    table = np.where(p["table"] >= 0, p["table"] + nb - small.shape[0], -1)
+    got = sfa.decode_tree(**dict(d, kv=kv, block_table=i32(table)))
+    assert sfa.last_device_status() == 0
+    check(p, got)
+    path_, acc = i32([[1, 4, -1], [2, 3, 8]]), i32([2, 3])
+    sfa.kv_commit(kv, i32(table), i32(p["cached"]), path_, acc)
+    assert sfa.last_device_status() == 0
+    want = tree.kv_commit(p["kv"].float().numpy(), p["table"], p["cached"], path_.cpu().numpy(), [2, 3])
+    assert np.array_equal(kv[nb - small.shape[0]:].float().cpu().numpy(), want)
+
+
+def test_decode_refuses_other_shapes_and_devices():
+    p = problem(90, [20], [4], 4, 16)
+    d = device(p)
+    for kw, err in ((dict(q=d["q"].float()), TypeError), (dict(kv=d["kv"][:, :, :512].contiguous()), ValueError),
+                    (dict(mask=d["mask"].int()), TypeError), (dict(mask=d["mask"][:-1]), ValueError),
+                    (dict(block_table=d["block_table"].cpu()), ValueError), (dict(cached_lens=d["cached_lens"].cpu()), ValueError),
+                    (dict(token_start=d["token_start"][:1]), ValueError), (dict(q=d["q"].transpose(0, 1)), ValueError),
+                    (dict(out=torch.empty((6, 4, 512), device="cuda", dtype=torch.float16)), TypeError),
+                    (dict(out=torch.empty((5, 4, 512), device="cuda")), ValueError),
+                    (dict(lse=torch.empty((6, 4, 1), device="cuda")), ValueError),
+                    (dict(workspace=torch.empty(1 << 20, dtype=torch.uint8)), ValueError),
+                    (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), sfa.SfaError)):
+        with pytest.raises(err):
+            sfa.decode_tree(**dict(d, **kw))
+    with pytest.raises(ValueError):
+        sfa.decode_tree(**dict(d, q=torch.zeros((6, 129, 576), dtype=torch.bfloat16, device="cuda")), out=torch.empty((6, 4, 512), device="cuda"))
+    with pytest.raises(sfa.SfaError):
+        sfa.decode_tree(**dict(d, q=torch.zeros((6, 129, 576), dtype=torch.bfloat16, device="cuda")))
+    assert sfa.last_device_status() == 0
+
+
 # ------------------------------------------------------------------------------ together
 def test_steps_of_drafted_trees():
     """Three steps over one pool: blocks from the step plan, rows by the cache write, attention, path,
