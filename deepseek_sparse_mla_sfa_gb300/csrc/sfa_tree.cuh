@@ -18,6 +18,9 @@ __device__ __forceinline__ int tree_request(const int32_t* token_start, int B, i
   return lo;
 }
 
+// positions that a row of the block table reaches
+__device__ __forceinline__ long long tree_reach(const TreeParams& p) { return (long long)p.max_blocks * p.block_size; }
+
 constexpr int kTreeSimtWarps = 4;
 constexpr int tree_simt_smem(int heads) {
   return 4 * (heads * kDQK + kTreeSimtWarps * heads * kDV + 2 * kTreeSimtWarps * heads);
@@ -68,6 +71,7 @@ __device__ __forceinline__ void tree_simt(const TreeParams& p, int t, int h0, fl
     for (int c = 0; c < 2 * kV; ++c) o[hh][c] = 0.f;
   }
   for (long long pos = warp; pos < (long long)cached + n; pos += kWarps) {
+    if (pos >= tree_reach(p) && pos + kWarps < cached) pos += (cached - 1 - pos) / kWarps * kWarps;   // no blocks there
     if (pos >= cached) {
       const int j = (int)(pos - cached);
       if (!(mask[j / 64] >> (j % 64) & 1)) continue;

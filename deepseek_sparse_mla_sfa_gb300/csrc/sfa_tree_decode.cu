@@ -103,8 +103,9 @@ struct Workspace {
   Partial* list;     // [slots]
   float* part;       // [slots][cap][512]
   float* lse;        // [slots][cap]
-  int2* bad;         // [2 * pairs]: requests to compute again, first and last
+  int2* bad;         // [2 * pairs + 1]: requests to compute again, first and last (the schedule's: at all)
   int cap, slots;    // rows of a slot, slots
+  int most;          // pieces that there is room for
 };
 
 struct TreeTcParams {
@@ -236,7 +237,8 @@ __device__ __forceinline__ Request request_of(const TreeParams& p, int b, int li
   r.cached = max(p.cached[b], 0);
   r.tiles = (int)(((long long)r.cached + r.n + kTile - 1) / kTile);
   r.cuts = r.cached / kTile;
-  r.units = r.n > 0 ? (r.n * p.h + kRows - 1) / kRows : 0;
+  // (cached positions behind the block table: all that there is, the last kernel computes)
+  r.units = r.n > 0 && r.cached <= tree_reach(p) ? (r.n * p.h + kRows - 1) / kRows : 0;
   r.chunks = 1;
   r.len = r.tiles;
   if (r.tiles > limit) {
@@ -328,6 +330,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   __shared__ Piece kept[kMaxPairs][kKept];
   __shared__ int n_of[3], split_of[3];
   __shared__ float cost_of[3], tiles_of, far_of;
+  __shared__ int bad_s[2];                                  // first and last request for the last kernel alone
   const TreeParams& p = tp.p;
   const int tid = threadIdx.x, lane = tid % 32, pairs = tp.pairs;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -338,7 +341,12 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     n_of[tid] = split_of[tid] = 0;
     cost_of[tid] = 0.f;
   }
-  if (tid == 0) tiles_of = far_of = 0.f;
+  if (tid == 0) {
+    tiles_of = far_of = 0.f;
+    bad_s[0] = 0x7fffffff;
+    bad_s[1] = -1;
+  }
+  __syncthreads();
   long long cost = 0;                          // of the units
   float tiles = 0.f, far = 0.f;                // their tiles; tiles of different rows
   for (int b = r0; b < r1; ++b) {
@@ -349,6 +357,10 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     if (p.B <= kPlanThreads) requests[b] = r;
     if (min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
       report_status(p.status, kStatusBadTree);
+    if (r.n > 0 && r.units == 0) {
+      atomicMin(&bad_s[0], b);
+      atomicMax(&bad_s[1], b);
+    }
   }
   long long total;
   long long at = block_before(cost, part, total);
@@ -539,11 +551,16 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   long long all;                               // (both counts in one sum)
   const long long before = block_before((long long)pieces << 32 | partials, part, all);
   int at_piece = (int)(before >> 32), at_partial = (int)(before & 0xffffffff);
-  if (have) tp.ws.start[tid] = at_piece;
+  // Requests whose tokens overlap can have more units than the workspace holds pieces: nothing is done then.
+  const bool fits = (all >> 32) <= tp.ws.most && (all & 0xffffffff) <= tp.ws.slots;
+  if (have) tp.ws.start[tid] = fits ? at_piece : 0;
   if (tid == 0) {
-    tp.ws.start[pairs] = (int)(all >> 32);
-    *tp.ws.partials = (int)(all & 0xffffffff);
+    tp.ws.start[pairs] = fits ? (int)(all >> 32) : 0;
+    *tp.ws.partials = fits ? (int)(all & 0xffffffff) : 0;
+    tp.ws.bad[2 * pairs] = make_int2(bad_s[0], bad_s[1]);
+    if (!fits) report_status(p.status, kStatusBadTree);
   }
+  if (!fits) return;
   auto write = [&](Piece x) {
     if (x.slot == 0) {
       x.slot = at_partial;
@@ -1083,7 +1100,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int partials = min(*tp.ws.partials, tp.ws.slots);
   int any = 0;
-  for (int j = tid; j < 2 * tp.pairs; j += kJoinThreads) any |= tp.ws.bad[j].x <= tp.ws.bad[j].y;
+  for (int j = tid; j <= 2 * tp.pairs; j += kJoinThreads) any |= tp.ws.bad[j].x <= tp.ws.bad[j].y;
   any = __syncthreads_or(any);
   int n_begins = 0, n_rows = 0;
   for (int j0 = 0; j0 < partials; j0 += kJoinThreads) {
@@ -1141,7 +1158,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
     }
     bool skip = false;                         // all of the request is computed again below
     if (any)
-      for (int j = 0; j < 2 * tp.pairs; ++j) skip |= tp.ws.bad[j].x <= me.request && me.request <= tp.ws.bad[j].y;
+      for (int j = 0; j <= 2 * tp.pairs; ++j) skip |= tp.ws.bad[j].x <= me.request && me.request <= tp.ws.bad[j].y;
     for (int it = it0 + warp; it < end && !skip; it += kWarps) {
       const int r = it - rows_before[lo];
       if (r >= tp.ws.cap) break;
@@ -1185,7 +1202,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
   // rare: the nodes of every marked request, a node and two heads at a time
   const int groups = (p.h + kFixHeads - 1) / kFixHeads;
   const int first = blockIdx.x, all = gridDim.x;
-  for (int j = 0; j < 2 * tp.pairs; ++j) {
+  for (int j = 0; j <= 2 * tp.pairs; ++j) {
     const int2 range = tp.ws.bad[j];
     for (int b = max(range.x, 0); b <= min(range.y, p.B - 1); ++b) {
       const Request r = request_of(p, b);
@@ -1216,13 +1233,14 @@ size_t lay_out(char* base, int pairs, int B, int T, int h, Workspace& ws) {
   ws.cap = rows < kRows ? (int)rows : kRows;
   // ranges: two cut units a pair; dealt chunks as many again, where there can be several units of a request
   ws.slots = (rows > kRows ? 4 : 2) * pairs;
-  ws.pieces = reinterpret_cast<Piece*>(part((size_t)(units_at_most(B, T, h) + 2 * ws.slots) * sizeof(Piece)));
+  ws.most = (int)(units_at_most(B, T, h) + 2 * ws.slots);
+  ws.pieces = reinterpret_cast<Piece*>(part((size_t)ws.most * sizeof(Piece)));
   ws.start = reinterpret_cast<int*>(part((size_t)(pairs + 1) * 4));
   ws.partials = reinterpret_cast<int*>(part(4));
   ws.list = reinterpret_cast<Partial*>(part((size_t)ws.slots * sizeof(Partial)));
   ws.part = reinterpret_cast<float*>(part((size_t)ws.slots * ws.cap * kDV * 4));
   ws.lse = reinterpret_cast<float*>(part((size_t)ws.slots * ws.cap * 4));
-  ws.bad = reinterpret_cast<int2*>(part((size_t)2 * pairs * sizeof(int2)));
+  ws.bad = reinterpret_cast<int2*>(part((size_t)(2 * pairs + 1) * sizeof(int2)));
   return at;
 }
 

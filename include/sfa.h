@@ -413,12 +413,14 @@ sfa_status sfa_tree_plan(const int32_t *parents, const int32_t *token_start, con
  *   workspace    device, sfa_decode_tree_workspace_bytes(B, num_tokens, h) bytes, 256-byte aligned;
  *                contents need no initialisation; calls that overlap on the GPU must not share it
  *   B <= SFA_PLAN_MAX_REQUESTS.
- * A position whose block-table entry is outside [0, num_blocks) is skipped and sets
- * SFA_ERR_DEVICE_BAD_BLOCK.  What rows hold that a node does not attend to (other branches, rows
+ * A position whose block-table entry is outside [0, num_blocks), or that lies behind the table, is skipped
+ * and sets SFA_ERR_DEVICE_BAD_BLOCK.  token_start that does not ascend gives rows of several requests any of their
+ * results, or none of the call's with SFA_ERR_DEVICE_BAD_TREE.  What rows hold that a node does not attend to (other branches, rows
  * behind the last node) does not reach its result, NaN and infinities included; a NaN or infinity in
  * a row that it attends to, or in its q, makes its out and lse NaN or infinite.
- * Accuracy: the softmax weights are rounded to bf16 for the second product, out by at most 2^-8 sum_p
- * w_p |kv_p| and its own type's rounding, lse by fp32 rounding.
+ * Accuracy: scores are fp32 sums of exact products.  Where out is bf16 the softmax weights are rounded to
+ * bf16 for the second product: out is off by at most 2^-8 sum_p w_p |kv_p| and its own rounding.  Where out is
+ * fp32 they are taken in two bf16 terms: 2^-16 sum_p w_p |kv_p|.  lse: by fp32 rounding.
  * sfa_set_kernel_path(1) selects a CUDA-core kernel.
  */
 size_t sfa_decode_tree_workspace_bytes(int B, int num_tokens, int h);
@@ -690,7 +692,7 @@ long long sfa_set_wait_limit(long long iterations);
 
 /*
  * sfa_set_stall_injection -- test hook for the failure path: with on != 0, the
- * kernels with bounded waits (the tcgen05 decode kernel and sfa_uv_proj) launched
+ * kernels with bounded waits (the tcgen05 decode kernels, sfa_decode_tree's and sfa_uv_proj) launched
  * afterwards from this process first wait on a barrier that nothing ever completes.
  * That wait runs out after the wait limit (sfa_set_wait_limit), the kernel records
  * SFA_ERR_DEVICE_TIMEOUT, drains its own copies and matrix operations and returns:

@@ -440,6 +440,34 @@ def test_decode_of_blocks_past_four_gigabytes(path, bs):
     assert np.array_equal(kv[nb - small.shape[0]:].float().cpu().numpy(), want)
 
 
+def test_decode_of_lengths_behind_the_table(path):
+    # positions behind the table have no block: what is left is the attention over the table's own
+    for h, n, bs, length in ((16, 5, 16, 4), (8, 3, 7, 2 ** 31 - 1), (128, 2, 64, 70)):
+        p = problem(100 + n, [200, 90], [n, 4], h, bs)
+        reach = p["table"].shape[1] * bs
+        p["table"][0] = np.where(p["table"][0] < 0, p["table"][1, 0], p["table"][0])
+        p["cached"][0] = length if length > reach else reach + length
+        got = sfa.decode_tree(**device(p))
+        assert sfa.last_device_status() == BAD_BLOCK
+        p["cached"][0] = reach
+        p["table"] = np.concatenate([p["table"], np.full((2, 2), -1)], 1)
+        check(p, got, (h, length))
+
+
+def test_decode_of_requests_whose_tokens_overlap(path):
+    p = problem(110, [3], [256], 128, 16, behind=0)
+    d = device(p)
+    B = 19
+    d.update(block_table=d["block_table"].expand(B, -1).contiguous(), cached_lens=d["cached_lens"].expand(B).contiguous(),
+             token_start=i32([0, 256] * 10))
+    out = torch.full((258, 128, 512), 3.0, device="cuda")
+    lse = torch.full((258, 128), 3.0, device="cuda")
+    sfa.decode_tree(**d, out=out[:256], lse=lse[:256])
+    assert sfa.last_device_status() in (0, BAD_TREE)       # more units than 256 tokens have: refused, or any of them
+    assert bool((out[256:] == 3).all()) and bool((lse[256:] == 3).all())
+    run(p)
+
+
 def test_decode_refuses_other_shapes_and_devices():
     p = problem(90, [20], [4], 4, 16)
     d = device(p)
