@@ -13,7 +13,9 @@
 // compact runs as one cluster whose CTAs split the table's entries and the pool's bitmaps and meet
 // at cluster barriers: no workspace, one launch.
 // Bound: latency (a chain of launch, lengths, table, block counters and the barriers between them)
-// up to some 10^5 table entries; kv_copy_blocks: HBM.
+// up to some 10^5 table entries; kv_copy_blocks: HBM.  On the device: fork of 8 and of 512 rows 4 and 5 us;
+// free of 8384 table entries 9 us, of 718000 (323000 freed) 19; compact of 512 blocks 8 us, of 10000 blocks
+// and 10200 entries 19; copies of 2500 blocks of 74 KB in each of two layers 109 us, 6.8 TB/s.
 #include <algorithm>
 #include <climits>
 
@@ -196,7 +198,8 @@ __device__ __forceinline__ int row_sums(int rows, int* sums, int* part, Count co
 // them.  1 to 4: a launch each, since the next step needs all of the one before; a launch fetches
 // the lengths and its first entries while the one before it ends.
 // Bound: latency, three to four dependent accesses a step.  No warp meets more than kFreeHeld * 32
-// entries at a time, which stay in registers from the table to the last step.
+// entries at a time, which stay in registers from the table to the last step.  (A cluster for every table,
+// its entries found and read again in each step: 323000 freed entries 295 us.)
 constexpr int kFreeCtas = 152, kFreeHeld = 4, kFreeWarps = kClusterThreads / 32, kFreeRound = kFreeHeld * kClusterThreads;
 
 template <int kStep>
@@ -607,7 +610,9 @@ cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t
 }
 
 // CTAs: one for each round of the table's entries, up to a cluster (one launch); else one for each
-// kClusterThreads entries, at most one for each SM
+// kClusterThreads entries, at most one for each SM.  2540 entries take 6.8 us by the cluster and 8.8 by
+// the four launches, 8128 10.8 and 9.2, 31750 11.4 and 9.7 in a captured graph; called one by one, a
+// cluster's call takes 16 us and four launches 25.
 static int free_ctas(int rows, int max_blocks) {
   const long long entries = (long long)rows * max_blocks;
   if (entries <= kClusterCtas * kFreeRound) return std::max(1, (int)((entries + kFreeRound - 1) / kFreeRound));
@@ -640,6 +645,8 @@ cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int
                                   const int32_t* taken, int block_size, int max_moves, int32_t* table_out,
                                   int32_t* shares_out, int32_t* free_out, int32_t* copies, int* status,
                                   cudaStream_t stream) {
+  // by one CTA and by a cluster: 128 blocks 7.2 and 12.3 us, 4000 blocks and 3400 entries 13.9 and 15.5,
+  // 10000 blocks and 10200 entries 26.7 and 18.5
   const bool small = (long long)rows * max_blocks <= 4 * kClusterThreads && num_blocks <= 8 * kClusterThreads;
   const int ctas = small ? 1 : kClusterCtas;
   const int all = (num_blocks + 31) / 32, words = (all + ctas - 1) / ctas;

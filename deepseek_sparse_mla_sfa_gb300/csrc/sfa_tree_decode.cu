@@ -20,13 +20,24 @@
 // an MMA of M = 128 takes 64 cycles for N = 256 and 66 for N = 128 (measured): tiles of 128 keys take
 // 1.5 times as long a key.
 //
-// Order of the chunks (16 KB a CTA, a ring of 7, or of 5 beside two terms): K(0), then K(i+1), V(i) by turns, so QK^T of the
-// next tile covers the softmax of this one.  The value columns of the CTA's own keys come twice (as
-// keys and as values); the second time is from L2, which gives 180 GB/s an SM where the ring takes 130.
+// Order of the chunks (16 KB a CTA, a ring of 7, or of 5 beside two terms): K(0), then K(i+1), V(i) by
+// turns, so QK^T of the next tile covers the softmax of this one.  The value columns of the CTA's own keys
+// come twice (as keys and as values); the second time is from L2, which gives 180 GB/s an SM where the
+// ring takes 80.
 //
 // Three launches: a block that lays out who works on what (the schedule, below), the pairs, and the joining
 // of units that several pairs had parts of.
-
+//
+// Bound.  From 128 query rows a request on, the tensor cores: a tile of 256 keys is 4353 cycles of MMAs (6400
+// with two terms), and takes 6300 to 6900 with its rows in L2 (keys awaited 700 to 1000, values 600, P 350;
+// shared memory itself needs 5600 for the MMAs' and the loads' traffic).  16 requests x 16 nodes x 128 heads x
+// 8192 positions, bf16 results: 427 us, 1370 TFLOP/s; 2 x 25 nodes x 64 heads x 131072 positions: 533 us,
+// 1390.  With fewer rows the latency of memory: 64 x 8 nodes x 16 heads x up to 16384 positions, fp32: 207 us
+// where the bytes need 97; a tile takes 11500 cycles, of which 4300 wait for keys (the ring's 5 x 16 KB
+// a CTA are not enough to cover 2500 cycles to memory and back at this rate).  Short calls: latency, 18 of
+// the 27 us of 6 nodes x 4 heads x 200 positions in the pairs' launch (keys 7000 cycles, products and
+// softmax 15000, the result 8000), the rest in the schedule and between the launches.
+//
 // Rows that nobody may see.  Positions behind the last node are brought as rows of zeros.  A cached row
 // of NaN or infinities that only some nodes see would reach the others as 0 x NaN in P V: such a row
 // shows as a score that is not finite in a masked place; the loading warps see a position that a node
@@ -34,8 +45,8 @@
 // cores, which reads only what a node attends to.
 //
 // Warps (512 threads): 0-7 softmax, rescaling, output (the first thread brings q); 8 issues the MMAs (in
-// the pair's first CTA); 9-15 bring keys and values, one a slot of the ring.  Every wait is bounded; one that gives up records
-// SFA_ERR_DEVICE_TIMEOUT and both CTAs unwind.
+// the pair's first CTA); 9-15 bring keys and values, one a slot of the ring.  Every wait is bounded; one
+// that gives up records SFA_ERR_DEVICE_TIMEOUT and both CTAs unwind.
 #include <atomic>
 #include <cuda.h>
 #include <string.h>
@@ -54,8 +65,8 @@ constexpr int kTile = 256;                     // positions of a tile
 constexpr int kKChunks = 9, kVChunks = 8;      // of a tile
 constexpr int kChunk = 16384;
 constexpr int kUnitCost = 1;                   // of starting a unit, in tiles
-// Cost a pair gets at least: a unit of one tile.  With 3, a pair could get the tiles of two units while others had
-// none: 4 requests of 200 positions 39 us, with 2 28 us; 1 of 8000 positions, 16 heads 35 and 29 us.
+// Cost a pair gets at least: a unit of one tile.  With 3, a pair could get the tiles of two units while
+// others had none: 4 requests of 200 positions 39 us, with 2 28; 1 of 8000 positions x 16 heads 35 and 29.
 constexpr int kMinSpan = 2;
 constexpr int kMaxPairs = 128, kMaxSlots = 4 * kMaxPairs;
 constexpr float kLog2e = 1.4426950408889634f;

@@ -1,6 +1,8 @@
 // sfa_tree_simt.cu -- the attention of a tree of drafted tokens on CUDA cores, every shape: one CTA
 // per (token, group of 8 heads).  The plain form of the definition, to cross-check the tensor cores'
-// kernel.  Bound: fp32 arithmetic and shared-memory reads of q.
+// kernel.  Bound: fp32 arithmetic and shared-memory reads of q, and for few tokens the chain of four warps
+// that take a position after the other: 6 nodes x 4 heads x 200 positions 74 us (tensor cores: 27; it is
+// ahead at one position, 9 us).
 #include <atomic>
 
 #include "sfa_tree.cuh"
