@@ -100,7 +100,8 @@ constexpr long long kDrainLimit = 1LL << 40;
 struct alignas(16) Piece {
   int row0, rows, k0, k1;
   int request, cached, n, first;       // the request, its cached positions, nodes and first token
-  int slot, pad[3];                    // of its partial result; -1: the piece is the whole unit
+  int slot;                            // of its partial result; -1: the piece is the whole unit
+  int alone, pad[2];                   // the request's only unit
 };
 // a partial result: a unit's rows, and whether it has the unit's first tile
 struct alignas(16) Partial {
@@ -175,28 +176,46 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
+// How long L2 is to keep what a load reads.  A row's 512 columns come as keys and, a tile later, as values,
+// then no more: keys stay, values and the keys' last 64 columns go first.  128 heads 428 us without the hints, 423
+// with; they also make the room for what is fetched ahead (below).
+__device__ __forceinline__ uint64_t l2_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t l2_normal() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t l2_last() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 // loads into this CTA that complete on a barrier of the pair's first CTA
-__device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, int y, uint32_t bar) {
+__device__ __forceinline__ void load_box(uint32_t dst, const void* map, int x, int y, uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "l"(policy)
       : "memory");
 }
 // four blocks of 64 columns (from the block-th on) of the rows from y on
-__device__ __forceinline__ void load_blocks(uint32_t dst, const void* map, int y, int block, uint32_t bar) {
+__device__ __forceinline__ void load_blocks(uint32_t dst, const void* map, int y, int block, uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(0), "r"(y), "r"(block), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(0), "r"(y), "r"(block), "r"(bar), "l"(policy)
       : "memory");
 }
 __device__ __forceinline__ void load_rows4(uint32_t dst, const void* map, int x, int r0, int r1, int r2, int r3,
-                                           uint32_t bar) {
+                                           uint32_t bar, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2 "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes.cta_group::2.L2::cache_hint "
+      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar), "l"(policy)
       : "memory");
 }
 // arrive on a barrier of the pair's first CTA.  What it announces lies in this SM (shared memory behind a
@@ -548,7 +567,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     x.n = r.n;
     x.first = r.first;
     x.slot = k0 == 0 && k1 == r.tiles ? -1 : 0;
-    x.pad[0] = x.pad[1] = x.pad[2] = 0;
+    x.alone = r.units == 1;
+    x.pad[0] = x.pad[1] = 0;
     return x;
   };
   int pieces = 0, partials = 0;
@@ -731,11 +751,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     // q of a piece: once the piece before has its last scores (the first thread has seen them)
     const uint32_t q_full = mapa(&bars[kBarQFull], 0);
+    const uint64_t q_policy = l2_normal();
     auto bring_q = [&](const Piece& y) {
       if (tid != 0) return;
       if (rank == 0) mbar_arrive_expect_tx(&bars[kBarQFull], 2 * kQBytes);
       for (int j = 0; j < 9; ++j)
-        load_box(smem_u32(smem + j * kQBlk), &map_q, 64 * j, y.row0 + kHalf * (int)rank, q_full);
+        load_box(smem_u32(smem + j * kQBlk), &map_q, 64 * j, y.row0 + kHalf * (int)rank, q_full, q_policy);
     };
     Piece y;
     bool more = walk.next(y);
@@ -970,6 +991,42 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       commit2(&bars[kBarFin]);
     }
     __syncwarp();
+    if (rank == 1) {
+      // The second CTA's warp has no MMAs: it fetches rows that only this pair reads into L2, once a tile's scores
+      // are there those of the tile after the next (of the next as well where a piece begins).  The ring
+      // alone has too few loads under way for memory's latency: 64 x 8 nodes x 16 heads, bf16 results, 182 us
+      // without and 169 with; three tiles ahead 183, L2 then loses rows before they are read.  A warp that is
+      // a round of the barrier behind would wait for the next, so the end ends the wait as well.
+      int g = 0;
+      bool ok = true;
+      while (ok && walk.next(x)) {
+        const int32_t* table = p.block_table + (size_t)x.request * p.max_blocks;
+        for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
+          if (!x.alone) continue;
+          for (int next = k == x.k0 ? k + 1 : k + 2; next <= k + 2; ++next) {
+            bool there = next < k + 2;
+            for (long long i = 0; i < wl && ok && !there; ++i) {
+              there = all(mbar_try_wait(&bars[kBarS + (g & 1)], (g >> 1) & 1));
+              ok = there || !(aborted() || all(mbar_try_wait(&bars[kBarFin], 0)));
+            }
+            ok = ok && there;
+            if (!ok || next >= x.k1) break;
+#pragma unroll 1
+            for (int u = 0; u < kTile / 32; ++u) {
+              const uint32_t q = (uint32_t)next * kTile + 32 * u + lane, blk = q / (uint32_t)p.block_size;
+              const int phys = blk < (uint32_t)p.max_blocks && q < (uint32_t)x.cached + x.n ? table[blk] : -1;
+              if ((uint32_t)phys < (uint32_t)p.num_blocks) {
+                const char* at = reinterpret_cast<const char*>(p.kv) +
+                                 ((size_t)phys * p.block_size + (q - blk * (uint32_t)p.block_size)) * (2 * kDQK);
+#pragma unroll
+                for (int c = 0; c < 9; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * c));
+              }
+              __syncwarp();
+            }
+          }
+        }
+      }
+    }
     // Every MMA has completed, and every arrival that commits send to either CTA has landed, before
     // TMEM and shared memory go away: an arrival at a CTA that has ended is a fault.
     if (len > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit)))
@@ -984,6 +1041,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int k_step = tp.box ? tp.box : 4, v_step = min(k_step, 32), v_boxes = 32 / v_step;
     const uint32_t full = mapa(&bars[kBarFull + slot], 0), dst = smem_u32(smem + kOffRing + slot * kChunk);
     bool ok = true, bad = false;
+    const uint64_t keep = l2_last(), drop = l2_first();
     int round = 0, group = 0, r = slot;        // r-th chunk of the piece's group (K or V of a tile)
     // no block for the positions [pos, pos + n): that matters where a node attends to one of them
     auto missed = [&](int pos, int n) {
@@ -1049,25 +1107,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // every lane with a box in one instruction (a loop over an elected lane's took half as long again);
       // where the sequence ends in a box, its rows four at a time, with zeros behind the end
       const bool four = !is_k && v_boxes == 1;
+      const uint64_t policy = is_k && r < 8 ? keep : drop;
       if (!tp.box) {
-        if (lane < boxes) load_rows4(to, &map_row, col, row[0], row[1], row[2], row[3], full);
+        if (lane < boxes) load_rows4(to, &map_row, col, row[0], row[1], row[2], row[3], full, policy);
       } else if (!cut) {
         if (four) {
-          if (lane == 0) load_blocks(to, &map_v, row[0], col / 64, full);
+          if (lane == 0) load_blocks(to, &map_v, row[0], col / 64, full, policy);
         } else if (lane < boxes) {
-          load_box(to, &map_box, col, row[0], full);
+          load_box(to, &map_box, col, row[0], full, policy);
         }
       } else {
         const bool whole = have == 0 || have == step;
         if (lane < boxes && whole) {
-          if (four) load_blocks(to, &map_v, row[0], col / 64, full); else load_box(to, &map_box, col, row[0], full);
+          if (four) load_blocks(to, &map_v, row[0], col / 64, full, policy); else load_box(to, &map_box, col, row[0], full, policy);
         }
         __syncwarp();
         for (int c = 0; c < (four ? 4 : 1); ++c)
           for (int a = 0; a < step; a += 4) {
             auto row_at = [&](int u) { return a + u < have ? row[0] + a + u : tp.num_rows; };
             if (lane < boxes && !whole)
-              load_rows4(to + c * 4096 + a * 128, &map_row, col + 64 * c, row_at(0), row_at(1), row_at(2), row_at(3), full);
+              load_rows4(to + c * 4096 + a * 128, &map_row, col + 64 * c, row_at(0), row_at(1), row_at(2), row_at(3), full, policy);
             __syncwarp();
           }
       }
