@@ -29,13 +29,12 @@
 // of units that several pairs had parts of.
 //
 // Bound.  From 128 query rows a request on, the tensor cores: a tile of 256 keys is 4353 cycles of MMAs (6400
-// with two terms), and takes 6300 to 6900 with its rows in L2 (keys awaited 700 to 1000, values 600, P 350;
+// with two terms), and takes 6200 to 6700 with its rows in L2 (keys awaited 700 to 1000, values 600, P 350;
 // shared memory itself needs 5600 for the MMAs' and the loads' traffic).  16 requests x 16 nodes x 128 heads x
-// 8192 positions, bf16 results: 427 us, 1370 TFLOP/s; 2 x 25 nodes x 64 heads x 131072 positions: 533 us,
-// 1390.  With fewer rows the latency of memory: 64 x 8 nodes x 16 heads x up to 16384 positions, fp32: 207 us
-// where the bytes need 97; a tile takes 11500 cycles, of which 4300 wait for keys (the ring's 5 x 16 KB
-// a CTA are not enough to cover 2500 cycles to memory and back at this rate).  Short calls: latency, 18 of
-// the 27 us of 6 nodes x 4 heads x 200 positions in the pairs' launch (keys 7000 cycles, products and
+// 8192 positions, bf16 results: 416 us, 1406 TFLOP/s; 2 x 25 nodes x 64 heads x 131072 positions: 518 us,
+// 1430.  With fewer rows the latency of memory: 64 x 2-8 nodes x 16 heads x 1000-16384 positions, fp32: 195 us
+// where the bytes need 97; with all rows in L2 it takes 163, its products alone 101.  Short calls: latency, 18
+// of the 29 us of 6 nodes x 4 heads x 200 positions in the pairs' launch (keys 7000 cycles, products and
 // softmax 15000, the result 8000), the rest in the schedule and between the launches.
 //
 // Rows that nobody may see.  Positions behind the last node are brought as rows of zeros.  A cached row
@@ -177,8 +176,8 @@ __device__ __forceinline__ void commit2(uint64_t* bar) {
       : "memory");
 }
 // How long L2 is to keep what a load reads.  A row's 512 columns come as keys and, a tile later, as values,
-// then no more: keys stay, values and the keys' last 64 columns go first.  128 heads 428 us without the hints, 423
-// with; they also make the room for what is fetched ahead (below).
+// then no more: keys stay, values and the keys' last 64 columns go first.  128 heads 428 us without the hints,
+// 423 with; they also make the room for what is fetched ahead (below).
 __device__ __forceinline__ uint64_t l2_first() {
   uint64_t p;
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
@@ -994,9 +993,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (rank == 1) {
       // The second CTA's warp has no MMAs: it fetches rows that only this pair reads into L2, once a tile's scores
       // are there those of the tile after the next (of the next as well where a piece begins).  The ring
-      // alone has too few loads under way for memory's latency: 64 x 8 nodes x 16 heads, bf16 results, 182 us
-      // without and 169 with; three tiles ahead 183, L2 then loses rows before they are read.  A warp that is
-      // a round of the barrier behind would wait for the next, so the end ends the wait as well.
+      // alone has too few loads under way for memory's latency: 64 x 8 nodes x 16 heads, bf16 results, 183 us
+      // without and 165 with.  Three tiles ahead 183: L2 then loses rows before they are read.  In a steady
+      // trickle, a line a time: with nine lines of a row at once 170.  (Calls of one tile a unit: 0.8 us more.)
+      // A warp that is a round of the barrier behind would wait for the next, so the end ends the wait as well.
       int g = 0;
       bool ok = true;
       while (ok && walk.next(x)) {
@@ -1018,7 +1018,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if ((uint32_t)phys < (uint32_t)p.num_blocks) {
                 const char* at = reinterpret_cast<const char*>(p.kv) +
                                  ((size_t)phys * p.block_size + (q - blk * (uint32_t)p.block_size)) * (2 * kDQK);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < 9; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * c));
               }
               __syncwarp();
