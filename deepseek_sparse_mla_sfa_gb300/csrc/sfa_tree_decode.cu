@@ -44,7 +44,7 @@
 // cores, which reads only what a node attends to.
 //
 // Warps (512 threads): 0-7 softmax, rescaling, output (the first thread brings q); 8 issues the MMAs (in
-// the pair's first CTA); 9-15 bring keys and values, one a slot of the ring.  Every wait is bounded; one
+// the pair's first CTA) or fetches rows ahead (in the second); 9-15 bring keys and values, one a slot of the ring.  Every wait is bounded; one
 // that gives up records SFA_ERR_DEVICE_TIMEOUT and both CTAs unwind.
 #include <atomic>
 #include <cuda.h>
@@ -917,7 +917,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) arrive_first(o_read);
     }
     if (!ok) fail();
-  } else if (warp == kMmaWarp) {
+  } else if (warp == kMmaWarp && rank == 0) {
     // =================== MMAs =========================================================
     // One elected lane, the waits included: in a region of one lane the operands stay in uniform registers
     // and four MMAs take it 267 cycles, their own time being 256 (a lane chosen by its number 375; a warp
@@ -990,48 +990,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       commit2(&bars[kBarFin]);
     }
     __syncwarp();
-    if (rank == 1) {
-      // The second CTA's warp has no MMAs: it fetches rows that only this pair reads into L2, once a tile's scores
-      // are there those of the tile after the next (of the next as well where a piece begins).  The ring
-      // alone has too few loads under way for memory's latency: 64 x 8 nodes x 16 heads, bf16 results, 183 us
-      // without and 165 with.  Three tiles ahead 183: L2 then loses rows before they are read.  In a steady
-      // trickle, a line a time: with nine lines of a row at once 170.  (Calls of one tile a unit: 0.8 us more.)
-      // A warp that is a round of the barrier behind would wait for the next, so the end ends the wait as well.
-      int g = 0;
-      bool ok = true;
-      while (ok && walk.next(x)) {
-        const int32_t* table = p.block_table + (size_t)x.request * p.max_blocks;
-        for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
-          if (!x.alone) continue;
-          for (int next = k == x.k0 ? k + 1 : k + 2; next <= k + 2; ++next) {
-            bool there = next < k + 2;
-            for (long long i = 0; i < wl && ok && !there; ++i) {
-              there = all(mbar_try_wait(&bars[kBarS + (g & 1)], (g >> 1) & 1));
-              ok = there || !(aborted() || all(mbar_try_wait(&bars[kBarFin], 0)));
-            }
-            ok = ok && there;
-            if (!ok || next >= x.k1) break;
-#pragma unroll 1
-            for (int u = 0; u < kTile / 32; ++u) {
-              const uint32_t q = (uint32_t)next * kTile + 32 * u + lane, blk = q / (uint32_t)p.block_size;
-              const int phys = blk < (uint32_t)p.max_blocks && q < (uint32_t)x.cached + x.n ? table[blk] : -1;
-              if ((uint32_t)phys < (uint32_t)p.num_blocks) {
-                const char* at = reinterpret_cast<const char*>(p.kv) +
-                                 ((size_t)phys * p.block_size + (q - blk * (uint32_t)p.block_size)) * (2 * kDQK);
-#pragma unroll 1
-                for (int c = 0; c < 9; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * c));
-              }
-              __syncwarp();
-            }
-          }
-        }
-      }
-    }
     // Every MMA has completed, and every arrival that commits send to either CTA has landed, before
     // TMEM and shared memory go away: an arrival at a CTA that has ended is a fault.
     if (len > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit)))
       report_status(p.status, kStatusTimeout);
-  } else if (warp < kLoadWarp + kSlots) {
+  } else if (warp >= kLoadWarp && warp < kLoadWarp + kSlots) {
     // =================== keys and values ============================================
     // Warp s fills slot s of the ring, every kSlots-th chunk of the order: it works out where its next chunk
     // lies while it waits for the slot, so a slot is asked for again ~200 cycles after it was read (four
@@ -1135,6 +1098,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       r += kSlots;
     }
     if (!ok) fail();
+  } else if (warp == kMmaWarp) {
+    // =================== rows fetched ahead ============================================
+    // The second CTA's warp has no MMAs: it fetches rows that only this pair reads into L2, once a tile's
+    // scores are there those of the tile after the next (of the next as well where a piece begins).  The
+    // ring alone has too few loads under way for memory's latency: 64 x 8 nodes x 16 heads, bf16 results,
+    // 183 us without and 165 with.  Three tiles ahead 183: L2 then loses rows before they are read.  In a
+    // steady trickle, a line a time: with nine lines of a row at once 170.
+    int g = 0;
+    bool ok = true;
+    while (ok && walk.next(x)) {
+      const int32_t* table = p.block_table + (size_t)x.request * p.max_blocks;
+      for (int k = x.k0; ok && k < x.k1; ++k, ++g) {
+        if (!x.alone) continue;
+        for (int next = k == x.k0 ? k + 1 : k + 2; next <= k + 2; ++next) {
+          // (a warp that is a round of the barrier behind would wait for the next: the end ends it)
+          bool there = next < k + 2;
+          for (long long i = 0; i < wl && ok && !there; ++i) {
+            there = all(mbar_try_wait(&bars[kBarS + (g & 1)], (g >> 1) & 1));
+            ok = there || !(aborted() || all(mbar_try_wait(&bars[kBarFin], 0)));
+          }
+          ok = ok && there;
+          if (!ok || next >= x.k1) break;
+#pragma unroll 1
+          for (int u = 0; u < kTile / 32; ++u) {
+            const uint32_t q = (uint32_t)next * kTile + 32 * u + lane, blk = q / (uint32_t)p.block_size;
+            const int phys = blk < (uint32_t)p.max_blocks && q < (uint32_t)x.cached + x.n ? table[blk] : -1;
+            if ((uint32_t)phys < (uint32_t)p.num_blocks) {
+              const char* at = reinterpret_cast<const char*>(p.kv) +
+                               ((size_t)phys * p.block_size + (q - blk * (uint32_t)p.block_size)) * (2 * kDQK);
+#pragma unroll 1
+              for (int c = 0; c < 9; ++c) asm volatile("prefetch.global.L2 [%0];" ::"l"(at + 128 * c));
+            }
+            __syncwarp();
+          }
+        }
+      }
+    }
+    // the arrivals at this CTA's barriers have landed, as above
+    if (len > 0 && !__all_sync(0xffffffffu, mbar_wait<true>(&bars[kBarFin], 0, kDrainLimit)))
+      report_status(p.status, kStatusTimeout);
   }
 
   // ---- teardown
