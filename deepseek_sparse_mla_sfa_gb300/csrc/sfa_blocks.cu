@@ -11,11 +11,13 @@
 // freed blocks from the first place that names them, ranks from prefix sums.
 //
 // compact runs as one cluster whose CTAs split the table's entries and the pool's bitmaps and meet
-// at cluster barriers: no workspace, one launch.
+// at cluster barriers: no workspace, one launch.  A cluster barrier orders global memory too, for the
+// cluster's threads; what another CTA wrote there is read past L1 (a fence of the GPU's scope before each
+// barrier cost 0.6 us a call).
 // Bound: latency (a chain of launch, lengths, table, block counters and the barriers between them)
 // up to some 10^5 table entries; kv_copy_blocks: HBM.  On the device: fork of 8 and of 512 rows 4 and 5 us;
 // free of 8384 table entries 9 us, of 718000 (323000 freed) 19; compact of 512 blocks 8 us, of 10000 blocks
-// and 10200 entries 19; copies of 2500 blocks of 74 KB in each of two layers 109 us, 6.8 TB/s.
+// and 10200 entries 17; copies of 2500 blocks of 74 KB in each of two layers 109 us, 6.8 TB/s.
 #include <algorithm>
 #include <climits>
 
@@ -210,12 +212,7 @@ __global__ void __launch_bounds__(kClusterThreads) blocks_free_kernel(const Free
   __shared__ int puts_here;
   constexpr bool kAll = kStep == 0;
   auto meet = [] {
-    if (gridDim.x > 1) {
-      __threadfence();
-      cg::this_cluster().sync();
-    } else {
-      __syncthreads();
-    }
+    if (gridDim.x > 1) cg::this_cluster().sync(); else __syncthreads();
   };
   const int rank = blockIdx.x, ctas = gridDim.x, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
   if (!kAll) asm volatile("griddepcontrol.launch_dependents;");
@@ -363,12 +360,7 @@ __global__ void __launch_bounds__(kClusterThreads) blocks_compact_kernel(const C
   const int gid = rank * kClusterThreads + tid;
   constexpr int kAll = kCtas * kClusterThreads;
   auto meet = [&] {
-    if (kCtas > 1) {
-      __threadfence();
-      cluster.sync();
-    } else {
-      __syncthreads();
-    }
+    if (kCtas > 1) cluster.sync(); else __syncthreads();
   };
   auto remote = [&](auto* at, int c) { return kCtas > 1 ? cluster.map_shared_rank(at, c) : at; };
   const int head = min(max(*p.taken, 0), p.num_free);
@@ -611,7 +603,7 @@ cudaError_t launch_blocks_fork(int32_t* table, int rows, int max_blocks, int32_t
 
 // CTAs: one for each round of the table's entries, up to a cluster (one launch); else one for each
 // kClusterThreads entries, at most one for each SM.  2540 entries take 6.8 us by the cluster and 8.8 by
-// the four launches, 8128 10.8 and 9.2, 31750 11.4 and 9.7 in a captured graph; called one by one, a
+// the four launches, 8128 10.1 and 9.2, 31750 10.8 and 9.7 in a captured graph; called one by one, a
 // cluster's call takes 16 us and four launches 25.
 static int free_ctas(int rows, int max_blocks) {
   const long long entries = (long long)rows * max_blocks;
@@ -646,7 +638,7 @@ cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int
                                   int32_t* shares_out, int32_t* free_out, int32_t* copies, int* status,
                                   cudaStream_t stream) {
   // by one CTA and by a cluster: 128 blocks 7.2 and 12.3 us, 4000 blocks and 3400 entries 13.9 and 15.5,
-  // 10000 blocks and 10200 entries 26.7 and 18.5
+  // 10000 blocks and 10200 entries 26.7 and 17.4
   const bool small = (long long)rows * max_blocks <= 4 * kClusterThreads && num_blocks <= 8 * kClusterThreads;
   const int ctas = small ? 1 : kClusterCtas;
   const int all = (num_blocks + 31) / 32, words = (all + ctas - 1) / ctas;
