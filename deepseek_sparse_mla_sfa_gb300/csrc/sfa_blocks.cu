@@ -564,14 +564,21 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const Copy
   }
 }
 
+constexpr int kUnasked = 40 * 1024;        // dynamic shared memory that a launch has beside the kernels' own
+constexpr int kFreeMaxSmem = (2 * kPlanMaxRequests + 1) * 4;
+constexpr int kCompactMaxSmem = (kMaxPoolBlocks / 32 / kClusterCtas) * 20 + (kPlanMaxRequests + 1) * 4;
+
+// What a kernel may take is the kernel's, not the launch's: always the most that any call takes, so that a
+// call on another host thread cannot lower it between this and the launch.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kernel, int most) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // after: begins while the launch before it on the stream ends (and waits for it itself)
 template <class Kernel, class Params>
 cudaError_t launch_ctas(Kernel kernel, int ctas, int cluster, size_t smem, const Params& p, cudaStream_t stream,
                         bool after = false) {
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kClusterThreads);
@@ -624,8 +631,17 @@ cudaError_t launch_blocks_free(const int32_t* table, const int32_t* held, const 
                      block_size, taken_out, static_cast<int*>(workspace), status};
   const size_t smem = (size_t)(2 * rows + 1) * 4;
   const int ctas = free_ctas(rows, max_blocks);
-  if (ctas <= kClusterCtas) return launch_ctas(blocks_free_kernel<0>, ctas, ctas, smem, p, stream);
-  cudaError_t e = launch_ctas(blocks_free_kernel<1>, ctas, 1, smem, p, stream);
+  const bool ask = smem > kUnasked;
+  cudaError_t e = cudaSuccess;
+  if (ctas <= kClusterCtas) {
+    if (ask) e = allow_smem(blocks_free_kernel<0>, kFreeMaxSmem);
+    return e != cudaSuccess ? e : launch_ctas(blocks_free_kernel<0>, ctas, ctas, smem, p, stream);
+  }
+  // for all four before the first, which already changes the shares
+  if (ask)
+    for (auto kernel : {blocks_free_kernel<1>, blocks_free_kernel<2>, blocks_free_kernel<3>, blocks_free_kernel<4>})
+      if (e == cudaSuccess) e = allow_smem(kernel, kFreeMaxSmem);
+  if (e == cudaSuccess) e = launch_ctas(blocks_free_kernel<1>, ctas, 1, smem, p, stream);
   if (e == cudaSuccess) e = launch_ctas(blocks_free_kernel<2>, ctas, 1, smem, p, stream, true);
   if (e == cudaSuccess) e = launch_ctas(blocks_free_kernel<3>, ctas, 1, smem, p, stream, true);
   if (e == cudaSuccess) e = launch_ctas(blocks_free_kernel<4>, ctas, 1, smem, p, stream, true);
@@ -645,7 +661,11 @@ cudaError_t launch_blocks_compact(const int32_t* table, const int32_t* lens, int
   const CompactParams p{table, lens, rows, max_blocks, shares, num_blocks, free_blocks, num_free, taken, block_size,
                         max_moves, words, table_out, shares_out, free_out, copies, status};
   const size_t smem = (size_t)words * 20 + (size_t)(rows + 1) * 4;
-  if (small) return launch_ctas(blocks_compact_kernel<1>, 1, 1, smem, p, stream);
+  if (small) return launch_ctas(blocks_compact_kernel<1>, 1, 1, smem, p, stream);   // (at most 22 KB)
+  if (smem > kUnasked) {
+    const cudaError_t e = allow_smem(blocks_compact_kernel<kClusterCtas>, kCompactMaxSmem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_ctas(blocks_compact_kernel<kClusterCtas>, kClusterCtas, kClusterCtas, smem, p, stream);
 }
 

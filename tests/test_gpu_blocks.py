@@ -279,3 +279,49 @@ def test_fork_decode_free_compact(captured):
     assert [held.count(x) - 1 for x in range(nb) if x in held] == [int(s2[x]) for x in range(nb) if x in held]
     rest = f2[int(k3):].tolist()
     assert rest == list(range(len(set(held)), nb))
+
+
+# ----------------------------------------------------------------------- two host threads
+def test_calls_of_other_sizes_on_two_host_threads():
+    """Two threads call at once, each on a stream of its own, with tables whose shared memory differs (above
+    what a launch has unasked): neither changes what the other's launches may take.  Straight through the C
+    ABI, so that the threads' calls follow one another closely."""
+    import threading
+
+    from deepseek_sparse_mla_sfa_gb300 import _lib
+
+    lib = _lib.load()
+
+    def free_of(rows):
+        d = [i32(np.full((rows, 1), -1)), i32(np.zeros(rows)), i32([0, 0]), i32([-1, -1]), i32([2]), i32([0])]
+        t, z, s, f, k, o = (x.data_ptr() for x in d)
+        return d, lambda stream: lib.sfa_blocks_free(t, z, z, rows, 1, s, 2, f, 2, k, 16, o, 0, 0, stream)
+
+    def compact_of(nb, rows):
+        d = [i32(np.full((rows, 1), -1)), i32(np.zeros(rows)), i32(np.zeros(nb)), i32([-1]), i32([1])]
+        d += [torch.empty_like(d[i]) for i in (0, 2, 3)] + [i32([0] * 3)]
+        t, z, s, f, k, t2, s2, f2, c = (x.data_ptr() for x in d)
+        return d, lambda stream: lib.sfa_blocks_compact(t, z, rows, 1, s, nb, f, 1, k, 16, 1, t2, s2, f2, c, stream)
+
+    for calls in ((free_of(8192), free_of(5200)), (compact_of(1 << 20, 8192), compact_of(600000, 100))):
+        torch.cuda.synchronize()
+        codes, gate = [], threading.Barrier(2)
+
+        def work(call):
+            torch.cuda.set_device(0)
+            stream = torch.cuda.Stream()
+            gate.wait()
+            for i in range(4000):
+                code = call(stream.cuda_stream)
+                if code:
+                    codes.append(code)
+                if i % 100 == 99:
+                    stream.synchronize()
+
+        threads = [threading.Thread(target=work, args=(c,)) for _, c in calls]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert not codes, (len(codes), codes[0])
+        assert sfa.last_device_status() == 0
