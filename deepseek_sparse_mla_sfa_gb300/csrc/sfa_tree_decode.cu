@@ -235,6 +235,15 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   return r;
 }
 
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 x, x, y;\n\t"
+      "mov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
 // ---------------------------------------------------------------- the schedule
 // One block lays out the pieces of every pair.  Units in order of requests make an axis, each as long as
 // its tiles and kUnitCost for its start; pair k gets the range [k span, (k + 1) span).  A cut never goes
@@ -762,7 +771,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (more) bring_q(y);
     while (ok && more) {
       x = y;
-      float m_ref = -INFINITY, l_sum = 0.f, u[3];
+      // The sums of the weights as they are, for lse, and as P's one term holds them: out is divided by the
+      // latter, so that the rounding of a row's heaviest weights cancels (with two terms 2^-17 of them is left, and
+      // the second sum cost 2 % for 8 % of the error).  128 heads 414-416 us without the second sum, 419 with, 423
+      // where it came before the hand-over of P.
+      float m_ref = -INFINITY, l_sum = 0.f, l_held = 0.f, u[3];
       const bool live = row < x.rows;
       const int node = live ? (x.row0 + row) / p.h - x.first : 0;
       const long long* words = p.mask + (size_t)(x.first + node) * p.words;
@@ -812,16 +825,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float alpha = m_ref == m_new ? 1.f : ex2(m_ref - base);
         const bool first = k == x.k0;
         m_ref = m_new;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 sum[2] = {};
         uint32_t pk[32], pl[kTwo ? 32 : 1];
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           const float e0 = ex2(fmaf(s[2 * j], c_abs, -base)), e1 = ex2(fmaf(s[2 * j + 1], c_abs, -base));
-          sum[j & 3] += e0 + e1;
+          sum[j & 1] = add2(sum[j & 1], make_float2(e0, e1));
           pk[j] = pack_bf16(e0, e1);
           if (kTwo) pl[j] = pack_bf16(e0 - __uint_as_float(pk[j] << 16), e1 - __uint_as_float(pk[j] & 0xffff0000u));
         }
-        l_sum = l_sum * alpha + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        l_sum = l_sum * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
         // P's place and O are free once P V of the tile before has completed
         if (g > 0) {
           if (!(ok = wait_warp(&bars[kBarPv], (g - 1) & 1))) break;
@@ -853,6 +866,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_first(p_ready);
+        if (!kTwo) {                           // (behind the hand-over, beside the MMAs)
+          float2 held[2] = {};
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            held[j & 1] = add2(held[j & 1], make_float2(__uint_as_float(pk[j] << 16), __uint_as_float(pk[j] & 0xffff0000u)));
+          l_held = l_held * alpha + ((held[0].x + held[0].y) + (held[1].x + held[1].y));
+        }
       }
       if (!ok) break;
       more = walk.next(y);
@@ -860,10 +880,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---- the piece's result
       others(l_sum, u);
       const float l = (l_sum + u[0]) + (u[1] + u[2]);
+      float l_of_p = l;
+      if (!kTwo) {
+        others(l_held, u);
+        l_of_p = (l_held + u[0]) + (u[1] + u[2]);
+      }
       if (!ok || !(ok = wait_warp(&bars[kBarPv], (g - 1) & 1))) break;
       tc_fence_after();
       const bool none = l == 0.f;
-      const float inv = none ? 0.f : 1.f / l;
+      const float inv = none ? 0.f : 1.f / l_of_p;
       const float lse = none ? -INFINITY : (m_ref + __log2f(l)) * kLn2;
       const bool whole = x.slot < 0;
       // A warp's 32 rows go through its own 4 KB of P, 128 bytes a row at a time, so that eight lanes write

@@ -538,3 +538,39 @@ def test_steps_of_drafted_trees():
         assert int(back) == taken and np.array_equal(d["free"].cpu(), free) and lens.tolist() == l_o.tolist()
         cached = l_o
         d["cached"], d["taken"], d["table"] = lens, back, table_d
+
+
+# ------------------------------------------------------------------- rounding of the weights
+@pytest.mark.parametrize("cached,h,bs", [([600], 16, 64), ([300, 1500], 128, 16), ([5000], 3, 64)])
+def test_decode_rounding_of_a_heavy_weight_cancels(path, cached, h, bs):
+    """out is sum w (1 + r) v / sum w (1 + r) with |r| <= 2^-8, the weights' rounding to bf16, so it is off by at
+    most sum w |r| |v - out| / (1 - 2^-8): next to nothing where one position has nearly all of the weight.  The
+    heavy position lies in the second tile, below the 2^8 from which the maximum is taken anew, so that its weight
+    has bits to round.  Scores move the weights likewise (2^-18 of sum |q k|, exponentials 2^-20), fp32 sums are
+    off by at most 2^-23 of sum w |v| a position, and the result's own rounding by 2^-8 of it."""
+    p = problem(200 + h, cached, [5] * len(cached), h, bs, std=0.3)
+    kv = p["kv"].float()
+    kv[..., 512] = 0.0
+    p["q"][..., 512] = 1.0
+    for b, c in enumerate(cached):
+        for pos, boost in ((3, 12.0), (270, 16.5)):
+            kv[int(p["table"][b, pos // bs]), pos % bs, 512] = boost / p["scale"]
+    p["kv"] = kv.to(torch.bfloat16)
+    out, lse = sfa.decode_tree(**device(p), out_dtype=torch.bfloat16)
+    assert sfa.last_device_status() == 0
+    q, k = p["q"].double(), p["kv"].double()
+    check(p, (out, lse))
+    for b, (c, n) in enumerate(zip(cached, [5] * len(cached))):
+        t0 = int(p["start"][b])
+        rows = torch.stack([k[int(p["table"][b, x // bs]), x % bs] for x in range(c + n)])
+        for i in range(n):
+            seen = list(range(c)) + [c + j for j in range(n) if p["mask"][t0 + i] >> j & 1]
+            kk = rows[seen]
+            s = p["scale"] * q[t0 + i] @ kk.T
+            w, v = torch.softmax(s, -1), kk[:, :512]
+            want = w @ v
+            away = torch.einsum("hp,hpc->hc", w, (v[None] - want[:, None]).abs())
+            d = 2.0 ** -18 * p["scale"] * (q[t0 + i].abs() @ kk.abs().T).amax(-1, keepdim=True) + 2.0 ** -20
+            tol = (2.0 ** -8 + 2 * d) * away / (1 - 2.0 ** -8) + 2.0 ** -23 * len(seen) * (w @ v.abs()) + 2.0 ** -8 * want.abs()
+            off = (out[t0 + i].double().cpu() - want).abs()
+            assert bool((w.amax(-1) > 0.8).all()) and bool((off <= tol + 1e-30).all()), float((off / tol).max())
