@@ -217,11 +217,13 @@ __device__ __forceinline__ void load_rows4(uint32_t dst, const void* map, int x,
       "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar), "l"(policy)
       : "memory");
 }
-// arrive on a barrier of the pair's first CTA.  What it announces lies in this SM (shared memory behind a
-// proxy fence, TMEM behind a tcgen05 fence) and is read by the tensor core here, so release at the CTA's
-// scope is enough; at the cluster's scope it waits some 2000 cycles for every store of the thread.
+// arrive on a barrier of the pair's first CTA, whose MMA thread waits with acquire at the cluster's scope.
+// What it announces lies in this CTA's shared memory (or in TMEM, behind a tcgen05 fence), so the release is
+// restricted to that: one of all memory (release.cluster on the arrival) waits for every store of the thread,
+// 460 us instead of 422 at 128 heads.
 __device__ __forceinline__ void arrive_first(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+  mbar_arrive_remote_relaxed(bar);
 }
 __device__ __forceinline__ float ex2(float x) {
   float y;
