@@ -40,8 +40,8 @@
 // Rows that nobody may see.  Positions behind the last node are brought as rows of zeros.  A cached row
 // of NaN or infinities that only some nodes see would reach the others as 0 x NaN in P V: such a row
 // shows as a score that is not finite in a masked place; the loading warps see a position that a node
-// attends to and that has no block.  Both mark the request, and the last kernel computes its nodes on CUDA
-// cores, which reads only what a node attends to.
+// attends to and that has no block.  Both mark the request, a bit each, and the last kernel computes the
+// nodes of every marked one on CUDA cores, once, which reads only what a node attends to.
 //
 // Warps (512 threads): 0-7 softmax, rescaling, output (the first thread brings q); 8 issues the MMAs (in
 // the pair's first CTA) or fetches rows ahead (in the second); 9-15 bring keys and values, one a slot of the ring.  Every wait is bounded; one
@@ -87,7 +87,7 @@ constexpr int kOffMx = kOffP + kPBytes + 7 * kChunk;     // float [2][256]: row 
 constexpr int kOffBar = kOffMx + 2048;
 constexpr int kBarFull = 0, kBarEmpty = 7, kBarQFull = 14, kBarS = kBarQFull + 1, kBarP = kBarS + 2, kBarPv = kBarP + 1, kBarO = kBarPv + 1,
               kBarMx = kBarO + 1, kBarFin = kBarMx + 2, kBarNever = kBarFin + 1, kNumBars = kBarNever + 1;
-constexpr int kOffMisc = kOffBar + 8 * kNumBars;         // TMEM address, abort, bad range
+constexpr int kOffMisc = kOffBar + 8 * kNumBars;         // TMEM address, abort
 constexpr int kSmem = kOffMisc + 64 + 1024;
 static_assert(kSmem <= 232448, "shared memory budget");
 static_assert(kOffBar % 8 == 0, "alignment");
@@ -114,9 +114,10 @@ struct Workspace {
   Partial* list;     // [slots]
   float* part;       // [slots][cap][512]
   float* lse;        // [slots][cap]
-  int2* bad;         // [2 * pairs + 1]: requests to compute again, first and last (the schedule's: at all)
+  unsigned* marks;   // [ceil(B / 32)]: a bit a request, which is to be computed on CUDA cores
   int cap, slots;    // rows of a slot, slots
   int most;          // pieces that there is room for
+  __device__ __forceinline__ void mark(int request) const { atomicOr(marks + request / 32, 1u << (request % 32)); }
 };
 
 struct TreeTcParams {
@@ -370,7 +371,6 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   __shared__ Piece kept[kMaxPairs][kKept];
   __shared__ int n_of[3], split_of[3];
   __shared__ float cost_of[3], tiles_of, far_of;
-  __shared__ int bad_s[2];                                  // first and last request for the last kernel alone
   const TreeParams& p = tp.p;
   const int tid = threadIdx.x, lane = tid % 32, pairs = tp.pairs;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -381,11 +381,8 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     n_of[tid] = split_of[tid] = 0;
     cost_of[tid] = 0.f;
   }
-  if (tid == 0) {
-    tiles_of = far_of = 0.f;
-    bad_s[0] = 0x7fffffff;
-    bad_s[1] = -1;
-  }
+  if (tid == 0) tiles_of = far_of = 0.f;
+  for (int w = tid; w < (p.B + 31) / 32; w += kPlanThreads) tp.ws.marks[w] = 0;
   __syncthreads();
   long long cost = 0;                          // of the units
   float tiles = 0.f, far = 0.f;                // their tiles; tiles of different rows
@@ -397,10 +394,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     if (p.B <= kPlanThreads) requests[b] = r;
     if (min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
       report_status(p.status, kStatusBadTree);
-    if (r.n > 0 && r.units == 0) {
-      atomicMin(&bad_s[0], b);
-      atomicMax(&bad_s[1], b);
-    }
+    if (r.n > 0 && r.units == 0) tp.ws.mark(b);
   }
   long long total;
   long long at = block_before(cost, part, total);
@@ -598,7 +592,6 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   if (tid == 0) {
     tp.ws.start[pairs] = fits ? (int)(all >> 32) : 0;
     *tp.ws.partials = fits ? (int)(all & 0xffffffff) : 0;
-    tp.ws.bad[2 * pairs] = make_int2(bad_s[0], bad_s[1]);
     if (!fits) report_status(p.status, kStatusBadTree);
   }
   if (!fits) return;
@@ -660,7 +653,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint32_t* tmem_s = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int* abort_s = reinterpret_cast<volatile int*>(smem + kOffMisc + 4);
-  int* bad_s = reinterpret_cast<int*>(smem + kOffMisc + 8);   // first and last request to compute again
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const int pair = blockIdx.x >> 1;
@@ -682,8 +674,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     mbar_init(&bars[kBarFin], 1);
     mbar_init(&bars[kBarNever], 1);           // nothing arrives: the stall test hook waits on it
     *abort_s = 0;
-    bad_s[0] = 0x7fffffff;
-    bad_s[1] = -1;
     fence_barrier_init();
   }
   if (warp == 0) {
@@ -726,10 +716,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     return false;
   };
   auto aborted = [&] { return __any_sync(0xffffffffu, *abort_s) != 0; };
-  auto mark_bad = [&](int request) {
-    atomicMin(&bad_s[0], request);
-    atomicMax(&bad_s[1], request);
-  };
 
   if (warp < kSoftWarps) {
     // =================== softmax, rescaling, output =================================
@@ -809,7 +795,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               bad |= !(fabsf(s[j]) <= 3.0e38f);   // (rows behind the end are zeros)
               s[j] = -INFINITY;
             }
-          if (bad) mark_bad(x.request);
+          if (bad) tp.ws.mark(x.request);
         }
         float t[16];
 #pragma unroll
@@ -1051,7 +1037,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (r >= count) {
         r -= count;
         if (++group == 2 * t) {
-          if (bad) mark_bad(x.request);
+          if (bad) tp.ws.mark(x.request);
           bad = false;
           group = 0;
           more = walk.next(x);
@@ -1171,7 +1157,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   __syncwarp();
   __syncthreads();
   if (threadIdx.x == 0) {
-    tp.ws.bad[blockIdx.x] = make_int2(bad_s[0], bad_s[1]);
     if (*abort_s) {
       // loads of either CTA may be in flight: they land within microseconds
       const uint64_t t0 = globaltimer_ns();
@@ -1200,7 +1185,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
   const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
   const int partials = min(*tp.ws.partials, tp.ws.slots);
   int any = 0;
-  for (int j = tid; j <= 2 * tp.pairs; j += kJoinThreads) any |= tp.ws.bad[j].x <= tp.ws.bad[j].y;
+  const int words = (p.B + 31) / 32;
+  for (int w = tid; w < words; w += kJoinThreads) any |= tp.ws.marks[w] != 0;
   any = __syncthreads_or(any);
   int n_begins = 0, n_rows = 0;
   for (int j0 = 0; j0 < partials; j0 += kJoinThreads) {
@@ -1256,9 +1242,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
       __syncthreads();
       n = n_parts;
     }
-    bool skip = false;                         // all of the request is computed again below
-    if (any)
-      for (int j = 0; j <= 2 * tp.pairs; ++j) skip |= tp.ws.bad[j].x <= me.request && me.request <= tp.ws.bad[j].y;
+    const bool skip = any && (tp.ws.marks[me.request / 32] >> (me.request % 32) & 1);   // all of it is computed below
     for (int it = it0 + warp; it < end && !skip; it += kWarps) {
       const int r = it - rows_before[lo];
       if (r >= tp.ws.cap) break;
@@ -1300,16 +1284,15 @@ __global__ void __launch_bounds__(kJoinThreads) join_tree_kernel(const TreeTcPar
   }
   if (!any) return;
   // rare: the nodes of every marked request, a node and two heads at a time
-  const int groups = (p.h + kFixHeads - 1) / kFixHeads;
-  const int first = blockIdx.x, all = gridDim.x;
-  for (int j = 0; j <= 2 * tp.pairs; ++j) {
-    const int2 range = tp.ws.bad[j];
-    for (int b = max(range.x, 0); b <= min(range.y, p.B - 1); ++b) {
-      const Request r = request_of(p, b);
-      for (int it = first; it < r.n * groups; it += all)
-        tree_simt<kFixHeads>(p, r.first + it / groups, it % groups * kFixHeads, smem_f);
+  const int groups = (p.h + kFixHeads - 1) / kFixHeads, all = gridDim.x;
+  int first = blockIdx.x;                      // the block's next item, counted from the request's first
+  for (int w = 0; w < words; ++w)
+    for (unsigned m = tp.ws.marks[w]; m; m &= m - 1) {
+      const Request r = request_of(p, 32 * w + __ffs(m) - 1);
+      const int items = r.n * groups;
+      for (; first < items; first += all) tree_simt<kFixHeads>(p, r.first + first / groups, first % groups * kFixHeads, smem_f);
+      first -= items;
     }
-  }
 }
 
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1340,7 +1323,7 @@ size_t lay_out(char* base, int pairs, int B, int T, int h, Workspace& ws) {
   ws.list = reinterpret_cast<Partial*>(part((size_t)ws.slots * sizeof(Partial)));
   ws.part = reinterpret_cast<float*>(part((size_t)ws.slots * ws.cap * kDV * 4));
   ws.lse = reinterpret_cast<float*>(part((size_t)ws.slots * ws.cap * 4));
-  ws.bad = reinterpret_cast<int2*>(part((size_t)(2 * pairs + 1) * sizeof(int2)));
+  ws.marks = reinterpret_cast<unsigned*>(part((size_t)((B + 31) / 32) * 4));
   return at;
 }
 

@@ -574,3 +574,80 @@ def test_decode_rounding_of_a_heavy_weight_cancels(path, cached, h, bs):
             tol = (2.0 ** -8 + 2 * d) * away / (1 - 2.0 ** -8) + 2.0 ** -23 * len(seen) * (w @ v.abs()) + 2.0 ** -8 * want.abs()
             off = (out[t0 + i].double().cpu() - want).abs()
             assert bool((w.amax(-1) > 0.8).all()) and bool((off <= tol + 1e-30).all()), float((off / tol).max())
+
+
+# ------------------------------------------------------------------------- marked requests
+def hide(p, b, value):
+    """A row that no other node attends to: the last node of request b, a leaf, holds `value`."""
+    n = int(p["start"][b + 1] - p["start"][b])
+    bs = p["kv"].shape[1]
+    pos = int(p["cached"][b]) + n - 1
+    p["kv"][int(p["table"][b, pos // bs]), pos % bs] = value
+    return int(p["start"][b]) + n - 1
+
+
+def test_decode_of_requests_beside_marked_ones_keeps_its_bits():
+    """A row of NaN in a branch changes nothing but the nodes that attend to it, and the other requests not at all:
+    a request is computed the other way only where it was marked itself, not where it lies between two that were."""
+    p = problem(120, [40 + b % 30 for b in range(300)], [4] * 300, 16, 16)
+    clean = [x[:1200].cpu() for x in sfa.decode_tree(**device(p))]
+    marked = [0, 3, 4, 40, 42, 131, 160, 299]
+    own = [hide(p, b, float("nan")) for b in marked]
+    got = [x[:1200].cpu() for x in sfa.decode_tree(**device(p))]
+    assert sfa.last_device_status() == 0
+    rest = [t for t in range(1200) if t // 4 not in marked]
+    for c, g in zip(clean, got):
+        assert torch.equal(c[rest], g[rest])
+    beside = [t for b in marked for t in range(4 * b, 4 * b + 4) if t not in own]
+    assert bool(torch.isnan(got[0][own]).all()) and bool(torch.isnan(got[1][own]).all())
+    # CUDA cores in fp32 against two bf16 terms (2^-16 of sum w |v|, |v| < 6) and both sides' scores (2^-18 sum |q k|)
+    assert float((got[0][beside] - clean[0][beside]).abs().max()) < 6 * (2.0 ** -16 + 4 * 2.0 ** -18 * 0.08 * 576 * 2)
+
+
+def test_decode_computes_a_marked_request_once():
+    """However many CTAs mark it: a marked request costs about a pass on CUDA cores, here of 16 units (up to 32
+    marks).  The kernel for every shape is the measure of such a pass."""
+    p = problem(121, [4000], [16], 128, 64)
+    hide(p, 0, float("nan"))
+    d = device(p)
+
+    def ms(n=3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        sfa.decode_tree(**d)
+        torch.cuda.synchronize()
+        a.record()
+        for _ in range(n):
+            sfa.decode_tree(**d)
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / n
+
+    marked = ms()
+    old = sfa.set_kernel_path(1)
+    try:
+        cores = ms()
+    finally:
+        sfa.set_kernel_path(old)
+    assert marked < 4 * cores + 2, (marked, cores)
+
+
+def test_decode_of_marked_requests_in_a_graph_forgets_them():
+    """Marks are of one call: a replay on clean rows gives the bits of a clean call."""
+    p = problem(122, [70, 3000, 9], [5, 7, 3], 32, 16)
+    d = device(p)
+    first = [x[:15].clone() for x in sfa.decode_tree(**d)]
+    saved = d["kv"].clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = sfa.decode_tree(**d)
+    for bad in (None, 1, None, 0, None):
+        d["kv"].copy_(saved)
+        if bad is not None:
+            q = dict(p, kv=p["kv"].clone())
+            hide(q, bad, float("inf"))
+            d["kv"].copy_(q["kv"])
+        g.replay()
+        torch.cuda.synchronize()
+        if bad is None:
+            assert all(torch.equal(x, y[:15]) for x, y in zip(first, got))
+    assert sfa.last_device_status() == 0
