@@ -369,8 +369,7 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   __shared__ long long share_at[kMaxPairs + 1];             // where the pairs' ranges lie
   __shared__ Request requests[kPlanThreads];                // where there is one a thread
   __shared__ Piece kept[kMaxPairs][kKept];
-  __shared__ int n_of[3], split_of[3];
-  __shared__ float cost_of[3], tiles_of, far_of;
+  __shared__ int n_of[3], split_of[3], cost_of[3], tiles_of, far_of;   // whole numbers: the same in any order
   const TreeParams& p = tp.p;
   const int tid = threadIdx.x, lane = tid % 32, pairs = tp.pairs;
   const int per = (p.B + kPlanThreads - 1) / kPlanThreads;
@@ -378,18 +377,17 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   Plan plan{kWhole, 0, 0};
   auto request = [&](int b) { return p.B <= kPlanThreads ? requests[b] : request_of(p, b, plan.limit); };
   if (tid < 3) {
-    n_of[tid] = split_of[tid] = 0;
-    cost_of[tid] = 0.f;
+    n_of[tid] = split_of[tid] = cost_of[tid] = 0;
   }
-  if (tid == 0) tiles_of = far_of = 0.f;
+  if (tid == 0) tiles_of = far_of = 0;
   for (int w = tid; w < (p.B + 31) / 32; w += kPlanThreads) tp.ws.marks[w] = 0;
   __syncthreads();
   long long cost = 0;                          // of the units
-  float tiles = 0.f, far = 0.f;                // their tiles; tiles of different rows
+  long long tiles = 0, far = 0;                // their tiles; tiles of different rows
   for (int b = r0; b < r1; ++b) {
     const Request r = request_of(p, b);
     cost += (long long)r.units * r.cost();
-    tiles += (float)r.units * r.tiles;
+    tiles += (long long)r.units * r.tiles;
     far += r.units > 0 ? r.tiles : 0;
     if (p.B <= kPlanThreads) requests[b] = r;
     if (min(max(p.token_start[b + 1], 0), p.T) - min(max(p.token_start[b], 0), p.T) > p.max_nodes)
@@ -399,41 +397,35 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
   long long total;
   long long at = block_before(cost, part, total);
   if (p.B <= kDealRequests && total > 2 * kFarTiles && total < (1 << 28)) {   // (32 bits from here on)
-    auto add = [&](float v, float* to) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    auto add = [&](int v, int* to) {
+      v = __reduce_add_sync(0xffffffffu, v);
       if (lane == 0) atomicAdd(to, v);
     };
-    add(tiles, &tiles_of);
-    add(far, &far_of);
+    add((int)tiles, &tiles_of);                // (both below `total`; with a task's starts and last chunk below 3 times that)
+    add((int)far, &far_of);
     __syncthreads();
-    if (far_of > kFarTiles && tiles_of >= 1.5f * far_of) {
+    if (far_of > kFarTiles && 2 * tiles_of >= 3 * far_of) {
       // whole units, or chunks that make a round or two; what is not dealt counts a third more
       int limits[3] = {kWhole, 0, 0};
       for (int c = 0; c < 3; ++c) {
-        if (c > 0) limits[c] = (int)fminf(ceilf(tiles_of / (c * pairs)), 1e9f);
-        int n = 0, split = 0;
-        float all = 0.f;
+        if (c > 0) limits[c] = (tiles_of + c * pairs - 1) / (c * pairs);
+        int n = 0, split = 0, all = 0;
         if (tid < p.B) {
           const Request r = request_of(p, tid, limits[c]);
           n = r.tasks();
-          all = (float)n * r.cost();
+          all = n * r.cost();
           split = r.chunks > 1 ? n : 0;
         }
         add(all, &cost_of[c]);
-        n = __reduce_add_sync(0xffffffffu, n);
-        split = __reduce_add_sync(0xffffffffu, split);
-        if (lane == 0) {
-          atomicAdd(&n_of[c], n);
-          atomicAdd(&split_of[c], split);
-        }
+        add(n, &n_of[c]);
+        add(split, &split_of[c]);
       }
       __syncthreads();
       float best = 1e30f;
       for (int c = 0; c < 3; ++c) {
         const int n = n_of[c];
         if (n < pairs || n > (1 << 24) || split_of[c] + 2 * pairs > tp.ws.slots) continue;
-        const float done = (float)(n / pairs * pairs) / (float)n, t = cost_of[c] * (done + 1.3f * (1.f - done));
+        const float done = (float)(n / pairs * pairs) / (float)n, t = (float)cost_of[c] * (done + 1.3f * (1.f - done));
         if (t < best) {
           best = t;
           plan.limit = limits[c];

@@ -651,3 +651,102 @@ def test_decode_of_marked_requests_in_a_graph_forgets_them():
         if bad is None:
             assert all(torch.equal(x, y[:15]) for x, y in zip(first, got))
     assert sfa.last_device_status() == 0
+
+
+# ---------------------------------------------------------------- dealt units, at the bound of two terms
+def formula(p, only=None):
+    """Per token: the formula in 64 bits with elementary torch operations on the GPU.  Yields (token, out [h, 512], lse
+    [h], sum w |v|, sum w |v - out|, the scores' error, positions), for every token or those of `only`."""
+    q, kv = p["q"].cuda().double(), p["kv"].cuda().double()
+    bs = kv.shape[1]
+    for b, c in enumerate(int(x) for x in p["cached"]):
+        t0, n = int(p["start"][b]), int(p["start"][b + 1] - p["start"][b])
+        table = torch.as_tensor(np.asarray(p["table"][b])).cuda().long()
+        pos = torch.arange(c + n, device="cuda")
+        rows = kv[table[pos // bs], pos % bs]
+        for i in range(n):
+            if only is not None and t0 + i not in only:
+                continue
+            k = rows[torch.tensor([j < c or bool(p["mask"][t0 + i] >> (j - c) & 1) for j in range(c + n)], device="cuda")]
+            s = p["scale"] * q[t0 + i] @ k.T
+            m = s.amax(-1, keepdim=True)
+            e = torch.exp(s - m)
+            z = e.sum(-1, keepdim=True)
+            w, v = e / z, k[:, :512]
+            out = w @ v
+            away = torch.stack([w[x] @ (v - out[x]).abs() for x in range(w.shape[0])])
+            d = 2.0 ** -18 * abs(p["scale"]) * (q[t0 + i].abs() @ k.abs().T).amax(-1, keepdim=True) + 2.0 ** -20
+            yield t0 + i, out, (m + torch.log(z))[:, 0], w @ v.abs(), away, d, k.shape[0], w
+
+
+def check_two_terms(p, got, only=None):
+    """fp32 results: the weights' two bf16 terms leave r, |r| <= 2^-16, of each, and sum w (1 + r) v is divided by sum w, so
+    that is off by at most 2^-16 sum w |v| (it does not cancel, as it would divided by sum w (1 + r)).  The scores' error d
+    moves numerator and sum alike, d sum w |v - out|, and the other's second order (2 %); sums over P positions are off by
+    at most 2^-23 of sum w |v| a position, lse by d and its rounding.  Returns the largest share of the bound that weights
+    of one bf16 term would have used."""
+    one = 0.0
+    for t, out, lse, wabs, away, d, n, w in formula(p, only):
+        tol = 2.0 ** -16 * wabs + 2 * d * away + 2.0 ** -23 * n * wabs + 2.0 ** -22 * out.abs()
+        assert bool(((got[0][t].double() - out).abs() <= tol).all()), (t, float(((got[0][t].double() - out).abs() / tol).max()))
+        assert bool(((got[1][t].double() - lse).abs() <= d[:, 0] + 2.0 ** -22 * lse.abs() + 2.0 ** -23 * n).all()), t
+        r = w.bfloat16().double()                     # (as a kernel would: to 8 bits, whatever the scale)
+        r = r / w - 1
+        top = w.topk(min(8, w.shape[1]), -1).indices   # what the heaviest weights' rounding alone does
+        one = max(one, float(((torch.gather(r * w, 1, top).sum(-1, keepdim=True) * out).abs() / tol).max()))
+    return one
+
+
+def heavy(p, positions, low=14.0, high=16.5):
+    """Cached positions of every request that have most of the weight, by the rope columns alone: each request's
+    `positions` rows get scores of `low` to `high` more than the others'."""
+    rng = np.random.default_rng(7)
+    kv, bs = p["kv"].float(), p["kv"].shape[1]
+    kv[..., 512] = 0.0
+    p["q"][..., 512] = 1.0
+    for b, c in enumerate(int(x) for x in p["cached"]):
+        for pos in rng.integers(0, c, positions):
+            kv[int(p["table"][b, pos // bs]), pos % bs, 512] = float(rng.uniform(low, high)) / p["scale"]
+    p["kv"] = kv.to(torch.bfloat16)
+    return p
+
+
+DEALT = [
+    # (cached, nodes, h, tokens to check): whole units, more than there are pairs; two rounds and a remainder; chunks of
+    # few units; chunks of units of several requests, ragged
+    ([6000 + 31 * i for i in range(12)], [8] * 12, 128, range(0, 96, 7)),
+    ([3300 + 17 * i for i in range(20)], [8] * 20, 128, range(0, 160, 13)),
+    ([70000], [5], 64, range(5)),
+    ([30000, 41000, 500, 0, 26000], [16, 3, 30, 5, 9], 96, range(0, 63, 4))]
+
+
+@pytest.mark.parametrize("cached,nodes,h,only", DEALT, ids=["whole", "rounds", "chunks", "ragged"])
+def test_decode_of_dealt_units_in_fp32(cached, nodes, h, only):
+    p = heavy(problem(130 + h, cached, nodes, h, 64, std=0.3), 3) if min(cached) > 0 else problem(131, cached, nodes, h, 64)
+    d = device(p)
+    first = [x.clone() for x in sfa.decode_tree(**d)]
+    assert sfa.last_device_status() == 0
+    one = check_two_terms(p, first, set(only))
+    # (behind 2^15 positions the bound of their sums, 2^-23 each, is above a weight's rounding, 2^-8, and hides it)
+    if 0 < min(cached) and max(cached) < 1 << 13:
+        assert one > 1.5, "the case would not see a second term that is missing"
+    T = sum(nodes)
+    for _ in range(4):                                     # the same plan and the same bits on every call
+        again = sfa.decode_tree(**d)
+        assert all(torch.equal(x[:T], y[:T]) for x, y in zip(first, again))
+    low = sfa.decode_tree(**d, out_dtype=torch.bfloat16)
+    for t, out, _, wabs, away, e, n, _ in formula(p, set(list(only)[:3])):
+        tol = (2.0 ** -8 + 2 * e) * away / (1 - 2.0 ** -8) + 2.0 ** -23 * n * wabs + 2.0 ** -8 * out.abs()
+        assert bool(((low[0][t].double() - out).abs() <= tol).all())
+
+
+def test_decode_of_more_requests_than_chunks_are_dealt_of():
+    # 257 requests with three units each, over more rows than stay in L2: ranges
+    B = 257
+    p = heavy(problem(140, [300 + b for b in range(B)], [3] * B, 128, 64, std=0.3), 3)
+    d = device(p)
+    got = [x.clone() for x in sfa.decode_tree(**d)]
+    assert sfa.last_device_status() == 0
+    assert check_two_terms(p, got, set(range(0, 3 * B, 37))) > 1.5
+    again = sfa.decode_tree(**d)
+    assert all(torch.equal(x[:3 * B], y[:3 * B]) for x, y in zip(got, again))
