@@ -750,3 +750,29 @@ def test_decode_of_more_requests_than_chunks_are_dealt_of():
     assert check_two_terms(p, got, set(range(0, 3 * B, 37))) > 1.5
     again = sfa.decode_tree(**d)
     assert all(torch.equal(x[:3 * B], y[:3 * B]) for x, y in zip(got, again))
+
+
+def test_decode_of_overlapping_requests_stays_in_its_workspace():
+    """Ten requests name the same 256 tokens: 2560 units of two tiles, where the workspace of 256 tokens holds 256 + 19
+    pieces and two for each of 4 slots a pair (at most 128 pairs): always refused, with outputs and what lies
+    behind the workspace as they were."""
+    p = problem(110, [3], [256], 128, 16, behind=0)
+    d = device(p)
+    B = 19
+    d.update(block_table=d["block_table"].expand(B, -1).contiguous(), cached_lens=d["cached_lens"].expand(B).contiguous(),
+             token_start=i32([0, 256] * 10))
+    size = sfa.decode_tree_workspace_bytes(B, 256, 128)
+    buffer = torch.full((size + (1 << 20),), 90, dtype=torch.uint8, device="cuda")
+    out = torch.full((258, 128, 512), 3.0, device="cuda")
+    lse = torch.full((258, 128), 3.0, device="cuda")
+    sfa.decode_tree(**d, out=out[:256], lse=lse[:256], workspace=buffer[:size])
+    assert sfa.last_device_status() == BAD_TREE
+    assert bool((out == 3).all()) and bool((lse == 3).all()) and bool((buffer[size:] == 90).all())
+    # and what it does do, it does in a workspace of just that size
+    B = 1
+    size = sfa.decode_tree_workspace_bytes(B, 256, 128)
+    buffer.fill_(90)
+    d = device(p)
+    got = sfa.decode_tree(**d, workspace=buffer[:size])
+    assert sfa.last_device_status() == 0 and bool((buffer[size:] == 90).all())
+    check(p, got)
