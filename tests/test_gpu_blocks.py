@@ -325,3 +325,49 @@ def test_calls_of_other_sizes_on_two_host_threads():
             t.join()
         assert not codes, (len(codes), codes[0])
         assert sfa.last_device_status() == 0
+
+
+# --------------------------------------------------------------------------- large tables
+@pytest.mark.parametrize("shared", [False, True])
+def test_free_of_more_entries_than_the_ctas_hold_at_once(shared):
+    # 8192 rows of 300 blocks given back: 2.46 million entries, 16168 a CTA, four rounds of 4096
+    rng = np.random.default_rng(60)
+    R, cols = 8192, 301
+    held = rng.integers(290, 301, R)
+    table, shares, free, taken, nb = pool(rng, held, 1, 5)
+    free = np.concatenate([np.full(nb, -1), free])
+    taken += nb
+    if shared:
+        for r in range(1, R, 3):                            # every third row has the beginning of the one before
+            k = int(rng.integers(1, 290))
+            table[r, :k] = table[r - 1, :k]
+            shares[table[r, :k]] = 1
+        keep = np.where(rng.random(R) < 0.1, rng.integers(0, 290, R), 0)
+    else:
+        keep = np.zeros(R, int)
+    assert table.shape[1] == cols
+    d = [i32(shares), i32(free)]
+    out = sfa.blocks_free(i32(table), i32(held), i32(keep), *d, i32([taken]), 1)
+    assert sfa.last_device_status() == 0
+    for g, w, name in zip((*d, out), tree.blocks_free(table, held, keep, shares, free, taken, 1), ("shares", "free", "taken")):
+        equal(g, w, name)
+
+
+@pytest.mark.parametrize("moves", [1 << 20, 1000])
+def test_compact_of_the_largest_pool(moves):
+    # 2^20 blocks: the bitmaps and ranks of a CTA take 80 KB of shared memory, the rows' sums 32 KB
+    rng = np.random.default_rng(61)
+    R, nb = 8192, 1 << 20
+    lens = rng.integers(0, 121, R)
+    table, shares, free, taken, total = pool(rng, lens, 1, nb - int(lens.sum()) - 50, lost=50)
+    assert total == nb
+    for _ in range(500):
+        a, b = rng.integers(0, R, 2)
+        k = int(rng.integers(0, min(lens[a], lens[b]) + 1))
+        table[a, :k] = table[b, :k]
+    shares[:] = rng.integers(0, 4, nb)
+    got = sfa.blocks_compact(i32(table), i32(lens), i32(shares), i32(free), i32([taken]), 1, moves)
+    assert sfa.last_device_status() == 0
+    for g, w, name in zip(got, tree.blocks_compact(table, lens, shares, free, taken, 1, moves),
+                          ("table", "shares", "free", "copies")):
+        equal(g, w, name)
