@@ -776,3 +776,45 @@ def test_decode_of_overlapping_requests_stays_in_its_workspace():
     got = sfa.decode_tree(**d, workspace=buffer[:size])
     assert sfa.last_device_status() == 0 and bool((buffer[size:] == 90).all())
     check(p, got)
+
+
+# ------------------------------------------------------------------------------ infinities
+def test_decode_of_infinities_that_a_node_attends_to(path):
+    """A score of -inf has weight 0: from a rope column nothing changes, from a value column that column alone is NaN
+    (0 x inf) and lse stays.  A score of +inf makes out and lse of the node and head NaN."""
+    for c, n, h in ((40, 5, 16), (700, 9, 128)):
+        p = problem(150 + n, [c], [n], h, 16)
+        for col in (530, 100):
+            kv, pos = p["kv"].clone(), c // 2
+            kv[int(p["table"][0, pos // 16]), pos % 16, col] = float("inf")
+            q = p["q"][:n, :, col].float()
+            out, lse = (x[:n].double().cpu() for x in sfa.decode_tree(**device(dict(p, kv=kv))))
+            assert sfa.last_device_status() == 0
+            without = p["kv"].clone()                      # the position's weight is 0: as if its score were far below
+            without[int(p["table"][0, pos // 16]), pos % 16] = 0
+            pw = dict(p, kv=without)
+            want = {t: (o.cpu(), l.cpu(), a.cpu(), e.cpu()) for t, o, l, a, _, e, _, _ in formula_without(pw, pos)}
+            for t in range(n):
+                up, down = q[t] > 0, q[t] < 0
+                assert bool(torch.isnan(out[t][up]).all()) and bool(torch.isnan(lse[t][up]).all())
+                o, l, a, e = want[t]
+                ok = torch.ones(512, dtype=torch.bool)
+                if col < 512:
+                    ok[col] = False
+                    assert bool(torch.isnan(out[t][down][:, col]).all())
+                assert bool(((lse[t] - l).abs() <= e[:, 0] + 2.0 ** -22 * l.abs() + 2.0 ** -20)[down].all())
+                tol = (2.0 ** -8 + 2 * e) * a + 1e-6
+                assert bool(((out[t] - o).abs() <= tol)[down][:, ok].all())
+
+
+def formula_without(p, pos):
+    """`formula` of one request with the cached position `pos` left out."""
+    q, kv, bs = p["q"].double(), p["kv"].double(), p["kv"].shape[1]
+    c, n = int(p["cached"][0]), int(p["start"][1])
+    for i in range(n):
+        seen = [j for j in range(c + n) if j != pos and (j < c or p["mask"][i] >> (j - c) & 1)]
+        k = torch.stack([kv[int(p["table"][0, j // bs]), j % bs] for j in seen])
+        s = p["scale"] * q[i] @ k.T
+        w, v = torch.softmax(s, -1), k[:, :512]
+        d = 2.0 ** -18 * p["scale"] * (q[i].abs() @ k.abs().T).amax(-1, keepdim=True) + 2.0 ** -20
+        yield i, w @ v, torch.logsumexp(s, -1), w @ v.abs(), None, d, len(seen), w
