@@ -740,7 +740,7 @@ def decode_tree(q, kv, block_table, cached_lens, token_start, mask, scale: float
     request b is the token token_start[b] + j and its row lies at position cached_lens[b] + j.
     Returns (out [T, h, 512] in out_dtype, torch.float32 or torch.bfloat16, or the dtype of the `out`
     given; lse [T, h] fp32); the rows of padding tokens are left as they were.
-    workspace: decode_tree_workspace_bytes(B, T, h) bytes (allocated when None).
+    workspace: decode_tree_workspace_bytes(B, T, h) bytes, 80 MB from 128 rows (T * h) on (allocated when None).
     """
     dev = q.device
     if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
