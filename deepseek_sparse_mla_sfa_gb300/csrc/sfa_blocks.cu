@@ -528,17 +528,21 @@ struct CopyParams {
   const int32_t* copies;
   long long n;
   int chunks;                              // of kCopyWords words a block
+  int turns;                               // CTAs that take a chunk's layers by turns
   int* status;
 };
 
 constexpr int kCopyThreads = 256, kCopyPer = 4, kCopyWords = kCopyThreads * kCopyPer;
+// Where copies and chunks alone make this many CTAs (the GPU holds 1216), each takes all layers of its chunk, so
+// that an unused entry costs one CTA a chunk, not one a layer: 4096 unused entries of 61 layers 744 us with one a
+// layer, 15 so; 2000 used ones 2566 and 2628, 3000 of 4000 in 6 layers 103 and 102.  (With 32768: 28, 2601, 111.)
+constexpr int kCopyCtas = 8192;
 
-// a CTA a chunk of 16 KB of one copy in one layer
+// a CTA a chunk of 16 KB of one copy, in every turns-th layer
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const CopyParams p) {
   const long long id = blockIdx.x;
   const int chunk = (int)(id % p.chunks);
   const long long item = id / p.chunks % p.n;
-  const int layer = (int)(id / p.chunks / p.n);
   const int src = p.copies[3 * item], dst = p.copies[3 * item + 1];
   const int rows = min(max(p.copies[3 * item + 2], 0), p.block_size);
   if (src < 0) return;
@@ -547,20 +551,22 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const Copy
     return;
   }
   const size_t block_words = (size_t)p.block_size * p.row_words;
-  const uint4* from = p.kv + ((size_t)layer * p.num_blocks + src) * block_words;
-  uint4* to = p.kv + ((size_t)layer * p.num_blocks + dst) * block_words;
   const long long end = (long long)rows * p.row_words, at = (long long)chunk * kCopyWords + threadIdx.x;
-  uint4 x[kCopyPer];
+  for (int layer = (int)(id / p.chunks / p.n); layer < p.layers; layer += p.turns) {
+    const uint4* from = p.kv + ((size_t)layer * p.num_blocks + src) * block_words;
+    uint4* to = p.kv + ((size_t)layer * p.num_blocks + dst) * block_words;
+    uint4 x[kCopyPer];
 #pragma unroll
-  for (int u = 0; u < kCopyPer; ++u)
-    if (at + u * kCopyThreads < end) x[u] = from[at + u * kCopyThreads];
+    for (int u = 0; u < kCopyPer; ++u)
+      if (at + u * kCopyThreads < end) x[u] = from[at + u * kCopyThreads];
 #pragma unroll
-  for (int u = 0; u < kCopyPer; ++u)
-    if (at + u * kCopyThreads < end) to[at + u * kCopyThreads] = x[u];
-  if (p.scales && chunk == 0) {
-    const int per = p.block_size / p.group, n = (rows + p.group - 1) / p.group;
-    for (int g = threadIdx.x; g < n; g += kCopyThreads)
-      p.scales[((size_t)layer * p.num_blocks + dst) * per + g] = p.scales[((size_t)layer * p.num_blocks + src) * per + g];
+    for (int u = 0; u < kCopyPer; ++u)
+      if (at + u * kCopyThreads < end) to[at + u * kCopyThreads] = x[u];
+    if (p.scales && chunk == 0) {
+      const int per = p.block_size / p.group, n = (rows + p.group - 1) / p.group;
+      for (int g = threadIdx.x; g < n; g += kCopyThreads)
+        p.scales[((size_t)layer * p.num_blocks + dst) * per + g] = p.scales[((size_t)layer * p.num_blocks + src) * per + g];
+    }
   }
 }
 
@@ -673,11 +679,13 @@ cudaError_t launch_kv_copy_blocks(void* kv, float* scales, int group, int row_by
                                   int block_size, const int32_t* copies, int n, int* status, cudaStream_t stream) {
   const int row_words = row_bytes / 16;
   const long long chunks = ((long long)block_size * row_words + kCopyWords - 1) / kCopyWords;
-  const long long grid = chunks * n * layers;
-  if (grid == 0) return cudaSuccess;
+  if (n == 0 || layers == 0) return cudaSuccess;
+  const long long most = std::min<long long>(layers, (kCopyCtas + chunks * n - 1) / (chunks * n));
+  const long long each = (layers + most - 1) / most, turns = (layers + each - 1) / each;   // layers of a CTA
+  const long long grid = chunks * n * turns;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const CopyParams p{static_cast<uint4*>(kv), scales, layers, num_blocks, block_size, row_words, group, copies, n,
-                     (int)chunks, status};
+                     (int)chunks, (int)turns, status};
   kv_copy_blocks_kernel<<<(unsigned)grid, kCopyThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }

@@ -371,3 +371,48 @@ def test_compact_of_the_largest_pool(moves):
     for g, w, name in zip(got, tree.blocks_compact(table, lens, shares, free, taken, 1, moves),
                           ("table", "shares", "free", "copies")):
         equal(g, w, name)
+
+
+@pytest.mark.parametrize("layers,n,bs", [(61, 3, 7), (5, 300, 64), (7, 9000, 3), (61, 800, 16)])
+def test_copies_of_many_layers_with_unused_entries(layers, n, bs):
+    # a CTA takes one layer, some or all, by the numbers of copies and layers; most entries are unused
+    rng = np.random.default_rng(layers)
+    nb = max(40, n // 100)
+    used = min(nb // 2, n)
+    copies, at = np.full((n, 3), -1), rng.permutation(n)[:used]
+    ids = rng.permutation(nb)
+    copies[at] = np.stack([ids[:used], ids[used:2 * used], rng.integers(0, bs + 1, used)], 1)
+    codes = torch.randint(0, 256, (layers, nb, bs, 576), dtype=torch.uint8)
+    scales = torch.rand((layers, nb, bs))
+    k8, sc = codes.cuda().view(torch.float8_e4m3fn), scales.cuda()
+    sfa.kv_copy_blocks_q8(k8, sc, i32(copies))
+    assert sfa.last_device_status() == 0
+    assert np.array_equal(k8.view(torch.uint8).cpu().numpy(), tree.copy_blocks(codes.numpy(), copies))
+    assert np.array_equal(sc.cpu().numpy(), tree.copy_blocks(scales.numpy()[..., None], copies)[..., 0])
+    kv = torch.randn((layers, nb, bs, 576)).to(torch.bfloat16)
+    d = sfa.kv_copy_blocks(kv.cuda(), i32(copies))
+    assert np.array_equal(d.view(torch.int16).cpu().numpy(), tree.copy_blocks(kv.view(torch.int16).numpy(), copies))
+
+
+def test_copies_of_nothing_cost_no_cta_a_layer():
+    """4096 unused entries of 61 layers, as a compaction that moves nothing leaves them, against one such layer: at
+    most ten times as long (one CTA a chunk, entry and layer took 60 times)."""
+    kv = torch.zeros((61, 2, 64, 576), dtype=torch.bfloat16, device="cuda")
+    copies = i32(np.full((4096, 3), -1))
+
+    def us(x, n=20):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        g = torch.cuda.CUDAGraph()
+        sfa.kv_copy_blocks(x, copies)
+        with torch.cuda.graph(g):
+            for _ in range(n):
+                sfa.kv_copy_blocks(x, copies)
+        g.replay()
+        torch.cuda.synchronize()
+        a.record()
+        g.replay()
+        b.record()
+        torch.cuda.synchronize()
+        return a.elapsed_time(b) / n
+
+    assert us(kv) < 10 * us(kv[:1])
