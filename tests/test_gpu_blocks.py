@@ -416,3 +416,53 @@ def test_copies_of_nothing_cost_no_cta_a_layer():
         return a.elapsed_time(b) / n
 
     assert us(kv) < 10 * us(kv[:1])
+
+
+def test_large_frees_captured_and_on_two_streams():
+    """The four launches of a large free, each of which begins while the one before it ends: in a graph that is
+    replayed on other lengths, and two frees at once on two streams with workspaces of their own."""
+    rng = np.random.default_rng(62)
+    sets = []
+    for seed in range(2):
+        R = 600
+        held = rng.integers(0, 1200, R)
+        table, shares, free, taken, nb = pool(rng, held, 4, 5, wide=300 - int(held.max()) // 4)
+        free = np.concatenate([np.full(nb, -1), free])
+        for _ in range(300):
+            a, b = rng.integers(0, R, 2)
+            k = int(rng.integers(0, min(held[a], held[b]) // 4 + 1))
+            table[a, :k] = table[b, :k]
+        shares[:] = 700                                     # whatever is named stays or goes by this many names
+        shares[rng.random(nb) < 0.7] = 0
+        sets.append((table, held, shares, free, taken + nb, nb))
+    cols = max(s[0].shape[1] for s in sets)
+    ws = [torch.full((max(sfa.blocks_free_workspace_bytes(600, cols), 1),), 255, dtype=torch.uint8, device="cuda") for _ in sets]
+    assert ws[0].numel() > 1                                # the large form
+
+    def want(s, keep):
+        return tree.blocks_free(s[0], s[1], keep, s[2], s[3], s[4], 4)
+
+    keeps = [np.where(rng.random(600) < 0.4, 0, np.maximum(sets[0][1] - rng.integers(0, 500, 600), 0)) for _ in range(3)]
+    s = sets[0]
+    d = dict(t=i32(s[0]), h=i32(s[1]), k=i32(keeps[0]), s=i32(s[2]), f=i32(s[3]), n=i32([s[4]]))
+    sfa.blocks_free(d["t"], d["h"], d["k"], d["s"], d["f"], d["n"], 4, workspace=ws[0])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = sfa.blocks_free(d["t"], d["h"], d["k"], d["s"], d["f"], d["n"], 4, workspace=ws[0])
+    for keep in keeps:
+        for x, v in (("k", keep), ("s", s[2]), ("f", s[3])):
+            d[x].copy_(i32(v))
+        g.replay()
+        for got, w, name in zip((d["s"], d["f"], out), want(s, keep), ("shares", "free", "taken")):
+            equal(got, w, name)
+    sfa.last_device_status()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(5):
+        ds = [[i32(x) for x in (s[0], s[1], keeps[0] if i == 0 else s[1] // 2, s[2], s[3], [s[4]])] for i, s in enumerate(sets)]
+        torch.cuda.synchronize()
+        outs = [sfa.blocks_free(*d, 4, workspace=ws[i], stream=streams[i]) for i, d in enumerate(ds)]
+        torch.cuda.synchronize()
+        for i, (s, dd) in enumerate(zip(sets, ds)):
+            for got, w, name in zip((dd[3], dd[4], outs[i]), want(s, keeps[0] if i == 0 else s[1] // 2), ("shares", "free", "taken")):
+                equal(got, w, (i, name))
+    sfa.last_device_status()
