@@ -526,7 +526,7 @@ struct CopyParams {
   float* scales;
   int layers, num_blocks, block_size, row_words, group;
   const int32_t* copies;
-  long long n;
+  int n;
   int chunks;                              // of kCopyWords words a block
   int turns;                               // CTAs that take a chunk's layers by turns
   int* status;
@@ -535,14 +535,16 @@ struct CopyParams {
 constexpr int kCopyThreads = 256, kCopyPer = 4, kCopyWords = kCopyThreads * kCopyPer;
 // Where copies and chunks alone make this many CTAs (the GPU holds 1216), each takes all layers of its chunk, so
 // that an unused entry costs one CTA a chunk, not one a layer: 4096 unused entries of 61 layers 744 us with one a
-// layer, 15 so; 2000 used ones 2566 and 2628, 3000 of 4000 in 6 layers 103 and 102.  (With 32768: 28, 2601, 111.)
+// layer, 13 so; 2000 used ones 2567 and 2625, 3000 of 4000 in 6 layers 103 and 101.  (With 32768: 28, 2601, 111.)
 constexpr int kCopyCtas = 8192;
 
-// a CTA a chunk of 16 KB of one copy, in every turns-th layer
+// a CTA a chunk of 16 KB of one copy, in every turns-th layer (kOne: in one layer; the loop costs 512 copies in 6
+// layers 2 of 16 us)
+template <bool kOne>
 __global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const CopyParams p) {
-  const long long id = blockIdx.x;
-  const int chunk = (int)(id % p.chunks);
-  const long long item = id / p.chunks % p.n;
+  const unsigned each = blockIdx.x / (unsigned)p.chunks, turn = each / (unsigned)p.n;
+  const int chunk = (int)(blockIdx.x - each * (unsigned)p.chunks);
+  const size_t item = each - turn * (unsigned)p.n;
   const int src = p.copies[3 * item], dst = p.copies[3 * item + 1];
   const int rows = min(max(p.copies[3 * item + 2], 0), p.block_size);
   if (src < 0) return;
@@ -552,7 +554,8 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const Copy
   }
   const size_t block_words = (size_t)p.block_size * p.row_words;
   const long long end = (long long)rows * p.row_words, at = (long long)chunk * kCopyWords + threadIdx.x;
-  for (int layer = (int)(id / p.chunks / p.n); layer < p.layers; layer += p.turns) {
+  int layer = (int)turn;
+  do {
     const uint4* from = p.kv + ((size_t)layer * p.num_blocks + src) * block_words;
     uint4* to = p.kv + ((size_t)layer * p.num_blocks + dst) * block_words;
     uint4 x[kCopyPer];
@@ -567,7 +570,7 @@ __global__ void __launch_bounds__(kCopyThreads) kv_copy_blocks_kernel(const Copy
       for (int g = threadIdx.x; g < n; g += kCopyThreads)
         p.scales[((size_t)layer * p.num_blocks + dst) * per + g] = p.scales[((size_t)layer * p.num_blocks + src) * per + g];
     }
-  }
+  } while (!kOne && (layer += p.turns) < p.layers);
 }
 
 constexpr int kUnasked = 40 * 1024;        // dynamic shared memory that a launch has beside the kernels' own
@@ -686,7 +689,7 @@ cudaError_t launch_kv_copy_blocks(void* kv, float* scales, int group, int row_by
   if (grid > 0x7fffffffLL) return cudaErrorInvalidValue;
   const CopyParams p{static_cast<uint4*>(kv), scales, layers, num_blocks, block_size, row_words, group, copies, n,
                      (int)chunks, (int)turns, status};
-  kv_copy_blocks_kernel<<<(unsigned)grid, kCopyThreads, 0, stream>>>(p);
+  (turns == layers ? kv_copy_blocks_kernel<true> : kv_copy_blocks_kernel<false>)<<<(unsigned)grid, kCopyThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
