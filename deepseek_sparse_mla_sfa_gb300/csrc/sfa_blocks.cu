@@ -17,7 +17,7 @@
 // Bound: latency (a chain of launch, lengths, table, block counters and the barriers between them)
 // up to some 10^5 table entries; kv_copy_blocks: HBM.  On the device: fork of 8 and of 512 rows 4 and 5 us;
 // free of 8384 table entries 9 us, of 718000 (323000 freed) 19; compact of 512 blocks 8 us, of 10000 blocks
-// and 10200 entries 17; copies of 2500 blocks of 74 KB in each of two layers 109 us, 6.8 TB/s.
+// and 10200 entries 17; copies of 2500 blocks of 74 KB in each of two layers 107 us, 6.9 TB/s.
 #include <algorithm>
 #include <climits>
 
@@ -171,7 +171,7 @@ struct FreeParams {
 };
 
 constexpr int kClusterThreads = 1024;
-constexpr int kClusterCtas = 8;            // of the forms for large tables
+constexpr int kClusterCtas = 8;            // free: at most, of the form for small tables; compact: of the form for large ones
 constexpr int kMarked = INT_MIN;           // shares of a freed block while the call runs: kMarked + e
 
 // sums [rows + 1] of the entries per row, counted by `count(row)`; returns the total

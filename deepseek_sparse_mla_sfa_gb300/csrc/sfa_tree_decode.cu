@@ -31,11 +31,15 @@
 // Bound.  From 128 query rows a request on, the tensor cores: a tile of 256 keys is 4353 cycles of MMAs (6400
 // with two terms), and takes 6200 to 6700 with its rows in L2 (keys awaited 700 to 1000, values 600, P 350;
 // shared memory itself needs 5600 for the MMAs' and the loads' traffic).  16 requests x 16 nodes x 128 heads x
-// 8192 positions, bf16 results: 416 us, 1406 TFLOP/s; 2 x 25 nodes x 64 heads x 131072 positions: 518 us,
-// 1430.  With fewer rows the latency of memory: 64 x 2-8 nodes x 16 heads x 1000-16384 positions, fp32: 195 us
+// 8192 positions, bf16 results: 418 us, 1399 TFLOP/s; 2 x 25 nodes x 64 heads x 131072 positions: 525 us,
+// 1411.  With fewer rows the latency of memory: 64 x 2-8 nodes x 16 heads x 1000-16384 positions, fp32: 193 us
 // where the bytes need 97; with all rows in L2 it takes 163, its products alone 101.  Short calls: latency, 18
-// of the 29 us of 6 nodes x 4 heads x 200 positions in the pairs' launch (keys 7000 cycles, products and
+// of the 27 us of 6 nodes x 4 heads x 200 positions in the pairs' launch (keys 7000 cycles, products and
 // softmax 15000, the result 8000), the rest in the schedule and between the launches.
+//
+// Accuracy of fp32 results.  Scores and O are fp32 sums in the tensor core, which cuts each off towards zero: against
+// 64 bits (2-norm) units of 250, 1000, 4000 and 16000 positions that one pair adds up are off by 1.1, 2.1, 4.3 and
+// 7.4e-6, and 16000 positions cut over all pairs, whose parts are joined in registers, by 1.0e-6.
 //
 // Rows that nobody may see.  Positions behind the last node are brought as rows of zeros.  A cached row
 // of NaN or infinities that only some nodes see would reach the others as 0 x NaN in P V: such a row
@@ -259,8 +263,12 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // the same rows at the same time; what is left of the last, unfilled round goes to ranges that even out
 // what the dealt chunks left uneven.
 constexpr int kPlanThreads = 256;
-constexpr int kDealRequests = 256;             // requests that chunks are dealt of
-constexpr int kFarTiles = 240;                 // tiles (256 rows of 1152 bytes) that stay in L2: 70 MB
+// Requests that chunks are dealt of: one a thread.  256 requests x 4 units x 2048 positions take 541 us dealt and
+// 640 in ranges, so 257 take 647.
+constexpr int kDealRequests = 256;
+// Tiles (256 rows of 1152 bytes) that stay in L2: 70 MB.  16 units a request x 4400 positions, dealt and in ranges:
+// 70 tiles 95 and 81 us, 140 140 and 145, 280 241 and 268, 600 476 and 552.
+constexpr int kFarTiles = 240;
 constexpr int kWhole = 0x7fffffff;             // `limit` that cuts nothing
 
 struct Request {
@@ -404,8 +412,12 @@ __global__ void __launch_bounds__(kPlanThreads) tree_schedule_kernel(const TreeT
     add((int)tiles, &tiles_of);                // (both below `total`; with a task's starts and last chunk below 3 times that)
     add((int)far, &far_of);
     __syncthreads();
+    // From 1.5 units a request on.  Dealt and in ranges, 8192 positions: 64 requests of 1.25 units 177 and 190 us, of 1.5
+    // 203 and 235, of 2 274 and 302; 16 requests of 1.5 units 89 and 74, of 2 106 and 92, of 3 124 and 119, of 6 186 and
+    // 210; 2 long ones of 131072 positions 498 and 698.
     if (far_of > kFarTiles && 2 * tiles_of >= 3 * far_of) {
-      // whole units, or chunks that make a round or two; what is not dealt counts a third more
+      // Whole units, or chunks that make a round or two; what is not dealt counts a third more (77 units of 7000 positions
+      // 137 us so, 144 where it counts as much, 138 where it counts twice; other shapes within 2 %)
       int limits[3] = {kWhole, 0, 0};
       for (int c = 0; c < 3; ++c) {
         if (c > 0) limits[c] = (tiles_of + c * pairs - 1) / (c * pairs);
@@ -753,8 +765,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       x = y;
       // The sums of the weights as they are, for lse, and as P's one term holds them: out is divided by the
       // latter, so that the rounding of a row's heaviest weights cancels (with two terms 2^-17 of them is left, and
-      // the second sum cost 2 % for 8 % of the error).  128 heads 414-416 us without the second sum, 419 with, 423
-      // where it came before the hand-over of P.
+      // the second sum costs 1 to 2 % for 3 to 8 % of the error).  128 heads 414-416 us without the second sum, 419 with,
+      // 423 where it came before the hand-over of P.
       float m_ref = -INFINITY, l_sum = 0.f, l_held = 0.f, u[3];
       const bool live = row < x.rows;
       const int node = live ? (x.row0 + row) / p.h - x.first : 0;
